@@ -35,6 +35,7 @@ SPARGE_OP_BLOCK_SPARSE_ATTN = 2
 SPARGE_OP_ATTN = 3
 SPARGE_OP_BLOCK_SPARSE_ATTN_Q8 = 4
 SPARGE_OP_ATTN_Q8 = 5
+SPARGE_OP_WINDOW_ATTN = 6
 SPARGE_OP_TOKEN_ORDER = 0x100  # flag OR-ed into an op: room for token-ordered copies of Q and K
 SPARGE_TOPK_CUMULATIVE = 0      # topk is a cumulative probability fraction (default)
 SPARGE_TOPK_COUNT = 1           # topk is a fraction of the valid blocks to keep
@@ -60,6 +61,11 @@ class sparge_params(ctypes.Structure):
                 ("topk_per_head", ctypes.c_void_p), ("theta_per_head", ctypes.c_void_p),
                 ("lambda_per_head", ctypes.c_void_p), ("token_order", ctypes.c_void_p), ("topk_mode", ctypes.c_int32),
                 ("topp", ctypes.c_float)]
+
+
+class sparge_cache4(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("n_pages", ctypes.c_int64), ("page_size", ctypes.c_int32),
+                ("H", ctypes.c_int32), ("d", ctypes.c_int32), ("pad_", ctypes.c_int32)]
 
 
 _lib = None
@@ -89,6 +95,25 @@ EXPORTS = {
     "sparge_hilbert_perm_3d": (ctypes.c_int, [ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_void_p]),
     "sparge_predict_mask_noalloc": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_float, ctypes.c_float,
                                                    ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p]),
+    "sparge_window_attn": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64,
+                                          ctypes.c_int64, ctypes.c_float, ctypes.c_void_p, ctypes.c_void_p,
+                                          ctypes.c_size_t, ctypes.c_void_p]),
+    "sparge_qk_norm_rope": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64,
+                                           ctypes.c_void_p, ctypes.c_int, ctypes.c_int, ctypes.c_void_p,
+                                           ctypes.c_void_p, ctypes.c_float, ctypes.c_void_p, ctypes.c_void_p,
+                                           ctypes.c_void_p]),
+    "sparge_cache4_bytes": (ctypes.c_size_t, [ctypes.c_int64, ctypes.c_int, ctypes.c_int, ctypes.c_int]),
+    "sparge_cache_tables": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64,
+                                           ctypes.c_int, ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p,
+                                           ctypes.c_int64, ctypes.c_int64, ctypes.c_void_p, ctypes.c_void_p,
+                                           ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
+    "sparge_cache4_store": (ctypes.c_int, [ctypes.c_void_p] * 5),
+    "sparge_cache4_load": (ctypes.c_int, [ctypes.c_void_p] * 5),
+    "sparge_cache4_attn_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int64] * 5),
+    "sparge_cache4_attn": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64,
+                                          ctypes.c_int64, ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64,
+                                          ctypes.c_float, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t,
+                                          ctypes.c_void_p]),
     "sparge_selftest_bounded_wait": (ctypes.c_int, [ctypes.c_int64, ctypes.c_void_p]),
     "sparge_last_error": (ctypes.c_char_p, []),
     "sparge_get_device_status": (ctypes.c_int, [ctypes.c_void_p]),
@@ -384,6 +409,165 @@ def unpermute_tokens(x, perm, out=None):
         out = torch.empty_like(x)
     dx, dy = _desc(x), _desc(out)
     _check(lib().sparge_unpermute_tokens(ctypes.byref(dx), perm.data_ptr(), ctypes.byref(dy), _stream()))
+    return out
+
+
+def window_attn(q, k, v, window: int, sinks: int = 0, scale: float = 0.0, out=None, ws=None):
+    """Causal attention over each query's last `window` keys (itself included) and the first `sinks` keys; q may be
+    shorter than k and v (its last query sits on the last key)."""
+    torch = _torch()
+    _same_device(q, k, v, out, ws)
+    if out is None:
+        out = torch.empty_like(q)
+    ws = _workspace(SPARGE_OP_WINDOW_ATTN, k, k, ws)
+    dq, dk, dv, do = _desc(q), _desc(k), _desc(v), _desc(out)
+    _check(lib().sparge_window_attn(ctypes.byref(dq), ctypes.byref(dk), ctypes.byref(dv), int(window), int(sinks),
+                                    float(scale), ctypes.byref(do), ws.data_ptr(), ws.numel(), _stream()))
+    return out
+
+
+def rope_freqs(rot_dim: int, base: float = 10000.0, device="cuda"):
+    """The rotation's inverse frequencies base^(-2i/rot_dim), float64, for qk_norm_rope (scaled variants: scale
+    this tensor)."""
+    torch = _torch()
+    return base ** (-torch.arange(0, rot_dim, 2, dtype=torch.float64, device=device) / rot_dim)
+
+
+def _array(x, dtype, name, like, shape=None):
+    """A contiguous CUDA array on the device of `like` as a device pointer (None: 0)."""
+    if x is None:
+        return 0
+    if x.dtype != dtype or x.device != like.device or not x.is_contiguous() or (shape is not None and x.shape != shape):
+        raise TypeError("%s must be a contiguous %s tensor%s on %s" % (
+            name, dtype, "" if shape is None else " of shape %s" % (tuple(shape),), like.device))
+    return x.data_ptr()
+
+
+def _same_device(*tensors):
+    """The calls run on the current device's current stream: every tensor must live there."""
+    torch = _torch()
+    here = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and not (t.is_cuda and t.device.index == here):
+            raise ValueError("expected tensors on the current CUDA device (cuda:%d), got one on %s" % (here, t.device))
+
+
+def qk_norm_rope(q, k, inv_freq=None, positions=None, start: int = 0, q_weight=None, k_weight=None, eps: float = 1e-6,
+                 interleaved: bool = False, q_out=None, k_out=None):
+    """Norm of q (B,Hq,N,d) and k (B,Hkv,N,d) over each head's channels, times the weights (float32, d
+    entries, or None), then the rotation of the first 2 len(inv_freq) channels by the positions ((B, N) int32,
+    or start, start + 1, ...); inv_freq: float64 CUDA tensor (rope_freqs) or None (norm only).  Returns (q_out,
+    k_out), which may be given and may be q and k."""
+    torch = _torch()
+    _same_device(q, k, inv_freq, positions, q_weight, k_weight, q_out, k_out)
+    if q_out is None:
+        q_out = torch.empty_like(q)
+    if k_out is None:
+        k_out = torch.empty_like(k)
+    dq, dk, eq, ek = _desc(q), _desc(k), _desc(q_out), _desc(k_out)
+    w = q.shape[3:]
+    _check(lib().sparge_qk_norm_rope(
+        ctypes.byref(dq), ctypes.byref(dk), _array(positions, torch.int32, "positions", q, (q.shape[0], q.shape[2])),
+        int(start), _array(inv_freq, torch.float64, "inv_freq", q), 0 if inv_freq is None else 2 * inv_freq.numel(),
+        int(interleaved), _array(q_weight, torch.float32, "q_weight", q, w), _array(k_weight, torch.float32, "k_weight", q, w),
+        float(eps), ctypes.byref(eq), ctypes.byref(ek), _stream()))
+    return q_out, k_out
+
+
+def cache_tables(lens, new_lens, free_pages, table, page_size: int, N: int, slots=None, positions=None, kv_lens=None,
+                 used=None):
+    """Block tables and slot maps of a step: extends table (R, width; int32, rows any stride) in place with pages
+    from the front of free_pages and returns (slots (R, N) int64, positions (R, N) int32, kv_lens (R) int32,
+    used (1) int32); the new tokens stand right-aligned, -1 in front of them (see sparge_cache_tables)."""
+    torch = _torch()
+    _same_device(lens, new_lens, free_pages, table, slots, positions, kv_lens, used)
+    R = lens.numel()
+    if table.dtype != torch.int32 or table.dim() != 2 or table.shape[0] != R or (table.shape[1] > 1 and table.stride(1) != 1):
+        raise TypeError("table must be an int32 (R, width) tensor with contiguous rows")
+    width = table.shape[1]
+    stride = table.stride(0) if R > 1 else width
+    if N < 0:
+        raise ValueError("N must not be negative")
+    if slots is None:
+        slots = torch.empty((R, N), dtype=torch.int64, device=lens.device)
+    if positions is None:
+        positions = torch.empty((R, N), dtype=torch.int32, device=lens.device)
+    if kv_lens is None:
+        kv_lens = torch.empty(R, dtype=torch.int32, device=lens.device)
+    if used is None:
+        used = torch.empty(1, dtype=torch.int32, device=lens.device)
+    i32 = torch.int32
+    _check(lib().sparge_cache_tables(
+        _array(lens, i32, "lens", lens), _array(new_lens, i32, "new_lens", lens, lens.shape), R, int(N), int(page_size),
+        _array(free_pages, i32, "free_pages", lens), free_pages.numel(), table.data_ptr(), width, stride,
+        _array(slots, torch.int64, "slots", lens, (R, N)), _array(positions, i32, "positions", lens, (R, N)),
+        _array(kv_lens, i32, "kv_lens", lens, lens.shape), _array(used, i32, "used", lens, (1,)), _stream()))
+    return slots, positions, kv_lens, used
+
+
+def cache4_pool(n_pages: int, page_size: int, H: int, d: int, device="cuda"):
+    """An empty pool of the 4-bit cache: a uint8 tensor (n_pages, H, page_size / 16, 18 d), from whose shape the
+    other calls read page size, heads and head dim."""
+    torch = _torch()
+    if n_pages > 0 and lib().sparge_cache4_bytes(n_pages, page_size, H, d) == 0:
+        raise ValueError("unsupported pool: n_pages=%d, page_size=%d, H=%d, d=%d" % (n_pages, page_size, H, d))
+    return torch.zeros((n_pages, H, page_size // 16, 18 * d), dtype=torch.uint8, device=device)
+
+
+def _pool_desc(pool) -> sparge_cache4:
+    torch = _torch()
+    if pool.dtype != torch.uint8 or pool.dim() != 4 or not pool.is_contiguous() or pool.shape[3] % 18:
+        raise TypeError("expected a contiguous uint8 pool of shape (n_pages, H, page_size / 16, 18 d)")
+    n, H, recs, rec = pool.shape
+    return sparge_cache4(pool.data_ptr(), n, 16 * recs, H, rec // 18, 0)
+
+
+def cache4_store(k, v, slots, pool):
+    """Stores rows (b, h, n) of k and v (B,H,N,d) at slots[b, n] ((B, N) int64; negative: left out) of the pool."""
+    torch = _torch()
+    _same_device(k, v, slots, pool)
+    dk, dv, dc = _desc(k), _desc(v), _pool_desc(pool)
+    _check(lib().sparge_cache4_store(ctypes.byref(dk), ctypes.byref(dv),
+                                     _array(slots, torch.int64, "slots", k, (k.shape[0], k.shape[2])), ctypes.byref(dc),
+                                     _stream()))
+
+
+def cache4_load(pool, slots, k_out=None, v_out=None):
+    """The rows at slots ((B, N) int64) as bf16 (B,H,N,d) tensors k and v; rows of negative slots stay as they were
+    (zero in tensors made here)."""
+    torch = _torch()
+    _same_device(pool, slots, k_out, v_out)
+    dc = _pool_desc(pool)
+    B, N = slots.shape
+    if k_out is None:
+        k_out = torch.zeros((B, dc.H, N, dc.d), dtype=torch.bfloat16, device=pool.device)
+    if v_out is None:
+        v_out = torch.zeros((B, dc.H, N, dc.d), dtype=torch.bfloat16, device=pool.device)
+    dk, dv = _desc(k_out), _desc(v_out)
+    _check(lib().sparge_cache4_load(ctypes.byref(dc), _array(slots, torch.int64, "slots", pool, (k_out.shape[0], k_out.shape[2])),
+                                    ctypes.byref(dk), ctypes.byref(dv), _stream()))
+    return k_out, v_out
+
+
+def cache4_attn(q, pool, table, kv_lens, window: int = 0, sinks: int = 0, scale: float = 0.0, out=None, ws=None):
+    """Attention of q (B,Hq,Nq,d) over the 4-bit cache: sequence b has kv_lens[b] tokens on the pages table[b, :]
+    ((B, width) int32) and q holds its last Nq; window > 0 keeps each query's last `window` tokens and the first
+    `sinks`."""
+    torch = _torch()
+    _same_device(q, pool, table, kv_lens, out, ws)
+    if out is None:
+        out = torch.empty_like(q)
+    dq, do, dc = _desc(q), _desc(out), _pool_desc(pool)
+    B, Hq, Nq, d = q.shape
+    if table.dtype != torch.int32 or table.dim() != 2 or table.shape[0] != B or (table.shape[1] > 1 and table.stride(1) != 1):
+        raise TypeError("table must be an int32 (B, width) tensor with contiguous rows")
+    width = table.shape[1]
+    if ws is None:
+        ws = torch.empty(max(1, lib().sparge_cache4_attn_workspace_bytes(B, Hq, dc.H, Nq, d)), dtype=torch.uint8, device=q.device)
+    _check(lib().sparge_cache4_attn(ctypes.byref(dq), ctypes.byref(dc), table.data_ptr(), width,
+                                    table.stride(0) if B > 1 else width,
+                                    _array(kv_lens, torch.int32, "kv_lens", q, (B,)), int(window), int(sinks), float(scale),
+                                    ctypes.byref(do), ws.data_ptr(), ws.numel(), _stream()))
     return out
 
 

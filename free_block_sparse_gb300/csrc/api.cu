@@ -17,18 +17,6 @@ namespace {
 
 thread_local char g_last_error[512] = "";
 
-int fail(int code, const char *fmt, ...) {
-  va_list ap;
-  va_start(ap, fmt);
-  vsnprintf(g_last_error, sizeof(g_last_error), fmt, ap);
-  va_end(ap);
-  return code;
-}
-
-int cuda_fail(cudaError_t e, const char *where) {
-  return fail(SPARGE_ERR_CUDA, "%s: %s", where, cudaGetErrorString(e));
-}
-
 // One status word per process in device memory (a __device__ variable, not an allocation);
 // kernels record a timed-out bounded wait there.
 __device__ int g_status_word = 0;
@@ -47,14 +35,29 @@ __global__ void bounded_wait_probe_kernel(int *status, uint64_t limit_ns) {
   if (threadIdx.x == 0) mbar_wait(&bar, 0, &abort_flag, status, limit_ns);
 }
 
+}  // namespace
+
+namespace sparge {
+
+void clear_error() { g_last_error[0] = 0; }
+
+int fail(int code, const char *fmt, ...) {
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(g_last_error, sizeof(g_last_error), fmt, ap);
+  va_end(ap);
+  return code;
+}
+
+int cuda_fail(cudaError_t e, const char *where) {
+  return fail(SPARGE_ERR_CUDA, "%s: %s", where, cudaGetErrorString(e));
+}
+
 int *status_ptr() {
   void *p = nullptr;
   if (cudaGetSymbolAddress(&p, g_status_word) != cudaSuccess) return nullptr;
   return static_cast<int *>(p);
 }
-
-int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
-size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 int check_tensor(const sparge_tensor *t, const char *name, View *v) {
   if (!t) return fail(SPARGE_ERR_INVALID_ARG, "%s is NULL", name);
@@ -79,6 +82,13 @@ int check_tensor(const sparge_tensor *t, const char *name, View *v) {
   *v = View{t->data, t->B, t->H, t->N, t->d, sb, sh, sn};
   return SPARGE_OK;
 }
+
+}  // namespace sparge
+
+namespace {
+
+int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 // q may be shorter (or, without the causal mask, longer) than k; the causal case is checked where
 // the mask kind is known (check_lengths).
@@ -426,6 +436,77 @@ int attn_impl(const View &q, const View &k, const View &v, const uint8_t *mask, 
   return record_event(ev, 5, s);
 }
 
+// --- causal attention over a sliding window and the first tokens ---
+
+// Key blocks of one query tile at most: those of the first tokens and of the window of its Nq queries.
+int64_t window_blocks(int64_t Nq, int64_t Nk, int64_t window, int64_t sinks) {
+  const int64_t first = Nk - Nq - window + 1, lo = first > 0 ? first / KBLK : 0, ns = cdiv(sinks, KBLK);
+  return (ns < lo ? ns : lo) + cdiv(Nk, KBLK) - lo;
+}
+
+// Shares of a decoding call's key blocks, at most: the split of decode_split before its rounding,
+// which grows with the number of blocks, so a workspace sized for all Nk keys holds every window's.
+int64_t window_chunks(int64_t B, int64_t Hkv, int64_t blocks) {
+  const int64_t units = B * Hkv > 0 ? B * Hkv : 1, n = (304 + units - 1) / units, most = blocks / 16;
+  return n < most ? n : (most > 1 ? most : 1);
+}
+
+size_t window_ws_bytes(int64_t B, int64_t Hkv, int64_t Nk, int64_t d) {
+  const size_t rows = static_cast<size_t>(B * Hkv) * window_chunks(B, Hkv, cdiv(Nk, KBLK)) * 128;
+  const size_t part = align256(rows * d * 4) + align256(rows * 2 * 4), v16 = v16_bytes(B, Hkv, Nk, d);
+  return part > v16 ? part : v16;
+}
+
+int window_impl(const View &q, const View &k, const View &v, const View &o, int64_t window, int64_t sinks, float scale,
+                void *ws, size_t ws_bytes, cudaStream_t s) {
+  int rc;
+  const size_t need = window_ws_bytes(k.B, k.H, k.N, k.d);
+  if (ws_bytes < need || (need && !ws))
+    return fail(SPARGE_ERR_WORKSPACE_TOO_SMALL, "workspace %zu bytes, need %zu", ws_bytes, need);
+  if ((reinterpret_cast<uintptr_t>(ws) & 255u) != 0) return fail(SPARGE_ERR_INVALID_ARG, "workspace not 256-byte aligned");
+  if (q.B == 0 || q.N == 0) return SPARGE_OK;
+  if (window > k.N) window = k.N;  // a longer one hides nothing
+  if (sinks > k.N) sinks = k.N;
+  AttnLaunch l;
+  memset(&l, 0, sizeof(l));
+  const int64_t blocks = window_blocks(q.N, k.N, window, sinks);
+  if (q.H / k.H * q.N <= 128 && blocks >= 32) {  // decoding tiles, as in attn_impl: V in place as bf16
+    const DecodeSplit sp = decode_split(k.B, k.H, blocks * KBLK);
+    const size_t rows = static_cast<size_t>(k.B * k.H) * sp.nchunk * 128;
+    l.decode = 1;
+    l.nchunk = sp.nchunk;
+    l.chunk_blocks = sp.chunk_blocks;
+    l.part_o = static_cast<float *>(ws);
+    l.part_ml = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + align256(rows * q.d * 4));
+    if ((rc = make_map(&l.tv, v, 64, "v"))) return rc;
+  } else {
+    // the f16 copy of the V rows that are read: the first tokens' blocks and those from the first
+    // query's window on
+    const int64_t first = k.N - q.N - window + 1, lo = first > 0 ? first / KBLK * KBLK : 0;
+    const int64_t ns = cdiv(sinks, KBLK) * KBLK;
+    cudaError_t e = launch_convert_v_f16(v, ws, nullptr, status_ptr(), s, lo, k.N);
+    if (e == cudaSuccess && lo > 0 && ns > 0)
+      e = launch_convert_v_f16(v, ws, nullptr, status_ptr(), s, 0, ns < lo ? ns : lo);
+    if (e != cudaSuccess) return cuda_fail(e, "convert_v launch");
+    View v16{ws, v.B, v.H, v.N, v.d, v.H * v.N * v.d, v.N * v.d, v.d};
+    if ((rc = make_map(&l.tv, v16, 64, "v", CU_TENSOR_MAP_DATA_TYPE_FLOAT16))) return rc;
+  }
+  if ((rc = make_map(&l.tq, q, 128, "q")) || (rc = make_map(&l.tk, k, 64, "k"))) return rc;
+  l.q = q.data;
+  l.q_sb = q.sb; l.q_sh = q.sh; l.q_sn = q.sn;
+  l.o = const_cast<void *>(o.data);
+  l.o_sb = o.sb; l.o_sh = o.sh; l.o_sn = o.sn;
+  l.B = (int)q.B; l.Hq = (int)q.H; l.Hkv = (int)k.H; l.Nq = (int)q.N; l.Nk = (int)k.N; l.d = (int)q.d;
+  l.causal = 1;
+  l.scale = scale;
+  l.lambda = -INFINITY;
+  l.window = (int)window;
+  l.sinks = (int)sinks;
+  l.status = status_ptr();
+  cudaError_t e = launch_bsattn(l, s);
+  return e == cudaSuccess ? SPARGE_OK : cuda_fail(e, "window attention launch");
+}
+
 }  // namespace
 
 namespace sparge {
@@ -502,6 +583,8 @@ size_t sparge_workspace_bytes(int op, int64_t B, int64_t Hq, int64_t Hkv, int64_
     case SPARGE_OP_ATTN:
       return predict_ws_bytes(B, Hq, Hkv, N, N, d) + align256((size_t)B * Hq * cdiv(N, QBLK) * cdiv(N, KBLK)) +
              attn_ws_bytes(SPARGE_PRECISION_BF16, B, Hq, Hkv, N, N, d);
+    case SPARGE_OP_WINDOW_ATTN:
+      return window_ws_bytes(B, Hkv, N, d);
     case SPARGE_OP_BLOCK_SPARSE_ATTN_Q8:
       return attn_ws_bytes(SPARGE_PRECISION_Q8, B, Hq, Hkv, N, N, d);
     case SPARGE_OP_ATTN_Q8:
@@ -667,6 +750,24 @@ int sparge_attn(const sparge_tensor *q, const sparge_tensor *k, const sparge_ten
   p.stats = nullptr;
   p.timing_events = nullptr;
   return sparge_attn_ex(q, k, v, topk, is_causal, &p, o, nullptr, ws, ws_bytes, stream);
+}
+
+int sparge_window_attn(const sparge_tensor *q, const sparge_tensor *k, const sparge_tensor *v, int64_t window,
+                       int64_t sinks, float scale, sparge_tensor *o, void *ws, size_t ws_bytes, sparge_stream_t stream) {
+  clear_error();
+  View qv, kv, vv, ov;
+  int rc;
+  if ((rc = check_tensor(q, "q", &qv)) || (rc = check_tensor(k, "k", &kv)) || (rc = check_tensor(v, "v", &vv)) ||
+      (rc = check_tensor(o, "o", &ov)) || (rc = check_qk(qv, kv)) || (rc = check_lengths(qv, kv, 1)))
+    return rc;
+  if (vv.B != qv.B || vv.N != kv.N || vv.d != qv.d || vv.H != kv.H) return fail(SPARGE_ERR_INVALID_ARG, "v disagrees with q/k");
+  if (ov.B != qv.B || ov.N != qv.N || ov.d != qv.d || ov.H != qv.H) return fail(SPARGE_ERR_INVALID_ARG, "o disagrees with q");
+  if (window < 1 || sinks < 0)
+    return fail(SPARGE_ERR_INVALID_ARG, "window=%lld must be positive, sinks=%lld not negative", (long long)window, (long long)sinks);
+  if (std::isnan(scale) || scale < 0.f || std::isinf(scale))
+    return fail(SPARGE_ERR_INVALID_ARG, "scale must be finite and >= 0");
+  return window_impl(qv, kv, vv, ov, window, sinks, scale > 0.f ? scale : 1.f / sqrtf((float)qv.d), ws, ws_bytes,
+                     reinterpret_cast<cudaStream_t>(stream));
 }
 
 static int permute_common(const sparge_tensor *x, const int32_t *perm, sparge_tensor *y, bool inverse,

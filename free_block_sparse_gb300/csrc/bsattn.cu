@@ -65,6 +65,19 @@ struct AttnArgs {
   float *part_o, *part_ml;
   const int32_t *dlist;
   const int *dcount;
+  int window, sinks;  // WIN: row at position p sees keys c <= p with c > p - window or c < sinks
+};
+
+// Key blocks of a window (WIN) for the queries from position p0 on: the blocks of the first
+// `sinks` keys that lie in front of the window, then those from the first query's window on.
+struct WinBlocks {
+  int ns, lo;
+  __device__ __forceinline__ WinBlocks(int p0, int window, int sinks) {
+    const int first = p0 - window + 1;  // window >= 1: no overflow
+    lo = first > 0 ? first / KBLK : 0;
+    ns = min(lo, sinks / KBLK + (sinks % KBLK != 0 ? 1 : 0));
+  }
+  __device__ __forceinline__ int at(int t) const { return t < ns ? t : lo + t - ns; }
 };
 
 // Warp-collective walk over the kept, valid key blocks of one mask row in ascending order, run
@@ -165,7 +178,7 @@ struct Ctrl {
 };
 static_assert(sizeof(Ctrl) <= 512, "control block");
 
-template <int D, int KST, int VST, bool QK8, bool PV8, bool DEC>
+template <int D, int KST, int VST, bool QK8, bool PV8, bool DEC, bool WIN>
 __global__ void __launch_bounds__(NTHREADS, 2)
     bsattn_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                   const __grid_constant__ CUtensorMap tv, const AttnArgs a) {
@@ -274,15 +287,16 @@ __global__ void __launch_bounds__(NTHREADS, 2)
     // arrive without data).
     KeptScan ks;
     ks.init(mrow, n_valid);
+    const WinBlocks wb(a.off + QBLK * i, a.window, a.sinks);
     // decoding tile: share `chunk` of the (batch, KV head)'s kept-block list, [d_lo, d_hi)
     int d_lo = 0, d_hi = 0;
     const int32_t *dl = nullptr;
     if constexpr (DEC) {
       const int chunk = blockIdx.x % a.nchunk, bk = blockIdx.x / a.nchunk;
-      const int cnt = a.mask ? __ldg(a.dcount + bk) : a.nkb;
+      const int cnt = WIN ? wb.ns + a.nkb - wb.lo : a.mask ? __ldg(a.dcount + bk) : a.nkb;
       d_lo = static_cast<int>(static_cast<int64_t>(chunk) * cnt / a.nchunk);
       d_hi = static_cast<int>(static_cast<int64_t>(chunk + 1) * cnt / a.nchunk);
-      if (a.mask) dl = a.dlist + static_cast<int64_t>(bk) * a.nkb;
+      if (!WIN && a.mask) dl = a.dlist + static_cast<int64_t>(bk) * a.nkb;
     }
     if (lane == 0) {
       prefetch_tmap(&tq);
@@ -293,7 +307,9 @@ __global__ void __launch_bounds__(NTHREADS, 2)
     for (int t = 0;; ++t) {
       int j;
       if constexpr (DEC)
-        j = d_lo + t < d_hi ? (dl ? __ldg(dl + d_lo + t) : d_lo + t) : -1;
+        j = d_lo + t < d_hi ? (WIN ? wb.at(d_lo + t) : dl ? __ldg(dl + d_lo + t) : d_lo + t) : -1;
+      else if constexpr (WIN)
+        j = wb.at(t) < n_valid ? wb.at(t) : -1;
       else
         j = ks.next(lane);
       const int kst = t % KST, js = t % JRING;
@@ -579,7 +595,8 @@ __global__ void __launch_bounds__(NTHREADS, 2)
       // the vote makes the branch warp-uniform, so interior tiles skip the masking code entirely
       // (decoding tiles always take it: their rows have their own heads' masks)
       const bool edge = DEC || (a.causal && KBLK * j + KBLK - 1 > a.off + QBLK * i) || (KBLK * j + KBLK > a.Nk) ||
-                        (QBLK * i + QBLK > a.Nq);
+                        (QBLK * i + QBLK > a.Nq) ||
+                        (WIN && KBLK * j <= a.off + QBLK * i + QBLK - 1 - a.window && KBLK * j + KBLK > a.sinks);
       float mraw = mhw;
       if (__any_sync(0xffffffffu, edge)) {
         int lim = a.causal ? a.off + row_g - KBLK * j : 1 << 30;  // cols c > lim are hidden
@@ -590,6 +607,11 @@ __global__ void __launch_bounds__(NTHREADS, 2)
         }
 #pragma unroll
         for (int c = 0; c < 64; ++c) x[c] = (c > lim) ? -INFINITY : x[c];
+        if constexpr (WIN) {  // columns between the first keys and this row's window
+          const int low = a.off + row_g - a.window - KBLK * j, open = a.sinks - KBLK * j;
+#pragma unroll
+          for (int c = 0; c < 64; ++c) x[c] = (c <= low && c >= open) ? -INFINITY : x[c];
+        }
         // the maximum of what stays visible
         mraw = fmax3(x[0], x[1], x[2]);
 #pragma unroll
@@ -769,18 +791,18 @@ __global__ void __launch_bounds__(NTHREADS, 2)
   if (warp == 5) tmem_dealloc(tmem, TMEM_COLS);
 }
 
-template <int D, int KST, int VST, bool QK8, bool PV8, bool DEC = false>
+template <int D, int KST, int VST, bool QK8, bool PV8, bool DEC = false, bool WIN = false>
 cudaError_t launch_t(const AttnLaunch &l, const AttnArgs &a, cudaStream_t st) {
   // each CTA allocates 256 TMEM columns, half of the SM's: at least 77 KB of shared memory keeps a
   // third CTA off the SM (it would only wait in tcgen05.alloc)
   constexpr uint32_t MIN_SMEM = 77u * 1024u;
   const uint32_t smem = Smem<D, KST, VST, QK8, PV8>::TOTAL > MIN_SMEM ? Smem<D, KST, VST, QK8, PV8>::TOTAL : MIN_SMEM;
   static std::atomic<unsigned long long> smem_set{0};
-  if (cudaError_t e = set_smem_limit_once(bsattn_kernel<D, KST, VST, QK8, PV8, DEC>, static_cast<int>(smem), smem_set);
+  if (cudaError_t e = set_smem_limit_once(bsattn_kernel<D, KST, VST, QK8, PV8, DEC, WIN>, static_cast<int>(smem), smem_set);
       e != cudaSuccess)
     return e;
   const int64_t grid = DEC ? static_cast<int64_t>(a.B) * a.Hkv * a.nchunk : static_cast<int64_t>(a.B) * a.Hq * a.nqb;
-  bsattn_kernel<D, KST, VST, QK8, PV8, DEC><<<static_cast<unsigned>(grid), NTHREADS, smem, st>>>(l.tq, l.tk, l.tv, a);
+  bsattn_kernel<D, KST, VST, QK8, PV8, DEC, WIN><<<static_cast<unsigned>(grid), NTHREADS, smem, st>>>(l.tq, l.tk, l.tv, a);
   return cudaGetLastError();
 }
 
@@ -811,6 +833,8 @@ cudaError_t launch_bsattn(const AttnLaunch &l, cudaStream_t st) {
   a.q = static_cast<const __nv_bfloat16 *>(l.q);
   a.q_sb = l.q_sb; a.q_sh = l.q_sh; a.q_sn = l.q_sn;
   a.qperm = l.qperm;
+  a.window = l.window;
+  a.sinks = l.sinks;
   if (static_cast<int64_t>(a.B) * a.Hq * a.nqb == 0) return cudaSuccess;
   if (l.q8 != 0 && l.d != 128) return cudaErrorInvalidValue;
   if (l.decode) {  // bf16 only: the host picks this path for few queries per head, lambda off
@@ -821,17 +845,27 @@ cudaError_t launch_bsattn(const AttnLaunch &l, cudaStream_t st) {
     a.part_ml = l.part_ml;
     a.dlist = l.dlist;
     a.dcount = l.dcount;
-    if (a.mask) {
+    if (a.mask && !l.window) {
       if (!l.dlist || !l.dcount) return cudaErrorInvalidValue;
       if (cudaError_t e = launch_decode_union(a.mask, a.B, a.Hq, a.Hkv, a.nqb, a.nkb, l.dlist, l.dcount, st);
           e != cudaSuccess)
         return e;
     }
-    cudaError_t e = l.d == 128 ? launch_t<128, 3, 2, false, false, true>(l, a, st)
-                               : launch_t<64, 4, 3, false, false, true>(l, a, st);
+    cudaError_t e;
+    if (l.window)
+      e = l.d == 128 ? launch_t<128, 3, 2, false, false, true, true>(l, a, st)
+                     : launch_t<64, 4, 3, false, false, true, true>(l, a, st);
+    else
+      e = l.d == 128 ? launch_t<128, 3, 2, false, false, true>(l, a, st)
+                     : launch_t<64, 4, 3, false, false, true>(l, a, st);
     if (e != cudaSuccess) return e;
     return launch_decode_combine(l.part_o, l.part_ml, l.nchunk, a.B, a.Hq, a.Hkv, a.Nq, l.d, a.o, a.o_sb, a.o_sh, a.o_sn,
                                  st);
+  }
+  if (l.window) {  // bf16, causal, no block mask: the host sees to it
+    if (l.q8 != 0 || !l.causal || l.mask) return cudaErrorInvalidValue;
+    return l.d == 128 ? launch_t<128, 3, 2, false, false, false, true>(l, a, st)
+                      : launch_t<64, 4, 3, false, false, false, true>(l, a, st);
   }
   if (l.q8 == 3) return launch_t<128, 3, 3, false, true>(l, a, st);  // bf16 Q.K^T, e4m3 P.V
   if (l.q8 == 2) return launch_t<128, 4, 3, true, true>(l, a, st);

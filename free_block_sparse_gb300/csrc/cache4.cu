@@ -1,0 +1,389 @@
+// The 4-bit key/value cache: storing tokens, reading them back, and the tables of its pages.
+//
+// Store: each token's 64-channel groups of K and V become 4-bit codes,
+//   minimum = min x, scale = bf16((max x - min x) / 15), n = round((x - minimum) / scale) in 0..15
+// (rounded to even; scale 0: n = 0), and go to the token's slot (page * page_size + place in the page).
+// The minimum is a bf16 input and stays exact; the scale is rounded before the codes are taken, so
+// the codes are nearest to what the cache will read back.  A group with an infinity or a NaN gets a
+// NaN scale and minimum: it reads back as NaN instead of a plausible number.
+// Load: x^ = n * scale + minimum (one rounding to bf16) from the slots.
+// Both are bound by memory: 2 d bytes of bf16 and 9 d/16 bytes of cache per token, head and side.
+#include <climits>
+#include <cmath>
+
+#include "../../include/sparge.h"
+#include "cache4.cuh"
+#include "common.cuh"
+#include "kernels.h"
+
+namespace sparge {
+namespace {
+
+struct Rows4 {  // K and V rows and the cache they go to or come from
+  const __nv_bfloat16 *x[2];
+  __nv_bfloat16 *y[2];
+  int64_t sb[2], sh[2], sn[2];
+  const int64_t *slots;
+  uint8_t *pool;
+  int64_t n_slots;
+  int page_shift, H, N, B, recs;  // recs: records of a page
+  int *status;
+};
+
+__device__ __forceinline__ uint8_t *record_of(const Rows4 &a, int64_t slot, int h, int bytes) {
+  const int64_t page = slot >> a.page_shift;
+  const int g = static_cast<int>(slot & ((1 << a.page_shift) - 1)) / C4_TOKENS;
+  return a.pool + ((page * a.H + h) * a.recs + g) * static_cast<int64_t>(bytes);
+}
+
+// Codes of a thread's 8 channels (nibble j: channel j) and its group's word; the 8 threads of a
+// group are adjacent lanes.
+__device__ __forceinline__ uint32_t quantise8(uint4 v, uint32_t &word) {
+  float f[8] = {bf16lo(v.x), bf16hi(v.x), bf16lo(v.y), bf16hi(v.y), bf16lo(v.z), bf16hi(v.z), bf16lo(v.w), bf16hi(v.w)};
+  float lo = f[0], hi = f[0];
+  bool fine = fabsf(f[0]) <= 3.4028235e38f;
+#pragma unroll
+  for (int j = 1; j < 8; ++j) {
+    lo = fminf(lo, f[j]);
+    hi = fmaxf(hi, f[j]);
+    fine = fine && fabsf(f[j]) <= 3.4028235e38f;
+  }
+  const uint32_t bad = __ballot_sync(0xffffffffu, !fine);
+#pragma unroll
+  for (int off = 4; off > 0; off >>= 1) {
+    lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, off));
+    hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, off));
+  }
+  const int lane = threadIdx.x & 31;
+  if ((bad >> (lane & 24)) & 0xFFu) {
+    word = 0x7FC07FC0u;
+    return 0u;
+  }
+  // a difference beyond fp32 (bf16 values near 3e38 of both signs) is held at the largest fp32
+  const float range = fminf(hi - lo, 3.4028235e38f);
+  const uint32_t sbits = pack_bf16x2(__fdiv_rn(range, 15.f), 0.f) & 0xFFFFu;
+  const float s = __uint_as_float(sbits << 16);
+  word = sbits | (__float_as_uint(lo) & 0xFFFF0000u);
+  uint32_t n = 0u;
+  if (s > 0.f) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float q = fminf(fmaxf(rintf(__fdiv_rn(f[j] - lo, s)), 0.f), 15.f);
+      n |= static_cast<uint32_t>(static_cast<int>(q)) << (4 * j);
+    }
+  }
+  return n;
+}
+
+// Byte of V codes that holds channels 16 (i / 2) + g (low) and + 8 (high) of token t, i = channel / 8.
+__device__ __forceinline__ int v_byte(int t, int i, int g) {
+  const int u = i >> 1;
+  return (u >> 2) * 512 + (4 * g + ((t & 7) >> 1)) * 16 + (u & 3) * 4 + ((t & 1) << 1) + (t >> 3);
+}
+
+// Writes a thread's 8 channels (piece i of token t's row) of K or V into a record, in global or
+// shared memory.  Called by all threads of a row together (V bytes join two threads' nibbles).
+template <int D>
+__device__ __forceinline__ void put8(uint8_t *rec, bool v, int t, int i, uint32_t n, uint32_t word, bool live) {
+  using R = Rec4<D>;
+  const uint32_t other = __shfl_xor_sync(0xffffffffu, n, 1);
+  if (!live) return;
+  if (!v) {
+    *reinterpret_cast<uint32_t *>(rec + R::K + t * (D / 2) + (i & 3) * (D / 8) + (i >> 2) * 4) = n;
+  } else {
+    const uint32_t lo = (i & 1) ? other : n, hi = (i & 1) ? n : other;
+    const int g0 = (i & 1) ? 4 : 0;
+#pragma unroll
+    for (int g = 0; g < 4; ++g)
+      rec[R::V + v_byte(t, i, g0 + g)] =
+          static_cast<uint8_t>(((lo >> (4 * (g0 + g))) & 15u) | (((hi >> (4 * (g0 + g))) & 15u) << 4));
+  }
+  if ((i & 7) == 0) *reinterpret_cast<uint32_t *>(rec + (v ? R::VW : R::KW) + (t * R::NG + (i >> 3)) * 4) = word;
+}
+
+// A thread's 8 channels back from a record.
+template <int D>
+__device__ __forceinline__ uint4 get8(const uint8_t *rec, bool v, int t, int i) {
+  using R = Rec4<D>;
+  uint32_t n = 0u;
+  if (!v) {
+    n = *reinterpret_cast<const uint32_t *>(rec + R::K + t * (D / 2) + (i & 3) * (D / 8) + (i >> 2) * 4);
+  } else {
+#pragma unroll
+    for (int g = 0; g < 8; ++g) n |= ((static_cast<uint32_t>(rec[R::V + v_byte(t, i, g)]) >> ((i & 1) * 4)) & 15u) << (4 * g);
+  }
+  const uint32_t word = *reinterpret_cast<const uint32_t *>(rec + (v ? R::VW : R::KW) + (t * R::NG + (i >> 3)) * 4);
+  const float s = bf16lo(word), m = bf16hi(word);
+  float f[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) f[j] = fmaf(static_cast<float>((n >> (4 * j)) & 15u), s, m);
+  return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+}
+
+// The slot of token m; negative: padding (the token is left out).  A slot past the pool is never
+// used as an address: it is reported and left out.
+__device__ __forceinline__ int64_t slot_of(const Rows4 &a, int64_t m, bool report) {
+  const int64_t s = __ldg(a.slots + m);
+  if (s >= a.n_slots) {
+    if (report) record_status(a.status, -1 /* SPARGE_ERR_INVALID_ARG */);
+    return -1;
+  }
+  return s;
+}
+
+// One row (token, head) per D / 8 threads, K and V by blockIdx.y.
+template <int D, bool LOAD>
+__global__ void __launch_bounds__(256) rows4_kernel(const Rows4 a) {
+  constexpr int TR = D / 8;
+  const int side = blockIdx.y, i = threadIdx.x % TR;
+  const int64_t row = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) / TR;
+  const int64_t m = row / a.H;
+  const int h = static_cast<int>(row % a.H);
+  const bool in = m < static_cast<int64_t>(a.B) * a.N;
+  const int64_t slot = in ? slot_of(a, m, i == 0 && h == 0 && side == 0) : -1;
+  const int b = in ? static_cast<int>(m / a.N) : 0, n = in ? static_cast<int>(m % a.N) : 0;
+  const int64_t at = b * a.sb[side] + h * a.sh[side] + n * a.sn[side] + 8 * i;
+  const bool live = slot >= 0;
+  uint8_t *rec = record_of(a, live ? slot : 0, h, Rec4<D>::BYTES);
+  const int t = static_cast<int>(slot & 15);
+  if (LOAD) {
+    if (live) *reinterpret_cast<uint4 *>(a.y[side] + at) = get8<D>(rec, side != 0, t, i);
+  } else {
+    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+    if (live) v = ld_stream_v4(a.x[side] + at);
+    uint32_t word;
+    const uint32_t c = quantise8(v, word);
+    put8<D>(rec, side != 0, t, i, c, word, live);
+  }
+}
+
+}  // namespace
+
+// Pool rules: page sizes 16, 32, 64, 128 or 256, d 64 or 128, 16-byte aligned.
+int check_cache4(const sparge_cache4 *c, Cache4 *out) {
+  if (!c) return fail(SPARGE_ERR_INVALID_ARG, "cache is NULL");
+  if (c->d != 64 && c->d != 128) return fail(SPARGE_ERR_UNSUPPORTED, "cache: head dim %d not in {64,128}", c->d);
+  if (c->page_size < 16 || c->page_size > 256 || (c->page_size & (c->page_size - 1)))
+    return fail(SPARGE_ERR_UNSUPPORTED, "cache: page_size %d not in {16,32,64,128,256}", c->page_size);
+  if (c->n_pages < 0 || c->H <= 0) return fail(SPARGE_ERR_INVALID_ARG, "cache: bad shape n_pages=%lld H=%d", (long long)c->n_pages, c->H);
+  if (c->n_pages > INT32_MAX || c->H > 65535) return fail(SPARGE_ERR_UNSUPPORTED, "cache: too large");
+  if (!c->data && c->n_pages) return fail(SPARGE_ERR_INVALID_ARG, "cache->data is NULL");
+  if (reinterpret_cast<uintptr_t>(c->data) & 15u) return fail(SPARGE_ERR_INVALID_ARG, "cache->data not 16-byte aligned");
+  out->data = static_cast<uint8_t *>(c->data);
+  out->n_pages = c->n_pages;
+  out->page_size = c->page_size;
+  out->page_shift = 0;
+  while ((1 << out->page_shift) < c->page_size) ++out->page_shift;
+  out->H = c->H;
+  out->d = c->d;
+  return SPARGE_OK;
+}
+
+namespace {
+
+int rows4(const sparge_tensor *k, const sparge_tensor *v, const int64_t *slots, const sparge_cache4 *cache, bool load,
+          sparge_stream_t stream) {
+  clear_error();
+  View x[2];
+  Cache4 c;
+  int rc;
+  if ((rc = check_tensor(k, "k", &x[0])) || (rc = check_tensor(v, "v", &x[1])) || (rc = check_cache4(cache, &c))) return rc;
+  if (x[0].B != x[1].B || x[0].H != x[1].H || x[0].N != x[1].N || x[0].d != x[1].d)
+    return fail(SPARGE_ERR_INVALID_ARG, "k and v have different shapes");
+  if (x[0].H != c.H || x[0].d != c.d) return fail(SPARGE_ERR_INVALID_ARG, "k and v disagree with the cache in H or d");
+  if (x[0].B * x[0].N == 0) return SPARGE_OK;
+  if (!slots) return fail(SPARGE_ERR_INVALID_ARG, "slots is NULL");
+  Rows4 a;
+  for (int s = 0; s < 2; ++s) {
+    a.x[s] = static_cast<const __nv_bfloat16 *>(x[s].data);
+    a.y[s] = static_cast<__nv_bfloat16 *>(const_cast<void *>(x[s].data));
+    a.sb[s] = x[s].sb; a.sh[s] = x[s].sh; a.sn[s] = x[s].sn;
+  }
+  a.slots = slots;
+  a.pool = c.data;
+  a.n_slots = c.n_pages * c.page_size;
+  a.page_shift = c.page_shift;
+  a.H = c.H; a.N = static_cast<int>(x[0].N); a.B = static_cast<int>(x[0].B);
+  a.recs = c.page_size / C4_TOKENS;
+  a.status = status_ptr();
+  const int64_t rows = x[0].B * x[0].N * c.H, per = 256 / (c.d / 8), ctas = (rows + per - 1) / per;
+  if (ctas > INT32_MAX) return fail(SPARGE_ERR_UNSUPPORTED, "too many tokens");
+  const dim3 grid(static_cast<unsigned>(ctas), 2);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (c.d == 128) {
+    if (load) rows4_kernel<128, true><<<grid, 256, 0, s>>>(a);
+    else rows4_kernel<128, false><<<grid, 256, 0, s>>>(a);
+  } else {
+    if (load) rows4_kernel<64, true><<<grid, 256, 0, s>>>(a);
+    else rows4_kernel<64, false><<<grid, 256, 0, s>>>(a);
+  }
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? SPARGE_OK : cuda_fail(e, load ? "cache load launch" : "cache store launch");
+}
+
+// --------------------------------------------------------------------------------------------
+// Tables.  One launch: every CTA sums the pages that the requests before its own need, so no
+// pass over the requests precedes it (a few thousand lengths come from L2 faster than a second
+// launch starts), then writes its requests' new table entries, slots and positions.  Nothing is
+// read that another CTA writes: a slot on a new page takes it from the free list itself.
+// --------------------------------------------------------------------------------------------
+struct TablesArgs {
+  const int32_t *lens, *new_lens, *free_pages;
+  int32_t *table, *positions, *kv_lens, *used;
+  int64_t *slots;
+  int64_t stride;
+  int R, N, width, n_free, shift, chunk;  // chunk: requests of a CTA
+  int *status;
+};
+
+constexpr int TB_THREADS = 256;
+constexpr int TB_CHUNK = 512;  // most requests of a CTA
+
+struct Request {
+  int64_t len, add;
+  int have, need;  // pages held before, pages taken now
+  bool bad;
+};
+
+__device__ __forceinline__ Request request_of(const TablesArgs &a, int r) {
+  Request q;
+  const int len = __ldg(a.lens + r), add = __ldg(a.new_lens + r);
+  q.bad = len < 0 || add < 0 || add > a.N || static_cast<int64_t>(len) + add > INT32_MAX;
+  q.len = q.bad ? 0 : len;
+  q.add = q.bad ? 0 : add;
+  const int64_t p = (int64_t(1) << a.shift) - 1;
+  q.have = static_cast<int>((q.len + p) >> a.shift);
+  q.need = static_cast<int>((q.len + q.add + p) >> a.shift) - q.have;
+  return q;
+}
+
+__global__ void __launch_bounds__(TB_THREADS) cache_tables_kernel(const TablesArgs a) {
+  __shared__ int64_t part[TB_THREADS / 32];
+  __shared__ int64_t first[TB_CHUNK + 1];
+  const int r0 = blockIdx.x * a.chunk, r1 = min(a.R, r0 + a.chunk);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int64_t sum = 0;
+  for (int r = threadIdx.x; r < r0; r += TB_THREADS) sum += request_of(a, r).need;
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+  if (lane == 0) part[warp] = sum;
+  __syncthreads();
+  if (warp == 0) {  // exclusive sums over the CTA's own requests
+    int64_t base = 0;
+    for (int u = 0; u < TB_THREADS / 32; ++u) base += part[u];
+    for (int r = r0; r < r1; r += 32) {
+      const int64_t need = r + lane < r1 ? request_of(a, r + lane).need : 0;
+      int64_t inc = need;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int64_t o = __shfl_up_sync(0xffffffffu, inc, off);
+        if (lane >= off) inc += o;
+      }
+      if (r + lane < r1) first[r + lane - r0] = base + inc - need;
+      base += __shfl_sync(0xffffffffu, inc, 31);
+    }
+    if (lane == 0 && blockIdx.y == 0 && r1 == a.R && a.used) {
+      *a.used = static_cast<int>(base < INT_MAX ? base : INT_MAX);
+    }
+  }
+  __syncthreads();
+  // new token places n of requests r0..r1, this CTA's share of the N
+  const int per = (a.N + static_cast<int>(gridDim.y) - 1) / static_cast<int>(gridDim.y);
+  const int n0 = min(a.N, static_cast<int>(blockIdx.y) * per), cnt = min(per, a.N - n0);
+  const int64_t items = static_cast<int64_t>(r1 - r0) * cnt;
+  const int64_t mask = (int64_t(1) << a.shift) - 1;
+  for (int64_t e = threadIdx.x; e < items; e += TB_THREADS) {
+    const int k = static_cast<int>(e / cnt), r = r0 + k, n = n0 + static_cast<int>(e % cnt);
+    const Request q = request_of(a, r);
+    const int64_t pos = q.len + n - (a.N - q.add);
+    int64_t slot = -1;
+    int32_t where = -1;
+    if (n >= a.N - q.add) {
+      where = static_cast<int32_t>(pos);
+      const int64_t col = pos >> a.shift;
+      int64_t page = -1;
+      if (col < a.width) {
+        if (col < q.have) page = a.table[r * a.stride + col];
+        else if (first[k] + col - q.have < a.n_free) page = __ldg(a.free_pages + first[k] + col - q.have);
+      }
+      if (page >= 0) slot = (page << a.shift) + (pos & mask);
+    }
+    if (a.slots) a.slots[static_cast<int64_t>(r) * a.N + n] = slot;
+    if (a.positions) a.positions[static_cast<int64_t>(r) * a.N + n] = where;
+  }
+  if (blockIdx.y != 0) return;
+  for (int k = warp; k < r1 - r0; k += TB_THREADS / 32) {
+    const int r = r0 + k;
+    const Request q = request_of(a, r);
+    if (lane == 0) {
+      if (a.kv_lens) a.kv_lens[r] = static_cast<int32_t>(q.len + q.add);
+      if (q.bad || q.have + q.need > a.width) record_status(a.status, -1 /* SPARGE_ERR_INVALID_ARG */);
+    }
+    for (int j = lane; j < q.need && q.have + j < a.width; j += 32)
+      a.table[r * a.stride + q.have + j] = first[k] + j < a.n_free ? __ldg(a.free_pages + first[k] + j) : -1;
+  }
+}
+
+}  // namespace
+}  // namespace sparge
+
+using namespace sparge;
+
+extern "C" {
+
+size_t sparge_cache4_bytes(int64_t n_pages, int page_size, int H, int d) {
+  if (n_pages < 0 || n_pages > INT32_MAX || H <= 0 || H > 65535 || (d != 64 && d != 128) || page_size < 16 ||
+      page_size > 256 || (page_size & (page_size - 1)))
+    return 0;
+  return static_cast<size_t>(n_pages) * H * (page_size / C4_TOKENS) * (18 * static_cast<size_t>(d));
+}
+
+int sparge_cache4_store(const sparge_tensor *k, const sparge_tensor *v, const int64_t *slots, const sparge_cache4 *cache,
+                        sparge_stream_t stream) {
+  return rows4(k, v, slots, cache, false, stream);
+}
+
+int sparge_cache4_load(const sparge_cache4 *cache, const int64_t *slots, sparge_tensor *k, sparge_tensor *v,
+                       sparge_stream_t stream) {
+  return rows4(k, v, slots, cache, true, stream);
+}
+
+int sparge_cache_tables(const int32_t *lens, const int32_t *new_lens, int64_t R, int64_t N, int page_size,
+                        const int32_t *free_pages, int64_t n_free, int32_t *table, int64_t width, int64_t table_stride,
+                        int64_t *slots, int32_t *positions, int32_t *kv_lens, int32_t *used, sparge_stream_t stream) {
+  clear_error();
+  if (R < 0 || N < 0 || width < 0 || n_free < 0 || table_stride < width)
+    return fail(SPARGE_ERR_INVALID_ARG, "bad shape R=%lld N=%lld width=%lld table_stride=%lld n_free=%lld", (long long)R,
+                (long long)N, (long long)width, (long long)table_stride, (long long)n_free);
+  if (page_size < 16 || page_size > 256 || (page_size & (page_size - 1)))
+    return fail(SPARGE_ERR_UNSUPPORTED, "page_size %d not in {16,32,64,128,256}", page_size);
+  if (R > 65535 || N > (int64_t(1) << 30) || width > INT32_MAX || n_free > INT32_MAX)
+    return fail(SPARGE_ERR_UNSUPPORTED, "shape too large");
+  if (R > 0 && (!lens || !new_lens)) return fail(SPARGE_ERR_INVALID_ARG, "lens or new_lens is NULL");
+  if (R > 0 && width > 0 && !table) return fail(SPARGE_ERR_INVALID_ARG, "table is NULL");
+  if (n_free > 0 && !free_pages) return fail(SPARGE_ERR_INVALID_ARG, "free_pages is NULL");
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  TablesArgs a;
+  a.lens = lens; a.new_lens = new_lens; a.free_pages = free_pages;
+  a.table = table; a.positions = positions; a.kv_lens = kv_lens; a.used = used;
+  a.slots = slots;
+  a.stride = table_stride;
+  a.R = static_cast<int>(R); a.N = static_cast<int>(N); a.width = static_cast<int>(width); a.n_free = static_cast<int>(n_free);
+  a.shift = 0;
+  while ((1 << a.shift) < page_size) ++a.shift;
+  a.status = status_ptr();
+  // requests of a CTA: one until the CTAs outnumber two for each of the 152 SMs
+  int64_t chunk = (R + 303) / 304;
+  if (chunk < 1) chunk = 1;
+  a.chunk = static_cast<int>(chunk);
+  const int64_t gx = R > 0 ? (R + chunk - 1) / chunk : 1;
+  int64_t gy = chunk * N / (4 * TB_THREADS);  // about 4 places per thread
+  const int64_t most = 4 * 152 / gx;
+  gy = gy > most ? most : gy;
+  gy = gy < 1 ? 1 : gy;
+  cache_tables_kernel<<<dim3(static_cast<unsigned>(gx), static_cast<unsigned>(gy)), TB_THREADS, 0, s>>>(a);
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? SPARGE_OK : cuda_fail(e, "cache tables launch");
+}
+
+}  // extern "C"

@@ -1,0 +1,733 @@
+// Attention over the paged 4-bit cache (decoding steps and short chunks).
+//
+//   O = softmax(scale Q K^^T) V^,  K^, V^ = code * scale + minimum per token and 64 channels,
+// causal with the last query on the last token of its sequence, optionally over a window and a few
+// first tokens.  Each cache byte is read once per tile of 8 or 16 query rows (the Nq rows of all heads
+// of a KV head), so for a decoding step memory bounds it: 18 d / 16 bytes per token and KV head.
+//
+// The products run on mma.sync with the codes as they lie in memory: a 4-bit code in the low bits of
+// an f16 is the subnormal code * 2^-24 (bits 4-7: code * 2^-20), so two ANDs and one shift per 4
+// codes make the operands - no conversion, no subtraction of a bias - and scales and minima enter in
+// fp32 on the small side, where each applies to a whole 64-channel dot product.  tcgen05 would want
+// the codes widened into shared memory first, 4 times their size through a port that then feeds
+// the tensor core from it again; for 1 to 16 rows that traffic, not the products, would bound it.
+//   S^T = K^ Q^T: A = 16 tokens x 16 channels of codes, B = Q^T (f16, each row scaled by a power of two
+//         to a maximum in [2^14, 2^15), so its 8 significant bits stay whole down to 2^-29 of it).
+//         x = k (sum_g s_g acc_g) + sum_g m_g (scale * sum of q over group g).
+//   O^T = V^T P^T: A = 16 channels x 16 tokens of codes, B = P^T s (f16: 11 bits, an eighth of the
+//         output's rounding) transposed in registers by movmatrix; the minima add sum P m per row.
+// P lies in [0, 2^8] (the reference follows the running maximum lazily) and s is scaled by a power
+// of two that follows its running maximum the same way, so P s stays in f16's range.
+//
+// Work: the (sequence, KV head, row tile) items' 64-token tiles in one line, cut into equal shares,
+// one per CTA (4 CTAs per SM), so ragged lengths fill the part evenly; every CTA sums the lengths
+// itself.  A warp takes every fourth 16-token record of its CTA's share through a ring of its own
+// of bulk copies, without any synchronisation among warps until an item ends; then the four warps'
+// sums are merged in shared memory, and an item cut between CTAs is put together by a second
+// kernel.
+#include <climits>
+#include <cmath>
+
+#include "../../include/sparge.h"
+#include "cache4.cuh"
+#include "common.cuh"
+#include "kernels.h"
+
+namespace sparge {
+int check_cache4(const ::sparge_cache4 *c, Cache4 *out);
+namespace {
+
+constexpr int CA_WARPS = 4;
+constexpr int CA_STAGES = 4;     // records in flight per warp
+constexpr int CA_SMS = 152;
+constexpr float CA_RESCALE = 8.f;  // the exponent reference moves when a score passes it by more (log2)
+constexpr float CA_SBOUND = 64.f;  // scaled V scales stay below this: P s < 2^8 2^6 < 65504
+
+struct CacheAttnArgs {
+  const __nv_bfloat16 *q;
+  __nv_bfloat16 *o;
+  int64_t q_sb, q_sh, q_sn, o_sb, o_sh, o_sn;
+  const uint8_t *pool;
+  const int32_t *table, *lens;
+  int64_t table_stride, n_pages;
+  int width, rec_shift;  // records of a page: 1 << rec_shift
+  int B, Hq, Hkv, G, Nq, rows, ntile;
+  int window, sinks;     // window 0: none
+  float scale_log2;
+  float *part_o, *part_ml;
+  int2 *ends;            // per item: first and last CTA
+  int *status;
+};
+
+// The records a sequence's queries see: the first `ns` (tokens that stay visible), then lo..hi-1.
+struct Span {
+  int len, ns, lo, recs;
+};
+__device__ __forceinline__ Span span_of(const CacheAttnArgs &a, int b) {
+  Span s;
+  int len = __ldg(a.lens + b);
+  const int64_t cap = static_cast<int64_t>(a.width) << (a.rec_shift + 4);
+  if (len > cap) len = static_cast<int>(cap);
+  s.len = max(len, 0);
+  const int hi = static_cast<int>((static_cast<int64_t>(s.len) + 15) >> 4);
+  s.ns = 0;
+  s.lo = 0;
+  if (a.window > 0) {
+    const int64_t first = static_cast<int64_t>(s.len) - a.Nq - a.window + 1;
+    s.lo = first > 0 ? static_cast<int>(first >> 4) : 0;
+    s.ns = min(s.lo, static_cast<int>((static_cast<int64_t>(a.sinks) + 15) >> 4));
+  }
+  s.recs = s.ns + hi - s.lo;
+  return s;
+}
+__device__ __forceinline__ int64_t units_of(const CacheAttnArgs &a, int b) {
+  return static_cast<int64_t>((span_of(a, b).recs + 3) >> 2) * (a.Hkv * a.ntile);
+}
+
+__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+// two floats to f16x2 without saturation: an infinity or a NaN stays one
+__device__ __forceinline__ uint32_t half2_of(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// 2^e for a whole e in -126..127
+__device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }
+// exponent of |x| (0 and subnormals: -127)
+__device__ __forceinline__ int exponent_of(float x) { return static_cast<int>((__float_as_uint(x) >> 23) & 0xFFu) - 127; }
+
+template <int D, int RT>
+struct CaSmem {
+  static constexpr int REC = Rec4<D>::BYTES;
+  static constexpr int RING = CA_WARPS * CA_STAGES * REC;
+  static constexpr int OROW = D + 4;  // floats of a merge row, padded against bank conflicts
+  static constexpr int MERGE = CA_WARPS * 8 * RT * OROW * 4;
+  static constexpr int OFF_MERGE = RING, OFF_ML = OFF_MERGE + MERGE, OFF_CTRL = OFF_ML + CA_WARPS * 8 * RT * 8;
+  static constexpr int TOTAL = OFF_CTRL + 512;
+};
+struct CaCtrl {
+  uint64_t full[CA_WARPS][CA_STAGES];
+  int64_t sums[CA_WARPS];
+  int64_t off;
+  int b0, abort;
+  uint8_t bad[CA_WARPS][CA_STAGES];  // the stage's page lies outside the pool: its tokens are left out
+};
+static_assert(sizeof(CaCtrl) <= 512, "control block");
+
+template <int D, int RT>
+__global__ void __launch_bounds__(CA_WARPS * 32, RT == 1 ? 4 : 3) cache4_attn_kernel(const CacheAttnArgs a) {
+  using S = CaSmem<D, RT>;
+  using R = Rec4<D>;
+  constexpr int NG = D / 64, NW = D / 32, MT = D / 16;
+  extern __shared__ __align__(128) uint8_t smem[];
+  CaCtrl &cs = *reinterpret_cast<CaCtrl *>(smem + S::OFF_CTRL);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+  uint8_t *ring = smem + warp * CA_STAGES * S::REC;
+
+  // ---- this CTA's share [start, end) of the line of tiles, and the sequence it starts in ----
+  const int per = (a.B + CA_WARPS * 32 - 1) / (CA_WARPS * 32);
+  const int bt = min(a.B, static_cast<int>(threadIdx.x) * per), bu = min(a.B, bt + per);
+  int64_t own = 0;
+  for (int b = bt; b < bu; ++b) own += units_of(a, b);
+  int64_t inc = own;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int64_t o = __shfl_up_sync(0xffffffffu, inc, off);
+    if (lane >= off) inc += o;
+  }
+  if (lane == 31) cs.sums[warp] = inc;
+  if (threadIdx.x == 0) {
+    cs.abort = 0;
+    for (int w = 0; w < CA_WARPS; ++w)
+      for (int s = 0; s < CA_STAGES; ++s) mbar_init(&cs.full[w][s], 1);
+    fence_barrier_init();
+  }
+  __syncthreads();
+  int64_t total = 0, before = inc - own;
+#pragma unroll
+  for (int w = 0; w < CA_WARPS; ++w) {
+    before += w < warp ? cs.sums[w] : 0;
+    total += cs.sums[w];
+  }
+  // shares only for as many CTAs as there are tiles: between an item's first and last CTA each holds some of it
+  const int64_t shares = total < gridDim.x ? total : gridDim.x;
+  if (blockIdx.x >= shares) return;
+  const int64_t start = total * blockIdx.x / shares, end = total * (blockIdx.x + 1) / shares;
+  if (before <= start && start < before + own) {
+    int b = bt;
+    int64_t at = before;
+    for (;; ++b) {
+      const int64_t u = units_of(a, b);
+      if (start < at + u) break;
+      at += u;
+    }
+    cs.b0 = b;
+    cs.off = start - at;
+  }
+  __syncthreads();
+  int b = cs.b0;
+  int64_t off = cs.off, left = end - start;
+  uint32_t used = 0;  // records this warp has taken through its ring (stage used % STAGES)
+
+  while (left > 0) {
+    const Span sp = span_of(a, b);
+    const int tiles = (sp.recs + 3) >> 2;
+    const int64_t units = static_cast<int64_t>(tiles) * (a.Hkv * a.ntile);
+    if (off >= units) {
+      off -= units;
+      ++b;
+      continue;
+    }
+    const int in_b = static_cast<int>(off / tiles), tile0 = static_cast<int>(off % tiles);
+    const int nt = static_cast<int>(left < tiles - tile0 ? left : tiles - tile0);
+    const int kvh = in_b / a.ntile, rt = in_b % a.ntile;
+    const int item = b * (a.Hkv * a.ntile) + in_b;
+    const int row0 = rt * 8 * RT;
+
+    // ---- the copies: this warp's records tile0 * 4 + warp, + 4, ... ----
+    const int k0 = tile0 * 4 + warp, kend = min(sp.recs, (tile0 + nt) * 4);
+    const int nrec = kend > k0 ? (kend - k0 + 3) >> 2 : 0;
+    const int32_t *trow = a.table + static_cast<int64_t>(b) * a.table_stride;
+    int pages = 0, pbase = -32;  // page of record i of this warp: lane i - pbase
+    auto record_at = [&](int i) {
+      const int k = k0 + 4 * i;
+      return k < sp.ns ? k : sp.lo + k - sp.ns;
+    };
+    auto issue = [&](int i) {  // called by the whole warp for i = 0, 1, ... in order
+      if (i >= pbase + 32) {
+        pbase = i;
+        const int mine = i + lane;
+        pages = mine < nrec ? __ldg(trow + (record_at(mine) >> a.rec_shift)) : 0;
+      }
+      const int page = __shfl_sync(0xffffffffu, pages, i - pbase);
+      const uint32_t st = (used + i) % CA_STAGES;
+      if (lane == 0) {
+        const int r = record_at(i);
+        const bool bad = page < 0 || page >= a.n_pages;
+        cs.bad[warp][st] = bad;
+        if (bad) {
+          record_status(a.status, -1 /* SPARGE_ERR_INVALID_ARG */);
+          mbar_arrive(&cs.full[warp][st]);
+        } else {
+          const int64_t at = ((static_cast<int64_t>(page) * a.Hkv + kvh) << a.rec_shift) + (r & ((1 << a.rec_shift) - 1));
+          mbar_arrive_expect_tx(&cs.full[warp][st], S::REC);
+          bulk_load(ring + st * S::REC, a.pool + at * S::REC, S::REC, &cs.full[warp][st]);
+        }
+      }
+    };
+    const int ahead = min(nrec, CA_STAGES);
+    for (int i = 0; i < ahead; ++i) issue(i);
+
+    // ---- Q: B operands of the score product, and per query row the multiplier and the group sums ----
+    uint32_t qf[RT][NW][4];
+    float qk[RT][2], qz[RT][2][NG];  // of this lane's rows 2c, 2c + 1 of each row tile
+    int pos[RT][2];
+#pragma unroll
+    for (int j = 0; j < RT; ++j) {
+      const int r = row0 + 8 * j + g;
+      const bool ok = r < a.rows;
+      const int h = kvh * a.G + (ok ? r / a.Nq : 0), qi = ok ? r % a.Nq : 0;
+      const uint4 *src = reinterpret_cast<const uint4 *>(a.q + b * a.q_sb + h * a.q_sh + static_cast<int64_t>(qi) * a.q_sn);
+      float x[NW][8];
+      float mx = 0.f, sum[NG];
+#pragma unroll
+      for (int w = 0; w < NG; ++w) sum[w] = 0.f;
+#pragma unroll
+      for (int w = 0; w < NW; ++w) {
+        const uint4 v = ok ? __ldg(src + 4 * w + c) : make_uint4(0u, 0u, 0u, 0u);
+        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          x[w][2 * k] = bf16lo(u[k]);
+          x[w][2 * k + 1] = bf16hi(u[k]);
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          mx = fmaxf(mx, fabsf(x[w][k]));
+          sum[w / 2] += x[w][k];
+        }
+      }
+#pragma unroll
+      for (int o = 1; o <= 2; o <<= 1) {
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+#pragma unroll
+        for (int w = 0; w < NG; ++w) sum[w] += __shfl_xor_sync(0xffffffffu, sum[w], o);
+      }
+      // a power of two that takes the row's maximum to [2^14, 2^15)
+      const int e = min(max(exponent_of(mx), -100), 116);
+      const float f = pow2i(14 - e);
+#pragma unroll
+      for (int w = 0; w < NW; ++w) {
+        const float f16 = f * 0.0625f;  // the odd channels' codes come 16 times as large
+        qf[j][w][0] = half2_of(x[w][0] * f, x[w][4] * f);
+        qf[j][w][1] = half2_of(x[w][1] * f16, x[w][5] * f16);
+        qf[j][w][2] = half2_of(x[w][2] * f, x[w][6] * f);
+        qf[j][w][3] = half2_of(x[w][3] * f16, x[w][7] * f16);
+      }
+      const float mult = a.scale_log2 * pow2i(e + 10);  // 2^24 / f
+      const int p = sp.len - a.Nq + qi;                   // rows past the last are computed and dropped
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int from = 4 * (2 * c + k);
+        qk[j][k] = __shfl_sync(0xffffffffu, mult, from);
+        pos[j][k] = __shfl_sync(0xffffffffu, p, from);
+#pragma unroll
+        for (int w = 0; w < NG; ++w) qz[j][k][w] = __shfl_sync(0xffffffffu, sum[w], from) * a.scale_log2;
+      }
+    }
+
+    float acc[MT][RT][4];   // O^T: rows g (channels 16 u + g, times 2^-24 vf) and g + 8 (times 2^-20 vf), columns 2c, 2c + 1
+    float zero[RT][2][NG];  // sum of P times the minima (this lane's tokens)
+    float m_ref[RT][2], l[RT][2];
+    float vf = 0.f;         // 0: not set yet
+#pragma unroll
+    for (int j = 0; j < RT; ++j)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        m_ref[j][k] = -INFINITY;
+        l[j][k] = 0.f;
+#pragma unroll
+        for (int w = 0; w < NG; ++w) zero[j][k][w] = 0.f;
+      }
+#pragma unroll
+    for (int u = 0; u < MT; ++u)
+#pragma unroll
+      for (int j = 0; j < RT; ++j)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) acc[u][j][k] = 0.f;
+
+    for (int i = 0; i < nrec; ++i) {
+      const uint32_t n = used + i, st = n % CA_STAGES;
+      const bool landed = mbar_wait(&cs.full[warp][st], (n / CA_STAGES) & 1, &cs.abort, a.status);
+      if (!__all_sync(0xffffffffu, landed)) break;
+      const uint8_t *p = ring + st * S::REC;
+      if (!cs.bad[warp][st]) {
+        // ---- scores of tokens g and g + 8 ----
+        float x[RT][4];
+        {
+          uint32_t ka[NW], kb[NW];
+          if constexpr (D == 128) {
+            const uint4 u = *reinterpret_cast<const uint4 *>(p + R::K + g * 64 + c * 16);
+            const uint4 v = *reinterpret_cast<const uint4 *>(p + R::K + (g + 8) * 64 + c * 16);
+            ka[0] = u.x; ka[1] = u.y; ka[2] = u.z; ka[3] = u.w;
+            kb[0] = v.x; kb[1] = v.y; kb[2] = v.z; kb[3] = v.w;
+          } else {
+            const uint2 u = *reinterpret_cast<const uint2 *>(p + R::K + g * 32 + c * 8);
+            const uint2 v = *reinterpret_cast<const uint2 *>(p + R::K + (g + 8) * 32 + c * 8);
+            ka[0] = u.x; ka[1] = u.y;
+            kb[0] = v.x; kb[1] = v.y;
+          }
+          float sc[NG][RT][4];
+#pragma unroll
+          for (int w = 0; w < NG; ++w)
+#pragma unroll
+            for (int j = 0; j < RT; ++j)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) sc[w][j][k] = 0.f;
+#pragma unroll
+          for (int w = 0; w < NW; ++w) {
+            const uint32_t va = ka[w] >> 8, vb = kb[w] >> 8;
+#pragma unroll
+            for (int j = 0; j < RT; ++j) {
+              mma_f16(sc[w / 2][j], ka[w] & 0x000F000Fu, kb[w] & 0x000F000Fu, ka[w] & 0x00F000F0u, kb[w] & 0x00F000F0u,
+                      qf[j][w][0], qf[j][w][1]);
+              mma_f16(sc[w / 2][j], va & 0x000F000Fu, vb & 0x000F000Fu, va & 0x00F000F0u, vb & 0x00F000F0u, qf[j][w][2],
+                      qf[j][w][3]);
+            }
+          }
+          const uint32_t *kw = reinterpret_cast<const uint32_t *>(p + R::KW);
+          float s0[NG], m0[NG], s1[NG], m1[NG];
+#pragma unroll
+          for (int w = 0; w < NG; ++w) {
+            const uint32_t u = kw[g * NG + w], v = kw[(g + 8) * NG + w];
+            s0[w] = bf16lo(u); m0[w] = bf16hi(u);
+            s1[w] = bf16lo(v); m1[w] = bf16hi(v);
+          }
+#pragma unroll
+          for (int j = 0; j < RT; ++j)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              float t0 = s0[0] * sc[0][j][k], t1 = s1[0] * sc[0][j][2 + k];
+              float z0 = m0[0] * qz[j][k][0], z1 = m1[0] * qz[j][k][0];
+              if constexpr (NG == 2) {
+                t0 = fmaf(s0[1], sc[1][j][k], t0);
+                t1 = fmaf(s1[1], sc[1][j][2 + k], t1);
+                z0 = fmaf(m0[1], qz[j][k][1], z0);
+                z1 = fmaf(m1[1], qz[j][k][1], z1);
+              }
+              x[j][k] = fmaf(t0, qk[j][k], z0);
+              x[j][2 + k] = fmaf(t1, qk[j][k], z1);
+            }
+        }
+        // ---- hidden tokens: past the row's position, or between the first tokens and the window ----
+        const int tok = record_at(i) * 16;
+        const bool edge = tok + 15 > sp.len - a.Nq ||
+                          (a.window > 0 && !(tok + 15 < a.sinks || tok > sp.len - 1 - a.window));
+        if (edge) {
+#pragma unroll
+          for (int j = 0; j < RT; ++j)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int t = tok + g + 8 * (k >> 1), q = pos[j][k & 1];
+              const bool seen = t <= q && (a.window == 0 || t < a.sinks || q - t < a.window);
+              if (!seen) x[j][k] = -INFINITY;
+            }
+        }
+        // ---- the exponent reference and the V scales' power of two follow lazily ----
+        const uint32_t *vw = reinterpret_cast<const uint32_t *>(p + R::VW);
+        float s0[NG], m0[NG], s1[NG], m1[NG];
+        float smax = 0.f;
+#pragma unroll
+        for (int w = 0; w < NG; ++w) {
+          uint32_t u = vw[g * NG + w], v = vw[(g + 8) * NG + w];
+          if (edge) {  // places behind the sequence hold anything
+            if (tok + g >= sp.len) u = 0u;
+            if (tok + g + 8 >= sp.len) v = 0u;
+          }
+          s0[w] = bf16lo(u); m0[w] = bf16hi(u);
+          s1[w] = bf16lo(v); m1[w] = bf16hi(v);
+          smax = fmaxf(smax, fmaxf(fabsf(s0[w]), fabsf(s1[w])));
+        }
+        bool move = smax * vf > CA_SBOUND;
+#pragma unroll
+        for (int j = 0; j < RT; ++j)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) move = move || fmaxf(x[j][k], x[j][2 + k]) > m_ref[j][k] + CA_RESCALE;
+        if (__any_sync(0xffffffffu, move)) {
+#pragma unroll
+          for (int o = 4; o <= 16; o <<= 1) smax = fmaxf(smax, __shfl_xor_sync(0xffffffffu, smax, o));
+          float vr = 1.f;
+          if (smax * vf > CA_SBOUND || vf == 0.f) {  // the largest scale to [1, 2): the first tokens set it, outliers move it
+            const float nf = pow2i(-min(max(exponent_of(smax), -100), 100));
+            vr = vf == 0.f ? 1.f : nf / vf;
+            vf = nf;
+          }
+#pragma unroll
+          for (int j = 0; j < RT; ++j)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              float mx = fmaxf(x[j][k], x[j][2 + k]);
+#pragma unroll
+              for (int o = 4; o <= 16; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+              float al = 1.f;
+              if (mx > m_ref[j][k] + CA_RESCALE) {
+                al = m_ref[j][k] == -INFINITY ? 0.f : exp2f(m_ref[j][k] - mx);
+                m_ref[j][k] = mx;
+              }
+              l[j][k] *= al;
+#pragma unroll
+              for (int w = 0; w < NG; ++w) zero[j][k][w] *= al;
+              al *= vr;
+#pragma unroll
+              for (int u = 0; u < MT; ++u) {
+                acc[u][j][k] *= al;
+                acc[u][j][2 + k] *= al;
+              }
+            }
+        }
+        // ---- P, its sums, and the B operands of the second product ----
+        uint32_t pb[NG][RT][2];
+#pragma unroll
+        for (int w = 0; w < NG; ++w) {
+          s0[w] *= vf;
+          s1[w] *= vf;
+        }
+#pragma unroll
+        for (int j = 0; j < RT; ++j) {
+          float pr[4];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const float mr = m_ref[j][k] == -INFINITY ? 0.f : m_ref[j][k];
+            pr[k] = fast_exp2(x[j][k] - mr);
+            pr[2 + k] = fast_exp2(x[j][2 + k] - mr);
+            l[j][k] += pr[k] + pr[2 + k];
+          }
+#pragma unroll
+          for (int w = 0; w < NG; ++w) {
+            float e0 = pr[0] * s0[w], e1 = pr[1] * s0[w], e2 = pr[2] * s1[w], e3 = pr[3] * s1[w];
+            float z0 = pr[0] * m0[w], z1 = pr[1] * m0[w], z2 = pr[2] * m1[w], z3 = pr[3] * m1[w];
+            if (edge) {  // a hidden token adds nothing, whatever its scale and minimum are
+              if (pr[0] == 0.f) e0 = z0 = 0.f;
+              if (pr[1] == 0.f) e1 = z1 = 0.f;
+              if (pr[2] == 0.f) e2 = z2 = 0.f;
+              if (pr[3] == 0.f) e3 = z3 = 0.f;
+            }
+            zero[j][0][w] += z0 + z2;
+            zero[j][1][w] += z1 + z3;
+            pb[w][j][0] = transpose8x8(half2_of(e0, e1));
+            pb[w][j][1] = transpose8x8(half2_of(e2, e3));
+          }
+        }
+        // ---- O^T += V^T P^T ----
+#pragma unroll
+        for (int w = 0; w < NG; ++w) {
+          const uint4 v4 = *reinterpret_cast<const uint4 *>(p + R::V + w * 512 + lane * 16);
+          const uint32_t v[4] = {v4.x, v4.y, v4.z, v4.w};
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const uint32_t hi = v[u] >> 8;
+#pragma unroll
+            for (int j = 0; j < RT; ++j)
+              mma_f16(acc[4 * w + u][j], v[u] & 0x000F000Fu, v[u] & 0x00F000F0u, hi & 0x000F000Fu, hi & 0x00F000F0u,
+                      pb[w][j][0], pb[w][j][1]);
+          }
+        }
+      }
+      __syncwarp();  // every lane has read the stage
+      if (i + CA_STAGES < nrec) issue(i + CA_STAGES);
+    }
+    used += nrec;
+
+    // ---- the item's (or its share's) end: the warps' sums into shared memory, then merged ----
+    float *mo = reinterpret_cast<float *>(smem + S::OFF_MERGE) + warp * 8 * RT * S::OROW;
+    float2 *ml = reinterpret_cast<float2 *>(smem + S::OFF_ML);
+    const float back = vf == 0.f ? 0.f : 16777216.f / vf;  // 2^24 / vf
+#pragma unroll
+    for (int j = 0; j < RT; ++j)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int row = 8 * j + 2 * c + k;
+        float ls = l[j][k];
+#pragma unroll
+        for (int o = 4; o <= 16; o <<= 1) ls += __shfl_xor_sync(0xffffffffu, ls, o);
+        float z[NG];
+#pragma unroll
+        for (int w = 0; w < NG; ++w) {
+          z[w] = zero[j][k][w];
+#pragma unroll
+          for (int o = 4; o <= 16; o <<= 1) z[w] += __shfl_xor_sync(0xffffffffu, z[w], o);
+        }
+        if (g == 0) ml[warp * 8 * RT + row] = make_float2(m_ref[j][k], ls);
+#pragma unroll
+        for (int u = 0; u < MT; ++u) {
+          mo[row * S::OROW + 16 * u + g] = fmaf(acc[u][j][k], back, z[u / 4]);
+          mo[row * S::OROW + 16 * u + 8 + g] = fmaf(acc[u][j][2 + k], back * 0.0625f, z[u / 4]);
+        }
+      }
+    __syncthreads();
+    const bool whole = nt == tiles;  // the item lies in this CTA alone
+    const int nrow = min(8 * RT, a.rows - row0);
+    if (threadIdx.x == 0) {
+      if (tile0 == 0) a.ends[item].x = blockIdx.x;
+      if (tile0 + nt == tiles) a.ends[item].y = blockIdx.x;
+    }
+    const int64_t slot = static_cast<int64_t>(blockIdx.x) + item;
+    for (int e = threadIdx.x; e < nrow * (D / 4); e += CA_WARPS * 32) {
+      const int row = e / (D / 4), d4 = e % (D / 4);
+      float2 w[CA_WARPS];
+      float M = -INFINITY;
+#pragma unroll
+      for (int u = 0; u < CA_WARPS; ++u) {
+        w[u] = ml[u * 8 * RT + row];
+        M = fmaxf(M, w[u].x);
+      }
+      float L = 0.f;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int u = 0; u < CA_WARPS; ++u) {
+        // a warp without a visible token has the reference -inf; its sums are 0 (NaN inputs: NaN)
+        const float f = w[u].x == -INFINITY ? (w[u].y == 0.f ? 0.f : 1.f) : exp2f(w[u].x - M);
+        const float4 v = *reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(smem + S::OFF_MERGE) +
+                                                           (u * 8 * RT + row) * S::OROW + 4 * d4);
+        if (f != 0.f) {
+          L = fmaf(f, w[u].y, L);
+          o.x = fmaf(f, v.x, o.x);
+          o.y = fmaf(f, v.y, o.y);
+          o.z = fmaf(f, v.z, o.z);
+          o.w = fmaf(f, v.w, o.w);
+        }
+      }
+      if (whole) {
+        const float inv = L == 0.f ? 0.f : 1.f / L;
+        const int r = row0 + row, h = kvh * a.G + r / a.Nq, qi = r % a.Nq;
+        uint2 w2;
+        w2.x = pack_bf16x2(o.x * inv, o.y * inv);
+        w2.y = pack_bf16x2(o.z * inv, o.w * inv);
+        *reinterpret_cast<uint2 *>(a.o + b * a.o_sb + h * a.o_sh + static_cast<int64_t>(qi) * a.o_sn + 4 * d4) = w2;
+      } else {
+        *reinterpret_cast<float4 *>(a.part_o + (slot * 8 * RT + row) * D + 4 * d4) = o;
+        if (d4 == 0) *reinterpret_cast<float2 *>(a.part_ml + (slot * 8 * RT + row) * 2) = make_float2(M, L);
+      }
+    }
+    __syncthreads();
+    if (*reinterpret_cast<volatile int *>(&cs.abort)) break;
+    off += nt;
+    left -= nt;
+  }
+  if (*reinterpret_cast<volatile int *>(&cs.abort)) {  // let copies already in flight land before the CTA exits
+    const uint64_t t0 = global_timer_ns();
+    while (global_timer_ns() - t0 < 1000000ull) {
+    }
+  }
+}
+
+// Items cut between CTAs: the CTAs' partial rows (at CTA + item, a place of its own for every pair
+// that meets) weighted by 2^(m - M) in the order of the CTAs and divided by the weighted sum.
+// Items without a token get zero rows.  One CTA of D / 4 threads per (item, row).
+template <int D, int RT>
+__global__ void __launch_bounds__(D / 4) cache4_combine_kernel(const CacheAttnArgs a) {
+  const int item = blockIdx.x, row = blockIdx.y, per = a.Hkv * a.ntile;
+  const int b = item / per, kvh = item % per / a.ntile, r = (item % a.ntile) * 8 * RT + row;
+  if (r >= a.rows) return;
+  const int h = kvh * a.G + r / a.Nq, qi = r % a.Nq, d4 = threadIdx.x;
+  __nv_bfloat16 *out = a.o + b * a.o_sb + h * a.o_sh + static_cast<int64_t>(qi) * a.o_sn + 4 * d4;
+  if (units_of(a, b) == 0) {
+    *reinterpret_cast<uint2 *>(out) = make_uint2(0u, 0u);
+    return;
+  }
+  const int2 ends = a.ends[item];
+  if (ends.x == ends.y) return;  // written by its only CTA
+  float M = -INFINITY;
+  for (int w = ends.x; w <= ends.y; ++w)
+    M = fmaxf(M, a.part_ml[((static_cast<int64_t>(w) + item) * 8 * RT + row) * 2]);
+  float L = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int w = ends.x; w <= ends.y; ++w) {
+    const int64_t at = (static_cast<int64_t>(w) + item) * 8 * RT + row;
+    const float2 ml = *reinterpret_cast<const float2 *>(a.part_ml + at * 2);
+    const float4 v = *reinterpret_cast<const float4 *>(a.part_o + at * D + 4 * d4);
+    const float f = ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : 1.f) : exp2f(ml.x - M);
+    if (f != 0.f) {
+      L = fmaf(f, ml.y, L);
+      o.x = fmaf(f, v.x, o.x);
+      o.y = fmaf(f, v.y, o.y);
+      o.z = fmaf(f, v.z, o.z);
+      o.w = fmaf(f, v.w, o.w);
+    }
+  }
+  const float inv = L == 0.f ? 0.f : 1.f / L;
+  uint2 w2;
+  w2.x = pack_bf16x2(o.x * inv, o.y * inv);
+  w2.y = pack_bf16x2(o.z * inv, o.w * inv);
+  *reinterpret_cast<uint2 *>(out) = w2;
+}
+
+// Row tiles of 8 rows for up to 8 query rows per KV head, else of 16: a CTA of 16-row tiles holds
+// twice the sums in registers (3 CTAs per SM instead of 4) and reads the cache half as often.
+int row_tile(int64_t rows) { return rows <= 8 ? 1 : 2; }
+int max_ctas(int rt) { return CA_SMS * (rt == 1 ? 4 : 3); }
+size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
+
+struct AttnWs {
+  size_t o, ml, ends, total;  // offsets
+};
+AttnWs ws_layout(int64_t B, int64_t Hkv, int64_t rows, int64_t d) {
+  const int rt = row_tile(rows);
+  const int64_t items = B * Hkv * ((rows + 8 * rt - 1) / (8 * rt)), slots = items + max_ctas(rt);
+  AttnWs w;
+  w.o = 0;
+  w.ml = up256(static_cast<size_t>(slots) * 8 * rt * d * 4);
+  w.ends = w.ml + up256(static_cast<size_t>(slots) * 8 * rt * 2 * 4);
+  w.total = w.ends + up256(static_cast<size_t>(items) * 8);
+  return w;
+}
+
+template <int D, int RT>
+cudaError_t launch_cache_attn(const CacheAttnArgs &a, int64_t tiles, cudaStream_t st) {
+  using S = CaSmem<D, RT>;
+  static std::atomic<unsigned long long> smem_set{0};
+  if (cudaError_t e = set_smem_limit_once(cache4_attn_kernel<D, RT>, S::TOTAL, smem_set); e != cudaSuccess) return e;
+  const int64_t most = max_ctas(RT), ctas = tiles < most ? tiles : most;
+  cache4_attn_kernel<D, RT><<<static_cast<unsigned>(ctas), CA_WARPS * 32, S::TOTAL, st>>>(a);
+  if (cudaError_t e = cudaGetLastError(); e != cudaSuccess) return e;
+  const unsigned items = static_cast<unsigned>(a.B * a.Hkv * a.ntile);
+  cache4_combine_kernel<D, RT><<<dim3(items, static_cast<unsigned>(a.rows < 8 * RT ? a.rows : 8 * RT)), D / 4, 0, st>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+}  // namespace sparge
+
+using namespace sparge;
+
+extern "C" {
+
+size_t sparge_cache4_attn_workspace_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_t Nq, int64_t d) {
+  if (B < 0 || Hq <= 0 || Hkv <= 0 || Nq < 0 || (d != 64 && d != 128) || Hq % Hkv || B > 65535 || Hq > 65535 ||
+      Nq > (int64_t(1) << 30))
+    return 0;
+  return ws_layout(B, Hkv, Hq / Hkv * Nq, d).total;
+}
+
+int sparge_cache4_attn(const sparge_tensor *q, const sparge_cache4 *cache, const int32_t *table, int64_t width,
+                       int64_t table_stride, const int32_t *kv_lens, int64_t window, int64_t sinks, float scale,
+                       sparge_tensor *o, void *ws, size_t ws_bytes, sparge_stream_t stream) {
+  clear_error();
+  View qv, ov;
+  Cache4 c;
+  int rc;
+  if ((rc = check_tensor(q, "q", &qv)) || (rc = check_tensor(o, "o", &ov)) || (rc = check_cache4(cache, &c))) return rc;
+  if (qv.B != ov.B || qv.H != ov.H || qv.N != ov.N || qv.d != ov.d) return fail(SPARGE_ERR_INVALID_ARG, "o disagrees with q");
+  if (qv.d != c.d) return fail(SPARGE_ERR_INVALID_ARG, "q and the cache disagree in d");
+  if (qv.H % c.H) return fail(SPARGE_ERR_UNSUPPORTED, "Hq=%lld not a multiple of the cache's %d heads", (long long)qv.H, c.H);
+  if (window < 0 || sinks < 0 || window > INT_MAX || sinks > INT_MAX)
+    return fail(SPARGE_ERR_INVALID_ARG, "window=%lld and sinks=%lld must be in 0..2^31-1", (long long)window, (long long)sinks);
+  if (window == 0 && sinks != 0) return fail(SPARGE_ERR_INVALID_ARG, "sinks need a window");
+  if (std::isnan(scale) || scale < 0.f || std::isinf(scale)) return fail(SPARGE_ERR_INVALID_ARG, "scale must be finite and >= 0");
+  if (width < 0 || table_stride < width || width > INT_MAX / c.page_size)
+    return fail(SPARGE_ERR_INVALID_ARG, "table width %lld and stride %lld: the stride must reach the width, the width 2^31 tokens at most",
+                (long long)width, (long long)table_stride);
+  const int64_t rows = qv.H / c.H * qv.N, rt = row_tile(rows), ntile = (rows + 8 * rt - 1) / (8 * rt);
+  if (rows > INT_MAX || qv.B * c.H * ntile > INT_MAX / 2) return fail(SPARGE_ERR_UNSUPPORTED, "too many query rows");
+  const AttnWs w = ws_layout(qv.B, c.H, rows, qv.d);
+  if (!ws || ws_bytes < w.total) return fail(SPARGE_ERR_WORKSPACE_TOO_SMALL, "workspace %zu bytes, need %zu", ws_bytes, w.total);
+  if (reinterpret_cast<uintptr_t>(ws) & 255u) return fail(SPARGE_ERR_INVALID_ARG, "workspace not 256-byte aligned");
+  if (qv.B == 0 || qv.N == 0) return SPARGE_OK;
+  if (!kv_lens || (width && !table)) return fail(SPARGE_ERR_INVALID_ARG, "table or kv_lens is NULL");
+  CacheAttnArgs a;
+  a.q = static_cast<const __nv_bfloat16 *>(qv.data);
+  a.o = static_cast<__nv_bfloat16 *>(const_cast<void *>(ov.data));
+  a.q_sb = qv.sb; a.q_sh = qv.sh; a.q_sn = qv.sn;
+  a.o_sb = ov.sb; a.o_sh = ov.sh; a.o_sn = ov.sn;
+  a.pool = c.data;
+  a.table = table;
+  a.lens = kv_lens;
+  a.table_stride = table_stride;
+  a.n_pages = c.n_pages;
+  a.width = static_cast<int>(width);
+  a.rec_shift = c.page_shift - 4;
+  a.B = static_cast<int>(qv.B); a.Hq = static_cast<int>(qv.H); a.Hkv = c.H; a.G = static_cast<int>(qv.H / c.H);
+  a.Nq = static_cast<int>(qv.N); a.rows = static_cast<int>(rows); a.ntile = static_cast<int>(ntile);
+  a.window = static_cast<int>(window);
+  a.sinks = static_cast<int>(sinks);
+  a.scale_log2 = (scale > 0.f ? scale : 1.f / sqrtf(static_cast<float>(qv.d))) * 1.4426950408889634f;
+  a.part_o = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + w.o);
+  a.part_ml = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + w.ml);
+  a.ends = reinterpret_cast<int2 *>(static_cast<uint8_t *>(ws) + w.ends);
+  a.status = status_ptr();
+  // an upper bound of the line of tiles, for the number of CTAs (the lengths are on the device)
+  int64_t recs = (width * c.page_size + 15) / 16;
+  if (window > 0) {
+    const int64_t most = (window + qv.N + 15) / 16 + 1 + (sinks + 15) / 16;
+    recs = recs < most ? recs : most;
+  }
+  int64_t tiles = (recs + 3) / 4 * qv.B * c.H * ntile;
+  if (tiles < 1) tiles = 1;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  if (qv.d == 128)
+    e = rt == 1 ? launch_cache_attn<128, 1>(a, tiles, s) : launch_cache_attn<128, 2>(a, tiles, s);
+  else
+    e = rt == 1 ? launch_cache_attn<64, 1>(a, tiles, s) : launch_cache_attn<64, 2>(a, tiles, s);
+  return e == cudaSuccess ? SPARGE_OK : cuda_fail(e, "cache attention launch");
+}
+
+}  // extern "C"

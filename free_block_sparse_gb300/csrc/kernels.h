@@ -77,6 +77,12 @@ int validate_predict_args(const ::sparge_tensor *q, const ::sparge_tensor *k, fl
 int run_predict(const View &q, const View &k, float topk, float theta, int causal, uint8_t *mask, void *ws,
                 size_t ws_bytes, cudaStream_t s);
 int report_error(int code, const char *msg);
+void clear_error();                               // the thread's last error message becomes empty
+int fail(int code, const char *fmt, ...);         // records the message, returns the code
+int cuda_fail(cudaError_t e, const char *where);  // records SPARGE_ERR_CUDA and the runtime's reason
+int *status_ptr();                                // the device status word of the current device
+// The tensor rules of sparge.h (type, d, alignment, strides); fills the validated view.
+int check_tensor(const ::sparge_tensor *t, const char *name, View *v);
 
 // qperm / kperm (or nullptr): token order of q / k; block row t of the pooling is token perm[t] (an
 // entry outside 0..N-1 is reported in *status and read as a zero token).  qcopy / kcopy (or
@@ -144,6 +150,9 @@ struct AttnLaunch {
   float *part_o, *part_ml;
   int32_t *dlist;
   int *dcount;
+  // window > 0 (bf16, causal, no mask): a query at position p sees key c <= p when c > p - window or
+  // c < sinks
+  int window, sinks;
 };
 
 // How a decoding call splits the key blocks of each (batch, KV head): about two CTAs per SM of a
@@ -184,7 +193,9 @@ cudaError_t launch_decode_combine(const float *part_o, const float *part_ml, int
                                   int d, void *o, int64_t o_sb, int64_t o_sh, int64_t o_sn, cudaStream_t st);
 
 // perm (or nullptr): row t of the copy is token perm[t] of v; bad entries are reported in *status.
-cudaError_t launch_convert_v_f16(const View &v, void *v16, const int32_t *perm, int *status, cudaStream_t st);
+// Rows first .. last - 1 are copied (last < 0: all).
+cudaError_t launch_convert_v_f16(const View &v, void *v16, const int32_t *perm, int *status, cudaStream_t st,
+                                 int64_t first = 0, int64_t last = -1);
 
 // 8-bit path: e4m3 copies of Q, K - mean(K) and V with their scales (all contiguous).
 struct Q8Ws {

@@ -1,0 +1,227 @@
+// Norm of queries and keys for each head and rotation by position, in one pass (the step that comes
+// before the attention of a model whose heads are normalised).
+//
+//   y = x / sqrt(mean(x^2) + eps) * w          per token and head, over the d channels
+//   (a, b) -> (a cos t - b sin t, a sin t + b cos t)   for the rot/2 pairs of the first rot channels,
+//                                                t = position * inv_freq[pair]
+//
+// Bound by memory: q and k are read once and written once; fp32 arithmetic, one rounding to bf16.
+// D / 16 threads share a row, 16 channels each as two 16-byte pieces chosen so that both channels of
+// every pair are in one thread.  A thread keeps its place in the row for all heads of a token, so
+// the angles of its 8 pairs are computed once per token and serve every head of its share.
+// Angles: the frequency is held as a fraction of a turn in 64-bit fixed point, so position times
+// frequency modulo one turn is one integer product, exact to position * 2^-64 turns at any
+// position; the top 32 bits give the half-turns that sincospif takes.
+#include <cmath>
+
+#include "../../include/sparge.h"
+#include "common.cuh"
+#include "kernels.h"
+
+namespace sparge {
+namespace {
+
+struct NormRopeArgs {
+  const __nv_bfloat16 *x[2];  // q, k
+  __nv_bfloat16 *y[2];
+  int64_t xsb[2], xsh[2], xsn[2], ysb[2], ysh[2], ysn[2];
+  const float *w[2];
+  int H[2];
+  const int32_t *pos;
+  const double *inv_freq;
+  int64_t start;
+  int64_t tokens;  // B N
+  int N, rot, per;  // per: heads of one CTA
+  float eps;
+};
+
+constexpr int NR_THREADS = 128;
+constexpr int NR_U = 4;  // heads whose rows a thread has in flight
+
+// inv_freq (radians per token) as turns per token in units of 2^-64, modulo one turn.  The double is
+// M 2^e with a 53-bit M; M 2^11 times 2^66 / (2 pi) (its high word) is M 2^13 / (2 pi), and a shift
+// by e + 51 brings it to units of 2^-64 turns.  Infinities and NaN have no angle: 0.
+__device__ __forceinline__ uint64_t turns64(double f) {
+  const uint64_t b = static_cast<uint64_t>(__double_as_longlong(f));
+  const int ex = static_cast<int>((b >> 52) & 0x7FFu);
+  if (ex == 0 || ex == 0x7FF) return 0ull;
+  const uint64_t m = ((b & 0xFFFFFFFFFFFFFull) | 0x10000000000000ull) << 11;
+  const uint64_t hi = __umul64hi(m, 0xA2F9836E4E44152Aull);  // 2^66 / (2 pi) = 2^65 / pi
+  const int sh = ex - 1075 + 51;
+  uint64_t t = sh >= 0 ? (sh < 64 ? hi << sh : 0ull) : (sh > -64 ? hi >> -sh : 0ull);
+  return (b >> 63) ? 0ull - t : t;
+}
+
+template <int D, bool INTER>
+__global__ void __launch_bounds__(NR_THREADS) norm_rope_kernel(const NormRopeArgs a) {
+  constexpr int TR = D / 16;                 // threads of a row
+  constexpr int TOK = NR_THREADS / TR;       // tokens of a CTA
+  const int t = threadIdx.x % TR;
+  const int64_t m = static_cast<int64_t>(blockIdx.x) * TOK + threadIdx.x / TR;
+  const bool live = m < a.tokens;
+  const int64_t mm = live ? m : a.tokens - 1;
+  const int b = static_cast<int>(mm / a.N), n = static_cast<int>(mm % a.N);
+  // the thread's two pieces of 8 channels: neighbouring pairs lie in adjacent pieces; pairs
+  // (i, i + rot/2) in pieces rot/16 apart, the channels behind rot two by two
+  const int rc = a.rot / 16;
+  int p0, p1;
+  if (INTER || t >= rc) {
+    p0 = 2 * t;
+    p1 = 2 * t + 1;
+  } else {
+    p0 = t;
+    p1 = t + rc;
+  }
+  const bool turn = t < rc;
+  float cs[8], sn[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    cs[j] = 1.f;
+    sn[j] = 0.f;
+  }
+  if (turn) {
+    const int64_t pos = a.pos ? static_cast<int64_t>(__ldg(a.pos + mm)) : a.start + n;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint64_t ph = static_cast<uint64_t>(pos) * turns64(__ldg(a.inv_freq + 8 * t + j));
+      const float half_turns = static_cast<float>(static_cast<int32_t>(ph >> 32)) * 4.656612873077393e-10f;  // 2^-31
+      sincospif(half_turns, &sn[j], &cs[j]);
+    }
+  }
+  int h = blockIdx.y * a.per, left = min(a.per, a.H[0] + a.H[1] - h);
+#pragma unroll 1
+  for (int s = 0; s < 2; ++s) {  // q heads, then k heads
+    const int h0 = s == 0 ? h : h - a.H[0];
+    const int cnt = s == 0 ? min(left, max(0, a.H[0] - h)) : left;
+    if (cnt <= 0) continue;
+    h += cnt;
+    left -= cnt;
+    float w[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) w[j] = a.w[s] ? __ldg(a.w[s] + 8 * (j < 8 ? p0 : p1) + (j & 7)) : 1.f;
+    const __nv_bfloat16 *x = a.x[s] + b * a.xsb[s] + static_cast<int64_t>(n) * a.xsn[s] + h0 * a.xsh[s];
+    __nv_bfloat16 *y = a.y[s] + b * a.ysb[s] + static_cast<int64_t>(n) * a.ysn[s] + h0 * a.ysh[s];
+    for (int i = 0; i < cnt; i += NR_U) {
+      uint4 v[NR_U][2];
+#pragma unroll
+      for (int u = 0; u < NR_U; ++u) {
+        if (i + u < cnt) {
+          const __nv_bfloat16 *xr = x + (i + u) * a.xsh[s];
+          v[u][0] = *reinterpret_cast<const uint4 *>(xr + 8 * p0);
+          v[u][1] = *reinterpret_cast<const uint4 *>(xr + 8 * p1);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < NR_U; ++u) {
+        if (i + u >= cnt) break;  // the same for the whole CTA
+        float f[16];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const uint32_t q[4] = {v[u][k].x, v[u][k].y, v[u][k].z, v[u][k].w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            f[8 * k + 2 * j] = bf16lo(q[j]);
+            f[8 * k + 2 * j + 1] = bf16hi(q[j]);
+          }
+        }
+        float ss = 0.f;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) ss = fmaf(f[j], f[j], ss);
+#pragma unroll
+        for (int off = TR / 2; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
+        const float r = 1.f / sqrtf(fmaf(ss, 1.f / D, a.eps));
+#pragma unroll
+        for (int j = 0; j < 16; ++j) f[j] = f[j] * r * w[j];
+        if (turn) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const int ia = INTER ? 2 * j : j, ib = INTER ? 2 * j + 1 : 8 + j;
+            const float fa = f[ia], fb = f[ib];
+            f[ia] = fa * cs[j] - fb * sn[j];
+            f[ib] = fa * sn[j] + fb * cs[j];
+          }
+        }
+        if (live) {
+          __nv_bfloat16 *yr = y + (i + u) * a.ysh[s];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            uint4 o;
+            o.x = pack_bf16x2(f[8 * k], f[8 * k + 1]);
+            o.y = pack_bf16x2(f[8 * k + 2], f[8 * k + 3]);
+            o.z = pack_bf16x2(f[8 * k + 4], f[8 * k + 5]);
+            o.w = pack_bf16x2(f[8 * k + 6], f[8 * k + 7]);
+            *reinterpret_cast<uint4 *>(yr + 8 * (k ? p1 : p0)) = o;
+          }
+        }
+      }
+    }
+  }
+}
+
+}  // namespace
+}  // namespace sparge
+
+using namespace sparge;
+
+extern "C" int sparge_qk_norm_rope(const sparge_tensor *q, const sparge_tensor *k, const int32_t *positions,
+                                   int64_t start, const double *inv_freq, int rot_dim, int interleaved,
+                                   const float *q_weight, const float *k_weight, float eps, sparge_tensor *q_out,
+                                   sparge_tensor *k_out, sparge_stream_t stream) {
+  clear_error();
+  View v[4];
+  int rc;
+  if ((rc = check_tensor(q, "q", &v[0])) || (rc = check_tensor(k, "k", &v[1])) ||
+      (rc = check_tensor(q_out, "q_out", &v[2])) || (rc = check_tensor(k_out, "k_out", &v[3])))
+    return rc;
+  if (v[0].B != v[1].B || v[0].N != v[1].N || v[0].d != v[1].d)
+    return fail(SPARGE_ERR_INVALID_ARG, "q and k disagree in B, N or d");
+  for (int s = 0; s < 2; ++s) {
+    const View &x = v[s], &y = v[2 + s];
+    if (x.B != y.B || x.H != y.H || x.N != y.N || x.d != y.d)
+      return fail(SPARGE_ERR_INVALID_ARG, "%s_out has another shape than %s", s ? "k" : "q", s ? "k" : "q");
+    if (x.data == y.data && (x.sb != y.sb || x.sh != y.sh || x.sn != y.sn))
+      return fail(SPARGE_ERR_INVALID_ARG, "in place, %s_out needs the strides of %s", s ? "k" : "q", s ? "k" : "q");
+  }
+  if (rot_dim < 0 || rot_dim > v[0].d || rot_dim % 16)
+    return fail(SPARGE_ERR_INVALID_ARG, "rot_dim=%d must be a multiple of 16 in 0..%lld", rot_dim, (long long)v[0].d);
+  if (rot_dim > 0 && !inv_freq) return fail(SPARGE_ERR_INVALID_ARG, "inv_freq is NULL");
+  if (!(eps >= 0.f) || std::isinf(eps)) return fail(SPARGE_ERR_INVALID_ARG, "eps=%g must be finite and >= 0", (double)eps);
+  if (v[0].B * v[0].N == 0) return SPARGE_OK;
+  NormRopeArgs a;
+  for (int s = 0; s < 2; ++s) {
+    a.x[s] = static_cast<const __nv_bfloat16 *>(v[s].data);
+    a.y[s] = static_cast<__nv_bfloat16 *>(const_cast<void *>(v[2 + s].data));
+    a.xsb[s] = v[s].sb; a.xsh[s] = v[s].sh; a.xsn[s] = v[s].sn;
+    a.ysb[s] = v[2 + s].sb; a.ysh[s] = v[2 + s].sh; a.ysn[s] = v[2 + s].sn;
+    a.H[s] = static_cast<int>(v[s].H);
+  }
+  a.w[0] = q_weight;
+  a.w[1] = k_weight;
+  a.pos = positions;
+  a.inv_freq = inv_freq;
+  a.start = start;
+  a.tokens = v[0].B * v[0].N;
+  a.N = static_cast<int>(v[0].N);
+  a.rot = rot_dim;
+  a.eps = eps;
+  const int d = static_cast<int>(v[0].d), tok = NR_THREADS / (d / 16), heads = a.H[0] + a.H[1];
+  const int64_t tiles = (a.tokens + tok - 1) / tok;
+  if (tiles > 0x7fffffffLL) return fail(SPARGE_ERR_UNSUPPORTED, "too many tokens");
+  // heads of a CTA: as many as leave 8 CTAs for each of the 152 SMs (the angles serve them all)
+  int64_t per = tiles * heads / (8 * 152);
+  per = per < 1 ? 1 : (per > heads ? heads : per);
+  const int64_t gy = (heads + per - 1) / per;
+  if (gy > 65535) per = (heads + 65534) / 65535;
+  a.per = static_cast<int>(per);
+  const dim3 grid(static_cast<unsigned>(tiles), static_cast<unsigned>((heads + per - 1) / per));
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (d == 128) {
+    if (interleaved) norm_rope_kernel<128, true><<<grid, NR_THREADS, 0, s>>>(a);
+    else norm_rope_kernel<128, false><<<grid, NR_THREADS, 0, s>>>(a);
+  } else {
+    if (interleaved) norm_rope_kernel<64, true><<<grid, NR_THREADS, 0, s>>>(a);
+    else norm_rope_kernel<64, false><<<grid, NR_THREADS, 0, s>>>(a);
+  }
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? SPARGE_OK : cuda_fail(e, "norm and rotation launch");
+}

@@ -74,13 +74,13 @@ __global__ void __launch_bounds__(256) permute_kernel(PermArgs a) {
 template <int D>
 __global__ void __launch_bounds__(256) convert_v_f16_kernel(const __nv_bfloat16 *x, int64_t sb, int64_t sh,
                                                              int64_t sn, __half *y, int N, const int32_t *perm,
-                                                             int *status) {
+                                                             int *status, int first, int last) {
   constexpr int VPR = D / 8;                 // 16-byte vectors per token row
   constexpr int ROWS = 2 * 256 / VPR;        // token rows per CTA
   const int h = blockIdx.y, b = blockIdx.z, H = gridDim.y;
   const __nv_bfloat16 *xb = x + b * sb + h * sh;
   __half *yb = y + (static_cast<int64_t>(b) * H + h) * N * D;
-  const int t0 = blockIdx.x * ROWS;
+  const int t0 = first + blockIdx.x * ROWS;
   uint4 v[2];
   int t[2], part[2];
 #pragma unroll
@@ -88,7 +88,7 @@ __global__ void __launch_bounds__(256) convert_v_f16_kernel(const __nv_bfloat16 
     const int e = threadIdx.x + u * 256;
     t[u] = t0 + e / VPR;
     part[u] = e % VPR;
-    if (t[u] < N) {
+    if (t[u] < last) {
       int src = t[u];
       if (perm) {
         src = __ldg(perm + t[u]);
@@ -103,7 +103,7 @@ __global__ void __launch_bounds__(256) convert_v_f16_kernel(const __nv_bfloat16 
   }
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
-    if (t[u] < N) {
+    if (t[u] < last) {
       uint4 o;
       o.x = pack_f16x2(bf16lo(v[u].x), bf16hi(v[u].x));
       o.y = pack_f16x2(bf16lo(v[u].y), bf16hi(v[u].y));
@@ -116,17 +116,19 @@ __global__ void __launch_bounds__(256) convert_v_f16_kernel(const __nv_bfloat16 
 
 }  // namespace
 
-cudaError_t launch_convert_v_f16(const View &v, void *v16, const int32_t *perm, int *status, cudaStream_t st) {
-  if (v.B * v.H * v.N == 0) return cudaSuccess;
+cudaError_t launch_convert_v_f16(const View &v, void *v16, const int32_t *perm, int *status, cudaStream_t st,
+                                 int64_t first, int64_t last) {
+  if (last < 0) last = v.N;
+  if (v.B * v.H == 0 || first >= last) return cudaSuccess;
   const int rows = 2 * 256 / static_cast<int>(v.d / 8);
-  dim3 grid(static_cast<unsigned>((v.N + rows - 1) / rows), static_cast<unsigned>(v.H), static_cast<unsigned>(v.B));
+  dim3 grid(static_cast<unsigned>((last - first + rows - 1) / rows), static_cast<unsigned>(v.H), static_cast<unsigned>(v.B));
   const __nv_bfloat16 *x = static_cast<const __nv_bfloat16 *>(v.data);
   if (v.d == 128)
     convert_v_f16_kernel<128><<<grid, 256, 0, st>>>(x, v.sb, v.sh, v.sn, static_cast<__half *>(v16), (int)v.N, perm,
-                                                    status);
+                                                    status, (int)first, (int)last);
   else
     convert_v_f16_kernel<64><<<grid, 256, 0, st>>>(x, v.sb, v.sh, v.sn, static_cast<__half *>(v16), (int)v.N, perm,
-                                                   status);
+                                                   status, (int)first, (int)last);
   return cudaGetLastError();
 }
 

@@ -85,6 +85,7 @@ enum sparge_op {
   SPARGE_OP_ATTN = 3,
   SPARGE_OP_BLOCK_SPARSE_ATTN_Q8 = 4, /* sparge_block_sparse_attn with an 8-bit precision */
   SPARGE_OP_ATTN_Q8 = 5,              /* sparge_attn_ex with an 8-bit precision */
+  SPARGE_OP_WINDOW_ATTN = 6,          /* sparge_window_attn */
   SPARGE_OP_TOKEN_ORDER = 0x100       /* flag OR-ed into an op: room for the token-ordered copies of
                                          Q and K that a call with sparge_params.token_order makes */
 };
@@ -161,6 +162,7 @@ typedef struct sparge_params {
  *   or e4m3 channel-major with the keys padded to a multiple of 64) and the fp32 scales;
  *   SPARGE_OP_ATTN_Q8: that plus the mask-prediction workspace and the mask.  Both return 0
  *   unless d = 128.
+ * SPARGE_OP_WINDOW_ATTN: an f16 copy of V, or a decoding call's partial rows.
  * op | SPARGE_OP_TOKEN_ORDER: the op's bytes plus room for bf16 copies of Q and K in a given
  *   token order (at the front of the workspace), for calls whose sparge_params.token_order is set
  *   (a call uses only the copies it needs; the room is reserved in full).
@@ -273,6 +275,108 @@ int sparge_attn(const sparge_tensor *q, const sparge_tensor *k, const sparge_ten
 int sparge_attn_ex(const sparge_tensor *q, const sparge_tensor *k, const sparge_tensor *v,
                    float topk, int is_causal, const sparge_params *params, sparge_tensor *o,
                    uint8_t *mask_out, void *ws, size_t ws_bytes, sparge_stream_t stream);
+
+/*
+ * Causal attention over a sliding window and a few first tokens that stay visible: the fixed pattern
+ * beside the predicted block masks.  q (B,Hq,Nq,d), k and v (B,Hkv,Nk,d), Nq <= Nk: query r stands at
+ * position p = Nk - Nq + r and sees key c <= p when c > p - window (window >= 1: itself and the window - 1
+ * before it) or c < sinks.  scale 0 means 1/sqrt(d).  Only the 64-key blocks that a query block sees are
+ * loaded and multiplied; single keys are masked at the edges.  bf16 Q.K^T, P.V on f16 operands (V
+ * copied to f16 into the workspace, |v| above 65504 saturates); few queries against many visible keys (G Nq <= 128 and
+ * at least 32 key blocks) run as decoding tiles with bf16 P and V in place.  ws: 256-byte aligned,
+ * sparge_workspace_bytes(SPARGE_OP_WINDOW_ATTN, B, Hq, Hkv, Nk, d) bytes.
+ */
+int sparge_window_attn(const sparge_tensor *q, const sparge_tensor *k, const sparge_tensor *v, int64_t window,
+                       int64_t sinks, float scale, sparge_tensor *o, void *ws, size_t ws_bytes,
+                       sparge_stream_t stream);
+
+/*
+ * Norm and rotation of queries and keys, the step before the attention in models whose heads are
+ * normalised.  For every token and head of q (B,Hq,N,d) and k (B,Hkv,N,d):
+ *   y = x / sqrt(mean(x^2) + eps) * weight     over the d channels (weight: d floats; NULL: all ones)
+ * and the first rot_dim channels are rotated by the token's position: the pair (a, b) number i
+ * becomes (a cos t - b sin t, a sin t + b cos t) with t = position * inv_freq[i].  Pairs are the
+ * channels (2i, 2i + 1) when interleaved, else (i, i + rot_dim/2).  Arithmetic in fp32 with one
+ * rounding to bf16; the angle is taken modulo a turn in 64-bit fixed point, so it is as exact at
+ * position 2^31 as at 0.
+ * positions: (B,N) int32, contiguous, or NULL: token n stands at start + n.  inv_freq: rot_dim/2
+ * doubles (radians per token; entries that are not finite do not rotate).  rot_dim: a multiple of 16 in 0..d (0: no rotation, inv_freq may
+ * be NULL).  eps finite and >= 0.  q_out and k_out have the shapes of q and k, any legal strides; they
+ * may be q and k themselves (same data and strides), else nothing may overlap.
+ */
+int sparge_qk_norm_rope(const sparge_tensor *q, const sparge_tensor *k, const int32_t *positions, int64_t start,
+                        const double *inv_freq, int rot_dim, int interleaved, const float *q_weight,
+                        const float *k_weight, float eps, sparge_tensor *q_out, sparge_tensor *k_out,
+                        sparge_stream_t stream);
+
+/*
+ * A paged key/value cache held in 4 bits.  The pool has n_pages pages of page_size tokens (16, 32,
+ * 64, 128 or 256) for H key/value heads of d channels: sparge_cache4_bytes bytes at a 16-byte aligned device
+ * address.  Every 64 channels of a token's K or V row are held as codes n in 0..15 with a bf16 scale and
+ * a bf16 minimum (n stands for n * scale + minimum): 4.5 bits per value.  A token's slot is
+ * page * page_size + place in the page.
+ * Layout: [n_pages][H][page_size / 16] records of 16 tokens, each 18 d bytes: K codes (16 x d/2 bytes),
+ * K words (16 x d/64 x uint32: scale in the low half, minimum in the high), V codes, V words.  K: channel
+ * 32 w + 8 c + j of token t is nibble j % 2 of byte t d/2 + c d/8 + 4 w + j/2.  V: channel
+ * 64 p + 16 u + 8 y + g of token t is nibble y of byte 512 p + 16 (4 g + (t % 8) / 2) + 4 u + 2 (t % 2) + t / 8.
+ */
+typedef struct sparge_cache4 {
+  void *data;
+  int64_t n_pages;
+  int32_t page_size, H, d, pad_;
+} sparge_cache4;
+
+/* Bytes of a pool (0 for an unsupported shape). */
+size_t sparge_cache4_bytes(int64_t n_pages, int page_size, int H, int d);
+
+/*
+ * Block tables and slot maps of one step, built on the device from the requests' lengths.
+ * lens[r] tokens of request r are in the cache, new_lens[r] (0..N) come now (R int32 each).  Request r then
+ * takes ceil((lens + new_lens)/page_size) - ceil(lens/page_size) pages from the front of free_pages
+ * (n_free int32), requests in order; they are written behind its pages in its row of table (R rows of
+ * width int32, table_stride apart), and no other entry is touched.
+ * slots (R,N) int64 and positions (R,N) int32 receive, right-aligned as the attention aligns queries
+ * (the last of the N places is the last new token), each new token's slot and position, and -1 in the
+ * places in front of them; kv_lens (R) receives lens + new_lens, used (1) the pages taken.  Each of the
+ * four may be NULL.  A token gets slot -1 and a table entry -1 where free_pages is used up (used then
+ * says more than n_free), and slot -1 where its page lies past width.  A request with a negative
+ * length, new_lens[r] > N or a total past 2^31 - 1 gets no tokens and length 0; that and a table too narrow record SPARGE_ERR_INVALID_ARG in
+ * the device status word.  R <= 65535.  The arrays must not overlap.
+ */
+int sparge_cache_tables(const int32_t *lens, const int32_t *new_lens, int64_t R, int64_t N, int page_size,
+                        const int32_t *free_pages, int64_t n_free, int32_t *table, int64_t width, int64_t table_stride,
+                        int64_t *slots, int32_t *positions, int32_t *kv_lens, int32_t *used, sparge_stream_t stream);
+
+/*
+ * Stores tokens in the cache: row (b, h, n) of k and v (B,H,N,d) goes to slot slots[b][n] ((B,N) int64,
+ * contiguous) of head h.  scale = bf16((max - minimum) / 15), n = round-to-even((x - minimum) / scale); a
+ * group that holds an infinity or a NaN reads back as NaN.  A negative slot leaves its token out; a slot past
+ * the pool is left out and records SPARGE_ERR_INVALID_ARG in the device status word.  Slots must
+ * differ from one another (of equal ones each byte holds one of them).
+ * sparge_cache4_load reads the same rows back as bf16 (rows with a left-out slot stay as they were),
+ * for instance all tokens of a sequence for sparge_attn over a chunk of queries.
+ */
+int sparge_cache4_store(const sparge_tensor *k, const sparge_tensor *v, const int64_t *slots,
+                        const sparge_cache4 *cache, sparge_stream_t stream);
+int sparge_cache4_load(const sparge_cache4 *cache, const int64_t *slots, sparge_tensor *k, sparge_tensor *v,
+                       sparge_stream_t stream);
+
+/*
+ * Attention over the 4-bit cache: q (B,Hq,Nq,d) bf16, o like q, Hq a multiple of the cache's H.  Sequence b has
+ * kv_lens[b] tokens (int32), on the pages table[b][0], table[b][1], ... ((B, width) int32, rows table_stride
+ * apart); its queries are its last Nq tokens: query r stands at position kv_lens[b] - Nq + r and sees
+ * the tokens up to there (a query in front of the first token gives a zero row).  With window > 0 it sees
+ * only the last `window` of them (itself included) and the first `sinks` tokens; window 0: all of them
+ * (sinks then 0).  scale 0 means 1/sqrt(d).  Products in f16 with fp32 sums; one rounding to bf16.
+ * A length outside 0..width * page_size is taken as the nearest of the two; a page outside the pool is left
+ * out and records SPARGE_ERR_INVALID_ARG in the device status word.
+ * Meant for decoding steps and short chunks: the cache is read once per 16 query rows of a key/value head
+ * ((Hq/H) Nq of them).  ws: 256-byte aligned, sparge_cache4_attn_workspace_bytes(...) bytes, used by one call at a time.
+ */
+size_t sparge_cache4_attn_workspace_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_t Nq, int64_t d);
+int sparge_cache4_attn(const sparge_tensor *q, const sparge_cache4 *cache, const int32_t *table, int64_t width,
+                       int64_t table_stride, const int32_t *kv_lens, int64_t window, int64_t sinks, float scale,
+                       sparge_tensor *o, void *ws, size_t ws_bytes, sparge_stream_t stream);
 
 /*
  * Hilbert-curve token order (SpargeAttention summary page: a space-filling Hilbert-curve
