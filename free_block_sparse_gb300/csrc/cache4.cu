@@ -27,6 +27,7 @@ struct Rows4 {  // K and V rows and the cache they go to or come from
   uint8_t *pool;
   int64_t n_slots;
   int page_shift, H, N, B, recs;  // recs: records of a page
+  int zero;                       // load: rows of left-out slots become zero
   int *status;
 };
 
@@ -36,26 +37,32 @@ __device__ __forceinline__ uint8_t *record_of(const Rows4 &a, int64_t slot, int 
   return a.pool + ((page * a.H + h) * a.recs + g) * static_cast<int64_t>(bytes);
 }
 
+__device__ __forceinline__ uint32_t min2_nan(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t max2_nan(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
 // Codes of a thread's 8 channels (nibble j: channel j) and its group's word; the 8 threads of a
-// group are adjacent lanes.
+// group are adjacent lanes.  Minimum and maximum are taken on packed bf16 pairs, NaN winning, so
+// one test of the two at the end finds an infinity or a NaN anywhere in the group.
 __device__ __forceinline__ uint32_t quantise8(uint4 v, uint32_t &word) {
-  float f[8] = {bf16lo(v.x), bf16hi(v.x), bf16lo(v.y), bf16hi(v.y), bf16lo(v.z), bf16hi(v.z), bf16lo(v.w), bf16hi(v.w)};
-  float lo = f[0], hi = f[0];
-  bool fine = fabsf(f[0]) <= 3.4028235e38f;
-#pragma unroll
-  for (int j = 1; j < 8; ++j) {
-    lo = fminf(lo, f[j]);
-    hi = fmaxf(hi, f[j]);
-    fine = fine && fabsf(f[j]) <= 3.4028235e38f;
-  }
-  const uint32_t bad = __ballot_sync(0xffffffffu, !fine);
+  uint32_t lo2 = min2_nan(min2_nan(v.x, v.y), min2_nan(v.z, v.w));
+  uint32_t hi2 = max2_nan(max2_nan(v.x, v.y), max2_nan(v.z, v.w));
 #pragma unroll
   for (int off = 4; off > 0; off >>= 1) {
-    lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, off));
-    hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, off));
+    lo2 = min2_nan(lo2, __shfl_xor_sync(0xffffffffu, lo2, off));
+    hi2 = max2_nan(hi2, __shfl_xor_sync(0xffffffffu, hi2, off));
   }
-  const int lane = threadIdx.x & 31;
-  if ((bad >> (lane & 24)) & 0xFFu) {
+  lo2 = min2_nan(lo2, lo2 >> 16);
+  hi2 = max2_nan(hi2, hi2 >> 16);
+  const float lo = bf16lo(lo2), hi = bf16lo(hi2);
+  if (!(fabsf(lo) <= 3.4028235e38f && fabsf(hi) <= 3.4028235e38f)) {
     word = 0x7FC07FC0u;
     return 0u;
   }
@@ -63,13 +70,26 @@ __device__ __forceinline__ uint32_t quantise8(uint4 v, uint32_t &word) {
   const float range = fminf(hi - lo, 3.4028235e38f);
   const uint32_t sbits = pack_bf16x2(__fdiv_rn(range, 15.f), 0.f) & 0xFFFFu;
   const float s = __uint_as_float(sbits << 16);
-  word = sbits | (__float_as_uint(lo) & 0xFFFF0000u);
+  word = sbits | (lo2 << 16);
   uint32_t n = 0u;
-  if (s > 0.f) {
+  const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+  if (s >= 1e-30f) {
+    // k = round((x - lo) * (1/s)) is at most one off; the remainder x - lo - k s is exact, and its
+    // comparison with s / 2 puts k right (to even on a tie) without a division per channel
+    const float r = __frcp_rn(s), half = 0.5f * s;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const float q = fminf(fmaxf(rintf(__fdiv_rn(f[j] - lo, s)), 0.f), 15.f);
-      n |= static_cast<uint32_t>(static_cast<int>(q)) << (4 * j);
+      const float f = ((j & 1) ? bf16hi(u[j / 2]) : bf16lo(u[j / 2])) - lo;
+      int k = __float2int_rn(f * r);
+      const float rem = fmaf(-static_cast<float>(k), s, f), ar = fabsf(rem);
+      if (ar > half || (ar == half && (k & 1))) k += rem > 0.f ? 1 : -1;
+      n |= static_cast<uint32_t>(min(max(k, 0), 15)) << (4 * j);
+    }
+  } else if (s > 0.f) {  // 1/s would overflow
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float f = ((j & 1) ? bf16hi(u[j / 2]) : bf16lo(u[j / 2])) - lo;
+      n |= static_cast<uint32_t>(min(max(__float2int_rn(__fdiv_rn(f, s)), 0), 15)) << (4 * j);
     }
   }
   return n;
@@ -131,7 +151,8 @@ __device__ __forceinline__ int64_t slot_of(const Rows4 &a, int64_t m, bool repor
   return s;
 }
 
-// One row (token, head) per D / 8 threads, K and V by blockIdx.y.
+// Few tokens of each sequence (N < 16, decoding steps): one row (token, head) per D / 8 threads, K and V
+// by blockIdx.y, straight between the rows and the cache's bytes.
 template <int D, bool LOAD>
 __global__ void __launch_bounds__(256) rows4_kernel(const Rows4 a) {
   constexpr int TR = D / 8;
@@ -148,6 +169,7 @@ __global__ void __launch_bounds__(256) rows4_kernel(const Rows4 a) {
   const int t = static_cast<int>(slot & 15);
   if (LOAD) {
     if (live) *reinterpret_cast<uint4 *>(a.y[side] + at) = get8<D>(rec, side != 0, t, i);
+    else if (in && a.zero) *reinterpret_cast<uint4 *>(a.y[side] + at) = make_uint4(0u, 0u, 0u, 0u);
   } else {
     uint4 v = make_uint4(0u, 0u, 0u, 0u);
     if (live) v = ld_stream_v4(a.x[side] + at);
@@ -155,6 +177,80 @@ __global__ void __launch_bounds__(256) rows4_kernel(const Rows4 a) {
     const uint32_t c = quantise8(v, word);
     put8<D>(rec, side != 0, t, i, c, word, live);
   }
+}
+
+// Longer rows: a CTA takes the tokens of one head that fall on one record, K and V together.  A row's
+// place among the 16 tokens follows the slots (the last one's place in its record lines the chunks up;
+// slots that do not run on are still handled, token by token).  A whole record is put together in
+// shared memory and moved in 16-byte pieces; single tokens go straight to the cache's bytes.
+template <int D, bool LOAD>
+__global__ void __launch_bounds__(2 * D) records4_kernel(const Rows4 a) {
+  using R = Rec4<D>;
+  constexpr int TR = D / 8;
+  __shared__ __align__(16) uint8_t rec[R::BYTES];
+  const int t = threadIdx.x / TR, i = threadIdx.x % TR, h = blockIdx.y, b = blockIdx.z;
+  const int64_t *slots = a.slots + static_cast<int64_t>(b) * a.N;
+  const int64_t last = __ldg(slots + a.N - 1);
+  const int shift = last < 0 ? 0 : static_cast<int>((last - (a.N - 1)) & 15);
+  const int n = static_cast<int>(blockIdx.x) * C4_TOKENS - shift + t;
+  const bool in = n >= 0 && n < a.N;
+  const int64_t slot = in ? slot_of(a, static_cast<int64_t>(b) * a.N + n, i == 0 && h == 0) : -1;
+  const bool live = slot >= 0;
+  __shared__ int64_t first;
+  if (threadIdx.x == 0) first = slot;
+  __syncthreads();
+  const bool whole = __syncthreads_and(live && (first & 15) == 0 && slot == first + t);
+  uint8_t *mem = record_of(a, live ? slot : 0, h, R::BYTES);
+  if (LOAD) {
+    if (whole) {
+      for (int e = threadIdx.x; e < R::BYTES / 16; e += 2 * D)
+        reinterpret_cast<uint4 *>(rec)[e] = ld_stream_v4(mem + 16 * e);
+      __syncthreads();
+    }
+    uint4 o[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
+    if (live) {
+      const uint8_t *src = whole ? rec : mem;
+      const int at = static_cast<int>(slot & 15);
+      o[0] = get8<D>(src, false, at, i);
+      o[1] = get8<D>(src, true, at, i);
+    }
+    if (live || (in && a.zero)) {
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+        *reinterpret_cast<uint4 *>(a.y[s] + b * a.sb[s] + h * a.sh[s] + n * a.sn[s] + 8 * i) = o[s];
+    }
+  } else {
+    uint4 v[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
+    if (live) {
+#pragma unroll
+      for (int s = 0; s < 2; ++s) v[s] = ld_stream_v4(a.x[s] + b * a.sb[s] + h * a.sh[s] + n * a.sn[s] + 8 * i);
+    }
+    uint8_t *dst = whole ? rec : mem;
+    const int at = static_cast<int>(slot & 15);
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      uint32_t word;
+      const uint32_t c = quantise8(v[s], word);
+      put8<D>(dst, s != 0, at, i, c, word, live);
+    }
+    if (whole) {
+      __syncthreads();
+      for (int e = threadIdx.x; e < R::BYTES / 16; e += 2 * D)
+        *reinterpret_cast<uint4 *>(mem + 16 * e) = reinterpret_cast<const uint4 *>(rec)[e];
+    }
+  }
+}
+
+template <int D, bool LOAD>
+cudaError_t launch_rows4(const Rows4 &a, cudaStream_t s) {
+  if (a.N >= C4_TOKENS) {
+    const dim3 grid(static_cast<unsigned>(a.N / C4_TOKENS + 2), static_cast<unsigned>(a.H), static_cast<unsigned>(a.B));
+    records4_kernel<D, LOAD><<<grid, 2 * D, 0, s>>>(a);
+  } else {
+    const int64_t rows = static_cast<int64_t>(a.B) * a.N * a.H, per = 256 / (D / 8);
+    rows4_kernel<D, LOAD><<<dim3(static_cast<unsigned>((rows + per - 1) / per), 2), 256, 0, s>>>(a);
+  }
+  return cudaGetLastError();
 }
 
 }  // namespace
@@ -182,7 +278,7 @@ int check_cache4(const sparge_cache4 *c, Cache4 *out) {
 namespace {
 
 int rows4(const sparge_tensor *k, const sparge_tensor *v, const int64_t *slots, const sparge_cache4 *cache, bool load,
-          sparge_stream_t stream) {
+          int zero, sparge_stream_t stream) {
   clear_error();
   View x[2];
   Cache4 c;
@@ -206,18 +302,13 @@ int rows4(const sparge_tensor *k, const sparge_tensor *v, const int64_t *slots, 
   a.H = c.H; a.N = static_cast<int>(x[0].N); a.B = static_cast<int>(x[0].B);
   a.recs = c.page_size / C4_TOKENS;
   a.status = status_ptr();
-  const int64_t rows = x[0].B * x[0].N * c.H, per = 256 / (c.d / 8), ctas = (rows + per - 1) / per;
-  if (ctas > INT32_MAX) return fail(SPARGE_ERR_UNSUPPORTED, "too many tokens");
-  const dim3 grid(static_cast<unsigned>(ctas), 2);
+  a.zero = zero;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (c.d == 128) {
-    if (load) rows4_kernel<128, true><<<grid, 256, 0, s>>>(a);
-    else rows4_kernel<128, false><<<grid, 256, 0, s>>>(a);
-  } else {
-    if (load) rows4_kernel<64, true><<<grid, 256, 0, s>>>(a);
-    else rows4_kernel<64, false><<<grid, 256, 0, s>>>(a);
-  }
-  const cudaError_t e = cudaGetLastError();
+  cudaError_t e;
+  if (c.d == 128)
+    e = load ? launch_rows4<128, true>(a, s) : launch_rows4<128, false>(a, s);
+  else
+    e = load ? launch_rows4<64, true>(a, s) : launch_rows4<64, false>(a, s);
   return e == cudaSuccess ? SPARGE_OK : cuda_fail(e, load ? "cache load launch" : "cache store launch");
 }
 
@@ -340,12 +431,12 @@ size_t sparge_cache4_bytes(int64_t n_pages, int page_size, int H, int d) {
 
 int sparge_cache4_store(const sparge_tensor *k, const sparge_tensor *v, const int64_t *slots, const sparge_cache4 *cache,
                         sparge_stream_t stream) {
-  return rows4(k, v, slots, cache, false, stream);
+  return rows4(k, v, slots, cache, false, 0, stream);
 }
 
-int sparge_cache4_load(const sparge_cache4 *cache, const int64_t *slots, sparge_tensor *k, sparge_tensor *v,
-                       sparge_stream_t stream) {
-  return rows4(k, v, slots, cache, true, stream);
+int sparge_cache4_load(const sparge_cache4 *cache, const int64_t *slots, int zero_left_out, sparge_tensor *k,
+                       sparge_tensor *v, sparge_stream_t stream) {
+  return rows4(k, v, slots, cache, true, zero_left_out ? 1 : 0, stream);
 }
 
 int sparge_cache_tables(const int32_t *lens, const int32_t *new_lens, int64_t R, int64_t N, int page_size,

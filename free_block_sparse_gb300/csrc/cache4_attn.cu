@@ -27,6 +27,7 @@
 // kernel.
 #include <climits>
 #include <cmath>
+#include <type_traits>
 
 #include "../../include/sparge.h"
 #include "cache4.cuh"
@@ -38,7 +39,6 @@ int check_cache4(const ::sparge_cache4 *c, Cache4 *out);
 namespace {
 
 constexpr int CA_WARPS = 4;
-constexpr int CA_STAGES = 4;     // records in flight per warp
 constexpr int CA_SMS = 152;
 constexpr float CA_RESCALE = 8.f;  // the exponent reference moves when a score passes it by more (log2)
 constexpr float CA_SBOUND = 64.f;  // scaled V scales stay below this: P s < 2^8 2^6 < 65504
@@ -80,8 +80,35 @@ __device__ __forceinline__ Span span_of(const CacheAttnArgs &a, int b) {
   s.recs = s.ns + hi - s.lo;
   return s;
 }
+// Shared memory and the step of a warp: U records at a time (one after another in a CTA's tile of
+// 4 U records), ST steps in a warp's ring.  With 8 rows two records a step keep two chains of dependent
+// products in flight and halve the waits, votes and branches per record; with 16 rows a record already
+// has two of everything and the registers of a second do not fit (d = 128).
+template <int D, int RT>
+struct CaSmem {
+  static constexpr int U = RT == 1 || D == 64 ? 2 : 1;
+  static constexpr int ST = D == 64 ? 5 : 6 / U;
+  static constexpr int REC = Rec4<D>::BYTES;
+  static constexpr int WRING = ST * U * REC;  // of one warp; the item's sums go there at its end
+  static constexpr int OROW = D + 4;          // floats of a row of sums, padded against bank conflicts
+  static_assert(8 * RT * OROW * 4 <= WRING, "a warp's sums fit its ring");
+  static_assert(ST <= 6 && ST * U <= 12, "barriers and flags");
+  static constexpr int OFF_ML = CA_WARPS * WRING, OFF_CTRL = OFF_ML + CA_WARPS * 8 * RT * 8;
+  static constexpr int TOTAL = OFF_CTRL + 512;
+};
+struct CaCtrl {
+  uint64_t full[CA_WARPS][6];
+  int64_t sums[CA_WARPS];
+  int64_t off;
+  int b0, abort;
+  uint8_t bad[CA_WARPS][12];  // the record's page lies outside the pool: its tokens are left out
+};
+static_assert(sizeof(CaCtrl) <= 512, "control block");
+
+// 64 or 32 U-token tiles of all heads and row tiles of a sequence.
+template <int U>
 __device__ __forceinline__ int64_t units_of(const CacheAttnArgs &a, int b) {
-  return static_cast<int64_t>((span_of(a, b).recs + 3) >> 2) * (a.Hkv * a.ntile);
+  return static_cast<int64_t>((span_of(a, b).recs + 4 * U - 1) / (4 * U)) * (a.Hkv * a.ntile);
 }
 
 __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
@@ -96,6 +123,28 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// the same with a zero accumulator
+__device__ __forceinline__ void mma_f16_zero(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                             uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+// scale words of tokens g (u) and g + 8 (v) of this lane, g = lane / 4
+template <int NG>
+__device__ __forceinline__ void words(const uint8_t *p, uint32_t (&u)[NG], uint32_t (&v)[NG]) {
+  const int g = (threadIdx.x & 31) >> 2;
+  if constexpr (NG == 2) {
+    const uint2 a = *reinterpret_cast<const uint2 *>(p + g * 8), b = *reinterpret_cast<const uint2 *>(p + 64 + g * 8);
+    u[0] = a.x; u[1] = a.y;
+    v[0] = b.x; v[1] = b.y;
+  } else {
+    u[0] = *reinterpret_cast<const uint32_t *>(p + g * 4);
+    v[0] = *reinterpret_cast<const uint32_t *>(p + 32 + g * 4);
+  }
 }
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   uint32_t y;
@@ -114,38 +163,20 @@ __device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) 
 __device__ __forceinline__ int exponent_of(float x) { return static_cast<int>((__float_as_uint(x) >> 23) & 0xFFu) - 127; }
 
 template <int D, int RT>
-struct CaSmem {
-  static constexpr int REC = Rec4<D>::BYTES;
-  static constexpr int RING = CA_WARPS * CA_STAGES * REC;
-  static constexpr int OROW = D + 4;  // floats of a merge row, padded against bank conflicts
-  static constexpr int MERGE = CA_WARPS * 8 * RT * OROW * 4;
-  static constexpr int OFF_MERGE = RING, OFF_ML = OFF_MERGE + MERGE, OFF_CTRL = OFF_ML + CA_WARPS * 8 * RT * 8;
-  static constexpr int TOTAL = OFF_CTRL + 512;
-};
-struct CaCtrl {
-  uint64_t full[CA_WARPS][CA_STAGES];
-  int64_t sums[CA_WARPS];
-  int64_t off;
-  int b0, abort;
-  uint8_t bad[CA_WARPS][CA_STAGES];  // the stage's page lies outside the pool: its tokens are left out
-};
-static_assert(sizeof(CaCtrl) <= 512, "control block");
-
-template <int D, int RT>
 __global__ void __launch_bounds__(CA_WARPS * 32, RT == 1 ? 4 : 3) cache4_attn_kernel(const CacheAttnArgs a) {
   using S = CaSmem<D, RT>;
   using R = Rec4<D>;
-  constexpr int NG = D / 64, NW = D / 32, MT = D / 16;
+  constexpr int NG = D / 64, NW = D / 32, MT = D / 16, U = S::U, ST = S::ST;
   extern __shared__ __align__(128) uint8_t smem[];
   CaCtrl &cs = *reinterpret_cast<CaCtrl *>(smem + S::OFF_CTRL);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-  uint8_t *ring = smem + warp * CA_STAGES * S::REC;
+  uint8_t *ring = smem + warp * S::WRING;
 
   // ---- this CTA's share [start, end) of the line of tiles, and the sequence it starts in ----
   const int per = (a.B + CA_WARPS * 32 - 1) / (CA_WARPS * 32);
   const int bt = min(a.B, static_cast<int>(threadIdx.x) * per), bu = min(a.B, bt + per);
   int64_t own = 0;
-  for (int b = bt; b < bu; ++b) own += units_of(a, b);
+  for (int b = bt; b < bu; ++b) own += units_of<U>(a, b);
   int64_t inc = own;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
@@ -156,7 +187,7 @@ __global__ void __launch_bounds__(CA_WARPS * 32, RT == 1 ? 4 : 3) cache4_attn_ke
   if (threadIdx.x == 0) {
     cs.abort = 0;
     for (int w = 0; w < CA_WARPS; ++w)
-      for (int s = 0; s < CA_STAGES; ++s) mbar_init(&cs.full[w][s], 1);
+      for (int s = 0; s < ST; ++s) mbar_init(&cs.full[w][s], U);
     fence_barrier_init();
   }
   __syncthreads();
@@ -169,12 +200,13 @@ __global__ void __launch_bounds__(CA_WARPS * 32, RT == 1 ? 4 : 3) cache4_attn_ke
   // shares only for as many CTAs as there are tiles: between an item's first and last CTA each holds some of it
   const int64_t shares = total < gridDim.x ? total : gridDim.x;
   if (blockIdx.x >= shares) return;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the combining kernel may be set up from here on
   const int64_t start = total * blockIdx.x / shares, end = total * (blockIdx.x + 1) / shares;
   if (before <= start && start < before + own) {
     int b = bt;
     int64_t at = before;
     for (;; ++b) {
-      const int64_t u = units_of(a, b);
+      const int64_t u = units_of<U>(a, b);
       if (start < at + u) break;
       at += u;
     }
@@ -184,11 +216,12 @@ __global__ void __launch_bounds__(CA_WARPS * 32, RT == 1 ? 4 : 3) cache4_attn_ke
   __syncthreads();
   int b = cs.b0;
   int64_t off = cs.off, left = end - start;
-  uint32_t used = 0;  // records this warp has taken through its ring (stage used % STAGES)
+  bool has_bad_once = true;
+  uint32_t used = 0;  // steps this warp has taken through its ring (stage used % ST)
 
   while (left > 0) {
     const Span sp = span_of(a, b);
-    const int tiles = (sp.recs + 3) >> 2;
+    const int tiles = (sp.recs + 4 * U - 1) / (4 * U);
     const int64_t units = static_cast<int64_t>(tiles) * (a.Hkv * a.ntile);
     if (off >= units) {
       off -= units;
@@ -201,57 +234,70 @@ __global__ void __launch_bounds__(CA_WARPS * 32, RT == 1 ? 4 : 3) cache4_attn_ke
     const int item = b * (a.Hkv * a.ntile) + in_b;
     const int row0 = rt * 8 * RT;
 
-    // ---- the copies: this warp's records tile0 * 4 + warp, + 4, ... ----
-    const int k0 = tile0 * 4 + warp, kend = min(sp.recs, (tile0 + nt) * 4);
-    const int nrec = kend > k0 ? (kend - k0 + 3) >> 2 : 0;
+    // ---- the copies: this warp's steps, step i: records k0 + 4 U i .. + U - 1 ----
+    const int k0 = (tile0 * 4 + warp) * U, kend = min(sp.recs, (tile0 + nt) * 4 * U);
+    const int nstep = kend > k0 ? (kend - k0 + 4 * U - 1) / (4 * U) : 0;
     const int32_t *trow = a.table + static_cast<int64_t>(b) * a.table_stride;
-    int pages = 0, pbase = -32;  // page of record i of this warp: lane i - pbase
-    auto record_at = [&](int i) {
-      const int k = k0 + 4 * i;
-      return k < sp.ns ? k : sp.lo + k - sp.ns;
-    };
-    auto issue = [&](int i) {  // called by the whole warp for i = 0, 1, ... in order
-      if (i >= pbase + 32) {
-        pbase = i;
-        const int mine = i + lane;
-        pages = mine < nrec ? __ldg(trow + (record_at(mine) >> a.rec_shift)) : 0;
+    auto record_at = [&](int k) { return k < sp.ns ? k : sp.lo + k - sp.ns; };
+    // The warp looks up the pages of 32 records at a time; the lane that holds a record's address
+    // issues its copy.
+    const uint8_t *src = nullptr;  // record lane % U of step sbase + lane / U (null: no such page, no such record)
+    int sbase = -32;
+    bool has_bad = false;          // some page was outside the pool: the stages' flags count
+    auto issue = [&](int i) {      // called by the whole warp for i = 0, 1, ... in order
+      if (i >= sbase + 32 / U) {
+        sbase = i;
+        const int k = k0 + 4 * U * (i + lane / U) + lane % U;
+        src = nullptr;
+        bool bad = false;
+        if (k < kend) {
+          const int r = record_at(k);
+          const int page = __ldg(trow + (r >> a.rec_shift));
+          bad = page < 0 || page >= a.n_pages;
+          if (bad)
+            record_status(a.status, -1 /* SPARGE_ERR_INVALID_ARG */);
+          else
+            src = a.pool + (((static_cast<int64_t>(page) * a.Hkv + kvh) << a.rec_shift) + (r & ((1 << a.rec_shift) - 1))) * S::REC;
+        }
+        has_bad = __any_sync(0xffffffffu, bad) || has_bad;
       }
-      const int page = __shfl_sync(0xffffffffu, pages, i - pbase);
-      const uint32_t st = (used + i) % CA_STAGES;
-      if (lane == 0) {
-        const int r = record_at(i);
-        const bool bad = page < 0 || page >= a.n_pages;
-        cs.bad[warp][st] = bad;
-        if (bad) {
-          record_status(a.status, -1 /* SPARGE_ERR_INVALID_ARG */);
-          mbar_arrive(&cs.full[warp][st]);
+      if (lane / U == i - sbase) {
+        const uint32_t st = (used + i) % ST;
+        uint64_t *bar = &cs.full[warp][st];
+        if (has_bad) cs.bad[warp][st * U + lane % U] = src == nullptr;
+        if (src != nullptr) {
+          mbar_arrive_expect_tx(bar, S::REC);
+          bulk_load(ring + (st * U + lane % U) * S::REC, src, S::REC, bar);
         } else {
-          const int64_t at = ((static_cast<int64_t>(page) * a.Hkv + kvh) << a.rec_shift) + (r & ((1 << a.rec_shift) - 1));
-          mbar_arrive_expect_tx(&cs.full[warp][st], S::REC);
-          bulk_load(ring + st * S::REC, a.pool + at * S::REC, S::REC, &cs.full[warp][st]);
+          mbar_arrive(bar);
         }
       }
     };
-    const int ahead = min(nrec, CA_STAGES);
+    if (has_bad_once) {  // flags of an earlier item
+      if (lane < 12) cs.bad[warp][lane] = 0;
+      __syncwarp();
+      has_bad_once = false;
+    }
+    const int ahead = min(nstep, ST);
     for (int i = 0; i < ahead; ++i) issue(i);
 
     // ---- Q: B operands of the score product, and per query row the multiplier and the group sums ----
     uint32_t qf[RT][NW][4];
-    float qk[RT][2], qz[RT][2][NG];  // of this lane's rows 2c, 2c + 1 of each row tile
+    float2 qk[RT], qz[RT][NG];  // of this lane's rows 2c, 2c + 1 of each row tile
     int pos[RT][2];
 #pragma unroll
     for (int j = 0; j < RT; ++j) {
       const int r = row0 + 8 * j + g;
       const bool ok = r < a.rows;
       const int h = kvh * a.G + (ok ? r / a.Nq : 0), qi = ok ? r % a.Nq : 0;
-      const uint4 *src = reinterpret_cast<const uint4 *>(a.q + b * a.q_sb + h * a.q_sh + static_cast<int64_t>(qi) * a.q_sn);
+      const uint4 *qrow = reinterpret_cast<const uint4 *>(a.q + b * a.q_sb + h * a.q_sh + static_cast<int64_t>(qi) * a.q_sn);
       float x[NW][8];
       float mx = 0.f, sum[NG];
 #pragma unroll
       for (int w = 0; w < NG; ++w) sum[w] = 0.f;
 #pragma unroll
       for (int w = 0; w < NW; ++w) {
-        const uint4 v = ok ? __ldg(src + 4 * w + c) : make_uint4(0u, 0u, 0u, 0u);
+        const uint4 v = ok ? __ldg(qrow + 4 * w + c) : make_uint4(0u, 0u, 0u, 0u);
         const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -283,29 +329,29 @@ __global__ void __launch_bounds__(CA_WARPS * 32, RT == 1 ? 4 : 3) cache4_attn_ke
       }
       const float mult = a.scale_log2 * pow2i(e + 10);  // 2^24 / f
       const int p = sp.len - a.Nq + qi;                   // rows past the last are computed and dropped
+      const int from = 8 * c;  // the lanes of rows 2c and 2c + 1
+      qk[j] = make_float2(__shfl_sync(0xffffffffu, mult, from), __shfl_sync(0xffffffffu, mult, from + 4));
+      pos[j][0] = __shfl_sync(0xffffffffu, p, from);
+      pos[j][1] = __shfl_sync(0xffffffffu, p, from + 4);
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int from = 4 * (2 * c + k);
-        qk[j][k] = __shfl_sync(0xffffffffu, mult, from);
-        pos[j][k] = __shfl_sync(0xffffffffu, p, from);
-#pragma unroll
-        for (int w = 0; w < NG; ++w) qz[j][k][w] = __shfl_sync(0xffffffffu, sum[w], from) * a.scale_log2;
-      }
+      for (int w = 0; w < NG; ++w)
+        qz[j][w] = make_float2(__shfl_sync(0xffffffffu, sum[w], from) * a.scale_log2,
+                               __shfl_sync(0xffffffffu, sum[w], from + 4) * a.scale_log2);
     }
 
     float acc[MT][RT][4];   // O^T: rows g (channels 16 u + g, times 2^-24 vf) and g + 8 (times 2^-20 vf), columns 2c, 2c + 1
-    float zero[RT][2][NG];  // sum of P times the minima (this lane's tokens)
-    float m_ref[RT][2], l[RT][2];
-    float vf = 0.f;         // 0: not set yet
+    float2 zero[RT][NG];    // sum of P times the minima, and the sum of P (this lane's tokens, rows 2c and 2c + 1)
+    float2 l[RT];
+    float2 nref[RT], thr[RT];  // minus the exponent references, and the scores that move them
+    float vf = 0.f, sbound = -1.f;  // power of two on the V scales (0: not set yet), the scale that moves it
 #pragma unroll
-    for (int j = 0; j < RT; ++j)
+    for (int j = 0; j < RT; ++j) {
+      nref[j] = both(0.f);
+      thr[j] = both(-INFINITY);  // nothing seen yet: the first score moves it
+      l[j] = both(0.f);
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        m_ref[j][k] = -INFINITY;
-        l[j][k] = 0.f;
-#pragma unroll
-        for (int w = 0; w < NG; ++w) zero[j][k][w] = 0.f;
-      }
+      for (int w = 0; w < NG; ++w) zero[j][w] = both(0.f);
+    }
 #pragma unroll
     for (int u = 0; u < MT; ++u)
 #pragma unroll
@@ -313,172 +359,175 @@ __global__ void __launch_bounds__(CA_WARPS * 32, RT == 1 ? 4 : 3) cache4_attn_ke
 #pragma unroll
         for (int k = 0; k < 4; ++k) acc[u][j][k] = 0.f;
 
-    for (int i = 0; i < nrec; ++i) {
-      const uint32_t n = used + i, st = n % CA_STAGES;
-      const bool landed = mbar_wait(&cs.full[warp][st], (n / CA_STAGES) & 1, &cs.abort, a.status);
-      if (!__all_sync(0xffffffffu, landed)) break;
-      const uint8_t *p = ring + st * S::REC;
-      if (!cs.bad[warp][st]) {
-        // ---- scores of tokens g and g + 8 ----
-        float x[RT][4];
-        {
-          uint32_t ka[NW], kb[NW];
-          if constexpr (D == 128) {
-            const uint4 u = *reinterpret_cast<const uint4 *>(p + R::K + g * 64 + c * 16);
-            const uint4 v = *reinterpret_cast<const uint4 *>(p + R::K + (g + 8) * 64 + c * 16);
-            ka[0] = u.x; ka[1] = u.y; ka[2] = u.z; ka[3] = u.w;
-            kb[0] = v.x; kb[1] = v.y; kb[2] = v.z; kb[3] = v.w;
-          } else {
-            const uint2 u = *reinterpret_cast<const uint2 *>(p + R::K + g * 32 + c * 8);
-            const uint2 v = *reinterpret_cast<const uint2 *>(p + R::K + (g + 8) * 32 + c * 8);
-            ka[0] = u.x; ka[1] = u.y;
-            kb[0] = v.x; kb[1] = v.y;
-          }
-          float sc[NG][RT][4];
+    // One step: tokens g and g + 8 of each of its records in this lane.  EDGE: some of its tokens are
+    // hidden from some row, or lie behind the sequence, or on no page.
+    auto step = [&](auto edge_tag, const uint8_t *p, int k) {
+      constexpr bool EDGE = decltype(edge_tag)::value;
+      int tok[U];
+      bool gone[U];  // EDGE: the record is not there
 #pragma unroll
-          for (int w = 0; w < NG; ++w)
+      for (int e = 0; e < U; ++e) {
+        tok[e] = record_at(k + e) * 16;
+        gone[e] = EDGE && (k + e >= kend || (has_bad && cs.bad[warp][static_cast<int>(p - ring) / S::REC + e] != 0));
+      }
+      // ---- scores ----
+      float2 x0[U][RT], x1[U][RT];
 #pragma unroll
-            for (int j = 0; j < RT; ++j)
+      for (int e = 0; e < U; ++e) {
+        const uint8_t *pe = p + e * S::REC;
+        uint32_t ka[NW], kb[NW];
+        if constexpr (D == 128) {
+          const uint4 u = *reinterpret_cast<const uint4 *>(pe + R::K + lane * 16);
+          const uint4 v = *reinterpret_cast<const uint4 *>(pe + R::K + 512 + lane * 16);
+          ka[0] = u.x; ka[1] = u.y; ka[2] = u.z; ka[3] = u.w;
+          kb[0] = v.x; kb[1] = v.y; kb[2] = v.z; kb[3] = v.w;
+        } else {
+          const uint2 u = *reinterpret_cast<const uint2 *>(pe + R::K + lane * 8);
+          const uint2 v = *reinterpret_cast<const uint2 *>(pe + R::K + 256 + lane * 8);
+          ka[0] = u.x; ka[1] = u.y;
+          kb[0] = v.x; kb[1] = v.y;
+        }
+        float sc[NG][RT][4];
 #pragma unroll
-              for (int k = 0; k < 4; ++k) sc[w][j][k] = 0.f;
+        for (int w = 0; w < NW; ++w) {
+          const uint32_t va = ka[w] >> 8, vb = kb[w] >> 8;
 #pragma unroll
-          for (int w = 0; w < NW; ++w) {
-            const uint32_t va = ka[w] >> 8, vb = kb[w] >> 8;
-#pragma unroll
-            for (int j = 0; j < RT; ++j) {
+          for (int j = 0; j < RT; ++j) {
+            if (w % 2 == 0)
+              mma_f16_zero(sc[w / 2][j], ka[w] & 0x000F000Fu, kb[w] & 0x000F000Fu, ka[w] & 0x00F000F0u, kb[w] & 0x00F000F0u,
+                           qf[j][w][0], qf[j][w][1]);
+            else
               mma_f16(sc[w / 2][j], ka[w] & 0x000F000Fu, kb[w] & 0x000F000Fu, ka[w] & 0x00F000F0u, kb[w] & 0x00F000F0u,
                       qf[j][w][0], qf[j][w][1]);
-              mma_f16(sc[w / 2][j], va & 0x000F000Fu, vb & 0x000F000Fu, va & 0x00F000F0u, vb & 0x00F000F0u, qf[j][w][2],
-                      qf[j][w][3]);
-            }
+            mma_f16(sc[w / 2][j], va & 0x000F000Fu, vb & 0x000F000Fu, va & 0x00F000F0u, vb & 0x00F000F0u, qf[j][w][2],
+                    qf[j][w][3]);
           }
-          const uint32_t *kw = reinterpret_cast<const uint32_t *>(p + R::KW);
-          float s0[NG], m0[NG], s1[NG], m1[NG];
-#pragma unroll
-          for (int w = 0; w < NG; ++w) {
-            const uint32_t u = kw[g * NG + w], v = kw[(g + 8) * NG + w];
-            s0[w] = bf16lo(u); m0[w] = bf16hi(u);
-            s1[w] = bf16lo(v); m1[w] = bf16hi(v);
-          }
-#pragma unroll
-          for (int j = 0; j < RT; ++j)
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              float t0 = s0[0] * sc[0][j][k], t1 = s1[0] * sc[0][j][2 + k];
-              float z0 = m0[0] * qz[j][k][0], z1 = m1[0] * qz[j][k][0];
-              if constexpr (NG == 2) {
-                t0 = fmaf(s0[1], sc[1][j][k], t0);
-                t1 = fmaf(s1[1], sc[1][j][2 + k], t1);
-                z0 = fmaf(m0[1], qz[j][k][1], z0);
-                z1 = fmaf(m1[1], qz[j][k][1], z1);
-              }
-              x[j][k] = fmaf(t0, qk[j][k], z0);
-              x[j][2 + k] = fmaf(t1, qk[j][k], z1);
-            }
         }
-        // ---- hidden tokens: past the row's position, or between the first tokens and the window ----
-        const int tok = record_at(i) * 16;
-        const bool edge = tok + 15 > sp.len - a.Nq ||
-                          (a.window > 0 && !(tok + 15 < a.sinks || tok > sp.len - 1 - a.window));
-        if (edge) {
-#pragma unroll
-          for (int j = 0; j < RT; ++j)
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const int t = tok + g + 8 * (k >> 1), q = pos[j][k & 1];
-              const bool seen = t <= q && (a.window == 0 || t < a.sinks || q - t < a.window);
-              if (!seen) x[j][k] = -INFINITY;
-            }
-        }
-        // ---- the exponent reference and the V scales' power of two follow lazily ----
-        const uint32_t *vw = reinterpret_cast<const uint32_t *>(p + R::VW);
-        float s0[NG], m0[NG], s1[NG], m1[NG];
-        float smax = 0.f;
-#pragma unroll
-        for (int w = 0; w < NG; ++w) {
-          uint32_t u = vw[g * NG + w], v = vw[(g + 8) * NG + w];
-          if (edge) {  // places behind the sequence hold anything
-            if (tok + g >= sp.len) u = 0u;
-            if (tok + g + 8 >= sp.len) v = 0u;
-          }
-          s0[w] = bf16lo(u); m0[w] = bf16hi(u);
-          s1[w] = bf16lo(v); m1[w] = bf16hi(v);
-          smax = fmaxf(smax, fmaxf(fabsf(s0[w]), fabsf(s1[w])));
-        }
-        bool move = smax * vf > CA_SBOUND;
-#pragma unroll
-        for (int j = 0; j < RT; ++j)
-#pragma unroll
-          for (int k = 0; k < 2; ++k) move = move || fmaxf(x[j][k], x[j][2 + k]) > m_ref[j][k] + CA_RESCALE;
-        if (__any_sync(0xffffffffu, move)) {
-#pragma unroll
-          for (int o = 4; o <= 16; o <<= 1) smax = fmaxf(smax, __shfl_xor_sync(0xffffffffu, smax, o));
-          float vr = 1.f;
-          if (smax * vf > CA_SBOUND || vf == 0.f) {  // the largest scale to [1, 2): the first tokens set it, outliers move it
-            const float nf = pow2i(-min(max(exponent_of(smax), -100), 100));
-            vr = vf == 0.f ? 1.f : nf / vf;
-            vf = nf;
-          }
-#pragma unroll
-          for (int j = 0; j < RT; ++j)
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              float mx = fmaxf(x[j][k], x[j][2 + k]);
-#pragma unroll
-              for (int o = 4; o <= 16; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-              float al = 1.f;
-              if (mx > m_ref[j][k] + CA_RESCALE) {
-                al = m_ref[j][k] == -INFINITY ? 0.f : exp2f(m_ref[j][k] - mx);
-                m_ref[j][k] = mx;
-              }
-              l[j][k] *= al;
-#pragma unroll
-              for (int w = 0; w < NG; ++w) zero[j][k][w] *= al;
-              al *= vr;
-#pragma unroll
-              for (int u = 0; u < MT; ++u) {
-                acc[u][j][k] *= al;
-                acc[u][j][2 + k] *= al;
-              }
-            }
-        }
-        // ---- P, its sums, and the B operands of the second product ----
-        uint32_t pb[NG][RT][2];
-#pragma unroll
-        for (int w = 0; w < NG; ++w) {
-          s0[w] *= vf;
-          s1[w] *= vf;
-        }
+        uint32_t u[NG], v[NG];
+        words(pe + R::KW, u, v);
 #pragma unroll
         for (int j = 0; j < RT; ++j) {
-          float pr[4];
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const float mr = m_ref[j][k] == -INFINITY ? 0.f : m_ref[j][k];
-            pr[k] = fast_exp2(x[j][k] - mr);
-            pr[2 + k] = fast_exp2(x[j][2 + k] - mr);
-            l[j][k] += pr[k] + pr[2 + k];
+          float2 t0 = fmul2(both(bf16lo(u[0])), make_float2(sc[0][j][0], sc[0][j][1]));
+          float2 t1 = fmul2(both(bf16lo(v[0])), make_float2(sc[0][j][2], sc[0][j][3]));
+          float2 z0 = fmul2(both(bf16hi(u[0])), qz[j][0]), z1 = fmul2(both(bf16hi(v[0])), qz[j][0]);
+          if constexpr (NG == 2) {
+            t0 = ffma2(both(bf16lo(u[1])), make_float2(sc[1][j][0], sc[1][j][1]), t0);
+            t1 = ffma2(both(bf16lo(v[1])), make_float2(sc[1][j][2], sc[1][j][3]), t1);
+            z0 = ffma2(both(bf16hi(u[1])), qz[j][1], z0);
+            z1 = ffma2(both(bf16hi(v[1])), qz[j][1], z1);
           }
+          x0[e][j] = ffma2(t0, qk[j], z0);
+          x1[e][j] = ffma2(t1, qk[j], z1);
+        }
+        // hidden tokens: past the row's position, or between the first tokens and the window
+        if constexpr (EDGE) {
+          auto hide = [&](float &x, int t, int q) {
+            if (!(t <= q && (a.window == 0 || t < a.sinks || q - t < a.window)) || gone[e]) x = -INFINITY;
+          };
 #pragma unroll
-          for (int w = 0; w < NG; ++w) {
-            float e0 = pr[0] * s0[w], e1 = pr[1] * s0[w], e2 = pr[2] * s1[w], e3 = pr[3] * s1[w];
-            float z0 = pr[0] * m0[w], z1 = pr[1] * m0[w], z2 = pr[2] * m1[w], z3 = pr[3] * m1[w];
-            if (edge) {  // a hidden token adds nothing, whatever its scale and minimum are
-              if (pr[0] == 0.f) e0 = z0 = 0.f;
-              if (pr[1] == 0.f) e1 = z1 = 0.f;
-              if (pr[2] == 0.f) e2 = z2 = 0.f;
-              if (pr[3] == 0.f) e3 = z3 = 0.f;
-            }
-            zero[j][0][w] += z0 + z2;
-            zero[j][1][w] += z1 + z3;
-            pb[w][j][0] = transpose8x8(half2_of(e0, e1));
-            pb[w][j][1] = transpose8x8(half2_of(e2, e3));
+          for (int j = 0; j < RT; ++j) {
+            hide(x0[e][j].x, tok[e] + g, pos[j][0]);
+            hide(x0[e][j].y, tok[e] + g, pos[j][1]);
+            hide(x1[e][j].x, tok[e] + g + 8, pos[j][0]);
+            hide(x1[e][j].y, tok[e] + g + 8, pos[j][1]);
           }
         }
-        // ---- O^T += V^T P^T ----
+      }
+      // ---- the exponent reference and the V scales' power of two follow lazily ----
+      uint32_t vu[U][NG], vv[U][NG];
+      float smax = 0.f;
+#pragma unroll
+      for (int e = 0; e < U; ++e) {
+        words(p + e * S::REC + R::VW, vu[e], vv[e]);
 #pragma unroll
         for (int w = 0; w < NG; ++w) {
-          const uint4 v4 = *reinterpret_cast<const uint4 *>(p + R::V + w * 512 + lane * 16);
+          if constexpr (EDGE) {  // places behind the sequence hold anything
+            if (gone[e] || tok[e] + g >= sp.len) vu[e][w] = 0u;
+            if (gone[e] || tok[e] + g + 8 >= sp.len) vv[e][w] = 0u;
+          }
+          smax = fmax3(smax, fabsf(bf16lo(vu[e][w])), fabsf(bf16lo(vv[e][w])));
+        }
+      }
+      bool move = smax > sbound;
+      float2 xm[RT];
+#pragma unroll
+      for (int j = 0; j < RT; ++j) {
+        xm[j] = make_float2(fmaxf(x0[0][j].x, x1[0][j].x), fmaxf(x0[0][j].y, x1[0][j].y));
+        if constexpr (U == 2) {
+          xm[j].x = fmax3(xm[j].x, x0[U - 1][j].x, x1[U - 1][j].x);
+          xm[j].y = fmax3(xm[j].y, x0[U - 1][j].y, x1[U - 1][j].y);
+        }
+        move = move || xm[j].x > thr[j].x || xm[j].y > thr[j].y;
+      }
+      if (__any_sync(0xffffffffu, move)) {
+#pragma unroll
+        for (int o = 4; o <= 16; o <<= 1) smax = fmaxf(smax, __shfl_xor_sync(0xffffffffu, smax, o));
+        float vr = 1.f;
+        if (smax > sbound) {  // the largest scale to [1, 2): the first tokens set it, outliers move it
+          const int e = min(max(exponent_of(smax), -100), 100);
+          const float nf = pow2i(-e);
+          vr = vf == 0.f ? 1.f : nf / vf;
+          vf = nf;
+          sbound = CA_SBOUND * pow2i(e);
+        }
+        auto follow = [&](float &t, float &m, float x) {  // the factor on what has been summed
+#pragma unroll
+          for (int o = 4; o <= 16; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+          if (!(x > t)) return 1.f;
+          const float f = t == -INFINITY ? 0.f : exp2f(-m - x);
+          m = -x;
+          t = x + CA_RESCALE;
+          return f;
+        };
+#pragma unroll
+        for (int j = 0; j < RT; ++j) {
+          float2 al;
+          al.x = follow(thr[j].x, nref[j].x, xm[j].x);
+          al.y = follow(thr[j].y, nref[j].y, xm[j].y);
+          l[j] = fmul2(l[j], al);
+#pragma unroll
+          for (int w = 0; w < NG; ++w) zero[j][w] = fmul2(zero[j][w], al);
+          al = fmul2(al, both(vr));
+#pragma unroll
+          for (int u = 0; u < MT; ++u) {
+            acc[u][j][0] *= al.x;
+            acc[u][j][1] *= al.y;
+            acc[u][j][2] *= al.x;
+            acc[u][j][3] *= al.y;
+          }
+        }
+      }
+      // ---- per record: P, its sums and the B operands of the second product, then O^T += V^T P^T ----
+#pragma unroll
+      for (int e = 0; e < U; ++e) {
+        uint32_t pb[NG][RT][2];
+#pragma unroll
+        for (int j = 0; j < RT; ++j) {
+          const float2 y0 = fadd2(x0[e][j], nref[j]), y1 = fadd2(x1[e][j], nref[j]);
+          const float2 p0 = make_float2(fast_exp2(y0.x), fast_exp2(y0.y));
+          const float2 p1 = make_float2(fast_exp2(y1.x), fast_exp2(y1.y));
+          l[j] = fadd2(l[j], fadd2(p0, p1));
+#pragma unroll
+          for (int w = 0; w < NG; ++w) {
+            const float m0 = bf16hi(vu[e][w]), m1 = bf16hi(vv[e][w]);
+            float2 e0 = fmul2(p0, both(bf16lo(vu[e][w]) * vf)), e1 = fmul2(p1, both(bf16lo(vv[e][w]) * vf));
+            if constexpr (EDGE) {  // a hidden token adds nothing, whatever its scale and minimum are
+              float2 z0 = fmul2(p0, both(m0)), z1 = fmul2(p1, both(m1));
+              if (p0.x == 0.f) e0.x = z0.x = 0.f;
+              if (p0.y == 0.f) e0.y = z0.y = 0.f;
+              if (p1.x == 0.f) e1.x = z1.x = 0.f;
+              if (p1.y == 0.f) e1.y = z1.y = 0.f;
+              zero[j][w] = fadd2(zero[j][w], fadd2(z0, z1));
+            } else {
+              zero[j][w] = ffma2(p0, both(m0), ffma2(p1, both(m1), zero[j][w]));
+            }
+            pb[w][j][0] = transpose8x8(half2_of(e0.x, e0.y));
+            pb[w][j][1] = transpose8x8(half2_of(e1.x, e1.y));
+          }
+        }
+#pragma unroll
+        for (int w = 0; w < NG; ++w) {
+          const uint4 v4 = *reinterpret_cast<const uint4 *>(p + e * S::REC + R::V + w * 512 + lane * 16);
           const uint32_t v[4] = {v4.x, v4.y, v4.z, v4.w};
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
@@ -490,13 +539,31 @@ __global__ void __launch_bounds__(CA_WARPS * 32, RT == 1 ? 4 : 3) cache4_attn_ke
           }
         }
       }
+    };
+
+    // records that every row sees whole: up to r_full, and (window) up to r_sinks or from r_win on
+    const int r_full = (sp.len - a.Nq - 15) >> 4;
+    const int r_win = a.window > 0 ? ((sp.len - 1 - a.window) >> 4) + 1 : INT_MIN;
+    const int r_sinks = a.sinks >> 4;
+    for (int i = 0; i < nstep; ++i) {
+      const uint32_t n = used + i, st = n % ST;
+      const bool landed = mbar_wait(&cs.full[warp][st], (n / ST) & 1, &cs.abort, a.status);
+      if (!__all_sync(0xffffffffu, landed)) break;
+      const uint8_t *p = ring + st * (U * S::REC);
+      const int k = k0 + 4 * U * i, r = record_at(k), r1 = record_at(k + U - 1);
+      // (a step that holds the last of the first tokens and the window's first record is an edge)
+      if (has_bad || k + U > kend || r1 > r_full || (r < r_win && (r1 >= r_sinks)))
+        step(std::true_type{}, p, k);
+      else
+        step(std::false_type{}, p, k);
       __syncwarp();  // every lane has read the stage
-      if (i + CA_STAGES < nrec) issue(i + CA_STAGES);
+      if (i + ST < nstep) issue(i + ST);
     }
-    used += nrec;
+    has_bad_once = has_bad;
+    used += nstep;
 
     // ---- the item's (or its share's) end: the warps' sums into shared memory, then merged ----
-    float *mo = reinterpret_cast<float *>(smem + S::OFF_MERGE) + warp * 8 * RT * S::OROW;
+    float *mo = reinterpret_cast<float *>(ring);  // every copy of the item has landed and been read
     float2 *ml = reinterpret_cast<float2 *>(smem + S::OFF_ML);
     const float back = vf == 0.f ? 0.f : 16777216.f / vf;  // 2^24 / vf
 #pragma unroll
@@ -504,17 +571,17 @@ __global__ void __launch_bounds__(CA_WARPS * 32, RT == 1 ? 4 : 3) cache4_attn_ke
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const int row = 8 * j + 2 * c + k;
-        float ls = l[j][k];
+        float ls = k ? l[j].y : l[j].x;
 #pragma unroll
         for (int o = 4; o <= 16; o <<= 1) ls += __shfl_xor_sync(0xffffffffu, ls, o);
         float z[NG];
 #pragma unroll
         for (int w = 0; w < NG; ++w) {
-          z[w] = zero[j][k][w];
+          z[w] = k ? zero[j][w].y : zero[j][w].x;
 #pragma unroll
           for (int o = 4; o <= 16; o <<= 1) z[w] += __shfl_xor_sync(0xffffffffu, z[w], o);
         }
-        if (g == 0) ml[warp * 8 * RT + row] = make_float2(m_ref[j][k], ls);
+        if (g == 0) ml[warp * 8 * RT + row] = make_float2((k ? thr[j].y : thr[j].x) == -INFINITY ? -INFINITY : -(k ? nref[j].y : nref[j].x), ls);
 #pragma unroll
         for (int u = 0; u < MT; ++u) {
           mo[row * S::OROW + 16 * u + g] = fmaf(acc[u][j][k], back, z[u / 4]);
@@ -544,8 +611,7 @@ __global__ void __launch_bounds__(CA_WARPS * 32, RT == 1 ? 4 : 3) cache4_attn_ke
       for (int u = 0; u < CA_WARPS; ++u) {
         // a warp without a visible token has the reference -inf; its sums are 0 (NaN inputs: NaN)
         const float f = w[u].x == -INFINITY ? (w[u].y == 0.f ? 0.f : 1.f) : exp2f(w[u].x - M);
-        const float4 v = *reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(smem + S::OFF_MERGE) +
-                                                           (u * 8 * RT + row) * S::OROW + 4 * d4);
+        const float4 v = *reinterpret_cast<const float4 *>(smem + u * S::WRING + (row * S::OROW + 4 * d4) * 4);
         if (f != 0.f) {
           L = fmaf(f, w[u].y, L);
           o.x = fmaf(f, v.x, o.x);
@@ -566,6 +632,7 @@ __global__ void __launch_bounds__(CA_WARPS * 32, RT == 1 ? 4 : 3) cache4_attn_ke
         if (d4 == 0) *reinterpret_cast<float2 *>(a.part_ml + (slot * 8 * RT + row) * 2) = make_float2(M, L);
       }
     }
+    fence_proxy_async_smem();  // the sums' reads and writes before the next item's copies into the same places
     __syncthreads();
     if (*reinterpret_cast<volatile int *>(&cs.abort)) break;
     off += nt;
@@ -579,39 +646,78 @@ __global__ void __launch_bounds__(CA_WARPS * 32, RT == 1 ? 4 : 3) cache4_attn_ke
 }
 
 // Items cut between CTAs: the CTAs' partial rows (at CTA + item, a place of its own for every pair
-// that meets) weighted by 2^(m - M) in the order of the CTAs and divided by the weighted sum.
-// Items without a token get zero rows.  One CTA of D / 4 threads per (item, row).
+// that meets) weighted by 2^(m - M) and divided by the weighted sum, in an order that the lengths alone
+// set.  Items without a token get zero rows.  One CTA per (item, row): its threads first find the weights,
+// one per share, then D / 4 threads times 512 / D groups add up the rows, each group every
+// (512 / D)-th share, so even the 76 shares of a single long sequence take a few memory latencies.
+// Launched so that it may start while the attention ends (programmatic dependent launch); nothing is
+// read before the wait.
+constexpr int CC_THREADS = 128;
 template <int D, int RT>
-__global__ void __launch_bounds__(D / 4) cache4_combine_kernel(const CacheAttnArgs a) {
+__global__ void __launch_bounds__(CC_THREADS) cache4_combine_kernel(const CacheAttnArgs a) {
+  constexpr int NL = D / 4, NGRP = CC_THREADS / NL;
+  __shared__ float wgt[CA_SMS * 4];
+  __shared__ float red[2][CC_THREADS / 32];
+  __shared__ float4 sums[NGRP][NL];
   const int item = blockIdx.x, row = blockIdx.y, per = a.Hkv * a.ntile;
   const int b = item / per, kvh = item % per / a.ntile, r = (item % a.ntile) * 8 * RT + row;
   if (r >= a.rows) return;
-  const int h = kvh * a.G + r / a.Nq, qi = r % a.Nq, d4 = threadIdx.x;
+  const int t = threadIdx.x, lane = t & 31, d4 = t % NL, grp = t / NL;
+  const int h = kvh * a.G + r / a.Nq, qi = r % a.Nq;
   __nv_bfloat16 *out = a.o + b * a.o_sb + h * a.o_sh + static_cast<int64_t>(qi) * a.o_sn + 4 * d4;
-  if (units_of(a, b) == 0) {
-    *reinterpret_cast<uint2 *>(out) = make_uint2(0u, 0u);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (span_of(a, b).recs == 0) {
+    if (grp == 0) *reinterpret_cast<uint2 *>(out) = make_uint2(0u, 0u);
     return;
   }
   const int2 ends = a.ends[item];
-  if (ends.x == ends.y) return;  // written by its only CTA
+  const int n = ends.y - ends.x + 1;
+  if (n <= 1) return;  // written by its only CTA
+  const int64_t at0 = (static_cast<int64_t>(ends.x) + item) * 8 * RT + row;
   float M = -INFINITY;
-  for (int w = ends.x; w <= ends.y; ++w)
-    M = fmaxf(M, a.part_ml[((static_cast<int64_t>(w) + item) * 8 * RT + row) * 2]);
+  for (int w = t; w < n; w += CC_THREADS) M = fmaxf(M, a.part_ml[(at0 + static_cast<int64_t>(w) * 8 * RT) * 2]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  if (lane == 0) red[0][t >> 5] = M;
+  __syncthreads();
+#pragma unroll
+  for (int u = 0; u < CC_THREADS / 32; ++u) M = fmaxf(M, red[0][u]);
   float L = 0.f;
+  for (int w = t; w < n; w += CC_THREADS) {
+    const float2 ml = *reinterpret_cast<const float2 *>(a.part_ml + (at0 + static_cast<int64_t>(w) * 8 * RT) * 2);
+    const float f = ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : 1.f) : exp2f(ml.x - M);
+    wgt[w] = f;
+    if (f != 0.f) L = fmaf(f, ml.y, L);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+  if (lane == 0) red[1][t >> 5] = L;
+  __syncthreads();
+  L = 0.f;
+#pragma unroll
+  for (int u = 0; u < CC_THREADS / 32; ++u) L += red[1][u];
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-  for (int w = ends.x; w <= ends.y; ++w) {
-    const int64_t at = (static_cast<int64_t>(w) + item) * 8 * RT + row;
-    const float2 ml = *reinterpret_cast<const float2 *>(a.part_ml + at * 2);
-    const float4 v = *reinterpret_cast<const float4 *>(a.part_o + at * D + 4 * d4);
-    const float f = ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : 1.f) : exp2f(ml.x - M);
+  for (int w = grp; w < n; w += NGRP) {
+    const float4 v = *reinterpret_cast<const float4 *>(a.part_o + (at0 + static_cast<int64_t>(w) * 8 * RT) * D + 4 * d4);
+    const float f = wgt[w];
     if (f != 0.f) {
-      L = fmaf(f, ml.y, L);
       o.x = fmaf(f, v.x, o.x);
       o.y = fmaf(f, v.y, o.y);
       o.z = fmaf(f, v.z, o.z);
       o.w = fmaf(f, v.w, o.w);
     }
+  }
+  sums[grp][d4] = o;
+  __syncthreads();
+  if (grp != 0) return;
+#pragma unroll
+  for (int u = 1; u < NGRP; ++u) {
+    const float4 v = sums[u][d4];
+    o.x += v.x;
+    o.y += v.y;
+    o.z += v.z;
+    o.w += v.w;
   }
   const float inv = L == 0.f ? 0.f : 1.f / L;
   uint2 w2;
@@ -649,8 +755,16 @@ cudaError_t launch_cache_attn(const CacheAttnArgs &a, int64_t tiles, cudaStream_
   cache4_attn_kernel<D, RT><<<static_cast<unsigned>(ctas), CA_WARPS * 32, S::TOTAL, st>>>(a);
   if (cudaError_t e = cudaGetLastError(); e != cudaSuccess) return e;
   const unsigned items = static_cast<unsigned>(a.B * a.Hkv * a.ntile);
-  cache4_combine_kernel<D, RT><<<dim3(items, static_cast<unsigned>(a.rows < 8 * RT ? a.rows : 8 * RT)), D / 4, 0, st>>>(a);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(items, static_cast<unsigned>(a.rows < 8 * RT ? a.rows : 8 * RT));
+  cfg.blockDim = dim3(CC_THREADS);
+  cfg.stream = st;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, cache4_combine_kernel<D, RT>, a);
 }
 
 }  // namespace
@@ -719,7 +833,8 @@ int sparge_cache4_attn(const sparge_tensor *q, const sparge_cache4 *cache, const
     const int64_t most = (window + qv.N + 15) / 16 + 1 + (sinks + 15) / 16;
     recs = recs < most ? recs : most;
   }
-  int64_t tiles = (recs + 3) / 4 * qv.B * c.H * ntile;
+  const int64_t step = qv.d == 64 || rt == 1 ? 8 : 4;  // records of a CTA's tile
+  int64_t tiles = (recs + step - 1) / step * qv.B * c.H * ntile;
   if (tiles < 1) tiles = 1;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e;

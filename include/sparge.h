@@ -353,12 +353,12 @@ int sparge_cache_tables(const int32_t *lens, const int32_t *new_lens, int64_t R,
  * group that holds an infinity or a NaN reads back as NaN.  A negative slot leaves its token out; a slot past
  * the pool is left out and records SPARGE_ERR_INVALID_ARG in the device status word.  Slots must
  * differ from one another (of equal ones each byte holds one of them).
- * sparge_cache4_load reads the same rows back as bf16 (rows with a left-out slot stay as they were),
- * for instance all tokens of a sequence for sparge_attn over a chunk of queries.
+ * sparge_cache4_load reads the same rows back as bf16, for instance all tokens of a sequence for sparge_attn
+ * over a chunk of queries.  Rows with a left-out slot become zero with zero_left_out, else stay as they were.
  */
 int sparge_cache4_store(const sparge_tensor *k, const sparge_tensor *v, const int64_t *slots,
                         const sparge_cache4 *cache, sparge_stream_t stream);
-int sparge_cache4_load(const sparge_cache4 *cache, const int64_t *slots, sparge_tensor *k, sparge_tensor *v,
+int sparge_cache4_load(const sparge_cache4 *cache, const int64_t *slots, int zero_left_out, sparge_tensor *k, sparge_tensor *v,
                        sparge_stream_t stream);
 
 /*

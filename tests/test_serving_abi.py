@@ -79,7 +79,7 @@ def test_store_and_load_refuse(lib, load, change, code):
     a.update(change)
     ref = lambda x: None if x is None else ctypes.byref(x)  # noqa: E731
     k, v, c = ref(a["k"]), ref(a["v"]), ref(a["c"])
-    rc = lib.sparge_cache4_load(c, a["slots"], k, v, None) if load else lib.sparge_cache4_store(k, v, a["slots"], c, None)
+    rc = lib.sparge_cache4_load(c, a["slots"], 0, k, v, None) if load else lib.sparge_cache4_store(k, v, a["slots"], c, None)
     refused(lib, rc, code)
 
 
