@@ -119,7 +119,7 @@ __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t b
 }
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -127,7 +127,7 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
 // the same with a zero accumulator
 __device__ __forceinline__ void mma_f16_zero(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                              uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
       : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
@@ -647,83 +647,117 @@ __global__ void __launch_bounds__(CA_WARPS * 32, RT == 1 ? 4 : 3) cache4_attn_ke
 
 // Items cut between CTAs: the CTAs' partial rows (at CTA + item, a place of its own for every pair
 // that meets) weighted by 2^(m - M) and divided by the weighted sum, in an order that the lengths alone
-// set.  Items without a token get zero rows.  One CTA per (item, row): its threads first find the weights,
-// one per share, then D / 4 threads times 512 / D groups add up the rows, each group every
-// (512 / D)-th share, so even the 76 shares of a single long sequence take a few memory latencies.
+// set.  Items without a token get zero rows.  A CTA takes `nrow` rows of an item: one row per warp
+// where the item has few shares (many items, each cut once or twice), the whole CTA on one row after
+// another where it has many (one long sequence: 76 shares), so either way a few memory latencies.
 // Launched so that it may start while the attention ends (programmatic dependent launch); nothing is
 // read before the wait.
-constexpr int CC_THREADS = 128;
+constexpr int CC_THREADS = 128, CC_FEW = 8;
 template <int D, int RT>
-__global__ void __launch_bounds__(CC_THREADS) cache4_combine_kernel(const CacheAttnArgs a) {
-  constexpr int NL = D / 4, NGRP = CC_THREADS / NL;
+__global__ void __launch_bounds__(CC_THREADS) cache4_combine_kernel(const CacheAttnArgs a, int nrow) {
+  constexpr int NL = D / 4, NGRP = CC_THREADS / NL, U = CaSmem<D, RT>::U;
   __shared__ float wgt[CA_SMS * 4];
   __shared__ float red[2][CC_THREADS / 32];
   __shared__ float4 sums[NGRP][NL];
-  const int item = blockIdx.x, row = blockIdx.y, per = a.Hkv * a.ntile;
-  const int b = item / per, kvh = item % per / a.ntile, r = (item % a.ntile) * 8 * RT + row;
-  if (r >= a.rows) return;
-  const int t = threadIdx.x, lane = t & 31, d4 = t % NL, grp = t / NL;
-  const int h = kvh * a.G + r / a.Nq, qi = r % a.Nq;
-  __nv_bfloat16 *out = a.o + b * a.o_sb + h * a.o_sh + static_cast<int64_t>(qi) * a.o_sn + 4 * d4;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (span_of(a, b).recs == 0) {
-    if (grp == 0) *reinterpret_cast<uint2 *>(out) = make_uint2(0u, 0u);
-    return;
-  }
-  const int2 ends = a.ends[item];
-  const int n = ends.y - ends.x + 1;
-  if (n <= 1) return;  // written by its only CTA
-  const int64_t at0 = (static_cast<int64_t>(ends.x) + item) * 8 * RT + row;
-  float M = -INFINITY;
-  for (int w = t; w < n; w += CC_THREADS) M = fmaxf(M, a.part_ml[(at0 + static_cast<int64_t>(w) * 8 * RT) * 2]);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  if (lane == 0) red[0][t >> 5] = M;
-  __syncthreads();
-#pragma unroll
-  for (int u = 0; u < CC_THREADS / 32; ++u) M = fmaxf(M, red[0][u]);
-  float L = 0.f;
-  for (int w = t; w < n; w += CC_THREADS) {
-    const float2 ml = *reinterpret_cast<const float2 *>(a.part_ml + (at0 + static_cast<int64_t>(w) * 8 * RT) * 2);
-    const float f = ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : 1.f) : exp2f(ml.x - M);
-    wgt[w] = f;
-    if (f != 0.f) L = fmaf(f, ml.y, L);
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-  if (lane == 0) red[1][t >> 5] = L;
-  __syncthreads();
-  L = 0.f;
-#pragma unroll
-  for (int u = 0; u < CC_THREADS / 32; ++u) L += red[1][u];
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int w = grp; w < n; w += NGRP) {
-    const float4 v = *reinterpret_cast<const float4 *>(a.part_o + (at0 + static_cast<int64_t>(w) * 8 * RT) * D + 4 * d4);
-    const float f = wgt[w];
+  const int item = blockIdx.x, per = a.Hkv * a.ntile;
+  const int b = item / per, kvh = item % per / a.ntile, row0 = (item % a.ntile) * 8 * RT;
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5, d4 = t % NL, grp = t / NL;
+  const int last = min(8 * RT, a.rows - row0), first = blockIdx.y * nrow;
+  auto out = [&](int row) {
+    const int r = row0 + row, h = kvh * a.G + r / a.Nq, qi = r % a.Nq;
+    return a.o + b * a.o_sb + h * a.o_sh + static_cast<int64_t>(qi) * a.o_sn;
+  };
+  auto put = [&](__nv_bfloat16 *to, float4 o, float inv) {
+    uint2 w;
+    w.x = pack_bf16x2(o.x * inv, o.y * inv);
+    w.y = pack_bf16x2(o.z * inv, o.w * inv);
+    *reinterpret_cast<uint2 *>(to) = w;
+  };
+  auto add = [](float4 &o, float f, float4 v) {
     if (f != 0.f) {
       o.x = fmaf(f, v.x, o.x);
       o.y = fmaf(f, v.y, o.y);
       o.z = fmaf(f, v.z, o.z);
       o.w = fmaf(f, v.w, o.w);
     }
+  };
+  // the weight of a share of reference m and sum l (without a visible token: -inf and 0; NaN inputs: NaN)
+  auto weight = [](float m, float l, float M) { return m == -INFINITY ? (l == 0.f ? 0.f : 1.f) : exp2f(m - M); };
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (units_of<U>(a, b) == 0) {
+    for (int row = first + warp; row < min(last, first + nrow); row += CC_THREADS / 32)
+      if (lane < NL) put(out(row) + 4 * lane, make_float4(0.f, 0.f, 0.f, 0.f), 0.f);
+    return;
   }
-  sums[grp][d4] = o;
-  __syncthreads();
-  if (grp != 0) return;
+  const int2 ends = a.ends[item];
+  const int n = ends.y - ends.x + 1;
+  if (n <= 1) return;  // written by its only CTA
+  const int64_t at0 = (static_cast<int64_t>(ends.x) + item) * 8 * RT;
+  if (n <= CC_FEW) {
+    for (int row = first + warp; row < min(last, first + nrow); row += CC_THREADS / 32) {
+      float2 ml = make_float2(-INFINITY, 0.f);
+      if (lane < n) ml = *reinterpret_cast<const float2 *>(a.part_ml + (at0 + static_cast<int64_t>(lane) * 8 * RT + row) * 2);
+      float4 v[CC_FEW];
+      if (lane < NL) {
 #pragma unroll
-  for (int u = 1; u < NGRP; ++u) {
-    const float4 v = sums[u][d4];
-    o.x += v.x;
-    o.y += v.y;
-    o.z += v.z;
-    o.w += v.w;
+        for (int w = 0; w < CC_FEW; ++w)
+          if (w < n) v[w] = *reinterpret_cast<const float4 *>(a.part_o + (at0 + static_cast<int64_t>(w) * 8 * RT + row) * D + 4 * lane);
+      }
+      float M = ml.x;
+#pragma unroll
+      for (int o = 4; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+      M = __shfl_sync(0xffffffffu, M, 0);
+      const float f = weight(ml.x, ml.y, M);
+      float L = f != 0.f ? f * ml.y : 0.f;
+#pragma unroll
+      for (int o = 4; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+      L = __shfl_sync(0xffffffffu, L, 0);
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < CC_FEW; ++w) {
+        const float fw = __shfl_sync(0xffffffffu, f, w);
+        if (w < n && lane < NL) add(o, fw, v[w]);
+      }
+      if (lane < NL) put(out(row) + 4 * lane, o, L == 0.f ? 0.f : 1.f / L);
+    }
+    return;
   }
-  const float inv = L == 0.f ? 0.f : 1.f / L;
-  uint2 w2;
-  w2.x = pack_bf16x2(o.x * inv, o.y * inv);
-  w2.y = pack_bf16x2(o.z * inv, o.w * inv);
-  *reinterpret_cast<uint2 *>(out) = w2;
+  for (int row = first; row < min(last, first + nrow); ++row) {
+    float M = -INFINITY;
+    for (int w = t; w < n; w += CC_THREADS) M = fmaxf(M, a.part_ml[(at0 + static_cast<int64_t>(w) * 8 * RT + row) * 2]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    if (lane == 0) red[0][warp] = M;
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < CC_THREADS / 32; ++u) M = fmaxf(M, red[0][u]);
+    float L = 0.f;
+    for (int w = t; w < n; w += CC_THREADS) {
+      const float2 ml = *reinterpret_cast<const float2 *>(a.part_ml + (at0 + static_cast<int64_t>(w) * 8 * RT + row) * 2);
+      const float f = weight(ml.x, ml.y, M);
+      wgt[w] = f;
+      if (f != 0.f) L = fmaf(f, ml.y, L);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+    if (lane == 0) red[1][warp] = L;
+    __syncthreads();
+    L = 0.f;
+#pragma unroll
+    for (int u = 0; u < CC_THREADS / 32; ++u) L += red[1][u];
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int w = grp; w < n; w += NGRP)
+      add(o, wgt[w], *reinterpret_cast<const float4 *>(a.part_o + (at0 + static_cast<int64_t>(w) * 8 * RT + row) * D + 4 * d4));
+    sums[grp][d4] = o;
+    __syncthreads();
+    if (grp == 0) {
+#pragma unroll
+      for (int u = 1; u < NGRP; ++u) add(o, 1.f, sums[u][d4]);
+      put(out(row) + 4 * d4, o, L == 0.f ? 0.f : 1.f / L);
+    }
+    __syncthreads();
+  }
 }
 
 // Row tiles of 8 rows for up to 8 query rows per KV head, else of 16: a CTA of 16-row tiles holds
@@ -754,9 +788,12 @@ cudaError_t launch_cache_attn(const CacheAttnArgs &a, int64_t tiles, cudaStream_
   const int64_t most = max_ctas(RT), ctas = tiles < most ? tiles : most;
   cache4_attn_kernel<D, RT><<<static_cast<unsigned>(ctas), CA_WARPS * 32, S::TOTAL, st>>>(a);
   if (cudaError_t e = cudaGetLastError(); e != cudaSuccess) return e;
-  const unsigned items = static_cast<unsigned>(a.B * a.Hkv * a.ntile);
+  // rows of a combining CTA: one per warp where items outnumber half the CTAs (an item then has few
+  // shares), else one
+  const int64_t items = static_cast<int64_t>(a.B) * a.Hkv * a.ntile;
+  const int nrow = 2 * items > ctas ? CC_THREADS / 32 : 1, rows = a.rows < 8 * RT ? a.rows : 8 * RT;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(items, static_cast<unsigned>(a.rows < 8 * RT ? a.rows : 8 * RT));
+  cfg.gridDim = dim3(static_cast<unsigned>(items), static_cast<unsigned>((rows + nrow - 1) / nrow));
   cfg.blockDim = dim3(CC_THREADS);
   cfg.stream = st;
   cudaLaunchAttribute at;
@@ -764,7 +801,7 @@ cudaError_t launch_cache_attn(const CacheAttnArgs &a, int64_t tiles, cudaStream_
   at.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, cache4_combine_kernel<D, RT>, a);
+  return cudaLaunchKernelEx(&cfg, cache4_combine_kernel<D, RT>, a, nrow);
 }
 
 }  // namespace
