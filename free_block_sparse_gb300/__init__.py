@@ -10,7 +10,6 @@ from __future__ import annotations
 import ctypes
 import math
 import os
-import struct
 from typing import Optional
 
 import numpy as np
@@ -159,67 +158,20 @@ def _stream():
     return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
 
 
-# The serving calls are made once per token and layer, so what they spend on the host counts: their
-# tensors are described by packed bytes (a sparge_tensor's layout) instead of a ctypes structure, and
-# device and stream are read without the wrappers' objects (a norm-and-rotation call from 28 to 12 us).
-_TENSOR = struct.Struct("@qiiqqqqqqq")
-_CACHE4 = struct.Struct("@qqiiii")
+_binding_module = None
 
 
-def _here(t):
-    """The current device, which must be t's: the calls run on its current stream."""
-    dev = _torch().cuda.current_device()
-    _on(t, "tensor", dev)
-    return dev
-
-
-def _on(t, name, dev):
-    if not isinstance(t, _torch_module.Tensor):
-        raise TypeError("%s must be a CUDA tensor" % name)
-    if t.get_device() != dev:
-        raise ValueError("%s is on %s, the current CUDA device is cuda:%d" % (name, t.device, dev))
-
-
-def _raw_stream(dev):
-    return _torch_module._C._cuda_getCurrentRawStream(dev)
-
-
-def _rows(t, name, dev):
-    """A bf16 (B, H, N, d) tensor as the bytes of a sparge_tensor."""
-    _on(t, name, dev)
-    shape, stride = t.shape, t.stride()
-    if t.dtype is not _torch_module.bfloat16 or len(shape) != 4 or stride[3] != 1:
-        raise TypeError("%s: expected a bf16 (B, H, N, d) tensor with contiguous last dim" % name)
-    return _TENSOR.pack(t.data_ptr(), SPARGE_BF16, 0, shape[0], shape[1], shape[2], shape[3], stride[0], stride[1], stride[2])
-
-
-def _array(x, dtype, name, dev, shape=None):
-    """A contiguous CUDA array (of the given shape) as a device pointer; None: NULL."""
-    if x is None:
-        return None
-    _on(x, name, dev)
-    if x.dtype is not dtype or not x.is_contiguous() or (shape is not None and x.shape != shape):
-        raise TypeError("%s must be a contiguous %s tensor%s" % (name, dtype, "" if shape is None else " of shape %s" % (tuple(shape),)))
-    return x.data_ptr()
-
-
-def _page_table(table, rows, dev):
-    """(pointer, width, stride between rows) of an int32 (rows, width) page table."""
-    _on(table, "table", dev)
-    shape, stride = table.shape, table.stride()
-    if table.dtype is not _torch_module.int32 or len(shape) != 2 or shape[0] != rows or (shape[1] > 1 and stride[1] != 1):
-        raise TypeError("table must be an int32 (%d, width) tensor with contiguous rows" % rows)
-    return table.data_ptr(), shape[1], stride[0] if rows > 1 else shape[1]
-
-
-def _pool(pool, dev):
-    """The bytes of a pool's sparge_cache4, its heads and its head dim."""
-    _on(pool, "pool", dev)
-    shape = pool.shape
-    if pool.dtype is not _torch_module.uint8 or len(shape) != 4 or not pool.is_contiguous() or shape[3] % 18:
-        raise TypeError("pool must be a contiguous uint8 tensor of shape (n_pages, H, page_size / 16, 18 d)")
-    H, d = shape[1], shape[3] // 18
-    return _CACHE4.pack(pool.data_ptr(), shape[0], 16 * shape[2], H, d, 0), H, d
+def _load_binding():
+    """The compiled binding of the serving calls (csrc/binding.cpp).  They are made once per token and layer, and at
+    decoding sizes a call through ctypes takes the host longer than its kernels take the GPU."""
+    global _binding_module
+    if _binding_module is None:
+        lib()     # the library the binding calls into
+        _torch()  # and torch's own libraries
+        from . import _binding as m
+        m.set_error(SpargeError)
+        _binding_module = m
+    return _binding_module
 
 
 def _desc(t) -> sparge_tensor:
@@ -487,19 +439,7 @@ def unpermute_tokens(x, perm, out=None):
 def window_attn(q, k, v, window: int, sinks: int = 0, scale: float = 0.0, out=None, ws=None):
     """Causal attention over each query's last `window` keys (itself included) and the first `sinks` keys; q may be
     shorter than k and v (its last query sits on the last key)."""
-    dev = _here(q)
-    if out is None:
-        out = _torch_module.empty_like(q)
-    dq, dk, dv, do = _rows(q, "q", dev), _rows(k, "k", dev), _rows(v, "v", dev), _rows(out, "out", dev)
-    L = lib()
-    if ws is None:
-        B, H, N, d = k.shape
-        ws = _torch_module.empty(max(1, L.sparge_workspace_bytes(SPARGE_OP_WINDOW_ATTN, B, q.shape[1], H, N, d)),
-                                 dtype=_torch_module.uint8, device=q.device)
-    _on(ws, "ws", dev)
-    _check(L.sparge_window_attn(dq, dk, dv, int(window), int(sinks), float(scale), do, ws.data_ptr(), ws.numel() * ws.element_size(),
-                                _raw_stream(dev)))
-    return out
+    return (_binding_module or _load_binding()).window_attn(q, k, v, window, sinks, scale, out, ws)
 
 
 def rope_freqs(rot_dim: int, base: float = 10000.0, device="cuda"):
@@ -515,21 +455,8 @@ def qk_norm_rope(q, k, inv_freq=None, positions=None, start: int = 0, q_weight=N
     entries, or None), then the rotation of the first 2 len(inv_freq) channels by the positions ((B, N) int32,
     or start, start + 1, ...); inv_freq: float64 CUDA tensor (rope_freqs) or None (norm only).  Returns (q_out,
     k_out), which may be given and may be q and k."""
-    dev = _here(q)
-    torch = _torch_module
-    if q_out is None:
-        q_out = torch.empty_like(q)
-    if k_out is None:
-        k_out = torch.empty_like(k)
-    dq, dk, eq, ek = _rows(q, "q", dev), _rows(k, "k", dev), _rows(q_out, "q_out", dev), _rows(k_out, "k_out", dev)
-    B, _, N, d = q.shape
-    f32 = torch.float32
-    _check(lib().sparge_qk_norm_rope(
-        dq, dk, _array(positions, torch.int32, "positions", dev, (B, N)), int(start),
-        _array(inv_freq, torch.float64, "inv_freq", dev), 0 if inv_freq is None else 2 * inv_freq.numel(),
-        bool(interleaved), _array(q_weight, f32, "q_weight", dev, (d,)), _array(k_weight, f32, "k_weight", dev, (d,)),
-        float(eps), eq, ek, _raw_stream(dev)))
-    return q_out, k_out
+    return (_binding_module or _load_binding()).qk_norm_rope(q, k, inv_freq, positions, start, q_weight, k_weight, eps,
+                                                        interleaved, q_out, k_out)
 
 
 def cache_tables(lens, new_lens, free_pages, table, page_size: int, N: int, slots=None, positions=None, kv_lens=None,
@@ -537,83 +464,35 @@ def cache_tables(lens, new_lens, free_pages, table, page_size: int, N: int, slot
     """Block tables and slot maps of a step: extends table (R, width; int32, rows any stride) in place with pages
     from the front of free_pages and returns (slots (R, N) int64, positions (R, N) int32, kv_lens (R) int32,
     used (1) int32); the new tokens stand right-aligned, -1 in front of them (see sparge_cache_tables)."""
-    dev = _here(lens)
-    torch = _torch_module
-    i32, R, N = torch.int32, lens.numel(), int(N)
-    if N < 0:
-        raise ValueError("N must not be negative")
-    if slots is None:
-        slots = torch.empty((R, N), dtype=torch.int64, device=lens.device)
-    if positions is None:
-        positions = torch.empty((R, N), dtype=i32, device=lens.device)
-    if kv_lens is None:
-        kv_lens = torch.empty(R, dtype=i32, device=lens.device)
-    if used is None:
-        used = torch.empty(1, dtype=i32, device=lens.device)
-    at, width, stride = _page_table(table, R, dev)
-    _check(lib().sparge_cache_tables(
-        _array(lens, i32, "lens", dev, (R,)), _array(new_lens, i32, "new_lens", dev, (R,)), R, N, int(page_size),
-        _array(free_pages, i32, "free_pages", dev), free_pages.numel(), at, width, stride,
-        _array(slots, torch.int64, "slots", dev, (R, N)), _array(positions, i32, "positions", dev, (R, N)),
-        _array(kv_lens, i32, "kv_lens", dev, (R,)), _array(used, i32, "used", dev, (1,)), _raw_stream(dev)))
-    return slots, positions, kv_lens, used
+    return (_binding_module or _load_binding()).cache_tables(lens, new_lens, free_pages, table, page_size, N, slots, positions,
+                                                        kv_lens, used)
 
 
 def cache4_pool(n_pages: int, page_size: int, H: int, d: int, device="cuda"):
     """An empty pool of the 4-bit cache: a uint8 tensor (n_pages, H, page_size / 16, 18 d), from whose shape the
     other calls read page size, heads and head dim."""
     torch = _torch()
-    if lib().sparge_cache4_bytes(max(1, n_pages), page_size, H, d) == 0 or n_pages < 0:
+    if n_pages < 0 or lib().sparge_cache4_bytes(max(1, n_pages), page_size, H, d) == 0:
         raise ValueError("unsupported pool: n_pages=%d, page_size=%d, H=%d, d=%d" % (n_pages, page_size, H, d))
     return torch.zeros((n_pages, H, page_size // 16, 18 * d), dtype=torch.uint8, device=device)
 
 
 def cache4_store(k, v, slots, pool):
     """Stores rows (b, h, n) of k and v (B,H,N,d) at slots[b, n] ((B, N) int64; negative: left out) of the pool."""
-    dev = _here(k)
-    dk, dv, dc = _rows(k, "k", dev), _rows(v, "v", dev), _pool(pool, dev)[0]
-    _check(lib().sparge_cache4_store(dk, dv, _array(slots, _torch_module.int64, "slots", dev, (k.shape[0], k.shape[2])), dc,
-                                     _raw_stream(dev)))
+    (_binding_module or _load_binding()).cache4_store(k, v, slots, pool)
 
 
 def cache4_load(pool, slots, k_out=None, v_out=None):
     """The rows at slots ((B, N) int64) as bf16 (B,H,N,d) tensors k and v.  Rows of left-out (negative) slots are zero
     in tensors made here and stay as they were in tensors that are given."""
-    dev = _here(pool)
-    torch = _torch_module
-    dc, H, d = _pool(pool, dev)
-    made = k_out is None or v_out is None
-    if made:
-        if k_out is not None or v_out is not None:
-            raise ValueError("k_out and v_out are given together")
-        B, N = slots.shape
-        k_out = torch.empty((B, H, N, d), dtype=torch.bfloat16, device=pool.device)
-        v_out = torch.empty((B, H, N, d), dtype=torch.bfloat16, device=pool.device)
-    dk, dv = _rows(k_out, "k_out", dev), _rows(v_out, "v_out", dev)
-    _check(lib().sparge_cache4_load(dc, _array(slots, torch.int64, "slots", dev, (k_out.shape[0], k_out.shape[2])), made, dk, dv,
-                                    _raw_stream(dev)))
-    return k_out, v_out
+    return (_binding_module or _load_binding()).cache4_load(pool, slots, k_out, v_out)
 
 
 def cache4_attn(q, pool, table, kv_lens, window: int = 0, sinks: int = 0, scale: float = 0.0, out=None, ws=None):
     """Attention of q (B,Hq,Nq,d) over the 4-bit cache: sequence b has kv_lens[b] tokens on the pages table[b, :]
     ((B, width) int32) and q holds its last Nq; window > 0 keeps each query's last `window` tokens and the first
     `sinks`."""
-    dev = _here(q)
-    torch = _torch_module
-    if out is None:
-        out = torch.empty_like(q)
-    dq, do = _rows(q, "q", dev), _rows(out, "out", dev)
-    dc, H, _ = _pool(pool, dev)
-    B, Hq, Nq, d = q.shape
-    at, width, stride = _page_table(table, B, dev)
-    L = lib()
-    if ws is None:
-        ws = torch.empty(max(1, L.sparge_cache4_attn_workspace_bytes(B, Hq, H, Nq, d)), dtype=torch.uint8, device=q.device)
-    _on(ws, "ws", dev)
-    _check(L.sparge_cache4_attn(dq, dc, at, width, stride, _array(kv_lens, torch.int32, "kv_lens", dev, (B,)), int(window), int(sinks),
-                                float(scale), do, ws.data_ptr(), ws.numel() * ws.element_size(), _raw_stream(dev)))
-    return out
+    return (_binding_module or _load_binding()).cache4_attn(q, pool, table, kv_lens, window, sinks, scale, out, ws)
 
 
 def hilbert_perm_2d(n_prefix: int, H: int, W: int) -> np.ndarray:

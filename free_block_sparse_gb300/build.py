@@ -1,18 +1,22 @@
 """Build libsparge.so in-tree: nvcc for sm_103a, one object per source file, compiled in
-parallel, then one shared-library link.  No CMake; runs the same on x86_64 and aarch64 hosts."""
+parallel, then one shared-library link; and _binding.so, the Python binding of the serving calls,
+against the installed torch's headers and libraries.  No CMake; runs the same on x86_64 and aarch64 hosts."""
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libsparge.so")
+BINDING = os.path.join(PKG, "_binding.so")
 
 CUDA_SOURCES = ["api.cu", "pool_sim.cu", "score_gemm.cu", "score_select.cu", "bsattn.cu", "decode.cu", "permute.cu", "noalloc.cu", "q8prep.cu",
                 "norm_rope.cu", "cache4.cu", "cache4_attn.cu"]
@@ -41,6 +45,35 @@ def _stale(obj, deps):
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _torch_dir() -> str:
+    """Where torch is installed (found without importing it)."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None or not spec.submodule_search_locations:
+        raise RuntimeError("torch not found (its headers are needed for the Python binding)")
+    return list(spec.submodule_search_locations)[0]
+
+
+def _binding_job(obj):
+    """The compile command of the binding; torch's version file is a dependency (another torch, another build)."""
+    t = _torch_dir()
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(_nvcc()))), "include")
+    inc = [os.path.join(t, "include"), os.path.join(t, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], cuda]
+    src = os.path.join(CSRC, "binding.cpp")
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-c", src, "-o", obj]
+    for d in inc:
+        cmd += ["-isystem", d]
+    return cmd, [src, os.path.join(ROOT, "include", "sparge.h"), os.path.join(t, "version.py")]
+
+
+def _link_binding(obj):
+    lib = os.path.join(_torch_dir(), "lib")
+    tmp = BINDING + ".tmp"
+    _run([os.environ.get("CXX", "g++"), "-shared", "-o", tmp, obj, "-L" + lib, "-ltorch_python", "-ltorch_cpu", "-ltorch",
+          "-lc10", "-lc10_cuda", "-L" + PKG, "-l:libsparge.so", "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + lib])
+    os.replace(tmp, BINDING)
+
+
 def build(verbose: bool = False, force: bool = False, ptxas_verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     nvcc = _nvcc()
@@ -63,14 +96,22 @@ def build(verbose: bool = False, force: bool = False, ptxas_verbose: bool = Fals
         objs.append(o)
         if force or _stale(o, [s] + headers):
             jobs.append([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-c", s, "-o", o])
+    binding_obj = os.path.join(BUILD, "binding.cpp.o")
+    binding_cmd, binding_deps = _binding_job(binding_obj)
+    binding_stale = force or _stale(binding_obj, binding_deps)
+    lib_stale = force or bool(jobs) or not os.path.exists(LIB)
+    if binding_stale:
+        jobs.append(binding_cmd)
     with cf.ThreadPoolExecutor(max_workers=max(1, min(len(jobs), os.cpu_count() or 4))) as ex:
         for out in ex.map(_run, jobs):
             if verbose and out.strip():
                 print(out)
-    if force or jobs or not os.path.exists(LIB):
+    if lib_stale:
         tmp = LIB + ".tmp"
         _run([nvcc] + ARCH + ["-shared", "-o", tmp] + objs)
         os.replace(tmp, LIB)
+    if binding_stale or lib_stale or not os.path.exists(BINDING):
+        _link_binding(binding_obj)
     return LIB
 
 

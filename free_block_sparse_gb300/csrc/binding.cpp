@@ -1,0 +1,312 @@
+// Python binding of the serving calls (the ones made once per token and layer): takes the tensors'
+// pointers, sizes and strides, the current stream and device straight from torch, makes the outputs
+// that are not given, and calls the C entries of libsparge.so.  Nothing is computed here.  Through
+// ctypes the same calls spend 17 to 34 us on the host, about twice what their kernels take at
+// decoding sizes; here 6 to 9 us.
+#define PY_SSIZE_T_CLEAN
+#include <Python.h>
+
+#include <ATen/ATen.h>
+#include <c10/cuda/CUDAFunctions.h>
+#include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/autograd/python_variable.h>
+
+#include "../../include/sparge.h"
+
+namespace {
+
+PyObject *g_error = nullptr;  // the package's SpargeError
+
+struct PyFail {};  // a Python exception is set
+
+[[noreturn]] void type_error(const char *fmt, const char *name) {
+  PyErr_Format(PyExc_TypeError, fmt, name);
+  throw PyFail{};
+}
+
+// The call's arguments after `self`, by position.
+struct Args {
+  PyObject *const *v;
+  const char *call;
+  Args(PyObject *const *v_, Py_ssize_t n, Py_ssize_t want, const char *call_) : v(v_), call(call_) {
+    if (n != want) {
+      PyErr_Format(PyExc_TypeError, "%s takes %zd arguments, got %zd", call, want, n);
+      throw PyFail{};
+    }
+  }
+  bool none(int i) const { return v[i] == Py_None; }
+  const at::Tensor &tensor(int i, const char *name) const {
+    if (!THPVariable_Check(v[i])) type_error("%s must be a CUDA tensor", name);
+    return THPVariable_Unpack(v[i]);
+  }
+  int64_t integer(int i) const {
+    PyObject *x = PyNumber_Index(v[i]);
+    if (!x) throw PyFail{};
+    const int64_t r = PyLong_AsLongLong(x);
+    Py_DECREF(x);
+    if (r == -1 && PyErr_Occurred()) throw PyFail{};
+    return r;
+  }
+  int small(int i) const {  // an int argument of the C entry
+    const int64_t r = integer(i);
+    return r > INT32_MAX ? INT32_MAX : r < INT32_MIN ? INT32_MIN : static_cast<int>(r);
+  }
+  float real(int i) const {
+    const double r = PyFloat_AsDouble(v[i]);
+    if (r == -1.0 && PyErr_Occurred()) throw PyFail{};
+    return static_cast<float>(r);
+  }
+  bool truth(int i) const {
+    const int r = PyObject_IsTrue(v[i]);
+    if (r < 0) throw PyFail{};
+    return r != 0;
+  }
+};
+
+// The device of a call's first tensor, which has to be the current one: the kernels run there, on
+// its current stream.
+struct Here {
+  int dev;
+  cudaStream_t stream;
+  explicit Here(const at::Tensor &t, const char *name) {
+    if (!t.is_cuda()) {
+      PyErr_Format(PyExc_ValueError, "%s is not on a CUDA device", name);
+      throw PyFail{};
+    }
+    dev = c10::cuda::current_device();
+    check(t, name);
+    stream = c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(dev)).stream();
+  }
+  void check(const at::Tensor &t, const char *name) const {
+    if (!t.is_cuda() || t.get_device() != dev) {
+      PyErr_Format(PyExc_ValueError, "%s is on %s, the current CUDA device is cuda:%d", name, t.device().str().c_str(), dev);
+      throw PyFail{};
+    }
+  }
+  sparge_stream_t s() const { return reinterpret_cast<sparge_stream_t>(stream); }
+  // a bf16 (B, H, N, d) tensor
+  sparge_tensor rows(const at::Tensor &t, const char *name) const {
+    check(t, name);
+    if (t.scalar_type() != at::kBFloat16 || t.dim() != 4 || t.stride(3) != 1)
+      type_error("%s: expected a bf16 (B, H, N, d) tensor with contiguous last dim", name);
+    return sparge_tensor{t.data_ptr(), SPARGE_BF16, 0, t.size(0), t.size(1), t.size(2), t.size(3),
+                         t.stride(0),  t.stride(1), t.stride(2)};
+  }
+  // a contiguous array of the given type and sizes (none: any)
+  void *array(const at::Tensor &t, at::ScalarType type, const char *name, at::IntArrayRef shape) const {
+    check(t, name);
+    if (t.scalar_type() != type || !t.is_contiguous() || (!shape.empty() && t.sizes() != shape)) {
+      PyErr_Format(PyExc_TypeError, "%s must be a contiguous %s tensor%s", name, at::toString(type),
+                   shape.empty() ? "" : " of the shape that goes with the others");
+      throw PyFail{};
+    }
+    return t.data_ptr();
+  }
+  sparge_cache4 pool(const at::Tensor &t) const {
+    check(t, "pool");
+    if (t.scalar_type() != at::kByte || t.dim() != 4 || !t.is_contiguous() || t.size(3) % 18 || t.size(1) > INT32_MAX ||
+        t.size(2) > INT32_MAX / 16 || t.size(3) > INT32_MAX)
+      type_error("%s must be a contiguous uint8 tensor of shape (n_pages, H, page_size / 16, 18 d)", "pool");
+    return sparge_cache4{t.data_ptr(), t.size(0), static_cast<int32_t>(16 * t.size(2)), static_cast<int32_t>(t.size(1)),
+                         static_cast<int32_t>(t.size(3) / 18), 0};
+  }
+  // an int32 (rows, width) page table: its stride between rows
+  int64_t table(const at::Tensor &t, int64_t rows) const {
+    check(t, "table");
+    if (t.scalar_type() != at::kInt || t.dim() != 2 || t.size(0) != rows || (t.size(1) > 1 && t.stride(1) != 1))
+      type_error("%s must be an int32 tensor of one row per request, with contiguous rows", "table");
+    return rows > 1 ? t.stride(0) : t.size(1);
+  }
+  at::Tensor make(at::IntArrayRef shape, at::ScalarType type) const {
+    return at::empty(shape, at::TensorOptions(at::kCUDA, static_cast<c10::DeviceIndex>(dev)).dtype(type));
+  }
+};
+
+void done(int rc) {
+  if (rc == SPARGE_OK) return;
+  PyObject *e = PyObject_CallFunction(g_error, "is", rc, sparge_last_error());
+  if (e) {
+    PyErr_SetObject(g_error, e);
+    Py_DECREF(e);
+  }
+  throw PyFail{};
+}
+
+PyObject *wrap(const at::Tensor &t) {
+  PyObject *r = THPVariable_Wrap(t);
+  if (!r) throw PyFail{};
+  return r;
+}
+
+// A given tensor as it came (a new reference), else the one that was made.
+PyObject *result(const Args &a, int i, const at::Tensor &t) {
+  if (a.none(i)) return wrap(t);
+  Py_INCREF(a.v[i]);
+  return a.v[i];
+}
+
+template <typename... T>
+PyObject *tuple_of(T... o) {
+  PyObject *r = PyTuple_New(sizeof...(o));
+  if (!r) {
+    (Py_DECREF(o), ...);
+    throw PyFail{};
+  }
+  Py_ssize_t i = 0;
+  (PyTuple_SET_ITEM(r, i++, o), ...);
+  return r;
+}
+
+at::Tensor workspace(const Args &a, int i, const Here &h, size_t bytes) {
+  if (a.none(i)) return h.make({static_cast<int64_t>(bytes ? bytes : 1)}, at::kByte);
+  const at::Tensor &t = a.tensor(i, "ws");
+  h.check(t, "ws");
+  if (!t.is_contiguous()) type_error("%s must be contiguous", "ws");
+  return t;
+}
+
+// (q, k, v, window, sinks, scale, out, ws)
+PyObject *window_attn(const Args &a) {
+  const at::Tensor &q = a.tensor(0, "q"), &k = a.tensor(1, "k"), &v = a.tensor(2, "v");
+  const Here h(q, "q");
+  const sparge_tensor dq = h.rows(q, "q"), dk = h.rows(k, "k"), dv = h.rows(v, "v");
+  const at::Tensor out = a.none(6) ? at::empty_like(q) : a.tensor(6, "out");
+  sparge_tensor dout = h.rows(out, "out");
+  const at::Tensor ws = workspace(a, 7, h, sparge_workspace_bytes(SPARGE_OP_WINDOW_ATTN, dk.B, dq.H, dk.H, dk.N, dk.d));
+  done(sparge_window_attn(&dq, &dk, &dv, a.integer(3), a.integer(4), a.real(5), &dout, ws.data_ptr(), ws.nbytes(), h.s()));
+  return result(a, 6, out);
+}
+
+// (q, k, inv_freq, positions, start, q_weight, k_weight, eps, interleaved, q_out, k_out)
+PyObject *qk_norm_rope(const Args &a) {
+  const at::Tensor &q = a.tensor(0, "q"), &k = a.tensor(1, "k");
+  const Here h(q, "q");
+  const sparge_tensor dq = h.rows(q, "q"), dk = h.rows(k, "k");
+  const at::Tensor qo = a.none(9) ? at::empty_like(q) : a.tensor(9, "q_out");
+  const at::Tensor ko = a.none(10) ? at::empty_like(k) : a.tensor(10, "k_out");
+  sparge_tensor eq = h.rows(qo, "q_out"), ek = h.rows(ko, "k_out");
+  const double *freq = nullptr;
+  int64_t rot = 0;
+  if (!a.none(2)) {
+    const at::Tensor &f = a.tensor(2, "inv_freq");
+    freq = static_cast<const double *>(h.array(f, at::kDouble, "inv_freq", {}));
+    rot = 2 * f.numel();
+  }
+  const void *pos = a.none(3) ? nullptr : h.array(a.tensor(3, "positions"), at::kInt, "positions", {dq.B, dq.N});
+  const void *w[2];
+  for (int i = 0; i < 2; ++i)
+    w[i] = a.none(5 + i) ? nullptr : h.array(a.tensor(5 + i, "weight"), at::kFloat, i ? "k_weight" : "q_weight", {dq.d});
+  done(sparge_qk_norm_rope(&dq, &dk, static_cast<const int32_t *>(pos), a.integer(4), freq,
+                           static_cast<int>(rot > INT32_MAX ? INT32_MAX : rot), a.truth(8), static_cast<const float *>(w[0]),
+                           static_cast<const float *>(w[1]), a.real(7), &eq, &ek, h.s()));
+  PyObject *r = result(a, 9, qo);
+  return tuple_of(r, result(a, 10, ko));
+}
+
+// (lens, new_lens, free_pages, table, page_size, N, slots, positions, kv_lens, used)
+PyObject *cache_tables(const Args &a) {
+  const at::Tensor &lens = a.tensor(0, "lens"), &add = a.tensor(1, "new_lens"), &free = a.tensor(2, "free_pages"),
+                   &table = a.tensor(3, "table");
+  const Here h(lens, "lens");
+  const int64_t R = lens.numel(), N = a.integer(5);
+  if (N < 0) {
+    PyErr_SetString(PyExc_ValueError, "N must not be negative");
+    throw PyFail{};
+  }
+  const at::Tensor slots = a.none(6) ? h.make({R, N}, at::kLong) : a.tensor(6, "slots");
+  const at::Tensor pos = a.none(7) ? h.make({R, N}, at::kInt) : a.tensor(7, "positions");
+  const at::Tensor kv = a.none(8) ? h.make({R}, at::kInt) : a.tensor(8, "kv_lens");
+  const at::Tensor used = a.none(9) ? h.make({1}, at::kInt) : a.tensor(9, "used");
+  const auto i32 = [&](const at::Tensor &t, const char *name, at::IntArrayRef shape) {
+    return static_cast<int32_t *>(h.array(t, at::kInt, name, shape));
+  };
+  const int64_t stride = h.table(table, R);
+  done(sparge_cache_tables(i32(lens, "lens", {R}), i32(add, "new_lens", {R}), R, N, a.small(4), i32(free, "free_pages", {}),
+                           free.numel(), static_cast<int32_t *>(table.data_ptr()), table.size(1), stride,
+                           static_cast<int64_t *>(h.array(slots, at::kLong, "slots", {R, N})), i32(pos, "positions", {R, N}),
+                           i32(kv, "kv_lens", {R}), i32(used, "used", {1}), h.s()));
+  PyObject *r0 = result(a, 6, slots), *r1 = result(a, 7, pos), *r2 = result(a, 8, kv);
+  return tuple_of(r0, r1, r2, result(a, 9, used));
+}
+
+// (k, v, slots, pool)
+PyObject *cache4_store(const Args &a) {
+  const at::Tensor &k = a.tensor(0, "k"), &v = a.tensor(1, "v");
+  const Here h(k, "k");
+  const sparge_tensor dk = h.rows(k, "k"), dv = h.rows(v, "v");
+  const sparge_cache4 c = h.pool(a.tensor(3, "pool"));
+  done(sparge_cache4_store(&dk, &dv, static_cast<int64_t *>(h.array(a.tensor(2, "slots"), at::kLong, "slots", {dk.B, dk.N})),
+                           &c, h.s()));
+  Py_RETURN_NONE;
+}
+
+// (pool, slots, k_out, v_out)
+PyObject *cache4_load(const Args &a) {
+  const at::Tensor &pool = a.tensor(0, "pool"), &slots = a.tensor(1, "slots");
+  const Here h(pool, "pool");
+  const sparge_cache4 c = h.pool(pool);
+  if (a.none(2) != a.none(3)) {
+    PyErr_SetString(PyExc_ValueError, "k_out and v_out are given together");
+    throw PyFail{};
+  }
+  const bool made = a.none(2);
+  if (slots.dim() != 2) type_error("%s must be a contiguous int64 (B, N) tensor", "slots");
+  const at::Tensor k = made ? h.make({slots.size(0), c.H, slots.size(1), c.d}, at::kBFloat16) : a.tensor(2, "k_out");
+  const at::Tensor v = made ? h.make({slots.size(0), c.H, slots.size(1), c.d}, at::kBFloat16) : a.tensor(3, "v_out");
+  sparge_tensor dk = h.rows(k, "k_out"), dv = h.rows(v, "v_out");
+  done(sparge_cache4_load(&c, static_cast<int64_t *>(h.array(slots, at::kLong, "slots", {dk.B, dk.N})), made, &dk, &dv, h.s()));
+  PyObject *r = result(a, 2, k);
+  return tuple_of(r, result(a, 3, v));
+}
+
+// (q, pool, table, kv_lens, window, sinks, scale, out, ws)
+PyObject *cache4_attn(const Args &a) {
+  const at::Tensor &q = a.tensor(0, "q"), &table = a.tensor(2, "table");
+  const Here h(q, "q");
+  const sparge_tensor dq = h.rows(q, "q");
+  const sparge_cache4 c = h.pool(a.tensor(1, "pool"));
+  const at::Tensor out = a.none(7) ? at::empty_like(q) : a.tensor(7, "out");
+  sparge_tensor o = h.rows(out, "out");
+  const int64_t stride = h.table(table, dq.B);
+  const at::Tensor ws = workspace(a, 8, h, sparge_cache4_attn_workspace_bytes(dq.B, dq.H, c.H, dq.N, dq.d));
+  done(sparge_cache4_attn(&dq, &c, static_cast<const int32_t *>(table.data_ptr()), table.size(1), stride,
+                          static_cast<int32_t *>(h.array(a.tensor(3, "kv_lens"), at::kInt, "kv_lens", {dq.B})), a.integer(4),
+                          a.integer(5), a.real(6), &o, ws.data_ptr(), ws.nbytes(), h.s()));
+  return result(a, 7, out);
+}
+
+// No C++ exception leaves through Python.
+template <PyObject *(*F)(const Args &), int N>
+PyObject *entry(PyObject *, PyObject *const *v, Py_ssize_t n) {
+  try {
+    return F(Args(v, n, N, "call"));
+  } catch (const PyFail &) {
+  } catch (const std::exception &e) {
+    if (!PyErr_Occurred()) PyErr_SetString(PyExc_RuntimeError, e.what());
+  } catch (...) {
+    if (!PyErr_Occurred()) PyErr_SetString(PyExc_RuntimeError, "unknown C++ exception");
+  }
+  return nullptr;
+}
+
+PyObject *set_error(PyObject *, PyObject *cls) {
+  Py_INCREF(cls);
+  Py_XDECREF(g_error);
+  g_error = cls;
+  Py_RETURN_NONE;
+}
+
+#define ENTRY(name, n) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(&entry<name, n>)), METH_FASTCALL, nullptr}
+PyMethodDef methods[] = {ENTRY(window_attn, 8),
+                         ENTRY(qk_norm_rope, 11),
+                         ENTRY(cache_tables, 10),
+                         ENTRY(cache4_store, 4),
+                         ENTRY(cache4_load, 4),
+                         ENTRY(cache4_attn, 9),
+                         {"set_error", set_error, METH_O, nullptr},
+                         {nullptr, nullptr, 0, nullptr}};
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods};
+
+}  // namespace
+
+extern "C" PyObject *PyInit__binding() { return PyModule_Create(&module); }
