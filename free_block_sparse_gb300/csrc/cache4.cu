@@ -71,21 +71,27 @@ __device__ __forceinline__ uint32_t quantise8(uint4 v, uint32_t &word) {
   const uint32_t sbits = pack_bf16x2(__fdiv_rn(range, 15.f), 0.f) & 0xFFFFu;
   const float s = __uint_as_float(sbits << 16);
   word = sbits | (lo2 << 16);
-  uint32_t n = 0u;
   const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-  if (s >= 1e-30f) {
-    // k = round((x - lo) * (1/s)) is at most one off; the remainder x - lo - k s is exact, and its
-    // comparison with s / 2 puts k right (to even on a tie) without a division per channel
-    const float r = __frcp_rn(s), half = 0.5f * s;
+  uint32_t n = 0u;
+  if (!(s > 0.f)) return n;
+  // k = round((x - lo) * (1/s)): adding 1.5 * 2^23 leaves it in the sum's low bits.  The quotient is off by
+  // at most 4e-6 here, so k is right unless the quotient lies that near a half; those few take the
+  // division (a scale below 1e-30, whose reciprocal may overflow, too).
+  constexpr float MAGIC = 12582912.f;
+  const float r = __frcp_rn(s);
+  float near = s < 1e-30f ? 1.f : 0.f;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float f = ((j & 1) ? bf16hi(u[j / 2]) : bf16lo(u[j / 2])) - lo;
-      int k = __float2int_rn(f * r);
-      const float rem = fmaf(-static_cast<float>(k), s, f), ar = fabsf(rem);
-      if (ar > half || (ar == half && (k & 1))) k += rem > 0.f ? 1 : -1;
-      n |= static_cast<uint32_t>(min(max(k, 0), 15)) << (4 * j);
-    }
-  } else if (s > 0.f) {  // 1/s would overflow
+  for (int j = 0; j < 4; ++j) {
+    const float2 f = fadd2(make_float2(bf16lo(u[j]), bf16hi(u[j])), make_float2(-lo, -lo));
+    const float2 t = ffma2(f, make_float2(r, r), make_float2(MAGIC, MAGIC));
+    const float2 k = fadd2(t, make_float2(-MAGIC, -MAGIC));
+    const float2 d = ffma2(f, make_float2(r, r), make_float2(-k.x, -k.y));
+    near = fmax3(near, fabsf(d.x), fabsf(d.y));
+    n += (__float_as_uint(fminf(t.x, MAGIC + 15.f)) - __float_as_uint(MAGIC)) << (8 * j);
+    n += (__float_as_uint(fminf(t.y, MAGIC + 15.f)) - __float_as_uint(MAGIC)) << (8 * j + 4);
+  }
+  if (near > 0.49999f) {
+    n = 0u;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const float f = ((j & 1) ? bf16hi(u[j / 2]) : bf16lo(u[j / 2])) - lo;
@@ -101,6 +107,13 @@ __device__ __forceinline__ int v_byte(int t, int i, int g) {
   return (u >> 2) * 512 + (4 * g + ((t & 7) >> 1)) * 16 + (u & 3) * 4 + ((t & 1) << 1) + (t >> 3);
 }
 
+// The low four nibbles of x, one to a byte.
+__device__ __forceinline__ uint32_t spread4(uint32_t x) {
+  x &= 0xFFFFu;
+  x = (x | (x << 8)) & 0x00FF00FFu;
+  return (x | (x << 4)) & 0x0F0F0F0Fu;
+}
+
 // Writes a thread's 8 channels (piece i of token t's row) of K or V into a record, in global or
 // shared memory.  Called by all threads of a row together (V bytes join two threads' nibbles).
 template <int D>
@@ -113,31 +126,46 @@ __device__ __forceinline__ void put8(uint8_t *rec, bool v, int t, int i, uint32_
   } else {
     const uint32_t lo = (i & 1) ? other : n, hi = (i & 1) ? n : other;
     const int g0 = (i & 1) ? 4 : 0;
+    const uint32_t z = spread4(lo >> (4 * g0)) | (spread4(hi >> (4 * g0)) << 4);
+    uint8_t *p = rec + R::V + v_byte(t, i, g0);
 #pragma unroll
-    for (int g = 0; g < 4; ++g)
-      rec[R::V + v_byte(t, i, g0 + g)] =
-          static_cast<uint8_t>(((lo >> (4 * (g0 + g))) & 15u) | (((hi >> (4 * (g0 + g))) & 15u) << 4));
+    for (int g = 0; g < 4; ++g) p[64 * g] = static_cast<uint8_t>(z >> (8 * g));
   }
   if ((i & 7) == 0) *reinterpret_cast<uint32_t *>(rec + (v ? R::VW : R::KW) + (t * R::NG + (i >> 3)) * 4) = word;
 }
 
-// A thread's 8 channels back from a record.
+// A thread's 8 channels back from a record.  A code's byte becomes the low byte of 2^23 (code + 2^23, exactly).
 template <int D>
 __device__ __forceinline__ uint4 get8(const uint8_t *rec, bool v, int t, int i) {
   using R = Rec4<D>;
-  uint32_t n = 0u;
+  uint32_t a, b;      // codes, a byte each: channels 0, 2, 4, 6 and 1, 3, 5, 7 (K), 0 - 3 and 4 - 7 (V)
   if (!v) {
-    n = *reinterpret_cast<const uint32_t *>(rec + R::K + t * (D / 2) + (i & 3) * (D / 8) + (i >> 2) * 4);
+    const uint32_t n = *reinterpret_cast<const uint32_t *>(rec + R::K + t * (D / 2) + (i & 3) * (D / 8) + (i >> 2) * 4);
+    a = n & 0x0F0F0F0Fu;
+    b = (n >> 4) & 0x0F0F0F0Fu;
   } else {
+    const uint8_t *p = rec + R::V + v_byte(t, i, 0);
+    uint32_t w[8];
 #pragma unroll
-    for (int g = 0; g < 8; ++g) n |= ((static_cast<uint32_t>(rec[R::V + v_byte(t, i, g)]) >> ((i & 1) * 4)) & 15u) << (4 * g);
+    for (int g = 0; g < 8; ++g) w[g] = p[64 * g];
+    a = w[0] | (w[1] << 8) | (w[2] << 16) | (w[3] << 24);
+    b = w[4] | (w[5] << 8) | (w[6] << 16) | (w[7] << 24);
+    a = (a >> ((i & 1) * 4)) & 0x0F0F0F0Fu;
+    b = (b >> ((i & 1) * 4)) & 0x0F0F0F0Fu;
   }
   const uint32_t word = *reinterpret_cast<const uint32_t *>(rec + (v ? R::VW : R::KW) + (t * R::NG + (i >> 3)) * 4);
-  const float s = bf16lo(word), m = bf16hi(word);
-  float f[8];
+  const float2 s = make_float2(bf16lo(word), bf16lo(word)), m = make_float2(bf16hi(word), bf16hi(word));
+  uint32_t o[4];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) f[j] = fmaf(static_cast<float>((n >> (4 * j)) & 15u), s, m);
-  return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t x = v ? (j < 2 ? a : b) : a, y = v ? (j < 2 ? a : b) : b;
+    const int bx = v ? 2 * (j & 1) : j, by = v ? 2 * (j & 1) + 1 : j;
+    float2 f = make_float2(__uint_as_float(__byte_perm(x, 0x4B000000u, 0x7650 + bx) ),
+                           __uint_as_float(__byte_perm(y, 0x4B000000u, 0x7650 + by)));
+    f = ffma2(fadd2(f, make_float2(-8388608.f, -8388608.f)), s, m);
+    o[j] = pack_bf16x2(f.x, f.y);
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
 // The slot of token m; negative: padding (the token is left out).  A slot past the pool is never
