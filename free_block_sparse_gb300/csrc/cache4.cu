@@ -28,6 +28,7 @@ struct Rows4 {  // K and V rows and the cache they go to or come from
   int64_t n_slots;
   int page_shift, H, N, B, recs;  // recs: records of a page
   int zero;                       // load: rows of left-out slots become zero
+  int per;                        // heads of a CTA
   int *status;
 };
 
@@ -49,54 +50,62 @@ __device__ __forceinline__ uint32_t max2_nan(uint32_t a, uint32_t b) {
 }
 
 // Codes of a thread's 8 channels (nibble j: channel j) and its group's word; the 8 threads of a
-// group are adjacent lanes.  Minimum and maximum are taken on packed bf16 pairs, NaN winning, so
-// one test of the two at the end finds an infinity or a NaN anywhere in the group.
+// group are adjacent lanes.  Minimum and maximum are taken on packed bf16 pairs, NaN winning, then
+// together as the maximum of (max, -min), so three shuffles serve both and one test of the two
+// finds an infinity or a NaN anywhere in the group.
 __device__ __forceinline__ uint32_t quantise8(uint4 v, uint32_t &word) {
   uint32_t lo2 = min2_nan(min2_nan(v.x, v.y), min2_nan(v.z, v.w));
   uint32_t hi2 = max2_nan(max2_nan(v.x, v.y), max2_nan(v.z, v.w));
-#pragma unroll
-  for (int off = 4; off > 0; off >>= 1) {
-    lo2 = min2_nan(lo2, __shfl_xor_sync(0xffffffffu, lo2, off));
-    hi2 = max2_nan(hi2, __shfl_xor_sync(0xffffffffu, hi2, off));
-  }
   lo2 = min2_nan(lo2, lo2 >> 16);
   hi2 = max2_nan(hi2, hi2 >> 16);
-  const float lo = bf16lo(lo2), hi = bf16lo(hi2);
+  uint32_t m = __byte_perm(hi2, lo2, 0x5410) ^ 0x80000000u;  // max, -min
+#pragma unroll
+  for (int off = 4; off > 0; off >>= 1) m = max2_nan(m, __shfl_xor_sync(0xffffffffu, m, off));
+  m ^= 0x80000000u;
+  const float lo = bf16hi(m), hi = bf16lo(m);
+  const float range = hi - lo;  // an infinity or a NaN if there is one in the group
+  const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+  uint32_t n = 0u;
+  if (range >= 1e-28f && range < 1e38f) {
+    // A quotient from the reciprocal and one correction is the correctly rounded one, or where the quotient
+    // is representable (a tie of codes is) exactly it.  scale = range / 15 to bf16; adding 1.5 * 2^23 to (x - lo) / scale rounds it to even and leaves it in the
+    // sum's low bits (at most 15 (1 + 2^-8): no code passes 15).
+    constexpr float MAGIC = 12582912.f;
+    constexpr uint32_t MAGIC_BITS = 0x4B400000u;
+    constexpr float R15 = 1.f / 15.f;
+    const float sq = range * R15;
+    const uint32_t sbits = pack_bf16x2(fmaf(fmaf(-15.f, sq, range), R15, sq), 0.f) & 0xFFFFu;
+    const float s = __uint_as_float(sbits << 16);
+    float r1;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r1) : "f"(s));  // the correction makes up for its last bit
+    word = sbits | (m & 0xFFFF0000u);
+    const float2 r = make_float2(r1, r1), ns = make_float2(-s, -s), nl = make_float2(-lo, -lo);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 f = fadd2(make_float2(bf16lo(u[j]), bf16hi(u[j])), nl);
+      float2 q = fmul2(f, r);
+      q = ffma2(ffma2(q, ns, f), r, q);
+      const float2 t = fadd2(q, make_float2(MAGIC, MAGIC));
+      n += (__float_as_uint(t.x) << (8 * j)) + (__float_as_uint(t.y) << (8 * j + 4));
+    }
+    uint32_t magic = 0u;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) magic += MAGIC_BITS << (4 * j);
+    return n - magic;
+  }
   if (!(fabsf(lo) <= 3.4028235e38f && fabsf(hi) <= 3.4028235e38f)) {
     word = 0x7FC07FC0u;
     return 0u;
   }
   // a difference beyond fp32 (bf16 values near 3e38 of both signs) is held at the largest fp32
-  const float range = fminf(hi - lo, 3.4028235e38f);
-  const uint32_t sbits = pack_bf16x2(__fdiv_rn(range, 15.f), 0.f) & 0xFFFFu;
+  const uint32_t sbits = pack_bf16x2(__fdiv_rn(fminf(range, 3.4028235e38f), 15.f), 0.f) & 0xFFFFu;
   const float s = __uint_as_float(sbits << 16);
-  word = sbits | (lo2 << 16);
-  const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-  uint32_t n = 0u;
+  word = sbits | (m & 0xFFFF0000u);
   if (!(s > 0.f)) return n;
-  // k = round((x - lo) * (1/s)): adding 1.5 * 2^23 leaves it in the sum's low bits.  The quotient is off by
-  // at most 4e-6 here, so k is right unless the quotient lies that near a half; those few take the
-  // division (a scale below 1e-30, whose reciprocal may overflow, too).
-  constexpr float MAGIC = 12582912.f;
-  const float r = __frcp_rn(s);
-  float near = s < 1e-30f ? 1.f : 0.f;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const float2 f = fadd2(make_float2(bf16lo(u[j]), bf16hi(u[j])), make_float2(-lo, -lo));
-    const float2 t = ffma2(f, make_float2(r, r), make_float2(MAGIC, MAGIC));
-    const float2 k = fadd2(t, make_float2(-MAGIC, -MAGIC));
-    const float2 d = ffma2(f, make_float2(r, r), make_float2(-k.x, -k.y));
-    near = fmax3(near, fabsf(d.x), fabsf(d.y));
-    n += (__float_as_uint(fminf(t.x, MAGIC + 15.f)) - __float_as_uint(MAGIC)) << (8 * j);
-    n += (__float_as_uint(fminf(t.y, MAGIC + 15.f)) - __float_as_uint(MAGIC)) << (8 * j + 4);
-  }
-  if (near > 0.49999f) {
-    n = 0u;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float f = ((j & 1) ? bf16hi(u[j / 2]) : bf16lo(u[j / 2])) - lo;
-      n |= static_cast<uint32_t>(min(max(__float2int_rn(__fdiv_rn(f, s)), 0), 15)) << (4 * j);
-    }
+  for (int j = 0; j < 8; ++j) {
+    const float f = ((j & 1) ? bf16hi(u[j / 2]) : bf16lo(u[j / 2])) - lo;
+    n |= static_cast<uint32_t>(min(max(__float2int_rn(fminf(__fdiv_rn(f, s), 15.f)), 0), 15)) << (4 * j);
   }
   return n;
 }
@@ -105,13 +114,6 @@ __device__ __forceinline__ uint32_t quantise8(uint4 v, uint32_t &word) {
 __device__ __forceinline__ int v_byte(int t, int i, int g) {
   const int u = i >> 1;
   return (u >> 2) * 512 + (4 * g + ((t & 7) >> 1)) * 16 + (u & 3) * 4 + ((t & 1) << 1) + (t >> 3);
-}
-
-// The low four nibbles of x, one to a byte.
-__device__ __forceinline__ uint32_t spread4(uint32_t x) {
-  x &= 0xFFFFu;
-  x = (x | (x << 8)) & 0x00FF00FFu;
-  return (x | (x << 4)) & 0x0F0F0F0Fu;
 }
 
 // Writes a thread's 8 channels (piece i of token t's row) of K or V into a record, in global or
@@ -124,9 +126,12 @@ __device__ __forceinline__ void put8(uint8_t *rec, bool v, int t, int i, uint32_
   if (!v) {
     *reinterpret_cast<uint32_t *>(rec + R::K + t * (D / 2) + (i & 3) * (D / 8) + (i >> 2) * 4) = n;
   } else {
-    const uint32_t lo = (i & 1) ? other : n, hi = (i & 1) ? n : other;
+    // this thread's four bytes, rows g0 .. g0 + 3: the even piece's code below the odd piece's.  The four
+    // codes' bytes side by side, then the middle nibbles of each half exchanged
     const int g0 = (i & 1) ? 4 : 0;
-    const uint32_t z = spread4(lo >> (4 * g0)) | (spread4(hi >> (4 * g0)) << 4);
+    uint32_t z = __byte_perm(n, other, (i & 1) ? 0x3726 : 0x5140);
+    const uint32_t x = (z ^ (z >> 4)) & 0x00F000F0u;
+    z ^= x ^ (x << 4);
     uint8_t *p = rec + R::V + v_byte(t, i, g0);
 #pragma unroll
     for (int g = 0; g < 4; ++g) p[64 * g] = static_cast<uint8_t>(z >> (8 * g));
@@ -207,72 +212,106 @@ __global__ void __launch_bounds__(256) rows4_kernel(const Rows4 a) {
   }
 }
 
-// Longer rows: a CTA takes the tokens of one head that fall on one record, K and V together.  A row's
-// place among the 16 tokens follows the slots (the last one's place in its record lines the chunks up;
-// slots that do not run on are still handled, token by token).  A whole record is put together in
-// shared memory and moved in 16-byte pieces; single tokens go straight to the cache's bytes.
+// Longer rows: a CTA takes the tokens that fall on one record, K and V together, for a few heads one
+// after another (the slots are looked up once, and a head's rows or record come while the one before it
+// is worked on).  A row's place among the 16 tokens follows the slots (the last one's place in its record lines the
+// chunks up; slots that do not run on are still handled, token by token).  A whole record is put
+// together or taken apart in shared memory and moved in 16-byte pieces; single tokens go straight
+// to the cache's bytes.
+// Measured, 4 x 8192 tokens of 8 heads, d = 128, K and V stored and read back: 68 us for 344 MB, 75% of the
+// measured copy rate (store 42 us, load 27): the store is bound by its arithmetic (17 instructions per value),
+// the load by the latency of its two steps.
+constexpr int R4_HEADS = 8;  // most heads of a CTA (8 heads: 68 us, 4: 70, 2: 79)
 template <int D, bool LOAD>
 __global__ void __launch_bounds__(2 * D) records4_kernel(const Rows4 a) {
   using R = Rec4<D>;
-  constexpr int TR = D / 8;
-  __shared__ __align__(16) uint8_t rec[R::BYTES];
-  const int t = threadIdx.x / TR, i = threadIdx.x % TR, h = blockIdx.y, b = blockIdx.z;
+  constexpr int TR = D / 8, PIECES = (R::BYTES / 16 + 2 * D - 1) / (2 * D);
+  __shared__ __align__(16) uint8_t rec[2][R::BYTES];
+  __shared__ int64_t first;
+  const int t = threadIdx.x / TR, i = threadIdx.x % TR, b = blockIdx.z;
+  const int h0 = blockIdx.y * a.per, h1 = min(h0 + a.per, a.H);
   const int64_t *slots = a.slots + static_cast<int64_t>(b) * a.N;
   const int64_t last = __ldg(slots + a.N - 1);
   const int shift = last < 0 ? 0 : static_cast<int>((last - (a.N - 1)) & 15);
   const int n = static_cast<int>(blockIdx.x) * C4_TOKENS - shift + t;
   const bool in = n >= 0 && n < a.N;
-  const int64_t slot = in ? slot_of(a, static_cast<int64_t>(b) * a.N + n, i == 0 && h == 0) : -1;
+  const int64_t slot = in ? slot_of(a, static_cast<int64_t>(b) * a.N + n, i == 0 && h0 == 0) : -1;
   const bool live = slot >= 0;
-  __shared__ int64_t first;
   if (threadIdx.x == 0) first = slot;
   __syncthreads();
   const bool whole = __syncthreads_and(live && (first & 15) == 0 && slot == first + t);
-  uint8_t *mem = record_of(a, live ? slot : 0, h, R::BYTES);
+  uint8_t *mem = record_of(a, live ? slot : 0, h0, R::BYTES);
+  const int64_t hstep = static_cast<int64_t>(a.recs) * R::BYTES;  // the next head's record of the page
+  const int at = static_cast<int>(slot & 15);
+  const int64_t o0 = b * a.sb[0] + h0 * a.sh[0] + n * a.sn[0] + 8 * i, o1 = b * a.sb[1] + h0 * a.sh[1] + n * a.sn[1] + 8 * i;
+  const uint4 none = make_uint4(0u, 0u, 0u, 0u);
   if (LOAD) {
-    if (whole) {
-      for (int e = threadIdx.x; e < R::BYTES / 16; e += 2 * D)
-        reinterpret_cast<uint4 *>(rec)[e] = ld_stream_v4(mem + 16 * e);
-      __syncthreads();
-    }
-    uint4 o[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
-    if (live) {
-      const uint8_t *src = whole ? rec : mem;
-      const int at = static_cast<int>(slot & 15);
-      o[0] = get8<D>(src, false, at, i);
-      o[1] = get8<D>(src, true, at, i);
-    }
-    if (live || (in && a.zero)) {
+    __nv_bfloat16 *y0 = a.y[0] + o0, *y1 = a.y[1] + o1;
+    uint4 piece[PIECES];
+    auto fetch = [&](const uint8_t *from) {
 #pragma unroll
-      for (int s = 0; s < 2; ++s)
-        *reinterpret_cast<uint4 *>(a.y[s] + b * a.sb[s] + h * a.sh[s] + n * a.sn[s] + 8 * i) = o[s];
+      for (int e = 0; e < PIECES; ++e)
+        if (whole && e * 2 * D + threadIdx.x < R::BYTES / 16) piece[e] = ld_stream_v4(from + 16 * (e * 2 * D + threadIdx.x));
+    };
+    fetch(mem);
+    for (int h = h0; h < h1; ++h) {
+      uint8_t *buf = rec[h & 1];
+      if (whole) {
+#pragma unroll
+        for (int e = 0; e < PIECES; ++e)
+          if (e * 2 * D + threadIdx.x < R::BYTES / 16) reinterpret_cast<uint4 *>(buf)[e * 2 * D + threadIdx.x] = piece[e];
+        __syncthreads();
+        if (h + 1 < h1) fetch(mem + hstep);
+      }
+      uint4 k = none, v = none;
+      if (live) {
+        const uint8_t *src = whole ? buf : mem;
+        k = get8<D>(src, false, at, i);
+        v = get8<D>(src, true, at, i);
+      }
+      if (live || (in && a.zero)) {
+        *reinterpret_cast<uint4 *>(y0) = k;
+        *reinterpret_cast<uint4 *>(y1) = v;
+      }
+      mem += hstep;
+      y0 += a.sh[0];
+      y1 += a.sh[1];
     }
   } else {
-    uint4 v[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
-    if (live) {
-#pragma unroll
-      for (int s = 0; s < 2; ++s) v[s] = ld_stream_v4(a.x[s] + b * a.sb[s] + h * a.sh[s] + n * a.sn[s] + 8 * i);
-    }
-    uint8_t *dst = whole ? rec : mem;
-    const int at = static_cast<int>(slot & 15);
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
+    const __nv_bfloat16 *x0 = a.x[0] + o0, *x1 = a.x[1] + o1;
+    uint4 k = live ? ld_stream_v4(x0) : none, v = live ? ld_stream_v4(x1) : none;
+    for (int h = h0; h < h1; ++h) {
+      const uint4 k0 = k, v0 = v;
+      if (live && h + 1 < h1) {
+        x0 += a.sh[0];
+        x1 += a.sh[1];
+        k = ld_stream_v4(x0);
+        v = ld_stream_v4(x1);
+      }
+      uint8_t *dst = whole ? rec[h & 1] : mem;
       uint32_t word;
-      const uint32_t c = quantise8(v[s], word);
-      put8<D>(dst, s != 0, at, i, c, word, live);
-    }
-    if (whole) {
-      __syncthreads();
-      for (int e = threadIdx.x; e < R::BYTES / 16; e += 2 * D)
-        *reinterpret_cast<uint4 *>(mem + 16 * e) = reinterpret_cast<const uint4 *>(rec)[e];
+      uint32_t c = quantise8(k0, word);
+      put8<D>(dst, false, at, i, c, word, live);
+      c = quantise8(v0, word);
+      put8<D>(dst, true, at, i, c, word, live);
+      if (whole) {
+        __syncthreads();
+        for (int e = threadIdx.x; e < R::BYTES / 16; e += 2 * D)
+          *reinterpret_cast<uint4 *>(mem + 16 * e) = reinterpret_cast<const uint4 *>(rec[h & 1])[e];
+      }
+      mem += hstep;
     }
   }
 }
 
 template <int D, bool LOAD>
-cudaError_t launch_rows4(const Rows4 &a, cudaStream_t s) {
+cudaError_t launch_rows4(Rows4 a, cudaStream_t s) {
   if (a.N >= C4_TOKENS) {
-    const dim3 grid(static_cast<unsigned>(a.N / C4_TOKENS + 2), static_cast<unsigned>(a.H), static_cast<unsigned>(a.B));
+    // as many heads per CTA as leave 8 CTAs for each of the 152 SMs
+    const int64_t chunks = a.N / C4_TOKENS + 2, per = chunks * a.B * a.H / (8 * 152);
+    a.per = static_cast<int>(per < 1 ? 1 : (per > R4_HEADS ? R4_HEADS : per));
+    if ((a.H + a.per - 1) / a.per > 65535) a.per = R4_HEADS;
+    const dim3 grid(static_cast<unsigned>(chunks), static_cast<unsigned>((a.H + a.per - 1) / a.per), static_cast<unsigned>(a.B));
     records4_kernel<D, LOAD><<<grid, 2 * D, 0, s>>>(a);
   } else {
     const int64_t rows = static_cast<int64_t>(a.B) * a.N * a.H, per = 256 / (D / 8);
@@ -331,6 +370,7 @@ int rows4(const sparge_tensor *k, const sparge_tensor *v, const int64_t *slots, 
   a.recs = c.page_size / C4_TOKENS;
   a.status = status_ptr();
   a.zero = zero;
+  a.per = 1;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (c.d == 128)
