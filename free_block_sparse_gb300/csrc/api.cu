@@ -454,7 +454,8 @@ int64_t window_chunks(int64_t B, int64_t Hkv, int64_t blocks) {
 size_t window_ws_bytes(int64_t B, int64_t Hkv, int64_t Nk, int64_t d) {
   const size_t rows = static_cast<size_t>(B * Hkv) * window_chunks(B, Hkv, cdiv(Nk, KBLK)) * 128;
   const size_t part = align256(rows * d * 4) + align256(rows * 2 * 4), v16 = v16_bytes(B, Hkv, Nk, d);
-  return part > v16 ? part : v16;
+  const size_t few = window_decode_ws_bytes(B, Hkv, d), most = part > v16 ? part : v16;
+  return few > most ? few : most;
 }
 
 int window_impl(const View &q, const View &k, const View &v, const View &o, int64_t window, int64_t sinks, float scale,
@@ -467,6 +468,22 @@ int window_impl(const View &q, const View &k, const View &v, const View &o, int6
   if (q.B == 0 || q.N == 0) return SPARGE_OK;
   if (window > k.N) window = k.N;  // a longer one hides nothing
   if (sinks > k.N) sinks = k.N;
+  if (q.H / k.H * q.N <= WINDOW_DECODE_ROWS) {
+    WindowDecode w;
+    memset(&w, 0, sizeof(w));
+    if ((rc = make_map(&w.tk, k, 16, "k")) || (rc = make_map(&w.tv, v, 16, "v"))) return rc;
+    w.q = q.data;
+    w.q_sb = q.sb; w.q_sh = q.sh; w.q_sn = q.sn;
+    w.o = const_cast<void *>(o.data);
+    w.o_sb = o.sb; w.o_sh = o.sh; w.o_sn = o.sn;
+    w.B = (int)q.B; w.Hkv = (int)k.H; w.G = (int)(q.H / k.H); w.Nq = (int)q.N; w.Nk = (int)k.N; w.d = (int)q.d;
+    w.window = (int)window; w.sinks = (int)sinks;
+    w.scale = scale;
+    w.status = status_ptr();
+    w.ws = ws;
+    const cudaError_t e = launch_window_decode(w, s);
+    return e == cudaSuccess ? SPARGE_OK : cuda_fail(e, "window attention launch");
+  }
   AttnLaunch l;
   memset(&l, 0, sizeof(l));
   const int64_t blocks = window_blocks(q.N, k.N, window, sinks);

@@ -33,30 +33,25 @@
 #include "cache4.cuh"
 #include "common.cuh"
 #include "kernels.h"
+#include "rowsplit.cuh"
 
 namespace sparge {
 int check_cache4(const ::sparge_cache4 *c, Cache4 *out);
 namespace {
 
-constexpr int CA_WARPS = 4;
-constexpr int CA_SMS = 152;
-constexpr float CA_RESCALE = 8.f;  // the exponent reference moves when a score passes it by more (log2)
 constexpr float CA_SBOUND = 64.f;  // scaled V scales stay below this: P s < 2^8 2^6 < 65504
 
-struct CacheAttnArgs {
+struct CacheAttnArgs : SplitArgs {
   const __nv_bfloat16 *q;
-  __nv_bfloat16 *o;
-  int64_t q_sb, q_sh, q_sn, o_sb, o_sh, o_sn;
+  int64_t q_sb, q_sh, q_sn;
   const uint8_t *pool;
   const int32_t *table, *lens;
   int64_t table_stride, n_pages;
   int width, rec_shift;  // records of a page: 1 << rec_shift
-  int B, Hq, Hkv, G, Nq, rows, ntile;
   int window, sinks;     // window 0: none
   float scale_log2;
-  float *part_o, *part_ml;
-  int2 *ends;            // per item: first and last CTA
   int *status;
+  __device__ __forceinline__ bool empty(int b) const { return width == 0 || __ldg(lens + b) <= 0; }
 };
 
 // The records a sequence's queries see: the first `ns` (tokens that stay visible), then lo..hi-1.
@@ -132,7 +127,6 @@ __device__ __forceinline__ void mma_f16_zero(float (&c)[4], uint32_t a0, uint32_
       : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
-__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 // scale words of tokens g (u) and g + 8 (v) of this lane, g = lane / 4
 template <int NG>
 __device__ __forceinline__ void words(const uint8_t *p, uint32_t (&u)[NG], uint32_t (&v)[NG]) {
@@ -145,11 +139,6 @@ __device__ __forceinline__ void words(const uint8_t *p, uint32_t (&u)[NG], uint3
     u[0] = *reinterpret_cast<const uint32_t *>(p + g * 4);
     v[0] = *reinterpret_cast<const uint32_t *>(p + 32 + g * 4);
   }
-}
-__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
-  uint32_t y;
-  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
-  return y;
 }
 // two floats to f16x2 without saturation: an infinity or a NaN stays one
 __device__ __forceinline__ uint32_t half2_of(float lo, float hi) {
@@ -470,15 +459,6 @@ __global__ void __launch_bounds__(CA_WARPS * 32, RT == 1 ? 4 : 3) cache4_attn_ke
           vf = nf;
           sbound = CA_SBOUND * pow2i(e);
         }
-        auto follow = [&](float &t, float &m, float x) {  // the factor on what has been summed
-#pragma unroll
-          for (int o = 4; o <= 16; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-          if (!(x > t)) return 1.f;
-          const float f = t == -INFINITY ? 0.f : exp2f(-m - x);
-          m = -x;
-          t = x + CA_RESCALE;
-          return f;
-        };
 #pragma unroll
         for (int j = 0; j < RT; ++j) {
           float2 al;
@@ -588,52 +568,7 @@ __global__ void __launch_bounds__(CA_WARPS * 32, RT == 1 ? 4 : 3) cache4_attn_ke
           mo[row * S::OROW + 16 * u + 8 + g] = fmaf(acc[u][j][2 + k], back * 0.0625f, z[u / 4]);
         }
       }
-    __syncthreads();
-    const bool whole = nt == tiles;  // the item lies in this CTA alone
-    const int nrow = min(8 * RT, a.rows - row0);
-    if (threadIdx.x == 0) {
-      if (tile0 == 0) a.ends[item].x = blockIdx.x;
-      if (tile0 + nt == tiles) a.ends[item].y = blockIdx.x;
-    }
-    const int64_t slot = static_cast<int64_t>(blockIdx.x) + item;
-    for (int e = threadIdx.x; e < nrow * (D / 4); e += CA_WARPS * 32) {
-      const int row = e / (D / 4), d4 = e % (D / 4);
-      float2 w[CA_WARPS];
-      float M = -INFINITY;
-#pragma unroll
-      for (int u = 0; u < CA_WARPS; ++u) {
-        w[u] = ml[u * 8 * RT + row];
-        M = fmaxf(M, w[u].x);
-      }
-      float L = 0.f;
-      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int u = 0; u < CA_WARPS; ++u) {
-        // a warp without a visible token has the reference -inf; its sums are 0 (NaN inputs: NaN)
-        const float f = w[u].x == -INFINITY ? (w[u].y == 0.f ? 0.f : 1.f) : exp2f(w[u].x - M);
-        const float4 v = *reinterpret_cast<const float4 *>(smem + u * S::WRING + (row * S::OROW + 4 * d4) * 4);
-        if (f != 0.f) {
-          L = fmaf(f, w[u].y, L);
-          o.x = fmaf(f, v.x, o.x);
-          o.y = fmaf(f, v.y, o.y);
-          o.z = fmaf(f, v.z, o.z);
-          o.w = fmaf(f, v.w, o.w);
-        }
-      }
-      if (whole) {
-        const float inv = L == 0.f ? 0.f : 1.f / L;
-        const int r = row0 + row, h = kvh * a.G + r / a.Nq, qi = r % a.Nq;
-        uint2 w2;
-        w2.x = pack_bf16x2(o.x * inv, o.y * inv);
-        w2.y = pack_bf16x2(o.z * inv, o.w * inv);
-        *reinterpret_cast<uint2 *>(a.o + b * a.o_sb + h * a.o_sh + static_cast<int64_t>(qi) * a.o_sn + 4 * d4) = w2;
-      } else {
-        *reinterpret_cast<float4 *>(a.part_o + (slot * 8 * RT + row) * D + 4 * d4) = o;
-        if (d4 == 0) *reinterpret_cast<float2 *>(a.part_ml + (slot * 8 * RT + row) * 2) = make_float2(M, L);
-      }
-    }
-    fence_proxy_async_smem();  // the sums' reads and writes before the next item's copies into the same places
-    __syncthreads();
+    end_item<D, RT>(a, smem, S::WRING, S::OROW, ml, item, b, kvh, row0, tile0 == 0, tile0 + nt == tiles);
     if (*reinterpret_cast<volatile int *>(&cs.abort)) break;
     off += nt;
     left -= nt;
@@ -645,139 +580,12 @@ __global__ void __launch_bounds__(CA_WARPS * 32, RT == 1 ? 4 : 3) cache4_attn_ke
   }
 }
 
-// Items cut between CTAs: the CTAs' partial rows (at CTA + item, a place of its own for every pair
-// that meets) weighted by 2^(m - M) and divided by the weighted sum, in an order that the lengths alone
-// set.  Items without a token get zero rows.  A CTA takes `nrow` rows of an item: one row per warp
-// where the item has few shares (many items, each cut once or twice), the whole CTA on one row after
-// another where it has many (one long sequence: 76 shares), so either way a few memory latencies.
-// Launched so that it may start while the attention ends (programmatic dependent launch); nothing is
-// read before the wait.
-constexpr int CC_THREADS = 128, CC_FEW = 8;
-template <int D, int RT>
-__global__ void __launch_bounds__(CC_THREADS) cache4_combine_kernel(const CacheAttnArgs a, int nrow) {
-  constexpr int NL = D / 4, NGRP = CC_THREADS / NL, U = CaSmem<D, RT>::U;
-  __shared__ float wgt[CA_SMS * 4];
-  __shared__ float red[2][CC_THREADS / 32];
-  __shared__ float4 sums[NGRP][NL];
-  const int item = blockIdx.x, per = a.Hkv * a.ntile;
-  const int b = item / per, kvh = item % per / a.ntile, row0 = (item % a.ntile) * 8 * RT;
-  const int t = threadIdx.x, lane = t & 31, warp = t >> 5, d4 = t % NL, grp = t / NL;
-  const int last = min(8 * RT, a.rows - row0), first = blockIdx.y * nrow;
-  auto out = [&](int row) {
-    const int r = row0 + row, h = kvh * a.G + r / a.Nq, qi = r % a.Nq;
-    return a.o + b * a.o_sb + h * a.o_sh + static_cast<int64_t>(qi) * a.o_sn;
-  };
-  auto put = [&](__nv_bfloat16 *to, float4 o, float inv) {
-    uint2 w;
-    w.x = pack_bf16x2(o.x * inv, o.y * inv);
-    w.y = pack_bf16x2(o.z * inv, o.w * inv);
-    *reinterpret_cast<uint2 *>(to) = w;
-  };
-  auto add = [](float4 &o, float f, float4 v) {
-    if (f != 0.f) {
-      o.x = fmaf(f, v.x, o.x);
-      o.y = fmaf(f, v.y, o.y);
-      o.z = fmaf(f, v.z, o.z);
-      o.w = fmaf(f, v.w, o.w);
-    }
-  };
-  // the weight of a share of reference m and sum l (without a visible token: -inf and 0; NaN inputs: NaN)
-  auto weight = [](float m, float l, float M) { return m == -INFINITY ? (l == 0.f ? 0.f : 1.f) : exp2f(m - M); };
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (units_of<U>(a, b) == 0) {
-    for (int row = first + warp; row < min(last, first + nrow); row += CC_THREADS / 32)
-      if (lane < NL) put(out(row) + 4 * lane, make_float4(0.f, 0.f, 0.f, 0.f), 0.f);
-    return;
-  }
-  const int2 ends = a.ends[item];
-  const int n = ends.y - ends.x + 1;
-  if (n <= 1) return;  // written by its only CTA
-  const int64_t at0 = (static_cast<int64_t>(ends.x) + item) * 8 * RT;
-  if (n <= CC_FEW) {
-    for (int row = first + warp; row < min(last, first + nrow); row += CC_THREADS / 32) {
-      float2 ml = make_float2(-INFINITY, 0.f);
-      if (lane < n) ml = *reinterpret_cast<const float2 *>(a.part_ml + (at0 + static_cast<int64_t>(lane) * 8 * RT + row) * 2);
-      float4 v[CC_FEW];
-      if (lane < NL) {
-#pragma unroll
-        for (int w = 0; w < CC_FEW; ++w)
-          if (w < n) v[w] = *reinterpret_cast<const float4 *>(a.part_o + (at0 + static_cast<int64_t>(w) * 8 * RT + row) * D + 4 * lane);
-      }
-      float M = ml.x;
-#pragma unroll
-      for (int o = 4; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-      M = __shfl_sync(0xffffffffu, M, 0);
-      const float f = weight(ml.x, ml.y, M);
-      float L = f != 0.f ? f * ml.y : 0.f;
-#pragma unroll
-      for (int o = 4; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-      L = __shfl_sync(0xffffffffu, L, 0);
-      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int w = 0; w < CC_FEW; ++w) {
-        const float fw = __shfl_sync(0xffffffffu, f, w);
-        if (w < n && lane < NL) add(o, fw, v[w]);
-      }
-      if (lane < NL) put(out(row) + 4 * lane, o, L == 0.f ? 0.f : 1.f / L);
-    }
-    return;
-  }
-  for (int row = first; row < min(last, first + nrow); ++row) {
-    float M = -INFINITY;
-    for (int w = t; w < n; w += CC_THREADS) M = fmaxf(M, a.part_ml[(at0 + static_cast<int64_t>(w) * 8 * RT + row) * 2]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    if (lane == 0) red[0][warp] = M;
-    __syncthreads();
-#pragma unroll
-    for (int u = 0; u < CC_THREADS / 32; ++u) M = fmaxf(M, red[0][u]);
-    float L = 0.f;
-    for (int w = t; w < n; w += CC_THREADS) {
-      const float2 ml = *reinterpret_cast<const float2 *>(a.part_ml + (at0 + static_cast<int64_t>(w) * 8 * RT + row) * 2);
-      const float f = weight(ml.x, ml.y, M);
-      wgt[w] = f;
-      if (f != 0.f) L = fmaf(f, ml.y, L);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-    if (lane == 0) red[1][warp] = L;
-    __syncthreads();
-    L = 0.f;
-#pragma unroll
-    for (int u = 0; u < CC_THREADS / 32; ++u) L += red[1][u];
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int w = grp; w < n; w += NGRP)
-      add(o, wgt[w], *reinterpret_cast<const float4 *>(a.part_o + (at0 + static_cast<int64_t>(w) * 8 * RT + row) * D + 4 * d4));
-    sums[grp][d4] = o;
-    __syncthreads();
-    if (grp == 0) {
-#pragma unroll
-      for (int u = 1; u < NGRP; ++u) add(o, 1.f, sums[u][d4]);
-      put(out(row) + 4 * d4, o, L == 0.f ? 0.f : 1.f / L);
-    }
-    __syncthreads();
-  }
-}
-
-// Row tiles of 8 rows for up to 8 query rows per KV head, else of 16: a CTA of 16-row tiles holds
-// twice the sums in registers (3 CTAs per SM instead of 4) and reads the cache half as often.
-int row_tile(int64_t rows) { return rows <= 8 ? 1 : 2; }
+// A CTA of 16-row tiles holds twice the sums in registers (3 CTAs per SM instead of 4) and reads the
+// cache half as often.
 int max_ctas(int rt) { return CA_SMS * (rt == 1 ? 4 : 3); }
-size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
-
-struct AttnWs {
-  size_t o, ml, ends, total;  // offsets
-};
-AttnWs ws_layout(int64_t B, int64_t Hkv, int64_t rows, int64_t d) {
+SplitWs ws_layout(int64_t B, int64_t Hkv, int64_t rows, int64_t d) {
   const int rt = row_tile(rows);
-  const int64_t items = B * Hkv * ((rows + 8 * rt - 1) / (8 * rt)), slots = items + max_ctas(rt);
-  AttnWs w;
-  w.o = 0;
-  w.ml = up256(static_cast<size_t>(slots) * 8 * rt * d * 4);
-  w.ends = w.ml + up256(static_cast<size_t>(slots) * 8 * rt * 2 * 4);
-  w.total = w.ends + up256(static_cast<size_t>(items) * 8);
-  return w;
+  return split_ws(B * Hkv * ((rows + 8 * rt - 1) / (8 * rt)), max_ctas(rt), rt, d);
 }
 
 template <int D, int RT>
@@ -788,20 +596,7 @@ cudaError_t launch_cache_attn(const CacheAttnArgs &a, int64_t tiles, cudaStream_
   const int64_t most = max_ctas(RT), ctas = tiles < most ? tiles : most;
   cache4_attn_kernel<D, RT><<<static_cast<unsigned>(ctas), CA_WARPS * 32, S::TOTAL, st>>>(a);
   if (cudaError_t e = cudaGetLastError(); e != cudaSuccess) return e;
-  // rows of a combining CTA: one per warp where items outnumber half the CTAs (an item then has few
-  // shares), else one
-  const int64_t items = static_cast<int64_t>(a.B) * a.Hkv * a.ntile;
-  const int nrow = 2 * items > ctas ? CC_THREADS / 32 : 1, rows = a.rows < 8 * RT ? a.rows : 8 * RT;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(items), static_cast<unsigned>((rows + nrow - 1) / nrow));
-  cfg.blockDim = dim3(CC_THREADS);
-  cfg.stream = st;
-  cudaLaunchAttribute at;
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, cache4_combine_kernel<D, RT>, a, nrow);
+  return launch_split_combine<D, RT>(a, ctas, st);
 }
 
 }  // namespace
@@ -838,7 +633,7 @@ int sparge_cache4_attn(const sparge_tensor *q, const sparge_cache4 *cache, const
                 (long long)width, (long long)table_stride);
   const int64_t rows = qv.H / c.H * qv.N, rt = row_tile(rows), ntile = (rows + 8 * rt - 1) / (8 * rt);
   if (rows > INT_MAX || qv.B * c.H * ntile > INT_MAX / 2) return fail(SPARGE_ERR_UNSUPPORTED, "too many query rows");
-  const AttnWs w = ws_layout(qv.B, c.H, rows, qv.d);
+  const SplitWs w = ws_layout(qv.B, c.H, rows, qv.d);
   if (!ws || ws_bytes < w.total) return fail(SPARGE_ERR_WORKSPACE_TOO_SMALL, "workspace %zu bytes, need %zu", ws_bytes, w.total);
   if (reinterpret_cast<uintptr_t>(ws) & 255u) return fail(SPARGE_ERR_INVALID_ARG, "workspace not 256-byte aligned");
   if (qv.B == 0 || qv.N == 0) return SPARGE_OK;
@@ -855,7 +650,7 @@ int sparge_cache4_attn(const sparge_tensor *q, const sparge_cache4 *cache, const
   a.n_pages = c.n_pages;
   a.width = static_cast<int>(width);
   a.rec_shift = c.page_shift - 4;
-  a.B = static_cast<int>(qv.B); a.Hq = static_cast<int>(qv.H); a.Hkv = c.H; a.G = static_cast<int>(qv.H / c.H);
+  a.B = static_cast<int>(qv.B); a.Hkv = c.H; a.G = static_cast<int>(qv.H / c.H);
   a.Nq = static_cast<int>(qv.N); a.rows = static_cast<int>(rows); a.ntile = static_cast<int>(ntile);
   a.window = static_cast<int>(window);
   a.sinks = static_cast<int>(sinks);

@@ -184,6 +184,23 @@ inline size_t decode_part_bytes(int64_t B, int64_t Hkv, int64_t Nk, int64_t d) {
 
 cudaError_t launch_bsattn(const AttnLaunch &a, cudaStream_t st);
 
+// Decoding under a sliding window, up to WINDOW_DECODE_ROWS query rows per KV head (window_decode.cu).  tk and
+// tv: 4-D maps over K and V (bf16, 128-byte swizzle, boxes 64 x 16).
+constexpr int WINDOW_DECODE_ROWS = 16;
+struct WindowDecode {
+  CUtensorMap tk, tv;
+  const void *q;
+  int64_t q_sb, q_sh, q_sn;
+  void *o;
+  int64_t o_sb, o_sh, o_sn;
+  int B, Hkv, G, Nq, Nk, d, window, sinks;  // window and sinks at most Nk
+  float scale;
+  int *status;
+  void *ws;
+};
+size_t window_decode_ws_bytes(int64_t B, int64_t Hkv, int64_t d);
+cudaError_t launch_window_decode(const WindowDecode &l, cudaStream_t st);
+
 // Decoding tiles (decode.cu): before the attention, the ascending list of key blocks that any of
 // the G heads of each (batch, KV head) keeps in query block 0 (list [B Hkv][nkb], count [B Hkv]);
 // after it, the shares' partial rows combined into o (bf16, strides in elements).
