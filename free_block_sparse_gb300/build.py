@@ -69,7 +69,7 @@ def _binding_job(obj):
 def _link_binding(obj):
     lib = os.path.join(_torch_dir(), "lib")
     tmp = BINDING + ".tmp"
-    _run([os.environ.get("CXX", "g++"), "-shared", "-o", tmp, obj, "-L" + lib, "-ltorch_python", "-ltorch_cpu", "-ltorch",
+    _run([os.environ.get("CXX", "g++"), "-shared", "-o", tmp, obj, "-L" + lib, "-ltorch_python", "-ltorch_cpu", "-ltorch_cuda", "-ltorch",
           "-lc10", "-lc10_cuda", "-L" + PKG, "-l:libsparge.so", "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + lib])
     os.replace(tmp, BINDING)
 

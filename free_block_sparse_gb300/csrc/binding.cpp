@@ -7,6 +7,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -117,8 +118,15 @@ struct Here {
       type_error("%s must be an int32 tensor of one row per request, with contiguous rows", "table");
     return rows > 1 ? t.stride(0) : t.size(1);
   }
+  // new tensors from torch's caching allocator, past the dispatcher (half of an empty()'s host time)
   at::Tensor make(at::IntArrayRef shape, at::ScalarType type) const {
-    return at::empty(shape, at::TensorOptions(at::kCUDA, static_cast<c10::DeviceIndex>(dev)).dtype(type));
+    return at::Tensor(at::detail::empty_cuda(shape, type, at::Device(at::kCUDA, static_cast<c10::DeviceIndex>(dev)), std::nullopt));
+  }
+  // like t: its strides where they leave no gaps, else contiguous
+  at::Tensor make_like(const at::Tensor &t) const {
+    if (t.is_contiguous() || !t.is_non_overlapping_and_dense()) return make(t.sizes(), t.scalar_type());
+    return at::Tensor(at::detail::empty_strided_cuda(t.sizes(), t.strides(), t.scalar_type(),
+                                                     at::Device(at::kCUDA, static_cast<c10::DeviceIndex>(dev))));
   }
 };
 
@@ -170,7 +178,7 @@ PyObject *window_attn(const Args &a) {
   const at::Tensor &q = a.tensor(0, "q"), &k = a.tensor(1, "k"), &v = a.tensor(2, "v");
   const Here h(q, "q");
   const sparge_tensor dq = h.rows(q, "q"), dk = h.rows(k, "k"), dv = h.rows(v, "v");
-  const at::Tensor out = a.none(6) ? at::empty_like(q) : a.tensor(6, "out");
+  const at::Tensor out = a.none(6) ? h.make_like(q) : a.tensor(6, "out");
   sparge_tensor dout = h.rows(out, "out");
   const at::Tensor ws = workspace(a, 7, h, sparge_workspace_bytes(SPARGE_OP_WINDOW_ATTN, dk.B, dq.H, dk.H, dk.N, dk.d));
   done(sparge_window_attn(&dq, &dk, &dv, a.integer(3), a.integer(4), a.real(5), &dout, ws.data_ptr(), ws.nbytes(), h.s()));
@@ -182,8 +190,8 @@ PyObject *qk_norm_rope(const Args &a) {
   const at::Tensor &q = a.tensor(0, "q"), &k = a.tensor(1, "k");
   const Here h(q, "q");
   const sparge_tensor dq = h.rows(q, "q"), dk = h.rows(k, "k");
-  const at::Tensor qo = a.none(9) ? at::empty_like(q) : a.tensor(9, "q_out");
-  const at::Tensor ko = a.none(10) ? at::empty_like(k) : a.tensor(10, "k_out");
+  const at::Tensor qo = a.none(9) ? h.make_like(q) : a.tensor(9, "q_out");
+  const at::Tensor ko = a.none(10) ? h.make_like(k) : a.tensor(10, "k_out");
   sparge_tensor eq = h.rows(qo, "q_out"), ek = h.rows(ko, "k_out");
   const double *freq = nullptr;
   int64_t rot = 0;
@@ -265,7 +273,7 @@ PyObject *cache4_attn(const Args &a) {
   const Here h(q, "q");
   const sparge_tensor dq = h.rows(q, "q");
   const sparge_cache4 c = h.pool(a.tensor(1, "pool"));
-  const at::Tensor out = a.none(7) ? at::empty_like(q) : a.tensor(7, "out");
+  const at::Tensor out = a.none(7) ? h.make_like(q) : a.tensor(7, "out");
   sparge_tensor o = h.rows(out, "out");
   const int64_t stride = h.table(table, dq.B);
   const at::Tensor ws = workspace(a, 8, h, sparge_cache4_attn_workspace_bytes(dq.B, dq.H, c.H, dq.N, dq.d));
