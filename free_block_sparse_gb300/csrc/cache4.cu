@@ -14,6 +14,7 @@
 #include "../../include/sparge.h"
 #include "cache4.cuh"
 #include "common.cuh"
+#include "dependent.cuh"
 #include "kernels.h"
 
 namespace sparge {
@@ -189,6 +190,8 @@ __device__ __forceinline__ int64_t slot_of(const Rows4 &a, int64_t m, bool repor
 template <int D, bool LOAD>
 __global__ void __launch_bounds__(256) rows4_kernel(const Rows4 a) {
   constexpr int TR = D / 8;
+  let_dependents_start();
+  wait_for_earlier();
   const int side = blockIdx.y, i = threadIdx.x % TR;
   const int64_t row = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) / TR;
   const int64_t m = row / a.H;
@@ -228,6 +231,8 @@ __global__ void __launch_bounds__(2 * D) records4_kernel(const Rows4 a) {
   constexpr int TR = D / 8, PIECES = (R::BYTES / 16 + 2 * D - 1) / (2 * D);
   __shared__ __align__(16) uint8_t rec[2][R::BYTES];
   __shared__ int64_t first;
+  let_dependents_start();
+  wait_for_earlier();
   const int t = threadIdx.x / TR, i = threadIdx.x % TR, b = blockIdx.z;
   const int h0 = blockIdx.y * a.per, h1 = min(h0 + a.per, a.H);
   const int64_t *slots = a.slots + static_cast<int64_t>(b) * a.N;
@@ -312,12 +317,11 @@ cudaError_t launch_rows4(Rows4 a, cudaStream_t s) {
     a.per = static_cast<int>(per < 1 ? 1 : (per > R4_HEADS ? R4_HEADS : per));
     if ((a.H + a.per - 1) / a.per > 65535) a.per = R4_HEADS;
     const dim3 grid(static_cast<unsigned>(chunks), static_cast<unsigned>((a.H + a.per - 1) / a.per), static_cast<unsigned>(a.B));
-    records4_kernel<D, LOAD><<<grid, 2 * D, 0, s>>>(a);
+    return launch_dependent(records4_kernel<D, LOAD>, grid, 2 * D, 0, s, a);
   } else {
     const int64_t rows = static_cast<int64_t>(a.B) * a.N * a.H, per = 256 / (D / 8);
-    rows4_kernel<D, LOAD><<<dim3(static_cast<unsigned>((rows + per - 1) / per), 2), 256, 0, s>>>(a);
+    return launch_dependent(rows4_kernel<D, LOAD>, dim3(static_cast<unsigned>((rows + per - 1) / per), 2), 256, 0, s, a);
   }
-  return cudaGetLastError();
 }
 
 }  // namespace
@@ -421,6 +425,8 @@ __global__ void __launch_bounds__(TB_THREADS) cache_tables_kernel(const TablesAr
   __shared__ int64_t first[TB_CHUNK + 1];
   const int r0 = blockIdx.x * a.chunk, r1 = min(a.R, r0 + a.chunk);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  let_dependents_start();
+  wait_for_earlier();
   int64_t sum = 0;
   for (int r = threadIdx.x; r < r0; r += TB_THREADS) sum += request_of(a, r).need;
 #pragma unroll
@@ -540,8 +546,8 @@ int sparge_cache_tables(const int32_t *lens, const int32_t *new_lens, int64_t R,
   const int64_t most = 4 * 152 / gx;
   gy = gy > most ? most : gy;
   gy = gy < 1 ? 1 : gy;
-  cache_tables_kernel<<<dim3(static_cast<unsigned>(gx), static_cast<unsigned>(gy)), TB_THREADS, 0, s>>>(a);
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_dependent(cache_tables_kernel, dim3(static_cast<unsigned>(gx), static_cast<unsigned>(gy)),
+                                         TB_THREADS, 0, s, a);
   return e == cudaSuccess ? SPARGE_OK : cuda_fail(e, "cache tables launch");
 }
 

@@ -161,6 +161,9 @@ __global__ void __launch_bounds__(CA_WARPS * 32, RT == 1 ? 4 : 3) cache4_attn_ke
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
   uint8_t *ring = smem + warp * S::WRING;
 
+  let_dependents_start();
+  wait_for_earlier();
+
   // ---- this CTA's share [start, end) of the line of tiles, and the sequence it starts in ----
   const int per = (a.B + CA_WARPS * 32 - 1) / (CA_WARPS * 32);
   const int bt = min(a.B, static_cast<int>(threadIdx.x) * per), bu = min(a.B, bt + per);
@@ -189,7 +192,6 @@ __global__ void __launch_bounds__(CA_WARPS * 32, RT == 1 ? 4 : 3) cache4_attn_ke
   // shares only for as many CTAs as there are tiles: between an item's first and last CTA each holds some of it
   const int64_t shares = total < gridDim.x ? total : gridDim.x;
   if (blockIdx.x >= shares) return;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the combining kernel may be set up from here on
   const int64_t start = total * blockIdx.x / shares, end = total * (blockIdx.x + 1) / shares;
   if (before <= start && start < before + own) {
     int b = bt;
@@ -594,8 +596,9 @@ cudaError_t launch_cache_attn(const CacheAttnArgs &a, int64_t tiles, cudaStream_
   static std::atomic<unsigned long long> smem_set{0};
   if (cudaError_t e = set_smem_limit_once(cache4_attn_kernel<D, RT>, S::TOTAL, smem_set); e != cudaSuccess) return e;
   const int64_t most = max_ctas(RT), ctas = tiles < most ? tiles : most;
-  cache4_attn_kernel<D, RT><<<static_cast<unsigned>(ctas), CA_WARPS * 32, S::TOTAL, st>>>(a);
-  if (cudaError_t e = cudaGetLastError(); e != cudaSuccess) return e;
+  if (cudaError_t e = launch_dependent(cache4_attn_kernel<D, RT>, dim3(static_cast<unsigned>(ctas)), CA_WARPS * 32, S::TOTAL, st, a);
+      e != cudaSuccess)
+    return e;
   return launch_split_combine<D, RT>(a, ctas, st);
 }
 

@@ -19,6 +19,7 @@
 
 #include "../../include/sparge.h"
 #include "common.cuh"
+#include "dependent.cuh"
 #include "kernels.h"
 
 namespace sparge {
@@ -62,6 +63,7 @@ template <int D, bool INTER>
 __global__ void __launch_bounds__(NR_THREADS) norm_rope_kernel(const NormRopeArgs a) {
   constexpr int TR = D / 16;                 // threads of a row
   constexpr int TOK = NR_THREADS / TR;       // tokens of a CTA
+  let_dependents_start();
   const int t = threadIdx.x % TR;
   const int64_t m = static_cast<int64_t>(blockIdx.x) * TOK + threadIdx.x / TR;
   const bool live = m < a.tokens;
@@ -97,6 +99,7 @@ __global__ void __launch_bounds__(NR_THREADS) norm_rope_kernel(const NormRopeArg
       }
     return cnt;
   };
+  wait_for_earlier();
   int cnt = load(h);
   __shared__ uint64_t turns[D / 2];
   for (int j = threadIdx.x; j < a.rot / 2; j += NR_THREADS) turns[j] = turns64(__ldg(a.inv_freq + j));
@@ -249,13 +252,9 @@ extern "C" int sparge_qk_norm_rope(const sparge_tensor *q, const sparge_tensor *
   a.per = static_cast<int>(per);
   const dim3 grid(static_cast<unsigned>(tiles), static_cast<unsigned>((heads + per - 1) / per));
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (d == 128) {
-    if (interleaved) norm_rope_kernel<128, true><<<grid, NR_THREADS, 0, s>>>(a);
-    else norm_rope_kernel<128, false><<<grid, NR_THREADS, 0, s>>>(a);
-  } else {
-    if (interleaved) norm_rope_kernel<64, true><<<grid, NR_THREADS, 0, s>>>(a);
-    else norm_rope_kernel<64, false><<<grid, NR_THREADS, 0, s>>>(a);
-  }
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e =
+      launch_dependent(d == 128 ? (interleaved ? norm_rope_kernel<128, true> : norm_rope_kernel<128, false>)
+                                : (interleaved ? norm_rope_kernel<64, true> : norm_rope_kernel<64, false>),
+                       grid, NR_THREADS, 0, s, a);
   return e == cudaSuccess ? SPARGE_OK : cuda_fail(e, "norm and rotation launch");
 }

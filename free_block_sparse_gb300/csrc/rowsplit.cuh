@@ -13,6 +13,7 @@
 #include <cstdint>
 
 #include "common.cuh"
+#include "dependent.cuh"
 
 namespace sparge {
 
@@ -131,99 +132,94 @@ __device__ __forceinline__ void end_item(const SplitArgs &a, const uint8_t *sums
 // Items cut between CTAs: the CTAs' partial rows (at CTA + item, a place of its own for every pair
 // that meets) weighted by 2^(m - M) and divided by the weighted sum, in an order that the lengths alone
 // set.  Items without a token get zero rows.  A CTA takes `nrow` rows of an item: one row per warp
-// where the item has few shares (many items, each cut once or twice), the whole CTA on one row after
-// another where it has many (one long sequence: 76 shares), so either way a few memory latencies.
-// Launched so that it may start while the attention ends (programmatic dependent launch); nothing is
-// read before the wait.
+// where the item has few shares (many items, each cut once or twice), its four warps on one row after
+// another where it has many (one long sequence: 76 shares).  A warp loads eight shares' references, sums and rows
+// together, so the eight cost one memory latency.  Launched so that it is set up while the attention ends.
 constexpr int CC_THREADS = 128, CC_FEW = 8;
 template <int D, int RT, typename Args>
 __global__ void __launch_bounds__(CC_THREADS) split_combine_kernel(const Args a, int nrow) {
-  constexpr int NL = D / 4, NGRP = CC_THREADS / NL;
-  __shared__ float wgt[CA_SMS * 4];
-  __shared__ float red[2][CC_THREADS / 32];
-  __shared__ float4 sums[NGRP][NL];
+  constexpr int NL = D / 4, NW = CC_THREADS / 32;
+  __shared__ float2 wml[NW];
+  __shared__ float4 sums[NW][NL];
   const int item = blockIdx.x, per = a.Hkv * a.ntile;
   const int b = item / per, kvh = item % per / a.ntile, row0 = (item % a.ntile) * 8 * RT;
-  const int t = threadIdx.x, lane = t & 31, warp = t >> 5, d4 = t % NL, grp = t / NL;
-  const int last = min(8 * RT, a.rows - row0), first = blockIdx.y * nrow;
-  auto out = [&](int row) { return out_row(a, b, kvh, row0 + row); };
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int first = blockIdx.y * nrow, last = min(min(8 * RT, a.rows - row0), first + nrow);
+  auto out = [&](int row) { return out_row(a, b, kvh, row0 + row) + 4 * lane; };
+  wait_for_earlier();
+  const int2 ends = a.ends[item];
   if (a.empty(b)) {
-    for (int row = first + warp; row < min(last, first + nrow); row += CC_THREADS / 32)
-      if (lane < NL) put_row(out(row) + 4 * lane, make_float4(0.f, 0.f, 0.f, 0.f), 0.f);
+    for (int row = first + warp; row < last; row += NW)
+      if (lane < NL) put_row(out(row), make_float4(0.f, 0.f, 0.f, 0.f), 0.f);
     return;
   }
-  const int2 ends = a.ends[item];
   const int n = ends.y - ends.x + 1;
   if (n <= 1) return;  // written by its only CTA
   const int64_t at0 = (static_cast<int64_t>(ends.x) + item) * 8 * RT;
-  if (n <= CC_FEW) {
-    for (int row = first + warp; row < min(last, first + nrow); row += CC_THREADS / 32) {
+  // shares w0, w0 + step, ... of a row: their reference M, sum L and, in lanes below NL, four channels of O
+  auto gather = [&](int row, int w0, int step, float &M, float &L, float4 &o) {
+    M = -INFINITY;
+    L = 0.f;
+    o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int w = w0; w < n; w += CC_FEW * step) {
       float2 ml = make_float2(-INFINITY, 0.f);
-      if (lane < n) ml = *reinterpret_cast<const float2 *>(a.part_ml + (at0 + static_cast<int64_t>(lane) * 8 * RT + row) * 2);
+      if (lane < CC_FEW && w + lane * step < n)
+        ml = *reinterpret_cast<const float2 *>(a.part_ml + (at0 + static_cast<int64_t>(w + lane * step) * 8 * RT + row) * 2);
       float4 v[CC_FEW];
-      if (lane < NL) {
 #pragma unroll
-        for (int w = 0; w < CC_FEW; ++w)
-          if (w < n) v[w] = *reinterpret_cast<const float4 *>(a.part_o + (at0 + static_cast<int64_t>(w) * 8 * RT + row) * D + 4 * lane);
+      for (int i = 0; i < CC_FEW; ++i)
+        if (w + i * step < n && lane < NL)
+          v[i] = *reinterpret_cast<const float4 *>(a.part_o + (at0 + static_cast<int64_t>(w + i * step) * 8 * RT + row) * D + 4 * lane);
+      float m = ml.x;
+#pragma unroll
+      for (int k = 4; k > 0; k >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
+      m = fmaxf(M, __shfl_sync(0xffffffffu, m, 0));
+      const float f0 = share_weight(M, L, m), f = share_weight(ml.x, ml.y, m);
+      M = m;
+      float l = f != 0.f ? f * ml.y : 0.f;
+#pragma unroll
+      for (int k = 4; k > 0; k >>= 1) l += __shfl_xor_sync(0xffffffffu, l, k);
+      L = (f0 != 0.f ? f0 * L : 0.f) + __shfl_sync(0xffffffffu, l, 0);
+      float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+      add_share(s, f0, o);
+#pragma unroll
+      for (int i = 0; i < CC_FEW; ++i) {
+        const float fi = __shfl_sync(0xffffffffu, f, i);
+        if (w + i * step < n && lane < NL) add_share(s, fi, v[i]);
       }
-      float M = ml.x;
-#pragma unroll
-      for (int o = 4; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-      M = __shfl_sync(0xffffffffu, M, 0);
-      const float f = share_weight(ml.x, ml.y, M);
-      float L = f != 0.f ? f * ml.y : 0.f;
-#pragma unroll
-      for (int o = 4; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-      L = __shfl_sync(0xffffffffu, L, 0);
-      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int w = 0; w < CC_FEW; ++w) {
-        const float fw = __shfl_sync(0xffffffffu, f, w);
-        if (w < n && lane < NL) add_share(o, fw, v[w]);
-      }
-      if (lane < NL) put_row(out(row) + 4 * lane, o, L == 0.f ? 0.f : 1.f / L);
+      o = s;
+    }
+  };
+  float M, L;
+  float4 o;
+  if (n <= CC_FEW) {
+    for (int row = first + warp; row < last; row += NW) {
+      gather(row, 0, 1, M, L, o);
+      if (lane < NL) put_row(out(row), o, L == 0.f ? 0.f : 1.f / L);
     }
     return;
   }
-  for (int row = first; row < min(last, first + nrow); ++row) {
-    float M = -INFINITY;
-    for (int w = t; w < n; w += CC_THREADS) M = fmaxf(M, a.part_ml[(at0 + static_cast<int64_t>(w) * 8 * RT + row) * 2]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    if (lane == 0) red[0][warp] = M;
+  for (int row = first; row < last; ++row) {
+    gather(row, warp, NW, M, L, o);
+    if (lane == 0) wml[warp] = make_float2(M, L);
+    if (lane < NL) sums[warp][lane] = o;
     __syncthreads();
+    if (warp == 0) {
 #pragma unroll
-    for (int u = 0; u < CC_THREADS / 32; ++u) M = fmaxf(M, red[0][u]);
-    float L = 0.f;
-    for (int w = t; w < n; w += CC_THREADS) {
-      const float2 ml = *reinterpret_cast<const float2 *>(a.part_ml + (at0 + static_cast<int64_t>(w) * 8 * RT + row) * 2);
-      const float f = share_weight(ml.x, ml.y, M);
-      wgt[w] = f;
-      if (f != 0.f) L = fmaf(f, ml.y, L);
-    }
+      for (int u = 0; u < NW; ++u) M = fmaxf(M, wml[u].x);
+      L = 0.f;
+      o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-    if (lane == 0) red[1][warp] = L;
-    __syncthreads();
-    L = 0.f;
-#pragma unroll
-    for (int u = 0; u < CC_THREADS / 32; ++u) L += red[1][u];
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int w = grp; w < n; w += NGRP)
-      add_share(o, wgt[w], *reinterpret_cast<const float4 *>(a.part_o + (at0 + static_cast<int64_t>(w) * 8 * RT + row) * D + 4 * d4));
-    sums[grp][d4] = o;
-    __syncthreads();
-    if (grp == 0) {
-#pragma unroll
-      for (int u = 1; u < NGRP; ++u) add_share(o, 1.f, sums[u][d4]);
-      put_row(out(row) + 4 * d4, o, L == 0.f ? 0.f : 1.f / L);
+      for (int u = 0; u < NW; ++u) {
+        const float f = share_weight(wml[u].x, wml[u].y, M);
+        if (f != 0.f) L = fmaf(f, wml[u].y, L);
+        if (lane < NL) add_share(o, f, sums[u][lane]);
+      }
+      if (lane < NL) put_row(out(row), o, L == 0.f ? 0.f : 1.f / L);
     }
     __syncthreads();
   }
 }
-
 
 // shares: the attention kernel's CTAs, at most
 template <int D, int RT, typename Args>
@@ -231,16 +227,8 @@ cudaError_t launch_split_combine(const Args &a, int64_t shares, cudaStream_t st)
   // rows of a combining CTA: one per warp where items outnumber half the shares (an item then has few), else one
   const int64_t items = static_cast<int64_t>(a.B) * a.Hkv * a.ntile;
   const int nrow = 2 * items > shares ? CC_THREADS / 32 : 1, rows = a.rows < 8 * RT ? a.rows : 8 * RT;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(items), static_cast<unsigned>((rows + nrow - 1) / nrow));
-  cfg.blockDim = dim3(CC_THREADS);
-  cfg.stream = st;
-  cudaLaunchAttribute at;
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, split_combine_kernel<D, RT, Args>, a, nrow);
+  const dim3 grid(static_cast<unsigned>(items), static_cast<unsigned>((rows + nrow - 1) / nrow));
+  return launch_dependent(split_combine_kernel<D, RT, Args>, grid, CC_THREADS, 0, st, a, nrow);
 }
 
 }  // namespace sparge

@@ -75,6 +75,7 @@ __global__ void __launch_bounds__(CA_WARPS * 32, 2)
   constexpr int MT = D / 16, ST = S::ST;
   extern __shared__ __align__(1024) uint8_t smem[];
   if (smem_u32(smem) & 1023u) {  // the swizzle assumes it
+    wait_for_earlier();
     if (threadIdx.x == 0) record_status(a.status, -4 /* SPARGE_ERR_CUDA */);
     return;
   }
@@ -90,7 +91,8 @@ __global__ void __launch_bounds__(CA_WARPS * 32, 2)
     prefetch_tmap(&tv);
   }
   __syncthreads();
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the combining kernel may be set up from here on
+  let_dependents_start();
+  wait_for_earlier();
 
   const int tiles = (a.recs + 3) >> 2;  // of an item, 64 tokens each; the grid has at most as many CTAs as there are tiles
   const int64_t total = static_cast<int64_t>(tiles) * a.B * a.Hkv * a.ntile;
@@ -302,8 +304,10 @@ cudaError_t launch_t(const WindowDecode &l, const WindowArgs &a, int64_t ctas, c
   using S = WdSmem<D, RT>;
   static std::atomic<unsigned long long> smem_set{0};
   if (cudaError_t e = set_smem_limit_once(window_decode_kernel<D, RT>, S::TOTAL, smem_set); e != cudaSuccess) return e;
-  window_decode_kernel<D, RT><<<static_cast<unsigned>(ctas), CA_WARPS * 32, S::TOTAL, st>>>(l.tk, l.tv, a);
-  if (cudaError_t e = cudaGetLastError(); e != cudaSuccess) return e;
+  if (cudaError_t e = launch_dependent(window_decode_kernel<D, RT>, dim3(static_cast<unsigned>(ctas)), CA_WARPS * 32, S::TOTAL, st,
+                                       l.tk, l.tv, a);
+      e != cudaSuccess)
+    return e;
   return launch_split_combine<D, RT>(a, ctas, st);
 }
 
