@@ -19,12 +19,16 @@
 // P lies in [0, 2^8] (the reference follows the running maximum lazily) and s is scaled by a power
 // of two that follows its running maximum the same way, so P s stays in f16's range.
 //
-// Work: the (sequence, KV head, row tile) items' 64-token tiles in one line, cut into equal shares,
-// one per CTA (4 CTAs per SM), so ragged lengths fill the part evenly; every CTA sums the lengths
-// itself.  A warp takes every fourth 16-token record of its CTA's share through a ring of its own
-// of bulk copies, without any synchronisation among warps until an item ends; then the four warps'
-// sums are merged in shared memory, and an item cut between CTAs is put together by a second
-// kernel.
+// Work: the (sequence, KV head, row tile) items' tiles in one line, cut into equal shares, one per CTA
+// (4 CTAs per SM, 3 with 16-row tiles), so ragged lengths fill the part evenly; every warp sums the lengths
+// itself.  A warp takes every fourth step of its CTA's share (two 16-token records, one with 16 rows of d = 128)
+// through a ring of its own of bulk copies, without any synchronisation among warps until an item
+// ends; then the four warps' sums are merged in shared memory, and an item cut between CTAs is put
+// together by a second kernel (rowsplit.cuh).
+// Measured: 64 sequences of 1K to 32K tokens, 32 + 8 heads, d = 128: 206 us for 1.25 GB, 90% of the
+// measured copy rate; one sequence of 4K 9 us, of which the chain length -> page -> record -> merge ->
+// combine is nearly all; 128 x 4 queries under a window of 4096, d = 64: 57 us, 38% (16 rows of 64 channels bring two
+// and a half times the arithmetic per byte: the products and the ALU are each over a third busy).
 #include <climits>
 #include <cmath>
 #include <type_traits>
@@ -39,6 +43,9 @@ namespace sparge {
 int check_cache4(const ::sparge_cache4 *c, Cache4 *out);
 namespace {
 
+// Tiles that an item's start and end weigh in a CTA's share (128 ragged sequences of 4 queries, d = 64, under a
+// window of 4096: 0 66 us, 2 58, 3 57; 64 sequences of up to 32K: 0 213, 3 206).
+constexpr int CA_ITEM = 3;
 constexpr float CA_SBOUND = 64.f;  // scaled V scales stay below this: P s < 2^8 2^6 < 65504
 
 struct CacheAttnArgs : SplitArgs {
@@ -93,17 +100,26 @@ struct CaSmem {
 };
 struct CaCtrl {
   uint64_t full[CA_WARPS][6];
-  int64_t sums[CA_WARPS];
-  int64_t off;
-  int b0, abort;
+  int abort;
   uint8_t bad[CA_WARPS][12];  // the record's page lies outside the pool: its tokens are left out
 };
 static_assert(sizeof(CaCtrl) <= 512, "control block");
 
-// 64 or 32 U-token tiles of all heads and row tiles of a sequence.
+// The line that is cut into shares: every item counts its tiles (4 U records each) and CA_ITEM more, about
+// the time that a CTA spends on an item apart from its tiles, so a CTA of many short items gets fewer tiles.
+// A place in those CA_ITEM stands for no work.
+template <int U>
+__device__ __forceinline__ int tiles_of(const Span &sp) {
+  return (sp.recs + 4 * U - 1) / (4 * U);
+}
 template <int U>
 __device__ __forceinline__ int64_t units_of(const CacheAttnArgs &a, int b) {
-  return static_cast<int64_t>((span_of(a, b).recs + 4 * U - 1) / (4 * U)) * (a.Hkv * a.ntile);
+  const int t = tiles_of<U>(span_of(a, b));
+  return t == 0 ? 0 : static_cast<int64_t>(t + CA_ITEM) * (a.Hkv * a.ntile);
+}
+// x / y for non-negative x and positive y, in 32 bits where they do
+__device__ __forceinline__ int64_t divide(int64_t x, int64_t y) {
+  return ((x | y) >> 32) == 0 ? static_cast<uint32_t>(x) / static_cast<uint32_t>(y) : x / y;
 }
 
 __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
@@ -164,110 +180,162 @@ __global__ void __launch_bounds__(CA_WARPS * 32, RT == 1 ? 4 : 3) cache4_attn_ke
   let_dependents_start();
   wait_for_earlier();
 
-  // ---- this CTA's share [start, end) of the line of tiles, and the sequence it starts in ----
-  const int per = (a.B + CA_WARPS * 32 - 1) / (CA_WARPS * 32);
-  const int bt = min(a.B, static_cast<int>(threadIdx.x) * per), bu = min(a.B, bt + per);
+  // ---- this CTA's share [start, end) of the line of tiles, and the sequence it starts in; every warp for
+  // itself, so that no barrier holds up the first loads ----
+  if (lane == 0) {
+    cs.abort = 0;
+    for (int s = 0; s < ST; ++s) mbar_init(&cs.full[warp][s], U);
+    fence_barrier_init();
+  }
+  __syncwarp();
+  const int per = (a.B + 31) / 32, bt = min(a.B, lane * per), bu = min(a.B, bt + per);
   int64_t own = 0;
   for (int b = bt; b < bu; ++b) own += units_of<U>(a, b);
   int64_t inc = own;
+  if (a.B > 1) {
 #pragma unroll
-  for (int off = 1; off < 32; off <<= 1) {
-    const int64_t o = __shfl_up_sync(0xffffffffu, inc, off);
-    if (lane >= off) inc += o;
+    for (int off = 1; off < 32; off <<= 1) {
+      const int64_t o = __shfl_up_sync(0xffffffffu, inc, off);
+      if (lane >= off) inc += o;
+    }
   }
-  if (lane == 31) cs.sums[warp] = inc;
-  if (threadIdx.x == 0) {
-    cs.abort = 0;
-    for (int w = 0; w < CA_WARPS; ++w)
-      for (int s = 0; s < ST; ++s) mbar_init(&cs.full[w][s], U);
-    fence_barrier_init();
-  }
-  __syncthreads();
-  int64_t total = 0, before = inc - own;
-#pragma unroll
-  for (int w = 0; w < CA_WARPS; ++w) {
-    before += w < warp ? cs.sums[w] : 0;
-    total += cs.sums[w];
-  }
-  // shares only for as many CTAs as there are tiles: between an item's first and last CTA each holds some of it
+  const int64_t total = __shfl_sync(0xffffffffu, inc, a.B > 1 ? 31 : 0);
+  // shares only for as many CTAs as there are places: between an item's first and last CTA each holds some of it
   const int64_t shares = total < gridDim.x ? total : gridDim.x;
   if (blockIdx.x >= shares) return;
-  const int64_t start = total * blockIdx.x / shares, end = total * (blockIdx.x + 1) / shares;
-  if (before <= start && start < before + own) {
-    int b = bt;
-    int64_t at = before;
-    for (;; ++b) {
-      const int64_t u = units_of<U>(a, b);
-      if (start < at + u) break;
-      at += u;
-    }
-    cs.b0 = b;
-    cs.off = start - at;
-  }
-  __syncthreads();
-  int b = cs.b0;
-  int64_t off = cs.off, left = end - start;
-  bool has_bad_once = true;
+  const int64_t start = divide(total * blockIdx.x, shares), end = divide(total * (blockIdx.x + 1), shares);
+  int b = bt;
+  int64_t off = start - (inc - own), left = end - start;
+  const uint32_t here = __ballot_sync(0xffffffffu, off >= 0 && off < own);  // the lane whose sequences hold the start
+  if (off >= 0 && off < own)
+    for (int64_t u; off >= (u = units_of<U>(a, b)); ++b) off -= u;
+  b = __shfl_sync(0xffffffffu, b, __ffs(here) - 1);
+  off = __shfl_sync(0xffffffffu, off, __ffs(here) - 1);
   uint32_t used = 0;  // steps this warp has taken through its ring (stage used % ST)
 
-  while (left > 0) {
-    const Span sp = span_of(a, b);
-    const int tiles = (sp.recs + 4 * U - 1) / (4 * U);
-    const int64_t units = static_cast<int64_t>(tiles) * (a.Hkv * a.ntile);
-    if (off >= units) {
-      off -= units;
-      ++b;
-      continue;
+  // ---- the item at the front of what is left of the share, and its first loads ----
+  Span sp;
+  int item, kvh, row0, tiles, tile0, nt;  // this CTA holds tiles tile0 .. tile0 + nt - 1 of the item
+  int k0, kend, nstep;                    // this warp's steps; step i: records k0 + 4 U i .. + U - 1, those below kend
+  auto locate = [&]() -> bool {           // false: nothing left
+    while (left > 0) {
+      sp = span_of(a, b);
+      tiles = tiles_of<U>(sp);
+      const int64_t in_b = tiles ? divide(off, tiles + CA_ITEM) : INT_MAX;
+      if (in_b >= a.Hkv * a.ntile) {
+        off -= units_of<U>(a, b);
+        ++b;
+        continue;
+      }
+      const int place = static_cast<int>(off - in_b * (tiles + CA_ITEM));
+      if (place < CA_ITEM) {
+        const int64_t skip = left < CA_ITEM - place ? left : CA_ITEM - place;
+        off += skip;
+        left -= skip;
+        if (left == 0) return false;
+      }
+      tile0 = max(place - CA_ITEM, 0);
+      nt = static_cast<int>(left < tiles - tile0 ? left : tiles - tile0);
+      off += nt;
+      left -= nt;
+      kvh = static_cast<int>(in_b) / a.ntile;
+      row0 = (static_cast<int>(in_b) - kvh * a.ntile) * 8 * RT;
+      item = b * (a.Hkv * a.ntile) + static_cast<int>(in_b);
+      k0 = (tile0 * 4 + warp) * U;
+      kend = min(sp.recs, (tile0 + nt) * 4 * U);
+      nstep = kend > k0 ? (kend - k0 + 4 * U - 1) / (4 * U) : 0;
+      return true;
     }
-    const int in_b = static_cast<int>(off / tiles), tile0 = static_cast<int>(off % tiles);
-    const int nt = static_cast<int>(left < tiles - tile0 ? left : tiles - tile0);
-    const int kvh = in_b / a.ntile, rt = in_b % a.ntile;
-    const int item = b * (a.Hkv * a.ntile) + in_b;
-    const int row0 = rt * 8 * RT;
+    return false;
+  };
+  auto record_at = [&](int k) { return k < sp.ns ? k : sp.lo + k - sp.ns; };
+  // The warp looks up the pages of 32 records at a time; the lane that holds a record's address issues
+  // its copy.
+  const uint8_t *src = nullptr;  // record lane % U of step sbase + lane / U (null: no such page, no such record)
+  int sbase = 0;
+  bool has_bad = false, had_bad = true;  // some page of the item (of the one before) was outside the pool: the flags count
+  auto look_up = [&](int i) {
+    sbase = i;
+    const int k = k0 + 4 * U * (i + lane / U) + lane % U;
+    src = nullptr;
+    bool bad = false;
+    if (k < kend) {
+      const int r = record_at(k);
+      const int page = __ldg(a.table + static_cast<int64_t>(b) * a.table_stride + (r >> a.rec_shift));
+      bad = page < 0 || page >= a.n_pages;
+      if (bad)
+        record_status(a.status, -1 /* SPARGE_ERR_INVALID_ARG */);
+      else
+        src = a.pool + (((static_cast<int64_t>(page) * a.Hkv + kvh) << a.rec_shift) + (r & ((1 << a.rec_shift) - 1))) * S::REC;
+    }
+    has_bad = __any_sync(0xffffffffu, bad) || has_bad;
+  };
+  auto issue = [&](int i) {  // called by the whole warp for i = 0, 1, ... in order
+    if (i >= sbase + 32 / U) look_up(i);
+    if (lane / U == i - sbase) {
+      const uint32_t st = (used + i) % ST;
+      uint64_t *bar = &cs.full[warp][st];
+      if (has_bad) cs.bad[warp][st * U + lane % U] = src == nullptr;
+      if (src != nullptr) {
+        mbar_arrive_expect_tx(bar, S::REC);
+        bulk_load(ring + (st * U + lane % U) * S::REC, src, S::REC, bar);
+      } else {
+        mbar_arrive(bar);
+      }
+    }
+  };
+  // this lane's query row of row tile j (null: there is none) and its place among the Nq queries
+  auto query_of = [&](int j, int &qi) -> const uint4 * {
+    const int r = row0 + 8 * j + g;
+    const int hg = a.Nq == 1 ? r : r / a.Nq;
+    qi = a.Nq == 1 ? 0 : r - hg * a.Nq;
+    if (r >= a.rows) {
+      qi = 0;
+      return nullptr;
+    }
+    return reinterpret_cast<const uint4 *>(a.q + b * a.q_sb + (kvh * a.G + hg) * a.q_sh + static_cast<int64_t>(qi) * a.q_sn);
+  };
+  // Q rows of the next item: carried in registers over the end of the one before where they fit (d = 64),
+  // else only fetched ahead of their use
+  constexpr bool CARRY = D == 64;
+  uint4 qraw[RT][NW];
+  auto load_q = [&](int j) {
+    int qi;
+    const uint4 *qrow = query_of(j, qi);
+#pragma unroll
+    for (int w = 0; w < NW; ++w) qraw[j][w] = qrow != nullptr ? __ldg(qrow + 4 * w + c) : make_uint4(0u, 0u, 0u, 0u);
+  };
 
-    // ---- the copies: this warp's steps, step i: records k0 + 4 U i .. + U - 1 ----
-    const int k0 = (tile0 * 4 + warp) * U, kend = min(sp.recs, (tile0 + nt) * 4 * U);
-    const int nstep = kend > k0 ? (kend - k0 + 4 * U - 1) / (4 * U) : 0;
-    const int32_t *trow = a.table + static_cast<int64_t>(b) * a.table_stride;
-    auto record_at = [&](int k) { return k < sp.ns ? k : sp.lo + k - sp.ns; };
-    // The warp looks up the pages of 32 records at a time; the lane that holds a record's address
-    // issues its copy.
-    const uint8_t *src = nullptr;  // record lane % U of step sbase + lane / U (null: no such page, no such record)
-    int sbase = -32;
-    bool has_bad = false;          // some page was outside the pool: the stages' flags count
-    auto issue = [&](int i) {      // called by the whole warp for i = 0, 1, ... in order
-      if (i >= sbase + 32 / U) {
-        sbase = i;
-        const int k = k0 + 4 * U * (i + lane / U) + lane % U;
-        src = nullptr;
-        bool bad = false;
-        if (k < kend) {
-          const int r = record_at(k);
-          const int page = __ldg(trow + (r >> a.rec_shift));
-          bad = page < 0 || page >= a.n_pages;
-          if (bad)
-            record_status(a.status, -1 /* SPARGE_ERR_INVALID_ARG */);
-          else
-            src = a.pool + (((static_cast<int64_t>(page) * a.Hkv + kvh) << a.rec_shift) + (r & ((1 << a.rec_shift) - 1))) * S::REC;
-        }
-        has_bad = __any_sync(0xffffffffu, bad) || has_bad;
-      }
-      if (lane / U == i - sbase) {
-        const uint32_t st = (used + i) % ST;
-        uint64_t *bar = &cs.full[warp][st];
-        if (has_bad) cs.bad[warp][st * U + lane % U] = src == nullptr;
-        if (src != nullptr) {
-          mbar_arrive_expect_tx(bar, S::REC);
-          bulk_load(ring + (st * U + lane % U) * S::REC, src, S::REC, bar);
+  // The next item's first loads (queries, page numbers) go out before the end of the one before.
+  bool ending = false, first = false, last = false;
+  int item_done = 0, b_done = 0, kvh_done = 0, row_done = 0;
+  for (;;) {
+    const bool more = locate();
+    if (more) {
+#pragma unroll
+      for (int j = 0; j < RT; ++j) {
+        if constexpr (CARRY) {
+          load_q(j);
         } else {
-          mbar_arrive(bar);
+          int qi;
+          const uint4 *qrow = query_of(j, qi);
+          if (qrow != nullptr && (c & 1) == 0)
+#pragma unroll
+            for (int w = 0; w < NW; ++w) asm volatile("prefetch.global.L1 [%0];" ::"l"(qrow + 4 * w + c));
         }
       }
-    };
-    if (has_bad_once) {  // flags of an earlier item
+      has_bad = false;
+      look_up(0);
+    }
+    if (ending) {
+      end_item<D, RT>(a, smem, S::WRING, S::OROW, reinterpret_cast<const float2 *>(smem + S::OFF_ML), item_done, b_done,
+                      kvh_done, row_done, first, last);
+      if (*reinterpret_cast<volatile int *>(&cs.abort)) break;
+    }
+    if (!more) break;
+    if (had_bad) {  // flags of an earlier item
       if (lane < 12) cs.bad[warp][lane] = 0;
       __syncwarp();
-      has_bad_once = false;
     }
     const int ahead = min(nstep, ST);
     for (int i = 0; i < ahead; ++i) issue(i);
@@ -278,18 +346,16 @@ __global__ void __launch_bounds__(CA_WARPS * 32, RT == 1 ? 4 : 3) cache4_attn_ke
     int pos[RT][2];
 #pragma unroll
     for (int j = 0; j < RT; ++j) {
-      const int r = row0 + 8 * j + g;
-      const bool ok = r < a.rows;
-      const int h = kvh * a.G + (ok ? r / a.Nq : 0), qi = ok ? r % a.Nq : 0;
-      const uint4 *qrow = reinterpret_cast<const uint4 *>(a.q + b * a.q_sb + h * a.q_sh + static_cast<int64_t>(qi) * a.q_sn);
+      if constexpr (!CARRY) load_q(j);
+      int qi;
+      query_of(j, qi);
       float x[NW][8];
       float mx = 0.f, sum[NG];
 #pragma unroll
       for (int w = 0; w < NG; ++w) sum[w] = 0.f;
 #pragma unroll
       for (int w = 0; w < NW; ++w) {
-        const uint4 v = ok ? __ldg(qrow + 4 * w + c) : make_uint4(0u, 0u, 0u, 0u);
-        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+        const uint32_t u[4] = {qraw[j][w].x, qraw[j][w].y, qraw[j][w].z, qraw[j][w].w};
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           x[w][2 * k] = bf16lo(u[k]);
@@ -541,7 +607,7 @@ __global__ void __launch_bounds__(CA_WARPS * 32, RT == 1 ? 4 : 3) cache4_attn_ke
       __syncwarp();  // every lane has read the stage
       if (i + ST < nstep) issue(i + ST);
     }
-    has_bad_once = has_bad;
+    had_bad = has_bad;
     used += nstep;
 
     // ---- the item's (or its share's) end: the warps' sums into shared memory, then merged ----
@@ -570,10 +636,13 @@ __global__ void __launch_bounds__(CA_WARPS * 32, RT == 1 ? 4 : 3) cache4_attn_ke
           mo[row * S::OROW + 16 * u + 8 + g] = fmaf(acc[u][j][2 + k], back * 0.0625f, z[u / 4]);
         }
       }
-    end_item<D, RT>(a, smem, S::WRING, S::OROW, ml, item, b, kvh, row0, tile0 == 0, tile0 + nt == tiles);
-    if (*reinterpret_cast<volatile int *>(&cs.abort)) break;
-    off += nt;
-    left -= nt;
+    ending = true;
+    item_done = item;
+    b_done = b;
+    kvh_done = kvh;
+    row_done = row0;
+    first = tile0 == 0;
+    last = tile0 + nt == tiles;
   }
   if (*reinterpret_cast<volatile int *>(&cs.abort)) {  // let copies already in flight land before the CTA exits
     const uint64_t t0 = global_timer_ns();
@@ -669,8 +738,7 @@ int sparge_cache4_attn(const sparge_tensor *q, const sparge_cache4 *cache, const
     recs = recs < most ? recs : most;
   }
   const int64_t step = qv.d == 64 || rt == 1 ? 8 : 4;  // records of a CTA's tile
-  int64_t tiles = (recs + step - 1) / step * qv.B * c.H * ntile;
-  if (tiles < 1) tiles = 1;
+  const int64_t tiles = ((recs + step - 1) / step + CA_ITEM) * qv.B * c.H * ntile;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (qv.d == 128)
