@@ -438,24 +438,10 @@ int attn_impl(const View &q, const View &k, const View &v, const uint8_t *mask, 
 
 // --- causal attention over a sliding window and the first tokens ---
 
-// Key blocks of one query tile at most: those of the first tokens and of the window of its Nq queries.
-int64_t window_blocks(int64_t Nq, int64_t Nk, int64_t window, int64_t sinks) {
-  const int64_t first = Nk - Nq - window + 1, lo = first > 0 ? first / KBLK : 0, ns = cdiv(sinks, KBLK);
-  return (ns < lo ? ns : lo) + cdiv(Nk, KBLK) - lo;
-}
-
-// Shares of a decoding call's key blocks, at most: the split of decode_split before its rounding,
-// which grows with the number of blocks, so a workspace sized for all Nk keys holds every window's.
-int64_t window_chunks(int64_t B, int64_t Hkv, int64_t blocks) {
-  const int64_t units = B * Hkv > 0 ? B * Hkv : 1, n = (304 + units - 1) / units, most = blocks / 16;
-  return n < most ? n : (most > 1 ? most : 1);
-}
-
+// The f16 copy of V, or a decoding call's partial rows.
 size_t window_ws_bytes(int64_t B, int64_t Hkv, int64_t Nk, int64_t d) {
-  const size_t rows = static_cast<size_t>(B * Hkv) * window_chunks(B, Hkv, cdiv(Nk, KBLK)) * 128;
-  const size_t part = align256(rows * d * 4) + align256(rows * 2 * 4), v16 = v16_bytes(B, Hkv, Nk, d);
-  const size_t few = window_decode_ws_bytes(B, Hkv, d), most = part > v16 ? part : v16;
-  return few > most ? few : most;
+  const size_t few = window_decode_ws_bytes(B, Hkv, d), v16 = v16_bytes(B, Hkv, Nk, d);
+  return few > v16 ? few : v16;
 }
 
 int window_impl(const View &q, const View &k, const View &v, const View &o, int64_t window, int64_t sinks, float scale,
@@ -486,28 +472,16 @@ int window_impl(const View &q, const View &k, const View &v, const View &o, int6
   }
   AttnLaunch l;
   memset(&l, 0, sizeof(l));
-  const int64_t blocks = window_blocks(q.N, k.N, window, sinks);
-  if (q.H / k.H * q.N <= 128 && blocks >= 32) {  // decoding tiles, as in attn_impl: V in place as bf16
-    const DecodeSplit sp = decode_split(k.B, k.H, blocks * KBLK);
-    const size_t rows = static_cast<size_t>(k.B * k.H) * sp.nchunk * 128;
-    l.decode = 1;
-    l.nchunk = sp.nchunk;
-    l.chunk_blocks = sp.chunk_blocks;
-    l.part_o = static_cast<float *>(ws);
-    l.part_ml = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + align256(rows * q.d * 4));
-    if ((rc = make_map(&l.tv, v, 64, "v"))) return rc;
-  } else {
-    // the f16 copy of the V rows that are read: the first tokens' blocks and those from the first
-    // query's window on
-    const int64_t first = k.N - q.N - window + 1, lo = first > 0 ? first / KBLK * KBLK : 0;
-    const int64_t ns = cdiv(sinks, KBLK) * KBLK;
-    cudaError_t e = launch_convert_v_f16(v, ws, nullptr, status_ptr(), s, lo, k.N);
-    if (e == cudaSuccess && lo > 0 && ns > 0)
-      e = launch_convert_v_f16(v, ws, nullptr, status_ptr(), s, 0, ns < lo ? ns : lo);
-    if (e != cudaSuccess) return cuda_fail(e, "convert_v launch");
-    View v16{ws, v.B, v.H, v.N, v.d, v.H * v.N * v.d, v.N * v.d, v.d};
-    if ((rc = make_map(&l.tv, v16, 64, "v", CU_TENSOR_MAP_DATA_TYPE_FLOAT16))) return rc;
-  }
+  // the f16 copy of the V rows that are read: the first tokens' blocks and those from the first
+  // query's window on
+  const int64_t first = k.N - q.N - window + 1, lo = first > 0 ? first / KBLK * KBLK : 0;
+  const int64_t ns = cdiv(sinks, KBLK) * KBLK;
+  cudaError_t e = launch_convert_v_f16(v, ws, nullptr, status_ptr(), s, lo, k.N);
+  if (e == cudaSuccess && lo > 0 && ns > 0)
+    e = launch_convert_v_f16(v, ws, nullptr, status_ptr(), s, 0, ns < lo ? ns : lo);
+  if (e != cudaSuccess) return cuda_fail(e, "convert_v launch");
+  View v16{ws, v.B, v.H, v.N, v.d, v.H * v.N * v.d, v.N * v.d, v.d};
+  if ((rc = make_map(&l.tv, v16, 64, "v", CU_TENSOR_MAP_DATA_TYPE_FLOAT16))) return rc;
   if ((rc = make_map(&l.tq, q, 128, "q")) || (rc = make_map(&l.tk, k, 64, "k"))) return rc;
   l.q = q.data;
   l.q_sb = q.sb; l.q_sh = q.sh; l.q_sn = q.sn;
@@ -520,7 +494,7 @@ int window_impl(const View &q, const View &k, const View &v, const View &o, int6
   l.window = (int)window;
   l.sinks = (int)sinks;
   l.status = status_ptr();
-  cudaError_t e = launch_bsattn(l, s);
+  e = launch_bsattn(l, s);
   return e == cudaSuccess ? SPARGE_OK : cuda_fail(e, "window attention launch");
 }
 

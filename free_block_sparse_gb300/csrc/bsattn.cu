@@ -287,16 +287,16 @@ __global__ void __launch_bounds__(NTHREADS, 2)
     // arrive without data).
     KeptScan ks;
     ks.init(mrow, n_valid);
-    const WinBlocks wb(a.off + QBLK * i, a.window, a.sinks);
+    const WinBlocks wb(a.off + QBLK * i, a.window, a.sinks);  // used with WIN alone
     // decoding tile: share `chunk` of the (batch, KV head)'s kept-block list, [d_lo, d_hi)
     int d_lo = 0, d_hi = 0;
     const int32_t *dl = nullptr;
     if constexpr (DEC) {
       const int chunk = blockIdx.x % a.nchunk, bk = blockIdx.x / a.nchunk;
-      const int cnt = WIN ? wb.ns + a.nkb - wb.lo : a.mask ? __ldg(a.dcount + bk) : a.nkb;
+      const int cnt = a.mask ? __ldg(a.dcount + bk) : a.nkb;
       d_lo = static_cast<int>(static_cast<int64_t>(chunk) * cnt / a.nchunk);
       d_hi = static_cast<int>(static_cast<int64_t>(chunk + 1) * cnt / a.nchunk);
-      if (!WIN && a.mask) dl = a.dlist + static_cast<int64_t>(bk) * a.nkb;
+      if (a.mask) dl = a.dlist + static_cast<int64_t>(bk) * a.nkb;
     }
     if (lane == 0) {
       prefetch_tmap(&tq);
@@ -307,7 +307,7 @@ __global__ void __launch_bounds__(NTHREADS, 2)
     for (int t = 0;; ++t) {
       int j;
       if constexpr (DEC)
-        j = d_lo + t < d_hi ? (WIN ? wb.at(d_lo + t) : dl ? __ldg(dl + d_lo + t) : d_lo + t) : -1;
+        j = d_lo + t < d_hi ? (dl ? __ldg(dl + d_lo + t) : d_lo + t) : -1;
       else if constexpr (WIN)
         j = wb.at(t) < n_valid ? wb.at(t) : -1;
       else
@@ -838,26 +838,21 @@ cudaError_t launch_bsattn(const AttnLaunch &l, cudaStream_t st) {
   if (static_cast<int64_t>(a.B) * a.Hq * a.nqb == 0) return cudaSuccess;
   if (l.q8 != 0 && l.d != 128) return cudaErrorInvalidValue;
   if (l.decode) {  // bf16 only: the host picks this path for few queries per head, lambda off
-    if (l.q8 != 0 || a.G * a.Nq > 128 || l.nchunk <= 0) return cudaErrorInvalidValue;
+    if (l.window != 0 || l.q8 != 0 || a.G * a.Nq > 128 || l.nchunk <= 0) return cudaErrorInvalidValue;
     a.nchunk = l.nchunk;
     a.chunk_blocks = l.chunk_blocks;
     a.part_o = l.part_o;
     a.part_ml = l.part_ml;
     a.dlist = l.dlist;
     a.dcount = l.dcount;
-    if (a.mask && !l.window) {
+    if (a.mask) {
       if (!l.dlist || !l.dcount) return cudaErrorInvalidValue;
       if (cudaError_t e = launch_decode_union(a.mask, a.B, a.Hq, a.Hkv, a.nqb, a.nkb, l.dlist, l.dcount, st);
           e != cudaSuccess)
         return e;
     }
-    cudaError_t e;
-    if (l.window)
-      e = l.d == 128 ? launch_t<128, 3, 2, false, false, true, true>(l, a, st)
-                     : launch_t<64, 4, 3, false, false, true, true>(l, a, st);
-    else
-      e = l.d == 128 ? launch_t<128, 3, 2, false, false, true>(l, a, st)
-                     : launch_t<64, 4, 3, false, false, true>(l, a, st);
+    cudaError_t e = l.d == 128 ? launch_t<128, 3, 2, false, false, true>(l, a, st)
+                               : launch_t<64, 4, 3, false, false, true>(l, a, st);
     if (e != cudaSuccess) return e;
     return launch_decode_combine(l.part_o, l.part_ml, l.nchunk, a.B, a.Hq, a.Hkv, a.Nq, l.d, a.o, a.o_sb, a.o_sh, a.o_sn,
                                  st);

@@ -186,7 +186,7 @@ cudaError_t launch_bsattn(const AttnLaunch &a, cudaStream_t st);
 
 // Decoding under a sliding window, up to WINDOW_DECODE_ROWS query rows per KV head (window_decode.cu).  tk and
 // tv: 4-D maps over K and V (bf16, 128-byte swizzle, boxes 64 x 16).
-constexpr int WINDOW_DECODE_ROWS = 16;
+constexpr int WINDOW_DECODE_ROWS = 128;
 struct WindowDecode {
   CUtensorMap tk, tv;
   const void *q;

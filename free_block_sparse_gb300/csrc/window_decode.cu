@@ -313,7 +313,9 @@ cudaError_t launch_t(const WindowDecode &l, const WindowArgs &a, int64_t ctas, c
 
 }  // namespace
 
-size_t window_decode_ws_bytes(int64_t B, int64_t Hkv, int64_t d) { return split_ws(B * Hkv, WD_CTAS, 2, d).total; }
+size_t window_decode_ws_bytes(int64_t B, int64_t Hkv, int64_t d) {
+  return split_ws(B * Hkv * (WINDOW_DECODE_ROWS / 16), WD_CTAS, 2, d).total;
+}
 
 cudaError_t launch_window_decode(const WindowDecode &l, cudaStream_t st) {
   const int64_t rows = static_cast<int64_t>(l.G) * l.Nq;
@@ -324,8 +326,8 @@ cudaError_t launch_window_decode(const WindowDecode &l, cudaStream_t st) {
   a.o_sb = l.o_sb; a.o_sh = l.o_sh; a.o_sn = l.o_sn;
   a.B = l.B; a.Hkv = l.Hkv; a.G = l.G; a.Nq = l.Nq;
   a.rows = static_cast<int>(rows);
-  a.ntile = 1;
-  const int64_t items = static_cast<int64_t>(l.B) * l.Hkv;
+  a.ntile = static_cast<int>((rows + 8 * rt - 1) / (8 * rt));
+  const int64_t items = static_cast<int64_t>(l.B) * l.Hkv * a.ntile;
   if (items > INT_MAX) return cudaErrorInvalidValue;
   const SplitWs w = split_ws(items, WD_CTAS, rt, l.d);
   uint8_t *ws = static_cast<uint8_t *>(l.ws);

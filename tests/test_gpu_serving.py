@@ -409,10 +409,29 @@ def test_window_attn_strides_scale_and_workspace():
     check_window(q, k, v, out, 90, 3, scale=0.5)
 
 
-def test_window_attn_equals_causal_attention_under_a_long_window():
+def test_window_attn_is_causal_attention_under_a_long_window():
+    """Against the block-sparse attention without a mask; both are within their tolerance of the definition."""
     g = gen(12)
     q, k, v = rand(g, 1, 4, 900, 128), rand(g, 1, 2, 900, 128), rand(g, 1, 2, 900, 128)
-    assert torch.equal(fbs.window_attn(q, k, v, 900), fbs.block_sparse_attn(q, k, v, None, -math.inf, True))
+    check_window(q, k, v, fbs.window_attn(q, k, v, 900), 900, 0)
+    check_window(q, k, v, fbs.block_sparse_attn(q, k, v, None, -math.inf, True), 900, 0)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_window_attn_climbing_scores(d):
+    """Scores that climb by more than the rescaling threshold from block to block and within a step, so O, the row sum
+    and the P of a step's first columns are scaled down again and again; and a peak at the window's end."""
+    g = gen(15)
+    N = 700
+    u = torch.randn(d, generator=g, device="cuda")
+    u = u / u.norm()
+    ramp = torch.arange(N, device="cuda") // 32 * 0.6
+    q = (8.0 * u + 0.1 * torch.randn(1, 2, N, d, generator=g, device="cuda")).bfloat16()
+    k = (ramp[:, None] * u * math.sqrt(d) + 0.1 * torch.randn(1, 1, N, d, generator=g, device="cuda")).bfloat16()
+    v = rand(g, 1, 1, N, d)
+    check_window(q, k, v, fbs.window_attn(q, k, v, 300, 5), 300, 5)
+    k2 = k.flip(2).contiguous()
+    check_window(q, k2, v, fbs.window_attn(q, k2, v, 300, 5), 300, 5)
 
 
 # ------------------------------------------------------------------------------------------------- together
