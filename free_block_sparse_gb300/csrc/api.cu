@@ -472,13 +472,14 @@ int window_impl(const View &q, const View &k, const View &v, const View &o, int6
   }
   AttnLaunch l;
   memset(&l, 0, sizeof(l));
-  // the f16 copy of the V rows that are read: the first tokens' blocks and those from the first
-  // query's window on
+  // The f16 copy of the V rows that are read: the first tokens' blocks and those from the first query's
+  // window on.  Rows of these blocks that no query sees become zero, so leftovers there (NaN times a P of
+  // zero is NaN) reach nothing.
   const int64_t first = k.N - q.N - window + 1, lo = first > 0 ? first / KBLK * KBLK : 0;
   const int64_t ns = cdiv(sinks, KBLK) * KBLK;
-  cudaError_t e = launch_convert_v_f16(v, ws, nullptr, status_ptr(), s, lo, k.N);
+  cudaError_t e = launch_convert_v_f16(v, ws, nullptr, status_ptr(), s, lo, k.N, sinks, first);
   if (e == cudaSuccess && lo > 0 && ns > 0)
-    e = launch_convert_v_f16(v, ws, nullptr, status_ptr(), s, 0, ns < lo ? ns : lo);
+    e = launch_convert_v_f16(v, ws, nullptr, status_ptr(), s, 0, ns < lo ? ns : lo, sinks, first);
   if (e != cudaSuccess) return cuda_fail(e, "convert_v launch");
   View v16{ws, v.B, v.H, v.N, v.d, v.H * v.N * v.d, v.N * v.d, v.d};
   if ((rc = make_map(&l.tv, v16, 64, "v", CU_TENSOR_MAP_DATA_TYPE_FLOAT16))) return rc;

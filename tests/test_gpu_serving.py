@@ -472,6 +472,135 @@ def test_serving_steps_together(window, sinks):
     assert lens.tolist() == [25, 6, 13] and fbs.device_status() == 0
 
 
+def test_cache_attn_long_chunk_of_queries():
+    """Many row tiles: 1200 query rows per KV head, in tiles of 16."""
+    g = gen(16)
+    lens, d = [777, 300], 128
+    pool, table = filled(g, lens, 2, d, 32)
+    q = rand(g, 2, 8, 300, d)
+    out = fbs.cache4_attn(q, pool, table, torch.tensor(lens, dtype=torch.int32, device="cuda"), window=200, sinks=3)
+    check_cache_attn(q, pool, table, lens, out, d, 200, 3)
+
+
+def test_cache_attn_shared_pages_and_repeated_calls():
+    """Two sequences on the same pages (a shared prefix) and the same sequence twice; calls give the same bits each time."""
+    g = gen(17)
+    d = 64
+    pool, table = filled(g, [600], 2, d, 16)
+    table = table.expand(3, -1)
+    lens = [600, 333, 600]
+    q = rand(g, 1, 4, 1, d).expand(3, -1, -1, -1).contiguous()
+    kv = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    out = fbs.cache4_attn(q, pool, table.contiguous(), kv)
+    check_cache_attn(q, pool, table, lens, out, d)
+    # the cut into shares differs between the two, so their sums may round differently
+    assert (out[0].float() - out[2].float()).abs().max() <= 2.0 ** -7 * out[0].float().abs().max()
+    for _ in range(3):
+        assert torch.equal(fbs.cache4_attn(q, pool, table.contiguous(), kv), out)
+
+
+def test_pool_past_32_bits():
+    """Pages past 4 GiB of pool: stored, read back and attended to."""
+    g = gen(18)
+    d, page, H = 128, 256, 8
+    per = page * H * (d + d // 8)
+    pool = torch.empty((5 << 30) // per, H, page // 16, 18 * d, dtype=torch.uint8, device="cuda")
+    n = pool.shape[0]
+    assert n * per > 1 << 32
+    table = torch.tensor([[n - 1, 3, n - 2]], dtype=torch.int32, device="cuda")
+    k, v = rand(g, 1, H, 600, d), rand(g, 1, H, 600, d)
+    t = torch.arange(600, device="cuda")
+    slots = (table[0].long()[t // page] * page + t % page)[None].contiguous()
+    fbs.cache4_store(k, v, slots, pool)
+    a, b = fbs.cache4_load(pool, slots)
+    assert torch.equal(a, R.dequantise(*R.quantise(k.double())).float().bfloat16())
+    q = rand(g, 1, 16, 1, d)
+    out = fbs.cache4_attn(q, pool, table, torch.tensor([600], dtype=torch.int32, device="cuda"))
+    kk, vv = (R.dequantise(*R.quantise(x.double()))[0] for x in (k, v))
+    o, _, x = R.attention(q[0].double(), kk, vv, torch.tensor([599], device="cuda"), 0, 0, d ** -0.5)
+    within(out[0], o, 2.0 ** -8 * o.abs() + 2 * (2.0 ** -11 + 2.0 ** -16 * x + 2.0 ** -20) * 2 * vv.abs().amax())
+    assert fbs.device_status() == 0
+
+
+def test_calls_on_two_streams_at_once():
+    g = gen(19)
+    d = 128
+    pools = [filled(g, [3000 + 100 * i, 70], 2, d, 64) for i in range(2)]
+    qs = [rand(g, 2, 8, 1, d) for _ in range(2)]
+    kv = [torch.tensor([3000 + 100 * i, 70], dtype=torch.int32, device="cuda") for i in range(2)]
+    kw, qw = rand(g, 1, 2, 5000, d), rand(g, 1, 8, 1, d)
+    want = [fbs.cache4_attn(q, p, t, n) for q, (p, t), n in zip(qs, pools, kv)]
+    want_w = fbs.window_attn(qw, kw, kw, 3000, 4)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append((fbs.cache4_attn(qs[i], *pools[i], kv[i]), fbs.window_attn(qw, kw, kw, 3000, 4)))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for a, w in got[i]:
+            assert torch.equal(a, want[i]) and torch.equal(w, want_w)
+
+
+@pytest.mark.parametrize("Nq", [1, 3, 200])
+def test_window_attn_ignores_keys_that_no_query_sees(Nq):
+    """NaN and infinities in keys and values in front of the window (a ring buffer's leftovers) change nothing."""
+    g = gen(20)
+    q, k, v = rand(g, 1, 4, Nq, 64), rand(g, 1, 2, 1000, 64), rand(g, 1, 2, 1000, 64)
+    good = fbs.window_attn(q, k, v, 333, 5)
+    k2, v2 = k.clone(), v.clone()
+    k2[:, :, 5:1000 - Nq - 333 + 1] = math.nan
+    v2[:, :, 5:1000 - Nq - 333 + 1] = math.inf
+    v2[:, :, 7] = v2[:, :, 1000 - Nq - 333] = math.nan
+    assert torch.equal(fbs.window_attn(q, k2, v2, 333, 5), good)
+
+
+def test_empty_calls():
+    e = lambda *s: torch.empty(*s, dtype=torch.bfloat16, device="cuda")  # noqa: E731
+    i32 = lambda *s: torch.empty(*s, dtype=torch.int32, device="cuda")  # noqa: E731
+    pool = fbs.cache4_pool(2, 16, 2, 64)
+    assert fbs.cache4_attn(e(0, 4, 1, 64), pool, i32(0, 3), i32(0)).shape == (0, 4, 1, 64)
+    assert fbs.cache4_attn(e(2, 4, 0, 64), pool, i32(2, 3), i32(2)).shape == (2, 4, 0, 64)
+    assert (fbs.cache4_attn(torch.ones_like(e(2, 4, 1, 64)), pool, i32(2, 0), torch.full((2,), 9, dtype=torch.int32, device="cuda")) == 0).all()
+    assert fbs.window_attn(e(1, 4, 0, 64), e(1, 2, 5, 64), e(1, 2, 5, 64), 3).shape == (1, 4, 0, 64)
+    a, b = fbs.qk_norm_rope(e(2, 4, 0, 64), e(2, 2, 0, 64), fbs.rope_freqs(64))
+    assert a.shape == (2, 4, 0, 64) and b.shape == (2, 2, 0, 64)
+    fbs.cache4_store(e(2, 2, 0, 64), e(2, 2, 0, 64), torch.empty(2, 0, dtype=torch.int64, device="cuda"), pool)
+    assert fbs.cache4_load(pool, torch.empty(2, 0, dtype=torch.int64, device="cuda"))[0].shape == (2, 2, 0, 64)
+    slots, pos, kv, used = fbs.cache_tables(i32(0), i32(0), i32(0), i32(0, 3), 16, 4)
+    assert slots.shape == (0, 4) and int(used) == 0
+    torch.cuda.synchronize()
+    assert fbs.device_status() == 0
+
+
+def test_calls_refuse_what_they_cannot_take():
+    g = gen(21)
+    q, k = rand(g, 1, 4, 8, 64), rand(g, 1, 2, 8, 64)
+    pool = fbs.cache4_pool(4, 16, 2, 64)
+    slots = torch.zeros(1, 8, dtype=torch.int64, device="cuda")
+    table, kv = torch.zeros(1, 2, dtype=torch.int32, device="cuda"), torch.ones(1, dtype=torch.int32, device="cuda")
+    for call, err in ((lambda: fbs.window_attn(q.float(), k, k, 4), TypeError), (lambda: fbs.window_attn(q, k.cpu(), k, 4), ValueError),
+                      (lambda: fbs.window_attn(q, k, k, 0), fbs.SpargeError), (lambda: fbs.window_attn(q.transpose(2, 3), k, k, 4), TypeError),
+                      (lambda: fbs.window_attn(q, k, k, 4, ws=torch.empty(16, dtype=torch.uint8, device="cuda")), fbs.SpargeError),
+                      (lambda: fbs.qk_norm_rope(q, k, fbs.rope_freqs(64).float()), TypeError),
+                      (lambda: fbs.qk_norm_rope(q, k, fbs.rope_freqs(64), positions=torch.zeros(8, dtype=torch.int32, device="cuda")), TypeError),
+                      (lambda: fbs.qk_norm_rope(q, k, fbs.rope_freqs(64), q_weight=torch.ones(32, device="cuda")), TypeError),
+                      (lambda: fbs.qk_norm_rope(q, k, fbs.rope_freqs(24)), fbs.SpargeError),
+                      (lambda: fbs.cache4_store(k, k, slots.int(), pool), TypeError), (lambda: fbs.cache4_store(k, k, slots[:, :7], pool), TypeError),
+                      (lambda: fbs.cache4_store(q, q, slots, pool), fbs.SpargeError), (lambda: fbs.cache4_store(k, k, slots, pool[..., :100]), TypeError),
+                      (lambda: fbs.cache4_load(pool, slots, k_out=k), ValueError),
+                      (lambda: fbs.cache4_attn(q, pool, table.long(), kv), TypeError), (lambda: fbs.cache4_attn(q, pool, table, kv.long()), TypeError),
+                      (lambda: fbs.cache4_attn(q, pool, table.expand(2, -1), kv), TypeError),
+                      (lambda: fbs.cache4_attn(q, pool, table, kv, sinks=3), fbs.SpargeError),
+                      (lambda: fbs.cache_tables(kv, kv, kv, table, 16, -1), ValueError), (lambda: fbs.cache_tables(kv, kv.cpu(), kv, table, 16, 1), ValueError),
+                      (lambda: fbs.cache_tables(kv, kv, kv, table, 24, 1), fbs.SpargeError), (lambda: fbs.cache4_pool(4, 20, 2, 64), ValueError)):
+        with pytest.raises(err):
+            call()
+    assert fbs.device_status() == 0
+
+
 def test_a_captured_step_replays():
     """Store and attention of a step captured into a graph, replayed on new inputs in place, on a stream of its own."""
     g = gen(14)

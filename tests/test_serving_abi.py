@@ -150,3 +150,18 @@ def test_cache4_struct_layout(tmp_path):
     got = [int(x) for x in subprocess.run([str(exe)], capture_output=True, text=True, check=True).stdout.split()]
     C = fbs.sparge_cache4
     assert got == [ctypes.sizeof(C), C.n_pages.offset, C.page_size.offset, C.H.offset, C.d.offset]
+
+
+def test_binding_refuses_host_tensors(lib):
+    """The Python calls take CUDA tensors alone and say so, without a GPU as well."""
+    torch = pytest.importorskip("torch")
+    t4 = torch.zeros(1, 1, 1, 64, dtype=torch.bfloat16)
+    i = torch.zeros(1, dtype=torch.int32)
+    for call in (lambda: fbs.window_attn(t4, t4, t4, 1), lambda: fbs.qk_norm_rope(t4, t4), lambda: fbs.cache4_store(t4, t4, i, i),
+                 lambda: fbs.cache4_load(t4, i), lambda: fbs.cache4_attn(t4, t4, i, i), lambda: fbs.cache_tables(i, i, i, i, 16, 1)):
+        with pytest.raises(ValueError):
+            call()
+    with pytest.raises(TypeError):
+        fbs.window_attn(1, t4, t4, 1)
+    with pytest.raises(TypeError):
+        fbs._load_binding().cache4_store(t4)
