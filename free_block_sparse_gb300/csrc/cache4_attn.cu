@@ -20,8 +20,8 @@
 // of two that follows its running maximum the same way, so P s stays in f16's range.
 //
 // Work: the (sequence, KV head, row tile) items' tiles in one line, cut into equal shares, one per CTA
-// (4 CTAs per SM, 3 with 16-row tiles), so ragged lengths fill the part evenly; every warp sums the lengths
-// itself.  A warp takes every fourth step of its CTA's share (two 16-token records, one with 16 rows of d = 128)
+// (2 to 4 CTAs per SM), so ragged lengths fill the part evenly; every warp sums the lengths
+// itself.  A warp takes every fourth step of its CTA's share (two 16-token records)
 // through a ring of its own of bulk copies, without any synchronisation among warps until an item
 // ends; then the four warps' sums are merged in shared memory, and an item cut between CTAs is put
 // together by a second kernel (rowsplit.cuh).
@@ -82,14 +82,18 @@ __device__ __forceinline__ Span span_of(const CacheAttnArgs &a, int b) {
   s.recs = s.ns + hi - s.lo;
   return s;
 }
-// Shared memory and the step of a warp: U records at a time (one after another in a CTA's tile of
-// 4 U records), ST steps in a warp's ring.  With 8 rows two records a step keep two chains of dependent
-// products in flight and halve the waits, votes and branches per record; with 16 rows a record already
-// has two of everything and the registers of a second do not fit (d = 128).
+// CTAs per SM, by registers: the sums of 16 rows of 128 channels alone take 64 per thread.  (16 rows of
+// d = 128, 4 queries of 128 sequences of 4100: 2 CTAs 93 us, 3 with one record a step and spills 113; d = 64: 3 CTAs
+// 56 us, 2 65.)
+constexpr int ca_ctas(int D, int RT) { return RT == 1 ? 4 : D == 64 ? 3 : 2; }
+
+// Shared memory and the step of a warp: U = 2 records at a time (a CTA's tile is 4 U records, one step of each
+// warp), which keeps two chains of dependent products in flight and halves the waits, votes and
+// branches per record; ST steps in a warp's ring.
 template <int D, int RT>
 struct CaSmem {
-  static constexpr int U = RT == 1 || D == 64 ? 2 : 1;
-  static constexpr int ST = D == 64 ? 5 : 6 / U;
+  static constexpr int U = 2;
+  static constexpr int ST = D == 64 ? 5 : 3;
   static constexpr int REC = Rec4<D>::BYTES;
   static constexpr int WRING = ST * U * REC;  // of one warp; the item's sums go there at its end
   static constexpr int OROW = D + 4;          // floats of a row of sums, padded against bank conflicts
@@ -168,7 +172,7 @@ __device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) 
 __device__ __forceinline__ int exponent_of(float x) { return static_cast<int>((__float_as_uint(x) >> 23) & 0xFFu) - 127; }
 
 template <int D, int RT>
-__global__ void __launch_bounds__(CA_WARPS * 32, RT == 1 ? 4 : 3) cache4_attn_kernel(const CacheAttnArgs a) {
+__global__ void __launch_bounds__(CA_WARPS * 32, ca_ctas(D, RT)) cache4_attn_kernel(const CacheAttnArgs a) {
   using S = CaSmem<D, RT>;
   using R = Rec4<D>;
   constexpr int NG = D / 64, NW = D / 32, MT = D / 16, U = S::U, ST = S::ST;
@@ -651,12 +655,9 @@ __global__ void __launch_bounds__(CA_WARPS * 32, RT == 1 ? 4 : 3) cache4_attn_ke
   }
 }
 
-// A CTA of 16-row tiles holds twice the sums in registers (3 CTAs per SM instead of 4) and reads the
-// cache half as often.
-int max_ctas(int rt) { return CA_SMS * (rt == 1 ? 4 : 3); }
 SplitWs ws_layout(int64_t B, int64_t Hkv, int64_t rows, int64_t d) {
   const int rt = row_tile(rows);
-  return split_ws(B * Hkv * ((rows + 8 * rt - 1) / (8 * rt)), max_ctas(rt), rt, d);
+  return split_ws(B * Hkv * ((rows + 8 * rt - 1) / (8 * rt)), CA_SMS * ca_ctas(static_cast<int>(d), rt), rt, d);
 }
 
 template <int D, int RT>
@@ -664,7 +665,7 @@ cudaError_t launch_cache_attn(const CacheAttnArgs &a, int64_t tiles, cudaStream_
   using S = CaSmem<D, RT>;
   static std::atomic<unsigned long long> smem_set{0};
   if (cudaError_t e = set_smem_limit_once(cache4_attn_kernel<D, RT>, S::TOTAL, smem_set); e != cudaSuccess) return e;
-  const int64_t most = max_ctas(RT), ctas = tiles < most ? tiles : most;
+  const int64_t most = CA_SMS * ca_ctas(D, RT), ctas = tiles < most ? tiles : most;
   if (cudaError_t e = launch_dependent(cache4_attn_kernel<D, RT>, dim3(static_cast<unsigned>(ctas)), CA_WARPS * 32, S::TOTAL, st, a);
       e != cudaSuccess)
     return e;
@@ -737,7 +738,7 @@ int sparge_cache4_attn(const sparge_tensor *q, const sparge_cache4 *cache, const
     const int64_t most = (window + qv.N + 15) / 16 + 1 + (sinks + 15) / 16;
     recs = recs < most ? recs : most;
   }
-  const int64_t step = qv.d == 64 || rt == 1 ? 8 : 4;  // records of a CTA's tile
+  const int64_t step = 4 * CaSmem<128, 1>::U;  // records of a CTA's tile
   const int64_t tiles = ((recs + step - 1) / step + CA_ITEM) * qv.B * c.H * ntile;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e;
