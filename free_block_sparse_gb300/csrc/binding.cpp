@@ -2,7 +2,7 @@
 // pointers, sizes and strides, the current stream and device straight from torch, makes the outputs
 // that are not given, and calls the C entries of libsparge.so.  Nothing is computed here.  Through
 // ctypes the same calls spend 17 to 34 us on the host, about twice what their kernels take at
-// decoding sizes; here 6 to 9 us.
+// decoding sizes; here 4 to 8 us.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 

@@ -221,8 +221,8 @@ __global__ void __launch_bounds__(256) rows4_kernel(const Rows4 a) {
 // chunks up; slots that do not run on are still handled, token by token).  A whole record is put
 // together or taken apart in shared memory and moved in 16-byte pieces; single tokens go straight
 // to the cache's bytes.
-// Measured, 4 x 8192 tokens of 8 heads, d = 128, K and V stored and read back: 68 us for 344 MB, 75% of the
-// measured copy rate (store 42 us, load 27): the store is bound by its arithmetic (17 instructions per value),
+// Measured, 4 x 8192 tokens of 8 heads, d = 128, K and V stored and read back: 69 us for 344 MB, 74% of the
+// measured copy rate (cold: store 43 us, load 38): the store is bound by its arithmetic (16 instructions per value),
 // the load by the latency of its two steps.
 constexpr int R4_HEADS = 8;  // most heads of a CTA (8 heads: 68 us, 4: 70, 2: 79)
 template <int D, bool LOAD>

@@ -1,7 +1,8 @@
-// Decoding steps under a sliding window with a few first tokens: up to 16 query rows per KV head (the Nq
-// queries of its G heads) against contiguous bf16 keys and values.
+// Decoding steps and short chunks under a sliding window with a few first tokens: up to WINDOW_DECODE_ROWS query
+// rows per KV head (the Nq queries of its G heads), in tiles of 8 or 16, against contiguous bf16 keys and values.
 //
-// Bound by memory: every visible key and value is read once, 4 d bytes per token and KV head.  A 128-row
+// Bound by memory: a tile reads every visible key and value once, 4 d bytes per token and KV head (the tiles of
+// one KV head side by side, from L2).  A 128-row
 // tensor-core tile would be almost empty here and its softmax would still be done for all its rows, so the
 // rows are the narrow side of mma.sync products (n = 8):
 //   S^T = K Q^T: A = 16 tokens x 16 channels by ldmatrix, B = Q^T held in registers;
