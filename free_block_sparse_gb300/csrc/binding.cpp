@@ -122,6 +122,15 @@ struct Here {
   at::Tensor make(at::IntArrayRef shape, at::ScalarType type) const {
     return at::Tensor(at::detail::empty_cuda(shape, type, at::Device(at::kCUDA, static_cast<c10::DeviceIndex>(dev)), std::nullopt));
   }
+  // a tensor of its own over a part of block's memory, `at` bytes in (several small outputs in one allocation)
+  static at::Tensor part(const at::Tensor &block, int64_t at, at::IntArrayRef shape, at::ScalarType type) {
+    at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(block.storage()), block.key_set(),
+                                                            c10::scalarTypeToTypeMeta(type));
+    c10::TensorImpl *i = t.unsafeGetTensorImpl();
+    i->set_sizes_contiguous(shape);
+    i->set_storage_offset(at / static_cast<int64_t>(c10::elementSize(type)));
+    return t;
+  }
   // like t: its strides where they leave no gaps, else contiguous
   at::Tensor make_like(const at::Tensor &t) const {
     if (t.is_contiguous() || !t.is_non_overlapping_and_dense()) return make(t.sizes(), t.scalar_type());
@@ -217,14 +226,17 @@ PyObject *cache_tables(const Args &a) {
                    &table = a.tensor(3, "table");
   const Here h(lens, "lens");
   const int64_t R = lens.numel(), N = a.integer(5);
-  if (N < 0) {
-    PyErr_SetString(PyExc_ValueError, "N must not be negative");
+  if (N < 0 || N > (int64_t(1) << 30) || R > 65535) {
+    PyErr_SetString(PyExc_ValueError, "N must be in 0..2^30, the requests at most 65535");
     throw PyFail{};
   }
-  const at::Tensor slots = a.none(6) ? h.make({R, N}, at::kLong) : a.tensor(6, "slots");
-  const at::Tensor pos = a.none(7) ? h.make({R, N}, at::kInt) : a.tensor(7, "positions");
-  const at::Tensor kv = a.none(8) ? h.make({R}, at::kInt) : a.tensor(8, "kv_lens");
-  const at::Tensor used = a.none(9) ? h.make({1}, at::kInt) : a.tensor(9, "used");
+  // the outputs that are not given share one allocation (four of them take the host longer than the kernel the GPU)
+  at::Tensor block;
+  if (a.none(6) || a.none(7) || a.none(8) || a.none(9)) block = h.make({12 * R * N + 4 * R + 4}, at::kByte);
+  const at::Tensor slots = a.none(6) ? Here::part(block, 0, {R, N}, at::kLong) : a.tensor(6, "slots");
+  const at::Tensor pos = a.none(7) ? Here::part(block, 8 * R * N, {R, N}, at::kInt) : a.tensor(7, "positions");
+  const at::Tensor kv = a.none(8) ? Here::part(block, 12 * R * N, {R}, at::kInt) : a.tensor(8, "kv_lens");
+  const at::Tensor used = a.none(9) ? Here::part(block, 12 * R * N + 4 * R, {1}, at::kInt) : a.tensor(9, "used");
   const auto i32 = [&](const at::Tensor &t, const char *name, at::IntArrayRef shape) {
     return static_cast<int32_t *>(h.array(t, at::kInt, name, shape));
   };

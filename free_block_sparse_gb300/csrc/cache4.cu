@@ -534,6 +534,8 @@ int sparge_cache_tables(const int32_t *lens, const int32_t *new_lens, int64_t R,
   if (R > 65535 || N > (int64_t(1) << 30) || width > INT32_MAX || n_free > INT32_MAX)
     return fail(SPARGE_ERR_UNSUPPORTED, "shape too large");
   if (R > 0 && (!lens || !new_lens)) return fail(SPARGE_ERR_INVALID_ARG, "lens or new_lens is NULL");
+  if (R > 0 && kv_lens && (kv_lens == lens || kv_lens == new_lens))
+    return fail(SPARGE_ERR_INVALID_ARG, "kv_lens must not be lens or new_lens (every CTA reads them all)");
   if (R > 0 && width > 0 && !table) return fail(SPARGE_ERR_INVALID_ARG, "table is NULL");
   if (n_free > 0 && !free_pages) return fail(SPARGE_ERR_INVALID_ARG, "free_pages is NULL");
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);

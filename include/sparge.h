@@ -343,7 +343,8 @@ size_t sparge_cache4_bytes(int64_t n_pages, int page_size, int H, int d);
  * four may be NULL.  A token gets slot -1 and a table entry -1 where free_pages is used up (used then
  * says more than n_free), and slot -1 where its page lies past width.  A request with a negative
  * length, new_lens[r] > N or a total past 2^31 - 1 gets no tokens and length 0; that and a table too narrow record SPARGE_ERR_INVALID_ARG in
- * the device status word.  R <= 65535.  The arrays must not overlap.
+ * the device status word.  R <= 65535.  The arrays must not overlap (kv_lens as
+ * lens or new_lens is refused).
  */
 int sparge_cache_tables(const int32_t *lens, const int32_t *new_lens, int64_t R, int64_t N, int page_size,
                         const int32_t *free_pages, int64_t n_free, int32_t *table, int64_t width, int64_t table_stride,
@@ -352,7 +353,8 @@ int sparge_cache_tables(const int32_t *lens, const int32_t *new_lens, int64_t R,
 /*
  * Stores tokens in the cache: row (b, h, n) of k and v (B,H,N,d) goes to slot slots[b][n] ((B,N) int64,
  * contiguous) of head h.  scale = bf16((max - minimum) / 15), n = round-to-even((x - minimum) / scale); a
- * group that holds an infinity or a NaN reads back as NaN.  A negative slot leaves its token out; a slot past
+ * group that holds an infinity or a NaN reads back as NaN (and values past 2^100 can overflow in
+ * sparge_cache4_attn, as can |q| past 2^117).  A negative slot leaves its token out; a slot past
  * the pool is left out and records SPARGE_ERR_INVALID_ARG in the device status word.  Slots must
  * differ from one another (of equal ones each byte holds one of them).
  * sparge_cache4_load reads the same rows back as bf16, for instance all tokens of a sequence for sparge_attn

@@ -601,6 +601,68 @@ def test_calls_refuse_what_they_cannot_take():
     assert fbs.device_status() == 0
 
 
+def test_tables_outputs_stand_apart():
+    """Outputs that the call makes hold their own values, mixed with given ones too."""
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    want = ([[-1, 5 * 16], [7 * 16, 7 * 16 + 1]], [[-1, 16], [0, 1]], [17, 2], [2])
+    for given in ((), (0,), (1, 3), (2,)):
+        out = [torch.empty(2, 2, dtype=torch.int64, device="cuda"), i32(0, 0, 0, 0).view(2, 2), i32(0, 0), i32(0)]
+        table = i32(3, -9, -9, -9).view(2, 2)
+        got = fbs.cache_tables(i32(16, 0), i32(1, 2), i32(5, 7), table, 16, 2, *[o if i in given else None for i, o in enumerate(out)])
+        assert tuple(x.tolist() for x in got) == want and table.tolist() == [[3, 5], [7, -9]]
+        assert all(got[i] is out[i] for i in given)
+        for i, x in enumerate(got):  # writing one changes no other
+            x.fill_(-77)
+            assert all(y.tolist() == want[j] for j, y in enumerate(got) if j > i)
+
+
+def test_capture_over_two_streams():
+    """Calls on a side stream that forks off the captured one and joins it again, behind kernels, copies and events: the
+    graph's replays give what the calls give one after another."""
+    g = gen(22)
+    d = 64
+    pool, table = filled(g, [500, 77], 2, d, 16)
+    kv = torch.tensor([500, 77], dtype=torch.int32, device="cuda")
+    q, k = rand(g, 2, 4, 1, d), rand(g, 2, 2, 1, d)
+    src = rand(g, 2, 4, 1, d)
+    freq = fbs.rope_freqs(d)
+
+    def step(s, side):
+        q.copy_(src)
+        side.wait_stream(s)
+        with torch.cuda.stream(side):
+            n0, _ = fbs.qk_norm_rope(q, k, freq, start=7)
+            o0 = fbs.cache4_attn(n0, pool, table, kv)
+        n1, _ = fbs.qk_norm_rope(q, k, freq, start=9)
+        o1 = fbs.cache4_attn(n1, pool, table, kv, window=50, sinks=2)
+        s.wait_stream(side)
+        n2, _ = fbs.qk_norm_rope(o0, k, freq)
+        return o0, o1, fbs.cache4_attn(n2 + o1, pool, table, kv)
+
+    s, side = torch.cuda.Stream(), torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step(s, side)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            out = step(s, side)
+    torch.cuda.synchronize()
+    for _ in range(5):
+        src.copy_(rand(g, 2, 4, 1, d))
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        a = []
+        n0, _ = fbs.qk_norm_rope(src, k, freq, start=7)
+        a.append(fbs.cache4_attn(n0, pool, table, kv))
+        n1, _ = fbs.qk_norm_rope(src, k, freq, start=9)
+        a.append(fbs.cache4_attn(n1, pool, table, kv, window=50, sinks=2))
+        n2, _ = fbs.qk_norm_rope(a[0], k, freq)
+        a.append(fbs.cache4_attn(n2 + a[1], pool, table, kv))
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(a, out))
+
+
 def test_a_captured_step_replays():
     """Store and attention of a step captured into a graph, replayed on new inputs in place, on a stream of its own."""
     g = gen(14)

@@ -67,6 +67,13 @@ def test_cache_tables_refuses(lib, change, code):
                                          a["width"], a["stride"], PTR, PTR, PTR, PTR, None), code)
 
 
+@pytest.mark.parametrize("lens,new,kv", [(PTR, 2 * PTR, PTR), (2 * PTR, PTR, PTR)])
+def test_cache_tables_refuses_lengths_in_place(lib, lens, new, kv):
+    """Every CTA reads the lengths of the requests in front of its own: none may be overwritten meanwhile."""
+    refused(lib, lib.sparge_cache_tables(lens, new, 3, 2, 64, 4 * PTR, 5, 5 * PTR, 8, 8, 6 * PTR, 7 * PTR, kv, 8 * PTR, None), BAD)
+    assert b"kv_lens" in lib.sparge_last_error()
+
+
 @pytest.mark.parametrize("load", [False, True])
 @pytest.mark.parametrize("change,code", [
     (dict(c=None), BAD), (dict(c=pool(H=3)), BAD), (dict(c=pool(d=64)), BAD), (dict(c=pool(d=96)), UNSUP),
