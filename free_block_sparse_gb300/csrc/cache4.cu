@@ -29,7 +29,7 @@ struct Rows4 {  // K and V rows and the cache they go to or come from
   int64_t n_slots;
   int page_shift, H, N, B, recs;  // recs: records of a page
   int zero;                       // load: rows of left-out slots become zero
-  int per;                        // heads of a CTA
+  int wide;                       // every row's 16-channel pieces are 32-byte aligned
   int *status;
 };
 
@@ -50,27 +50,89 @@ __device__ __forceinline__ uint32_t max2_nan(uint32_t a, uint32_t b) {
   return r;
 }
 
-// Codes of a thread's 8 channels (nibble j: channel j) and its group's word; the 8 threads of a
+// 16 channels of a row, 32 bytes: in one piece where the rows allow it (a warp's accesses then fill whole sectors).
+__device__ __forceinline__ void load16(const __nv_bfloat16 *p, bool wide, uint32_t (&u)[8]) {
+  if (wide) {
+    asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7])
+                 : "l"(p));
+  } else {
+    const uint4 a = __ldg(reinterpret_cast<const uint4 *>(p)), b = __ldg(reinterpret_cast<const uint4 *>(p) + 1);
+    u[0] = a.x; u[1] = a.y; u[2] = a.z; u[3] = a.w;
+    u[4] = b.x; u[5] = b.y; u[6] = b.z; u[7] = b.w;
+  }
+}
+__device__ __forceinline__ void store16(__nv_bfloat16 *p, bool wide, const uint32_t (&u)[8]) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]),
+                 "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7])
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4 *>(p)[0] = make_uint4(u[0], u[1], u[2], u[3]);
+    reinterpret_cast<uint4 *>(p)[1] = make_uint4(u[4], u[5], u[6], u[7]);
+  }
+}
+
+// Four words of four bytes as their transpose: z[b] holds byte b of a, b, c, d.
+__device__ __forceinline__ void transpose_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d, uint32_t (&z)[4]) {
+  const uint32_t x0 = __byte_perm(a, b, 0x5140), x1 = __byte_perm(a, b, 0x7362);
+  const uint32_t y0 = __byte_perm(c, d, 0x5140), y1 = __byte_perm(c, d, 0x7362);
+  z[0] = __byte_perm(x0, y0, 0x5410);
+  z[1] = __byte_perm(x0, y0, 0x7632);
+  z[2] = __byte_perm(x1, y1, 0x5410);
+  z[3] = __byte_perm(x1, y1, 0x7632);
+}
+
+// Place of channel ch's code among the 16 of a thread, 4 bits each: K in order; V, whose bytes hold channels g and
+// g + 8, at byte g.
+__device__ __forceinline__ constexpr int nibble_of(bool v, int ch) { return v ? 2 * (ch & 7) + (ch >> 3) : ch; }
+
+// The groups that quantise16 leaves: no range, one past fp32's middle, an infinity or a NaN.  Codes in x and y; the
+// word is z with the minimum's bits under the mask w.  (Out of line: the callers' loops hold the other case eight times.)
+template <bool V>
+__device__ __noinline__ uint4 quantise_rest(uint4 a, uint4 b, float lo, float hi) {
+  if (!(fabsf(lo) <= 3.4028235e38f && fabsf(hi) <= 3.4028235e38f)) return make_uint4(0u, 0u, 0x7FC07FC0u, 0u);
+  // a difference beyond fp32 (bf16 values near 3e38 of both signs) is held at the largest fp32
+  const uint32_t sbits = pack_bf16x2(__fdiv_rn(fminf(hi - lo, 3.4028235e38f), 15.f), 0.f) & 0xFFFFu;
+  const float s = __uint_as_float(sbits << 16);
+  uint32_t n[2] = {0u, 0u};
+  if (s > 0.f) {
+    const uint32_t u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int ch = 0; ch < 16; ++ch) {
+      const float f = ((ch & 1) ? bf16hi(u[ch / 2]) : bf16lo(u[ch / 2])) - lo;
+      const int at = nibble_of(V, ch);
+      n[at / 8] |= static_cast<uint32_t>(min(max(__float2int_rn(fminf(__fdiv_rn(f, s), 15.f)), 0), 15)) << (4 * (at % 8));
+    }
+  }
+  return make_uint4(n[0], n[1], sbits, 0xFFFF0000u);
+}
+
+// Codes of a thread's 16 channels (n[0]: nibbles 0 - 7, n[1]: 8 - 15) and its group's word; the 4 threads of a
 // group are adjacent lanes.  Minimum and maximum are taken on packed bf16 pairs, NaN winning, then
-// together as the maximum of (max, -min), so three shuffles serve both and one test of the two
+// together as the maximum of (max, -min), so two shuffles serve both and one test of the two
 // finds an infinity or a NaN anywhere in the group.
-__device__ __forceinline__ uint32_t quantise8(uint4 v, uint32_t &word) {
-  uint32_t lo2 = min2_nan(min2_nan(v.x, v.y), min2_nan(v.z, v.w));
-  uint32_t hi2 = max2_nan(max2_nan(v.x, v.y), max2_nan(v.z, v.w));
+template <bool V>
+__device__ __forceinline__ uint32_t quantise16(const uint32_t (&u)[8], uint32_t (&n)[2]) {
+  uint32_t lo2 = u[0], hi2 = u[0];
+#pragma unroll
+  for (int j = 1; j < 8; ++j) {
+    lo2 = min2_nan(lo2, u[j]);
+    hi2 = max2_nan(hi2, u[j]);
+  }
   lo2 = min2_nan(lo2, lo2 >> 16);
   hi2 = max2_nan(hi2, hi2 >> 16);
   uint32_t m = __byte_perm(hi2, lo2, 0x5410) ^ 0x80000000u;  // max, -min
 #pragma unroll
-  for (int off = 4; off > 0; off >>= 1) m = max2_nan(m, __shfl_xor_sync(0xffffffffu, m, off));
+  for (int off = 2; off > 0; off >>= 1) m = max2_nan(m, __shfl_xor_sync(0xffffffffu, m, off));
   m ^= 0x80000000u;
   const float lo = bf16hi(m), hi = bf16lo(m);
   const float range = hi - lo;  // an infinity or a NaN if there is one in the group
-  const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-  uint32_t n = 0u;
+  n[0] = n[1] = 0u;
   if (range >= 1e-28f && range < 1e38f) {
     // A quotient from the reciprocal and one correction is the correctly rounded one, or where the quotient
-    // is representable (a tie of codes is) exactly it.  scale = range / 15 to bf16; adding 1.5 * 2^23 to (x - lo) / scale rounds it to even and leaves it in the
-    // sum's low bits (at most 15 (1 + 2^-8): no code passes 15).
+    // is representable (a tie of codes is) exactly it.  scale = range / 15 to bf16; adding 1.5 * 2^23 to
+    // (x - lo) / scale rounds it to even and leaves it in the sum's low bits (at most 15 (1 + 2^-8): no code passes 15).
     constexpr float MAGIC = 12582912.f;
     constexpr uint32_t MAGIC_BITS = 0x4B400000u;
     constexpr float R15 = 1.f / 15.f;
@@ -79,99 +141,91 @@ __device__ __forceinline__ uint32_t quantise8(uint4 v, uint32_t &word) {
     const float s = __uint_as_float(sbits << 16);
     float r1;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r1) : "f"(s));  // the correction makes up for its last bit
-    word = sbits | (m & 0xFFFF0000u);
     const float2 r = make_float2(r1, r1), ns = make_float2(-s, -s), nl = make_float2(-lo, -lo);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < 8; ++j) {
       const float2 f = fadd2(make_float2(bf16lo(u[j]), bf16hi(u[j])), nl);
       float2 q = fmul2(f, r);
       q = ffma2(ffma2(q, ns, f), r, q);
       const float2 t = fadd2(q, make_float2(MAGIC, MAGIC));
-      n += (__float_as_uint(t.x) << (8 * j)) + (__float_as_uint(t.y) << (8 * j + 4));
+      const int a = nibble_of(V, 2 * j), b = nibble_of(V, 2 * j + 1);
+      n[a / 8] += __float_as_uint(t.x) << (4 * (a % 8));
+      n[b / 8] += __float_as_uint(t.y) << (4 * (b % 8));
     }
     uint32_t magic = 0u;
 #pragma unroll
     for (int j = 0; j < 8; ++j) magic += MAGIC_BITS << (4 * j);
-    return n - magic;
+    n[0] -= magic;
+    n[1] -= magic;
+    return sbits | (m & 0xFFFF0000u);
   }
-  if (!(fabsf(lo) <= 3.4028235e38f && fabsf(hi) <= 3.4028235e38f)) {
-    word = 0x7FC07FC0u;
-    return 0u;
-  }
-  // a difference beyond fp32 (bf16 values near 3e38 of both signs) is held at the largest fp32
-  const uint32_t sbits = pack_bf16x2(__fdiv_rn(fminf(range, 3.4028235e38f), 15.f), 0.f) & 0xFFFFu;
-  const float s = __uint_as_float(sbits << 16);
-  word = sbits | (m & 0xFFFF0000u);
-  if (!(s > 0.f)) return n;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const float f = ((j & 1) ? bf16hi(u[j / 2]) : bf16lo(u[j / 2])) - lo;
-    n |= static_cast<uint32_t>(min(max(__float2int_rn(fminf(__fdiv_rn(f, s), 15.f)), 0), 15)) << (4 * j);
-  }
-  return n;
+  const uint4 r = quantise_rest<V>(make_uint4(u[0], u[1], u[2], u[3]), make_uint4(u[4], u[5], u[6], u[7]), lo, hi);
+  n[0] = r.x;
+  n[1] = r.y;
+  return r.z | (m & r.w);
 }
 
-// Byte of V codes that holds channels 16 (i / 2) + g (low) and + 8 (high) of token t, i = channel / 8.
-__device__ __forceinline__ int v_byte(int t, int i, int g) {
-  const int u = i >> 1;
-  return (u >> 2) * 512 + (4 * g + ((t & 7) >> 1)) * 16 + (u & 3) * 4 + ((t & 1) << 1) + (t >> 3);
-}
-
-// Writes a thread's 8 channels (piece i of token t's row) of K or V into a record, in global or
-// shared memory.  Called by all threads of a row together (V bytes join two threads' nibbles).
+// A thread's 16 channels (piece i of the row) inside a record.  K codes: two words, bytes k_at and k_at + D/8 of the
+// token's.  V codes: byte v_at + 64 g holds channels g (low) and g + 8 (high).
 template <int D>
-__device__ __forceinline__ void put8(uint8_t *rec, bool v, int t, int i, uint32_t n, uint32_t word, bool live) {
-  using R = Rec4<D>;
-  const uint32_t other = __shfl_xor_sync(0xffffffffu, n, 1);
-  if (!live) return;
-  if (!v) {
-    *reinterpret_cast<uint32_t *>(rec + R::K + t * (D / 2) + (i & 3) * (D / 8) + (i >> 2) * 4) = n;
-  } else {
-    // this thread's four bytes, rows g0 .. g0 + 3: the even piece's code below the odd piece's.  The four
-    // codes' bytes side by side, then the middle nibbles of each half exchanged
-    const int g0 = (i & 1) ? 4 : 0;
-    uint32_t z = __byte_perm(n, other, (i & 1) ? 0x3726 : 0x5140);
-    const uint32_t x = (z ^ (z >> 4)) & 0x00F000F0u;
-    z ^= x ^ (x << 4);
-    uint8_t *p = rec + R::V + v_byte(t, i, g0);
-#pragma unroll
-    for (int g = 0; g < 4; ++g) p[64 * g] = static_cast<uint8_t>(z >> (8 * g));
-  }
-  if ((i & 7) == 0) *reinterpret_cast<uint32_t *>(rec + (v ? R::VW : R::KW) + (t * R::NG + (i >> 3)) * 4) = word;
+__device__ __forceinline__ int k_at(int t, int i) {
+  return Rec4<D>::K + t * (D / 2) + (i & 1) * (D / 4) + (i >> 1) * 4;
+}
+template <int D>
+__device__ __forceinline__ int v_at(int t, int i) {
+  return Rec4<D>::V + (i >> 2) * 512 + ((t & 7) >> 1) * 16 + (i & 3) * 4 + ((t & 1) << 1) + (t >> 3);
+}
+template <int D>
+__device__ __forceinline__ int word_at(bool v, int t, int i) {
+  return (v ? Rec4<D>::VW : Rec4<D>::KW) + (t * Rec4<D>::NG + (i >> 2)) * 4;
 }
 
-// A thread's 8 channels back from a record.  A code's byte becomes the low byte of 2^23 (code + 2^23, exactly).
-template <int D>
-__device__ __forceinline__ uint4 get8(const uint8_t *rec, bool v, int t, int i) {
-  using R = Rec4<D>;
-  uint32_t a, b;      // codes, a byte each: channels 0, 2, 4, 6 and 1, 3, 5, 7 (K), 0 - 3 and 4 - 7 (V)
-  if (!v) {
-    const uint32_t n = *reinterpret_cast<const uint32_t *>(rec + R::K + t * (D / 2) + (i & 3) * (D / 8) + (i >> 2) * 4);
-    a = n & 0x0F0F0F0Fu;
-    b = (n >> 4) & 0x0F0F0F0Fu;
+// Writes a thread's 16 channels of token t; reads them back as codes.
+template <int D, bool V>
+__device__ __forceinline__ void put16(uint8_t *rec, int t, int i, const uint32_t (&n)[2], uint32_t word) {
+  if constexpr (V) {
+    uint8_t *p = rec + v_at<D>(t, i);
+#pragma unroll
+    for (int g = 0; g < 8; ++g) p[64 * g] = static_cast<uint8_t>(n[g / 4] >> (8 * (g % 4)));
   } else {
-    const uint8_t *p = rec + R::V + v_byte(t, i, 0);
+    uint8_t *p = rec + k_at<D>(t, i);
+    *reinterpret_cast<uint32_t *>(p) = n[0];
+    *reinterpret_cast<uint32_t *>(p + D / 8) = n[1];
+  }
+  if ((i & 3) == 0) *reinterpret_cast<uint32_t *>(rec + word_at<D>(V, t, i)) = word;
+}
+template <int D, bool V>
+__device__ __forceinline__ uint32_t get16(const uint8_t *rec, int t, int i, uint32_t (&n)[2]) {
+  if constexpr (V) {
+    const uint8_t *p = rec + v_at<D>(t, i);
     uint32_t w[8];
 #pragma unroll
     for (int g = 0; g < 8; ++g) w[g] = p[64 * g];
-    a = w[0] | (w[1] << 8) | (w[2] << 16) | (w[3] << 24);
-    b = w[4] | (w[5] << 8) | (w[6] << 16) | (w[7] << 24);
-    a = (a >> ((i & 1) * 4)) & 0x0F0F0F0Fu;
-    b = (b >> ((i & 1) * 4)) & 0x0F0F0F0Fu;
-  }
-  const uint32_t word = *reinterpret_cast<const uint32_t *>(rec + (v ? R::VW : R::KW) + (t * R::NG + (i >> 3)) * 4);
-  const float2 s = make_float2(bf16lo(word), bf16lo(word)), m = make_float2(bf16hi(word), bf16hi(word));
-  uint32_t o[4];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const uint32_t x = v ? (j < 2 ? a : b) : a, y = v ? (j < 2 ? a : b) : b;
-    const int bx = v ? 2 * (j & 1) : j, by = v ? 2 * (j & 1) + 1 : j;
-    float2 f = make_float2(__uint_as_float(__byte_perm(x, 0x4B000000u, 0x7650 + bx) ),
-                           __uint_as_float(__byte_perm(y, 0x4B000000u, 0x7650 + by)));
-    f = ffma2(fadd2(f, make_float2(-8388608.f, -8388608.f)), s, m);
-    o[j] = pack_bf16x2(f.x, f.y);
+    for (int k = 0; k < 2; ++k) n[k] = w[4 * k] | (w[4 * k + 1] << 8) | (w[4 * k + 2] << 16) | (w[4 * k + 3] << 24);
+  } else {
+    const uint8_t *p = rec + k_at<D>(t, i);
+    n[0] = *reinterpret_cast<const uint32_t *>(p);
+    n[1] = *reinterpret_cast<const uint32_t *>(p + D / 8);
   }
-  return make_uint4(o[0], o[1], o[2], o[3]);
+  return *reinterpret_cast<const uint32_t *>(rec + word_at<D>(V, t, i));
+}
+
+// Codes to bf16.  A code's byte becomes the low byte of 2^23 (code + 2^23, exactly).
+template <bool V>
+__device__ __forceinline__ void expand16(const uint32_t (&n)[2], uint32_t word, uint32_t (&o)[8]) {
+  const uint32_t even[2] = {n[0] & 0x0F0F0F0Fu, n[1] & 0x0F0F0F0Fu}, odd[2] = {(n[0] >> 4) & 0x0F0F0F0Fu, (n[1] >> 4) & 0x0F0F0F0Fu};
+  const float2 s = make_float2(bf16lo(word), bf16lo(word)), m = make_float2(bf16hi(word), bf16hi(word));
+  auto code = [&](int ch) {
+    const int a = nibble_of(V, ch);
+    return __uint_as_float(__byte_perm((a & 1) ? odd[a / 8] : even[a / 8], 0x4B000000u, 0x7650 + (a % 8) / 2));
+  };
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float2 f = fadd2(make_float2(code(2 * j), code(2 * j + 1)), make_float2(-8388608.f, -8388608.f));
+    const float2 x = ffma2(f, s, m);
+    o[j] = pack_bf16x2(x.x, x.y);
+  }
 }
 
 // The slot of token m; negative: padding (the token is left out).  A slot past the pool is never
@@ -185,143 +239,169 @@ __device__ __forceinline__ int64_t slot_of(const Rows4 &a, int64_t m, bool repor
   return s;
 }
 
-// Few tokens of each sequence (N < 16, decoding steps): one row (token, head) per D / 8 threads, K and V
+// Few tokens of each sequence (N < 16, decoding steps): one row (token, head) per D / 16 threads, K and V
 // by blockIdx.y, straight between the rows and the cache's bytes.
-template <int D, bool LOAD>
-__global__ void __launch_bounds__(256) rows4_kernel(const Rows4 a) {
-  constexpr int TR = D / 8;
-  let_dependents_start();
-  wait_for_earlier();
-  const int side = blockIdx.y, i = threadIdx.x % TR;
+template <int D, bool LOAD, bool V>
+__device__ __forceinline__ void row4(const Rows4 &a) {
+  constexpr int TR = D / 16;
+  const int i = threadIdx.x % TR;
   const int64_t row = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) / TR;
   const int64_t m = row / a.H;
   const int h = static_cast<int>(row % a.H);
   const bool in = m < static_cast<int64_t>(a.B) * a.N;
-  const int64_t slot = in ? slot_of(a, m, i == 0 && h == 0 && side == 0) : -1;
+  const int64_t slot = in ? slot_of(a, m, i == 0 && h == 0 && !V) : -1;
   const int b = in ? static_cast<int>(m / a.N) : 0, n = in ? static_cast<int>(m % a.N) : 0;
-  const int64_t at = b * a.sb[side] + h * a.sh[side] + n * a.sn[side] + 8 * i;
+  const int64_t at = b * a.sb[V] + h * a.sh[V] + n * a.sn[V] + 16 * i;
   const bool live = slot >= 0;
   uint8_t *rec = record_of(a, live ? slot : 0, h, Rec4<D>::BYTES);
   const int t = static_cast<int>(slot & 15);
+  uint32_t u[8], c[2];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) u[j] = 0u;
   if (LOAD) {
-    if (live) *reinterpret_cast<uint4 *>(a.y[side] + at) = get8<D>(rec, side != 0, t, i);
-    else if (in && a.zero) *reinterpret_cast<uint4 *>(a.y[side] + at) = make_uint4(0u, 0u, 0u, 0u);
+    if (live) {
+      const uint32_t word = get16<D, V>(rec, t, i, c);
+      expand16<V>(c, word, u);
+    }
+    if (live || (in && a.zero)) store16(a.y[V] + at, a.wide, u);
   } else {
-    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-    if (live) v = ld_stream_v4(a.x[side] + at);
-    uint32_t word;
-    const uint32_t c = quantise8(v, word);
-    put8<D>(rec, side != 0, t, i, c, word, live);
+    if (live) load16(a.x[V] + at, a.wide, u);
+    const uint32_t word = quantise16<V>(u, c);
+    if (live) put16<D, V>(rec, t, i, c, word);
   }
 }
-
-// Longer rows: a CTA takes the tokens that fall on one record, K and V together, for a few heads one
-// after another (the slots are looked up once, and a head's rows or record come while the one before it
-// is worked on).  A row's place among the 16 tokens follows the slots (the last one's place in its record lines the
-// chunks up; slots that do not run on are still handled, token by token).  A whole record is put
-// together or taken apart in shared memory and moved in 16-byte pieces; single tokens go straight
-// to the cache's bytes.
-// Measured, 4 x 8192 tokens of 8 heads, d = 128, K and V stored and read back: 69 us for 344 MB, 74% of the
-// measured copy rate (cold: store 43 us, load 38): the store is bound by its arithmetic (16 instructions per value),
-// the load by the latency of its two steps.
-constexpr int R4_HEADS = 8;  // most heads of a CTA (8 heads: 68 us, 4: 70, 2: 79)
 template <int D, bool LOAD>
-__global__ void __launch_bounds__(2 * D) records4_kernel(const Rows4 a) {
-  using R = Rec4<D>;
-  constexpr int TR = D / 8, PIECES = (R::BYTES / 16 + 2 * D - 1) / (2 * D);
-  __shared__ __align__(16) uint8_t rec[2][R::BYTES];
-  __shared__ int64_t first;
+__global__ void __launch_bounds__(256) rows4_kernel(const Rows4 a) {
   let_dependents_start();
   wait_for_earlier();
-  const int t = threadIdx.x / TR, i = threadIdx.x % TR, b = blockIdx.z;
-  const int h0 = blockIdx.y * a.per, h1 = min(h0 + a.per, a.H);
+  if (blockIdx.y == 0)
+    row4<D, LOAD, false>(a);
+  else
+    row4<D, LOAD, true>(a);
+}
+
+// Longer rows: D / 4 threads take the tokens that fall on one record of one head, K or V (the parity of blockIdx.x),
+// with nothing between the threads but the groups' shuffles.  A thread holds 16 channels (piece i) of the four tokens
+// 2j, 2j + 1, 2j + 8, 2j + 9, whose V codes lie in the same 32-bit words.  A token's place among the 16 follows the
+// slots (the last one's place in its record lines the chunks up).  A record whose 16 slots run on is moved in
+// words; else (a sequence's ends, slots that do not run on) the V codes go byte by byte.
+// Measured, 4 x 8192 tokens of 8 heads, d = 128, K and V stored and read back: 59 us for 344 MB, 86% of the
+// measured copy rate (cold: store 33 us at 65% of its issue slots, load 29, bound by the latency of last slot, slots,
+// record).  K and V in the same threads: 104 registers, store 36 us; several heads one after another in a
+// thread: the same; 8 channels a thread with the record put together in shared memory: 43 and 38.
+template <int D, bool LOAD, bool V>
+__device__ __forceinline__ void record4(const Rows4 &a) {
+  using R = Rec4<D>;
+  constexpr int TR = D / 16, UNIT = D / 4;  // threads of a row, of a record
+  const int lane = threadIdx.x & 31, i = lane % TR, j = (lane / TR) & 3, b = blockIdx.z;
+  const int h = static_cast<int>(blockIdx.y * blockDim.x + threadIdx.x) / UNIT;
   const int64_t *slots = a.slots + static_cast<int64_t>(b) * a.N;
   const int64_t last = __ldg(slots + a.N - 1);
   const int shift = last < 0 ? 0 : static_cast<int>((last - (a.N - 1)) & 15);
-  const int n = static_cast<int>(blockIdx.x) * C4_TOKENS - shift + t;
-  const bool in = n >= 0 && n < a.N;
-  const int64_t slot = in ? slot_of(a, static_cast<int64_t>(b) * a.N + n, i == 0 && h0 == 0) : -1;
-  const bool live = slot >= 0;
-  if (threadIdx.x == 0) first = slot;
-  __syncthreads();
-  const bool whole = __syncthreads_and(live && (first & 15) == 0 && slot == first + t);
-  uint8_t *mem = record_of(a, live ? slot : 0, h0, R::BYTES);
-  const int64_t hstep = static_cast<int64_t>(a.recs) * R::BYTES;  // the next head's record of the page
-  const int at = static_cast<int>(slot & 15);
-  const int64_t o0 = b * a.sb[0] + h0 * a.sh[0] + n * a.sn[0] + 8 * i, o1 = b * a.sb[1] + h0 * a.sh[1] + n * a.sn[1] + 8 * i;
-  const uint4 none = make_uint4(0u, 0u, 0u, 0u);
-  if (LOAD) {
-    __nv_bfloat16 *y0 = a.y[0] + o0, *y1 = a.y[1] + o1;
-    uint4 piece[PIECES];
-    auto fetch = [&](const uint8_t *from) {
+  const int n0 = static_cast<int>(blockIdx.x >> 1) * C4_TOKENS - shift;
+  auto place = [&](int k) { return 2 * j + (k & 1) + 8 * (k >> 1); };
+  bool in[4];
+  int64_t slot[4];
 #pragma unroll
-      for (int e = 0; e < PIECES; ++e)
-        if (whole && e * 2 * D + threadIdx.x < R::BYTES / 16) piece[e] = ld_stream_v4(from + 16 * (e * 2 * D + threadIdx.x));
-    };
-    fetch(mem);
-    for (int h = h0; h < h1; ++h) {
-      uint8_t *buf = rec[h & 1];
-      if (whole) {
+  for (int k = 0; k < 4; ++k) {
+    const int n = n0 + place(k);
+    in[k] = h < a.H && n >= 0 && n < a.N;
+    slot[k] = in[k] ? slot_of(a, static_cast<int64_t>(b) * a.N + n, i == 0 && h == 0 && !V) : -1;
+  }
+  const int64_t hoff = b * a.sb[V] + min(h, a.H - 1) * a.sh[V] + 16 * i;
+  uint32_t x[4][8], c[4][2], word[4];
+  if constexpr (!LOAD) {  // every row of the tensors may be read: places in front, behind and left out give codes that go nowhere
 #pragma unroll
-        for (int e = 0; e < PIECES; ++e)
-          if (e * 2 * D + threadIdx.x < R::BYTES / 16) reinterpret_cast<uint4 *>(buf)[e * 2 * D + threadIdx.x] = piece[e];
-        __syncthreads();
-        if (h + 1 < h1) fetch(mem + hstep);
+    for (int k = 0; k < 4; ++k) load16(a.x[V] + hoff + min(max(n0 + place(k), 0), a.N - 1) * a.sn[V], a.wide, x[k]);
+  }
+  const int64_t first = __shfl_sync(0xffffffffu, slot[0], lane & ~(UNIT - 1));
+  bool run = first >= 0 && (first & 15) == 0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) run = run && slot[k] == first + place(k);
+  const uint32_t unit = UNIT == 32 ? 0xffffffffu : 0xffffu << (lane & 16);
+  const bool whole = (__ballot_sync(0xffffffffu, run) & unit) == unit;
+  uint8_t *mem = record_of(a, whole ? first : 0, h, R::BYTES);
+  // V codes of a whole record: bytes 0 - 3 of word g are tokens 2j, 2j + 8, 2j + 1, 2j + 9
+  uint8_t *vp = mem + v_at<D>(2 * j, i);
+  constexpr int ORDER[4] = {0, 2, 1, 3};
+  if constexpr (LOAD) {
+    if (whole) {
+      if constexpr (V) {
+        uint32_t w[8];
+#pragma unroll
+        for (int g = 0; g < 8; ++g) w[g] = *reinterpret_cast<const uint32_t *>(vp + 64 * g);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) word[k] = *reinterpret_cast<const uint32_t *>(mem + word_at<D>(true, place(k), i));
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          uint32_t z[4];
+          transpose_bytes(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3], z);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) c[ORDER[k]][q] = z[k];
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) word[k] = get16<D, false>(mem, place(k), i, c[k]);
       }
-      uint4 k = none, v = none;
-      if (live) {
-        const uint8_t *src = whole ? buf : mem;
-        k = get8<D>(src, false, at, i);
-        v = get8<D>(src, true, at, i);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        c[k][0] = c[k][1] = word[k] = 0u;  // left out: zeros
+        if (slot[k] >= 0) word[k] = get16<D, V>(record_of(a, slot[k], h, R::BYTES), static_cast<int>(slot[k] & 15), i, c[k]);
       }
-      if (live || (in && a.zero)) {
-        *reinterpret_cast<uint4 *>(y0) = k;
-        *reinterpret_cast<uint4 *>(y1) = v;
-      }
-      mem += hstep;
-      y0 += a.sh[0];
-      y1 += a.sh[1];
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      expand16<V>(c[k], word[k], x[k]);
+      if (slot[k] >= 0 || (in[k] && a.zero)) store16(a.y[V] + hoff + (n0 + place(k)) * a.sn[V], a.wide, x[k]);
     }
   } else {
-    const __nv_bfloat16 *x0 = a.x[0] + o0, *x1 = a.x[1] + o1;
-    uint4 k = live ? ld_stream_v4(x0) : none, v = live ? ld_stream_v4(x1) : none;
-    for (int h = h0; h < h1; ++h) {
-      const uint4 k0 = k, v0 = v;
-      if (live && h + 1 < h1) {
-        x0 += a.sh[0];
-        x1 += a.sh[1];
-        k = ld_stream_v4(x0);
-        v = ld_stream_v4(x1);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) word[k] = quantise16<V>(x[k], c[k]);
+    if (whole) {
+      if constexpr (V) {
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          uint32_t z[4];
+          transpose_bytes(c[ORDER[0]][q], c[ORDER[1]][q], c[ORDER[2]][q], c[ORDER[3]][q], z);
+#pragma unroll
+          for (int g = 0; g < 4; ++g) *reinterpret_cast<uint32_t *>(vp + 64 * (4 * q + g)) = z[g];
+        }
+        if ((i & 3) == 0)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) *reinterpret_cast<uint32_t *>(mem + word_at<D>(true, place(k), i)) = word[k];
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) put16<D, false>(mem, place(k), i, c[k], word[k]);
       }
-      uint8_t *dst = whole ? rec[h & 1] : mem;
-      uint32_t word;
-      uint32_t c = quantise8(k0, word);
-      put8<D>(dst, false, at, i, c, word, live);
-      c = quantise8(v0, word);
-      put8<D>(dst, true, at, i, c, word, live);
-      if (whole) {
-        __syncthreads();
-        for (int e = threadIdx.x; e < R::BYTES / 16; e += 2 * D)
-          *reinterpret_cast<uint4 *>(mem + 16 * e) = reinterpret_cast<const uint4 *>(rec[h & 1])[e];
-      }
-      mem += hstep;
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (slot[k] >= 0) put16<D, V>(record_of(a, slot[k], h, R::BYTES), static_cast<int>(slot[k] & 15), i, c[k], word[k]);
     }
   }
 }
+template <int D, bool LOAD>
+__global__ void __launch_bounds__(128) records4_kernel(const Rows4 a) {
+  let_dependents_start();
+  wait_for_earlier();
+  if (blockIdx.x & 1)
+    record4<D, LOAD, true>(a);
+  else
+    record4<D, LOAD, false>(a);
+}
 
 template <int D, bool LOAD>
-cudaError_t launch_rows4(Rows4 a, cudaStream_t s) {
+cudaError_t launch_rows4(const Rows4 &a, cudaStream_t s) {
   if (a.N >= C4_TOKENS) {
-    // as many heads per CTA as leave 8 CTAs for each of the 152 SMs
-    const int64_t chunks = a.N / C4_TOKENS + 2, per = chunks * a.B * a.H / (8 * 152);
-    a.per = static_cast<int>(per < 1 ? 1 : (per > R4_HEADS ? R4_HEADS : per));
-    if ((a.H + a.per - 1) / a.per > 65535) a.per = R4_HEADS;
-    const dim3 grid(static_cast<unsigned>(chunks), static_cast<unsigned>((a.H + a.per - 1) / a.per), static_cast<unsigned>(a.B));
-    return launch_dependent(records4_kernel<D, LOAD>, grid, 2 * D, 0, s, a);
-  } else {
-    const int64_t rows = static_cast<int64_t>(a.B) * a.N * a.H, per = 256 / (D / 8);
-    return launch_dependent(rows4_kernel<D, LOAD>, dim3(static_cast<unsigned>((rows + per - 1) / per), 2), 256, 0, s, a);
+    constexpr int HW = 128 / D;  // heads of a warp
+    const int warps = (a.H + HW - 1) / HW < 4 ? (a.H + HW - 1) / HW : 4;
+    const dim3 grid(static_cast<unsigned>(2 * (a.N / C4_TOKENS + 2)), static_cast<unsigned>((a.H + warps * HW - 1) / (warps * HW)),
+                    static_cast<unsigned>(a.B));
+    return launch_dependent(records4_kernel<D, LOAD>, grid, static_cast<unsigned>(warps * 32), 0, s, a);
   }
+  const int64_t rows = static_cast<int64_t>(a.B) * a.N * a.H, per = 256 / (D / 16);
+  return launch_dependent(rows4_kernel<D, LOAD>, dim3(static_cast<unsigned>((rows + per - 1) / per), 2), 256, 0, s, a);
 }
 
 }  // namespace
@@ -374,7 +454,9 @@ int rows4(const sparge_tensor *k, const sparge_tensor *v, const int64_t *slots, 
   a.recs = c.page_size / C4_TOKENS;
   a.status = status_ptr();
   a.zero = zero;
-  a.per = 1;
+  a.wide = 1;  // 32-byte pieces: base and strides allow it
+  for (int t = 0; t < 2; ++t)
+    if ((reinterpret_cast<uintptr_t>(x[t].data) & 31u) || ((x[t].sb | x[t].sh | x[t].sn) & 15)) a.wide = 0;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (c.d == 128)

@@ -211,6 +211,64 @@ def test_store_edge_values():
     assert torch.isfinite(a[0, 0, 5]).all() and torch.isfinite(a[0, 0, 6]).all()
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_store_edge_values_in_long_rows(d):
+    """Groups without a range, past fp32's range, with infinities and NaN between ordinary ones, in whole records and at
+    the ends of rows: codes, scales and minima as defined, NaN only where a group holds one."""
+    g = gen(23)
+    k, v = rand(g, 1, 3, 70, d), rand(g, 1, 3, 70, d)
+    for x in (k, v):
+        x[0, 0, ::7] = 3.0
+        x[0, 1, 3::9, :64] = 0.0
+        x[0, 2, 5::8] *= 1e-36
+        x[0, 1, 6, 0], x[0, 1, 6, 1] = 3.3e38, -3.3e38
+        x[0, 0, 20, 5], x[0, 2, 69, d - 1], x[0, 1, 40, 33] = math.inf, math.nan, -math.inf
+    pool = fbs.cache4_pool(2, 64, 3, d)
+    slots = (torch.arange(70, device="cuda")[None] + 25).contiguous()
+    fbs.cache4_store(k, v, slots, pool)
+    a, b = fbs.cache4_load(pool, slots)
+    for x, y in ((k, a), (v, b)):
+        groups, back = x.view(1, 3, 70, d // 64, 64), y.reshape(1, 3, 70, d // 64, 64)
+        bad = ~torch.isfinite(groups.float()).all(-1)
+        assert torch.isnan(back[bad]).all() and torch.isfinite(back[~bad]).all()
+        plain = ~bad
+        plain[0, 1, 6, 0] = False  # its scale is the one that fp32 can hold
+        want = R.dequantise(*R.quantise(torch.where(bad[..., None], torch.zeros_like(groups), groups).reshape(k.shape).double()))
+        assert torch.equal(back[plain], want.float().bfloat16().view_as(back)[plain])
+
+
+@pytest.mark.parametrize("H,d,shift", [(3, 64, 8), (1, 64, 8), (5, 128, 8), (2, 128, 16)])
+def test_store_and_load_strided_rows_with_gaps(H, d, shift):
+    """Rows that start on 16 but not on 32 bytes (or on 32, with gaps), long rows with padding in front and slots left out in
+    the middle; padding rows hold NaN, left-out rows of given outputs keep what they held."""
+    g = gen(24)
+    B, N, page = 2, 61, 32
+    wide = lambda: rand(g, B, N, H, d + shift)[..., shift:].transpose(1, 2)  # noqa: E731
+    k, v = wide(), wide()
+    slots = torch.stack([torch.arange(N, device="cuda") + 7, torch.arange(N, device="cuda") + 100])
+    slots[0, :20] = -1
+    slots[1, 30:33] = -4
+    k.transpose(1, 2)[slots < 0] = math.nan
+    v.transpose(1, 2)[slots < 0] = math.inf
+    pool = fbs.cache4_pool(6, page, H, d)
+    pool.random_(0, 256, generator=g)
+    before = pool.clone()
+    fbs.cache4_store(k, v, slots, pool)
+    a, b = wide().fill_(9.0), wide().fill_(9.0)
+    fbs.cache4_load(pool, slots, a, b)
+    a2, b2 = fbs.cache4_load(pool, slots)
+    live = slots >= 0
+    for x, got, made in ((k, a, a2), (v, b, b2)):
+        want = R.dequantise(*R.quantise(x.transpose(1, 2)[live].double())).float().bfloat16()
+        assert torch.equal(got.transpose(1, 2)[live], want) and torch.equal(made.transpose(1, 2)[live], want)
+        assert (got.transpose(1, 2)[~live] == 9).all() and (made.transpose(1, 2)[~live] == 0).all()
+    other = torch.ones(6 * page, dtype=torch.bool, device="cuda")
+    other[slots[live]] = False
+    rest = other.nonzero().view(1, -1)
+    for x, y in zip(values_of(pool, d, rest), values_of(before, d, rest)):
+        assert torch.equal(torch.nan_to_num(x), torch.nan_to_num(y))
+
+
 def test_slots_left_out():
     d, page, H = 64, 16, 2
     g = gen(4)
