@@ -470,8 +470,6 @@ int window_impl(const View &q, const View &k, const View &v, const View &o, int6
     const cudaError_t e = launch_window_decode(w, s);
     return e == cudaSuccess ? SPARGE_OK : cuda_fail(e, "window attention launch");
   }
-  AttnLaunch l;
-  memset(&l, 0, sizeof(l));
   // The f16 copy of the V rows that are read: the first tokens' blocks and those from the first query's
   // window on.  Rows of these blocks that no query sees become zero, so leftovers there (NaN times a P of
   // zero is NaN) reach nothing.
@@ -482,20 +480,39 @@ int window_impl(const View &q, const View &k, const View &v, const View &o, int6
     e = launch_convert_v_f16(v, ws, nullptr, status_ptr(), s, 0, ns < lo ? ns : lo, sinks, first);
   if (e != cudaSuccess) return cuda_fail(e, "convert_v launch");
   View v16{ws, v.B, v.H, v.N, v.d, v.H * v.N * v.d, v.N * v.d, v.d};
-  if ((rc = make_map(&l.tv, v16, 64, "v", CU_TENSOR_MAP_DATA_TYPE_FLOAT16))) return rc;
-  if ((rc = make_map(&l.tq, q, 128, "q")) || (rc = make_map(&l.tk, k, 64, "k"))) return rc;
-  l.q = q.data;
-  l.q_sb = q.sb; l.q_sh = q.sh; l.q_sn = q.sn;
-  l.o = const_cast<void *>(o.data);
-  l.o_sb = o.sb; l.o_sh = o.sh; l.o_sn = o.sn;
-  l.B = (int)q.B; l.Hq = (int)q.H; l.Hkv = (int)k.H; l.Nq = (int)q.N; l.Nk = (int)k.N; l.d = (int)q.d;
-  l.causal = 1;
-  l.scale = scale;
-  l.lambda = -INFINITY;
-  l.window = (int)window;
-  l.sinks = (int)sinks;
-  l.status = status_ptr();
-  e = launch_bsattn(l, s);
+  CUtensorMap tq, tk, tv;
+  if ((rc = make_map(&tv, v16, 64, "v", CU_TENSOR_MAP_DATA_TYPE_FLOAT16))) return rc;
+  if ((rc = make_map(&tq, q, 128, "q")) || (rc = make_map(&tk, k, 64, "k"))) return rc;
+  // d = 64, and few key blocks per query block (window up to about 1300): the kernel with more and simpler CTAs.  At d = 128
+  // over 16K of 32 heads: window 256 176 us against 202, 1024 324 against 334, but 1536 424 against 412, 4096 876
+  // against 810; at d = 64 never behind (4096: 537 against 668).
+  if (q.d == 64 || cdiv(window + QBLK - 1, KBLK) + 1 + cdiv(sinks, KBLK) <= 24) {
+    WindowAttn w;
+    w.tq = tq; w.tk = tk; w.tv = tv;
+    w.o = const_cast<void *>(o.data);
+    w.o_sb = o.sb; w.o_sh = o.sh; w.o_sn = o.sn;
+    w.B = (int)q.B; w.Hkv = (int)k.H; w.G = (int)(q.H / k.H); w.Nq = (int)q.N; w.Nk = (int)k.N; w.d = (int)q.d;
+    w.window = (int)window; w.sinks = (int)sinks;
+    w.scale = scale;
+    w.status = status_ptr();
+    e = launch_window_attn(w, s);
+  } else {
+    AttnLaunch l;
+    memset(&l, 0, sizeof(l));
+    l.tq = tq; l.tk = tk; l.tv = tv;
+    l.q = q.data;
+    l.q_sb = q.sb; l.q_sh = q.sh; l.q_sn = q.sn;
+    l.o = const_cast<void *>(o.data);
+    l.o_sb = o.sb; l.o_sh = o.sh; l.o_sn = o.sn;
+    l.B = (int)q.B; l.Hq = (int)q.H; l.Hkv = (int)k.H; l.Nq = (int)q.N; l.Nk = (int)k.N; l.d = (int)q.d;
+    l.causal = 1;
+    l.scale = scale;
+    l.lambda = -INFINITY;
+    l.window = (int)window;
+    l.sinks = (int)sinks;
+    l.status = status_ptr();
+    e = launch_bsattn(l, s);
+  }
   return e == cudaSuccess ? SPARGE_OK : cuda_fail(e, "window attention launch");
 }
 

@@ -857,10 +857,9 @@ cudaError_t launch_bsattn(const AttnLaunch &l, cudaStream_t st) {
     return launch_decode_combine(l.part_o, l.part_ml, l.nchunk, a.B, a.Hq, a.Hkv, a.Nq, l.d, a.o, a.o_sb, a.o_sh, a.o_sn,
                                  st);
   }
-  if (l.window) {  // bf16, causal, no block mask: the host sees to it
-    if (l.q8 != 0 || !l.causal || l.mask) return cudaErrorInvalidValue;
-    return l.d == 128 ? launch_t<128, 3, 2, false, false, false, true>(l, a, st)
-                      : launch_t<64, 4, 3, false, false, false, true>(l, a, st);
+  if (l.window) {  // bf16, causal, no block mask, long windows at d = 128: the host sees to it
+    if (l.q8 != 0 || !l.causal || l.mask || l.d != 128) return cudaErrorInvalidValue;
+    return launch_t<128, 3, 2, false, false, false, true>(l, a, st);
   }
   if (l.q8 == 3) return launch_t<128, 3, 3, false, true>(l, a, st);  // bf16 Q.K^T, e4m3 P.V
   if (l.q8 == 2) return launch_t<128, 4, 3, true, true>(l, a, st);

@@ -184,6 +184,18 @@ inline size_t decode_part_bytes(int64_t B, int64_t Hkv, int64_t Nk, int64_t d) {
 
 cudaError_t launch_bsattn(const AttnLaunch &a, cudaStream_t st);
 
+// Chunks under a sliding window (window_attn.cu).  tq, tk, tv: 4-D maps over Q (boxes 64 x 128), K and the f16
+// copy of V (boxes 64 x 64), 128-byte swizzle.
+struct WindowAttn {
+  CUtensorMap tq, tk, tv;
+  void *o;
+  int64_t o_sb, o_sh, o_sn;
+  int B, Hkv, G, Nq, Nk, d, window, sinks;  // window and sinks at most Nk
+  float scale;
+  int *status;
+};
+cudaError_t launch_window_attn(const WindowAttn &l, cudaStream_t st);
+
 // Decoding under a sliding window, up to WINDOW_DECODE_ROWS query rows per KV head (window_decode.cu).  tk and
 // tv: 4-D maps over K and V (bf16, 128-byte swizzle, boxes 64 x 16).
 constexpr int WINDOW_DECODE_ROWS = 128;

@@ -445,6 +445,11 @@ def check_window(q, k, v, out, window, sinks, scale=0.0, decode=False):
     (1, 2, 2, 640, 640, 128, 5000, 3, False),      # a window longer than the keys: causal
     (1, 2, 1, 2049, 2049, 128, 511, 4, False),
     (1, 4, 1, 1, 500, 128, 64, 4, False),          # few queries, few blocks
+    (1, 2, 1, 700, 4000, 128, 2000, 100, False),   # long windows
+    (2, 4, 2, 1500, 2500, 128, 1700, 4, False),
+    (1, 2, 2, 2000, 2000, 64, 1900, 70, False),
+    (1, 6, 1, 130, 1400, 128, 1270, 3, False),     # 23 and 24 blocks a query block
+    (1, 6, 1, 130, 1500, 128, 1330, 3, False),
     (2, 8, 2, 1, 5000, 128, 2100, 4, True),        # decoding tiles
     (1, 8, 1, 7, 4001, 64, 2500, 0, True),
     (3, 4, 4, 1, 2300, 64, 10000, 0, True),
@@ -490,6 +495,26 @@ def test_window_attn_climbing_scores(d):
     check_window(q, k, v, fbs.window_attn(q, k, v, 300, 5), 300, 5)
     k2 = k.flip(2).contiguous()
     check_window(q, k2, v, fbs.window_attn(q, k2, v, 300, 5), 300, 5)
+
+
+def test_window_attn_beside_other_attention():
+    """Window attention at both head dims and the block-sparse attention on three streams at once, all of them with
+    accumulators in tensor memory: the same bits as one after another."""
+    g = gen(25)
+    a = [rand(g, 1, h, 2500, 64) for h in (16, 4, 4)]
+    b = [rand(g, 1, h, 2500, 128) for h in (8, 2, 2)]
+    calls = [lambda: fbs.window_attn(*a, 500, 4), lambda: fbs.window_attn(*b, 300, 4), lambda: fbs.block_sparse_attn(*b, None, -math.inf, True)]
+    want = [c() for c in calls]
+    streams = [torch.cuda.Stream() for _ in calls]
+    torch.cuda.synchronize()
+    got = [[], [], []]
+    for _ in range(10):
+        for i, (c, s) in enumerate(zip(calls, streams)):
+            with torch.cuda.stream(s):
+                got[i].append(c())
+    torch.cuda.synchronize()
+    for i in range(3):
+        assert all(torch.equal(x, want[i]) for x in got[i])
 
 
 # ------------------------------------------------------------------------------------------------- together
