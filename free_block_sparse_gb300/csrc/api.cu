@@ -127,12 +127,12 @@ encode_fn_t get_encode() {
 }
 
 int make_map(CUtensorMap *m, const View &v, int box_rows, const char *name,
-             CUtensorMapDataType dt = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16) {
+             CUtensorMapDataType dt = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, int box_heads = 1) {
   encode_fn_t enc = get_encode();
   if (!enc) return fail(SPARGE_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
   cuuint64_t dims[4] = {(cuuint64_t)v.d, (cuuint64_t)v.N, (cuuint64_t)v.H, (cuuint64_t)v.B};
   cuuint64_t strides[3] = {(cuuint64_t)v.sn * 2, (cuuint64_t)v.sh * 2, (cuuint64_t)v.sb * 2};
-  cuuint32_t box[4] = {64, (cuuint32_t)box_rows, 1, 1};
+  cuuint32_t box[4] = {64, (cuuint32_t)box_rows, (cuuint32_t)box_heads, 1};
   cuuint32_t es[4] = {1, 1, 1, 1};
   CUresult r = enc(m, dt, 4, const_cast<void *>(v.data), dims, strides, box, es,
                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -482,12 +482,14 @@ int window_impl(const View &q, const View &k, const View &v, const View &o, int6
   View v16{ws, v.B, v.H, v.N, v.d, v.H * v.N * v.d, v.N * v.d, v.d};
   CUtensorMap tq, tk, tv;
   if ((rc = make_map(&tv, v16, 64, "v", CU_TENSOR_MAP_DATA_TYPE_FLOAT16))) return rc;
-  if ((rc = make_map(&tq, q, 128, "q")) || (rc = make_map(&tk, k, 64, "k"))) return rc;
-  // d = 64, and few key blocks per query block (window up to about 1300): the kernel with more and simpler CTAs.  At d = 128
-  // over 16K of 32 heads: window 256 176 us against 202, 1024 324 against 334, but 1536 424 against 412, 4096 876
-  // against 810; at d = 64 never behind (4096: 537 against 668).
-  if (q.d == 64 || cdiv(window + QBLK - 1, KBLK) + 1 + cdiv(sinks, KBLK) <= 24) {
+  if ((rc = make_map(&tk, k, 64, "k"))) return rc;
+  // d = 64, and few key blocks per tile of queries (window up to about 1300): the kernel with more and simpler CTAs.  At
+  // d = 128 over 16K of 32 + 8 heads: window 256 162 us against 209, 1280 364 against 375, 1536 415 against 415, but 2048 514
+  // against 495, 4096 859 against 767 (16 + 16 heads: 1024 188 against 188); at d = 64 never behind (4096: 538 against 668).
+  const int P = window_attn_queries(q.H / k.H);
+  if (q.d == 64 || cdiv(window + P - 1, KBLK) + 1 + cdiv(sinks, KBLK) <= 24) {
     WindowAttn w;
+    if ((rc = make_map(&tq, q, P, "q", CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 128 / P))) return rc;
     w.tq = tq; w.tk = tk; w.tv = tv;
     w.o = const_cast<void *>(o.data);
     w.o_sb = o.sb; w.o_sh = o.sh; w.o_sn = o.sn;
@@ -499,6 +501,7 @@ int window_impl(const View &q, const View &k, const View &v, const View &o, int6
   } else {
     AttnLaunch l;
     memset(&l, 0, sizeof(l));
+    if ((rc = make_map(&tq, q, 128, "q"))) return rc;
     l.tq = tq; l.tk = tk; l.tv = tv;
     l.q = q.data;
     l.q_sb = q.sb; l.q_sh = q.sh; l.q_sn = q.sn;

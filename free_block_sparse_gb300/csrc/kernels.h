@@ -184,8 +184,8 @@ inline size_t decode_part_bytes(int64_t B, int64_t Hkv, int64_t Nk, int64_t d) {
 
 cudaError_t launch_bsattn(const AttnLaunch &a, cudaStream_t st);
 
-// Chunks under a sliding window (window_attn.cu).  tq, tk, tv: 4-D maps over Q (boxes 64 x 128), K and the f16
-// copy of V (boxes 64 x 64), 128-byte swizzle.
+// Chunks under a sliding window (window_attn.cu).  tq, tk, tv: 4-D maps over Q (boxes 64 x window_attn_queries(G) x
+// 128 / that many heads), K and the f16 copy of V (boxes 64 x 64), 128-byte swizzle.
 struct WindowAttn {
   CUtensorMap tq, tk, tv;
   void *o;
@@ -194,6 +194,12 @@ struct WindowAttn {
   float scale;
   int *status;
 };
+// Queries of a tile: 128 rows of as many heads of the group of G as is a power of two up to 16 that divides it.
+inline int window_attn_queries(int64_t G) {
+  int heads = 1;
+  while (heads < 16 && G % (2 * heads) == 0) heads *= 2;
+  return 128 / heads;
+}
 cudaError_t launch_window_attn(const WindowAttn &l, cudaStream_t st);
 
 // Decoding under a sliding window, up to WINDOW_DECODE_ROWS query rows per KV head (window_decode.cu).  tk and

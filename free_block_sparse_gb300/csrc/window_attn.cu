@@ -1,8 +1,10 @@
 // Causal attention over a sliding window and a few first tokens, for chunks of queries, on tcgen05 tensor
 // cores: query row at position p sees key c <= p when c > p - window or c < sinks.
 //
-// One CTA computes one 128-row query block of one head against the 64-key blocks that its rows see (the first
-// tokens', then the window's), one after another.  Warp roles (160 threads):
+// One CTA computes 128 rows against the 64-key blocks that they see (the first tokens', then the window's), one after
+// another.  The rows are P = 128 / heads queries of as many heads of a KV head as its group allows (a power of two up to 16):
+// P queries see window + P - 1 keys between them, so fewer of them mean fewer blocks and fewer hidden scores for the
+// same rows.  Warp roles (160 threads):
 //   warps 0-3  softmax + epilogue; one query row per thread (TMEM lane).
 //   warp 4     one thread: TMA loads of Q, then of each block's K and V (an f16 copy), and the products: the next
 //              block's S = Q K^T as soon as the softmax has read this one's, then O += P V of this one.
@@ -17,9 +19,10 @@
 // bit mask per row.  P and V enter the second product as f16, which keeps 3 more bits of P than bf16 would.
 //
 // Measured (f16 copy of V included; beside it the block-sparse kernel under the same mask, two score buffers per CTA):
-// d = 64, 32 + 8 heads of 16K, window 4096: 537 us (668), 46% of the tensor peak; 2 x 15K of 64 + 8 heads, window 461: 455 us
-// (792); d = 128, 32 + 8 heads of 16K: window 256 176 us (202), 1024 324 (334), 1536 424 (412), 4096 876 (810): at
-// d = 128 the products alone fill the tensor unit, which two score buffers feed better over a long window.
+// d = 64, 32 + 8 heads of 16K, window 4096: 538 us (668), 46% of the tensor peak; 2 x 15K of 64 + 8 heads, window 461: 413 us
+// (792; 454 with tiles of 128 queries of one head); d = 128, 32 + 8 heads of 16K: window 256 162 us (209), 1280 364 (375),
+// 1536 415 (415), 4096 859 (767): at d = 128 the products alone fill the tensor unit, which two score buffers
+// feed better over a long window.
 // At d = 64 a block takes 570 cycles of an SM: the softmax's instructions (about 300 of each of 12 warps) and the
 // chain's waits; the products 330.
 #include <cfloat>
@@ -38,7 +41,8 @@ constexpr float WA_RESCALE = 8.f;
 struct WindowAttnArgs {
   __nv_bfloat16 *o;
   int64_t o_sb, o_sh, o_sn;
-  int B, Hq, Hkv, G, Nq, Nk, nqb, nkb, off, window, sinks;  // off = Nk - Nq
+  int Hkv, G, Nq, Nk, ntile, nkb, off, window, sinks;  // off = Nk - Nq
+  int shift;                                           // P = 1 << shift queries of a tile, of 128 / P heads
   float scale_log2;
   int *status;
 };
@@ -64,14 +68,14 @@ struct WaCtrl {
 };
 static_assert(sizeof(WaCtrl) <= 512, "control block");
 
-// The key blocks of a query block: `ns` of the first tokens, then from `lo` up to `end`.
+// The key blocks of the P queries from position p0 on: `ns` of the first tokens, then from `lo` on, n in all.
 struct WaBlocks {
   int ns, lo, n;
-  __device__ __forceinline__ WaBlocks(const WindowAttnArgs &a, int i) {
-    const int p0 = a.off + QBLK * i, first = p0 - a.window + 1;
+  __device__ __forceinline__ WaBlocks(const WindowAttnArgs &a, int p0) {
+    const int first = p0 - a.window + 1;
     lo = first > 0 ? first / KBLK : 0;
     ns = min(lo, a.sinks / KBLK + (a.sinks % KBLK != 0 ? 1 : 0));
-    n = ns + min(a.nkb, causal_key_blocks(i, a.off)) - lo;
+    n = ns + min(a.nkb, (p0 + (1 << a.shift) - 1) / KBLK + 1) - lo;
   }
   __device__ __forceinline__ int at(int t) const { return t < ns ? t : lo + t - ns; }
 };
@@ -107,11 +111,12 @@ __global__ void __launch_bounds__(WA_THREADS, WaCfg<D>::CTAS)
   volatile int *abort = &cs.abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  // work item: (b, kvh) outermost so that CTAs of the same time share K and V in L2, heads of a group adjacent
-  const int per_bk = a.nqb * a.G;
+  // work item: (b, kvh) outermost so that CTAs of the same time share K and V in L2, a tile's groups of heads adjacent
+  const int heads = 128 >> a.shift, groups = a.G / heads, per_bk = a.ntile * groups;
   const int bk = blockIdx.x / per_bk, rem = blockIdx.x % per_bk;
-  const int b = bk / a.Hkv, kvh = bk % a.Hkv, i = a.nqb - 1 - rem / a.G, h = kvh * a.G + rem % a.G;
-  const WaBlocks wb(a, i);
+  const int b = bk / a.Hkv, kvh = bk % a.Hkv, h0 = kvh * a.G + rem % groups * heads;
+  const int q0 = (a.ntile - 1 - rem / groups) << a.shift;  // the tile's first query
+  const WaBlocks wb(a, a.off + q0);
 
   if (threadIdx.x == 0) {
     mbar_init(&cs.q_full, 1);
@@ -150,7 +155,7 @@ __global__ void __launch_bounds__(WA_THREADS, WaCfg<D>::CTAS)
     if (lane == 0) {
       mbar_arrive_expect_tx(&cs.q_full, 2 * C::TILE);
       for (uint32_t c = 0; c < C::CH; ++c)
-        tma_load_4d(smem + C::Q + c * 2 * C::CHUNK, &tq, &cs.q_full, 64 * c, QBLK * i, h, b);
+        tma_load_4d(smem + C::Q + c * 2 * C::CHUNK, &tq, &cs.q_full, 64 * c, q0, h0, b);
       load(C::K, &tk, cs.k_full, 0);
       load(C::V, &tv, cs.v_full, 0);
       if (wb.n > 1) load(C::K, &tk, cs.k_full, 1);
@@ -195,8 +200,10 @@ __global__ void __launch_bounds__(WA_THREADS, WaCfg<D>::CTAS)
   } else {
     // ------------------------------------ softmax warps ------------------------------------
     // (rows past the last query: zeros from TMA, computed and dropped)
-    const int row = QBLK * i + warp * 32 + lane, pos = a.off + row, pos0 = pos - lane;
-    const bool row_ok = row < a.Nq;
+    const int r = warp * 32 + lane, qi = q0 + (r & ((1 << a.shift) - 1)), pos = a.off + qi;
+    // the positions of the warp's rows lie in pos0 .. pos1
+    const int pos0 = a.off + q0 + ((warp * 32) & ((1 << a.shift) - 1)), pos1 = pos0 + min(32, 1 << a.shift) - 1;
+    const bool row_ok = qi < a.Nq;
     const uint32_t tl = tmem + (static_cast<uint32_t>(warp * 32) << 16);
     float m_ref = -INFINITY, l = 0.f;
     bool ok = true;
@@ -221,10 +228,10 @@ __global__ void __launch_bounds__(WA_THREADS, WaCfg<D>::CTAS)
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         const int key0 = KBLK * j + 32 * c;
-        hidden[c] = key0 > pos0 + 31 || (key0 + 31 <= pos0 - a.window && key0 >= a.sinks);
+        hidden[c] = key0 > pos1 || (key0 + 31 <= pos0 - a.window && key0 >= a.sinks);
         if (hidden[c]) {
           mh[c] = -INFINITY;
-        } else if (key0 + 31 > pos0 || (key0 <= pos0 + 31 - a.window && key0 + 31 >= a.sinks)) {
+        } else if (key0 + 31 > pos0 || (key0 <= pos1 - a.window && key0 + 31 >= a.sinks)) {
           // bit k: this row sees column k (up to its position, and in its window or among the first tokens)
           const int lim = pos - key0, low = lim - a.window, open = a.sinks - key0;
           const uint32_t seen = upto(lim) & (~upto(low) | upto(open - 1));
@@ -293,7 +300,7 @@ __global__ void __launch_bounds__(WA_THREADS, WaCfg<D>::CTAS)
     tc_fence_after();
     const bool all_ok = __all_sync(0xffffffffu, ok);
     const float inv_l = l > 0.f ? 1.f / l : 0.f;
-    __nv_bfloat16 *orow = a.o + b * a.o_sb + h * a.o_sh + static_cast<int64_t>(row) * a.o_sn;
+    __nv_bfloat16 *orow = a.o + b * a.o_sb + (h0 + (r >> a.shift)) * a.o_sh + static_cast<int64_t>(qi) * a.o_sn;
 #pragma unroll 1
     for (int q = 0; q < (all_ok ? D / 16 : 0); ++q) {
       uint32_t o[16];
@@ -323,7 +330,7 @@ cudaError_t launch_t(const WindowAttn &l, const WindowAttnArgs &a, cudaStream_t 
   static std::atomic<unsigned long long> smem_set{0};
   if (cudaError_t e = set_smem_limit_once(window_attn_kernel<D>, static_cast<int>(WaCfg<D>::SMEM), smem_set); e != cudaSuccess)
     return e;
-  const int64_t grid = static_cast<int64_t>(a.B) * a.Hq * a.nqb;
+  const int64_t grid = static_cast<int64_t>(l.B) * a.Hkv * (a.G / (128 >> a.shift)) * a.ntile;
   if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
   window_attn_kernel<D><<<static_cast<unsigned>(grid), WA_THREADS, WaCfg<D>::SMEM, st>>>(l.tq, l.tk, l.tv, a);
   return cudaGetLastError();
@@ -335,9 +342,12 @@ cudaError_t launch_window_attn(const WindowAttn &l, cudaStream_t st) {
   WindowAttnArgs a;
   a.o = static_cast<__nv_bfloat16 *>(l.o);
   a.o_sb = l.o_sb; a.o_sh = l.o_sh; a.o_sn = l.o_sn;
-  a.B = l.B; a.Hkv = l.Hkv; a.G = l.G; a.Hq = l.Hkv * l.G;
+  a.Hkv = l.Hkv; a.G = l.G;
   a.Nq = l.Nq; a.Nk = l.Nk; a.off = l.Nk - l.Nq;
-  a.nqb = (l.Nq + QBLK - 1) / QBLK;
+  const int P = window_attn_queries(l.G);
+  a.shift = 0;
+  while ((1 << a.shift) < P) ++a.shift;
+  a.ntile = (l.Nq + P - 1) / P;
   a.nkb = (l.Nk + KBLK - 1) / KBLK;
   a.window = l.window;
   a.sinks = l.sinks;

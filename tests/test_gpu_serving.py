@@ -448,6 +448,10 @@ def check_window(q, k, v, out, window, sinks, scale=0.0, decode=False):
     (1, 2, 1, 700, 4000, 128, 2000, 100, False),   # long windows
     (2, 4, 2, 1500, 2500, 128, 1700, 4, False),
     (1, 2, 2, 2000, 2000, 64, 1900, 70, False),
+    (1, 16, 1, 333, 700, 64, 200, 5, False),       # tiles of 8 queries of 16 heads
+    (2, 12, 1, 77, 1000, 128, 100, 0, False),      # of 32 queries of 4
+    (1, 20, 10, 300, 300, 64, 47, 1, False),       # of 64 queries of 2
+    (1, 32, 1, 9, 200, 64, 30, 0, False),          # two groups of 16 heads
     (1, 6, 1, 130, 1400, 128, 1270, 3, False),     # 23 and 24 blocks a query block
     (1, 6, 1, 130, 1500, 128, 1330, 3, False),
     (2, 8, 2, 1, 5000, 128, 2100, 4, True),        # decoding tiles
