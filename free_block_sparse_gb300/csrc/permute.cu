@@ -5,6 +5,7 @@
 // tasks).  y[:, :, t] = x[:, :, perm[t]] (gather) or y[:, :, perm[t]] = x[:, :, t] (scatter).
 // A pure row copy: each group of d/8 lanes moves one token row with 16-byte loads and stores.
 #include "common.cuh"
+#include "dependent.cuh"
 #include "kernels.h"
 
 #include <cuda_fp16.h>
@@ -79,6 +80,8 @@ __global__ void __launch_bounds__(256) convert_v_f16_kernel(const __nv_bfloat16 
   constexpr int VPR = D / 8;                 // 16-byte vectors per token row
   constexpr int ROWS = 2 * 256 / VPR;        // token rows per CTA
   const int h = blockIdx.y, b = blockIdx.z, H = gridDim.y;
+  let_dependents_start();
+  wait_for_earlier();
   const __nv_bfloat16 *xb = x + b * sb + h * sh;
   __half *yb = y + (static_cast<int64_t>(b) * H + h) * N * D;
   const int t0 = first + blockIdx.x * ROWS;
@@ -125,13 +128,9 @@ cudaError_t launch_convert_v_f16(const View &v, void *v16, const int32_t *perm, 
   const int rows = 2 * 256 / static_cast<int>(v.d / 8);
   dim3 grid(static_cast<unsigned>((last - first + rows - 1) / rows), static_cast<unsigned>(v.H), static_cast<unsigned>(v.B));
   const __nv_bfloat16 *x = static_cast<const __nv_bfloat16 *>(v.data);
-  if (v.d == 128)
-    convert_v_f16_kernel<128><<<grid, 256, 0, st>>>(x, v.sb, v.sh, v.sn, static_cast<__half *>(v16), (int)v.N, perm,
-                                                    status, (int)first, (int)last, (int)zero_from, (int)zero_to);
-  else
-    convert_v_f16_kernel<64><<<grid, 256, 0, st>>>(x, v.sb, v.sh, v.sn, static_cast<__half *>(v16), (int)v.N, perm,
-                                                   status, (int)first, (int)last, (int)zero_from, (int)zero_to);
-  return cudaGetLastError();
+  return launch_dependent(v.d == 128 ? convert_v_f16_kernel<128> : convert_v_f16_kernel<64>, grid, 256, 0, st, x, v.sb, v.sh, v.sn,
+                          static_cast<__half *>(v16), static_cast<int>(v.N), perm, status, static_cast<int>(first),
+                          static_cast<int>(last), static_cast<int>(zero_from), static_cast<int>(zero_to));
 }
 
 cudaError_t launch_permute(const View &x, const int32_t *perm, void *y, int64_t ysb, int64_t ysh, int64_t ysn,

@@ -30,6 +30,7 @@
 #include <cuda_fp16.h>
 
 #include "common.cuh"
+#include "dependent.cuh"
 #include "kernels.h"
 
 namespace sparge {
@@ -104,6 +105,7 @@ __global__ void __launch_bounds__(WA_THREADS, WaCfg<D>::CTAS)
   extern __shared__ __align__(1024) uint8_t smem[];
   // the 128-byte swizzle of TMA and of the MMA descriptors assumes 1024-byte aligned tiles
   if (smem_u32(smem) & 1023u) {
+    wait_for_earlier();
     if (threadIdx.x == 0) record_status(a.status, -4 /* SPARGE_ERR_CUDA */);
     return;
   }
@@ -141,6 +143,8 @@ __global__ void __launch_bounds__(WA_THREADS, WaCfg<D>::CTAS)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  let_dependents_start();
+  wait_for_earlier();
   const uint32_t tmem = cs.tmem_base, tmem_p = D == 64 ? cs.tmem_p : tmem + C::SCOL + KBLK;
 
   // block t of K or V into its stage, t % 2
@@ -332,8 +336,14 @@ cudaError_t launch_t(const WindowAttn &l, const WindowAttnArgs &a, cudaStream_t 
     return e;
   const int64_t grid = static_cast<int64_t>(l.B) * a.Hkv * (a.G / (128 >> a.shift)) * a.ntile;
   if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
-  window_attn_kernel<D><<<static_cast<unsigned>(grid), WA_THREADS, WaCfg<D>::SMEM, st>>>(l.tq, l.tk, l.tv, a);
-  return cudaGetLastError();
+  // Set up while the copy of V runs (4 x 16 heads of 323 queries 13.0 us, else 14.3), but for few CTAs of many blocks: those
+  // would crowd on the SMs that the copy leaves (210 CTAs of 65 blocks 65 us, else 62).
+  if (grid < 152 * WaCfg<D>::CTAS && a.window > 24 * KBLK) {
+    window_attn_kernel<D><<<static_cast<unsigned>(grid), WA_THREADS, WaCfg<D>::SMEM, st>>>(l.tq, l.tk, l.tv, a);
+    return cudaGetLastError();
+  }
+  return launch_dependent(window_attn_kernel<D>, dim3(static_cast<unsigned>(grid)), WA_THREADS, WaCfg<D>::SMEM, st, l.tq, l.tk,
+                          l.tv, a);
 }
 
 }  // namespace
