@@ -282,8 +282,8 @@ int sparge_attn_ex(const sparge_tensor *q, const sparge_tensor *k, const sparge_
  * position p = Nk - Nq + r and sees key c <= p when c > p - window (window >= 1: itself and the window - 1
  * before it) or c < sinks.  scale 0 means 1/sqrt(d).  Only the 64-key blocks that a query block sees are
  * loaded and multiplied; single keys are masked at the edges.  Keys and values that no query of the call
- * sees may hold anything; one that some queries see should be finite (an infinity or a NaN there can reach rows
- * of the same 128 queries that do not see it).  bf16 Q.K^T, P.V on f16 operands (V copied to f16 into the
+ * sees may hold anything; one that some queries see should be finite (an infinity or a NaN there can reach
+ * queries up to 127 places away that do not see it, of the heads that share the key/value head).  bf16 Q.K^T, P.V on f16 operands (V copied to f16 into the
  * workspace, |v| above 65504 saturates); up to 128 query rows per key/value head ((Hq/Hkv) Nq) run as row tiles of
  * 8 or 16, the keys split over CTAs, with V in place and P as two bf16.  ws: 256-byte aligned,
  * sparge_workspace_bytes(SPARGE_OP_WINDOW_ATTN, B, Hq, Hkv, Nk, d) bytes, used by one call at a time.
