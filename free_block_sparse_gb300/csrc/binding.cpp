@@ -199,8 +199,18 @@ PyObject *qk_norm_rope(const Args &a) {
   const at::Tensor &q = a.tensor(0, "q"), &k = a.tensor(1, "k");
   const Here h(q, "q");
   const sparge_tensor dq = h.rows(q, "q"), dk = h.rows(k, "k");
-  const at::Tensor qo = a.none(9) ? h.make_like(q) : a.tensor(9, "q_out");
-  const at::Tensor ko = a.none(10) ? h.make_like(k) : a.tensor(10, "k_out");
+  // small outputs share one allocation (64 tokens of 32 + 8 heads: 4.0 us of host time, 3.6 so); large ones do not, so that
+  // letting go of one frees it
+  at::Tensor qo, ko;
+  const int64_t nq = static_cast<int64_t>(q.nbytes()), nk = static_cast<int64_t>(k.nbytes()), k0 = (nq + 255) / 256 * 256;
+  if (a.none(9) && a.none(10) && nq + nk <= (1 << 20) && q.is_contiguous() && k.is_contiguous()) {
+    const at::Tensor block = h.make({k0 + nk}, at::kByte);
+    qo = Here::part(block, 0, q.sizes(), at::kBFloat16);
+    ko = Here::part(block, k0, k.sizes(), at::kBFloat16);
+  } else {
+    qo = a.none(9) ? h.make_like(q) : a.tensor(9, "q_out");
+    ko = a.none(10) ? h.make_like(k) : a.tensor(10, "k_out");
+  }
   sparge_tensor eq = h.rows(qo, "q_out"), ek = h.rows(ko, "k_out");
   const double *freq = nullptr;
   int64_t rot = 0;

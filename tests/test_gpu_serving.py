@@ -68,6 +68,24 @@ def test_norm_rope(B, Hq, Hkv, N, d, rot, interleaved, weights, far):
         within(y, ref, 2.0 ** -8 * ref.abs() + (2.0 ** -19 + 2.0 ** -50 * abs(far)) * mag)
 
 
+def test_norm_rope_outputs_stand_apart():
+    """The outputs that a small call makes are tensors of their own: writing one leaves the other, one given output is
+    filled and returned, and the empty call gives empty tensors."""
+    g = gen(26)
+    q, k = rand(g, 2, 3, 5, 64), rand(g, 2, 1, 5, 64)
+    freq = fbs.rope_freqs(64)
+    a, b = fbs.qk_norm_rope(q, k, freq)
+    keep = b.clone()
+    a.fill_(7.0)
+    assert torch.equal(b, keep) and a.is_contiguous() and b.is_contiguous()
+    mine = torch.empty_like(q)
+    c, d = fbs.qk_norm_rope(q, k, freq, q_out=mine)
+    assert c is mine and torch.equal(d, keep)
+    big = rand(g, 1, 8, 2000, 64)
+    x, y = fbs.qk_norm_rope(big, big, freq)
+    assert torch.equal(x, y) and x.untyped_storage().data_ptr() != y.untyped_storage().data_ptr()
+
+
 def test_norm_rope_strides_start_and_in_place():
     g = gen(2)
     B, Hq, Hkv, N, d = 2, 6, 2, 50, 128
