@@ -2,8 +2,8 @@
 cache's store and load, the attention over it, and the window attention.
 
 Tolerances.  A bf16 output is off by at most half a step, 2^-8 of its value.  Norm and rotation: about 30
-fp32 operations (2^-24 each) on what is summed, 2^-19 of it.  Attention: P rounded to f16 (2^-11) or, in
-decoding tiles, bf16 (2^-8), times sum P |v| (for the 4-bit cache |scale code|, what P multiplies); scores are
+fp32 operations (2^-24 each) on what is summed, 2^-19 of it.  Attention: P rounded to f16 (2^-11) or, with
+few rows, to two bf16 (2^-16), times sum P |v| (for the 4-bit cache |scale code|, what P multiplies); scores are
 fp32 sums of d <= 128 products, off by at most 2^-16 of sum |q||k| scale, and with the exponent's own error (2^-20)
 move the output by at most twice that times the largest |v|."""
 import math
@@ -448,7 +448,7 @@ def check_window(q, k, v, out, window, sinks, scale=0.0, decode=False):
     for b in range(B):
         pos = Nk - Nq + torch.arange(Nq, device="cuda")
         o, a, x = R.attention(q[b].double(), k[b].double(), v[b].double(), pos, window, sinks, scale or d ** -0.5)
-        p = 2.0 ** -8 if decode else 2.0 ** -11
+        p = 2.0 ** -16 if decode else 2.0 ** -11
         within(out[b], o, 2.0 ** -8 * o.abs() + p * a + 2 * (2.0 ** -16 * x + 2.0 ** -20) * v[b].double().abs().amax())
 
 
@@ -472,7 +472,7 @@ def check_window(q, k, v, out, window, sinks, scale=0.0, decode=False):
     (1, 32, 1, 9, 200, 64, 30, 0, False),          # two groups of 16 heads
     (1, 6, 1, 130, 1400, 128, 1270, 3, False),     # 23 and 24 blocks a query block
     (1, 6, 1, 130, 1500, 128, 1330, 3, False),
-    (2, 8, 2, 1, 5000, 128, 2100, 4, True),        # decoding tiles
+    (2, 8, 2, 1, 5000, 128, 2100, 4, True),        # few rows: tiles of 8 or 16
     (1, 8, 1, 7, 4001, 64, 2500, 0, True),
     (3, 4, 4, 1, 2300, 64, 10000, 0, True),
     (1, 16, 2, 16, 9000, 128, 3000, 130, True),
