@@ -281,8 +281,16 @@ PyObject *cache4_load(const Args &a) {
   }
   const bool made = a.none(2);
   if (slots.dim() != 2) type_error("%s must be a contiguous int64 (B, N) tensor", "slots");
-  const at::Tensor k = made ? h.make({slots.size(0), c.H, slots.size(1), c.d}, at::kBFloat16) : a.tensor(2, "k_out");
-  const at::Tensor v = made ? h.make({slots.size(0), c.H, slots.size(1), c.d}, at::kBFloat16) : a.tensor(3, "v_out");
+  const int64_t shape[4] = {slots.size(0), c.H, slots.size(1), c.d}, bytes = 2 * slots.numel() * c.H * c.d;
+  at::Tensor k, v;
+  if (made && bytes <= (1 << 19)) {  // small outputs share one allocation, as those of qk_norm_rope
+    const at::Tensor block = h.make({2 * bytes}, at::kByte);
+    k = Here::part(block, 0, shape, at::kBFloat16);
+    v = Here::part(block, bytes, shape, at::kBFloat16);
+  } else {
+    k = made ? h.make(shape, at::kBFloat16) : a.tensor(2, "k_out");
+    v = made ? h.make(shape, at::kBFloat16) : a.tensor(3, "v_out");
+  }
   sparge_tensor dk = h.rows(k, "k_out"), dv = h.rows(v, "v_out");
   done(sparge_cache4_load(&c, static_cast<int64_t *>(h.array(slots, at::kLong, "slots", {dk.B, dk.N})), made, &dk, &dv, h.s()));
   PyObject *r = result(a, 2, k);

@@ -255,6 +255,20 @@ def test_store_edge_values_in_long_rows(d):
         assert torch.equal(back[plain], want.float().bfloat16().view_as(back)[plain])
 
 
+def test_loaded_outputs_stand_apart():
+    """K and V that a small load makes are tensors of their own; a load of nothing gives empty ones."""
+    g = gen(27)
+    k, v = rand(g, 2, 1, 3, 64), rand(g, 2, 1, 3, 64)
+    pool = fbs.cache4_pool(1, 16, 1, 64)
+    slots = torch.arange(6, device="cuda").view(2, 3)
+    fbs.cache4_store(k, v, slots, pool)
+    a, b = fbs.cache4_load(pool, slots)
+    keep = b.clone()
+    a.fill_(7.0)
+    assert torch.equal(b, keep) and torch.equal(b, R.dequantise(*R.quantise(v.double())).float().bfloat16())
+    assert fbs.cache4_load(pool, slots[:0])[1].shape == (0, 1, 3, 64)
+
+
 @pytest.mark.parametrize("H,d,shift", [(3, 64, 8), (1, 64, 8), (5, 128, 8), (2, 128, 16)])
 def test_store_and_load_strided_rows_with_gaps(H, d, shift):
     """Rows that start on 16 but not on 32 bytes (or on 32, with gaps), long rows with padding in front and slots left out in
