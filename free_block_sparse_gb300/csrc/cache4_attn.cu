@@ -16,8 +16,9 @@
 //         x = k (sum_g s_g acc_g) + sum_g m_g (scale * sum of q over group g).
 //   O^T = V^T P^T: A = 16 channels x 16 tokens of codes, B = P^T s (f16: 11 bits, an eighth of the
 //         output's rounding) transposed in registers by movmatrix; the minima add sum P m per row.
-// P lies in [0, 2^8] (the reference follows the running maximum lazily) and s is scaled by a power
-// of two that follows its running maximum the same way, so P s stays in f16's range.
+// P lies in [0, 2^8] (the reference follows the running maximum lazily).  P s is scaled by a power of two per row and
+// channel group that follows its own running maximum the same way, so the largest P s of a row stays in
+// [2^3, 2^15]: what is less than 2^-17 of it loses bits in f16, what is less than 2^-28 is lost.
 //
 // Work: the (sequence, KV head, row tile) items' tiles in one line, cut into equal shares, one per CTA
 // (2 to 4 CTAs per SM), so ragged lengths fill the part evenly; every warp sums the lengths
@@ -46,7 +47,10 @@ namespace {
 // Tiles that an item's start and end weigh in a CTA's share (128 ragged sequences of 4 queries, d = 64, under a
 // window of 4096: 0 66 us, 2 58, 3 57; 64 sequences of up to 32K: 0 213, 3 206).
 constexpr int CA_ITEM = 3;
-constexpr float CA_SBOUND = 64.f;  // scaled V scales stay below this: P s < 2^8 2^6 < 65504
+// Where a row's largest P s goes when its power of two is set (to 2^(CA_ROOM - 1) .. 2^CA_ROOM), and how far it may grow before
+// that moves: to 2^15, within f16.
+constexpr int CA_ROOM = 4, CA_GROW = 15 - CA_ROOM;
+constexpr float CA_SBOUND = 128.f;  // 2^15 / 2^CA_RESCALE
 
 struct CacheAttnArgs : SplitArgs {
   const __nv_bfloat16 *q;
@@ -170,6 +174,26 @@ __device__ __forceinline__ uint32_t half2_of(float lo, float hi) {
 __device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }
 // exponent of |x| (0 and subnormals: -127)
 __device__ __forceinline__ int exponent_of(float x) { return static_cast<int>((__float_as_uint(x) >> 23) & 0xFFu) - 127; }
+
+// 2^e / f for a power of two f
+__device__ __forceinline__ float over2(float f, int e) {
+  return __uint_as_float((static_cast<uint32_t>(254 + e) << 23) - __float_as_uint(f));
+}
+
+// The power of two f on a row's P s of one channel group, set anew when y, the largest score + log2 s (a maximum over the
+// warp's tokens, reduced here), is 2^CA_GROW above what it was set for, and when the exponent reference (its negative m)
+// has moved, by al on what was summed (0: nothing before).  A row's f depends on the row's own P s alone: y that far above
+// means a scale past CA_SBOUND, and moves of the reference are the row's own.  Returns the factor on the sums.
+__device__ __forceinline__ float follow_scale(float &f, float y, float m, float al) {
+#pragma unroll
+  for (int o = 4; o <= 16; o <<= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, o));
+  const int e0 = CA_ROOM - exponent_of(f);
+  const float top = y + m;
+  if (!(top > static_cast<float>(e0 + CA_GROW)) && al == 1.f) return 1.f;
+  const int e = min(max(__float2int_ru(fmaxf(top, static_cast<float>(e0) + __log2f(al))), -100), 108);
+  f = pow2i(CA_ROOM - e);
+  return al * pow2i(min(max(e0 - e, -126), 127));
+}
 
 template <int D, int RT>
 __global__ void __launch_bounds__(CA_WARPS * 32, ca_ctas(D, RT)) cache4_attn_kernel(const CacheAttnArgs a) {
@@ -400,18 +424,24 @@ __global__ void __launch_bounds__(CA_WARPS * 32, ca_ctas(D, RT)) cache4_attn_ker
                                __shfl_sync(0xffffffffu, sum[w], from + 4) * a.scale_log2);
     }
 
-    float acc[MT][RT][4];   // O^T: rows g (channels 16 u + g, times 2^-24 vf) and g + 8 (times 2^-20 vf), columns 2c, 2c + 1
+    float acc[MT][RT][4];   // O^T: rows g (channels 16 u + g, times 2^-24 vfac) and g + 8 (times 2^-20 vfac), columns 2c, 2c + 1
     float2 zero[RT][NG];    // sum of P times the minima, and the sum of P (this lane's tokens, rows 2c and 2c + 1)
     float2 l[RT];
     float2 nref[RT], thr[RT];  // minus the exponent references, and the scores that move them
-    float vf = 0.f, sbound = -1.f;  // power of two on the V scales (0: not set yet), the scale that moves it
+    // per row and channel group: the power of two on P s.  It follows what the row itself sees, weighed by P, so neither a
+    // hidden token nor an improbable one nor the other group takes bits from the rest.
+    float2 vfac[NG][RT];
+    float sbound = 0.f;  // d = 64, where there is a register for it: CA_SBOUND over the largest of this lane's powers
 #pragma unroll
     for (int j = 0; j < RT; ++j) {
       nref[j] = both(0.f);
       thr[j] = both(-INFINITY);  // nothing seen yet: the first score moves it
       l[j] = both(0.f);
 #pragma unroll
-      for (int w = 0; w < NG; ++w) zero[j][w] = both(0.f);
+      for (int w = 0; w < NG; ++w) {
+        zero[j][w] = both(0.f);
+        vfac[w][j] = both(1.f);
+      }
     }
 #pragma unroll
     for (int u = 0; u < MT; ++u)
@@ -494,22 +524,11 @@ __global__ void __launch_bounds__(CA_WARPS * 32, ca_ctas(D, RT)) cache4_attn_ker
           }
         }
       }
-      // ---- the exponent reference and the V scales' power of two follow lazily ----
+      // ---- the exponent reference and the powers of two on P s follow lazily ----
       uint32_t vu[U][NG], vv[U][NG];
-      float smax = 0.f;
 #pragma unroll
-      for (int e = 0; e < U; ++e) {
-        words(p + e * S::REC + R::VW, vu[e], vv[e]);
-#pragma unroll
-        for (int w = 0; w < NG; ++w) {
-          if constexpr (EDGE) {  // places behind the sequence hold anything
-            if (gone[e] || tok[e] + g >= sp.len) vu[e][w] = 0u;
-            if (gone[e] || tok[e] + g + 8 >= sp.len) vv[e][w] = 0u;
-          }
-          smax = fmax3(smax, fabsf(bf16lo(vu[e][w])), fabsf(bf16lo(vv[e][w])));
-        }
-      }
-      bool move = smax > sbound;
+      for (int e = 0; e < U; ++e) words(p + e * S::REC + R::VW, vu[e], vv[e]);
+      bool move = false;
       float2 xm[RT];
 #pragma unroll
       for (int j = 0; j < RT; ++j) {
@@ -520,17 +539,20 @@ __global__ void __launch_bounds__(CA_WARPS * 32, ca_ctas(D, RT)) cache4_attn_ker
         }
         move = move || xm[j].x > thr[j].x || xm[j].y > thr[j].y;
       }
-      if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
-        for (int o = 4; o <= 16; o <<= 1) smax = fmaxf(smax, __shfl_xor_sync(0xffffffffu, smax, o));
-        float vr = 1.f;
-        if (smax > sbound) {  // the largest scale to [1, 2): the first tokens set it, outliers move it
-          const int e = min(max(exponent_of(smax), -100), 100);
-          const float nf = pow2i(-e);
-          vr = vf == 0.f ? 1.f : nf / vf;
-          vf = nf;
-          sbound = CA_SBOUND * pow2i(e);
+      for (int w = 0; w < NG; ++w) {
+        float smax = fmaxf(fabsf(bf16lo(vu[0][w])), fabsf(bf16lo(vv[0][w])));
+        if constexpr (U == 2) smax = fmax3(smax, fabsf(bf16lo(vu[U - 1][w])), fabsf(bf16lo(vv[U - 1][w])));
+        // while P is at most 2^CA_RESCALE this bounds P s of every row of this lane
+        if constexpr (NG == 1) {
+          move = move || smax > sbound;
+        } else {
+          float f = fmaxf(vfac[w][0].x, vfac[w][0].y);
+          if constexpr (RT == 2) f = fmax3(f, vfac[w][RT - 1].x, vfac[w][RT - 1].y);
+          move = move || smax * f > CA_SBOUND;
         }
+      }
+      if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
         for (int j = 0; j < RT; ++j) {
           float2 al;
@@ -538,15 +560,30 @@ __global__ void __launch_bounds__(CA_WARPS * 32, ca_ctas(D, RT)) cache4_attn_ker
           al.y = follow(thr[j].y, nref[j].y, xm[j].y);
           l[j] = fmul2(l[j], al);
 #pragma unroll
-          for (int w = 0; w < NG; ++w) zero[j][w] = fmul2(zero[j][w], al);
-          al = fmul2(al, both(vr));
+          for (int w = 0; w < NG; ++w) {
+            zero[j][w] = fmul2(zero[j][w], al);
+            float2 y = both(-INFINITY);  // score + log2 s, token by token (a hidden one: -inf)
 #pragma unroll
-          for (int u = 0; u < MT; ++u) {
-            acc[u][j][0] *= al.x;
-            acc[u][j][1] *= al.y;
-            acc[u][j][2] *= al.x;
-            acc[u][j][3] *= al.y;
+            for (int e = 0; e < U; ++e) {
+              const float lu = __log2f(fabsf(bf16lo(vu[e][w]))), lv = __log2f(fabsf(bf16lo(vv[e][w])));
+              y.x = fmax3(y.x, x0[e][j].x + lu, x1[e][j].x + lv);
+              y.y = fmax3(y.y, x0[e][j].y + lu, x1[e][j].y + lv);
+            }
+            const float fx = follow_scale(vfac[w][j].x, y.x, nref[j].x, al.x);
+            const float fy = follow_scale(vfac[w][j].y, y.y, nref[j].y, al.y);
+#pragma unroll
+            for (int u = 4 * w; u < 4 * w + 4; ++u) {
+              acc[u][j][0] *= fx;
+              acc[u][j][1] *= fy;
+              acc[u][j][2] *= fx;
+              acc[u][j][3] *= fy;
+            }
           }
+        }
+        if constexpr (NG == 1) {
+          float f = fmaxf(vfac[0][0].x, vfac[0][0].y);
+          if constexpr (RT == 2) f = fmax3(f, vfac[0][RT - 1].x, vfac[0][RT - 1].y);
+          sbound = CA_SBOUND * over2(f, 0);
         }
       }
       // ---- per record: P, its sums and the B operands of the second product, then O^T += V^T P^T ----
@@ -562,8 +599,8 @@ __global__ void __launch_bounds__(CA_WARPS * 32, ca_ctas(D, RT)) cache4_attn_ker
 #pragma unroll
           for (int w = 0; w < NG; ++w) {
             const float m0 = bf16hi(vu[e][w]), m1 = bf16hi(vv[e][w]);
-            float2 e0 = fmul2(p0, both(bf16lo(vu[e][w]) * vf)), e1 = fmul2(p1, both(bf16lo(vv[e][w]) * vf));
-            if constexpr (EDGE) {  // a hidden token adds nothing, whatever its scale and minimum are
+            float2 e0 = fmul2(fmul2(p0, vfac[w][j]), both(bf16lo(vu[e][w]))), e1 = fmul2(fmul2(p1, vfac[w][j]), both(bf16lo(vv[e][w])));
+            if constexpr (EDGE) {  // a hidden token adds nothing, whatever its scale and minimum are (behind the sequence: anything)
               float2 z0 = fmul2(p0, both(m0)), z1 = fmul2(p1, both(m1));
               if (p0.x == 0.f) e0.x = z0.x = 0.f;
               if (p0.y == 0.f) e0.y = z0.y = 0.f;
@@ -617,7 +654,6 @@ __global__ void __launch_bounds__(CA_WARPS * 32, ca_ctas(D, RT)) cache4_attn_ker
     // ---- the item's (or its share's) end: the warps' sums into shared memory, then merged ----
     float *mo = reinterpret_cast<float *>(ring);  // every copy of the item has landed and been read
     float2 *ml = reinterpret_cast<float2 *>(smem + S::OFF_ML);
-    const float back = vf == 0.f ? 0.f : 16777216.f / vf;  // 2^24 / vf
 #pragma unroll
     for (int j = 0; j < RT; ++j)
 #pragma unroll
@@ -634,10 +670,13 @@ __global__ void __launch_bounds__(CA_WARPS * 32, ca_ctas(D, RT)) cache4_attn_ker
           for (int o = 4; o <= 16; o <<= 1) z[w] += __shfl_xor_sync(0xffffffffu, z[w], o);
         }
         if (g == 0) ml[warp * 8 * RT + row] = make_float2((k ? thr[j].y : thr[j].x) == -INFINITY ? -INFINITY : -(k ? nref[j].y : nref[j].x), ls);
+        float back[NG];
+#pragma unroll
+        for (int w = 0; w < NG; ++w) back[w] = over2(k ? vfac[w][j].y : vfac[w][j].x, 24);
 #pragma unroll
         for (int u = 0; u < MT; ++u) {
-          mo[row * S::OROW + 16 * u + g] = fmaf(acc[u][j][k], back, z[u / 4]);
-          mo[row * S::OROW + 16 * u + 8 + g] = fmaf(acc[u][j][2 + k], back * 0.0625f, z[u / 4]);
+          mo[row * S::OROW + 16 * u + g] = fmaf(acc[u][j][k], back[u / 4], z[u / 4]);
+          mo[row * S::OROW + 16 * u + 8 + g] = fmaf(acc[u][j][2 + k], back[u / 4] * 0.0625f, z[u / 4]);
         }
       }
     ending = true;

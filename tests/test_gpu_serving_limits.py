@@ -1,0 +1,132 @@
+"""The serving operators where values, masks and sizes reach their ends, against fp64 definitions.
+
+Tolerances of the cache attention, per output channel: half a bf16 step of the result (2^-8); P times the scale in f16
+(2^-11) and subnormal below 2^-14 while a row's largest stays at 2^3 or above (2^-28 of the largest for each of n
+tokens' codes up to 15); scores are fp32 sums of d <= 128 products, off by at most 2^-16 of sum |q||k| scale, and with the
+exponent's own error (2^-20) they move each P by that share of itself, before and after the division by the sum."""
+import math
+
+import pytest
+import torch
+
+import free_block_sparse_gb300 as fbs
+import serving_ref as R
+from test_gpu_serving import filled, gen, rand, within
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    fbs.lib()
+    assert torch.cuda.is_available()
+    yield
+    torch.cuda.synchronize()
+    assert fbs.device_status() == 0
+
+
+# ------------------------------------------------------------------------------ values of uneven size in the cache
+def i32(*v):
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+def store_at(pool, table, t, k, v):
+    """Stores k and v (1, H, len(t), d) as tokens t of the sequence on table's first row."""
+    page = 16 * pool.shape[2]
+    t = torch.as_tensor(t, device="cuda")
+    fbs.cache4_store(k, v, (table[0].long()[t // page] * page + t % page)[None].contiguous(), pool)
+
+
+def check_channels(q, pool, table, n, out, d, window=0, sinks=0):
+    """One sequence; the tolerance of every channel from what this row and channel sum up."""
+    page = 16 * pool.shape[2]
+    t = torch.arange(n, device="cuda")
+    kn, ks, km, vn, vs, vm = (x[table[0].long()[t // page], :, t % page].transpose(0, 1) for x in R.read_pool(pool, d))
+    k, v, e = R.dequantise(kn, ks, km), R.dequantise(vn, vs, vm), R.dequantise(vn, vs, torch.zeros_like(vm))
+    Nq = q.shape[2]
+    pos = n - Nq + torch.arange(Nq, device="cuda")
+    o, a, x = R.attention(q[0].double(), k, v, pos, window, sinks, d ** -0.5, e)
+    _, av, _ = R.attention(q[0].double(), k, v, pos, window, sinks, d ** -0.5, v)
+    # P s, summed in place of its maximum, per channel group
+    s = vs.repeat_interleave(64, -1)
+    _, top, _ = R.attention(q[0].double(), k, v, pos, window, sinks, d ** -0.5, s)
+    within(out[0], o, 2.0 ** -8 * o.abs() + 2.0 ** -11 * a + 15 * n * 2.0 ** -28 * top + 2 * (2.0 ** -16 * x + 2.0 ** -20) * (av + a))
+
+
+SHAPES = [(2, 1, 64), (8, 1, 128), (4, 4, 64), (3, 5, 128)]  # heads of one KV head, queries, d: 8 and 16 rows
+
+
+@pytest.mark.parametrize("power", [16, 20, 24, 30, 60])
+@pytest.mark.parametrize("Hq,Nq,d", SHAPES)
+def test_hidden_values_of_any_size_change_nothing(Hq, Nq, d, power):
+    """Finite values between the first tokens and the window, in records that hold visible tokens too: the same bits."""
+    g = gen(40)
+    n = 400
+    pool, table = filled(g, [n], 1, d, 64)
+    q, kv = rand(g, 1, Hq, Nq, d), i32(n)
+    good = fbs.cache4_attn(q, pool, table, kv, window=50, sinks=2)
+    k, v = rand(g, 1, 1, 4, d), rand(g, 1, 1, 4, d, std=2.0 ** power)
+    store_at(pool, table, [2, 15, 337, 344], k, v)
+    assert torch.equal(fbs.cache4_attn(q, pool, table, kv, window=50, sinks=2), good)
+    check_channels(q, pool, table, n, good, d, 50, 2)
+
+
+@pytest.mark.parametrize("power", [0, 16, 24, 30])
+@pytest.mark.parametrize("Hq,d", [(2, 64), (5, 128)])
+def test_values_that_only_the_last_query_sees(Hq, d, power):
+    """The last token is hidden from the other queries of its tile: their rows keep their bits."""
+    g = gen(41)
+    n, Nq = 300, 3
+    pool, table = filled(g, [n], 1, d, 32)
+    q, kv = rand(g, 1, Hq, Nq, d), i32(n)
+    good = fbs.cache4_attn(q, pool, table, kv)
+    store_at(pool, table, [n - 1], rand(g, 1, 1, 1, d), rand(g, 1, 1, 1, d, std=2.0 ** power))
+    got = fbs.cache4_attn(q, pool, table, kv)
+    assert torch.equal(got[:, :, :-1], good[:, :, :-1])
+    check_channels(q, pool, table, n, got, d)
+
+
+@pytest.mark.parametrize("power", [12, 20, 24, 30, 40])
+@pytest.mark.parametrize("at", [0, 3, 200, 298])
+@pytest.mark.parametrize("Hq,Nq,d", SHAPES)
+def test_large_values_of_improbable_tokens(Hq, Nq, d, at, power):
+    """A token that every query sees with a probability of about 2^-30 and values up to 2^40 times the others': the others'
+    share of the result stays as exact as without it."""
+    g = gen(42)
+    n = 300
+    pool, table = filled(g, [n], 1, d, 16)
+    q = (1 + 0.25 * torch.randn(1, Hq, Nq, d, generator=g, device="cuda")).bfloat16()
+    k, v = rand(g, 1, 1, 1, d), rand(g, 1, 1, 1, d, std=2.0 ** power)
+    k[:] = -20.0 * d ** -0.5
+    store_at(pool, table, [at], k, v)
+    check_channels(q, pool, table, n, fbs.cache4_attn(q, pool, table, i32(n)), d)
+
+
+@pytest.mark.parametrize("power", [16, 24, 30])
+@pytest.mark.parametrize("Hq,Nq", [(8, 1), (4, 4)])
+def test_large_values_in_one_channel_group(Hq, Nq, power):
+    """Channels 64 to 127 of a few tokens 2^16 and more times the rest: channels 0 to 63 stay as exact as without them."""
+    g = gen(43)
+    n, d = 300, 128
+    pool, table = filled(g, [n], 1, d, 64)
+    q = rand(g, 1, Hq, Nq, d)
+    k, v = rand(g, 1, 1, 3, d), rand(g, 1, 1, 3, d)
+    v[..., 64:] *= 2.0 ** power
+    store_at(pool, table, [1, 100, 299], k, v)
+    check_channels(q, pool, table, n, fbs.cache4_attn(q, pool, table, i32(n)), d)
+
+
+@pytest.mark.parametrize("std", [2.0 ** -60, 2.0 ** -20, 2.0 ** 40])
+@pytest.mark.parametrize("Hq,Nq,d", SHAPES)
+def test_scores_that_climb_past_a_large_value(Hq, Nq, d, std):
+    """The first token has values 2^30 times the others', and scores climb by 100 behind it, so that its part fades; values
+    of any size as a whole."""
+    g = gen(44)
+    n = 400
+    pool, table = filled(g, [n], 1, d, 64)
+    q = (1 + 0.1 * torch.randn(1, Hq, Nq, d, generator=g, device="cuda")).bfloat16()
+    k, v = rand(g, 1, 1, n, d, std=0.1), rand(g, 1, 1, n, d, std=std)
+    k += (torch.arange(n, device="cuda") * (100.0 / n) * d ** -0.5)[:, None].bfloat16()
+    v[:, :, 0] *= 2.0 ** 30
+    store_at(pool, table, range(n), k, v)
+    check_channels(q, pool, table, n, fbs.cache4_attn(q, pool, table, i32(n)), d)
