@@ -53,11 +53,11 @@ __device__ __forceinline__ uint32_t max2_nan(uint32_t a, uint32_t b) {
 // 16 channels of a row, 32 bytes: in one piece where the rows allow it (a warp's accesses then fill whole sectors).
 __device__ __forceinline__ void load16(const __nv_bfloat16 *p, bool wide, uint32_t (&u)[8]) {
   if (wide) {
-    asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+    asm volatile("ld.global.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
                  : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7])
                  : "l"(p));
   } else {
-    const uint4 a = __ldg(reinterpret_cast<const uint4 *>(p)), b = __ldg(reinterpret_cast<const uint4 *>(p) + 1);
+    const uint4 a = *reinterpret_cast<const uint4 *>(p), b = reinterpret_cast<const uint4 *>(p)[1];
     u[0] = a.x; u[1] = a.y; u[2] = a.z; u[3] = a.w;
     u[4] = b.x; u[5] = b.y; u[6] = b.z; u[7] = b.w;
   }
@@ -231,7 +231,7 @@ __device__ __forceinline__ void expand16(const uint32_t (&n)[2], uint32_t word, 
 // The slot of token m; negative: padding (the token is left out).  A slot past the pool is never
 // used as an address: it is reported and left out.
 __device__ __forceinline__ int64_t slot_of(const Rows4 &a, int64_t m, bool report) {
-  const int64_t s = __ldg(a.slots + m);
+  const int64_t s = a.slots[m];
   if (s >= a.n_slots) {
     if (report) record_status(a.status, -1 /* SPARGE_ERR_INVALID_ARG */);
     return -1;
@@ -296,7 +296,7 @@ __device__ __forceinline__ void record4(const Rows4 &a) {
   const int lane = threadIdx.x & 31, i = lane % TR, j = (lane / TR) & 3, b = blockIdx.z;
   const int h = static_cast<int>(blockIdx.y * blockDim.x + threadIdx.x) / UNIT;
   const int64_t *slots = a.slots + static_cast<int64_t>(b) * a.N;
-  const int64_t last = __ldg(slots + a.N - 1);
+  const int64_t last = slots[a.N - 1];
   const int shift = last < 0 ? 0 : static_cast<int>((last - (a.N - 1)) & 15);
   const int n0 = static_cast<int>(blockIdx.x >> 1) * C4_TOKENS - shift;
   auto place = [&](int k) { return 2 * j + (k & 1) + 8 * (k >> 1); };
@@ -493,7 +493,7 @@ struct Request {
 
 __device__ __forceinline__ Request request_of(const TablesArgs &a, int r) {
   Request q;
-  const int len = __ldg(a.lens + r), add = __ldg(a.new_lens + r);
+  const int len = a.lens[r], add = a.new_lens[r];
   q.bad = len < 0 || add < 0 || add > a.N || static_cast<int64_t>(len) + add > INT32_MAX;
   q.len = q.bad ? 0 : len;
   q.add = q.bad ? 0 : add;
@@ -549,7 +549,7 @@ __global__ void __launch_bounds__(TB_THREADS) cache_tables_kernel(const TablesAr
       int64_t page = -1;
       if (col < a.width) {
         if (col < q.have) page = a.table[r * a.stride + col];
-        else if (first[k] + col - q.have < a.n_free) page = __ldg(a.free_pages + first[k] + col - q.have);
+        else if (first[k] + col - q.have < a.n_free) page = a.free_pages[first[k] + col - q.have];
       }
       if (page >= 0) slot = (page << a.shift) + (pos & mask);
     }
@@ -576,7 +576,7 @@ __global__ void __launch_bounds__(TB_THREADS) cache_tables_kernel(const TablesAr
       if (q.bad || q.have + q.need > a.width) record_status(a.status, -1 /* SPARGE_ERR_INVALID_ARG */);
     }
     for (int j = lane; j < q.need && q.have + j < a.width; j += 32)
-      a.table[r * a.stride + q.have + j] = first[k] + j < a.n_free ? __ldg(a.free_pages + first[k] + j) : -1;
+      a.table[r * a.stride + q.have + j] = first[k] + j < a.n_free ? a.free_pages[first[k] + j] : -1;
   }
 }
 

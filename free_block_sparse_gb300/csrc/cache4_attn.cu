@@ -62,7 +62,7 @@ struct CacheAttnArgs : SplitArgs {
   int window, sinks;     // window 0: none
   float scale_log2;
   int *status;
-  __device__ __forceinline__ bool empty(int b) const { return width == 0 || __ldg(lens + b) <= 0; }
+  __device__ __forceinline__ bool empty(int b) const { return width == 0 || lens[b] <= 0; }
 };
 
 // The records a sequence's queries see: the first `ns` (tokens that stay visible), then lo..hi-1.
@@ -71,7 +71,7 @@ struct Span {
 };
 __device__ __forceinline__ Span span_of(const CacheAttnArgs &a, int b) {
   Span s;
-  int len = __ldg(a.lens + b);
+  int len = a.lens[b];
   const int64_t cap = static_cast<int64_t>(a.width) << (a.rec_shift + 4);
   if (len > cap) len = static_cast<int>(cap);
   s.len = max(len, 0);
@@ -289,7 +289,7 @@ __global__ void __launch_bounds__(CA_WARPS * 32, ca_ctas(D, RT)) cache4_attn_ker
     bool bad = false;
     if (k < kend) {
       const int r = record_at(k);
-      const int page = __ldg(a.table + static_cast<int64_t>(b) * a.table_stride + (r >> a.rec_shift));
+      const int page = a.table[static_cast<int64_t>(b) * a.table_stride + (r >> a.rec_shift)];
       bad = page < 0 || page >= a.n_pages;
       if (bad)
         record_status(a.status, -1 /* SPARGE_ERR_INVALID_ARG */);
@@ -331,7 +331,7 @@ __global__ void __launch_bounds__(CA_WARPS * 32, ca_ctas(D, RT)) cache4_attn_ker
     int qi;
     const uint4 *qrow = query_of(j, qi);
 #pragma unroll
-    for (int w = 0; w < NW; ++w) qraw[j][w] = qrow != nullptr ? __ldg(qrow + 4 * w + c) : make_uint4(0u, 0u, 0u, 0u);
+    for (int w = 0; w < NW; ++w) qraw[j][w] = qrow != nullptr ? qrow[4 * w + c] : make_uint4(0u, 0u, 0u, 0u);
   };
 
   // The next item's first loads (queries, page numbers) go out before the end of the one before.

@@ -11,9 +11,18 @@ namespace sparge {
 // completed and its writes are visible.  Every thread of the kernel calls it before it reads or
 // writes global memory, and none returns without it, so the order along the stream is whole.
 // let_dependents_start() allows the same to the kernel behind this one.
+// What the kernel in front may have written is read with ordinary loads: the non-coherent ones (__ldg, ld.global.nc) want data
+// that nothing writes while the kernel lives, and it lives from before that write.
 // ------------------------------------------------------------------------------------------
 __device__ __forceinline__ void wait_for_earlier() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void let_dependents_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// 16 bytes that are read once: past the L1 cache
+__device__ __forceinline__ uint4 ld_once_v4(const void *p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
 
 template <typename... KArgs, typename... Args>
 inline cudaError_t launch_dependent(void (*kernel)(KArgs...), dim3 grid, unsigned threads, size_t smem, cudaStream_t st,

@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(NR_THREADS) norm_rope_kernel(const NormRopeArg
   wait_for_earlier();
   int cnt = load(h);
   __shared__ uint64_t turns[D / 2];
-  for (int j = threadIdx.x; j < a.rot / 2; j += NR_THREADS) turns[j] = turns64(__ldg(a.inv_freq + j));
+  for (int j = threadIdx.x; j < a.rot / 2; j += NR_THREADS) turns[j] = turns64(a.inv_freq[j]);
   __syncthreads();
   float cs[8], sn[8];
 #pragma unroll
@@ -111,7 +111,7 @@ __global__ void __launch_bounds__(NR_THREADS) norm_rope_kernel(const NormRopeArg
     sn[j] = 0.f;
   }
   if (t < rc) {
-    const int64_t pos = a.pos ? static_cast<int64_t>(__ldg(a.pos + mm)) : a.start + n;
+    const int64_t pos = a.pos ? static_cast<int64_t>(a.pos[mm]) : a.start + n;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const uint64_t ph = static_cast<uint64_t>(pos) * turns[8 * t + j];
@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(NR_THREADS) norm_rope_kernel(const NormRopeArg
       side = s;
       float w[16], o[16], p[16];
 #pragma unroll
-      for (int j = 0; j < 16; ++j) w[j] = a.w[s] ? __ldg(a.w[s] + 8 * (j < 8 ? p0 : p1) + (j & 7)) : 1.f;
+      for (int j = 0; j < 16; ++j) w[j] = a.w[s] ? a.w[s][8 * (j < 8 ? p0 : p1) + (j & 7)] : 1.f;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const int ia = INTER ? 2 * j : j, ib = INTER ? 2 * j + 1 : 8 + j;

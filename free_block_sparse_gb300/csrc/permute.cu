@@ -95,7 +95,7 @@ __global__ void __launch_bounds__(256) convert_v_f16_kernel(const __nv_bfloat16 
     if (t[u] < last) {
       int src = t[u];
       if (perm) {
-        src = __ldg(perm + t[u]);
+        src = perm[t[u]];
         if (static_cast<unsigned>(src) >= static_cast<unsigned>(N)) {
           if (part[u] == 0) record_status(status, -1 /* SPARGE_ERR_INVALID_ARG */);
           v[u] = make_uint4(0, 0, 0, 0);
@@ -103,7 +103,7 @@ __global__ void __launch_bounds__(256) convert_v_f16_kernel(const __nv_bfloat16 
         }
       }
       v[u] = t[u] >= zero_from && t[u] < zero_to ? make_uint4(0, 0, 0, 0)
-                                                 : ld_stream_v4(xb + static_cast<int64_t>(src) * sn + part[u] * 8);
+                                                 : ld_once_v4(xb + static_cast<int64_t>(src) * sn + part[u] * 8);
     }
   }
 #pragma unroll

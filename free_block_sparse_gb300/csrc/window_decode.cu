@@ -136,8 +136,8 @@ __global__ void __launch_bounds__(CA_WARPS * 32, 2)
       const uint32_t *src = reinterpret_cast<const uint32_t *>(a.q + b * a.q_sb + h * a.q_sh + static_cast<int64_t>(qi) * a.q_sn);
 #pragma unroll
       for (int u = 0; u < MT; ++u) {
-        qf[j][u][0] = ok ? __ldg(src + 8 * u + c) : 0u;
-        qf[j][u][1] = ok ? __ldg(src + 8 * u + 4 + c) : 0u;
+        qf[j][u][0] = ok ? src[8 * u + c] : 0u;
+        qf[j][u][1] = ok ? src[8 * u + 4 + c] : 0u;
       }
       const int p = a.Nk - a.Nq + qi;  // rows past the last are computed and dropped
       pos[j][0] = __shfl_sync(0xffffffffu, p, 8 * c);

@@ -130,3 +130,52 @@ def test_scores_that_climb_past_a_large_value(Hq, Nq, d, std):
     v[:, :, 0] *= 2.0 ** 30
     store_at(pool, table, range(n), k, v)
     check_channels(q, pool, table, n, fbs.cache4_attn(q, pool, table, i32(n)), d)
+
+
+# ----------------------------------------------------------------------------------------- calls one behind another
+@pytest.mark.parametrize("d,page,Nq", [(128, 64, 1), (64, 16, 4)])
+def test_steps_without_a_pause(d, page, Nq):
+    """Tables, norm and rotation, store, attention and window attention enqueued one behind another for many steps, every call
+    on what the one in front of it writes into the same buffers: the bits of a run that waits after every call."""
+    B, Hq, Hkv, steps, W = 5, 8, 2, 40, 40
+    g = gen(45)
+    x = [rand(g, steps, B, Hq, Nq, d), rand(g, steps, B, Hkv, Nq, d), rand(g, steps, B, Hkv, Nq, d)]
+    new = torch.randint(0, Nq + 1, (steps, B), generator=g, device="cuda", dtype=torch.int32)
+    ids = torch.randperm(B * W, generator=g, device="cuda").to(torch.int32)
+    freq = fbs.rope_freqs(d)
+
+    def run(wait):
+        pause = torch.cuda.synchronize if wait else lambda: None
+        pool = fbs.cache4_pool(B * W, page, Hkv, d)
+        table = torch.full((B, W), -1, dtype=torch.int32, device="cuda")
+        lens = [torch.zeros(B, dtype=torch.int32, device="cuda") for _ in range(2)]
+        slots = torch.empty(B, Nq, dtype=torch.int64, device="cuda")
+        pos, used = torch.empty(B, Nq, dtype=torch.int32, device="cuda"), torch.empty(1, dtype=torch.int32, device="cuda")
+        q, k, o = (torch.empty(B, h, Nq, d, dtype=torch.bfloat16, device="cuda") for h in (Hq, Hkv, Hq))
+        free = ids.clone()
+        outs = []
+        for i in range(steps):
+            a, b = lens[i % 2], lens[1 - i % 2]
+            fbs.cache_tables(a, new[i], free, table, page, Nq, slots=slots, positions=pos, kv_lens=b, used=used)
+            pause()
+            fbs.qk_norm_rope(x[0][i], x[1][i], freq, positions=pos, q_out=q, k_out=k)
+            pause()
+            fbs.cache4_store(k, x[2][i], slots, pool)
+            pause()
+            fbs.cache4_attn(q, pool, table, b, out=o)
+            pause()
+            fbs.qk_norm_rope(o, k, freq, start=i, q_out=o, k_out=k)
+            pause()
+            outs.append(fbs.window_attn(o, k, k, 3, 1))
+            pause()
+            kk, vv = fbs.cache4_load(pool, slots)
+            pause()
+            outs += [o.clone(), kk, vv, slots.clone(), b.clone()]
+            free = torch.roll(free, -B)        # the next step's pages
+            pause()
+        torch.cuda.synchronize()
+        return outs
+
+    want = run(True)
+    for _ in range(3):
+        assert all(torch.equal(torch.nan_to_num(x), torch.nan_to_num(y)) for x, y in zip(run(False), want))
