@@ -19,7 +19,7 @@ LIB = os.path.join(PKG, "libsparge.so")
 BINDING = os.path.join(PKG, "_binding.so")
 
 CUDA_SOURCES = ["api.cu", "pool_sim.cu", "score_gemm.cu", "score_select.cu", "bsattn.cu", "decode.cu", "permute.cu", "noalloc.cu", "q8prep.cu",
-                "norm_rope.cu", "cache4.cu", "cache4_attn.cu", "window_decode.cu", "window_attn.cu"]
+                "norm_rope.cu", "cache4.cu", "cache4_attn.cu", "window_decode.cu", "window_attn.cu", "window_v.cu"]
 CXX_SOURCES = ["hilbert.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

@@ -438,9 +438,9 @@ int attn_impl(const View &q, const View &k, const View &v, const uint8_t *mask, 
 
 // --- causal attention over a sliding window and the first tokens ---
 
-// The f16 copy of V, or a decoding call's partial rows.
+// The f16 copy of V with what it counts in, or a decoding call's partial rows.
 size_t window_ws_bytes(int64_t B, int64_t Hkv, int64_t Nk, int64_t d) {
-  const size_t few = window_decode_ws_bytes(B, Hkv, d), v16 = v16_bytes(B, Hkv, Nk, d);
+  const size_t few = window_decode_ws_bytes(B, Hkv, d), v16 = window_v_ws_bytes(B, Hkv, Nk, d);
   return few > v16 ? few : v16;
 }
 
@@ -475,10 +475,9 @@ int window_impl(const View &q, const View &k, const View &v, const View &o, int6
   // zero is NaN) reach nothing.
   const int64_t first = k.N - q.N - window + 1, lo = first > 0 ? first / KBLK * KBLK : 0;
   const int64_t ns = cdiv(sinks, KBLK) * KBLK;
-  cudaError_t e = launch_convert_v_f16(v, ws, nullptr, status_ptr(), s, lo, k.N, sinks, first);
-  if (e == cudaSuccess && lo > 0 && ns > 0)
-    e = launch_convert_v_f16(v, ws, nullptr, status_ptr(), s, 0, ns < lo ? ns : lo, sinks, first);
-  if (e != cudaSuccess) return cuda_fail(e, "convert_v launch");
+  const float *unit;
+  cudaError_t e = launch_window_v(v, ws, ns, lo, sinks, first, &unit, s);
+  if (e != cudaSuccess) return cuda_fail(e, "copy of V launch");
   View v16{ws, v.B, v.H, v.N, v.d, v.H * v.N * v.d, v.N * v.d, v.d};
   CUtensorMap tq, tk, tv;
   if ((rc = make_map(&tv, v16, 64, "v", CU_TENSOR_MAP_DATA_TYPE_FLOAT16))) return rc;
@@ -491,6 +490,7 @@ int window_impl(const View &q, const View &k, const View &v, const View &o, int6
     WindowAttn w;
     if ((rc = make_map(&tq, q, P, "q", CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 128 / P))) return rc;
     w.tq = tq; w.tk = tk; w.tv = tv;
+    w.v_unit = unit;
     w.o = const_cast<void *>(o.data);
     w.o_sb = o.sb; w.o_sh = o.sh; w.o_sn = o.sn;
     w.B = (int)q.B; w.Hkv = (int)k.H; w.G = (int)(q.H / k.H); w.Nq = (int)q.N; w.Nk = (int)k.N; w.d = (int)q.d;
@@ -513,6 +513,7 @@ int window_impl(const View &q, const View &k, const View &v, const View &o, int6
     l.lambda = -INFINITY;
     l.window = (int)window;
     l.sinks = (int)sinks;
+    l.v_unit = unit;
     l.status = status_ptr();
     e = launch_bsattn(l, s);
   }

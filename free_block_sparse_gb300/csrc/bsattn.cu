@@ -66,6 +66,7 @@ struct AttnArgs {
   const int32_t *dlist;
   const int *dcount;
   int window, sinks;  // WIN: row at position p sees keys c <= p with c > p - window or c < sinks
+  const float *v_unit;  // WIN: what the copy of V of each (batch, KV head) counts in
 };
 
 // Key blocks of a window (WIN) for the queries from position p0 on: the blocks of the first
@@ -732,7 +733,8 @@ __global__ void __launch_bounds__(NTHREADS, 2)
         a.part_ml[2 * prow + 1] = any ? l : 0.f;
       }
     } else {
-      const float inv_l = (l > 0.f) ? 1.f / l : 0.f;
+      float inv_l = (l > 0.f) ? 1.f / l : 0.f;
+      if constexpr (WIN) inv_l *= a.v_unit[static_cast<int64_t>(b) * a.Hkv + kvh];
       const float *svrow = PV8 ? a.sv + (static_cast<int64_t>(b) * a.Hkv + kvh) * D : nullptr;
       // the output row: token row_g, or token perm[row_g] of o under a token order (an entry outside
       // 0..N-1 is reported and its row left unwritten)
@@ -835,6 +837,7 @@ cudaError_t launch_bsattn(const AttnLaunch &l, cudaStream_t st) {
   a.qperm = l.qperm;
   a.window = l.window;
   a.sinks = l.sinks;
+  a.v_unit = l.v_unit;
   if (static_cast<int64_t>(a.B) * a.Hq * a.nqb == 0) return cudaSuccess;
   if (l.q8 != 0 && l.d != 128) return cudaErrorInvalidValue;
   if (l.decode) {  // bf16 only: the host picks this path for few queries per head, lambda off

@@ -151,8 +151,9 @@ struct AttnLaunch {
   int32_t *dlist;
   int *dcount;
   // window > 0 (bf16, causal, no mask): a query at position p sees key c <= p when c > p - window or
-  // c < sinks
+  // c < sinks; v_unit: what the copy of V of each (batch, KV head) counts in
   int window, sinks;
+  const float *v_unit;
 };
 
 // How a decoding call splits the key blocks of each (batch, KV head): about two CTAs per SM of a
@@ -190,6 +191,7 @@ struct WindowAttn {
   CUtensorMap tq, tk, tv;
   void *o;
   int64_t o_sb, o_sh, o_sn;
+  const float *v_unit;                      // what the copy of V of each (batch, KV head) counts in
   int B, Hkv, G, Nq, Nk, d, window, sinks;  // window and sinks at most Nk
   float scale;
   int *status;
@@ -228,9 +230,12 @@ cudaError_t launch_decode_combine(const float *part_o, const float *part_ml, int
                                   int d, void *o, int64_t o_sb, int64_t o_sh, int64_t o_sn, cudaStream_t st);
 
 // perm (or nullptr): row t of the copy is token perm[t] of v; bad entries are reported in *status.
-// Rows first .. last - 1 are copied (last < 0: all), rows zero_from .. zero_to - 1 of them as zeros.
-cudaError_t launch_convert_v_f16(const View &v, void *v16, const int32_t *perm, int *status, cudaStream_t st,
-                                 int64_t first = 0, int64_t last = -1, int64_t zero_from = 0, int64_t zero_to = 0);
+cudaError_t launch_convert_v_f16(const View &v, void *v16, const int32_t *perm, int *status, cudaStream_t st);
+// The window attention's f16 copy of V (window_v.cu), at the front of ws (window_v_ws_bytes): rows 0 .. front - 1 and
+// lo .. N - 1, of these rows zero_from .. zero_to - 1 as zeros.  *unit: what the copy of each (batch, KV head) counts in.
+size_t window_v_ws_bytes(int64_t B, int64_t H, int64_t N, int64_t d);
+cudaError_t launch_window_v(const View &v, void *ws, int64_t front, int64_t lo, int64_t zero_from, int64_t zero_to,
+                            const float **unit, cudaStream_t st);
 
 // 8-bit path: e4m3 copies of Q, K - mean(K) and V with their scales (all contiguous).
 struct Q8Ws {

@@ -71,12 +71,11 @@ __global__ void __launch_bounds__(256) permute_kernel(PermArgs a) {
 // cvt.rn.satfinite: exact for |v| <= 65504 (every bf16 value in f16 range keeps its 8 significant
 // bits), larger magnitudes saturate.  Grid (token chunks, H, B); each thread moves 16 bytes per
 // step with streaming loads, two independent vectors in flight.  With a token order, row t of
-// the copy is token perm[t] of V (an entry outside 0..N-1 gives a zero row and is reported).  Rows
-// zero_from .. zero_to - 1 become zero, whatever V holds there.
+// the copy is token perm[t] of V (an entry outside 0..N-1 gives a zero row and is reported).
 template <int D>
 __global__ void __launch_bounds__(256) convert_v_f16_kernel(const __nv_bfloat16 *x, int64_t sb, int64_t sh,
                                                              int64_t sn, __half *y, int N, const int32_t *perm,
-                                                             int *status, int first, int last, int zero_from, int zero_to) {
+                                                             int *status) {
   constexpr int VPR = D / 8;                 // 16-byte vectors per token row
   constexpr int ROWS = 2 * 256 / VPR;        // token rows per CTA
   const int h = blockIdx.y, b = blockIdx.z, H = gridDim.y;
@@ -84,7 +83,7 @@ __global__ void __launch_bounds__(256) convert_v_f16_kernel(const __nv_bfloat16 
   wait_for_earlier();
   const __nv_bfloat16 *xb = x + b * sb + h * sh;
   __half *yb = y + (static_cast<int64_t>(b) * H + h) * N * D;
-  const int t0 = first + blockIdx.x * ROWS;
+  const int t0 = blockIdx.x * ROWS;
   uint4 v[2];
   int t[2], part[2];
 #pragma unroll
@@ -92,7 +91,7 @@ __global__ void __launch_bounds__(256) convert_v_f16_kernel(const __nv_bfloat16 
     const int e = threadIdx.x + u * 256;
     t[u] = t0 + e / VPR;
     part[u] = e % VPR;
-    if (t[u] < last) {
+    if (t[u] < N) {
       int src = t[u];
       if (perm) {
         src = perm[t[u]];
@@ -102,13 +101,12 @@ __global__ void __launch_bounds__(256) convert_v_f16_kernel(const __nv_bfloat16 
           continue;
         }
       }
-      v[u] = t[u] >= zero_from && t[u] < zero_to ? make_uint4(0, 0, 0, 0)
-                                                 : ld_once_v4(xb + static_cast<int64_t>(src) * sn + part[u] * 8);
+      v[u] = ld_once_v4(xb + static_cast<int64_t>(src) * sn + part[u] * 8);
     }
   }
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
-    if (t[u] < last) {
+    if (t[u] < N) {
       uint4 o;
       o.x = pack_f16x2(bf16lo(v[u].x), bf16hi(v[u].x));
       o.y = pack_f16x2(bf16lo(v[u].y), bf16hi(v[u].y));
@@ -121,16 +119,13 @@ __global__ void __launch_bounds__(256) convert_v_f16_kernel(const __nv_bfloat16 
 
 }  // namespace
 
-cudaError_t launch_convert_v_f16(const View &v, void *v16, const int32_t *perm, int *status, cudaStream_t st,
-                                 int64_t first, int64_t last, int64_t zero_from, int64_t zero_to) {
-  if (last < 0) last = v.N;
-  if (v.B * v.H == 0 || first >= last) return cudaSuccess;
+cudaError_t launch_convert_v_f16(const View &v, void *v16, const int32_t *perm, int *status, cudaStream_t st) {
+  if (v.B * v.H * v.N == 0) return cudaSuccess;
   const int rows = 2 * 256 / static_cast<int>(v.d / 8);
-  dim3 grid(static_cast<unsigned>((last - first + rows - 1) / rows), static_cast<unsigned>(v.H), static_cast<unsigned>(v.B));
+  dim3 grid(static_cast<unsigned>((v.N + rows - 1) / rows), static_cast<unsigned>(v.H), static_cast<unsigned>(v.B));
   const __nv_bfloat16 *x = static_cast<const __nv_bfloat16 *>(v.data);
   return launch_dependent(v.d == 128 ? convert_v_f16_kernel<128> : convert_v_f16_kernel<64>, grid, 256, 0, st, x, v.sb, v.sh, v.sn,
-                          static_cast<__half *>(v16), static_cast<int>(v.N), perm, status, static_cast<int>(first),
-                          static_cast<int>(last), static_cast<int>(zero_from), static_cast<int>(zero_to));
+                          static_cast<__half *>(v16), static_cast<int>(v.N), perm, status);
 }
 
 cudaError_t launch_permute(const View &x, const int32_t *perm, void *y, int64_t ysb, int64_t ysh, int64_t ysn,

@@ -41,6 +41,7 @@ constexpr float WA_RESCALE = 8.f;
 
 struct WindowAttnArgs {
   __nv_bfloat16 *o;
+  const float *v_unit;
   int64_t o_sb, o_sh, o_sn;
   int Hkv, G, Nq, Nk, ntile, nkb, off, window, sinks;  // off = Nk - Nq
   int shift;                                           // P = 1 << shift queries of a tile, of 128 / P heads
@@ -303,7 +304,7 @@ __global__ void __launch_bounds__(WA_THREADS, WaCfg<D>::CTAS)
     __syncwarp();
     tc_fence_after();
     const bool all_ok = __all_sync(0xffffffffu, ok);
-    const float inv_l = l > 0.f ? 1.f / l : 0.f;
+    const float inv_l = l > 0.f ? a.v_unit[bk] / l : 0.f;  // (bk: this (batch, KV head))
     __nv_bfloat16 *orow = a.o + b * a.o_sb + (h0 + (r >> a.shift)) * a.o_sh + static_cast<int64_t>(qi) * a.o_sn;
 #pragma unroll 1
     for (int q = 0; q < (all_ok ? D / 16 : 0); ++q) {
@@ -351,6 +352,7 @@ cudaError_t launch_t(const WindowAttn &l, const WindowAttnArgs &a, cudaStream_t 
 cudaError_t launch_window_attn(const WindowAttn &l, cudaStream_t st) {
   WindowAttnArgs a;
   a.o = static_cast<__nv_bfloat16 *>(l.o);
+  a.v_unit = l.v_unit;
   a.o_sb = l.o_sb; a.o_sh = l.o_sh; a.o_sn = l.o_sn;
   a.Hkv = l.Hkv; a.G = l.G;
   a.Nq = l.Nq; a.Nk = l.Nk; a.off = l.Nk - l.Nq;

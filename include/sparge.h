@@ -162,7 +162,7 @@ typedef struct sparge_params {
  *   or e4m3 channel-major with the keys padded to a multiple of 64) and the fp32 scales;
  *   SPARGE_OP_ATTN_Q8: that plus the mask-prediction workspace and the mask.  Both return 0
  *   unless d = 128.
- * SPARGE_OP_WINDOW_ATTN: an f16 copy of V, or a decoding call's partial rows.
+ * SPARGE_OP_WINDOW_ATTN: an f16 copy of V with what it counts in, or a decoding call's partial rows.
  * op | SPARGE_OP_TOKEN_ORDER: the op's bytes plus room for bf16 copies of Q and K in a given
  *   token order (at the front of the workspace), for calls whose sparge_params.token_order is set
  *   (a call uses only the copies it needs; the room is reserved in full).
@@ -284,7 +284,8 @@ int sparge_attn_ex(const sparge_tensor *q, const sparge_tensor *k, const sparge_
  * loaded and multiplied; single keys are masked at the edges.  Keys and values that no query of the call
  * sees may hold anything; one that some queries see should be finite (an infinity or a NaN there can reach
  * queries up to 127 places away that do not see it, of the heads that share the key/value head).  bf16 Q.K^T, P.V on f16 operands (V copied to f16 into the
- * workspace, |v| above 65504 saturates); up to 128 query rows per key/value head ((Hq/Hkv) Nq) run as row tiles of
+ * workspace, times a power of two where a head's largest finite value lies outside of 2^-6 .. 65504: values of any size, each off by at
+ * most 2^-19 of that largest one); up to 128 query rows per key/value head ((Hq/Hkv) Nq) run as row tiles of
  * 8 or 16, the keys split over CTAs, with V in place and P as two bf16.  ws: 256-byte aligned,
  * sparge_workspace_bytes(SPARGE_OP_WINDOW_ATTN, B, Hq, Hkv, Nk, d) bytes, used by one call at a time.
  */

@@ -29,7 +29,7 @@ def test_the_check_finds_such_loads():
     assert NON_COHERENT.search('asm("ld.weak.global.nc.b32")') and not NON_COHERENT.search('asm("ld.global.L1::no_allocate.v8.b32 {")')
 
 
-@pytest.mark.parametrize("name", ["cache4.cu", "cache4_attn.cu", "rowsplit.cuh", "window_attn.cu", "window_decode.cu", "norm_rope.cu"])
+@pytest.mark.parametrize("name", ["cache4.cu", "cache4_attn.cu", "rowsplit.cuh", "window_attn.cu", "window_decode.cu", "window_v.cu", "norm_rope.cu"])
 def test_serving_kernels_read_with_ordinary_loads(name):
     assert not NON_COHERENT.findall(source(name))
 
@@ -40,4 +40,4 @@ def test_the_copy_of_v_reads_with_ordinary_loads():
 
 def test_every_file_with_dependent_kernels_is_looked_at():
     waits = sorted(f for f in os.listdir(CSRC) if "wait_for_earlier();" in source(f) and f != "dependent.cuh")
-    assert waits == ["cache4.cu", "cache4_attn.cu", "norm_rope.cu", "permute.cu", "rowsplit.cuh", "window_attn.cu", "window_decode.cu"]
+    assert waits == ["cache4.cu", "cache4_attn.cu", "norm_rope.cu", "permute.cu", "rowsplit.cuh", "window_attn.cu", "window_decode.cu", "window_v.cu"]

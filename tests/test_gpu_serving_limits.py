@@ -179,3 +179,54 @@ def test_steps_without_a_pause(d, page, Nq):
     want = run(True)
     for _ in range(3):
         assert all(torch.equal(torch.nan_to_num(x), torch.nan_to_num(y)) for x, y in zip(run(False), want))
+
+
+# ---------------------------------------------------------------------------------- window attention, values of any size
+def check_window_values(q, k, v, out, window, sinks, channels=slice(None)):
+    """Tolerance: half a bf16 step; P in f16 (2^-11), with up to 128 rows per KV head in two bf16 (2^-16); above that a copied
+    value is off by 2^-19 of the largest of its head; scores as in the cache attention, by what a row and channel sum up."""
+    B, Hq, Nq, d = q.shape
+    Hkv, Nk = k.shape[1:3]
+    few = Hq // Hkv * Nq <= 128
+    pos = Nk - Nq + torch.arange(Nq, device="cuda")
+    for b in range(B):
+        o, a, x = R.attention(q[b].double(), k[b].double(), v[b].double(), pos, window, sinks, d ** -0.5)
+        top = torch.nan_to_num(v[b].double(), 0, 0, 0).abs().amax((1, 2)).repeat_interleave(Hq // Hkv)[:, None, None]
+        tol = 2.0 ** -8 * o.abs() + (2.0 ** -16 if few else 2.0 ** -11) * a + (0 if few else 2.0 ** -19) * top
+        tol = tol + 4 * (2.0 ** -16 * x + 2.0 ** -20) * a
+        within(out[b][..., channels], o[..., channels], tol[..., channels])
+
+
+WINDOWS = [  # Hq, Hkv, Nq, Nk, d, window, sinks: at most 128 rows per KV head, just above, chunks, long windows
+    (4, 1, 32, 700, 64, 200, 4), (4, 1, 33, 700, 64, 200, 4), (2, 2, 128, 500, 128, 100, 70), (2, 2, 129, 500, 128, 100, 70),
+    (1, 1, 700, 900, 64, 300, 0), (6, 2, 300, 2000, 128, 1500, 5), (3, 1, 400, 400, 128, 64, 0),
+]
+
+
+@pytest.mark.parametrize("power", [-100, -40, -20, -10, 15, 20, 60, 110])
+@pytest.mark.parametrize("Hq,Hkv,Nq,Nk,d,window,sinks", WINDOWS)
+def test_window_attn_values_of_any_size(Hq, Hkv, Nq, Nk, d, window, sinks, power):
+    g = gen(46)
+    q, k, v = rand(g, 2, Hq, Nq, d), rand(g, 2, Hkv, Nk, d), rand(g, 2, Hkv, Nk, d, std=2.0 ** power)
+    v[1] = rand(g, Hkv, Nk, d)                    # the other sequence's values are of the usual size
+    check_window_values(q, k, v, fbs.window_attn(q, k, v, window, sinks), window, sinks)
+
+
+@pytest.mark.parametrize("Hq,Hkv,Nq,Nk,d,window,sinks", WINDOWS)
+def test_window_attn_infinite_and_unseen_values(Hq, Hkv, Nq, Nk, d, window, sinks):
+    """An infinity that every query sees stays in its channel and does not become a plausible number; finite values of any
+    size that no query sees change no bit."""
+    g = gen(47)
+    q, k, v = rand(g, 1, Hq, Nq, d), rand(g, 1, Hkv, Nk, d), rand(g, 1, Hkv, Nk, d)
+    good = fbs.window_attn(q, k, v, window, sinks)
+    hidden = Nk - Nq - window + 1
+    if hidden > sinks:
+        v2 = v.clone()
+        v2[:, :, sinks:hidden] = rand(g, 1, Hkv, hidden - sinks, d, std=2.0 ** 100)
+        assert torch.equal(fbs.window_attn(q, k, v2, window, sinks), good)
+    if sinks:
+        v[:, :, sinks - 1, 5], v[:, :, sinks - 1, 7] = math.inf, math.nan
+        got = fbs.window_attn(q, k, v, window, sinks)
+        assert not torch.isfinite(got[..., 5]).any() and torch.isnan(got[..., 7]).all()
+        rest = [c for c in range(d) if c not in (5, 7)]
+        check_window_values(q, k, v, got, window, sinks, rest)
