@@ -734,7 +734,8 @@ __global__ void __launch_bounds__(NTHREADS, 2)
       }
     } else {
       float inv_l = (l > 0.f) ? 1.f / l : 0.f;
-      if constexpr (WIN) inv_l *= a.v_unit[static_cast<int64_t>(b) * a.Hkv + kvh];
+      // (a sum that is NaN stays one: the filter takes a warp whose scores are all NaN for a hidden one and leaves its O at 0)
+      if constexpr (WIN) inv_l = l == 0.f ? 0.f : a.v_unit[static_cast<int64_t>(b) * a.Hkv + kvh] / l;
       const float *svrow = PV8 ? a.sv + (static_cast<int64_t>(b) * a.Hkv + kvh) * D : nullptr;
       // the output row: token row_g, or token perm[row_g] of o under a token order (an entry outside
       // 0..N-1 is reported and its row left unwritten)

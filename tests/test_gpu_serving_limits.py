@@ -230,3 +230,18 @@ def test_window_attn_infinite_and_unseen_values(Hq, Hkv, Nq, Nk, d, window, sink
         assert not torch.isfinite(got[..., 5]).any() and torch.isnan(got[..., 7]).all()
         rest = [c for c in range(d) if c not in (5, 7)]
         check_window_values(q, k, v, got, window, sinks, rest)
+
+
+@pytest.mark.parametrize("Hq,Hkv,Nq,Nk,d,window,sinks", WINDOWS)
+def test_window_attn_nan_queries(Hq, Hkv, Nq, Nk, d, window, sinks):
+    """Queries of NaN, alone and all 64 of a stretch, give NaN; the others keep their bits."""
+    g = gen(48)
+    q, k, v = rand(g, 1, Hq, Nq, d), rand(g, 1, Hkv, Nk, d), rand(g, 1, Hkv, Nk, d)
+    good = fbs.window_attn(q, k, v, window, sinks)
+    bad = torch.zeros(Nq, dtype=torch.bool, device="cuda")
+    bad[3] = True
+    if Nq >= 256:
+        bad[128:192] = True
+    q[:, :, bad] = math.nan
+    got = fbs.window_attn(q, k, v, window, sinks)
+    assert torch.isnan(got[:, :, bad]).all() and torch.equal(got[:, :, ~bad], good[:, :, ~bad])
