@@ -126,7 +126,7 @@ __global__ void __launch_bounds__(NR_THREADS) norm_rope_kernel(const NormRopeArg
     const int s = h >= a.H[0] ? 1 : 0;
     // The weights go into the rotation: pair number j of the thread is channels (ia, ib) of its 16, and
     // y_a = r (x_a w_a cos - x_b w_b sin), y_b = r (x_b w_b cos + x_a w_a sin); own[i] multiplies channel
-    // i itself, other[i] its partner.  Channels that do not turn have cos 1 and sin 0.
+    // i itself, other[i] its partner.
     if (s != side) {
       side = s;
       float w[16], o[16], p[16];
@@ -178,11 +178,19 @@ __global__ void __launch_bounds__(NR_THREADS) norm_rope_kernel(const NormRopeArg
       // x r first: x w may leave fp32's range where the norm would have brought it back
 #pragma unroll
       for (int j = 0; j < 8; ++j) f[j] = fmul2(f[j], r2);
+      if (t < rc) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float2 partner = INTER ? make_float2(f[j].y, f[j].x) : f[(j + 4) % 8];
-        const float2 g = ffma2(f[j], own[j], fmul2(partner, other[j]));
-        o[j] = pack_bf16x2(g.x, g.y);
+        for (int j = 0; j < 8; ++j) {
+          const float2 partner = INTER ? make_float2(f[j].y, f[j].x) : f[(j + 4) % 8];
+          const float2 g = ffma2(f[j], own[j], fmul2(partner, other[j]));
+          o[j] = pack_bf16x2(g.x, g.y);
+        }
+      } else {  // channels that do not turn have no partner: an infinity or a NaN stays in its own
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float2 g = fmul2(f[j], own[j]);
+          o[j] = pack_bf16x2(g.x, g.y);
+        }
       }
       if (live) {
         *reinterpret_cast<uint4 *>(y + u * a.ysh[s] + 8 * p0) = make_uint4(o[0], o[1], o[2], o[3]);

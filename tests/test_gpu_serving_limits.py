@@ -245,3 +245,27 @@ def test_window_attn_nan_queries(Hq, Hkv, Nq, Nk, d, window, sinks):
     q[:, :, bad] = math.nan
     got = fbs.window_attn(q, k, v, window, sinks)
     assert torch.isnan(got[:, :, bad]).all() and torch.equal(got[:, :, ~bad], good[:, :, ~bad])
+
+
+# ------------------------------------------------------------------------------------------------ norm and rotation
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("d,rot", [(64, 0), (128, 0), (128, 64), (64, 16), (64, 64), (128, 128)])
+def test_norm_rope_infinities_stay_where_the_formula_has_them(d, rot, interleaved):
+    """An infinity makes its own channel NaN (and its pair's, where it turns) and the rest of its row 0; a NaN makes
+    the row NaN; an infinite weight of a channel that does not turn reaches that channel alone."""
+    g = gen(49)
+    q, k = rand(g, 1, d, 5, d), rand(g, 1, 2, 5, d)
+    c = torch.arange(d, device="cuda")
+    q[0, c, 1, c] = math.inf                       # head i: channel i
+    q[0, c, 3, c] = -math.inf
+    q[0, 2, 2, 7] = math.nan
+    w = torch.ones(d, device="cuda")
+    if rot < d:
+        w[d - 3] = math.inf
+    freq = fbs.rope_freqs(rot) if rot else None
+    pos = 3 + torch.arange(5, dtype=torch.int32, device="cuda")[None]
+    a, _ = fbs.qk_norm_rope(q, k, freq, positions=pos, q_weight=w, interleaved=interleaved)
+    ref, mag = R.norm_rope(q.double(), w, freq, pos, 1e-6, interleaved)
+    assert torch.equal(torch.isnan(a), torch.isnan(ref)) and torch.equal(torch.isinf(a), torch.isinf(ref))
+    fine = torch.isfinite(ref)
+    within(a[fine], ref[fine], (2.0 ** -8 * ref.abs() + 2.0 ** -19 * mag)[fine])
