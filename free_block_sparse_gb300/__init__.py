@@ -168,6 +168,8 @@ def _load_binding():
     if _binding_module is None:
         lib()     # the library the binding calls into
         _torch()  # and torch's own libraries
+        if not os.path.exists(os.path.join(_PKG, "_binding.so")):
+            raise RuntimeError("_binding.so is not built (it needs torch at build time); run free_block_sparse_gb300.build.build()")
         from . import _binding as m
         m.set_error(SpargeError)
         _binding_module = m

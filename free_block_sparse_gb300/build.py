@@ -1,6 +1,7 @@
 """Build libsparge.so in-tree: nvcc for sm_103a, one object per source file, compiled in
 parallel, then one shared-library link; and _binding.so, the Python binding of the serving calls,
-against the installed torch's headers and libraries.  No CMake; runs the same on x86_64 and aarch64 hosts."""
+against the installed torch's headers and libraries (left out where there is no torch: the C library needs none).
+No CMake; runs the same on x86_64 and aarch64 hosts."""
 from __future__ import annotations
 
 import concurrent.futures as cf
@@ -45,11 +46,11 @@ def _stale(obj, deps):
     return any(os.path.getmtime(d) > t for d in deps)
 
 
-def _torch_dir() -> str:
-    """Where torch is installed (found without importing it)."""
+def _torch_dir():
+    """Where torch is installed (found without importing it), or None."""
     spec = importlib.util.find_spec("torch")
     if spec is None or not spec.submodule_search_locations:
-        raise RuntimeError("torch not found (its headers are needed for the Python binding)")
+        return None
     return list(spec.submodule_search_locations)[0]
 
 
@@ -97,12 +98,13 @@ def build(verbose: bool = False, force: bool = False, ptxas_verbose: bool = Fals
         if force or _stale(o, [s] + headers):
             jobs.append([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-c", s, "-o", o])
     binding_obj = os.path.join(BUILD, "binding.cpp.o")
-    binding_cmd, binding_deps = _binding_job(binding_obj)
-    binding_stale = force or _stale(binding_obj, binding_deps)
+    binding, binding_stale = _torch_dir() is not None, False
+    if binding:
+        binding_cmd, binding_deps = _binding_job(binding_obj)
+        binding_stale = force or _stale(binding_obj, binding_deps)
     lib_stale = force or bool(jobs) or not os.path.exists(LIB)
-    if binding_stale:
-        jobs.append(binding_cmd)
-    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(jobs), os.cpu_count() or 4))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(jobs) + 1, os.cpu_count() or 4))) as ex:
+        compiled = ex.submit(_run, binding_cmd) if binding_stale else None
         for out in ex.map(_run, jobs):
             if verbose and out.strip():
                 print(out)
@@ -110,8 +112,12 @@ def build(verbose: bool = False, force: bool = False, ptxas_verbose: bool = Fals
         tmp = LIB + ".tmp"
         _run([nvcc] + ARCH + ["-shared", "-o", tmp] + objs)
         os.replace(tmp, LIB)
-    if binding_stale or lib_stale or not os.path.exists(BINDING):
+    if compiled is not None:
+        compiled.result()   # a binding that does not compile is an error, after the library is there
+    if binding and (binding_stale or lib_stale or not os.path.exists(BINDING)):
         _link_binding(binding_obj)
+    elif not binding and verbose:
+        print("torch not found: the Python binding of the serving calls is left out")
     return LIB
 
 
