@@ -25,6 +25,18 @@ struct PyFail {};  // a Python exception is set
   throw PyFail{};
 }
 
+// f() while other Python threads run: what may wait for the GPU (an allocation that frees others first, a launch into a full
+// queue) belongs there.  f touches no Python object and raises no PyFail: a call's arguments are read and checked before.
+// (One such stretch per call: each takes a few tenths of a microsecond.)
+template <typename F>
+auto unlocked(F f) {
+  struct Unlock {
+    PyThreadState *state = PyEval_SaveThread();
+    ~Unlock() { PyEval_RestoreThread(state); }
+  } u;
+  return f();
+}
+
 // The call's arguments after `self`, by position.
 struct Args {
   PyObject *const *v;
@@ -90,6 +102,9 @@ struct Here {
     check(t, name);
     if (t.scalar_type() != at::kBFloat16 || t.dim() != 4 || t.stride(3) != 1)
       type_error("%s: expected a bf16 (B, H, N, d) tensor with contiguous last dim", name);
+    return describe(t);
+  }
+  static sparge_tensor describe(const at::Tensor &t) {
     return sparge_tensor{t.data_ptr(), SPARGE_BF16, 0, t.size(0), t.size(1), t.size(2), t.size(3),
                          t.stride(0),  t.stride(1), t.stride(2)};
   }
@@ -174,23 +189,35 @@ PyObject *tuple_of(T... o) {
   return r;
 }
 
-at::Tensor workspace(const Args &a, int i, const Here &h, size_t bytes) {
-  if (a.none(i)) return h.make({static_cast<int64_t>(bytes ? bytes : 1)}, at::kByte);
+// Argument i, a bf16 (B, H, N, d) tensor, or an undefined tensor for None.
+at::Tensor given_rows(const Args &a, int i, const Here &h, const char *name) {
+  if (a.none(i)) return {};
+  h.rows(a.tensor(i, name), name);
+  return a.tensor(i, name);
+}
+at::Tensor given_workspace(const Args &a, int i, const Here &h) {
+  if (a.none(i)) return {};
   const at::Tensor &t = a.tensor(i, "ws");
   h.check(t, "ws");
   if (!t.is_contiguous()) type_error("%s must be contiguous", "ws");
   return t;
 }
+at::Tensor make_workspace(const Here &h, size_t bytes) { return h.make({static_cast<int64_t>(bytes ? bytes : 1)}, at::kByte); }
 
 // (q, k, v, window, sinks, scale, out, ws)
 PyObject *window_attn(const Args &a) {
   const at::Tensor &q = a.tensor(0, "q"), &k = a.tensor(1, "k"), &v = a.tensor(2, "v");
   const Here h(q, "q");
   const sparge_tensor dq = h.rows(q, "q"), dk = h.rows(k, "k"), dv = h.rows(v, "v");
-  const at::Tensor out = a.none(6) ? h.make_like(q) : a.tensor(6, "out");
-  sparge_tensor dout = h.rows(out, "out");
-  const at::Tensor ws = workspace(a, 7, h, sparge_workspace_bytes(SPARGE_OP_WINDOW_ATTN, dk.B, dq.H, dk.H, dk.N, dk.d));
-  done(sparge_window_attn(&dq, &dk, &dv, a.integer(3), a.integer(4), a.real(5), &dout, ws.data_ptr(), ws.nbytes(), h.s()));
+  const int64_t window = a.integer(3), sinks = a.integer(4);
+  const float scale = a.real(5);
+  at::Tensor out = given_rows(a, 6, h, "out"), ws = given_workspace(a, 7, h);
+  done(unlocked([&] {
+    if (!out.defined()) out = h.make_like(q);
+    if (!ws.defined()) ws = make_workspace(h, sparge_workspace_bytes(SPARGE_OP_WINDOW_ATTN, dk.B, dq.H, dk.H, dk.N, dk.d));
+    sparge_tensor o = Here::describe(out);
+    return sparge_window_attn(&dq, &dk, &dv, window, sinks, scale, &o, ws.data_ptr(), ws.nbytes(), h.s());
+  }));
   return result(a, 6, out);
 }
 
@@ -199,19 +226,7 @@ PyObject *qk_norm_rope(const Args &a) {
   const at::Tensor &q = a.tensor(0, "q"), &k = a.tensor(1, "k");
   const Here h(q, "q");
   const sparge_tensor dq = h.rows(q, "q"), dk = h.rows(k, "k");
-  // small outputs share one allocation (64 tokens of 32 + 8 heads: 4.0 us of host time, 3.6 so); large ones do not, so that
-  // letting go of one frees it
-  at::Tensor qo, ko;
-  const int64_t nq = static_cast<int64_t>(q.nbytes()), nk = static_cast<int64_t>(k.nbytes()), k0 = (nq + 255) / 256 * 256;
-  if (a.none(9) && a.none(10) && nq + nk <= (1 << 20) && q.is_contiguous() && k.is_contiguous()) {
-    const at::Tensor block = h.make({k0 + nk}, at::kByte);
-    qo = Here::part(block, 0, q.sizes(), at::kBFloat16);
-    ko = Here::part(block, k0, k.sizes(), at::kBFloat16);
-  } else {
-    qo = a.none(9) ? h.make_like(q) : a.tensor(9, "q_out");
-    ko = a.none(10) ? h.make_like(k) : a.tensor(10, "k_out");
-  }
-  sparge_tensor eq = h.rows(qo, "q_out"), ek = h.rows(ko, "k_out");
+  at::Tensor qo = given_rows(a, 9, h, "q_out"), ko = given_rows(a, 10, h, "k_out");
   const double *freq = nullptr;
   int64_t rot = 0;
   if (!a.none(2)) {
@@ -223,9 +238,25 @@ PyObject *qk_norm_rope(const Args &a) {
   const void *w[2];
   for (int i = 0; i < 2; ++i)
     w[i] = a.none(5 + i) ? nullptr : h.array(a.tensor(5 + i, "weight"), at::kFloat, i ? "k_weight" : "q_weight", {dq.d});
-  done(sparge_qk_norm_rope(&dq, &dk, static_cast<const int32_t *>(pos), a.integer(4), freq,
-                           static_cast<int>(rot > INT32_MAX ? INT32_MAX : rot), a.truth(8), static_cast<const float *>(w[0]),
-                           static_cast<const float *>(w[1]), a.real(7), &eq, &ek, h.s()));
+  const int64_t start = a.integer(4);
+  const float eps = a.real(7);
+  const bool interleaved = a.truth(8);
+  done(unlocked([&] {
+    // small outputs share one allocation (64 tokens of 32 + 8 heads: 4.0 us of host time, 3.6 so); large ones do not, so that
+    // letting go of one frees it
+    const int64_t nq = static_cast<int64_t>(q.nbytes()), nk = static_cast<int64_t>(k.nbytes()), k0 = (nq + 255) / 256 * 256;
+    if (!qo.defined() && !ko.defined() && nq + nk <= (1 << 20) && q.is_contiguous() && k.is_contiguous()) {
+      const at::Tensor block = h.make({k0 + nk}, at::kByte);
+      qo = Here::part(block, 0, q.sizes(), at::kBFloat16);
+      ko = Here::part(block, k0, k.sizes(), at::kBFloat16);
+    }
+    if (!qo.defined()) qo = h.make_like(q);
+    if (!ko.defined()) ko = h.make_like(k);
+    sparge_tensor eq = Here::describe(qo), ek = Here::describe(ko);
+    return sparge_qk_norm_rope(&dq, &dk, static_cast<const int32_t *>(pos), start, freq,
+                               static_cast<int>(rot > INT32_MAX ? INT32_MAX : rot), interleaved, static_cast<const float *>(w[0]),
+                               static_cast<const float *>(w[1]), eps, &eq, &ek, h.s());
+  }));
   PyObject *r = result(a, 9, qo);
   return tuple_of(r, result(a, 10, ko));
 }
@@ -236,25 +267,35 @@ PyObject *cache_tables(const Args &a) {
                    &table = a.tensor(3, "table");
   const Here h(lens, "lens");
   const int64_t R = lens.numel(), N = a.integer(5);
+  const int page = a.small(4);
   if (N < 0 || N > (int64_t(1) << 30) || R > 65535) {
     PyErr_SetString(PyExc_ValueError, "N must be in 0..2^30, the requests at most 65535");
     throw PyFail{};
   }
-  // the outputs that are not given share one allocation (four of them take the host longer than the kernel the GPU)
-  at::Tensor block;
-  if (a.none(6) || a.none(7) || a.none(8) || a.none(9)) block = h.make({12 * R * N + 4 * R + 4}, at::kByte);
-  const at::Tensor slots = a.none(6) ? Here::part(block, 0, {R, N}, at::kLong) : a.tensor(6, "slots");
-  const at::Tensor pos = a.none(7) ? Here::part(block, 8 * R * N, {R, N}, at::kInt) : a.tensor(7, "positions");
-  const at::Tensor kv = a.none(8) ? Here::part(block, 12 * R * N, {R}, at::kInt) : a.tensor(8, "kv_lens");
-  const at::Tensor used = a.none(9) ? Here::part(block, 12 * R * N + 4 * R, {1}, at::kInt) : a.tensor(9, "used");
   const auto i32 = [&](const at::Tensor &t, const char *name, at::IntArrayRef shape) {
     return static_cast<int32_t *>(h.array(t, at::kInt, name, shape));
   };
+  const auto given = [&](int i, at::ScalarType type, const char *name, at::IntArrayRef shape) {
+    if (a.none(i)) return at::Tensor();
+    h.array(a.tensor(i, name), type, name, shape);
+    return a.tensor(i, name);
+  };
+  const int32_t *pl = i32(lens, "lens", {R}), *pa = i32(add, "new_lens", {R}), *pf = i32(free, "free_pages", {});
   const int64_t stride = h.table(table, R);
-  done(sparge_cache_tables(i32(lens, "lens", {R}), i32(add, "new_lens", {R}), R, N, a.small(4), i32(free, "free_pages", {}),
-                           free.numel(), static_cast<int32_t *>(table.data_ptr()), table.size(1), stride,
-                           static_cast<int64_t *>(h.array(slots, at::kLong, "slots", {R, N})), i32(pos, "positions", {R, N}),
-                           i32(kv, "kv_lens", {R}), i32(used, "used", {1}), h.s()));
+  at::Tensor slots = given(6, at::kLong, "slots", {R, N}), pos = given(7, at::kInt, "positions", {R, N}),
+             kv = given(8, at::kInt, "kv_lens", {R}), used = given(9, at::kInt, "used", {1});
+  done(unlocked([&] {
+    // the outputs that are not given share one allocation (four of them take the host longer than the kernel the GPU)
+    at::Tensor block;
+    if (!slots.defined() || !pos.defined() || !kv.defined() || !used.defined()) block = h.make({12 * R * N + 4 * R + 4}, at::kByte);
+    if (!slots.defined()) slots = Here::part(block, 0, {R, N}, at::kLong);
+    if (!pos.defined()) pos = Here::part(block, 8 * R * N, {R, N}, at::kInt);
+    if (!kv.defined()) kv = Here::part(block, 12 * R * N, {R}, at::kInt);
+    if (!used.defined()) used = Here::part(block, 12 * R * N + 4 * R, {1}, at::kInt);
+    return sparge_cache_tables(pl, pa, R, N, page, pf, free.numel(), static_cast<int32_t *>(table.data_ptr()), table.size(1), stride,
+                               static_cast<int64_t *>(slots.data_ptr()), static_cast<int32_t *>(pos.data_ptr()),
+                               static_cast<int32_t *>(kv.data_ptr()), static_cast<int32_t *>(used.data_ptr()), h.s());
+  }));
   PyObject *r0 = result(a, 6, slots), *r1 = result(a, 7, pos), *r2 = result(a, 8, kv);
   return tuple_of(r0, r1, r2, result(a, 9, used));
 }
@@ -265,8 +306,8 @@ PyObject *cache4_store(const Args &a) {
   const Here h(k, "k");
   const sparge_tensor dk = h.rows(k, "k"), dv = h.rows(v, "v");
   const sparge_cache4 c = h.pool(a.tensor(3, "pool"));
-  done(sparge_cache4_store(&dk, &dv, static_cast<int64_t *>(h.array(a.tensor(2, "slots"), at::kLong, "slots", {dk.B, dk.N})),
-                           &c, h.s()));
+  const int64_t *slots = static_cast<int64_t *>(h.array(a.tensor(2, "slots"), at::kLong, "slots", {dk.B, dk.N}));
+  done(unlocked([&] { return sparge_cache4_store(&dk, &dv, slots, &c, h.s()); }));
   Py_RETURN_NONE;
 }
 
@@ -281,18 +322,22 @@ PyObject *cache4_load(const Args &a) {
   }
   const bool made = a.none(2);
   if (slots.dim() != 2) type_error("%s must be a contiguous int64 (B, N) tensor", "slots");
-  const int64_t shape[4] = {slots.size(0), c.H, slots.size(1), c.d}, bytes = 2 * slots.numel() * c.H * c.d;
-  at::Tensor k, v;
-  if (made && bytes <= (1 << 19)) {  // small outputs share one allocation, as those of qk_norm_rope
-    const at::Tensor block = h.make({2 * bytes}, at::kByte);
-    k = Here::part(block, 0, shape, at::kBFloat16);
-    v = Here::part(block, bytes, shape, at::kBFloat16);
-  } else {
-    k = made ? h.make(shape, at::kBFloat16) : a.tensor(2, "k_out");
-    v = made ? h.make(shape, at::kBFloat16) : a.tensor(3, "v_out");
-  }
-  sparge_tensor dk = h.rows(k, "k_out"), dv = h.rows(v, "v_out");
-  done(sparge_cache4_load(&c, static_cast<int64_t *>(h.array(slots, at::kLong, "slots", {dk.B, dk.N})), made, &dk, &dv, h.s()));
+  at::Tensor k = given_rows(a, 2, h, "k_out"), v = given_rows(a, 3, h, "v_out");
+  const int64_t shape[4] = {made ? slots.size(0) : k.size(0), c.H, made ? slots.size(1) : k.size(2), c.d};
+  const int64_t *where = static_cast<int64_t *>(h.array(slots, at::kLong, "slots", {shape[0], shape[2]}));
+  done(unlocked([&] {
+    const int64_t bytes = 2 * slots.numel() * c.H * c.d;
+    if (made && bytes <= (1 << 19)) {  // small outputs share one allocation, as those of qk_norm_rope
+      const at::Tensor block = h.make({2 * bytes}, at::kByte);
+      k = Here::part(block, 0, shape, at::kBFloat16);
+      v = Here::part(block, bytes, shape, at::kBFloat16);
+    } else if (made) {
+      k = h.make(shape, at::kBFloat16);
+      v = h.make(shape, at::kBFloat16);
+    }
+    sparge_tensor dk = Here::describe(k), dv = Here::describe(v);
+    return sparge_cache4_load(&c, where, made, &dk, &dv, h.s());
+  }));
   PyObject *r = result(a, 2, k);
   return tuple_of(r, result(a, 3, v));
 }
@@ -303,13 +348,18 @@ PyObject *cache4_attn(const Args &a) {
   const Here h(q, "q");
   const sparge_tensor dq = h.rows(q, "q");
   const sparge_cache4 c = h.pool(a.tensor(1, "pool"));
-  const at::Tensor out = a.none(7) ? h.make_like(q) : a.tensor(7, "out");
-  sparge_tensor o = h.rows(out, "out");
   const int64_t stride = h.table(table, dq.B);
-  const at::Tensor ws = workspace(a, 8, h, sparge_cache4_attn_workspace_bytes(dq.B, dq.H, c.H, dq.N, dq.d));
-  done(sparge_cache4_attn(&dq, &c, static_cast<const int32_t *>(table.data_ptr()), table.size(1), stride,
-                          static_cast<int32_t *>(h.array(a.tensor(3, "kv_lens"), at::kInt, "kv_lens", {dq.B})), a.integer(4),
-                          a.integer(5), a.real(6), &o, ws.data_ptr(), ws.nbytes(), h.s()));
+  const int32_t *lens = static_cast<int32_t *>(h.array(a.tensor(3, "kv_lens"), at::kInt, "kv_lens", {dq.B}));
+  const int64_t window = a.integer(4), sinks = a.integer(5);
+  const float scale = a.real(6);
+  at::Tensor out = given_rows(a, 7, h, "out"), ws = given_workspace(a, 8, h);
+  done(unlocked([&] {
+    if (!out.defined()) out = h.make_like(q);
+    if (!ws.defined()) ws = make_workspace(h, sparge_cache4_attn_workspace_bytes(dq.B, dq.H, c.H, dq.N, dq.d));
+    sparge_tensor o = Here::describe(out);
+    return sparge_cache4_attn(&dq, &c, static_cast<const int32_t *>(table.data_ptr()), table.size(1), stride, lens, window, sinks,
+                              scale, &o, ws.data_ptr(), ws.nbytes(), h.s());
+  }));
   return result(a, 7, out);
 }
 

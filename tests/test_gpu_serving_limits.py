@@ -269,3 +269,42 @@ def test_norm_rope_infinities_stay_where_the_formula_has_them(d, rot, interleave
     assert torch.equal(torch.isnan(a), torch.isnan(ref)) and torch.equal(torch.isinf(a), torch.isinf(ref))
     fine = torch.isfinite(ref)
     within(a[fine], ref[fine], (2.0 ** -8 * ref.abs() + 2.0 ** -19 * mag)[fine])
+
+
+# ------------------------------------------------------------------------------------------------------ the binding
+def test_other_threads_run_while_a_call_waits_for_the_gpu():
+    """With the launch queue full a call waits until the GPU has caught up; other Python threads go on meanwhile."""
+    import threading
+    import time
+    lens, table, free = i32(3, 4), torch.zeros(2, 4, dtype=torch.int32, device="cuda"), i32(1, 2)
+    slots, pos = torch.empty(2, 1, dtype=torch.int64, device="cuda"), torch.empty(2, 1, dtype=torch.int32, device="cuda")
+    kv, used = torch.empty_like(lens), i32(0)
+    one = torch.ones_like(lens)
+    call = lambda: fbs.cache_tables(lens, one, free, table, 16, 1, slots, pos, kv, used)  # noqa: E731
+    call()
+    torch.cuda.synchronize()
+    stop, gaps = threading.Event(), [0.0]
+
+    def watch():
+        last = time.perf_counter()
+        while not stop.is_set():
+            time.sleep(0.001)
+            now = time.perf_counter()
+            gaps[0] = max(gaps[0], now - last)
+            last = now
+
+    thread = threading.Thread(target=watch)
+    thread.start()
+    torch.cuda._sleep(1_500_000_000)                # most of a second on the GPU
+    waited = 0.0
+    for _ in range(20000):
+        t0 = time.perf_counter()
+        call()
+        waited = max(waited, time.perf_counter() - t0)
+        if waited > 0.1:
+            break
+    torch.cuda.synchronize()
+    stop.set()
+    thread.join()
+    assert waited > 0.1, "the queue did not fill: nothing was tested"
+    assert gaps[0] < 0.5 * waited
