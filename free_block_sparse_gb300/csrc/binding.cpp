@@ -10,6 +10,7 @@
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
+#include <c10/util/Exception.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include "../../include/sparge.h"
@@ -369,6 +370,14 @@ PyObject *entry(PyObject *, PyObject *const *v, Py_ssize_t n) {
   try {
     return F(Args(v, n, N, "call"));
   } catch (const PyFail &) {
+  } catch (const c10::OutOfMemoryError &e) {  // torch's own exception for it
+    if (PyObject *torch = PyImport_ImportModule("torch")) {
+      if (PyObject *cls = PyObject_GetAttrString(torch, "OutOfMemoryError")) {
+        PyErr_SetString(cls, e.what_without_backtrace());
+        Py_DECREF(cls);
+      }
+      Py_DECREF(torch);
+    }
   } catch (const std::exception &e) {
     if (!PyErr_Occurred()) PyErr_SetString(PyExc_RuntimeError, e.what());
   } catch (...) {

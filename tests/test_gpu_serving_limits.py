@@ -308,3 +308,10 @@ def test_other_threads_run_while_a_call_waits_for_the_gpu():
     thread.join()
     assert waited > 0.1, "the queue did not fill: nothing was tested"
     assert gaps[0] < 0.5 * waited
+
+
+def test_outputs_too_large_for_the_gpu_raise_torchs_error():
+    """1024 requests of 2^30 places (13 TB of outputs): torch's out-of-memory error, as from an allocation of its own."""
+    lens = torch.zeros(1024, dtype=torch.int32, device="cuda")
+    with pytest.raises(torch.OutOfMemoryError):
+        fbs.cache_tables(lens, lens, lens, torch.zeros(1024, 2, dtype=torch.int32, device="cuda"), 16, 1 << 30)
