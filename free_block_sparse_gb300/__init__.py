@@ -456,7 +456,7 @@ def qk_norm_rope(q, k, inv_freq=None, positions=None, start: int = 0, q_weight=N
     """Norm of q (B,Hq,N,d) and k (B,Hkv,N,d) over each head's channels, times the weights (float32, d
     entries, or None), then the rotation of the first 2 len(inv_freq) channels by the positions ((B, N) int32,
     or start, start + 1, ...); inv_freq: float64 CUDA tensor (rope_freqs) or None (norm only).  Returns (q_out,
-    k_out), which may be given and may be q and k."""
+    k_out), which may be given and may be q and k (made here, they share one storage up to 1 MB in all)."""
     return (_binding_module or _load_binding()).qk_norm_rope(q, k, inv_freq, positions, start, q_weight, k_weight, eps,
                                                         interleaved, q_out, k_out)
 
@@ -465,7 +465,8 @@ def cache_tables(lens, new_lens, free_pages, table, page_size: int, N: int, slot
                  used=None):
     """Block tables and slot maps of a step: extends table (R, width; int32, rows any stride) in place with pages
     from the front of free_pages and returns (slots (R, N) int64, positions (R, N) int32, kv_lens (R) int32,
-    used (1) int32); the new tokens stand right-aligned, -1 in front of them (see sparge_cache_tables)."""
+    used (1) int32); the new tokens stand right-aligned, -1 in front of them (see sparge_cache_tables).  Outputs that the
+    call makes share one storage up to 64 KB in all."""
     return (_binding_module or _load_binding()).cache_tables(lens, new_lens, free_pages, table, page_size, N, slots, positions,
                                                         kv_lens, used)
 
@@ -486,7 +487,7 @@ def cache4_store(k, v, slots, pool):
 
 def cache4_load(pool, slots, k_out=None, v_out=None):
     """The rows at slots ((B, N) int64) as bf16 (B,H,N,d) tensors k and v.  Rows of left-out (negative) slots are zero
-    in tensors made here and stay as they were in tensors that are given."""
+    in tensors made here (which share one storage up to 1 MB in all) and stay as they were in tensors that are given."""
     return (_binding_module or _load_binding()).cache4_load(pool, slots, k_out, v_out)
 
 

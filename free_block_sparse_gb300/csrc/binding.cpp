@@ -286,13 +286,20 @@ PyObject *cache_tables(const Args &a) {
   at::Tensor slots = given(6, at::kLong, "slots", {R, N}), pos = given(7, at::kInt, "positions", {R, N}),
              kv = given(8, at::kInt, "kv_lens", {R}), used = given(9, at::kInt, "used", {1});
   done(unlocked([&] {
-    // the outputs that are not given share one allocation (four of them take the host longer than the kernel the GPU)
-    at::Tensor block;
-    if (!slots.defined() || !pos.defined() || !kv.defined() || !used.defined()) block = h.make({12 * R * N + 4 * R + 4}, at::kByte);
-    if (!slots.defined()) slots = Here::part(block, 0, {R, N}, at::kLong);
-    if (!pos.defined()) pos = Here::part(block, 8 * R * N, {R, N}, at::kInt);
-    if (!kv.defined()) kv = Here::part(block, 12 * R * N, {R}, at::kInt);
-    if (!used.defined()) used = Here::part(block, 12 * R * N + 4 * R, {1}, at::kInt);
+    // small outputs share one allocation (four of them take the host longer than the kernel the GPU); large ones do not: the
+    // lengths are kept for the next step, and would keep the slots and positions of this one
+    const int64_t bs = slots.defined() ? 0 : 8 * R * N, bp = pos.defined() ? 0 : 4 * R * N, bk = kv.defined() ? 0 : 4 * R,
+                  bu = used.defined() ? 0 : 4;
+    const bool share = bs + bp + bk + bu <= (1 << 16);
+    const bool any = !slots.defined() || !pos.defined() || !kv.defined() || !used.defined();
+    const at::Tensor block = share && any ? h.make({bs + bp + bk + bu}, at::kByte) : at::Tensor();
+    const auto made = [&](int64_t at, at::IntArrayRef shape, at::ScalarType type) {
+      return share ? Here::part(block, at, shape, type) : h.make(shape, type);
+    };
+    if (!slots.defined()) slots = made(0, {R, N}, at::kLong);
+    if (!pos.defined()) pos = made(bs, {R, N}, at::kInt);
+    if (!kv.defined()) kv = made(bs + bp, {R}, at::kInt);
+    if (!used.defined()) used = made(bs + bp + bk, {1}, at::kInt);
     return sparge_cache_tables(pl, pa, R, N, page, pf, free.numel(), static_cast<int32_t *>(table.data_ptr()), table.size(1), stride,
                                static_cast<int64_t *>(slots.data_ptr()), static_cast<int32_t *>(pos.data_ptr()),
                                static_cast<int32_t *>(kv.data_ptr()), static_cast<int32_t *>(used.data_ptr()), h.s());

@@ -315,3 +315,19 @@ def test_outputs_too_large_for_the_gpu_raise_torchs_error():
     lens = torch.zeros(1024, dtype=torch.int32, device="cuda")
     with pytest.raises(torch.OutOfMemoryError):
         fbs.cache_tables(lens, lens, lens, torch.zeros(1024, 2, dtype=torch.int32, device="cuda"), 16, 1 << 30)
+
+
+def test_kept_lengths_do_not_keep_the_slots():
+    """The lengths of a step with long chunks are a tensor of their own size; where some outputs are given, only the others are
+    made; small outputs share one storage of just their size."""
+    R_, N = 64, 4096
+    lens, new, free = (torch.zeros(R_, dtype=torch.int32, device="cuda") for _ in range(3))
+    table = torch.zeros(R_, 2, dtype=torch.int32, device="cuda")
+    out = fbs.cache_tables(lens, new, free, table, 64, N)
+    assert [x.untyped_storage().nbytes() for x in out] == [8 * R_ * N, 4 * R_ * N, 4 * R_, 4]
+    out = fbs.cache_tables(lens, new, free, table, 64, N, slots=out[0], positions=out[1])
+    assert [x.untyped_storage().nbytes() for x in out[2:]] == [4 * R_ + 4] * 2
+    out = fbs.cache_tables(lens, new, free, table, 64, 1)
+    assert [x.untyped_storage().nbytes() for x in out] == [12 * R_ + 4 * R_ + 4] * 4
+    out = fbs.cache_tables(lens[:0], new[:0], free, table[:0], 64, N, used=out[3])
+    assert [tuple(x.shape) for x in out] == [(0, N), (0, N), (0,), (1,)]
