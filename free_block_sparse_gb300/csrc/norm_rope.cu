@@ -221,7 +221,7 @@ extern "C" int sparge_qk_norm_rope(const sparge_tensor *q, const sparge_tensor *
     const View &x = v[s], &y = v[2 + s];
     if (x.B != y.B || x.H != y.H || x.N != y.N || x.d != y.d)
       return fail(SPARGE_ERR_INVALID_ARG, "%s_out has another shape than %s", s ? "k" : "q", s ? "k" : "q");
-    if (x.data == y.data && (x.sb != y.sb || x.sh != y.sh || x.sn != y.sn))
+    if (x.B * x.N != 0 && x.data == y.data && (x.sb != y.sb || x.sh != y.sh || x.sn != y.sn))
       return fail(SPARGE_ERR_INVALID_ARG, "in place, %s_out needs the strides of %s", s ? "k" : "q", s ? "k" : "q");
   }
   if (rot_dim < 0 || rot_dim > v[0].d || rot_dim % 16)
