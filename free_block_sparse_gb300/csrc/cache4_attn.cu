@@ -694,6 +694,12 @@ __global__ void __launch_bounds__(CA_WARPS * 32, ca_ctas(D, RT)) cache4_attn_ker
   }
 }
 
+// Query rows of a KV head and items that a call takes (its places are 32-bit numbers).
+bool too_many(int64_t B, int64_t Hkv, int64_t rows) {
+  const int64_t rt = row_tile(rows);
+  return rows > INT_MAX || B * Hkv > (int64_t(1) << 24) || B * Hkv * ((rows + 8 * rt - 1) / (8 * rt)) > INT_MAX / 2;
+}
+
 SplitWs ws_layout(int64_t B, int64_t Hkv, int64_t rows, int64_t d) {
   const int rt = row_tile(rows);
   return split_ws(B * Hkv * ((rows + 8 * rt - 1) / (8 * rt)), CA_SMS * ca_ctas(static_cast<int>(d), rt), rt, d);
@@ -720,7 +726,7 @@ extern "C" {
 
 size_t sparge_cache4_attn_workspace_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_t Nq, int64_t d) {
   if (B < 0 || Hq <= 0 || Hkv <= 0 || Nq < 0 || (d != 64 && d != 128) || Hq % Hkv || B > 65535 || Hq > 65535 ||
-      Nq > (int64_t(1) << 30))
+      Nq > (int64_t(1) << 30) || too_many(B, Hkv, Hq / Hkv * Nq))
     return 0;
   return ws_layout(B, Hkv, Hq / Hkv * Nq, d).total;
 }
@@ -744,7 +750,7 @@ int sparge_cache4_attn(const sparge_tensor *q, const sparge_cache4 *cache, const
     return fail(SPARGE_ERR_INVALID_ARG, "table width %lld and stride %lld: the stride must reach the width, the width 2^31 tokens at most",
                 (long long)width, (long long)table_stride);
   const int64_t rows = qv.H / c.H * qv.N, rt = row_tile(rows), ntile = (rows + 8 * rt - 1) / (8 * rt);
-  if (rows > INT_MAX || qv.B * c.H * ntile > INT_MAX / 2) return fail(SPARGE_ERR_UNSUPPORTED, "too many query rows");
+  if (too_many(qv.B, c.H, rows)) return fail(SPARGE_ERR_UNSUPPORTED, "too many query rows");
   const SplitWs w = ws_layout(qv.B, c.H, rows, qv.d);
   if (!ws || ws_bytes < w.total) return fail(SPARGE_ERR_WORKSPACE_TOO_SMALL, "workspace %zu bytes, need %zu", ws_bytes, w.total);
   if (reinterpret_cast<uintptr_t>(ws) & 255u) return fail(SPARGE_ERR_INVALID_ARG, "workspace not 256-byte aligned");
