@@ -331,3 +331,80 @@ def test_kept_lengths_do_not_keep_the_slots():
     assert [x.untyped_storage().nbytes() for x in out] == [12 * R_ + 4 * R_ + 4] * 4
     out = fbs.cache_tables(lens[:0], new[:0], free, table[:0], 64, N, used=out[3])
     assert [tuple(x.shape) for x in out] == [(0, N), (0, N), (0,), (1,)]
+
+
+# ---------------------------------------------------------------- window attention: strides, row counts, masked places
+@pytest.mark.parametrize("Hq,Hkv,Nq,Nk,d,window,sinks", WINDOWS + [(1, 1, 1, 1, 64, 1, 0), (4, 1, 1, 500, 128, 64, 4), (8, 2, 1, 900, 64, 300, 0)])
+def test_window_attn_strides_on_every_path(Hq, Hkv, Nq, Nk, d, window, sinks):
+    """Rows in (B, N, H, d) order, with gaps between heads, tokens and sequences, 16-byte aligned only; outputs so too: the
+    bits of contiguous tensors, within the tolerance that the row count sets, nothing written beside the rows."""
+    g = gen(50)
+
+    def strided(H, N):
+        whole = torch.full((2, N + 3, H + 1, d + 8), 77.0, dtype=torch.bfloat16, device="cuda")
+        return whole, whole[:, 1:N + 1, :H, 8:].transpose(1, 2)
+
+    q, k, v = rand(g, 2, Hq, Nq, d), rand(g, 2, Hkv, Nk, d), rand(g, 2, Hkv, Nk, d)
+    views = []
+    for x in (q, k, v):
+        _, y = strided(*x.shape[1:3])
+        views.append(y.copy_(x))
+    whole, out = strided(Hq, Nq)
+    good = fbs.window_attn(q, k, v, window, sinks)
+    assert fbs.window_attn(*views, window, sinks, out=out) is out
+    assert torch.equal(out, good) and torch.equal(fbs.window_attn(*views, window, sinks), good)
+    check_window_values(q, k, v, good, window, sinks)
+    out.fill_(77.0)
+    assert (whole == 77.0).all()
+
+
+@pytest.mark.parametrize("Hq,Hkv,Nq,Nk,d,window,sinks", [w for w in WINDOWS if w[3] - w[2] - w[5] + 1 > w[6] + 2] + [
+    (2, 1, 200, 4000, 128, 2000, 5), (2, 1, 200, 4000, 128, 300, 5), (2, 1, 200, 4000, 64, 300, 0), (1, 1, 200, 4000, 128, 2000, 64)])
+def test_window_attn_ignores_rubbish_that_no_query_sees(Hq, Hkv, Nq, Nk, d, window, sinks):
+    """NaN and infinities in keys and values between the first tokens and the window, on every path: the same bits."""
+    g = gen(51)
+    q, k, v = rand(g, 1, Hq, Nq, d), rand(g, 1, Hkv, Nk, d), rand(g, 1, Hkv, Nk, d)
+    good = fbs.window_attn(q, k, v, window, sinks)
+    lo, hi = sinks, Nk - Nq - window + 1
+    k[:, :, lo:hi], v[:, :, lo:hi] = math.nan, math.inf
+    v[:, :, lo], v[:, :, hi - 1], k[:, :, hi - 1] = math.nan, math.nan, math.inf
+    assert torch.equal(fbs.window_attn(q, k, v, window, sinks), good)
+
+
+@pytest.mark.parametrize("Hq,Nq,d", SHAPES)
+def test_cache_attn_nan_queries(Hq, Nq, d):
+    """A query of NaN gives NaN; the others keep their bits."""
+    g = gen(52)
+    pool, table = filled(g, [300], 1, d, 64)
+    q = rand(g, 1, Hq, Nq, d)
+    good = fbs.cache4_attn(q, pool, table, i32(300))
+    q[:, 1] = math.nan
+    got = fbs.cache4_attn(q, pool, table, i32(300))
+    keep = [h for h in range(Hq) if h != 1]
+    assert torch.isnan(got[:, 1]).all() and torch.equal(got[:, keep], good[:, keep])
+
+
+@pytest.mark.parametrize("Hq,Nq,d", SHAPES)
+def test_cache_attn_calls_share_a_workspace_and_a_graph_replays(Hq, Nq, d):
+    """Two calls one behind the other on one workspace, also captured into two graphs that share it; the workspace's old
+    contents do not matter."""
+    g = gen(53)
+    pool, table = filled(g, [3000], 1, d, 64)
+    q = rand(g, 1, Hq, Nq, d)
+    kv, kv2 = i32(3000), i32(900)
+    ws = torch.full((fbs.lib().sparge_cache4_attn_workspace_bytes(1, Hq, 1, Nq, d),), 255, dtype=torch.uint8, device="cuda")
+    want, want2 = fbs.cache4_attn(q, pool, table, kv), fbs.cache4_attn(q, pool, table, kv2, window=100, sinks=4)
+    assert torch.equal(fbs.cache4_attn(q, pool, table, kv, ws=ws), want)
+    assert torch.equal(fbs.cache4_attn(q, pool, table, kv2, window=100, sinks=4, ws=ws), want2)
+    s = torch.cuda.Stream()
+    graphs, outs = [torch.cuda.CUDAGraph() for _ in range(2)], []
+    torch.cuda.synchronize()
+    for graph, n, kw in ((graphs[0], kv, {}), (graphs[1], kv2, dict(window=100, sinks=4))):
+        with torch.cuda.graph(graph, stream=s):
+            outs.append(fbs.cache4_attn(q, pool, table, n, ws=ws, **kw))
+    for i in (0, 1, 1, 0, 1, 0):
+        ws.random_(0, 256)
+        outs[i].zero_()
+        graphs[i].replay()
+        torch.cuda.synchronize()
+        assert torch.equal(outs[i], (want, want2)[i])
