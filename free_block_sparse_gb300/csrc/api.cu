@@ -482,11 +482,13 @@ int window_impl(const View &q, const View &k, const View &v, const View &o, int6
   CUtensorMap tq, tk, tv;
   if ((rc = make_map(&tv, v16, 64, "v", CU_TENSOR_MAP_DATA_TYPE_FLOAT16))) return rc;
   if ((rc = make_map(&tk, k, 64, "k"))) return rc;
-  // d = 64, and few key blocks per tile of queries (window up to about 1300): the kernel with more and simpler CTAs.  At
-  // d = 128 over 16K of 32 + 8 heads: window 256 162 us against 209, 1280 364 against 375, 1536 415 against 415, but 2048 514
-  // against 495, 4096 859 against 767 (16 + 16 heads: 1024 188 against 188); at d = 64 never behind (4096: 538 against 668).
+  // d = 64, and few key blocks per tile of queries: the kernel with more and simpler CTAs.  At d = 128 over 16K, in us (window
+  // kernel against block-sparse): 32 + 8 heads 512 214 / 244, 1024 314 / 328, 1280 365 / 367, 1408 390 / 387, 1792 464 / 447; two,
+  // eight and sixteen heads per KV head cross at 1250 to 1400 too.  A group of an odd number of heads has tiles of 128
+  // queries of one head, with more hidden scores: 16 + 16 heads 512 135 / 143, 896 175 / 176, 1024 189 / 187, 1280 216 / 208; 24 +
+  // 8 heads of 9000 768 126 / 129, 896 137 / 137, 1024 148 / 146.  At d = 64 it is never behind (4096: 538 / 668).
   const int P = window_attn_queries(q.H / k.H);
-  if (q.d == 64 || cdiv(window + P - 1, KBLK) + 1 + cdiv(sinks, KBLK) <= 24) {
+  if (q.d == 64 || cdiv(window + P - 1, KBLK) + 1 + cdiv(sinks, KBLK) <= (P == 128 ? 18 : 24)) {
     WindowAttn w;
     if ((rc = make_map(&tq, q, P, "q", CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 128 / P))) return rc;
     w.tq = tq; w.tk = tk; w.tv = tv;

@@ -408,3 +408,12 @@ def test_cache_attn_calls_share_a_workspace_and_a_graph_replays(Hq, Nq, d):
         graphs[i].replay()
         torch.cuda.synchronize()
         assert torch.equal(outs[i], (want, want2)[i])
+
+
+@pytest.mark.parametrize("window", [830, 897, 898, 960, 1025, 1281, 1345])
+@pytest.mark.parametrize("Hq,Hkv", [(3, 1), (2, 2), (4, 1)])
+def test_window_attn_around_the_choice_of_kernels(Hq, Hkv, window):
+    """d = 128 around the windows where the two chunk kernels take over from each other, which depends on the heads per KV head."""
+    g = gen(54)
+    q, k, v = rand(g, 1, Hq, 330, 128), rand(g, 1, Hkv, 1700, 128), rand(g, 1, Hkv, 1700, 128)
+    check_window_values(q, k, v, fbs.window_attn(q, k, v, window, 5), window, 5)
