@@ -130,8 +130,11 @@ __device__ __forceinline__ uint32_t quantise16(const uint32_t (&u)[8], uint32_t 
   const float range = hi - lo;  // an infinity or a NaN if there is one in the group
   n[0] = n[1] = 0u;
   if (range >= 1e-28f && range < 1e38f) {
-    // A quotient from the reciprocal and one correction is the correctly rounded one, or where the quotient
-    // is representable (a tie of codes is) exactly it.  scale = range / 15 to bf16; adding 1.5 * 2^23 to
+    // Quotients by the reciprocal and one correction by the exact remainder (Markstein, 1990: q' = q + (a - q b) r).  Rounded
+    // correctly here: q is within two ulps, the fma's remainder is exact, so q' before its rounding is off by
+    // about 2^-22 ulp, and a 24-bit a over an 8-bit b lies no closer than 2^-9 ulp to the middle between two floats (a - m b is a
+    // whole multiple of a's last place, and not 0: an odd 25-bit m times b has more bits than a).  Where the quotient is
+    // representable (a tie of codes is) it is exactly it.  scale = range / 15 (b = 15) to bf16; adding 1.5 * 2^23 to
     // (x - lo) / scale rounds it to even and leaves it in the sum's low bits (at most 15 (1 + 2^-8): no code passes 15).
     constexpr float MAGIC = 12582912.f;
     constexpr uint32_t MAGIC_BITS = 0x4B400000u;

@@ -12,10 +12,12 @@
 // the codes widened into shared memory first, 4 times their size through a port that then feeds
 // the tensor core from it again; for 1 to 16 rows that traffic, not the products, would bound it.
 //   S^T = K^ Q^T: A = 16 tokens x 16 channels of codes, B = Q^T (f16, each row scaled by a power of two
-//         to a maximum in [2^14, 2^15), so its 8 significant bits stay whole down to 2^-29 of it).
+//         to a maximum in [2^14, 2^15); the odd channels' 1/16 of that, as their codes come 16 times as
+//         large: the 8 significant bits stay whole down to 2^-27 of the maximum, in even channels to 2^-31).
 //         x = k (sum_g s_g acc_g) + sum_g m_g (scale * sum of q over group g).
 //   O^T = V^T P^T: A = 16 channels x 16 tokens of codes, B = P^T s (f16: 11 bits, an eighth of the
-//         output's rounding) transposed in registers by movmatrix; the minima add sum P m per row.
+//         output's rounding: against 64 bits 1.79e-3 in place of the 1.66e-3 of an fp32 form, 64 sequences)
+//         transposed in registers by movmatrix; the minima add sum P m per row.
 // P lies in [0, 2^8] (the reference follows the running maximum lazily).  P s is scaled by a power of two per row and
 // channel group that follows its own running maximum the same way, so the largest P s of a row stays in
 // [2^3, 2^15]: what is less than 2^-17 of it loses bits in f16, what is less than 2^-28 is lost.
@@ -27,9 +29,10 @@
 // ends; then the four warps' sums are merged in shared memory, and an item cut between CTAs is put
 // together by a second kernel (rowsplit.cuh).
 // Measured: 64 sequences of 1K to 32K tokens, 32 + 8 heads, d = 128: 206 us for 1.25 GB, 90% of the
-// measured copy rate; one sequence of 4K 9 us, of which the chain length -> page -> record -> merge ->
-// combine is nearly all; 128 x 4 queries under a window of 4096, d = 64: 57 us, 38% (16 rows of 64 channels bring two
-// and a half times the arithmetic per byte: the products and the ALU are each over a third busy).
+// measured copy rate; one sequence of 4K 9.8 us, of which the chain length -> page -> record -> merge ->
+// combine is nearly all; 128 x 4 queries under a window of 4096, d = 64: 58 us, 38% (16 rows of 64 channels bring two
+// and a half times the arithmetic per byte: the ALU is 43% busy, the tensor pipe 28%).  One power of two per warp in place
+// of one per row and group: 9.2, 206 and 57 us, but hidden and improbable tokens took bits from the others.
 #include <climits>
 #include <cmath>
 #include <type_traits>
@@ -44,8 +47,8 @@ namespace sparge {
 int check_cache4(const ::sparge_cache4 *c, Cache4 *out);
 namespace {
 
-// Tiles that an item's start and end weigh in a CTA's share (128 ragged sequences of 4 queries, d = 64, under a
-// window of 4096: 0 66 us, 2 58, 3 57; 64 sequences of up to 32K: 0 213, 3 206).
+// Tiles that an item's start and end weigh in a CTA's share (128 ragged sequences of 4 queries, d = 64, under a window of
+// 4096: 0 66 us, 2 58, 3 57; 64 sequences of up to 32K: 0 213, 3 206; measured before the powers of two went by row).
 constexpr int CA_ITEM = 3;
 // Where a row's largest P s goes when its power of two is set (to 2^(CA_ROOM - 1) .. 2^CA_ROOM), and how far it may grow before
 // that moves: to 2^15, within f16.
@@ -87,8 +90,8 @@ __device__ __forceinline__ Span span_of(const CacheAttnArgs &a, int b) {
   return s;
 }
 // CTAs per SM, by registers: the sums of 16 rows of 128 channels alone take 64 per thread.  (16 rows of
-// d = 128, 4 queries of 128 sequences of 4100: 2 CTAs 93 us, 3 with one record a step and spills 113; d = 64: 3 CTAs
-// 56 us, 2 65.)
+// d = 128, 4 queries of 128 sequences of 4100 with 4 KV heads: 2 CTAs 93 us, 3 with one record a step and spills 113; with 8, 180;
+// d = 64: 3 CTAs 56 us, 2 65.)
 constexpr int ca_ctas(int D, int RT) { return RT == 1 ? 4 : D == 64 ? 3 : 2; }
 
 // Shared memory and the step of a warp: U = 2 records at a time (a CTA's tile is 4 U records, one step of each

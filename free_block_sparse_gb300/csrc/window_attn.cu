@@ -19,12 +19,12 @@
 // bit mask per row.  P and V enter the second product as f16, which keeps 3 more bits of P than bf16 would.
 //
 // Measured (f16 copy of V included; beside it the block-sparse kernel under the same mask, two score buffers per CTA):
-// d = 64, 32 + 8 heads of 16K, window 4096: 538 us (668), 46% of the tensor peak; 2 x 15K of 64 + 8 heads, window 461: 413 us
-// (792; 454 with tiles of 128 queries of one head); d = 128, 32 + 8 heads of 16K: window 256 162 us (209), 1280 364 (375),
-// 1536 415 (415), 4096 859 (767): at d = 128 the products alone fill the tensor unit, which two score buffers
+// d = 64, 32 + 8 heads of 16K, window 4096: 534 us (668), 46% of the tensor peak; 2 x 15K of 64 + 8 heads, window 461: 409 us
+// (792; 454 with tiles of 128 queries of one head); d = 128, 32 + 8 heads of 16K: window 256 162 us (209), 1280 365 (367),
+// 1536 415 (405), 4096 859 (767): at d = 128 the products alone fill the tensor unit, which two score buffers
 // feed better over a long window.
-// At d = 64 a block takes 570 cycles of an SM: the softmax's instructions (about 300 of each of 12 warps) and the
-// chain's waits; the products 330.
+// At d = 64 under the long window a block takes 680 cycles of an SM: 1510 instructions (380 per scheduler) and the chain's waits; the
+// products 340.
 #include <cfloat>
 
 #include <cuda_fp16.h>
