@@ -372,7 +372,8 @@ int sparge_cache4_load(const sparge_cache4 *cache, const int64_t *slots, int zer
  * apart); its queries are its last Nq tokens: query r stands at position kv_lens[b] - Nq + r and sees
  * the tokens up to there (a query in front of the first token gives a zero row).  With window > 0 it sees
  * only the last `window` of them (itself included) and the first `sinks` tokens; window 0: all of them
- * (sinks then 0).  scale 0 means 1/sqrt(d).  Products in f16 with fp32 sums; one rounding to bf16.
+ * (sinks then 0).  scale 0 means 1/sqrt(d).  Products in f16 with fp32 sums (a probability times a V scale keeps 11 bits down
+ * to 2^-17 of its row's largest); one rounding to bf16.  A row depends on the tokens that it sees alone.
  * A length outside 0..width * page_size is taken as the nearest of the two; a page outside the pool is left
  * out and records SPARGE_ERR_INVALID_ARG in the device status word.
  * Meant for decoding steps and short chunks: the cache is read once per 16 query rows of a key/value head
