@@ -417,3 +417,25 @@ def test_window_attn_around_the_choice_of_kernels(Hq, Hkv, window):
     g = gen(54)
     q, k, v = rand(g, 1, Hq, 330, 128), rand(g, 1, Hkv, 1700, 128), rand(g, 1, Hkv, 1700, 128)
     check_window_values(q, k, v, fbs.window_attn(q, k, v, window, 5), window, 5)
+
+
+def test_captured_window_attn_replays_on_values_of_another_size():
+    """The power of two on the copy of V is found on the device: a graph captured with usual values replays on large and small
+    ones, head by head."""
+    g = gen(55)
+    Hq, Hkv, N, d = 4, 2, 400, 64
+    q, k, v = rand(g, 1, Hq, N, d), rand(g, 1, Hkv, N, d), rand(g, 1, Hkv, N, d)
+    s = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    fbs.window_attn(q, k, v, 100, 3)
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=s):
+        out = fbs.window_attn(q, k, v, 100, 3)
+    for powers in ((0, 0), (30, -30), (-50, 0), (0, 100), (0, 0)):
+        for h, p in enumerate(powers):
+            v[:, h] = rand(g, 1, N, d, std=2.0 ** p)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        check_window_values(q, k, v, out, 100, 3)
+        assert torch.equal(out, fbs.window_attn(q, k, v, 100, 3))
