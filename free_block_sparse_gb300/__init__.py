@@ -115,6 +115,29 @@ EXPORTS = {
                                           ctypes.c_int64, ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64,
                                           ctypes.c_float, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t,
                                           ctypes.c_void_p]),
+    "sparge_qk_norm_rope_axes": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int,
+                                                ctypes.c_int64, ctypes.c_int64, ctypes.c_void_p, ctypes.c_void_p,
+                                                ctypes.c_int, ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p,
+                                                ctypes.c_float, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
+    "sparge_cache4_bounds_bytes": (ctypes.c_size_t, [ctypes.c_int64, ctypes.c_int, ctypes.c_int]),
+    "sparge_cache4_bounds_update": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64,
+                                                   ctypes.c_int64, ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p,
+                                                   ctypes.c_size_t, ctypes.c_void_p]),
+    "sparge_cache4_bounds_load": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p,
+                                                 ctypes.c_int64, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
+    "sparge_cache4_select": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t,
+                                            ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64, ctypes.c_void_p,
+                                            ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, ctypes.c_void_p,
+                                            ctypes.c_void_p, ctypes.c_void_p]),
+    "sparge_cache4_pages_attn_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int64] * 5),
+    "sparge_cache4_pages_attn": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64,
+                                                ctypes.c_void_p, ctypes.c_float, ctypes.c_void_p, ctypes.c_void_p,
+                                                ctypes.c_size_t, ctypes.c_void_p]),
+    "sparge_cache4_prefix_attn_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int64] * 5),
+    "sparge_cache4_prefix_attn": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64,
+                                                 ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64, ctypes.c_void_p,
+                                                 ctypes.c_float, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t,
+                                                 ctypes.c_void_p]),
     "sparge_selftest_bounded_wait": (ctypes.c_int, [ctypes.c_int64, ctypes.c_void_p]),
     "sparge_last_error": (ctypes.c_char_p, []),
     "sparge_get_device_status": (ctypes.c_int, [ctypes.c_void_p]),
@@ -461,6 +484,42 @@ def qk_norm_rope(q, k, inv_freq=None, positions=None, start: int = 0, q_weight=N
                                                         interleaved, q_out, k_out)
 
 
+def rope_axes(sections, woven: bool = False, device="cuda"):
+    """The axis of each rotated pair, int32, for qk_norm_rope_axes: sections[x] pairs of axis x, one axis after the other, or
+    (woven) the axes taking turns pair by pair while they have pairs left."""
+    torch = _torch()
+    if woven:
+        left, axes = list(sections), []
+        while any(left):
+            for x, n in enumerate(left):
+                if n > 0:
+                    left[x] = n - 1
+                    axes.append(x)
+    else:
+        axes = [x for x, n in enumerate(sections) for _ in range(n)]
+    return torch.tensor(axes, dtype=torch.int32, device=device)
+
+
+def rope_grid_positions(n_prefix: int, T: int, H: int, W: int, order=None, device="cuda"):
+    """Positions (3, 1, N) int32 of n_prefix text tokens and a T x H x W grid behind them (tokens row-major, as
+    hilbert_perm_3d numbers them): text token i stands at i on every axis, grid token (t, y, x) at n_prefix + t, + y,
+    + x.  order (int32, N entries): positions of the tokens in that order."""
+    torch = _torch()
+    text = torch.arange(n_prefix, dtype=torch.int32, device=device).expand(3, -1)
+    grid = torch.stack(torch.meshgrid(*(torch.arange(n, dtype=torch.int32, device=device) for n in (T, H, W)), indexing="ij"))
+    pos = torch.cat([text, n_prefix + grid.flatten(1)], 1)
+    return (pos if order is None else pos[:, order.long()])[:, None].contiguous()
+
+
+def qk_norm_rope_axes(q, k, inv_freq, axes, positions, q_weight=None, k_weight=None, eps: float = 1e-6,
+                      interleaved: bool = False, q_out=None, k_out=None):
+    """qk_norm_rope with positions on several axes (images, video): pair i turns by positions[axes[i], b, n] *
+    inv_freq[i].  positions (A, B, N) int32, A <= 4, tokens contiguous, any other strides (a batch may be expanded); axes: int32 CUDA
+    tensor of as many entries as inv_freq (rope_axes)."""
+    return (_binding_module or _load_binding()).qk_norm_rope_axes(q, k, inv_freq, axes, positions, q_weight, k_weight, eps,
+                                                             interleaved, q_out, k_out)
+
+
 def cache_tables(lens, new_lens, free_pages, table, page_size: int, N: int, slots=None, positions=None, kv_lens=None,
                  used=None):
     """Block tables and slot maps of a step: extends table (R, width; int32, rows any stride) in place with pages
@@ -496,6 +555,45 @@ def cache4_attn(q, pool, table, kv_lens, window: int = 0, sinks: int = 0, scale:
     ((B, width) int32) and q holds its last Nq; window > 0 keeps each query's last `window` tokens and the first
     `sinks`."""
     return (_binding_module or _load_binding()).cache4_attn(q, pool, table, kv_lens, window, sinks, scale, out, ws)
+
+
+def cache4_bounds(n_pages: int, H: int, d: int, device="cuda"):
+    """Bounds for a pool of n_pages pages, all zero: a uint8 tensor (n_pages, bytes of a page's bounds)."""
+    torch = _torch()
+    row = int(lib().sparge_cache4_bounds_bytes(1, H, d)) if H > 0 else 0
+    if n_pages < 0 or row == 0:
+        raise ValueError("unsupported pool: n_pages=%d, H=%d, d=%d" % (n_pages, H, d))
+    return torch.zeros((n_pages, row), dtype=torch.uint8, device=device)
+
+
+def cache4_bounds_update(pool, table, kv_lens, N: int, bounds):
+    """Renews the bounds of the pages on which the last N of each sequence's kv_lens[b] tokens lie (after a
+    cache4_store of N new ones); table ((B, width) int32) and kv_lens as cache4_attn takes them."""
+    (_binding_module or _load_binding()).cache4_bounds_update(pool, table, kv_lens, N, bounds)
+
+
+def cache4_bounds_load(pool, bounds, pages):
+    """The bounds of pages (int32, any shape) as values: hi and lo, bf16 of shape (pages.numel(), H, d), zero for
+    negative pages."""
+    return (_binding_module or _load_binding()).cache4_bounds_load(pool, bounds, pages)
+
+
+def cache4_select(q, pool, bounds, table, kv_lens, keep: int, first: int = 1, last: int = 1, pages=None, lens=None):
+    """For each query of q (B,Hq,Nq,d) and KV head the pages that its keys' bounds say matter most: the `first` first and the `last`
+    last pages that the query sees, then the largest bounds on a product with a query of the head's group, up to keep pages.
+    Returns (pages (B,Nq,Hkv,keep) int32, in order, -1 behind them; lens (B,Nq) int32, the tokens on them)."""
+    return (_binding_module or _load_binding()).cache4_select(q, pool, bounds, table, kv_lens, keep, first, last, pages, lens)
+
+
+def cache4_pages_attn(q, pool, pages, lens, scale: float = 0.0, out=None, ws=None):
+    """Attention of each query over its own list of pages (from cache4_select) in every KV head."""
+    return (_binding_module or _load_binding()).cache4_pages_attn(q, pool, pages, lens, scale, out, ws)
+
+
+def cache4_prefix_attn(q, pool, prefix_pages, table, kv_lens, scale: float = 0.0, out=None, ws=None):
+    """cache4_attn for sequences that all begin with the tokens on prefix_pages (int32): those are attended once for the whole
+    batch.  The rows of table hold the prefix's pages too, kv_lens counts its tokens."""
+    return (_binding_module or _load_binding()).cache4_prefix_attn(q, pool, prefix_pages, table, kv_lens, scale, out, ws)
 
 
 def hilbert_perm_2d(n_prefix: int, H: int, W: int) -> np.ndarray:

@@ -222,6 +222,19 @@ PyObject *window_attn(const Args &a) {
   return result(a, 6, out);
 }
 
+// The outputs of a norm and rotation that are not given.  Small ones share one allocation (64 tokens of 32 + 8 heads: 4.0 us of
+// host time, 3.6 so); large ones do not, so that letting go of one frees it.
+void make_rope_outputs(const Here &h, const at::Tensor &q, const at::Tensor &k, at::Tensor &qo, at::Tensor &ko) {
+  const int64_t nq = static_cast<int64_t>(q.nbytes()), nk = static_cast<int64_t>(k.nbytes()), k0 = (nq + 255) / 256 * 256;
+  if (!qo.defined() && !ko.defined() && nq + nk <= (1 << 20) && q.is_contiguous() && k.is_contiguous()) {
+    const at::Tensor block = h.make({k0 + nk}, at::kByte);
+    qo = Here::part(block, 0, q.sizes(), at::kBFloat16);
+    ko = Here::part(block, k0, k.sizes(), at::kBFloat16);
+  }
+  if (!qo.defined()) qo = h.make_like(q);
+  if (!ko.defined()) ko = h.make_like(k);
+}
+
 // (q, k, inv_freq, positions, start, q_weight, k_weight, eps, interleaved, q_out, k_out)
 PyObject *qk_norm_rope(const Args &a) {
   const at::Tensor &q = a.tensor(0, "q"), &k = a.tensor(1, "k");
@@ -243,20 +256,42 @@ PyObject *qk_norm_rope(const Args &a) {
   const float eps = a.real(7);
   const bool interleaved = a.truth(8);
   done(unlocked([&] {
-    // small outputs share one allocation (64 tokens of 32 + 8 heads: 4.0 us of host time, 3.6 so); large ones do not, so that
-    // letting go of one frees it
-    const int64_t nq = static_cast<int64_t>(q.nbytes()), nk = static_cast<int64_t>(k.nbytes()), k0 = (nq + 255) / 256 * 256;
-    if (!qo.defined() && !ko.defined() && nq + nk <= (1 << 20) && q.is_contiguous() && k.is_contiguous()) {
-      const at::Tensor block = h.make({k0 + nk}, at::kByte);
-      qo = Here::part(block, 0, q.sizes(), at::kBFloat16);
-      ko = Here::part(block, k0, k.sizes(), at::kBFloat16);
-    }
-    if (!qo.defined()) qo = h.make_like(q);
-    if (!ko.defined()) ko = h.make_like(k);
+    make_rope_outputs(h, q, k, qo, ko);
     sparge_tensor eq = Here::describe(qo), ek = Here::describe(ko);
     return sparge_qk_norm_rope(&dq, &dk, static_cast<const int32_t *>(pos), start, freq,
                                static_cast<int>(rot > INT32_MAX ? INT32_MAX : rot), interleaved, static_cast<const float *>(w[0]),
                                static_cast<const float *>(w[1]), eps, &eq, &ek, h.s());
+  }));
+  PyObject *r = result(a, 9, qo);
+  return tuple_of(r, result(a, 10, ko));
+}
+
+// (q, k, inv_freq, axes, positions, q_weight, k_weight, eps, interleaved, q_out, k_out)
+PyObject *qk_norm_rope_axes(const Args &a) {
+  const at::Tensor &q = a.tensor(0, "q"), &k = a.tensor(1, "k"), &f = a.tensor(2, "inv_freq"), &axes = a.tensor(3, "axes"),
+                   &pos = a.tensor(4, "positions");
+  const Here h(q, "q");
+  const sparge_tensor dq = h.rows(q, "q"), dk = h.rows(k, "k");
+  at::Tensor qo = given_rows(a, 9, h, "q_out"), ko = given_rows(a, 10, h, "k_out");
+  const double *freq = static_cast<const double *>(h.array(f, at::kDouble, "inv_freq", {}));
+  const int64_t rot = 2 * f.numel();
+  const int32_t *of = static_cast<const int32_t *>(h.array(axes, at::kInt, "axes", {f.numel()}));
+  h.check(pos, "positions");
+  if (pos.scalar_type() != at::kInt || pos.dim() != 3 || pos.size(1) != dq.B || pos.size(2) != dq.N ||
+      (pos.size(2) > 1 && pos.stride(2) != 1))
+    type_error("%s must be an int32 tensor (axes, B, N) with contiguous tokens", "positions");
+  const void *w[2];
+  for (int i = 0; i < 2; ++i)
+    w[i] = a.none(5 + i) ? nullptr : h.array(a.tensor(5 + i, "weight"), at::kFloat, i ? "k_weight" : "q_weight", {dq.d});
+  const float eps = a.real(7);
+  const bool interleaved = a.truth(8);
+  done(unlocked([&] {
+    make_rope_outputs(h, q, k, qo, ko);
+    sparge_tensor eq = Here::describe(qo), ek = Here::describe(ko);
+    return sparge_qk_norm_rope_axes(&dq, &dk, static_cast<const int32_t *>(pos.data_ptr()),
+                                    static_cast<int>(pos.size(0) > INT32_MAX ? INT32_MAX : pos.size(0)), pos.stride(0), pos.stride(1),
+                                    of, freq, static_cast<int>(rot > INT32_MAX ? INT32_MAX : rot), interleaved,
+                                    static_cast<const float *>(w[0]), static_cast<const float *>(w[1]), eps, &eq, &ek, h.s());
   }));
   PyObject *r = result(a, 9, qo);
   return tuple_of(r, result(a, 10, ko));
@@ -371,6 +406,139 @@ PyObject *cache4_attn(const Args &a) {
   return result(a, 7, out);
 }
 
+// The bounds tensor of a pool: one row per page.
+void *bounds_of(const Here &h, const at::Tensor &t, const sparge_cache4 &c) {
+  h.check(t, "bounds");
+  if (t.scalar_type() != at::kByte || t.dim() != 2 || !t.is_contiguous() || t.size(0) != c.n_pages ||
+      (c.n_pages && static_cast<size_t>(t.size(1)) != sparge_cache4_bounds_bytes(1, c.H, c.d)))
+    type_error("%s must be a contiguous uint8 tensor of the pool's (cache4_bounds)", "bounds");
+  return t.data_ptr();
+}
+
+// (pool, table, kv_lens, N, bounds)
+PyObject *cache4_bounds_update(const Args &a) {
+  const at::Tensor &pool = a.tensor(0, "pool"), &table = a.tensor(1, "table"), &lens = a.tensor(2, "kv_lens"),
+                   &bounds = a.tensor(4, "bounds");
+  const Here h(pool, "pool");
+  const sparge_cache4 c = h.pool(pool);
+  const int64_t B = lens.numel(), N = a.integer(3);
+  const int32_t *len = static_cast<int32_t *>(h.array(lens, at::kInt, "kv_lens", {B}));
+  const int64_t stride = h.table(table, B);
+  void *to = bounds_of(h, bounds, c);
+  done(unlocked([&] {
+    return sparge_cache4_bounds_update(&c, static_cast<const int32_t *>(table.data_ptr()), B, table.size(1), stride, len, N, to,
+                                       bounds.nbytes(), h.s());
+  }));
+  Py_RETURN_NONE;
+}
+
+// (pool, bounds, pages)
+PyObject *cache4_bounds_load(const Args &a) {
+  const at::Tensor &pool = a.tensor(0, "pool"), &bounds = a.tensor(1, "bounds"), &pages = a.tensor(2, "pages");
+  const Here h(pool, "pool");
+  const sparge_cache4 c = h.pool(pool);
+  const void *from = bounds_of(h, bounds, c);
+  const int32_t *ids = static_cast<int32_t *>(h.array(pages, at::kInt, "pages", {}));
+  at::Tensor hi, lo;
+  done(unlocked([&] {
+    const int64_t n = pages.numel(), bytes = 2 * n * c.H * c.d;
+    if (bytes <= (1 << 19)) {  // small outputs share one allocation, as those of cache4_load
+      const at::Tensor block = h.make({2 * bytes}, at::kByte);
+      hi = Here::part(block, 0, {n, c.H, c.d}, at::kBFloat16);
+      lo = Here::part(block, bytes, {n, c.H, c.d}, at::kBFloat16);
+    } else {
+      hi = h.make({n, c.H, c.d}, at::kBFloat16);
+      lo = h.make({n, c.H, c.d}, at::kBFloat16);
+    }
+    return sparge_cache4_bounds_load(&c, from, bounds.nbytes(), ids, n, hi.data_ptr(), lo.data_ptr(), h.s());
+  }));
+  PyObject *r = wrap(hi);
+  return tuple_of(r, wrap(lo));
+}
+
+// (q, pool, bounds, table, kv_lens, keep, first, last, pages, lens)
+PyObject *cache4_select(const Args &a) {
+  const at::Tensor &q = a.tensor(0, "q"), &bounds = a.tensor(2, "bounds"), &table = a.tensor(3, "table");
+  const Here h(q, "q");
+  const sparge_tensor dq = h.rows(q, "q");
+  const sparge_cache4 c = h.pool(a.tensor(1, "pool"));
+  const void *from = bounds_of(h, bounds, c);
+  const int64_t stride = h.table(table, dq.B);
+  const int32_t *len = static_cast<int32_t *>(h.array(a.tensor(4, "kv_lens"), at::kInt, "kv_lens", {dq.B}));
+  const int64_t keep = a.integer(5), first = a.integer(6), last = a.integer(7);
+  if (keep < 0 || keep > (int64_t(1) << 27)) {
+    PyErr_SetString(PyExc_ValueError, "keep must be in 0..2^27");
+    throw PyFail{};
+  }
+  at::Tensor pages, lens;
+  if (!a.none(8)) {
+    pages = a.tensor(8, "pages");
+    h.array(pages, at::kInt, "pages", {dq.B, dq.N, c.H, keep});
+  }
+  if (!a.none(9)) {
+    lens = a.tensor(9, "lens");
+    h.array(lens, at::kInt, "lens", {dq.B, dq.N});
+  }
+  done(unlocked([&] {
+    const int64_t np = pages.defined() ? 0 : 4 * dq.B * dq.N * c.H * keep, nl = lens.defined() ? 0 : 4 * dq.B * dq.N;
+    if (np && nl && np + nl <= (1 << 19)) {  // small outputs share one allocation
+      const at::Tensor block = h.make({np + nl}, at::kByte);
+      pages = Here::part(block, 0, {dq.B, dq.N, c.H, keep}, at::kInt);
+      lens = Here::part(block, np, {dq.B, dq.N}, at::kInt);
+    }
+    if (!pages.defined()) pages = h.make({dq.B, dq.N, c.H, keep}, at::kInt);
+    if (!lens.defined()) lens = h.make({dq.B, dq.N}, at::kInt);
+    return sparge_cache4_select(&dq, &c, from, bounds.nbytes(), static_cast<const int32_t *>(table.data_ptr()), table.size(1), stride,
+                                len, keep, first, last, static_cast<int32_t *>(pages.data_ptr()),
+                                static_cast<int32_t *>(lens.data_ptr()), h.s());
+  }));
+  PyObject *r = result(a, 8, pages);
+  return tuple_of(r, result(a, 9, lens));
+}
+
+// (q, pool, pages, lens, scale, out, ws)
+PyObject *cache4_pages_attn(const Args &a) {
+  const at::Tensor &q = a.tensor(0, "q"), &pages = a.tensor(2, "pages");
+  const Here h(q, "q");
+  const sparge_tensor dq = h.rows(q, "q");
+  const sparge_cache4 c = h.pool(a.tensor(1, "pool"));
+  if (pages.dim() != 4) type_error("%s must be a contiguous int32 (B, Nq, Hkv, keep) tensor", "pages");
+  const int64_t keep = pages.size(3);
+  const int32_t *ids = static_cast<int32_t *>(h.array(pages, at::kInt, "pages", {dq.B, dq.N, c.H, keep}));
+  const int32_t *lens = static_cast<int32_t *>(h.array(a.tensor(3, "lens"), at::kInt, "lens", {dq.B, dq.N}));
+  const float scale = a.real(4);
+  at::Tensor out = given_rows(a, 5, h, "out"), ws = given_workspace(a, 6, h);
+  done(unlocked([&] {
+    if (!out.defined()) out = h.make_like(q);
+    if (!ws.defined()) ws = make_workspace(h, sparge_cache4_pages_attn_workspace_bytes(dq.B, dq.H, c.H, dq.N, dq.d));
+    sparge_tensor o = Here::describe(out);
+    return sparge_cache4_pages_attn(&dq, &c, ids, keep, lens, scale, &o, ws.data_ptr(), ws.nbytes(), h.s());
+  }));
+  return result(a, 5, out);
+}
+
+// (q, pool, prefix_pages, table, kv_lens, scale, out, ws)
+PyObject *cache4_prefix_attn(const Args &a) {
+  const at::Tensor &q = a.tensor(0, "q"), &prefix = a.tensor(2, "prefix_pages"), &table = a.tensor(3, "table");
+  const Here h(q, "q");
+  const sparge_tensor dq = h.rows(q, "q");
+  const sparge_cache4 c = h.pool(a.tensor(1, "pool"));
+  const int64_t n = prefix.numel();
+  const int32_t *ids = static_cast<int32_t *>(h.array(prefix, at::kInt, "prefix_pages", {n}));
+  const int64_t stride = h.table(table, dq.B);
+  const int32_t *lens = static_cast<int32_t *>(h.array(a.tensor(4, "kv_lens"), at::kInt, "kv_lens", {dq.B}));
+  const float scale = a.real(5);
+  at::Tensor out = given_rows(a, 6, h, "out"), ws = given_workspace(a, 7, h);
+  done(unlocked([&] {
+    if (!out.defined()) out = h.make_like(q);
+    if (!ws.defined()) ws = make_workspace(h, sparge_cache4_prefix_attn_workspace_bytes(dq.B, dq.H, c.H, dq.N, dq.d));
+    sparge_tensor o = Here::describe(out);
+    return sparge_cache4_prefix_attn(&dq, &c, ids, n, static_cast<const int32_t *>(table.data_ptr()), table.size(1), stride, lens, scale,
+                                     &o, ws.data_ptr(), ws.nbytes(), h.s());
+  }));
+  return result(a, 6, out);
+}
+
 // No C++ exception leaves through Python.
 template <PyObject *(*F)(const Args &), int N>
 PyObject *entry(PyObject *, PyObject *const *v, Py_ssize_t n) {
@@ -407,6 +575,12 @@ PyMethodDef methods[] = {ENTRY(window_attn, 8),
                          ENTRY(cache4_store, 4),
                          ENTRY(cache4_load, 4),
                          ENTRY(cache4_attn, 9),
+                         ENTRY(qk_norm_rope_axes, 11),
+                         ENTRY(cache4_bounds_update, 5),
+                         ENTRY(cache4_bounds_load, 3),
+                         ENTRY(cache4_select, 10),
+                         ENTRY(cache4_pages_attn, 7),
+                         ENTRY(cache4_prefix_attn, 8),
                          {"set_error", set_error, METH_O, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods};

@@ -55,6 +55,11 @@ constexpr int CA_ITEM = 3;
 constexpr int CA_ROOM = 4, CA_GROW = 15 - CA_ROOM;
 constexpr float CA_SBOUND = 128.f;  // 2^15 / 2^CA_RESCALE
 
+// The records a sequence's queries see: the first `ns` (tokens that stay visible), then lo..hi-1.
+struct Span {
+  int len, ns, lo, recs;
+};
+
 struct CacheAttnArgs : SplitArgs {
   const __nv_bfloat16 *q;
   int64_t q_sb, q_sh, q_sn;
@@ -66,29 +71,44 @@ struct CacheAttnArgs : SplitArgs {
   float scale_log2;
   int *status;
   __device__ __forceinline__ bool empty(int b) const { return width == 0 || lens[b] <= 0; }
+  __device__ __forceinline__ const int32_t *pages(int b, int) const { return table + static_cast<int64_t>(b) * table_stride; }
+  __device__ __forceinline__ const __nv_bfloat16 *queries(int b, int h) const { return q + b * q_sb + h * q_sh; }
+  __device__ __forceinline__ int length(int b) const {
+    const int len = lens[b];
+    const int64_t cap = static_cast<int64_t>(width) << (rec_shift + 4);
+    return max(len > cap ? static_cast<int>(cap) : len, 0);
+  }
+  __device__ __forceinline__ Span span(int b) const {
+    Span s;
+    s.len = length(b);
+    const int hi = static_cast<int>((static_cast<int64_t>(s.len) + 15) >> 4);
+    s.ns = 0;
+    s.lo = 0;
+    if (window > 0) {
+      const int64_t first = static_cast<int64_t>(s.len) - Nq - window + 1;
+      s.lo = first > 0 ? static_cast<int>(first >> 4) : 0;
+      s.ns = min(s.lo, static_cast<int>((static_cast<int64_t>(sinks) + 15) >> 4));
+    }
+    s.recs = s.ns + hi - s.lo;
+    return s;
+  }
 };
 
-// The records a sequence's queries see: the first `ns` (tokens that stay visible), then lo..hi-1.
-struct Span {
-  int len, ns, lo, recs;
-};
-__device__ __forceinline__ Span span_of(const CacheAttnArgs &a, int b) {
-  Span s;
-  int len = a.lens[b];
-  const int64_t cap = static_cast<int64_t>(a.width) << (a.rec_shift + 4);
-  if (len > cap) len = static_cast<int>(cap);
-  s.len = max(len, 0);
-  const int hi = static_cast<int>((static_cast<int64_t>(s.len) + 15) >> 4);
-  s.ns = 0;
-  s.lo = 0;
-  if (a.window > 0) {
-    const int64_t first = static_cast<int64_t>(s.len) - a.Nq - a.window + 1;
-    s.lo = first > 0 ? static_cast<int>(first >> 4) : 0;
-    s.ns = min(s.lo, static_cast<int>((static_cast<int64_t>(a.sinks) + 15) >> 4));
+// Every query and KV head with a page list of its own: "sequence" b is query b % queries_of of sequence b / queries_of, the
+// last token of its list.  (G rows each, so the selected bytes of a KV head are read once for its heads.)
+struct CacheListArgs : CacheAttnArgs {
+  int queries_of;
+  __device__ __forceinline__ const int32_t *pages(int b, int kvh) const {
+    return table + (static_cast<int64_t>(b) * Hkv + kvh) * width;
   }
-  s.recs = s.ns + hi - s.lo;
-  return s;
-}
+  __device__ __forceinline__ const __nv_bfloat16 *queries(int b, int h) const {
+    return q + (b / queries_of) * q_sb + static_cast<int64_t>(b % queries_of) * q_sn + h * q_sh;
+  }
+  __device__ __forceinline__ __nv_bfloat16 *row(int b, int kvh, int r) const {
+    return o + (b / queries_of) * o_sb + static_cast<int64_t>(b % queries_of) * o_sn + (kvh * G + r) * o_sh;
+  }
+};
+
 // CTAs per SM, by registers: the sums of 16 rows of 128 channels alone take 64 per thread.  (16 rows of
 // d = 128, 4 queries of 128 sequences of 4100 with 4 KV heads: 2 CTAs 93 us, 3 with one record a step and spills 113; with 8, 180;
 // d = 64: 3 CTAs 56 us, 2 65.)
@@ -123,9 +143,9 @@ template <int U>
 __device__ __forceinline__ int tiles_of(const Span &sp) {
   return (sp.recs + 4 * U - 1) / (4 * U);
 }
-template <int U>
-__device__ __forceinline__ int64_t units_of(const CacheAttnArgs &a, int b) {
-  const int t = tiles_of<U>(span_of(a, b));
+template <int U, typename Args>
+__device__ __forceinline__ int64_t units_of(const Args &a, int b) {
+  const int t = tiles_of<U>(a.span(b));
   return t == 0 ? 0 : static_cast<int64_t>(t + CA_ITEM) * (a.Hkv * a.ntile);
 }
 // x / y for non-negative x and positive y, in 32 bits where they do
@@ -198,8 +218,8 @@ __device__ __forceinline__ float follow_scale(float &f, float y, float m, float 
   return al * pow2i(min(max(e0 - e, -126), 127));
 }
 
-template <int D, int RT>
-__global__ void __launch_bounds__(CA_WARPS * 32, ca_ctas(D, RT)) cache4_attn_kernel(const CacheAttnArgs a) {
+template <int D, int RT, typename Args>
+__global__ void __launch_bounds__(CA_WARPS * 32, ca_ctas(D, RT)) cache4_attn_kernel(const Args a) {
   using S = CaSmem<D, RT>;
   using R = Rec4<D>;
   constexpr int NG = D / 64, NW = D / 32, MT = D / 16, U = S::U, ST = S::ST;
@@ -250,7 +270,7 @@ __global__ void __launch_bounds__(CA_WARPS * 32, ca_ctas(D, RT)) cache4_attn_ker
   int k0, kend, nstep;                    // this warp's steps; step i: records k0 + 4 U i .. + U - 1, those below kend
   auto locate = [&]() -> bool {           // false: nothing left
     while (left > 0) {
-      sp = span_of(a, b);
+      sp = a.span(b);
       tiles = tiles_of<U>(sp);
       const int64_t in_b = tiles ? divide(off, tiles + CA_ITEM) : INT_MAX;
       if (in_b >= a.Hkv * a.ntile) {
@@ -292,7 +312,7 @@ __global__ void __launch_bounds__(CA_WARPS * 32, ca_ctas(D, RT)) cache4_attn_ker
     bool bad = false;
     if (k < kend) {
       const int r = record_at(k);
-      const int page = a.table[static_cast<int64_t>(b) * a.table_stride + (r >> a.rec_shift)];
+      const int page = a.pages(b, kvh)[r >> a.rec_shift];
       bad = page < 0 || page >= a.n_pages;
       if (bad)
         record_status(a.status, -1 /* SPARGE_ERR_INVALID_ARG */);
@@ -324,7 +344,7 @@ __global__ void __launch_bounds__(CA_WARPS * 32, ca_ctas(D, RT)) cache4_attn_ker
       qi = 0;
       return nullptr;
     }
-    return reinterpret_cast<const uint4 *>(a.q + b * a.q_sb + (kvh * a.G + hg) * a.q_sh + static_cast<int64_t>(qi) * a.q_sn);
+    return reinterpret_cast<const uint4 *>(a.queries(b, kvh * a.G + hg) + static_cast<int64_t>(qi) * a.q_sn);
   };
   // Q rows of the next item: carried in registers over the end of the one before where they fit (d = 64),
   // else only fetched ahead of their use
@@ -708,16 +728,66 @@ SplitWs ws_layout(int64_t B, int64_t Hkv, int64_t rows, int64_t d) {
   return split_ws(B * Hkv * ((rows + 8 * rt - 1) / (8 * rt)), CA_SMS * ca_ctas(static_cast<int>(d), rt), rt, d);
 }
 
-template <int D, int RT>
-cudaError_t launch_cache_attn(const CacheAttnArgs &a, int64_t tiles, cudaStream_t st) {
+template <int D, int RT, typename Args>
+cudaError_t launch_cache_attn(const Args &a, int64_t tiles, cudaStream_t st) {
   using S = CaSmem<D, RT>;
   static std::atomic<unsigned long long> smem_set{0};
-  if (cudaError_t e = set_smem_limit_once(cache4_attn_kernel<D, RT>, S::TOTAL, smem_set); e != cudaSuccess) return e;
+  if (cudaError_t e = set_smem_limit_once(cache4_attn_kernel<D, RT, Args>, S::TOTAL, smem_set); e != cudaSuccess) return e;
   const int64_t most = CA_SMS * ca_ctas(D, RT), ctas = tiles < most ? tiles : most;
-  if (cudaError_t e = launch_dependent(cache4_attn_kernel<D, RT>, dim3(static_cast<unsigned>(ctas)), CA_WARPS * 32, S::TOTAL, st, a);
+  if (cudaError_t e = launch_dependent(cache4_attn_kernel<D, RT, Args>, dim3(static_cast<unsigned>(ctas)), CA_WARPS * 32, S::TOTAL, st, a);
       e != cudaSuccess)
     return e;
   return launch_split_combine<D, RT>(a, ctas, st);
+}
+
+// recs: an upper bound of the records that a sequence's queries see, for the number of CTAs (the lengths are on the device)
+template <typename Args>
+cudaError_t run_cache_attn(const Args &a, int d, int64_t recs, cudaStream_t s) {
+  const int64_t step = 4 * CaSmem<128, 1>::U;  // records of a CTA's tile
+  const int64_t tiles = ((recs + step - 1) / step + CA_ITEM) * a.B * a.Hkv * a.ntile;
+  if (d == 128) return row_tile(a.rows) == 1 ? launch_cache_attn<128, 1>(a, tiles, s) : launch_cache_attn<128, 2>(a, tiles, s);
+  return row_tile(a.rows) == 1 ? launch_cache_attn<64, 1>(a, tiles, s) : launch_cache_attn<64, 2>(a, tiles, s);
+}
+
+// The tensors, the pool and the scale of a call over the cache: checked, and what of its arguments follows from them (pages,
+// lengths and the split's rows are the caller's).
+int checked_args(const sparge_tensor *q, const sparge_cache4 *cache, float scale, sparge_tensor *o, View &qv, Cache4 &c,
+                 CacheAttnArgs &a) {
+  View ov;
+  int rc;
+  if ((rc = check_tensor(q, "q", &qv)) || (rc = check_tensor(o, "o", &ov)) || (rc = check_cache4(cache, &c))) return rc;
+  if (qv.B != ov.B || qv.H != ov.H || qv.N != ov.N || qv.d != ov.d) return fail(SPARGE_ERR_INVALID_ARG, "o disagrees with q");
+  if (qv.d != c.d) return fail(SPARGE_ERR_INVALID_ARG, "q and the cache disagree in d");
+  if (qv.H % c.H) return fail(SPARGE_ERR_UNSUPPORTED, "Hq=%lld not a multiple of the cache's %d heads", (long long)qv.H, c.H);
+  if (std::isnan(scale) || scale < 0.f || std::isinf(scale)) return fail(SPARGE_ERR_INVALID_ARG, "scale must be finite and >= 0");
+  a.q = static_cast<const __nv_bfloat16 *>(qv.data);
+  a.o = static_cast<__nv_bfloat16 *>(const_cast<void *>(ov.data));
+  a.q_sb = qv.sb; a.q_sh = qv.sh; a.q_sn = qv.sn;
+  a.o_sb = ov.sb; a.o_sh = ov.sh; a.o_sn = ov.sn;
+  a.pool = c.data;
+  a.n_pages = c.n_pages;
+  a.rec_shift = c.page_shift - 4;
+  a.Hkv = c.H;
+  a.G = static_cast<int>(qv.H / c.H);
+  a.window = a.sinks = 0;
+  a.scale_log2 = (scale > 0.f ? scale : 1.f / sqrtf(static_cast<float>(qv.d))) * 1.4426950408889634f;
+  return SPARGE_OK;
+}
+// B sequences of Nq queries, and the workspace of their split
+int set_split(CacheAttnArgs &a, int64_t B, int64_t Nq, int64_t d, void *ws, size_t ws_bytes) {
+  const int64_t rows = a.G * Nq, rt = row_tile(rows);
+  if (too_many(B, a.Hkv, rows)) return fail(SPARGE_ERR_UNSUPPORTED, "too many query rows");
+  const SplitWs w = ws_layout(B, a.Hkv, rows, d);
+  if (!ws || ws_bytes < w.total) return fail(SPARGE_ERR_WORKSPACE_TOO_SMALL, "workspace %zu bytes, need %zu", ws_bytes, w.total);
+  if (reinterpret_cast<uintptr_t>(ws) & 255u) return fail(SPARGE_ERR_INVALID_ARG, "workspace not 256-byte aligned");
+  a.B = static_cast<int>(B);
+  a.Nq = static_cast<int>(Nq);
+  a.rows = static_cast<int>(rows);
+  a.ntile = static_cast<int>((rows + 8 * rt - 1) / (8 * rt));
+  a.part_o = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + w.o);
+  a.part_ml = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + w.ml);
+  a.ends = reinterpret_cast<int2 *>(static_cast<uint8_t *>(ws) + w.ends);
+  return SPARGE_OK;
 }
 
 }  // namespace
@@ -738,63 +808,79 @@ int sparge_cache4_attn(const sparge_tensor *q, const sparge_cache4 *cache, const
                        int64_t table_stride, const int32_t *kv_lens, int64_t window, int64_t sinks, float scale,
                        sparge_tensor *o, void *ws, size_t ws_bytes, sparge_stream_t stream) {
   clear_error();
-  View qv, ov;
+  View qv;
   Cache4 c;
+  CacheAttnArgs a;
   int rc;
-  if ((rc = check_tensor(q, "q", &qv)) || (rc = check_tensor(o, "o", &ov)) || (rc = check_cache4(cache, &c))) return rc;
-  if (qv.B != ov.B || qv.H != ov.H || qv.N != ov.N || qv.d != ov.d) return fail(SPARGE_ERR_INVALID_ARG, "o disagrees with q");
-  if (qv.d != c.d) return fail(SPARGE_ERR_INVALID_ARG, "q and the cache disagree in d");
-  if (qv.H % c.H) return fail(SPARGE_ERR_UNSUPPORTED, "Hq=%lld not a multiple of the cache's %d heads", (long long)qv.H, c.H);
+  if ((rc = checked_args(q, cache, scale, o, qv, c, a))) return rc;
   if (window < 0 || sinks < 0 || window > INT_MAX || sinks > INT_MAX)
     return fail(SPARGE_ERR_INVALID_ARG, "window=%lld and sinks=%lld must be in 0..2^31-1", (long long)window, (long long)sinks);
   if (window == 0 && sinks != 0) return fail(SPARGE_ERR_INVALID_ARG, "sinks need a window");
-  if (std::isnan(scale) || scale < 0.f || std::isinf(scale)) return fail(SPARGE_ERR_INVALID_ARG, "scale must be finite and >= 0");
   if (width < 0 || table_stride < width || width > INT_MAX / c.page_size)
     return fail(SPARGE_ERR_INVALID_ARG, "table width %lld and stride %lld: the stride must reach the width, the width 2^31 tokens at most",
                 (long long)width, (long long)table_stride);
-  const int64_t rows = qv.H / c.H * qv.N, rt = row_tile(rows), ntile = (rows + 8 * rt - 1) / (8 * rt);
-  if (too_many(qv.B, c.H, rows)) return fail(SPARGE_ERR_UNSUPPORTED, "too many query rows");
-  const SplitWs w = ws_layout(qv.B, c.H, rows, qv.d);
-  if (!ws || ws_bytes < w.total) return fail(SPARGE_ERR_WORKSPACE_TOO_SMALL, "workspace %zu bytes, need %zu", ws_bytes, w.total);
-  if (reinterpret_cast<uintptr_t>(ws) & 255u) return fail(SPARGE_ERR_INVALID_ARG, "workspace not 256-byte aligned");
+  if ((rc = set_split(a, qv.B, qv.N, qv.d, ws, ws_bytes))) return rc;
   if (qv.B == 0 || qv.N == 0) return SPARGE_OK;
   if (!kv_lens || (width && !table)) return fail(SPARGE_ERR_INVALID_ARG, "table or kv_lens is NULL");
-  CacheAttnArgs a;
-  a.q = static_cast<const __nv_bfloat16 *>(qv.data);
-  a.o = static_cast<__nv_bfloat16 *>(const_cast<void *>(ov.data));
-  a.q_sb = qv.sb; a.q_sh = qv.sh; a.q_sn = qv.sn;
-  a.o_sb = ov.sb; a.o_sh = ov.sh; a.o_sn = ov.sn;
-  a.pool = c.data;
   a.table = table;
   a.lens = kv_lens;
   a.table_stride = table_stride;
-  a.n_pages = c.n_pages;
   a.width = static_cast<int>(width);
-  a.rec_shift = c.page_shift - 4;
-  a.B = static_cast<int>(qv.B); a.Hkv = c.H; a.G = static_cast<int>(qv.H / c.H);
-  a.Nq = static_cast<int>(qv.N); a.rows = static_cast<int>(rows); a.ntile = static_cast<int>(ntile);
   a.window = static_cast<int>(window);
   a.sinks = static_cast<int>(sinks);
-  a.scale_log2 = (scale > 0.f ? scale : 1.f / sqrtf(static_cast<float>(qv.d))) * 1.4426950408889634f;
-  a.part_o = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + w.o);
-  a.part_ml = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + w.ml);
-  a.ends = reinterpret_cast<int2 *>(static_cast<uint8_t *>(ws) + w.ends);
   a.status = status_ptr();
-  // an upper bound of the line of tiles, for the number of CTAs (the lengths are on the device)
   int64_t recs = (width * c.page_size + 15) / 16;
   if (window > 0) {
     const int64_t most = (window + qv.N + 15) / 16 + 1 + (sinks + 15) / 16;
     recs = recs < most ? recs : most;
   }
-  const int64_t step = 4 * CaSmem<128, 1>::U;  // records of a CTA's tile
-  const int64_t tiles = ((recs + step - 1) / step + CA_ITEM) * qv.B * c.H * ntile;
-  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  cudaError_t e;
-  if (qv.d == 128)
-    e = rt == 1 ? launch_cache_attn<128, 1>(a, tiles, s) : launch_cache_attn<128, 2>(a, tiles, s);
-  else
-    e = rt == 1 ? launch_cache_attn<64, 1>(a, tiles, s) : launch_cache_attn<64, 2>(a, tiles, s);
+  const cudaError_t e = run_cache_attn(a, static_cast<int>(qv.d), recs, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? SPARGE_OK : cuda_fail(e, "cache attention launch");
+}
+
+size_t sparge_cache4_pages_attn_workspace_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_t Nq, int64_t d) {
+  if (B < 0 || Hq <= 0 || Hkv <= 0 || Nq < 0 || (d != 64 && d != 128) || Hq % Hkv || B > 65535 || Hq > 65535 ||
+      Nq > (int64_t(1) << 30) || too_many(B * Nq, Hkv, Hq / Hkv))
+    return 0;
+  return ws_layout(B * Nq, Hkv, Hq / Hkv, d).total;
+}
+
+int sparge_cache4_pages_attn(const sparge_tensor *q, const sparge_cache4 *cache, const int32_t *pages, int64_t keep,
+                             const int32_t *lens, float scale, sparge_tensor *o, void *ws, size_t ws_bytes,
+                             sparge_stream_t stream) {
+  clear_error();
+  View qv;
+  Cache4 c;
+  CacheListArgs a;
+  int rc;
+  if ((rc = checked_args(q, cache, scale, o, qv, c, a))) return rc;
+  if (keep < 0 || keep > INT_MAX / c.page_size)
+    return fail(SPARGE_ERR_INVALID_ARG, "keep=%lld pages: 0 to 2^31 - 1 tokens", (long long)keep);
+  if ((rc = set_split(a, qv.B * qv.N, 1, qv.d, ws, ws_bytes))) return rc;
+  if (qv.B == 0 || qv.N == 0) return SPARGE_OK;
+  if (!lens || (keep && !pages)) return fail(SPARGE_ERR_INVALID_ARG, "pages or lens is NULL");
+  a.table = pages;
+  a.lens = lens;
+  a.table_stride = 0;
+  a.width = static_cast<int>(keep);
+  a.queries_of = static_cast<int>(qv.N);
+  a.status = status_ptr();
+  const cudaError_t e = run_cache_attn(a, static_cast<int>(qv.d), keep * c.page_size / 16, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? SPARGE_OK : cuda_fail(e, "attention over selected pages: launch");
+}
+
+size_t sparge_cache4_prefix_attn_workspace_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_t Nq, int64_t d) {
+  return sparge_cache4_attn_workspace_bytes(B, Hq, Hkv, Nq, d);
+}
+
+int sparge_cache4_prefix_attn(const sparge_tensor *q, const sparge_cache4 *cache, const int32_t *prefix_pages, int64_t n_prefix,
+                              const int32_t *table, int64_t width, int64_t table_stride, const int32_t *kv_lens, float scale,
+                              sparge_tensor *o, void *ws, size_t ws_bytes, sparge_stream_t stream) {
+  clear_error();
+  if (n_prefix < 0 || n_prefix > width)
+    return fail(SPARGE_ERR_INVALID_ARG, "n_prefix=%lld pages not in 0..%lld, the table's width", (long long)n_prefix, (long long)width);
+  if (n_prefix && !prefix_pages) return fail(SPARGE_ERR_INVALID_ARG, "prefix_pages is NULL");
+  return sparge_cache4_attn(q, cache, table, width, table_stride, kv_lens, 0, 0, scale, o, ws, ws_bytes, stream);
 }
 
 }  // extern "C"

@@ -17,11 +17,37 @@ namespace sparge {
 __device__ __forceinline__ void wait_for_earlier() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void let_dependents_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
+// Both at a kernel's start: the one behind it may be set up from now on, and this one waits for the one in front.
+__device__ __forceinline__ void start_after_earlier() {
+  let_dependents_start();
+  wait_for_earlier();
+}
+
 // 16 bytes that are read once: past the L1 cache
 __device__ __forceinline__ uint4 ld_once_v4(const void *p) {
   uint4 v;
   asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
   return v;
+}
+
+// cluster: thread blocks of a cluster along the grid's x
+template <typename... KArgs, typename... Args>
+inline cudaError_t launch_dependent_clusters(void (*kernel)(KArgs...), dim3 grid, unsigned threads, size_t smem, unsigned cluster,
+                                             cudaStream_t st, const Args &...args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = cluster;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 template <typename... KArgs, typename... Args>

@@ -37,7 +37,14 @@ struct NormRopeArgs {
   int64_t tokens;  // B N
   int N, rot, per;  // per: heads of one CTA
   float eps;
+  // several position axes: pair i turns by the position on axis axes[i]; positions pos[axis pos_sa + b pos_sb + n]
+  const int32_t *axes;
+  int64_t pos_sa, pos_sb;
+  int n_axes;
+  int *status;
 };
+
+constexpr int NR_AXES = 4;
 
 constexpr int NR_THREADS = 128;
 // Heads whose rows a thread has in flight while it computes as many (32K tokens of 32 + 8 heads: 104 us;
@@ -59,7 +66,7 @@ __device__ __forceinline__ uint64_t turns64(double f) {
   return (b >> 63) ? 0ull - t : t;
 }
 
-template <int D, bool INTER>
+template <int D, bool INTER, bool AXES>
 __global__ void __launch_bounds__(NR_THREADS) norm_rope_kernel(const NormRopeArgs a) {
   constexpr int TR = D / 16;                 // threads of a row
   constexpr int TOK = NR_THREADS / TR;       // tokens of a CTA
@@ -102,7 +109,24 @@ __global__ void __launch_bounds__(NR_THREADS) norm_rope_kernel(const NormRopeArg
   wait_for_earlier();
   int cnt = load(h);
   __shared__ uint64_t turns[D / 2];
-  for (int j = threadIdx.x; j < a.rot / 2; j += NR_THREADS) turns[j] = turns64(a.inv_freq[j]);
+  __shared__ int8_t axis_of[AXES ? D / 2 : 1];
+  int32_t at[NR_AXES];  // the token's position on each axis, on its way while the frequencies are
+  if constexpr (AXES) {
+#pragma unroll
+    for (int x = 0; x < NR_AXES; ++x) at[x] = t < rc && x < a.n_axes ? a.pos[x * a.pos_sa + b * a.pos_sb + n] : 0;
+  }
+  for (int j = threadIdx.x; j < a.rot / 2; j += NR_THREADS) {
+    turns[j] = turns64(a.inv_freq[j]);
+    if constexpr (AXES) {
+      const int x = a.axes[j];
+      axis_of[j] = static_cast<int8_t>(x);
+      if (x < 0 || x >= a.n_axes) {  // no such axis: the pair does not turn
+        turns[j] = 0ull;
+        axis_of[j] = 0;
+        record_status(a.status, -1 /* SPARGE_ERR_INVALID_ARG */);
+      }
+    }
+  }
   __syncthreads();
   float cs[8], sn[8];
 #pragma unroll
@@ -111,9 +135,14 @@ __global__ void __launch_bounds__(NR_THREADS) norm_rope_kernel(const NormRopeArg
     sn[j] = 0.f;
   }
   if (t < rc) {
-    const int64_t pos = a.pos ? static_cast<int64_t>(a.pos[mm]) : a.start + n;
+    int64_t pos = 0;
+    if constexpr (!AXES) pos = a.pos ? static_cast<int64_t>(a.pos[mm]) : a.start + n;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
+      if constexpr (AXES) {
+        const int x = axis_of[8 * t + j];
+        pos = x == 0 ? at[0] : x == 1 ? at[1] : x == 2 ? at[2] : at[3];
+      }
       const uint64_t ph = static_cast<uint64_t>(pos) * turns[8 * t + j];
       const float angle = static_cast<float>(static_cast<int32_t>(ph >> 32)) * 1.4629180792671596e-9f;  // pi 2^-31
       sn[j] = __sinf(angle);
@@ -205,10 +234,20 @@ __global__ void __launch_bounds__(NR_THREADS) norm_rope_kernel(const NormRopeArg
 
 using namespace sparge;
 
-extern "C" int sparge_qk_norm_rope(const sparge_tensor *q, const sparge_tensor *k, const int32_t *positions,
-                                   int64_t start, const double *inv_freq, int rot_dim, int interleaved,
-                                   const float *q_weight, const float *k_weight, float eps, sparge_tensor *q_out,
-                                   sparge_tensor *k_out, sparge_stream_t stream) {
+namespace {
+
+// positions of one axis (axes NULL), or of n_axes with the axis of each pair
+struct Positions {
+  const int32_t *at;
+  int64_t start;
+  const int32_t *axes;
+  int n_axes;
+  int64_t sa, sb;
+};
+
+int norm_rope(const sparge_tensor *q, const sparge_tensor *k, const Positions &p, bool several, const double *inv_freq, int rot_dim,
+              int interleaved, const float *q_weight, const float *k_weight, float eps, sparge_tensor *q_out, sparge_tensor *k_out,
+              sparge_stream_t stream) {
   clear_error();
   View v[4];
   int rc;
@@ -227,6 +266,12 @@ extern "C" int sparge_qk_norm_rope(const sparge_tensor *q, const sparge_tensor *
   if (rot_dim < 0 || rot_dim > v[0].d || rot_dim % 16)
     return fail(SPARGE_ERR_INVALID_ARG, "rot_dim=%d must be a multiple of 16 in 0..%lld", rot_dim, (long long)v[0].d);
   if (rot_dim > 0 && !inv_freq) return fail(SPARGE_ERR_INVALID_ARG, "inv_freq is NULL");
+  if (several) {
+    if (p.n_axes < 1 || p.n_axes > NR_AXES)
+      return fail(SPARGE_ERR_UNSUPPORTED, "n_axes=%d not in 1..%d", p.n_axes, NR_AXES);
+    if (p.sa < 0 || p.sb < 0) return fail(SPARGE_ERR_INVALID_ARG, "negative strides of positions");
+    if (rot_dim > 0 && v[0].B * v[0].N != 0 && (!p.axes || !p.at)) return fail(SPARGE_ERR_INVALID_ARG, "axes or positions is NULL");
+  }
   if (!(eps >= 0.f) || std::isinf(eps)) return fail(SPARGE_ERR_INVALID_ARG, "eps=%g must be finite and >= 0", (double)eps);
   if (v[0].B * v[0].N == 0) return SPARGE_OK;
   NormRopeArgs a;
@@ -239,9 +284,14 @@ extern "C" int sparge_qk_norm_rope(const sparge_tensor *q, const sparge_tensor *
   }
   a.w[0] = q_weight;
   a.w[1] = k_weight;
-  a.pos = positions;
+  a.pos = p.at;
   a.inv_freq = inv_freq;
-  a.start = start;
+  a.start = p.start;
+  a.axes = p.axes;
+  a.n_axes = p.n_axes;
+  a.pos_sa = p.sa;
+  a.pos_sb = p.sb;
+  a.status = several ? status_ptr() : nullptr;
   a.tokens = v[0].B * v[0].N;
   a.N = static_cast<int>(v[0].N);
   a.rot = rot_dim;
@@ -260,9 +310,32 @@ extern "C" int sparge_qk_norm_rope(const sparge_tensor *q, const sparge_tensor *
   a.per = static_cast<int>(per);
   const dim3 grid(static_cast<unsigned>(tiles), static_cast<unsigned>((heads + per - 1) / per));
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const cudaError_t e =
-      launch_dependent(d == 128 ? (interleaved ? norm_rope_kernel<128, true> : norm_rope_kernel<128, false>)
-                                : (interleaved ? norm_rope_kernel<64, true> : norm_rope_kernel<64, false>),
-                       grid, NR_THREADS, 0, s, a);
+  auto kernel = d == 128 ? (interleaved ? norm_rope_kernel<128, true, false> : norm_rope_kernel<128, false, false>)
+                         : (interleaved ? norm_rope_kernel<64, true, false> : norm_rope_kernel<64, false, false>);
+  if (several)
+    kernel = d == 128 ? (interleaved ? norm_rope_kernel<128, true, true> : norm_rope_kernel<128, false, true>)
+                      : (interleaved ? norm_rope_kernel<64, true, true> : norm_rope_kernel<64, false, true>);
+  const cudaError_t e = launch_dependent(kernel, grid, NR_THREADS, 0, s, a);
   return e == cudaSuccess ? SPARGE_OK : cuda_fail(e, "norm and rotation launch");
 }
+
+}  // namespace
+
+extern "C" {
+
+int sparge_qk_norm_rope(const sparge_tensor *q, const sparge_tensor *k, const int32_t *positions, int64_t start,
+                        const double *inv_freq, int rot_dim, int interleaved, const float *q_weight, const float *k_weight, float eps,
+                        sparge_tensor *q_out, sparge_tensor *k_out, sparge_stream_t stream) {
+  return norm_rope(q, k, Positions{positions, start, nullptr, 0, 0, 0}, false, inv_freq, rot_dim, interleaved, q_weight, k_weight, eps,
+                   q_out, k_out, stream);
+}
+
+int sparge_qk_norm_rope_axes(const sparge_tensor *q, const sparge_tensor *k, const int32_t *positions, int n_axes, int64_t axis_stride,
+                             int64_t batch_stride, const int32_t *axes, const double *inv_freq, int rot_dim, int interleaved,
+                             const float *q_weight, const float *k_weight, float eps, sparge_tensor *q_out, sparge_tensor *k_out,
+                             sparge_stream_t stream) {
+  return norm_rope(q, k, Positions{positions, 0, axes, n_axes, axis_stride, batch_stride}, true, inv_freq, rot_dim, interleaved, q_weight,
+                   k_weight, eps, q_out, k_out, stream);
+}
+
+}  // extern "C"

@@ -27,6 +27,12 @@ struct SplitArgs {
   int B, Hkv, G, Nq, rows, ntile;  // rows = G Nq, ntile row tiles
   float *part_o, *part_ml;         // [CTA + item][8 RT][D], [CTA + item][8 RT] (reference, sum)
   int2 *ends;                      // per item: its first and last CTA
+  // every item leaves partial results, also one inside a single CTA (another kernel adds to them)
+  static constexpr bool PARTIAL = false;
+  // output row r of KV head kvh of sequence b
+  __device__ __forceinline__ __nv_bfloat16 *row(int b, int kvh, int r) const {
+    return o + b * o_sb + (kvh * G + r / Nq) * o_sh + static_cast<int64_t>(r % Nq) * o_sn;
+  }
 };
 
 // Row tiles of 8 rows for up to 8 query rows per KV head, else of 16.
@@ -84,15 +90,12 @@ __device__ __forceinline__ void put_row(__nv_bfloat16 *to, float4 o, float inv) 
   w.y = pack_bf16x2(o.z * inv, o.w * inv);
   *reinterpret_cast<uint2 *>(to) = w;
 }
-__device__ __forceinline__ __nv_bfloat16 *out_row(const SplitArgs &a, int b, int kvh, int r) {
-  return a.o + b * a.o_sb + (kvh * a.G + r / a.Nq) * a.o_sh + static_cast<int64_t>(r % a.Nq) * a.o_sn;
-}
 
 // The end of an item in a CTA, called by all its threads.  sums + w * wstride: warp w's O rows, orow
 // floats apart; ml: (reference, sum) of warp w's row at w * 8 RT + row.  first / last: this CTA holds the
 // item's first / last tile.
-template <int D, int RT>
-__device__ __forceinline__ void end_item(const SplitArgs &a, const uint8_t *sums, int wstride, int orow, const float2 *ml,
+template <int D, int RT, typename Args>
+__device__ __forceinline__ void end_item(const Args &a, const uint8_t *sums, int wstride, int orow, const float2 *ml,
                                          int item, int b, int kvh, int row0, bool first, bool last) {
   __syncthreads();
   if (threadIdx.x == 0) {
@@ -118,8 +121,8 @@ __device__ __forceinline__ void end_item(const SplitArgs &a, const uint8_t *sums
       if (f != 0.f) L = fmaf(f, w[u].y, L);
       add_share(o, f, *reinterpret_cast<const float4 *>(sums + u * wstride + (row * orow + 4 * d4) * 4));
     }
-    if (first && last) {
-      put_row(out_row(a, b, kvh, row0 + row) + 4 * d4, o, L == 0.f ? 0.f : 1.f / L);
+    if (!Args::PARTIAL && first && last) {
+      put_row(a.row(b, kvh, row0 + row) + 4 * d4, o, L == 0.f ? 0.f : 1.f / L);
     } else {
       *reinterpret_cast<float4 *>(a.part_o + (slot * 8 * RT + row) * D + 4 * d4) = o;
       if (d4 == 0) *reinterpret_cast<float2 *>(a.part_ml + (slot * 8 * RT + row) * 2) = make_float2(M, L);
@@ -145,7 +148,7 @@ __global__ void __launch_bounds__(CC_THREADS) split_combine_kernel(const Args a,
   const int b = item / per, kvh = item % per / a.ntile, row0 = (item % a.ntile) * 8 * RT;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int first = blockIdx.y * nrow, last = min(min(8 * RT, a.rows - row0), first + nrow);
-  auto out = [&](int row) { return out_row(a, b, kvh, row0 + row) + 4 * lane; };
+  auto out = [&](int row) { return a.row(b, kvh, row0 + row) + 4 * lane; };
   wait_for_earlier();
   const int2 ends = a.ends[item];
   if (a.empty(b)) {

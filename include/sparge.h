@@ -313,6 +313,18 @@ int sparge_qk_norm_rope(const sparge_tensor *q, const sparge_tensor *k, const in
                         sparge_stream_t stream);
 
 /*
+ * sparge_qk_norm_rope with positions on several axes (time, height and width of image and video tokens): pair i
+ * turns by t = position on axis axes[i] * inv_freq[i].  positions: n_axes (1..4) times (B,N) int32, the position of token
+ * n of sequence b on axis x at x * axis_stride + b * batch_stride + n (strides in elements, 0 where axes or
+ * sequences share positions).  axes: rot_dim/2 int32; an entry outside 0..n_axes-1 leaves its pair unturned and records
+ * SPARGE_ERR_INVALID_ARG in the device status word.  Everything else as there; with rot_dim 0 both may be NULL.
+ */
+int sparge_qk_norm_rope_axes(const sparge_tensor *q, const sparge_tensor *k, const int32_t *positions, int n_axes,
+                             int64_t axis_stride, int64_t batch_stride, const int32_t *axes, const double *inv_freq,
+                             int rot_dim, int interleaved, const float *q_weight, const float *k_weight, float eps,
+                             sparge_tensor *q_out, sparge_tensor *k_out, sparge_stream_t stream);
+
+/*
  * A paged key/value cache held in 4 bits.  The pool has n_pages pages of page_size tokens (16, 32,
  * 64, 128 or 256) for H key/value heads of d channels: sparge_cache4_bytes bytes at a 16-byte aligned device
  * address.  Every 64 channels of a token's K or V row are held as codes n in 0..15 with a bf16 scale and
@@ -383,6 +395,61 @@ size_t sparge_cache4_attn_workspace_bytes(int64_t B, int64_t Hq, int64_t Hkv, in
 int sparge_cache4_attn(const sparge_tensor *q, const sparge_cache4 *cache, const int32_t *table, int64_t width,
                        int64_t table_stride, const int32_t *kv_lens, int64_t window, int64_t sinks, float scale,
                        sparge_tensor *o, void *ws, size_t ws_bytes, sparge_stream_t stream);
+
+/*
+ * Bounds of the cache's pages, for attention over the pages that matter to a query.  For every page and head: the largest
+ * and the smallest key of each channel over the page's tokens (as the cache reads them back), as int8 codes of one power of two s,
+ * rounded outwards: s ceil(max / s) and s floor(min / s), s the least power of two whose codes stay within +-127 (at
+ * least 2^-126); s is infinite where the page holds an infinity or a NaN.  A page's bounds: codes [H][max, min][d], then H floats s, padded to
+ * 32 bytes; sparge_cache4_bounds_bytes for n_pages of them (0 for an unsupported shape), 16-byte aligned.
+ * sparge_cache4_bounds_update renews the bounds of the pages on which the last N of the kv_lens[b] tokens of each sequence
+ * lie (lengths and table as sparge_cache4_attn takes them), all other pages' stay as they are: call it after a store, with
+ * the N new tokens.  A page in two rows of the table gets the bounds of either length.
+ * sparge_cache4_bounds_load reads the bounds of pages[0 .. n-1] back as values: hi and lo (n,H,d) bf16 (exact), zero
+ * rows for negative pages.  A page past the pool is left out (there: a zero row) and records SPARGE_ERR_INVALID_ARG in the
+ * device status word.
+ */
+size_t sparge_cache4_bounds_bytes(int64_t n_pages, int H, int d);
+int sparge_cache4_bounds_update(const sparge_cache4 *cache, const int32_t *table, int64_t B, int64_t width, int64_t table_stride,
+                                const int32_t *kv_lens, int64_t N, void *bounds, size_t bounds_bytes, sparge_stream_t stream);
+int sparge_cache4_bounds_load(const sparge_cache4 *cache, const void *bounds, size_t bounds_bytes, const int32_t *pages, int64_t n,
+                              void *hi, void *lo, sparge_stream_t stream);
+
+/*
+ * The pages that matter to each query, by the bounds.  q (B,Hq,Nq,d), table and kv_lens as in sparge_cache4_attn: query r of
+ * sequence b sees seen = kv_lens[b] - Nq + r + 1 tokens on its first ceil(seen / page_size) pages.  A page's score for a query row is
+ * t s sum_c max(r_c hi_c, r_c lo_c) with r = round-to-even(q / t) in int8, t the least power of two for it as s above: no
+ * token of the page has a larger product with t r.  A key/value head's score is the largest of its query heads'; a page of infinite s
+ * scores infinity, a query row with an infinity or a NaN scores every finite page 0.  Kept are the `first` first and the `last` last pages of those
+ * that the query sees (last >= 1), then the largest scores, the earlier page where scores are equal, up to `keep`
+ * pages in all.
+ * pages (B,Nq,H,keep) int32 receives the kept pages' numbers in the pool, in the order of the sequence, -1 behind them; lens (B,Nq)
+ * int32 the number of tokens on them.  At most 64 query heads per key/value head and 40960 table columns.
+ */
+int sparge_cache4_select(const sparge_tensor *q, const sparge_cache4 *cache, const void *bounds, size_t bounds_bytes,
+                         const int32_t *table, int64_t width, int64_t table_stride, const int32_t *kv_lens, int64_t keep,
+                         int64_t first, int64_t last, int32_t *pages, int32_t *lens, sparge_stream_t stream);
+
+/*
+ * Attention over lists of pages: query r of sequence b sees, in key/value head h, the first lens[b][r] tokens on the pages
+ * pages[b][r][h][0 .. keep-1] (arrays as sparge_cache4_select writes them).  Everything else as sparge_cache4_attn; the
+ * cache is read once per query and 16 heads of a key/value head.
+ */
+size_t sparge_cache4_pages_attn_workspace_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_t Nq, int64_t d);
+int sparge_cache4_pages_attn(const sparge_tensor *q, const sparge_cache4 *cache, const int32_t *pages, int64_t keep,
+                             const int32_t *lens, float scale, sparge_tensor *o, void *ws, size_t ws_bytes,
+                             sparge_stream_t stream);
+
+/*
+ * sparge_cache4_attn (without a window) for a batch whose sequences begin with the same tokens: those on the pages
+ * prefix_pages[0 .. n_prefix-1], every token of them.  They are read and multiplied once for all sequences.  Each row of table
+ * holds these pages in its first n_prefix columns (n_prefix <= width), then the sequence's own; kv_lens counts both.  A sequence whose
+ * queries do not all stand behind the prefix is attended over its own row alone, so any length is taken.
+ */
+size_t sparge_cache4_prefix_attn_workspace_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_t Nq, int64_t d);
+int sparge_cache4_prefix_attn(const sparge_tensor *q, const sparge_cache4 *cache, const int32_t *prefix_pages, int64_t n_prefix,
+                              const int32_t *table, int64_t width, int64_t table_stride, const int32_t *kv_lens, float scale,
+                              sparge_tensor *o, void *ws, size_t ws_bytes, sparge_stream_t stream);
 
 /*
  * Hilbert-curve token order (SpargeAttention summary page: a space-filling Hilbert-curve
