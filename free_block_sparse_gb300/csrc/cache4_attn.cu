@@ -109,6 +109,21 @@ struct CacheListArgs : CacheAttnArgs {
   }
 };
 
+// What stands behind a prefix that is attended elsewhere: a sequence's records from first_rec on (all of them if its queries do
+// not all stand behind the prefix), as shares for another kernel to combine.
+struct CacheTailArgs : CacheAttnArgs {
+  int first_rec;
+  static constexpr bool PARTIAL = true;
+  __device__ __forceinline__ Span span(int b) const {
+    Span s;
+    s.len = length(b);
+    s.ns = 0;
+    s.lo = (s.len - Nq) >= first_rec * 16 ? first_rec : 0;
+    s.recs = static_cast<int>((static_cast<int64_t>(s.len) + 15) >> 4) - s.lo;
+    return s;
+  }
+};
+
 // CTAs per SM, by registers: the sums of 16 rows of 128 channels alone take 64 per thread.  (16 rows of
 // d = 128, 4 queries of 128 sequences of 4100 with 4 KV heads: 2 CTAs 93 us, 3 with one record a step and spills 113; with 8, 180;
 // d = 64: 3 CTAs 56 us, 2 65.)
@@ -737,6 +752,7 @@ cudaError_t launch_cache_attn(const Args &a, int64_t tiles, cudaStream_t st) {
   if (cudaError_t e = launch_dependent(cache4_attn_kernel<D, RT, Args>, dim3(static_cast<unsigned>(ctas)), CA_WARPS * 32, S::TOTAL, st, a);
       e != cudaSuccess)
     return e;
+  if constexpr (Args::PARTIAL) return cudaSuccess;
   return launch_split_combine<D, RT>(a, ctas, st);
 }
 
@@ -771,6 +787,12 @@ int checked_args(const sparge_tensor *q, const sparge_cache4 *cache, float scale
   a.G = static_cast<int>(qv.H / c.H);
   a.window = a.sinks = 0;
   a.scale_log2 = (scale > 0.f ? scale : 1.f / sqrtf(static_cast<float>(qv.d))) * 1.4426950408889634f;
+  return SPARGE_OK;
+}
+int checked_table(const Cache4 &c, int64_t width, int64_t table_stride) {
+  if (width < 0 || table_stride < width || width > INT_MAX / c.page_size)
+    return fail(SPARGE_ERR_INVALID_ARG, "table width %lld and stride %lld: the stride must reach the width, the width 2^31 tokens at most",
+                (long long)width, (long long)table_stride);
   return SPARGE_OK;
 }
 // B sequences of Nq queries, and the workspace of their split
@@ -816,10 +838,7 @@ int sparge_cache4_attn(const sparge_tensor *q, const sparge_cache4 *cache, const
   if (window < 0 || sinks < 0 || window > INT_MAX || sinks > INT_MAX)
     return fail(SPARGE_ERR_INVALID_ARG, "window=%lld and sinks=%lld must be in 0..2^31-1", (long long)window, (long long)sinks);
   if (window == 0 && sinks != 0) return fail(SPARGE_ERR_INVALID_ARG, "sinks need a window");
-  if (width < 0 || table_stride < width || width > INT_MAX / c.page_size)
-    return fail(SPARGE_ERR_INVALID_ARG, "table width %lld and stride %lld: the stride must reach the width, the width 2^31 tokens at most",
-                (long long)width, (long long)table_stride);
-  if ((rc = set_split(a, qv.B, qv.N, qv.d, ws, ws_bytes))) return rc;
+  if ((rc = checked_table(c, width, table_stride)) || (rc = set_split(a, qv.B, qv.N, qv.d, ws, ws_bytes))) return rc;
   if (qv.B == 0 || qv.N == 0) return SPARGE_OK;
   if (!kv_lens || (width && !table)) return fail(SPARGE_ERR_INVALID_ARG, "table or kv_lens is NULL");
   a.table = table;
@@ -870,17 +889,59 @@ int sparge_cache4_pages_attn(const sparge_tensor *q, const sparge_cache4 *cache,
 }
 
 size_t sparge_cache4_prefix_attn_workspace_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_t Nq, int64_t d) {
-  return sparge_cache4_attn_workspace_bytes(B, Hq, Hkv, Nq, d);
+  const size_t own = sparge_cache4_attn_workspace_bytes(B, Hq, Hkv, Nq, d);
+  return own == 0 || B * (Hq / Hkv) * Nq > INT_MAX / 2 ? 0 : own + prefix_ws_bytes(B * (Hq / Hkv) * Nq, Hkv, d);
 }
 
 int sparge_cache4_prefix_attn(const sparge_tensor *q, const sparge_cache4 *cache, const int32_t *prefix_pages, int64_t n_prefix,
                               const int32_t *table, int64_t width, int64_t table_stride, const int32_t *kv_lens, float scale,
                               sparge_tensor *o, void *ws, size_t ws_bytes, sparge_stream_t stream) {
   clear_error();
+  View qv;
+  Cache4 c;
+  CacheTailArgs a;
+  int rc;
+  if ((rc = checked_args(q, cache, scale, o, qv, c, a)) || (rc = checked_table(c, width, table_stride))) return rc;
   if (n_prefix < 0 || n_prefix > width)
     return fail(SPARGE_ERR_INVALID_ARG, "n_prefix=%lld pages not in 0..%lld, the table's width", (long long)n_prefix, (long long)width);
   if (n_prefix && !prefix_pages) return fail(SPARGE_ERR_INVALID_ARG, "prefix_pages is NULL");
-  return sparge_cache4_attn(q, cache, table, width, table_stride, kv_lens, 0, 0, scale, o, ws, ws_bytes, stream);
+  if (qv.B * a.G * qv.N > INT_MAX / 2) return fail(SPARGE_ERR_UNSUPPORTED, "too many query rows");
+  if ((rc = set_split(a, qv.B, qv.N, qv.d, ws, ws_bytes))) return rc;
+  const size_t own = ws_layout(qv.B, c.H, a.rows, qv.d).total, need = own + prefix_ws_bytes(qv.B * a.rows, c.H, qv.d);
+  if (ws_bytes < need) return fail(SPARGE_ERR_WORKSPACE_TOO_SMALL, "workspace %zu bytes, need %zu", ws_bytes, need);
+  if (qv.B == 0 || qv.N == 0) return SPARGE_OK;
+  if (!kv_lens || (width && !table)) return fail(SPARGE_ERR_INVALID_ARG, "table or kv_lens is NULL");
+  a.table = table;
+  a.lens = kv_lens;
+  a.table_stride = table_stride;
+  a.width = static_cast<int>(width);
+  a.status = status_ptr();
+  const int d = static_cast<int>(qv.d), per = c.page_size / 16;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  if (n_prefix == 0) {
+    e = run_cache_attn(static_cast<const CacheAttnArgs &>(a), d, width * per, s);
+    return e == cudaSuccess ? SPARGE_OK : cuda_fail(e, "cache attention launch");
+  }
+  a.first_rec = static_cast<int>(n_prefix) * per;
+  PrefixAttn l;
+  l.q = qv.data;
+  l.q_sb = qv.sb; l.q_sh = qv.sh; l.q_sn = qv.sn;
+  l.pool = c.data;
+  l.pages = prefix_pages;
+  l.lens = kv_lens;
+  l.n_pages = c.n_pages;
+  l.rec_shift = a.rec_shift;
+  l.prefix = a.first_rec * 16;
+  l.width = a.width;
+  l.d = d;
+  l.scale_log2 = a.scale_log2;
+  l.ws = static_cast<uint8_t *>(ws) + own;
+  l.status = a.status;
+  e = launch_prefix_attn(l, a, s);
+  if (e == cudaSuccess) e = run_cache_attn(a, d, (width - n_prefix) * per, s);
+  if (e == cudaSuccess) e = launch_prefix_combine(l, a, s);
+  return e == cudaSuccess ? SPARGE_OK : cuda_fail(e, "attention behind a prefix: launch");
 }
 
 }  // extern "C"

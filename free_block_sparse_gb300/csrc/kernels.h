@@ -221,6 +221,24 @@ struct WindowDecode {
 size_t window_decode_ws_bytes(int64_t B, int64_t Hkv, int64_t d);
 cudaError_t launch_window_decode(const WindowDecode &l, cudaStream_t st);
 
+// Attention of a batch over the prefix that its sequences share (prefix_attn.cu), and the combination of its shares with those
+// of the sequences' own tokens, which the cache attention leaves in `own`.
+struct SplitArgs;
+struct PrefixAttn {
+  const void *q;
+  int64_t q_sb, q_sh, q_sn;
+  const uint8_t *pool;
+  const int32_t *pages, *lens;
+  int64_t n_pages;
+  int rec_shift, prefix, width, d;  // prefix: its tokens; width: columns of the sequences' table
+  float scale_log2;
+  void *ws;
+  int *status;
+};
+size_t prefix_ws_bytes(int64_t rows, int64_t Hkv, int64_t d);
+cudaError_t launch_prefix_attn(const PrefixAttn &l, const SplitArgs &own, cudaStream_t st);
+cudaError_t launch_prefix_combine(const PrefixAttn &l, const SplitArgs &own, cudaStream_t st);
+
 // Decoding tiles (decode.cu): before the attention, the ascending list of key blocks that any of
 // the G heads of each (batch, KV head) keeps in query block 0 (list [B Hkv][nkb], count [B Hkv]);
 // after it, the shares' partial rows combined into o (bf16, strides in elements).
