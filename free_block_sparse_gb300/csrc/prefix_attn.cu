@@ -14,7 +14,8 @@ namespace sparge {
 namespace {
 
 constexpr int PF_SOFT = 8, PF_WIDE = 4;  // softmax warps, widening warps
-constexpr int PF_THREADS = (PF_SOFT + PF_WIDE + 2) * 32;
+constexpr int PF_PROD = PF_SOFT + PF_WIDE, PF_LOAD = PF_PROD + 2;  // a products warp per stream, the loads warp
+constexpr int PF_THREADS = (PF_LOAD + 1) * 32;
 constexpr int PF_ROWS = 256;             // rows of a slot: two streams of 128
 constexpr float PF_RESCALE = 8.f;
 constexpr float PF_TOP = 15.f;           // P' stays below 2^15, within f16
@@ -39,14 +40,14 @@ struct PfCfg {
   static constexpr int PITCH = Rec4<D>::BYTES + 64;  // of a record in the ring, so that two of them fall on different banks
   static constexpr int RAW = 4 * PITCH;
   static constexpr int RS = 6, NS = R == 2 ? 3 : 4;  // stages of raw tiles, of widened ones
-  static constexpr bool QSMEM = D == 128 && R == 2;  // the second stream's Q has no TMEM left
+  static constexpr bool QSMEM = D == 128 && R == 2;  // no room in TMEM for two tiles of Q
   static constexpr uint32_t TILE = 64 * D * 2;       // of K or V, f16
-  static constexpr uint32_t K = 0, V = K + NS * TILE, Q = V + NS * TILE, RING = Q + (QSMEM ? 128 * D * 2 : 0);
-  static constexpr uint32_t TABK = RING + RS * RAW, TABV = TABK + 64 * 16, CTRL = TABV + 2 * 2 * 64 * 2;
+  static constexpr uint32_t K = 0, V = K + NS * TILE, Q = V + NS * TILE, RING = Q + (QSMEM ? 2 * 128 * D * 2 : 0);
+  static constexpr uint32_t TABK = RING + RS * RAW, TABV = TABK + 2 * 64 * 16, CTRL = TABV + 2 * 512;
   static constexpr uint32_t SMEM = CTRL + 1024;
   // TMEM columns
   static constexpr uint32_t O = 0, S = 2 * D, P = S + 128, QC = P + 64, QCOLS = D / 2;
-  static_assert(QC + (QSMEM ? 1 : 2) * QCOLS <= 512 || R == 1, "TMEM");
+  static_assert(QC + (QSMEM ? 0 : R) * QCOLS <= 512, "TMEM");
   static_assert(SMEM <= 227 * 1024, "shared memory");
 };
 struct PfInfo {  // of a widened tile: K = K' k_unit, V = V' 2^g; bit r of missing: record r is not there
@@ -56,9 +57,9 @@ struct PfInfo {  // of a widened tile: K = K' k_unit, V = V' 2^g; bit r of missi
 };
 struct PfCtrl {
   uint64_t raw_full[8], raw_free[8], kv_full[4], kv_free[4];
-  uint64_t q_full[2], s_full[2], s_free[2], p_full[2], pv_done[2], drained;
+  uint64_t q_full[2], q_free, s_full[2], s_free[2], p_full[2], pv_done[2], drained[2];
   PfInfo info[4];
-  int need[PF_WIDE];
+  int need[2][PF_WIDE];
   uint8_t bad[8][4];
   uint32_t tmem;
   int abort, no_abort;
@@ -143,7 +144,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefix_attn_kernel(const Prefix
     }
     for (int s = 0; s < NS; ++s) {
       mbar_init(&cs.kv_full[s], PF_WIDE);
-      mbar_init(&cs.kv_free[s], 1);
+      mbar_init(&cs.kv_free[s], R);
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(&cs.q_full[t], 4);
@@ -152,12 +153,14 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefix_attn_kernel(const Prefix
       mbar_init(&cs.p_full[t], 4);
       mbar_init(&cs.pv_done[t], 1);
     }
-    mbar_init(&cs.drained, 1);
+    mbar_init(&cs.drained[0], 1);
+    mbar_init(&cs.drained[1], 1);
+    mbar_init(&cs.q_free, 1);
     cs.abort = 0;
     cs.no_abort = 0;
     fence_barrier_init();
   }
-  if (warp == PF_SOFT + PF_WIDE) {
+  if (warp == PF_PROD) {
     tmem_alloc(&cs.tmem, 512);
     tmem_relinquish();
   }
@@ -175,9 +178,9 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefix_attn_kernel(const Prefix
     const int t = warp >> 2, row = (warp & 3) * 32 + lane;
     const uint32_t tl = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const uint32_t oc = tl + C::O + t * D, sc = tl + C::S + t * 64, pc = tl + C::P + t * 32;
-    uint32_t done = 0;  // jobs of this stream so far
+    uint32_t done = 0, piece = 0;  // jobs of this stream so far, pieces
     bool ok = true;
-    while (ok && share.next(a, item, tile0, n)) {
+    for (; ok && share.next(a, item, tile0, n); ++piece) {
       // ---- the row's queries: f16, times a power of two that takes its maximum to [2^14, 2^15) ----
       const int kvh = item / a.groups, r = (item % a.groups) * (128 * R) + (R == 2 ? t * 128 : 0) + row;
       float rm = 0.f;  // 2^(e - 14) scale: what a product of the scaled row counts
@@ -199,6 +202,12 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefix_attn_kernel(const Prefix
         rm = a.scale_log2 * pf_pow2(e - 14);
         // in each 8 channels the order 0 4 1 5 2 6 3 7, in which the codes' words give them
         if (R == 2 || t == 0) {
+          // the other stream's products with the rows before these have been made (this one's have: its O is complete)
+          if (R == 1 && piece > 0) {
+            ok = __all_sync(0xffffffffu, mbar_wait(&cs.q_free, (piece - 1) & 1, abort, a.status));
+            if (!ok) break;
+            tc_fence_after();
+          }
 #pragma unroll
           for (int i = 0; i < D / 8; i += 4) {
             uint32_t w[16];
@@ -210,8 +219,8 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefix_attn_kernel(const Prefix
               w[4 * k + 2] = pf_half2(bf16lo(u.y) * f, bf16lo(u.w) * f);
               w[4 * k + 3] = pf_half2(bf16hi(u.y) * f, bf16hi(u.w) * f);
             }
-            if (C::QSMEM && t == 1) {
-              const uint32_t at = smem_u32(smem) + C::Q + (i / 8) * 16384 + row * 128;
+            if (C::QSMEM) {
+              const uint32_t at = smem_u32(smem) + C::Q + t * (128 * D * 2) + (i / 8) * 16384 + row * 128;
 #pragma unroll
               for (int k = 0; k < 4; ++k)
                 pf_sts128(at + ((((i & 7) + k) ^ (row & 7)) << 4), w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
@@ -353,61 +362,75 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefix_attn_kernel(const Prefix
     }
   } else if (warp < PF_SOFT + PF_WIDE) {
     // ------------------------------------ widening: codes to f16 tiles ------------------------------------
+    // A tile's power of two for K and the one for V follow from the words of all its tokens.  The words of the tile behind are
+    // looked at, and its table is made, around the widening of the one in front, so that one barrier a tile is enough.
     const int w4 = warp - PF_SOFT, tid = w4 * 32 + lane;
+    const int side = tid >> 6, rec = (tid >> 4) & 3, tk = tid & 15;  // this thread's token and side in words and tables
     const uint32_t base = smem_u32(smem);
+    float s[NG], m[NG];  // its words of the tile behind
     bool ok = true;
-    while (ok && share.next(a, item, tile0, n)) {
-      for (int j = 0; j < n; ++j) {
-        const uint32_t tile = tc + j, rs = tile % RS, st = tile % NS;
-        // (a warp whose wait gave up goes on to the next barrier, where all four leave together)
-        ok = __all_sync(0xffffffffu, mbar_wait(&cs.raw_full[rs], (tile / RS) & 1, abort, a.status));
+    auto words = [&](uint32_t tile) {
+      const uint32_t rs = tile % RS;
+      // (a warp whose wait gives up goes on to the next barrier, where all four leave together)
+      ok = __all_sync(0xffffffffu, mbar_wait(&cs.raw_full[rs], (tile / RS) & 1, abort, a.status)) && ok;
+      const bool gone = cs.bad[rs][rec] != 0;
+      const uint8_t *at = smem + C::RING + rs * C::RAW + rec * C::PITCH + (side ? Rec::VW : Rec::KW) + tk * NG * 4;
+      int need = -200;  // f <= -need: code * 2^-24 s 2^(f + 24) is within f16, and so is the value
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+        const uint32_t word = *reinterpret_cast<const uint32_t *>(at + 4 * g);
+        s[g] = gone ? 0.f : bf16lo(word);
+        m[g] = gone ? 0.f : bf16hi(word);
+        if (fabsf(s[g]) < INFINITY && fabsf(m[g]) < INFINITY)
+          need = max(need, max(pf_exponent(s[g]) + 9, max(pf_exponent(m[g]), pf_exponent(fmaf(15.f, s[g], m[g]))) - 14));
+      }
+      need = __reduce_max_sync(0xffffffffu, need);
+      if (lane == 0) cs.need[tile & 1][w4] = need;
+    };
+    int fk = 0, fv = 0;
+    auto table = [&](uint32_t tile) {
+      const int *need = cs.need[tile & 1];
+      fk = min(max(-max(need[0], need[1]), -126), 100);
+      fv = min(max(-max(need[2], need[3]), -126), 100);
+      const int f = side ? fv : fk;
+      const float fs = pf_pow2(f + 24), fm = pf_pow2(f);
+      const int pos = 32 * (rec >> 1) + 8 * ((tk & 7) >> 1) + 4 * (rec & 1) + 2 * (tk >> 3) + (tk & 1);
+      uint8_t *tk_ = smem + C::TABK + (tile & 1) * 1024, *tv = smem + C::TABV + (tile & 1) * 512;
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+        const uint32_t ss = pf_half2(s[g] * fs, s[g] * fs), mm = pf_half2(m[g] * fm, m[g] * fm);
+        if (side) {
+          *reinterpret_cast<uint16_t *>(tv + (g * 64 + pos) * 2) = static_cast<uint16_t>(ss);
+          *reinterpret_cast<uint16_t *>(tv + 256 + (g * 64 + pos) * 2) = static_cast<uint16_t>(mm);
+        } else {
+          *reinterpret_cast<uint2 *>(tk_ + pos * 16 + g * 8) = make_uint2(ss, mm);
+        }
+      }
+    };
+    auto all_ok = [&]() { return ok = !bar_red_or(1, PF_WIDE * 32, !ok); };
+    const uint32_t total = static_cast<uint32_t>(share.end - share.at);  // tiles of all the CTA's pieces
+    if (total > 0) {
+      words(0);
+      if (all_ok()) {
+        table(0);
+        if (total > 1) words(1);
+      }
+    }
+    for (uint32_t tile = 0; tile < total; ++tile) {
+      {
+        const uint32_t rs = tile % RS, st = tile % NS;
+        if (tile >= NS) ok = __all_sync(0xffffffffu, mbar_wait(&cs.kv_free[st], (tile / NS - 1) & 1, abort, a.status)) && ok;
+        const int k_is = fk, v_is = fv;
+        if (!all_ok()) break;  // this tile's table and the next one's powers are there
         const uint8_t *raw = smem + C::RING + rs * C::RAW;
-        // ---- a power of two for the tile's K and one for its V: this thread's token of one side ----
-        const int side = tid >> 6, tok = tid & 63, rec = tok >> 4, tk = tok & 15;
-        const bool gone = cs.bad[rs][rec] != 0;
-        float s[NG], m[NG];
-        int need = -200;  // f <= -need: code * 2^-24 s 2^(f + 24) is within f16, and so is the value
-#pragma unroll
-        for (int g = 0; g < NG; ++g) {
-          const uint32_t word = *reinterpret_cast<const uint32_t *>(raw + rec * C::PITCH + (side ? Rec::VW : Rec::KW) + (tk * NG + g) * 4);
-          s[g] = gone ? 0.f : bf16lo(word);
-          m[g] = gone ? 0.f : bf16hi(word);
-          if (fabsf(s[g]) < INFINITY && fabsf(m[g]) < INFINITY)
-            need = max(need, max(pf_exponent(s[g]) + 9, max(pf_exponent(m[g]), pf_exponent(fmaf(15.f, s[g], m[g]))) - 14));
-        }
-        need = __reduce_max_sync(0xffffffffu, need);
-        if (lane == 0) cs.need[w4] = need;
-        if (bar_red_or(1, PF_WIDE * 32, !ok)) {
-          ok = false;
-          break;
-        }
-        const int fk = min(max(-max(cs.need[0], cs.need[1]), -126), 100), fv = min(max(-max(cs.need[2], cs.need[3]), -126), 100);
-        {
-          const int f = side ? fv : fk;
-          const float fs = pf_pow2(min(f + 24, 127)), fm = pf_pow2(f);
-          const int pos = 32 * (rec >> 1) + 8 * ((tk & 7) >> 1) + 4 * (rec & 1) + 2 * (tk >> 3) + (tk & 1);
-#pragma unroll
-          for (int g = 0; g < NG; ++g) {
-            const uint32_t ss = pf_half2(s[g] * fs, s[g] * fs), mm = pf_half2(m[g] * fm, m[g] * fm);
-            if (side) {
-              *reinterpret_cast<uint16_t *>(smem + C::TABV + (g * 64 + pos) * 2) = static_cast<uint16_t>(ss);
-              *reinterpret_cast<uint16_t *>(smem + C::TABV + 256 + (g * 64 + pos) * 2) = static_cast<uint16_t>(mm);
-            } else {
-              *reinterpret_cast<uint2 *>(smem + C::TABK + pos * 16 + g * 8) = make_uint2(ss, mm);
-            }
-          }
-        }
-        if (tile >= NS) ok = __all_sync(0xffffffffu, mbar_wait(&cs.kv_free[st], (tile / NS - 1) & 1, abort, a.status));
-        if (bar_red_or(1, PF_WIDE * 32, !ok)) {
-          ok = false;
-          break;
-        }
+        const uint8_t *tabk = smem + C::TABK + (tile & 1) * 1024, *tabv = smem + C::TABV + (tile & 1) * 512;
         if (tid == 0) {
           PfInfo &i = cs.info[st];
-          i.k_unit = pf_pow2(-fk);
-          i.g = -fv;
+          i.k_unit = pf_pow2(-k_is);
+          i.g = -v_is;
           i.missing = cs.bad[rs][0] | (cs.bad[rs][1] << 1) | (cs.bad[rs][2] << 2) | (cs.bad[rs][3] << 3);
         }
+        if (tile + 1 < total) table(tile + 1);
         // ---- K: a lane takes the codes of 8-channel piece c of every 32 channels of a token ----
         {
           const int c = lane & 3, r = (lane >> 2) & 1;
@@ -419,14 +442,14 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefix_attn_kernel(const Prefix
             uint32_t code[2 * NG];
             uint2 sm[NG];
             if constexpr (D == 128) {
-              const uint4 u = *reinterpret_cast<const uint4 *>(src), x = *reinterpret_cast<const uint4 *>(smem + C::TABK + pos * 16);
+              const uint4 u = *reinterpret_cast<const uint4 *>(src), x = *reinterpret_cast<const uint4 *>(tabk + pos * 16);
               code[0] = u.x; code[1] = u.y; code[2] = u.z; code[3] = u.w;
               sm[0] = make_uint2(x.x, x.y);
               sm[1] = make_uint2(x.z, x.w);
             } else {
               const uint2 u = *reinterpret_cast<const uint2 *>(src);
               code[0] = u.x; code[1] = u.y;
-              sm[0] = *reinterpret_cast<const uint2 *>(smem + C::TABK + pos * 16);
+              sm[0] = *reinterpret_cast<const uint2 *>(tabk + pos * 16);
             }
             const uint32_t to = base + C::K + st * C::TILE + pos * 128;
 #pragma unroll
@@ -442,8 +465,8 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefix_attn_kernel(const Prefix
           const int g = lane >> 2, c = lane & 3;
           constexpr int NU = 2 * NG;  // words of a warp: d = 128: a half of the channels and a pair of records; d = 64: a quarter
           const int part = D == 128 ? w4 >> 1 : 0, u0 = D == 128 ? 0 : 2 * (w4 >> 1), pr = (w4 & 1) ^ (g & 1);
-          const uint4 s4 = *reinterpret_cast<const uint4 *>(smem + C::TABV + (part * 64 + 32 * pr + 8 * c) * 2);
-          const uint4 m4 = *reinterpret_cast<const uint4 *>(smem + C::TABV + 256 + (part * 64 + 32 * pr + 8 * c) * 2);
+          const uint4 s4 = *reinterpret_cast<const uint4 *>(tabv + (part * 64 + 32 * pr + 8 * c) * 2);
+          const uint4 m4 = *reinterpret_cast<const uint4 *>(tabv + 256 + (part * 64 + 32 * pr + 8 * c) * 2);
           const uint32_t ss[4] = {s4.x, s4.y, s4.z, s4.w}, mm[4] = {m4.x, m4.y, m4.z, m4.w};
           uint32_t sh[4], code[2][NU];
 #pragma unroll
@@ -476,62 +499,60 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefix_attn_kernel(const Prefix
           mbar_arrive(&cs.kv_full[st]);
           mbar_arrive(&cs.raw_free[rs]);
         }
+        if (tile + 2 < total) words(tile + 2);
       }
-      tc += n;
     }
-  } else if (warp == PF_SOFT + PF_WIDE) {
-    // ------------------------------------ products ------------------------------------
+  } else if (warp < PF_LOAD) {
+    // ------------------------------------ products of one stream ------------------------------------
+    // (a thread for each stream: waits, fences and issue of a job take it about as long as the tensor unit takes the products)
+    const int t = warp - PF_PROD;
     if (lane == 0) {
       const uint64_t dk = smem_desc_sw128(smem_u32(smem + C::K), 16, 1024), dv = smem_desc_sw128(smem_u32(smem + C::V), 16, 1024);
-      const uint64_t dq = smem_desc_sw128(smem_u32(smem + C::Q), 16, 1024);
-      uint32_t scored[2] = {0, 0}, added[2] = {0, 0};  // jobs of each stream so far
-      uint32_t piece = 0;
+      const uint64_t dq = smem_desc_sw128(smem_u32(smem + C::Q) + (C::QSMEM ? t * 128 * D * 2 : 0), 16, 1024);
+      const uint32_t sc = tmem + C::S + t * 64, oc = tmem + C::O + t * D, pc = tmem + C::P + t * 32;
+      const uint32_t qc = tmem + C::QC + (R == 2 ? t * C::QCOLS : 0);
+      uint32_t done = 0, piece = 0;  // jobs so far, pieces
       bool ok = true;
-      while (ok && share.next(a, item, tile0, n)) {
-        ok = mbar_wait(&cs.q_full[0], piece & 1, abort, a.status) && (R == 1 || mbar_wait(&cs.q_full[1], piece & 1, abort, a.status));
-        ++piece;
-        const int jobs = R * n;
-        uint32_t fresh = 3;  // streams whose O starts
-        for (int i = 0; ok && i < jobs + 2; ++i) {
-          if (i < jobs) {  // scores of job i
-            const int t = i & 1;
-            const uint32_t tile = tc + (R == 2 ? i >> 1 : i), st = tile % NS;
+      for (; ok && share.next(a, item, tile0, n); ++piece) {
+        const int jobs = R == 2 ? n : (n - t + 1) / 2;
+        ok = mbar_wait(&cs.q_full[R == 2 ? t : 0], piece & 1, abort, a.status);
+        for (int j = 0; ok && j <= jobs; ++j) {
+          if (j < jobs) {  // scores of job j, once the softmax has read those before
+            const uint32_t tile = tc + (R == 2 ? j : 2 * j + t), st = tile % NS;
             ok = mbar_wait(&cs.kv_full[st], (tile / NS) & 1, abort, a.status) &&
-                 (scored[t] == 0 || mbar_wait(&cs.s_free[t], (scored[t] - 1) & 1, abort, a.status));
+                 (done == 0 || mbar_wait(&cs.s_free[t], (done - 1) & 1, abort, a.status));
             if (!ok) break;
             tc_fence_after();
+            const uint64_t b = dk + st * (C::TILE >> 4);
 #pragma unroll
             for (int s = 0; s < D / 16; ++s) {
-              const uint64_t b = dk + st * (C::TILE >> 4) + (s >> 2) * (8192 >> 4) + (s & 3) * 2;
-              if (C::QSMEM && t == 1)
-                mma_bf16_ss(tmem + C::S + t * 64, dq + (s >> 2) * (16384 >> 4) + (s & 3) * 2, b, IDESC_S, s > 0 ? 1u : 0u);
+              if (C::QSMEM)
+                mma_bf16_ss(sc, dq + (s >> 2) * (16384 >> 4) + (s & 3) * 2, b + (s >> 2) * (8192 >> 4) + (s & 3) * 2, IDESC_S, s > 0 ? 1u : 0u);
               else
-                mma_bf16_ts(tmem + C::S + t * 64, tmem + C::QC + (R == 2 ? t * C::QCOLS : 0) + s * 8, b, IDESC_S, s > 0 ? 1u : 0u);
+                mma_bf16_ts(sc, qc + s * 8, b + (s >> 2) * (8192 >> 4) + (s & 3) * 2, IDESC_S, s > 0 ? 1u : 0u);
             }
             mma_commit(&cs.s_full[t]);
-            ++scored[t];
+            if (R == 1 && t == 1 && j == jobs - 1) mma_commit(&cs.q_free);
+            ++done;
           }
-          if (i >= 2) {  // P V of job i - 2
-            const int t = i & 1;
-            const uint32_t tile = tc + (R == 2 ? (i - 2) >> 1 : i - 2), st = tile % NS;
-            ok = mbar_wait(&cs.p_full[t], added[t] & 1, abort, a.status);
+          if (j > 0) {  // P V of job j - 1
+            const uint32_t tile = tc + (R == 2 ? j - 1 : 2 * (j - 1) + t), st = tile % NS, nth = done - (j < jobs ? 2 : 1);
+            ok = mbar_wait(&cs.p_full[t], nth & 1, abort, a.status);
             if (!ok) break;
             tc_fence_after();
+            const uint64_t b = dv + st * (C::TILE >> 4);
 #pragma unroll
-            for (int s = 0; s < 4; ++s)
-              mma_bf16_ts(tmem + C::O + t * D, tmem + C::P + t * 32 + s * 8, dv + st * (C::TILE >> 4) + s * 2, IDESC_PV,
-                          s > 0 || !((fresh >> t) & 1u) ? 1u : 0u);
-            fresh &= ~(1u << t);
+            for (int s = 0; s < 4; ++s) mma_bf16_ts(oc, pc + s * 8, b + s * 2, IDESC_PV, s > 0 || j > 1 ? 1u : 0u);
             mma_commit(&cs.pv_done[t]);
-            ++added[t];
-            if (R == 1 || t == 1) mma_commit(&cs.kv_free[st]);
+            mma_commit(&cs.kv_free[st]);
           }
         }
+        if (R == 1 && t == 1 && jobs == 0) mma_commit(&cs.q_free);
         tc += n;
       }
       if (!ok) {  // products in flight end before the CTA gives its TMEM back
-        mma_commit(&cs.drained);
-        mbar_wait(&cs.drained, 0, &cs.no_abort, a.status);
+        mma_commit(&cs.drained[t]);
+        mbar_wait(&cs.drained[t], 0, &cs.no_abort, a.status);
       }
     }
     __syncwarp();
@@ -582,7 +603,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefix_attn_kernel(const Prefix
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == PF_SOFT + PF_WIDE) tmem_dealloc(tmem, 512);
+  if (warp == PF_PROD) tmem_dealloc(tmem, 512);
 }
 
 // --------------------------------------------------------------------------------------------
