@@ -128,7 +128,8 @@ EXPORTS = {
     "sparge_cache4_select": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t,
                                             ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64, ctypes.c_void_p,
                                             ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, ctypes.c_void_p,
-                                            ctypes.c_void_p, ctypes.c_void_p]),
+                                            ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "sparge_cache4_select_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int64] * 4),
     "sparge_cache4_pages_attn_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int64] * 5),
     "sparge_cache4_pages_attn": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64,
                                                 ctypes.c_void_p, ctypes.c_float, ctypes.c_void_p, ctypes.c_void_p,
@@ -578,11 +579,13 @@ def cache4_bounds_load(pool, bounds, pages):
     return (_binding_module or _load_binding()).cache4_bounds_load(pool, bounds, pages)
 
 
-def cache4_select(q, pool, bounds, table, kv_lens, keep: int, first: int = 1, last: int = 1, pages=None, lens=None):
+def cache4_select(q, pool, bounds, table, kv_lens, keep: int, first: int = 1, last: int = 1, pages=None, lens=None,
+                  ws=None):
     """For each query of q (B,Hq,Nq,d) and KV head the pages that its keys' bounds say matter most: the `first` first and the `last`
     last pages that the query sees, then the largest bounds on a product with a query of the head's group, up to keep pages.
     Returns (pages (B,Nq,Hkv,keep) int32, in order, -1 behind them; lens (B,Nq) int32, the tokens on them)."""
-    return (_binding_module or _load_binding()).cache4_select(q, pool, bounds, table, kv_lens, keep, first, last, pages, lens)
+    return (_binding_module or _load_binding()).cache4_select(q, pool, bounds, table, kv_lens, keep, first, last, pages, lens,
+                                                            ws)
 
 
 def cache4_pages_attn(q, pool, pages, lens, scale: float = 0.0, out=None, ws=None):

@@ -456,7 +456,7 @@ PyObject *cache4_bounds_load(const Args &a) {
   return tuple_of(r, wrap(lo));
 }
 
-// (q, pool, bounds, table, kv_lens, keep, first, last, pages, lens)
+// (q, pool, bounds, table, kv_lens, keep, first, last, pages, lens, ws)
 PyObject *cache4_select(const Args &a) {
   const at::Tensor &q = a.tensor(0, "q"), &bounds = a.tensor(2, "bounds"), &table = a.tensor(3, "table");
   const Here h(q, "q");
@@ -470,7 +470,7 @@ PyObject *cache4_select(const Args &a) {
     PyErr_SetString(PyExc_ValueError, "keep must be in 0..2^27");
     throw PyFail{};
   }
-  at::Tensor pages, lens;
+  at::Tensor pages, lens, ws = given_workspace(a, 10, h);
   if (!a.none(8)) {
     pages = a.tensor(8, "pages");
     h.array(pages, at::kInt, "pages", {dq.B, dq.N, c.H, keep});
@@ -488,9 +488,10 @@ PyObject *cache4_select(const Args &a) {
     }
     if (!pages.defined()) pages = h.make({dq.B, dq.N, c.H, keep}, at::kInt);
     if (!lens.defined()) lens = h.make({dq.B, dq.N}, at::kInt);
+    if (!ws.defined()) ws = make_workspace(h, sparge_cache4_select_workspace_bytes(dq.B, c.H, dq.N, table.size(1)));
     return sparge_cache4_select(&dq, &c, from, bounds.nbytes(), static_cast<const int32_t *>(table.data_ptr()), table.size(1), stride,
                                 len, keep, first, last, static_cast<int32_t *>(pages.data_ptr()),
-                                static_cast<int32_t *>(lens.data_ptr()), h.s());
+                                static_cast<int32_t *>(lens.data_ptr()), ws.data_ptr(), ws.nbytes(), h.s());
   }));
   PyObject *r = result(a, 8, pages);
   return tuple_of(r, result(a, 9, lens));
@@ -578,7 +579,7 @@ PyMethodDef methods[] = {ENTRY(window_attn, 8),
                          ENTRY(qk_norm_rope_axes, 11),
                          ENTRY(cache4_bounds_update, 5),
                          ENTRY(cache4_bounds_load, 3),
-                         ENTRY(cache4_select, 10),
+                         ENTRY(cache4_select, 11),
                          ENTRY(cache4_pages_attn, 7),
                          ENTRY(cache4_prefix_attn, 8),
                          {"set_error", set_error, METH_O, nullptr},

@@ -197,9 +197,15 @@ __global__ void __launch_bounds__(256) bounds_load_kernel(const BoundsArgs a) {
 }
 
 // --------------------------------------------------------------------------------------------
-// Selection: a cluster of 1 to 8 CTAs per list (sequence, query, KV head).  Each scores its part of the pages and writes their
-// keys (scores as unsigned numbers of the same order) into the first CTA's shared memory; that one finds the
-// smallest key to keep digit by digit and writes the list in the pages' order.
+// Selection, in two kernels.  The first scores pages: all sequences' and heads' pages stand in one line of stretches that is
+// cut into equal shares, one per CTA, so ragged lengths fill the part evenly; a warp takes 16 (d = 64: 32) pages at a time against the
+// rows of up to SEL_ROWS query heads, on mma.sync with the codes as f16 (whole numbers up to 127; sums below 2^21 are exact in fp32 in any
+// order).  It is bound by the latency of its chain - page number, bounds, product - so both are loaded a step ahead, 4 KB a warp, and
+// 16 warps share an SM.
+// The second has a CTA for each list: it takes the list's scores into shared memory, finds the smallest to keep, and writes the
+// pages in order.  That score comes from one histogram of 256 equal steps between the smallest
+// and the largest score, then the scores of the step that holds it are ranked among themselves; more than 256 of them, or infinities
+// at the ends, go digit by digit from the highest bit that differs.
 // --------------------------------------------------------------------------------------------
 struct SelectArgs {
   const __nv_bfloat16 *q;
@@ -207,253 +213,506 @@ struct SelectArgs {
   const uint8_t *bounds;
   const int32_t *table, *lens;
   int64_t table_stride, n_pages, row;
-  int width, page_shift, Hkv, G, Nq, keep, first, last;
+  int B, width, page_shift, Hkv, G, Nq, keep, first, last;
+  int rows_log;  // rows of a query in the product: 1, 2 or 4 (three heads: the first again), or tiles of 8
+  int tiles;     // of a query; 0: a tile holds 8 >> rows_log queries
+  int at_once;   // queries of a round (blockIdx.y)
+  float *keys;     // scores [B][Nq][Hkv][pitch]; -inf: a page that is not there
+  int pitch;       // the table's width in whole fours
   int32_t *pages, *out_lens;
   int *status;
+
+  __device__ __forceinline__ int tokens(int len, int i) const {  // that query i sees
+    const int64_t n = static_cast<int64_t>(len) - Nq + 1 + i;
+    return static_cast<int>(n > 0 ? n : 0);
+  }
+  __device__ __forceinline__ int pages_of(int len, int i) const {
+    return static_cast<int>((static_cast<int64_t>(tokens(len, i)) + (1 << page_shift) - 1) >> page_shift);
+  }
+  // pages to choose from (0: all of them are kept, or none is left to choose)
+  __device__ __forceinline__ int choices(int len, int i) const {
+    const int n = pages_of(len, i);
+    return n > keep && keep > first + last ? n - first - last : 0;
+  }
 };
 
-constexpr int SEL_THREADS = 256, SEL_WARPS = SEL_THREADS / 32, SEL_HEADS = 64;
-constexpr int SEL_PAGES = 40960;  // keys that shared memory holds beside the queries
+constexpr int SEL_THREADS = 128, SEL_WARPS = SEL_THREADS / 32, SEL_CTAS = 4;
+__host__ __device__ constexpr int sel_tiles(int) { return 1; }                             // tiles of 16 pages of a warp and step
+__host__ __device__ constexpr int sel_stretch(int D) { return SEL_WARPS * 16 * sel_tiles(D); }  // pages of a CTA and step
+constexpr int SEL_HEADS = 64, SEL_ROWS = 64;  // query heads of a KV head at most; rows of a round
+constexpr int SEL_PAGES = 32768;              // scores that shared memory holds
+constexpr int LIST_THREADS = 256, LIST_WARPS = LIST_THREADS / 32;
 
-// Scores as numbers of the same order (a score is never a NaN; both zeros are one).
-__device__ __forceinline__ uint32_t key_of(float x) {
-  const uint32_t b = __float_as_uint(x + 0.f);
-  return (b & 0x80000000u) ? ~b : b | 0x80000000u;
+// Codes as f16, two channels a register.
+__device__ __forceinline__ uint32_t half2_of(int lo, int hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(static_cast<float>(hi)), "f"(static_cast<float>(lo)));
+  return r;
+}
+// Four int8 codes: b + 128 in the low bits of 1024 + .., less 1152.
+__device__ __forceinline__ void widen4(uint32_t w, uint32_t &a, uint32_t &b) {
+  const uint32_t u = w ^ 0x80808080u;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(a) : "r"(__byte_perm(u, 0x64646464u, 0x4140)), "r"(0x64806480u));
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(b) : "r"(__byte_perm(u, 0x64646464u, 0x4342)), "r"(0x64806480u));
+}
+__device__ __forceinline__ void mma_codes(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint2 b) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b.x), "r"(b.y));
 }
 
-__device__ __forceinline__ void cluster_arrive_wait() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// a 32-bit store into shared memory of the cluster's first CTA
-__device__ __forceinline__ void store_first(uint32_t *p, uint32_t v) {
-  uint32_t to;
-  asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(to) : "r"(smem_u32(p)));
-  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(to), "r"(v) : "memory");
+// Codes of query row r by a warp, as B operands: step k of the product holds, for lane 4 n + c of row n of the tile, channels
+// 64 j + 16 c + 4 w .. + 3 with k = 4 j + w - the bytes that a lane reads of a page - first of r+ (beside hi), then of r- (beside lo).
+// Returns t (0 for a row with an infinity or a NaN: it scores every page 0).
+template <int D>
+__device__ __forceinline__ float code_row(const uint32_t (&u)[D / 64], uint8_t *codes, int r, int lane) {
+  constexpr int C = D / 32, S = D / 8;
+  float x[C], big = 0.f;
+  bool fine = true;
+#pragma unroll
+  for (int k = 0; k < C; ++k) {
+    x[k] = (k & 1) ? bf16hi(u[k / 2]) : bf16lo(u[k / 2]);
+    fine = fine && fabsf(x[k]) < INFINITY;
+    big = fmaxf(big, fabsf(x[k]));
+  }
+  fine = __all_sync(0xffffffffu, fine);
+  big = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(big)));
+  const float t = fine ? code_unit(big) : 0.f, inv = fine ? over_unit(t) : 0.f;
+  int v[C];
+#pragma unroll
+  for (int k = 0; k < C; ++k) v[k] = fine ? __float2int_rn(x[k] * inv) : 0;
+  uint8_t *tile = codes + (r / 8) * (S * 256);
+  if constexpr (C == 4) {
+    const int k = 4 * (lane >> 4) + (lane & 3), at = 4 * (r % 8) + ((lane >> 2) & 3);
+    *reinterpret_cast<uint2 *>(tile + (k * 32 + at) * 8) = make_uint2(half2_of(max(v[0], 0), max(v[1], 0)), half2_of(max(v[2], 0), max(v[3], 0)));
+    *reinterpret_cast<uint2 *>(tile + ((k + S / 2) * 32 + at) * 8) =
+        make_uint2(half2_of(min(v[0], 0), min(v[1], 0)), half2_of(min(v[2], 0), min(v[3], 0)));
+  } else {
+    const int k = (lane >> 1) & 3, at = 4 * (r % 8) + (lane >> 3);
+    *reinterpret_cast<uint32_t *>(tile + (k * 32 + at) * 8 + 4 * (lane & 1)) = half2_of(max(v[0], 0), max(v[1], 0));
+    *reinterpret_cast<uint32_t *>(tile + ((k + S / 2) * 32 + at) * 8 + 4 * (lane & 1)) = half2_of(min(v[0], 0), min(v[1], 0));
+  }
+  return t;
 }
 
 template <int D>
-__global__ void __launch_bounds__(SEL_THREADS) select_kernel(const SelectArgs a) {
-  constexpr int LPP = D / 16;  // lanes that share a page, 16 channels each; pages of such a group of lanes at a time
-  extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ float unit[SEL_HEADS];
-  __shared__ uint32_t hist[256], found[2], ends[2], count[SEL_WARPS][2];
+__global__ void __launch_bounds__(SEL_THREADS, SEL_CTAS) select_score_kernel(const SelectArgs a) {
+  constexpr int S = D / 8, NP = D / 32;  // steps of a product, 16 codes each, hi's then lo's; 16-byte pieces of a page and lane
+  constexpr int MT = sel_tiles(D), STRETCH = sel_stretch(D);
+  __shared__ __align__(16) uint8_t codes[SEL_ROWS * 4 * D];
+  __shared__ float2 unit[SEL_ROWS / 2];  // t of the rows
+  __shared__ int limit[SEL_ROWS];        // pages to choose from of each query of the round
   start_after_earlier();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  uint32_t clusters, rank;
-  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(clusters));
-  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
-  const int64_t list = blockIdx.x / clusters;
-  const int h = static_cast<int>(list % a.Hkv), i = static_cast<int>(list / a.Hkv % a.Nq), b = static_cast<int>(list / a.Hkv / a.Nq);
-  const int64_t behind = static_cast<int64_t>(length_of(a.lens, b, a.width, a.page_shift)) - a.Nq + 1 + i;
-  const int seen = static_cast<int>(behind > 0 ? behind : 0), P = 1 << a.page_shift;
-  const int np = static_cast<int>((static_cast<int64_t>(seen) + P - 1) >> a.page_shift), n = min(np, a.keep);
-  const int32_t *table = a.table + static_cast<int64_t>(b) * a.table_stride;
-  int32_t *out = a.pages + list * a.keep;
-  if (rank == 0) {
-    if (h == 0 && threadIdx.x == 0)
-      a.out_lens[static_cast<int64_t>(b) * a.Nq + i] = n > 0 ? static_cast<int>(static_cast<int64_t>(n - 1) * P) + (seen - 1) % P + 1 : 0;
-    // every page, or those that are kept whatever their scores; then the places without one
-    for (int k = threadIdx.x; k < a.keep; k += SEL_THREADS) {
-      const bool middle = np > a.keep && k >= a.first && k < a.keep - a.last;
-      if (!middle) out[k] = k >= n ? -1 : table[np > a.keep && k >= a.first ? np - (a.keep - k) : k];
-    }
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+  const int i0 = blockIdx.y * a.at_once, ni = min(a.at_once, a.Nq - i0);
+  // ---- this CTA's share of the line: every warp for itself; the last query of the round sees the most pages ----
+  auto stretches = [&](int b) {
+    return static_cast<int64_t>((a.choices(length_of(a.lens, b, a.width, a.page_shift), i0 + ni - 1) + STRETCH - 1) / STRETCH) * a.Hkv;
+  };
+  const int per = (a.B + 31) / 32, bt = min(a.B, lane * per), bu = min(a.B, bt + per);
+  int64_t own = 0;
+#pragma unroll 4
+  for (int b = bt; b < bu; ++b) own += stretches(b);
+  int64_t inc = own;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int64_t o = __shfl_up_sync(0xffffffffu, inc, off);
+    if (lane >= off) inc += o;
   }
-  const int m = np - a.first - a.last, want = a.keep - a.first - a.last;  // pages to choose from, to choose
-  if (np <= a.keep || want == 0) return;  // the same for the whole cluster
-  // ---- the queries' codes: bytes r+ and r- of each head ----
-  uint32_t *keys = reinterpret_cast<uint32_t *>(smem);
-  uint8_t *codes = smem + (static_cast<int64_t>(a.width) * 4 + 15) / 16 * 16;  // [G][r+, r-][D]
-  for (int g = warp; g < a.G; g += SEL_WARPS) {
-    const __nv_bfloat16 *q = a.q + b * a.q_sb + (static_cast<int64_t>(h) * a.G + g) * a.q_sh + static_cast<int64_t>(i) * a.q_sn;
-    constexpr int C = D / 32;
-    float x[C], big = 0.f;
-    bool fine = true;
-    if constexpr (C == 4) {
-      const uint2 u = *reinterpret_cast<const uint2 *>(q + 4 * lane);
-      x[0] = bf16lo(u.x); x[1] = bf16hi(u.x); x[2] = bf16lo(u.y); x[3] = bf16hi(u.y);
-    } else {
-      const uint32_t u = *reinterpret_cast<const uint32_t *>(q + 2 * lane);
-      x[0] = bf16lo(u); x[1] = bf16hi(u);
+  const int64_t total = __shfl_sync(0xffffffffu, inc, 31);
+  const int64_t begin = total * blockIdx.x / gridDim.x, end = total * (blockIdx.x + 1) / gridDim.x;
+  if (begin >= end) return;
+  int b = bt;
+  int64_t off = begin - (inc - own), left = end - begin;
+  const uint32_t here = __ballot_sync(0xffffffffu, off >= 0 && off < own);  // the lane whose sequences hold the start
+  if (off >= 0 && off < own)
+    for (int64_t n; off >= (n = stretches(b)); ++b) off -= n;
+  b = __shfl_sync(0xffffffffu, b, __ffs(here) - 1);
+  off = __shfl_sync(0xffffffffu, off, __ffs(here) - 1);
+  while (left > 0) {
+    const int len = length_of(a.lens, b, a.width, a.page_shift), most = a.choices(len, i0 + ni - 1), nst = (most + STRETCH - 1) / STRETCH;
+    if (off >= static_cast<int64_t>(nst) * a.Hkv) {
+      off -= static_cast<int64_t>(nst) * a.Hkv;
+      ++b;
+      continue;
     }
+    const int h = static_cast<int>(off) / nst, s0 = static_cast<int>(off) - h * nst;
+    const int s1 = static_cast<int>(left < nst - s0 ? s0 + left : nst);  // stretches s0 .. s1 - 1 of the head
+    off += s1 - s0;
+    left -= s1 - s0;
+    const int32_t *table = a.table + static_cast<int64_t>(b) * a.table_stride + a.first;
+    const uint8_t *base = a.bounds + h * 2 * D + 16 * c, *scales = a.bounds + a.Hkv * 2 * D + 4 * h;
+    // ---- the pages' numbers of the first step, and the queries' codes meanwhile ----
+    const int p_end = min(most, s1 * STRETCH);
+    int p0 = s0 * STRETCH + warp * (16 * MT);
+    int id[MT][2];  // of the step after this one: pages g and g + 8 of each tile
+    auto look_up = [&](int p) {
 #pragma unroll
-    for (int k = 0; k < C; ++k) {
-      fine = fine && fabsf(x[k]) < INFINITY;
-      big = fmaxf(big, fabsf(x[k]));
-    }
-    fine = __all_sync(0xffffffffu, fine);
+      for (int u = 0; u < MT; ++u)
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, off));
-    const float t = fine ? code_unit(big) : 0.f, inv = fine ? over_unit(t) : 0.f;  // a query of NaN scores every page 0
-    uint32_t plus = 0u, minus = 0u;
+        for (int y = 0; y < 2; ++y) id[u][y] = p + 16 * u + g + 8 * y < p_end ? table[p + 16 * u + g + 8 * y] : -1;
+    };
+    look_up(p0);
+    const int rows = a.tiles ? ni * a.tiles * 8 : ni << a.rows_log, nt = (rows + 7) / 8;
+    __syncthreads();  // the codes of the head before have been read
+    for (int r0 = warp * 4; r0 < rows; r0 += SEL_WARPS * 4) {  // (the last tile's rows past them hold anything: no sum of another row's)
+      uint32_t u[4][D / 64];
 #pragma unroll
-    for (int k = 0; k < C; ++k) {
-      const int r = fine ? __float2int_rn(x[k] * inv) : 0;
-      plus |= (static_cast<uint32_t>(max(r, 0)) & 0xFFu) << (8 * k);
-      minus |= (static_cast<uint32_t>(min(r, 0)) & 0xFFu) << (8 * k);
-    }
-    uint8_t *to = codes + g * 2 * D;
-    if constexpr (C == 4) {
-      *reinterpret_cast<uint32_t *>(to + 4 * lane) = plus;
-      *reinterpret_cast<uint32_t *>(to + D + 4 * lane) = minus;
-    } else {
-      *reinterpret_cast<uint16_t *>(to + 2 * lane) = static_cast<uint16_t>(plus);
-      *reinterpret_cast<uint16_t *>(to + D + 2 * lane) = static_cast<uint16_t>(minus);
-    }
-    if (lane == 0) unit[g] = t;
-  }
-  if (clusters > 1)
-    cluster_arrive_wait();  // and the first CTA is there
-  else
-    __syncthreads();
-  // ---- scores: 32 pages a warp and step; a group of LPP lanes takes LPP of them, and after the sums are exchanged each lane holds one ----
-  const int e = lane % LPP;
-  const uint8_t *base = a.bounds + h * 2 * D;
-  for (int p0 = (static_cast<int>(rank) * SEL_WARPS + warp) * 32; p0 < m; p0 += static_cast<int>(clusters) * SEL_THREADS) {
-    const int p = p0 + lane;
-    int page = p < m ? table[a.first + p] : -1;
-    if (p < m && (page < 0 || page >= a.n_pages)) {
-      record_status(a.status, -1 /* SPARGE_ERR_INVALID_ARG */);
-      page = -1;
-    }
-    uint4 hi[LPP], lo[LPP];
-#pragma unroll
-    for (int u = 0; u < LPP; ++u) {
-      const int id = __shfl_sync(0xffffffffu, page, (lane & ~(LPP - 1)) + u);
-      hi[u] = lo[u] = make_uint4(0u, 0u, 0u, 0u);
-      if (id >= 0) {
-        const uint8_t *src = base + static_cast<int64_t>(id) * a.row + 16 * e;
-        hi[u] = *reinterpret_cast<const uint4 *>(src);
-        lo[u] = *reinterpret_cast<const uint4 *>(src + D);
-      }
-    }
-    const float s = page >= 0 ? *reinterpret_cast<const float *>(a.bounds + static_cast<int64_t>(page) * a.row + a.Hkv * 2 * D + 4 * h) : 0.f;
-    float best = -INFINITY;
-    for (int g = 0; g < a.G; ++g) {
-      const uint4 rp = *reinterpret_cast<const uint4 *>(codes + g * 2 * D + 16 * e), rn = *reinterpret_cast<const uint4 *>(codes + g * 2 * D + D + 16 * e);
-      int x[LPP];
-#pragma unroll
-      for (int u = 0; u < LPP; ++u) {
-        int v = __dp4a(static_cast<int>(hi[u].x), static_cast<int>(rp.x), 0);
-        v = __dp4a(static_cast<int>(hi[u].y), static_cast<int>(rp.y), v);
-        v = __dp4a(static_cast<int>(hi[u].z), static_cast<int>(rp.z), v);
-        v = __dp4a(static_cast<int>(hi[u].w), static_cast<int>(rp.w), v);
-        v = __dp4a(static_cast<int>(lo[u].x), static_cast<int>(rn.x), v);
-        v = __dp4a(static_cast<int>(lo[u].y), static_cast<int>(rn.y), v);
-        v = __dp4a(static_cast<int>(lo[u].z), static_cast<int>(rn.z), v);
-        x[u] = __dp4a(static_cast<int>(lo[u].w), static_cast<int>(rn.w), v);
-      }
-      // lane e of the group ends with the sum of its page e
-#pragma unroll
-      for (int half = LPP / 2; half > 0; half /= 2) {
-        const bool up = (e & half) != 0;
-#pragma unroll
-        for (int u = 0; u < LPP / 2; ++u) {
-          if (u >= half) break;
-          const int give = up ? x[u] : x[u + half], mine = up ? x[u + half] : x[u];
-          x[u] = mine + __shfl_xor_sync(0xffffffffu, give, half);
+      for (int k = 0; k < 4; ++k) {
+        const int r = r0 + k, i = a.tiles ? r / (8 * a.tiles) : r >> a.rows_log, hd = a.tiles ? r % (8 * a.tiles) : r & ((1 << a.rows_log) - 1);
+        const __nv_bfloat16 *q = a.q + b * a.q_sb + (static_cast<int64_t>(h) * a.G + (hd < a.G ? hd : 0)) * a.q_sh +
+                                 static_cast<int64_t>(i0 + min(i, ni - 1)) * a.q_sn;
+        if constexpr (D == 128) {
+          const uint2 x = *reinterpret_cast<const uint2 *>(q + 4 * lane);
+          u[k][0] = x.x;
+          u[k][1] = x.y;
+        } else {
+          u[k][0] = *reinterpret_cast<const uint32_t *>(q + 2 * lane);
         }
       }
-      best = fmaxf(best, static_cast<float>(x[0]) * unit[g]);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float t = code_row<D>(u[k], codes, r0 + k, lane);
+        if (lane == 0) reinterpret_cast<float *>(unit)[r0 + k] = t;
+      }
     }
-    if (p < m) {
-      const uint32_t key = key_of(page < 0 ? -INFINITY : s < INFINITY ? best * s : INFINITY);
-      if (clusters > 1)
-        store_first(keys + p, key);
-      else
-        keys[p] = key;
-    }
-  }
-  if (clusters > 1) {
-    cluster_arrive_wait();
-    if (rank != 0) return;
-  } else {
+    for (int i = threadIdx.x; i < ni; i += SEL_THREADS) limit[i] = a.choices(len, i0 + i);
+    float *keys = a.keys + ((static_cast<int64_t>(b) * a.Nq + i0) * a.Hkv + h) * a.pitch + g;
+    const int64_t query = static_cast<int64_t>(a.Hkv) * a.pitch;
     __syncthreads();
+    // ---- 16 MT pages a step: lane 4 g + c reads of pages g and g + 8 of a tile the 16 codes from 64 j + 16 c on, and holds the sums of
+    // rows 2c and 2c + 1 with them ----
+    uint4 code[MT][2][NP];
+    float next[MT][2];  // the pages' scales; NaN: there is no such page
+    auto fetch = [&](int p) {
+#pragma unroll
+      for (int u = 0; u < MT; ++u)
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          const bool there = static_cast<uint32_t>(id[u][y]) < static_cast<uint32_t>(a.n_pages);
+          const int64_t at = static_cast<int64_t>(there ? id[u][y] : 0) * a.row;  // (page 0's codes are as good as any)
+          if (!there && p + 16 * u + g + 8 * y < p_end) record_status(a.status, -1 /* SPARGE_ERR_INVALID_ARG */);
+#pragma unroll
+          for (int k = 0; k < NP; ++k) code[u][y][k] = *reinterpret_cast<const uint4 *>(base + at + 64 * k);
+          const float sc = *reinterpret_cast<const float *>(scales + at);
+          next[u][y] = there ? sc : __uint_as_float(0x7FFFFFFFu);
+        }
+    };
+    fetch(p0);
+    look_up(p0 + STRETCH);
+    for (; p0 < p_end; p0 += STRETCH) {
+      uint32_t w[MT][S][4];  // the pages' codes as A operands
+      float s[MT][2];
+#pragma unroll
+      for (int u = 0; u < MT; ++u)
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          s[u][y] = next[u][y];
+#pragma unroll
+          for (int k = 0; k < NP; ++k) {
+            const uint4 v = code[u][y][k];
+            widen4(v.x, w[u][4 * k][y], w[u][4 * k][2 + y]);
+            widen4(v.y, w[u][4 * k + 1][y], w[u][4 * k + 1][2 + y]);
+            widen4(v.z, w[u][4 * k + 2][y], w[u][4 * k + 2][2 + y]);
+            widen4(v.w, w[u][4 * k + 3][y], w[u][4 * k + 3][2 + y]);
+          }
+        }
+      fetch(p0 + STRETCH);
+      look_up(p0 + 2 * STRETCH);
+      float best[MT][2];  // of a query of several tiles of rows
+#pragma unroll
+      for (int u = 0; u < MT; ++u) best[u][0] = best[u][1] = -INFINITY;
+      int i = 0, nth = 0;  // of a query of whole tiles: the query, its tile
+      const uint8_t *tile = codes + lane * 8;
+#pragma unroll 1
+      for (int t = 0; t < nt; ++t, tile += S * 256) {
+        float acc[MT][4];
+#pragma unroll
+        for (int u = 0; u < MT; ++u) acc[u][0] = acc[u][1] = acc[u][2] = acc[u][3] = 0.f;
+#pragma unroll
+        for (int k = 0; k < S; ++k) {
+          const uint2 q = *reinterpret_cast<const uint2 *>(tile + k * 256);
+#pragma unroll
+          for (int u = 0; u < MT; ++u) mma_codes(acc[u], w[u][k][0], w[u][k][1], w[u][k][2], w[u][k][3], q);
+        }
+        const float2 un = unit[t * 4 + c];
+        // which lanes write: each its first row's value, the largest of a query's rows; with one row a query its second's too
+        const bool several = a.rows_log > 0 || a.tiles > 0;
+        const bool put = !several || (a.tiles ? c == 0 && nth == a.tiles - 1 : a.rows_log == 1 || (c & 1) == 0);
+        const int at = a.tiles ? i : (t * 8 + 2 * c) >> a.rows_log;
+        const int lim0 = (put && at < ni ? limit[at] : 0) - p0 - g, lim1 = (!several && at + 1 < ni ? limit[at + 1] : 0) - p0 - g;
+        float *to = keys + at * query + p0;
+#pragma unroll
+        for (int u = 0; u < MT; ++u)
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            float v = acc[u][2 * y] * un.x;
+            const float v1 = acc[u][2 * y + 1] * un.y;
+            if (several) {
+              v = fmaxf(v, v1);
+              if (a.rows_log > 1 || a.tiles) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
+              if (a.tiles) {
+                v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
+                best[u][y] = v = fmaxf(best[u][y], v);
+              }
+            }
+            const float sc = s[u][y];
+            auto score = [&](float x) { return sc < INFINITY ? x * sc : sc == INFINITY ? INFINITY : -INFINITY; };
+            const int p = 16 * u + 8 * y;
+            if (p < lim0) to[p] = score(v);
+            if (p < lim1) to[query + p] = score(v1);
+          }
+        if (a.tiles && ++nth == a.tiles) {
+          nth = 0;
+          ++i;
+#pragma unroll
+          for (int u = 0; u < MT; ++u) best[u][0] = best[u][1] = -INFINITY;
+        }
+      }
+    }
   }
-  // ---- the smallest key to keep: digits of 8 bits from the highest bit in which keys differ ----
-  uint32_t low = 0xFFFFFFFFu, high = 0u;
-  for (int k = threadIdx.x; k < m; k += SEL_THREADS) {
-    low = min(low, keys[k]);
-    high = max(high, keys[k]);
-  }
-  low = __reduce_min_sync(0xffffffffu, low);
-  high = __reduce_max_sync(0xffffffffu, high);
-  if (threadIdx.x == 0) {
-    ends[0] = 0xFFFFFFFFu;
-    ends[1] = 0u;
+}
+
+struct ListShared {
+  uint32_t hist[256];
+  float cand[LIST_THREADS], red[2][LIST_WARPS];
+  uint32_t count[LIST_WARPS][2], found[3], n_cand;
+  float bound;
+};
+
+__device__ __forceinline__ float warp_min(float x) {
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) x = fminf(x, __shfl_xor_sync(0xffffffffu, x, off));
+  return x;
+}
+__device__ __forceinline__ float warp_max(float x) { return -warp_min(-x); }
+
+// minimum and maximum over the CTA
+__device__ __forceinline__ void min_max(ListShared &sh, float &low, float &high) {
+  low = warp_min(low);
+  high = warp_max(high);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) {
+    sh.red[0][threadIdx.x >> 5] = low;
+    sh.red[1][threadIdx.x >> 5] = high;
   }
   __syncthreads();
-  if (lane == 0) {
-    atomicMin(&ends[0], low);
-    atomicMax(&ends[1], high);
+#pragma unroll
+  for (int w = 0; w < LIST_WARPS; ++w) {
+    low = fminf(low, sh.red[0][w]);
+    high = fmaxf(high, sh.red[1][w]);
+  }
+}
+// The histogram's place (found[0]) that holds the want-th largest, its rank there (found[1]) and the place's count (found[2]).
+__device__ __forceinline__ void find_place(ListShared &sh, uint32_t want) {
+  __syncthreads();
+  if (threadIdx.x < 32) {  // lane l: places 8 (31 - l) + 7 .. 8 (31 - l), from the largest down
+    const int lane = threadIdx.x;
+    uint32_t own = 0u, v[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) own += v[k] = sh.hist[8 * (31 - lane) + 7 - k];
+    uint32_t before = own;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const uint32_t o = __shfl_up_sync(0xffffffffu, before, off);
+      if (lane >= off) before += o;
+    }
+    before -= own;
+    if (before < want && before + own >= want) {
+      bool open = true;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        if (open && before + v[k] >= want) {
+          sh.found[0] = static_cast<uint32_t>(8 * (31 - lane) + 7 - k);
+          sh.found[1] = want - before;
+          sh.found[2] = v[k];
+          open = false;
+        }
+        if (open) before += v[k];
+      }
+    }
   }
   __syncthreads();
-  low = ends[0];
-  high = ends[1];
-  int top = 32 - __clz(low ^ high);  // bits below `top` differ
-  uint32_t bound = top < 32 ? (high >> top) << top : 0u;  // keys to keep are at least this, as far as it is known
-  int left = want;  // how many of those that agree with bound above bit `top`
+}
+
+// f(score) for every score, four at a time of a thread.  The array is filled up to whole fours with -inf: below or equal to every score,
+// and behind all of them.
+template <typename F>
+__device__ __forceinline__ void each_score(const float *scores, int m, F f) {
+  const float4 *at = reinterpret_cast<const float4 *>(scores);
+  const int n = (m + 3) / 4;
+#pragma unroll 4
+  for (int k = threadIdx.x; k < n; k += LIST_THREADS) {
+    const float4 v = at[k];
+    f(v.x);
+    f(v.y);
+    f(v.z);
+    f(v.w);
+  }
+}
+
+// The want-th largest of m scores, and how many of its equals are among the want largest.  Called by the whole CTA; low and high:
+// the smallest and the largest score that the thread has seen.
+__device__ __forceinline__ void want_th(ListShared &sh, const float *scores, int m, int want, float low, float high, float &bound, int &left) {
+  sh.hist[threadIdx.x] = 0u;
+  if (threadIdx.x == 0) sh.n_cand = 0u;
+  min_max(sh, low, high);
+  const float range = high - low;
+  left = want;
+  if (range > 1e-30f && range < 1e30f) {
+    const float step = 255.f / range, zero = low;
+    auto place = [&](float x) { return min(static_cast<uint32_t>((x - zero) * step), 255u); };  // (-inf: 0)
+    each_score(scores, m, [&](float x) { atomicAdd(&sh.hist[place(x)], 1u); });
+    find_place(sh, static_cast<uint32_t>(want));
+    const uint32_t at = sh.found[0], n = sh.found[2];
+    left = static_cast<int>(sh.found[1]);
+    if (n <= LIST_THREADS) {
+      each_score(scores, m, [&](float x) {
+        if (place(x) == at) sh.cand[atomicAdd(&sh.n_cand, 1u)] = x;
+      });
+      __syncthreads();
+      if (threadIdx.x < n) {
+        const float mine = sh.cand[threadIdx.x];
+        uint32_t above = 0u, equal = 0u;
+        for (uint32_t k = 0; k < n; ++k) {
+          above += sh.cand[k] > mine;
+          equal += sh.cand[k] == mine;
+        }
+        if (above < static_cast<uint32_t>(left) && above + equal >= static_cast<uint32_t>(left)) {
+          sh.bound = mine;
+          sh.found[1] = static_cast<uint32_t>(left) - above;
+        }
+      }
+      __syncthreads();
+      bound = sh.bound;
+      left = static_cast<int>(sh.found[1]);
+      return;
+    }
+    low = INFINITY;
+    high = -INFINITY;
+    each_score(scores, m, [&](float x) {
+      if (place(x) == at) {
+        low = fminf(low, x);
+        high = fmaxf(high, x);
+      }
+    });
+    min_max(sh, low, high);
+  }
+  // digits of 8 bits among the scores from low to high, as unsigned numbers of the same order (both zeros are one)
+  auto key_of = [](float x) {
+    const uint32_t b = __float_as_uint(x + 0.f);
+    return (b & 0x80000000u) ? ~b : b | 0x80000000u;
+  };
+  const uint32_t first = key_of(low), last = key_of(high);
+  int top = 32 - __clz(first ^ last);  // bits below `top` differ
+  uint32_t key = top < 32 ? (last >> top) << top : 0u;
   while (top > 0) {
     const int shift = max(top - 8, 0);
-    hist[threadIdx.x] = 0u;
     __syncthreads();
-    for (int k = threadIdx.x; k < m; k += SEL_THREADS) {
-      const uint32_t key = keys[k];
-      if (top == 32 || (key >> top) == (bound >> top)) atomicAdd(&hist[(key >> shift) & ((1u << (top - shift)) - 1u)], 1u);
-    }
+    sh.hist[threadIdx.x] = 0u;
     __syncthreads();
-    if (warp == 0) {  // lane l: digits 8 (31 - l) + 7 .. 8 (31 - l), from the largest down
-      uint32_t own = 0u, v[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) own += v[k] = hist[8 * (31 - lane) + 7 - k];
-      uint32_t before = own;
-#pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const uint32_t o = __shfl_up_sync(0xffffffffu, before, off);
-        if (lane >= off) before += o;
-      }
-      before -= own;
-      const uint32_t need = static_cast<uint32_t>(left);
-      if (before < need && before + own >= need) {
-        int k = 0;
-        while (before + v[k] < need) before += v[k++];
-        found[0] = static_cast<uint32_t>(8 * (31 - lane) + 7 - k);
-        found[1] = need - before;
-      }
-    }
-    __syncthreads();
-    bound |= found[0] << shift;
-    left = static_cast<int>(found[1]);
+    each_score(scores, m, [&](float x) {
+      const uint32_t k = key_of(x);
+      if (k >= first && k <= last && (top == 32 || (k >> top) == (key >> top)))
+        atomicAdd(&sh.hist[(k >> shift) & ((1u << (top - shift)) - 1u)], 1u);
+    });
+    find_place(sh, static_cast<uint32_t>(left));
+    key |= sh.found[0] << shift;
+    left = static_cast<int>(sh.found[1]);
     top = shift;
   }
-  // ---- the list: keys above the bound, and the first `left` that equal it; every warp a stretch of the pages ----
-  const int per = (m + SEL_THREADS - 1) / SEL_THREADS * 32, k0 = min(warp * per, m), k1 = min(k0 + per, m);
-  uint32_t above = 0u, equal = 0u;
-  for (int k = k0; k < k1; k += 32) {
-    const uint32_t key = k + lane < k1 ? keys[k + lane] : 0u;
-    above += __popc(__ballot_sync(0xffffffffu, k + lane < k1 && key > bound));
-    equal += __popc(__ballot_sync(0xffffffffu, k + lane < k1 && key == bound));
+  bound = __uint_as_float((key & 0x80000000u) ? key & 0x7FFFFFFFu : ~key);
+}
+
+__global__ void __launch_bounds__(LIST_THREADS) select_list_kernel(const SelectArgs a) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ ListShared sh;
+  start_after_earlier();
+  float4 *scores = reinterpret_cast<float4 *>(smem);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, P = 1 << a.page_shift;
+  const int64_t list = blockIdx.x;
+  const int h = static_cast<int>(list % a.Hkv), i = static_cast<int>(list / a.Hkv % a.Nq), b = static_cast<int>(list / a.Hkv / a.Nq);
+  const int32_t *table = a.table + static_cast<int64_t>(b) * a.table_stride;
+  const int len = length_of(a.lens, b, a.width, a.page_shift), seen = a.tokens(len, i), np = a.pages_of(len, i), n = min(np, a.keep);
+  int32_t *out = a.pages + list * a.keep;
+  if (h == 0 && threadIdx.x == 0)
+    a.out_lens[static_cast<int64_t>(b) * a.Nq + i] = n > 0 ? static_cast<int>(static_cast<int64_t>(n - 1) * P) + (seen - 1) % P + 1 : 0;
+  const int m = a.choices(len, i), m4 = (m + 3) / 4;
+  float low = INFINITY, high = -INFINITY;
+  const float4 *from = reinterpret_cast<const float4 *>(a.keys + list * a.pitch);
+#pragma unroll 4
+  for (int k = threadIdx.x; k < m4; k += LIST_THREADS) {
+    float4 v = from[k];
+    if (4 * k + 3 >= m) {
+      if (4 * k + 1 >= m) v.y = -INFINITY;
+      if (4 * k + 2 >= m) v.z = -INFINITY;
+      if (4 * k + 3 >= m) v.w = -INFINITY;
+    }
+    low = fminf(fminf(low, v.x), fminf(4 * k + 1 < m ? v.y : v.x, fminf(4 * k + 2 < m ? v.z : v.x, 4 * k + 3 < m ? v.w : v.x)));
+    high = fmaxf(fmaxf(high, v.x), fmax3(v.y, v.z, v.w));
+    scores[k] = v;
   }
+  // every page, or those that are kept whatever their scores; then the places without one
+  for (int k = threadIdx.x; k < a.keep; k += LIST_THREADS) {
+    const bool middle = np > a.keep && k >= a.first && k < a.keep - a.last;
+    if (!middle) out[k] = k >= n ? -1 : table[np > a.keep && k >= a.first ? np - (a.keep - k) : k];
+  }
+  if (m == 0) return;
+  __syncthreads();
+  float bound;
+  int left;
+  want_th(sh, reinterpret_cast<const float *>(scores), m, a.keep - a.first - a.last, low, high, bound, left);
+  // scores above the bound, and the first `left` that equal it: every warp a stretch, a lane four in a row; counts of those above in
+  // the low and of equal ones in the high half
+  const int per = (m4 + LIST_THREADS - 1) / LIST_THREADS * 32, f0 = min(warp * per, m4), f1 = min(f0 + per, m4);
+  auto counts = [&](const float4 &v) {
+    return (v.x > bound) + (v.y > bound) + (v.z > bound) + (v.w > bound) +
+           (((v.x == bound) + (v.y == bound) + (v.z == bound) + (v.w == bound)) << 16);
+  };
+  uint32_t both = 0u;
+#pragma unroll 4
+  for (int k = f0 + lane; k < f1; k += 32) both += counts(scores[k]);
+  const uint32_t above = __reduce_add_sync(0xffffffffu, both & 0xFFFFu), equal = __reduce_add_sync(0xffffffffu, both >> 16);
   if (lane == 0) {
-    count[warp][0] = above;
-    count[warp][1] = equal;
+    sh.count[warp][0] = above;
+    sh.count[warp][1] = equal;
   }
   __syncthreads();
-  uint32_t at = a.first, ties = 0u;  // where this warp's pages go, ties in front of its own
+  uint32_t at = 0u, ties = 0u;  // in front of this warp's: scores above, equal ones
   for (int w = 0; w < warp; ++w) {
-    const uint32_t room = static_cast<uint32_t>(left) - min(ties, static_cast<uint32_t>(left));
-    at += count[w][0] + min(count[w][1], room);
-    ties += count[w][1];
+    at += sh.count[w][0];
+    ties += sh.count[w][1];
   }
-  for (int k = k0; k < k1; k += 32) {
-    const bool in = k + lane < k1;
-    const uint32_t key = in ? keys[k + lane] : 0u, mask = (1u << lane) - 1u;
-    const uint32_t eq = __ballot_sync(0xffffffffu, in && key == bound);
-    const bool take = in && (key > bound || (key == bound && ties + __popc(eq & mask) < static_cast<uint32_t>(left)));
-    const uint32_t taken = __ballot_sync(0xffffffffu, take);
-    if (take) out[at + __popc(taken & mask)] = table[a.first + k + lane];
-    at += __popc(taken);
-    ties += __popc(eq);
+  // (a stretch without one to take is passed over: equal ones behind the first `left` are not taken)
+  const bool some = above > 0u || (equal > 0u && ties < static_cast<uint32_t>(left));
+  for (int k = f0; some && k < f1; k += 32) {
+    const float4 v = k + lane < f1 ? scores[k + lane] : make_float4(0.f, 0.f, 0.f, 0.f);
+    const uint32_t own = k + lane < f1 ? counts(v) : 0u;
+    if (!__any_sync(0xffffffffu, own != 0u)) continue;
+    uint32_t sum = own;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const uint32_t o = __shfl_up_sync(0xffffffffu, sum, off);
+      if (lane >= off) sum += o;
+    }
+    uint32_t up = at + ((sum - own) & 0xFFFFu), eq = ties + ((sum - own) >> 16);
+    const float x[4] = {v.x, v.y, v.z, v.w};
+    if (own != 0u)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const bool is = x[j] == bound;
+        if (x[j] > bound || (is && eq < static_cast<uint32_t>(left)))
+          out[a.first + up + min(eq, static_cast<uint32_t>(left))] = a.first + 4 * (k + lane) + j;
+        up += x[j] > bound;
+        eq += is;
+      }
+    const uint32_t all = __shfl_sync(0xffffffffu, sum, 31);
+    at += all & 0xFFFFu;
+    ties += all >> 16;
   }
+  // places in the sequence's row become pages, all at once
+  __syncthreads();
+  for (int k = a.first + threadIdx.x; k < a.keep - a.last; k += LIST_THREADS) out[k] = table[out[k]];
 }
 
 // A bounds array for the pool: its bytes fit and it is aligned.
@@ -548,9 +807,17 @@ int sparge_cache4_bounds_load(const sparge_cache4 *cache, const void *bounds, si
   return e == cudaSuccess ? SPARGE_OK : cuda_fail(e, "page bounds load launch");
 }
 
+size_t sparge_cache4_select_workspace_bytes(int64_t B, int64_t Hkv, int64_t Nq, int64_t width) {
+  if (B < 0 || B > 65535 || Hkv <= 0 || Hkv > 65535 || Nq < 0 || Nq > (int64_t(1) << 30) || width < 0 || width > SEL_PAGES ||
+      B * Nq * Hkv > INT_MAX)
+    return 0;
+  return static_cast<size_t>(B * Nq * Hkv) * static_cast<size_t>((width + 3) / 4 * 16);
+}
+
 int sparge_cache4_select(const sparge_tensor *q, const sparge_cache4 *cache, const void *bounds, size_t bounds_bytes,
                          const int32_t *table, int64_t width, int64_t table_stride, const int32_t *kv_lens, int64_t keep,
-                         int64_t first, int64_t last, int32_t *pages, int32_t *lens, sparge_stream_t stream) {
+                         int64_t first, int64_t last, int32_t *pages, int32_t *lens, void *ws, size_t ws_bytes,
+                         sparge_stream_t stream) {
   clear_error();
   View qv;
   Cache4 c;
@@ -566,11 +833,14 @@ int sparge_cache4_select(const sparge_tensor *q, const sparge_cache4 *cache, con
   if (first < 0 || last < 1 || keep > INT_MAX / c.page_size || first > keep || last > keep - first)
     return fail(SPARGE_ERR_INVALID_ARG, "first=%lld >= 0, last=%lld >= 1 and their sum at most keep=%lld, keep 2^31 tokens at most",
                 (long long)first, (long long)last, (long long)keep);
-  if (qv.B * qv.N == 0) return SPARGE_OK;
+  const int64_t lists = qv.B * qv.N * c.H;
+  if (lists > INT_MAX) return fail(SPARGE_ERR_UNSUPPORTED, "too many queries");
+  if (lists == 0) return SPARGE_OK;
+  const size_t need = sparge_cache4_select_workspace_bytes(qv.B, c.H, qv.N, width);
+  if (need && (!ws || ws_bytes < need)) return fail(SPARGE_ERR_WORKSPACE_TOO_SMALL, "workspace %zu bytes, need %zu", ws_bytes, need);
+  if (reinterpret_cast<uintptr_t>(ws) & 255u) return fail(SPARGE_ERR_INVALID_ARG, "workspace not 256-byte aligned");
   if (!pages || !lens) return fail(SPARGE_ERR_INVALID_ARG, "pages or lens is NULL");
   if (lens == kv_lens) return fail(SPARGE_ERR_INVALID_ARG, "lens must not be kv_lens: every list reads those");
-  const int64_t lists = qv.B * qv.N * c.H;
-  if (lists > INT_MAX / 8) return fail(SPARGE_ERR_UNSUPPORTED, "too many queries");
   SelectArgs a;
   a.q = static_cast<const __nv_bfloat16 *>(qv.data);
   a.q_sb = qv.sb; a.q_sh = qv.sh; a.q_sn = qv.sn;
@@ -580,6 +850,7 @@ int sparge_cache4_select(const sparge_tensor *q, const sparge_cache4 *cache, con
   a.table_stride = table_stride;
   a.n_pages = c.n_pages;
   a.row = bounds_row(c.H, c.d);
+  a.B = static_cast<int>(qv.B);
   a.width = static_cast<int>(width);
   a.page_shift = c.page_shift;
   a.Hkv = c.H;
@@ -588,21 +859,31 @@ int sparge_cache4_select(const sparge_tensor *q, const sparge_cache4 *cache, con
   a.keep = static_cast<int>(keep);
   a.first = static_cast<int>(first);
   a.last = static_cast<int>(last);
+  a.keys = static_cast<float *>(ws);
+  a.pitch = static_cast<int>((width + 3) / 4 * 4);
   a.pages = pages;
   a.out_lens = lens;
   a.status = status_ptr();
-  // CTAs of a list: two for every SM in all, each with at least one round of its warps
-  unsigned cluster = 1;
-  while (cluster < 8 && lists * cluster < 152 && static_cast<int64_t>(cluster) * SEL_THREADS < width) cluster *= 2;
-  const size_t smem = static_cast<size_t>((width * 4 + 15) / 16 * 16) + static_cast<size_t>(a.G) * 2 * c.d;
-  static std::atomic<unsigned long long> set64{0}, set128{0};
-  constexpr int MOST = SEL_PAGES * 4 + SEL_HEADS * 2 * 128;
-  cudaError_t e = c.d == 128 ? set_smem_limit_once(select_kernel<128>, MOST, set128) : set_smem_limit_once(select_kernel<64>, MOST, set64);
+  a.rows_log = a.G == 1 ? 0 : a.G == 2 ? 1 : 2;
+  a.tiles = a.G <= 4 ? 0 : (a.G + 7) / 8;
+  const int row = a.tiles ? 8 * a.tiles : 1 << a.rows_log;
+  a.at_once = SEL_ROWS / row < a.Nq ? SEL_ROWS / row : a.Nq;
+  const int rounds = (a.Nq + a.at_once - 1) / a.at_once;
+  if (rounds > 65535) return fail(SPARGE_ERR_UNSUPPORTED, "too many queries");
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const dim3 grid(static_cast<unsigned>(lists * cluster));
+  cudaError_t e = cudaSuccess;
+  if (width > keep && keep > first + last) {  // else there is nothing to choose
+    const int64_t most = qv.B * c.H * ((width + sel_stretch(c.d) - 1) / sel_stretch(c.d)), ctas = most < 152 * SEL_CTAS ? most : 152 * SEL_CTAS;
+    const dim3 grid(static_cast<unsigned>(ctas), static_cast<unsigned>(rounds));
+    e = c.d == 128 ? launch_dependent(select_score_kernel<128>, grid, SEL_THREADS, 0, s, a)
+                   : launch_dependent(select_score_kernel<64>, grid, SEL_THREADS, 0, s, a);
+  }
+  if (e == cudaSuccess) {
+    static std::atomic<unsigned long long> smem_set{0};
+    e = set_smem_limit_once(select_list_kernel, SEL_PAGES * 4, smem_set);
+  }
   if (e == cudaSuccess)
-    e = c.d == 128 ? launch_dependent_clusters(select_kernel<128>, grid, SEL_THREADS, smem, cluster, s, a)
-                   : launch_dependent_clusters(select_kernel<64>, grid, SEL_THREADS, smem, cluster, s, a);
+    e = launch_dependent(select_list_kernel, dim3(static_cast<unsigned>(lists)), LIST_THREADS, static_cast<size_t>((width + 3) / 4 * 16), s, a);
   return e == cudaSuccess ? SPARGE_OK : cuda_fail(e, "page selection launch");
 }
 

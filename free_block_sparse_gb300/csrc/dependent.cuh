@@ -30,26 +30,6 @@ __device__ __forceinline__ uint4 ld_once_v4(const void *p) {
   return v;
 }
 
-// cluster: thread blocks of a cluster along the grid's x
-template <typename... KArgs, typename... Args>
-inline cudaError_t launch_dependent_clusters(void (*kernel)(KArgs...), dim3 grid, unsigned threads, size_t smem, unsigned cluster,
-                                             cudaStream_t st, const Args &...args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute at[2];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  at[1].id = cudaLaunchAttributeClusterDimension;
-  at[1].val.clusterDim.x = cluster;
-  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
 template <typename... KArgs, typename... Args>
 inline cudaError_t launch_dependent(void (*kernel)(KArgs...), dim3 grid, unsigned threads, size_t smem, cudaStream_t st,
                                     const Args &...args) {

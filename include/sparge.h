@@ -424,11 +424,15 @@ int sparge_cache4_bounds_load(const sparge_cache4 *cache, const void *bounds, si
  * that the query sees (last >= 1), then the largest scores, the earlier page where scores are equal, up to `keep`
  * pages in all.
  * pages (B,Nq,H,keep) int32 receives the kept pages' numbers in the pool, in the order of the sequence, -1 behind them; lens (B,Nq)
- * int32 the number of tokens on them.  At most 64 query heads per key/value head and 40960 table columns.
+ * int32 the number of tokens on them (lens must not be kv_lens).  At most 64 query heads per key/value head and 32768 table
+ * columns.  ws: 256-byte aligned, sparge_cache4_select_workspace_bytes(...) bytes (a score for every query, head and table
+ * column), used by one call at a time.
  */
+size_t sparge_cache4_select_workspace_bytes(int64_t B, int64_t Hkv, int64_t Nq, int64_t width);
 int sparge_cache4_select(const sparge_tensor *q, const sparge_cache4 *cache, const void *bounds, size_t bounds_bytes,
                          const int32_t *table, int64_t width, int64_t table_stride, const int32_t *kv_lens, int64_t keep,
-                         int64_t first, int64_t last, int32_t *pages, int32_t *lens, sparge_stream_t stream);
+                         int64_t first, int64_t last, int32_t *pages, int32_t *lens, void *ws, size_t ws_bytes,
+                         sparge_stream_t stream);
 
 /*
  * Attention over lists of pages: query r of sequence b sees, in key/value head h, the first lens[b][r] tokens on the pages

@@ -57,17 +57,17 @@ def test_bounds_load_refuses(lib, change, code):
 
 @pytest.mark.parametrize("change,code", [
     (dict(q=None), BAD), (dict(q=t(H=3)), UNSUP), (dict(q=t(d=64)), BAD), (dict(q=t(H=130)), UNSUP), (dict(c=pool(page=24)), UNSUP),
-    (dict(bounds=None), BAD), (dict(bytes=99), BAD), (dict(width=-1), BAD), (dict(stride=7), BAD), (dict(width=40961, stride=40961), UNSUP),
+    (dict(bounds=None), BAD), (dict(bytes=99), BAD), (dict(width=-1), BAD), (dict(stride=7), BAD), (dict(width=32769, stride=32769), UNSUP),
     (dict(table=None), BAD), (dict(lens=None), BAD), (dict(keep=-1), BAD), (dict(keep=1 << 30), BAD), (dict(first=-1), BAD),
     (dict(last=0), BAD), (dict(keep=3, first=2, last=2), BAD), (dict(first=1 << 62, last=1 << 62), BAD), (dict(pages=None), BAD),
-    (dict(out=None), BAD), (dict(out=3 * PTR), BAD),
+    (dict(out=None), BAD), (dict(out=3 * PTR), BAD), (dict(ws=None), SMALL), (dict(wsb=2 * 8 * 2 * 8 * 4 - 1), SMALL), (dict(ws=PTR + 16), BAD),
 ])
 def test_select_refuses(lib, change, code):
     a = dict(q=t(), c=pool(), bounds=PTR, bytes=4 * 544, table=PTR, width=8, stride=8, lens=3 * PTR, keep=6, first=1, last=1, pages=PTR,
-             out=2 * PTR)
+             out=2 * PTR, ws=PTR, wsb=BIG)
     a.update(change)
     refused(lib, lib.sparge_cache4_select(ref(a["q"]), ref(a["c"]), a["bounds"], a["bytes"], a["table"], a["width"], a["stride"],
-                                          a["lens"], a["keep"], a["first"], a["last"], a["pages"], a["out"], None), code)
+                                          a["lens"], a["keep"], a["first"], a["last"], a["pages"], a["out"], a["ws"], a["wsb"], None), code)
 
 
 @pytest.mark.parametrize("change,code", [
@@ -101,7 +101,7 @@ def test_calls_of_nothing(lib):
     assert lib.sparge_qk_norm_rope_axes(ref(e), ref(e), None, 1, 0, 0, None, PTR, 64, 0, None, None, 1e-6, ref(e), ref(e), None) == 0
     assert lib.sparge_cache4_bounds_update(ref(c), None, 0, 0, 0, None, 1, None, 0, None) == 0
     assert lib.sparge_cache4_bounds_load(ref(c), None, 0, None, 0, None, None, None) == 0
-    assert lib.sparge_cache4_select(ref(e), ref(c), None, 0, None, 0, 0, PTR, 2, 1, 1, None, None, None) == 0
+    assert lib.sparge_cache4_select(ref(e), ref(c), None, 0, None, 0, 0, PTR, 2, 1, 1, None, None, None, 0, None) == 0
     assert lib.sparge_cache4_pages_attn(ref(e), ref(c), None, 4, None, 0.0, ref(e), PTR, BIG, None) == 0
     assert lib.sparge_cache4_prefix_attn(ref(e), ref(c), None, 0, None, 0, 0, None, 0.0, ref(e), PTR, BIG, None) == 0
 
@@ -111,6 +111,9 @@ def test_sizes(lib):
         assert lib.sparge_cache4_bounds_bytes(1, H, d) == row and lib.sparge_cache4_bounds_bytes(1 << 24, H, d) == row << 24
     for bad in ((-1, 2, 128), (1, 0, 128), (1, 2, 96), (1, 65536, 64)):
         assert lib.sparge_cache4_bounds_bytes(*bad) == 0
+    assert lib.sparge_cache4_select_workspace_bytes(3, 8, 2, 1001) == 3 * 8 * 2 * 1004 * 4
+    for bad in ((-1, 8, 2, 10), (3, 0, 2, 10), (3, 8, -1, 10), (3, 8, 2, 32769), (65535, 65535, 1, 10)):
+        assert lib.sparge_cache4_select_workspace_bytes(*bad) == 0
     for f in (lib.sparge_cache4_pages_attn_workspace_bytes, lib.sparge_cache4_prefix_attn_workspace_bytes):
         assert f(4, 32, 8, 1, 128) > 0 and f(4, 32, 5, 1, 128) == 0 and f(4, 32, 8, 1, 96) == 0 and f(-1, 32, 8, 1, 128) == 0
         assert f(65536, 32, 8, 1, 128) == 0 and f(65535, 32, 32, 1 << 30, 128) == 0
