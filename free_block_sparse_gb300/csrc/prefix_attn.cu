@@ -13,8 +13,8 @@
 namespace sparge {
 namespace {
 
-constexpr int PF_SOFT = 8, PF_WIDE = 4;  // softmax warps, widening warps
-constexpr int PF_PROD = PF_SOFT + PF_WIDE, PF_LOAD = PF_PROD + 2;  // a products warp per stream, the loads warp
+// Warps: softmax (4 per stream, a row a thread), widening (two groups of 4 that take turns), products (one per stream), loads.
+constexpr int PF_SOFT = 8, PF_WIDE = 8, PF_PROD = PF_SOFT + PF_WIDE, PF_LOAD = PF_PROD + 2;
 constexpr int PF_THREADS = (PF_LOAD + 1) * 32;
 constexpr int PF_ROWS = 256;             // rows of a slot: two streams of 128
 constexpr float PF_RESCALE = 8.f;
@@ -39,11 +39,11 @@ template <int D, int R>
 struct PfCfg {
   static constexpr int PITCH = Rec4<D>::BYTES + 64;  // of a record in the ring, so that two of them fall on different banks
   static constexpr int RAW = 4 * PITCH;
-  static constexpr int RS = 6, NS = R == 2 ? 3 : 4;  // stages of raw tiles, of widened ones
+  static constexpr int RS = 6, NS = R == 2 ? 3 : 4;  // stages of raw tiles, of widened ones: of K, and of V
   static constexpr bool QSMEM = D == 128 && R == 2;  // no room in TMEM for two tiles of Q
   static constexpr uint32_t TILE = 64 * D * 2;       // of K or V, f16
   static constexpr uint32_t K = 0, V = K + NS * TILE, Q = V + NS * TILE, RING = Q + (QSMEM ? 2 * 128 * D * 2 : 0);
-  static constexpr uint32_t TABK = RING + RS * RAW, TABV = TABK + 2 * 64 * 16, CTRL = TABV + 2 * 512;
+  static constexpr uint32_t TABK = RING + RS * RAW, TABV = TABK + 4 * 64 * 16, CTRL = TABV + 4 * 512;
   static constexpr uint32_t SMEM = CTRL + 1024;
   // TMEM columns
   static constexpr uint32_t O = 0, S = 2 * D, P = S + 128, QC = P + 64, QCOLS = D / 2;
@@ -56,10 +56,10 @@ struct PfInfo {  // of a widened tile: K = K' k_unit, V = V' 2^g; bit r of missi
   uint32_t missing;
 };
 struct PfCtrl {
-  uint64_t raw_full[8], raw_free[8], kv_full[4], kv_free[4];
+  uint64_t raw_full[8], raw_free[8], k_full[4], k_free[4], v_full[4], v_free[4];
   uint64_t q_full[2], q_free, s_full[2], s_free[2], p_full[2], pv_done[2], drained[2];
-  PfInfo info[4];
-  int need[2][PF_WIDE];
+  PfInfo info[8];  // (tile % 8: K's stage is free again before the softmax has read what goes with it)
+  int need[4][4];  // of a tile (tile % 4): K by warps 0 and 1 of its group, V by 2 and 3
   uint8_t bad[8][4];
   uint32_t tmem;
   int abort, no_abort;
@@ -140,11 +140,13 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefix_attn_kernel(const Prefix
   if (threadIdx.x == 0) {
     for (int s = 0; s < RS; ++s) {
       mbar_init(&cs.raw_full[s], 4);
-      mbar_init(&cs.raw_free[s], PF_WIDE);
+      mbar_init(&cs.raw_free[s], 4);
     }
     for (int s = 0; s < NS; ++s) {
-      mbar_init(&cs.kv_full[s], PF_WIDE);
-      mbar_init(&cs.kv_free[s], R);
+      mbar_init(&cs.k_full[s], 4);
+      mbar_init(&cs.k_free[s], R);
+      mbar_init(&cs.v_full[s], 4);
+      mbar_init(&cs.v_free[s], R);
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(&cs.q_full[t], 4);
@@ -188,14 +190,18 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefix_attn_kernel(const Prefix
         const int b = r / (a.G * a.Nq), rr = r % (a.G * a.Nq);
         const uint4 *src = reinterpret_cast<const uint4 *>(a.q + b * a.q_sb + (kvh * a.G + rr / a.Nq) * a.q_sh +
                                                            static_cast<int64_t>(rr % a.Nq) * a.q_sn);
-        uint4 v[D / 8];
         float mx = 0.f;
+#pragma unroll 1
+        for (int i = 0; i < D / 8; i += 4) {
+          uint4 v[4];
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-          v[i] = r < a.rows ? src[i] : make_uint4(0u, 0u, 0u, 0u);
-          const uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+          for (int k = 0; k < 4; ++k) v[k] = r < a.rows ? src[i + k] : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) mx = fmaxf(mx, fmaxf(fabsf(bf16lo(u[k])), fabsf(bf16hi(u[k]))));
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t u[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+#pragma unroll
+            for (int x = 0; x < 4; ++x) mx = fmaxf(mx, fmaxf(fabsf(bf16lo(u[x])), fabsf(bf16hi(u[x]))));
+          }
         }
         const int e = min(max(pf_exponent(mx), -100), 116);
         const float f = pf_pow2(14 - e);
@@ -208,12 +214,15 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefix_attn_kernel(const Prefix
             if (!ok) break;
             tc_fence_after();
           }
-#pragma unroll
+#pragma unroll 1
           for (int i = 0; i < D / 8; i += 4) {
+            uint4 v[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[k] = r < a.rows ? src[i + k] : make_uint4(0u, 0u, 0u, 0u);
             uint32_t w[16];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              const uint4 u = v[i + k];
+              const uint4 u = v[k];
               w[4 * k] = pf_half2(bf16lo(u.x) * f, bf16lo(u.z) * f);
               w[4 * k + 1] = pf_half2(bf16hi(u.x) * f, bf16hi(u.z) * f);
               w[4 * k + 2] = pf_half2(bf16lo(u.y) * f, bf16lo(u.w) * f);
@@ -237,96 +246,108 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefix_attn_kernel(const Prefix
       }
       float m_ref = -INFINITY, l = 0.f;
       int G = 0;  // O counts 2^G
+      const bool live = r - lane < a.rows;  // a warp past the last row takes part in the waits alone
+      // columns 8 c + 4 r + i of a half are tokens of its record r: those that are not there are hidden; the others' maximum
+      auto hide = [](uint32_t (&x)[32], uint32_t gone) {
+        float m = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < 32; ++k) {
+          if ((gone >> ((k >> 2) & 1)) & 1u) x[k] = 0xFF800000u;
+          m = fmaxf(m, __uint_as_float(x[k]));
+        }
+        return m;
+      };
       const int jobs = R == 2 ? n : (n - t + 1) / 2;
       for (int j = 0; j < jobs; ++j, ++done) {
         const uint32_t tile = tc + (R == 2 ? j : 2 * j + t), st = tile % NS;
-        ok = mbar_wait(&cs.s_full[t], done & 1, abort, a.status) && mbar_wait(&cs.kv_full[st], (tile / NS) & 1, abort, a.status);
+        ok = mbar_wait(&cs.v_full[st], (tile / NS) & 1, abort, a.status) && mbar_wait(&cs.s_full[t], done & 1, abort, a.status);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
-        uint32_t v[2][32];
-        float mh[2];
-        tmem_ld32_max(sc, v[0], mh[0]);
-        tmem_ld32_max(sc + 32, v[1], mh[1]);
-        const float mult = rm * cs.info[st].k_unit;
-        const int g = cs.info[st].g;
-        const uint32_t missing = cs.info[st].missing;
-        pf_ld_wait_for(v[0], mh[0]);
-        pf_ld_wait_for(v[1], mh[1]);
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&cs.s_free[t]);
-        if (missing) {  // columns 32 h + 8 c + 4 r + i are tokens of record 2 h + r
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            mh[h] = -INFINITY;
-#pragma unroll
-            for (int k = 0; k < 32; ++k) {
-              if ((missing >> (2 * h + ((k >> 2) & 1))) & 1u) v[h][k] = 0xFF800000u;
-              mh[h] = fmaxf(mh[h], __uint_as_float(v[h][k]));
-            }
-          }
+        // 32 columns are held at a time; the others are read for their maximum now and once more for their turn
+        uint32_t v[32];
+        float mx = -INFINITY, m1;
+        const float mult = rm * cs.info[tile & 7].k_unit;
+        const int g = cs.info[tile & 7].g;
+        const uint32_t missing = cs.info[tile & 7].missing;
+        if (live) {
+          tmem_ld32_max(sc + 32, v, m1);
+          pf_ld_wait_for(v, m1);
+          if (missing) m1 = hide(v, missing >> 2);
+          tmem_ld32_max(sc, v, mx);
+          pf_ld_wait_for(v, mx);
+          if (missing) mx = hide(v, missing);
+          mx = fmaxf(mx, m1) * mult;
         }
-        const float mx = fmaxf(mh[0], mh[1]) * mult;
         if (j > 0) {  // the product before this one has read its P and added to O
           ok = __all_sync(0xffffffffu, mbar_wait(&cs.pv_done[t], (done - 1) & 1, abort, a.status));
           if (!ok) break;
           tc_fence_after();
         }
-        if (m_ref == -INFINITY) G = g;
-        const bool resc = mx > m_ref + PF_RESCALE || mx - m_ref + static_cast<float>(g - G) > PF_TOP;
-        if (__any_sync(0xffffffffu, resc)) {
-          float f = 1.f;
-          if (resc) {
-            const float to = fmaxf(m_ref, mx), al = fast_exp2(m_ref - to);
-            // O's unit follows: this tile's, or what the sums before need
-            const int Gn = m_ref == -INFINITY ? g : max(g, __float2int_ru(fmaxf(static_cast<float>(G) + (m_ref - to), -1000.f)));
-            f = al * pf_pow2(min(max(G - Gn, -126), 127));
-            l *= al;
-            m_ref = to;
-            G = Gn;
-          }
-          if (j > 0) {
+        if (live) {
+          if (m_ref == -INFINITY) G = g;
+          const bool resc = mx > m_ref + PF_RESCALE || mx - m_ref + static_cast<float>(g - G) > PF_TOP;
+          if (__any_sync(0xffffffffu, resc)) {
+            float f = 1.f;
+            if (resc) {
+              const float to = fmaxf(m_ref, mx), al = fast_exp2(m_ref - to);
+              // O's unit follows: this tile's, or what the sums before need
+              const int Gn = m_ref == -INFINITY ? g : max(g, __float2int_ru(fmaxf(static_cast<float>(G) + (m_ref - to), -1000.f)));
+              f = al * pf_pow2(min(max(G - Gn, -126), 127));
+              l *= al;
+              m_ref = to;
+              G = Gn;
+            }
+            if (j > 0) {
 #pragma unroll 1
-            for (int q = 0; q < D / 16; ++q) {
-              uint32_t o[16];
-              tmem_ld16(oc + 16 * q, o);
-              tmem_ld_wait();
+              for (int q = 0; q < D / 16; ++q) {
+                uint32_t o[16];
+                tmem_ld16(oc + 16 * q, o);
+                tmem_ld_wait();
 #pragma unroll
-              for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-              tmem_st16(oc + 16 * q, o);
+                for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                tmem_st16(oc + 16 * q, o);
+              }
             }
           }
-        }
-        // P' = 2^(x - m_ref + g - G); a row whose reference is still -inf has only hidden columns (or NaN)
-        const int up = G - g;
-        const float nref = m_ref == -INFINITY ? 0.f : -m_ref;
-        const float2 m2 = make_float2(mult, mult), nr2 = make_float2(nref - static_cast<float>(up), nref - static_cast<float>(up));
-        float2 rs[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+          // P' = 2^(x - m_ref + g - G); a row whose reference is still -inf has only hidden columns (or NaN)
+          const int up = G - g;
+          const float nref = m_ref == -INFINITY ? 0.f : -m_ref;
+          const bool tiny = __any_sync(0xffffffffu, up > 60);  // V of this tile beside what O holds: the sum of P goes by itself
+          const float2 m2 = make_float2(mult, mult), nr2 = make_float2(nref - static_cast<float>(up), nref - static_cast<float>(up));
+          float2 rs[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll 1
+          for (int h = 0; h < 2; ++h) {
+            if (h == 1) {
+              tmem_ld32_max(sc + 32, v, m1);
+              pf_ld_wait_for(v, m1);
+              if (missing) hide(v, missing >> 2);
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&cs.s_free[t]);
+            }
+            if (tiny) {
+              float sum = 0.f;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t pk[16];
+              for (int k = 0; k < 32; ++k) sum += fast_exp2(fmaf(__uint_as_float(v[k]), mult, nref));
+              l += sum;
+            }
+            uint32_t pk[16];
 #pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            const float2 e2 = ffma2(make_float2(__uint_as_float(v[h][2 * k]), __uint_as_float(v[h][2 * k + 1])), m2, nr2);
-            const float2 p2 = make_float2(fast_exp2(e2.x), fast_exp2(e2.y));
-            rs[k & 1] = fadd2(rs[k & 1], p2);
-            pk[k] = pack_f16x2(p2.x, p2.y);
+            for (int k = 0; k < 16; ++k) {
+              const float2 e2 = ffma2(make_float2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])), m2, nr2);
+              const float2 p2 = make_float2(fast_exp2(e2.x), fast_exp2(e2.y));
+              rs[k & 1] = fadd2(rs[k & 1], p2);
+              pk[k] = pack_f16x2(p2.x, p2.y);
+            }
+            tmem_st16(pc + 16 * h, pk);
           }
-          tmem_st16(pc + 16 * h, pk);
+          const float2 sum = fadd2(rs[0], rs[1]);
+          if (!tiny) l = fmaf(sum.x + sum.y, pf_pow2(max(up, -126)), l);
+          tmem_st_wait();
+        } else if (lane == 0) {
+          mbar_arrive(&cs.s_free[t]);
         }
-        const float2 sum = fadd2(rs[0], rs[1]);
-        if (__any_sync(0xffffffffu, up > 60)) {  // V of this tile is tiny beside what O holds: the sum of P by itself
-          float s = 0.f;
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int k = 0; k < 32; ++k) s += fast_exp2(fmaf(__uint_as_float(v[h][k]), mult, nref));
-          l += s;
-        } else {
-          l = fmaf(sum.x + sum.y, pf_pow2(max(up, -126)), l);
-        }
-        tmem_st_wait();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&cs.p_full[t]);
@@ -340,7 +361,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefix_attn_kernel(const Prefix
       }
       const int64_t at = (static_cast<int64_t>(blockIdx.x) + item) * PF_ROWS + t * 128 + row;
       if (r < a.rows) *reinterpret_cast<float2 *>(a.part_ml + 2 * at) = make_float2(m_ref, l);
-      if (jobs > 0) {
+      if (jobs > 0 && live) {
         const float back = pf_pow2(min(max(G, -126), 127));
         float *to = a.part_o + at * D;
 #pragma unroll 1
@@ -360,11 +381,11 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefix_attn_kernel(const Prefix
       }
       tc += n;
     }
-  } else if (warp < PF_SOFT + PF_WIDE) {
+  } else if (warp < PF_PROD) {
     // ------------------------------------ widening: codes to f16 tiles ------------------------------------
-    // A tile's power of two for K and the one for V follow from the words of all its tokens.  The words of the tile behind are
-    // looked at, and its table is made, around the widening of the one in front, so that one barrier a tile is enough.
-    const int w4 = warp - PF_SOFT, tid = w4 * 32 + lane;
+    // A tile's power of two for K and the one for V follow from the words of all its tokens.  The words of the group's next tiles are
+    // looked at, and the next table is made, around the widening of the one in front, so that one barrier a tile is enough.
+    const int w4 = warp & 3, tid = w4 * 32 + lane, group = (warp - PF_SOFT) >> 2;
     const int side = tid >> 6, rec = (tid >> 4) & 3, tk = tid & 15;  // this thread's token and side in words and tables
     const uint32_t base = smem_u32(smem);
     float s[NG], m[NG];  // its words of the tile behind
@@ -385,17 +406,17 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefix_attn_kernel(const Prefix
           need = max(need, max(pf_exponent(s[g]) + 9, max(pf_exponent(m[g]), pf_exponent(fmaf(15.f, s[g], m[g]))) - 14));
       }
       need = __reduce_max_sync(0xffffffffu, need);
-      if (lane == 0) cs.need[tile & 1][w4] = need;
+      if (lane == 0) cs.need[tile & 3][w4] = need;
     };
     int fk = 0, fv = 0;
     auto table = [&](uint32_t tile) {
-      const int *need = cs.need[tile & 1];
+      const int *need = cs.need[tile & 3];
       fk = min(max(-max(need[0], need[1]), -126), 100);
       fv = min(max(-max(need[2], need[3]), -126), 100);
       const int f = side ? fv : fk;
       const float fs = pf_pow2(f + 24), fm = pf_pow2(f);
       const int pos = 32 * (rec >> 1) + 8 * ((tk & 7) >> 1) + 4 * (rec & 1) + 2 * (tk >> 3) + (tk & 1);
-      uint8_t *tk_ = smem + C::TABK + (tile & 1) * 1024, *tv = smem + C::TABV + (tile & 1) * 512;
+      uint8_t *tk_ = smem + C::TABK + (tile & 3) * 1024, *tv = smem + C::TABV + (tile & 3) * 512;
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
         const uint32_t ss = pf_half2(s[g] * fs, s[g] * fs), mm = pf_half2(m[g] * fm, m[g] * fm);
@@ -407,30 +428,31 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefix_attn_kernel(const Prefix
         }
       }
     };
-    auto all_ok = [&]() { return ok = !bar_red_or(1, PF_WIDE * 32, !ok); };
+    auto all_ok = [&]() { return ok = !bar_red_or(1 + group, 128, !ok); };
     const uint32_t total = static_cast<uint32_t>(share.end - share.at);  // tiles of all the CTA's pieces
-    if (total > 0) {
-      words(0);
+    const uint32_t tile0 = group;  // the group takes every second tile
+    if (tile0 < total) {
+      words(tile0);
       if (all_ok()) {
-        table(0);
-        if (total > 1) words(1);
+        table(tile0);
+        if (tile0 + 2 < total) words(tile0 + 2);
       }
     }
-    for (uint32_t tile = 0; tile < total; ++tile) {
+    for (uint32_t tile = tile0; tile < total; tile += 2) {
       {
         const uint32_t rs = tile % RS, st = tile % NS;
-        if (tile >= NS) ok = __all_sync(0xffffffffu, mbar_wait(&cs.kv_free[st], (tile / NS - 1) & 1, abort, a.status)) && ok;
+        if (tile >= NS) ok = __all_sync(0xffffffffu, mbar_wait(&cs.k_free[st], (tile / NS - 1) & 1, abort, a.status)) && ok;
         const int k_is = fk, v_is = fv;
         if (!all_ok()) break;  // this tile's table and the next one's powers are there
         const uint8_t *raw = smem + C::RING + rs * C::RAW;
-        const uint8_t *tabk = smem + C::TABK + (tile & 1) * 1024, *tabv = smem + C::TABV + (tile & 1) * 512;
+        const uint8_t *tabk = smem + C::TABK + (tile & 3) * 1024, *tabv = smem + C::TABV + (tile & 3) * 512;
         if (tid == 0) {
-          PfInfo &i = cs.info[st];
+          PfInfo &i = cs.info[tile & 7];
           i.k_unit = pf_pow2(-k_is);
           i.g = -v_is;
           i.missing = cs.bad[rs][0] | (cs.bad[rs][1] << 1) | (cs.bad[rs][2] << 2) | (cs.bad[rs][3] << 3);
         }
-        if (tile + 1 < total) table(tile + 1);
+        if (tile + 2 < total) table(tile + 2);
         // ---- K: a lane takes the codes of 8-channel piece c of every 32 channels of a token ----
         {
           const int c = lane & 3, r = (lane >> 2) & 1;
@@ -460,6 +482,11 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefix_attn_kernel(const Prefix
             }
           }
         }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&cs.k_full[st]);
+        // (a warp whose wait gives up leaves its V as it is and goes on to the next barrier)
+        if (tile >= NS) ok = __all_sync(0xffffffffu, mbar_wait(&cs.v_free[st], (tile / NS - 1) & 1, abort, a.status)) && ok;
         // ---- V, transposed: lane 4 g + c holds channels g and g + 8 of every 16 for tokens 2c, 2c + 1, 2c + 8, 2c + 9 of two records ----
         {
           const int g = lane >> 2, c = lane & 3;
@@ -496,10 +523,10 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefix_attn_kernel(const Prefix
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(&cs.kv_full[st]);
+          mbar_arrive(&cs.v_full[st]);
           mbar_arrive(&cs.raw_free[rs]);
         }
-        if (tile + 2 < total) words(tile + 2);
+        if (tile + 4 < total) words(tile + 4);
       }
     }
   } else if (warp < PF_LOAD) {
@@ -519,7 +546,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefix_attn_kernel(const Prefix
         for (int j = 0; ok && j <= jobs; ++j) {
           if (j < jobs) {  // scores of job j, once the softmax has read those before
             const uint32_t tile = tc + (R == 2 ? j : 2 * j + t), st = tile % NS;
-            ok = mbar_wait(&cs.kv_full[st], (tile / NS) & 1, abort, a.status) &&
+            ok = mbar_wait(&cs.k_full[st], (tile / NS) & 1, abort, a.status) &&
                  (done == 0 || mbar_wait(&cs.s_free[t], (done - 1) & 1, abort, a.status));
             if (!ok) break;
             tc_fence_after();
@@ -532,19 +559,20 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefix_attn_kernel(const Prefix
                 mma_bf16_ts(sc, qc + s * 8, b + (s >> 2) * (8192 >> 4) + (s & 3) * 2, IDESC_S, s > 0 ? 1u : 0u);
             }
             mma_commit(&cs.s_full[t]);
+            mma_commit(&cs.k_free[st]);
             if (R == 1 && t == 1 && j == jobs - 1) mma_commit(&cs.q_free);
             ++done;
           }
           if (j > 0) {  // P V of job j - 1
             const uint32_t tile = tc + (R == 2 ? j - 1 : 2 * (j - 1) + t), st = tile % NS, nth = done - (j < jobs ? 2 : 1);
-            ok = mbar_wait(&cs.p_full[t], nth & 1, abort, a.status);
+            ok = mbar_wait(&cs.v_full[st], (tile / NS) & 1, abort, a.status) && mbar_wait(&cs.p_full[t], nth & 1, abort, a.status);
             if (!ok) break;
             tc_fence_after();
             const uint64_t b = dv + st * (C::TILE >> 4);
 #pragma unroll
             for (int s = 0; s < 4; ++s) mma_bf16_ts(oc, pc + s * 8, b + s * 2, IDESC_PV, s > 0 || j > 1 ? 1u : 0u);
             mma_commit(&cs.pv_done[t]);
-            mma_commit(&cs.kv_free[st]);
+            mma_commit(&cs.v_free[st]);
           }
         }
         if (R == 1 && t == 1 && jobs == 0) mma_commit(&cs.q_free);
