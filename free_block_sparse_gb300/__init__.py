@@ -24,6 +24,8 @@ SPARGE_ERR_WORKSPACE_TOO_SMALL = -3
 SPARGE_ERR_CUDA = -4
 SPARGE_ERR_DEVICE_TIMEOUT = -5
 SPARGE_BF16 = 1
+SPARGE_PREFIX_AUTO = 0
+SPARGE_PREFIX_SHARED = 1
 SPARGE_PRECISION_BF16 = 0
 SPARGE_PRECISION_Q8 = 1
 SPARGE_PRECISION_Q8_FP8PV = 2
@@ -137,8 +139,8 @@ EXPORTS = {
     "sparge_cache4_prefix_attn_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int64] * 5),
     "sparge_cache4_prefix_attn": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64,
                                                  ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64, ctypes.c_void_p,
-                                                 ctypes.c_float, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t,
-                                                 ctypes.c_void_p]),
+                                                 ctypes.c_float, ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p,
+                                                 ctypes.c_size_t, ctypes.c_void_p]),
     "sparge_selftest_bounded_wait": (ctypes.c_int, [ctypes.c_int64, ctypes.c_void_p]),
     "sparge_last_error": (ctypes.c_char_p, []),
     "sparge_get_device_status": (ctypes.c_int, [ctypes.c_void_p]),
@@ -593,10 +595,12 @@ def cache4_pages_attn(q, pool, pages, lens, scale: float = 0.0, out=None, ws=Non
     return (_binding_module or _load_binding()).cache4_pages_attn(q, pool, pages, lens, scale, out, ws)
 
 
-def cache4_prefix_attn(q, pool, prefix_pages, table, kv_lens, scale: float = 0.0, out=None, ws=None):
+def cache4_prefix_attn(q, pool, prefix_pages, table, kv_lens, scale: float = 0.0, out=None, ws=None,
+                       path: int = SPARGE_PREFIX_AUTO):
     """cache4_attn for sequences that all begin with the tokens on prefix_pages (int32): those are attended once for the whole
-    batch.  The rows of table hold the prefix's pages too, kv_lens counts its tokens."""
-    return (_binding_module or _load_binding()).cache4_prefix_attn(q, pool, prefix_pages, table, kv_lens, scale, out, ws)
+    batch, or, where path is SPARGE_PREFIX_AUTO and the sizes say that this takes longer, by each sequence.  The rows of table hold
+    the prefix's pages too, kv_lens counts its tokens."""
+    return (_binding_module or _load_binding()).cache4_prefix_attn(q, pool, prefix_pages, table, kv_lens, scale, path, out, ws)
 
 
 def hilbert_perm_2d(n_prefix: int, H: int, W: int) -> np.ndarray:

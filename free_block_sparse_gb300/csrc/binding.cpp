@@ -518,7 +518,7 @@ PyObject *cache4_pages_attn(const Args &a) {
   return result(a, 5, out);
 }
 
-// (q, pool, prefix_pages, table, kv_lens, scale, out, ws)
+// (q, pool, prefix_pages, table, kv_lens, scale, path, out, ws)
 PyObject *cache4_prefix_attn(const Args &a) {
   const at::Tensor &q = a.tensor(0, "q"), &prefix = a.tensor(2, "prefix_pages"), &table = a.tensor(3, "table");
   const Here h(q, "q");
@@ -529,15 +529,16 @@ PyObject *cache4_prefix_attn(const Args &a) {
   const int64_t stride = h.table(table, dq.B);
   const int32_t *lens = static_cast<int32_t *>(h.array(a.tensor(4, "kv_lens"), at::kInt, "kv_lens", {dq.B}));
   const float scale = a.real(5);
-  at::Tensor out = given_rows(a, 6, h, "out"), ws = given_workspace(a, 7, h);
+  const int path = static_cast<int>(a.integer(6));
+  at::Tensor out = given_rows(a, 7, h, "out"), ws = given_workspace(a, 8, h);
   done(unlocked([&] {
     if (!out.defined()) out = h.make_like(q);
     if (!ws.defined()) ws = make_workspace(h, sparge_cache4_prefix_attn_workspace_bytes(dq.B, dq.H, c.H, dq.N, dq.d));
     sparge_tensor o = Here::describe(out);
     return sparge_cache4_prefix_attn(&dq, &c, ids, n, static_cast<const int32_t *>(table.data_ptr()), table.size(1), stride, lens, scale,
-                                     &o, ws.data_ptr(), ws.nbytes(), h.s());
+                                     path, &o, ws.data_ptr(), ws.nbytes(), h.s());
   }));
-  return result(a, 6, out);
+  return result(a, 7, out);
 }
 
 // No C++ exception leaves through Python.
@@ -581,7 +582,7 @@ PyMethodDef methods[] = {ENTRY(window_attn, 8),
                          ENTRY(cache4_bounds_load, 3),
                          ENTRY(cache4_select, 11),
                          ENTRY(cache4_pages_attn, 7),
-                         ENTRY(cache4_prefix_attn, 8),
+                         ENTRY(cache4_prefix_attn, 9),
                          {"set_error", set_error, METH_O, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods};

@@ -895,7 +895,7 @@ size_t sparge_cache4_prefix_attn_workspace_bytes(int64_t B, int64_t Hq, int64_t 
 
 int sparge_cache4_prefix_attn(const sparge_tensor *q, const sparge_cache4 *cache, const int32_t *prefix_pages, int64_t n_prefix,
                               const int32_t *table, int64_t width, int64_t table_stride, const int32_t *kv_lens, float scale,
-                              sparge_tensor *o, void *ws, size_t ws_bytes, sparge_stream_t stream) {
+                              int path, sparge_tensor *o, void *ws, size_t ws_bytes, sparge_stream_t stream) {
   clear_error();
   View qv;
   Cache4 c;
@@ -904,6 +904,8 @@ int sparge_cache4_prefix_attn(const sparge_tensor *q, const sparge_cache4 *cache
   if ((rc = checked_args(q, cache, scale, o, qv, c, a)) || (rc = checked_table(c, width, table_stride))) return rc;
   if (n_prefix < 0 || n_prefix > width)
     return fail(SPARGE_ERR_INVALID_ARG, "n_prefix=%lld pages not in 0..%lld, the table's width", (long long)n_prefix, (long long)width);
+  if (path != SPARGE_PREFIX_AUTO && path != SPARGE_PREFIX_SHARED)
+    return fail(SPARGE_ERR_INVALID_ARG, "path=%d: SPARGE_PREFIX_AUTO or SPARGE_PREFIX_SHARED", path);
   if (n_prefix && !prefix_pages) return fail(SPARGE_ERR_INVALID_ARG, "prefix_pages is NULL");
   if (qv.B * a.G * qv.N > INT_MAX / 2) return fail(SPARGE_ERR_UNSUPPORTED, "too many query rows");
   if ((rc = set_split(a, qv.B, qv.N, qv.d, ws, ws_bytes))) return rc;
@@ -919,7 +921,7 @@ int sparge_cache4_prefix_attn(const sparge_tensor *q, const sparge_cache4 *cache
   const int d = static_cast<int>(qv.d), per = c.page_size / 16;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e;
-  if (n_prefix == 0) {
+  if (n_prefix == 0 || (path == SPARGE_PREFIX_AUTO && !prefix_shared(qv.B, a.rows, c.H, d, n_prefix * per))) {
     e = run_cache_attn(static_cast<const CacheAttnArgs &>(a), d, width * per, s);
     return e == cudaSuccess ? SPARGE_OK : cuda_fail(e, "cache attention launch");
   }

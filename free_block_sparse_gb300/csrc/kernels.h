@@ -236,6 +236,7 @@ struct PrefixAttn {
   int *status;
 };
 size_t prefix_ws_bytes(int64_t rows, int64_t Hkv, int64_t d);
+bool prefix_shared(int64_t B, int64_t rows, int64_t Hkv, int64_t d, int64_t recs);
 cudaError_t launch_prefix_attn(const PrefixAttn &l, const SplitArgs &own, cudaStream_t st);
 cudaError_t launch_prefix_combine(const PrefixAttn &l, const SplitArgs &own, cudaStream_t st);
 

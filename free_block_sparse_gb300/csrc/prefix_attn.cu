@@ -1,6 +1,7 @@
 // Attention of a whole batch over a prefix that its sequences share, from the paged 4-bit cache, on tcgen05 tensor cores.
 #include <climits>
 #include <cmath>
+#include <type_traits>
 
 #include <cuda_fp16.h>
 
@@ -13,12 +14,15 @@
 namespace sparge {
 namespace {
 
-// Warps: softmax (4 per stream, a row a thread), widening (two groups of 4 that take turns), products (one per stream), loads.
-constexpr int PF_SOFT = 8, PF_WIDE = 8, PF_PROD = PF_SOFT + PF_WIDE, PF_LOAD = PF_PROD + 2;
-constexpr int PF_THREADS = (PF_LOAD + 1) * 32;
-constexpr int PF_ROWS = 256;             // rows of a slot: two streams of 128
-constexpr float PF_RESCALE = 8.f;
-constexpr float PF_TOP = 15.f;           // P' stays below 2^15, within f16
+// Warps: softmax (4 per stream, a row a thread), widening (groups of four that take turns over the tiles), products (one per
+// stream), loads, powers of two: the registers are dealt out by groups of four.
+constexpr int PF_SOFT = 8, PF_WIDE = 4, PF_TEAMS = 1, PF_PROD = PF_SOFT + PF_TEAMS * PF_WIDE, PF_LOAD = PF_PROD + 2;
+constexpr int PF_THREADS = (PF_PROD + 4) * 32;
+constexpr int PF_REGS = 65536 / PF_THREADS / 8 * 8;  // a thread's at launch
+constexpr int PF_SOFT_REGS = 152, PF_WIDE_REGS = 120, PF_REST_REGS = 88;
+static_assert(PF_SOFT * PF_SOFT_REGS + PF_TEAMS * PF_WIDE * PF_WIDE_REGS + 4 * PF_REST_REGS <= PF_REGS * PF_THREADS / 32, "registers");
+constexpr int PF_ROWS = 256;     // rows of a slot: two streams of 128
+constexpr float PF_TOP = 15.f;   // the references move when a P or a P' passes 2^15, the last power of two within f16
 
 struct PrefixArgs {
   const __nv_bfloat16 *q;
@@ -29,7 +33,7 @@ struct PrefixArgs {
   int rec_shift, recs, tiles;       // records of a page (1 << rec_shift), of the prefix; 64-token tiles
   int Hkv, G, Nq, rows, groups;     // rows of a KV head: B G Nq; groups of them: items of a KV head
   float scale_log2;
-  float *part_o, *part_ml;          // [CTA + item][256][D], [CTA + item][256] (reference, sum)
+  float *part_o, *part_ml;          // [CTA + item][D / 32][256][32], [CTA + item][256] (reference, sum)
   int *status;
 };
 
@@ -42,24 +46,23 @@ struct PfCfg {
   static constexpr int RS = 6, NS = R == 2 ? 3 : 4;  // stages of raw tiles, of widened ones: of K, and of V
   static constexpr bool QSMEM = D == 128 && R == 2;  // no room in TMEM for two tiles of Q
   static constexpr uint32_t TILE = 64 * D * 2;       // of K or V, f16
-  static constexpr uint32_t K = 0, V = K + NS * TILE, Q = V + NS * TILE, RING = Q + (QSMEM ? 2 * 128 * D * 2 : 0);
-  static constexpr uint32_t TABK = RING + RS * RAW, TABV = TABK + 4 * 64 * 16, CTRL = TABV + 4 * 512;
-  static constexpr uint32_t SMEM = CTRL + 1024;
+  static constexpr uint32_t OUT = 128 * 32 * 4;      // 32 channels of a stream's O on their way out; over its Q where that lies here
+  static constexpr uint32_t K = 0, V = K + NS * TILE, Q = V + NS * TILE, QB = QSMEM ? 128 * D * 2 : OUT, RING = Q + 2 * QB;
+  static constexpr uint32_t CTRL = RING + RS * RAW, SMEM = CTRL + 1024;
   // TMEM columns
   static constexpr uint32_t O = 0, S = 2 * D, P = S + 128, QC = P + 64, QCOLS = D / 2;
   static_assert(QC + (QSMEM ? 0 : R) * QCOLS <= 512, "TMEM");
   static_assert(SMEM <= 227 * 1024, "shared memory");
 };
-struct PfInfo {  // of a widened tile: K = K' k_unit, V = V' 2^g; bit r of missing: record r is not there
-  float k_unit;
-  int g;
-  uint32_t missing;
+// What goes with a tile: K = K' 2^-kf, V = V' 2^-vf; bit r of missing: its record r is not there.
+struct alignas(16) PfInfo {
+  int kf, vf;
+  uint32_t missing, pad;
 };
 struct PfCtrl {
-  uint64_t raw_full[8], raw_free[8], k_full[4], k_free[4], v_full[4], v_free[4];
+  PfInfo info[16];  // (tile % 16: a tile that far behind has been turned into P)
+  uint64_t raw_full[8], raw_free[8], info_full[8], k_full[4], k_free[4], v_full[4], v_free[4];
   uint64_t q_full[2], q_free, s_full[2], s_free[2], p_full[2], pv_done[2], drained[2];
-  PfInfo info[8];  // (tile % 8: K's stage is free again before the softmax has read what goes with it)
-  int need[4][4];  // of a tile (tile % 4): K by warps 0 and 1 of its group, V by 2 and 3
   uint8_t bad[8][4];
   uint32_t tmem;
   int abort, no_abort;
@@ -71,6 +74,17 @@ __device__ __forceinline__ void pf_bulk_load(void *dst, const void *src, uint32_
                    smem_u32(dst)),
                "l"(src), "r"(bytes), "r"(smem_u32(bar))
                : "memory");
+}
+__device__ __forceinline__ void pf_bulk_store(void *dst, uint32_t src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void pf_more_regs() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void pf_fewer_regs() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 __device__ __forceinline__ float pf_pow2(int e) { return __int_as_float((e + 127) << 23); }  // e in -126..127
 __device__ __forceinline__ int pf_exponent(float x) { return static_cast<int>((__float_as_uint(x) >> 23) & 0xFFu) - 127; }
@@ -92,6 +106,29 @@ __device__ __forceinline__ uint32_t pf_sixteenth2(uint32_t a) {
 __device__ __forceinline__ void pf_sts128(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
+__device__ __forceinline__ uint4 pf_lds128(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+  return v;
+}
+// tcgen05.wait::ld that the loaded registers pass through, so nothing that uses them moves in front of it.
+__device__ __forceinline__ void pf_ld_wait_for(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+                 "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]),
+                 "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]),
+                 "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
+}
+__device__ __forceinline__ void pf_ld_wait_for(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+                 "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
+}
+
 __device__ __forceinline__ void pf_ld_wait_for(uint32_t (&r)[32], float &m) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
                : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
@@ -101,6 +138,13 @@ __device__ __forceinline__ void pf_ld_wait_for(uint32_t (&r)[32], float &m) {
                :
                : "memory");
 }
+// What a tile's power of two f has to keep to, from a word of its: f <= -need, so that a code's 2^-24 code * s 2^(f + 24) is within
+// f16 and the value below 2^15.  (A scale or minimum that is not finite makes its own values NaN and counts for nothing here.)
+__device__ __forceinline__ int pf_need(uint32_t word) {
+  const int s = (word >> 7) & 0xFF, m = (word >> 23) & 0xFF;
+  return max(s, m) == 255 ? -200 : max(s + 9, m - 13) - 127;
+}
+__device__ __forceinline__ int pf_power(int need) { return min(max(-need, -126), 100); }
 
 // A CTA's share of the line of all items' tiles, and its pieces: item, first tile, tiles.
 struct PfShare {
@@ -137,15 +181,17 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefix_attn_kernel(const Prefix
   PfCtrl &cs = *reinterpret_cast<PfCtrl *>(smem + C::CTRL);
   volatile int *abort = &cs.abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t base = smem_u32(smem);
   if (threadIdx.x == 0) {
     for (int s = 0; s < RS; ++s) {
       mbar_init(&cs.raw_full[s], 4);
-      mbar_init(&cs.raw_free[s], 4);
+      mbar_init(&cs.raw_free[s], PF_WIDE);
+      mbar_init(&cs.info_full[s], 1);
     }
     for (int s = 0; s < NS; ++s) {
-      mbar_init(&cs.k_full[s], 4);
+      mbar_init(&cs.k_full[s], PF_WIDE);
       mbar_init(&cs.k_free[s], R);
-      mbar_init(&cs.v_full[s], 4);
+      mbar_init(&cs.v_full[s], PF_WIDE);
       mbar_init(&cs.v_free[s], R);
     }
     for (int t = 0; t < 2; ++t) {
@@ -154,9 +200,8 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefix_attn_kernel(const Prefix
       mbar_init(&cs.s_free[t], 4);
       mbar_init(&cs.p_full[t], 4);
       mbar_init(&cs.pv_done[t], 1);
+      mbar_init(&cs.drained[t], 1);
     }
-    mbar_init(&cs.drained[0], 1);
-    mbar_init(&cs.drained[1], 1);
     mbar_init(&cs.q_free, 1);
     cs.abort = 0;
     cs.no_abort = 0;
@@ -180,353 +225,344 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefix_attn_kernel(const Prefix
     const int t = warp >> 2, row = (warp & 3) * 32 + lane;
     const uint32_t tl = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const uint32_t oc = tl + C::O + t * D, sc = tl + C::S + t * 64, pc = tl + C::P + t * 32;
-    uint32_t done = 0, piece = 0;  // jobs of this stream so far, pieces
+    const uint32_t qb = base + C::Q + t * C::QB;  // the stream's Q or, at a piece's end, its O
+    uint32_t done = 0, piece = 0;                 // jobs of this stream so far, pieces
     bool ok = true;
-    for (; ok && share.next(a, item, tile0, n); ++piece) {
-      // ---- the row's queries: f16, times a power of two that takes its maximum to [2^14, 2^15) ----
+    for (; share.next(a, item, tile0, n); ++piece) {
       const int kvh = item / a.groups, r = (item % a.groups) * (128 * R) + (R == 2 ? t * 128 : 0) + row;
-      float rm = 0.f;  // 2^(e - 14) scale: what a product of the scaled row counts
+      const bool live = r - lane < a.rows;  // a warp past the last row takes part in the waits alone
+      // ---- the row's queries: to their place as they are, then in place f16, times a power of two that takes the maximum to [2^14, 2^15),
+      // in each 8 channels in the order 0 4 1 5 2 6 3 7, in which the codes' words give them ----
+      float rm;  // 2^(e - 14) scale: what a product of the scaled row counts
       {
+        if (R == 1 && t == 0 && piece > 0) {  // the other stream's products with the rows before these have been made (this one's have)
+          ok = __all_sync(0xffffffffu, mbar_wait(&cs.q_free, (piece - 1) & 1, abort, a.status));
+          if (bar_red_or(1 + t, 128, !ok)) {  // (all four warps leave, or none)
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+        }
+        const bool keep = R == 2 || t == 0;  // (the second stream of one row tile wants the power alone)
+        const uint32_t qc = tl + C::QC + (R == 2 ? t * C::QCOLS : 0);
         const int b = r / (a.G * a.Nq), rr = r % (a.G * a.Nq);
         const uint4 *src = reinterpret_cast<const uint4 *>(a.q + b * a.q_sb + (kvh * a.G + rr / a.Nq) * a.q_sh +
                                                            static_cast<int64_t>(rr % a.Nq) * a.q_sn);
+        auto place = [&](int i) { return qb + (i / 8) * 16384 + row * 128 + (((i & 7) ^ (row & 7)) << 4); };
         float mx = 0.f;
-#pragma unroll 1
-        for (int i = 0; i < D / 8; i += 4) {
-          uint4 v[4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) v[k] = r < a.rows ? src[i + k] : make_uint4(0u, 0u, 0u, 0u);
+        for (int i = 0; i < D / 8; i += 8) {
+          uint4 v[8];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
+          for (int k = 0; k < 8; ++k) v[k] = r < a.rows ? src[i + k] : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
             const uint32_t u[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
 #pragma unroll
             for (int x = 0; x < 4; ++x) mx = fmaxf(mx, fmaxf(fabsf(bf16lo(u[x])), fabsf(bf16hi(u[x]))));
+          }
+          if (keep) {
+            if (C::QSMEM) {
+#pragma unroll
+              for (int k = 0; k < 8; ++k) pf_sts128(place(i + k), v[k].x, v[k].y, v[k].z, v[k].w);
+            } else {
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                uint32_t w[16];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  w[4 * k] = v[4 * h + k].x;
+                  w[4 * k + 1] = v[4 * h + k].y;
+                  w[4 * k + 2] = v[4 * h + k].z;
+                  w[4 * k + 3] = v[4 * h + k].w;
+                }
+                tmem_st16(qc + 4 * i + 16 * h, w);
+              }
+            }
           }
         }
         const int e = min(max(pf_exponent(mx), -100), 116);
         const float f = pf_pow2(14 - e);
         rm = a.scale_log2 * pf_pow2(e - 14);
-        // in each 8 channels the order 0 4 1 5 2 6 3 7, in which the codes' words give them
-        if (R == 2 || t == 0) {
-          // the other stream's products with the rows before these have been made (this one's have: its O is complete)
-          if (R == 1 && piece > 0) {
-            ok = __all_sync(0xffffffffu, mbar_wait(&cs.q_free, (piece - 1) & 1, abort, a.status));
-            if (!ok) break;
-            tc_fence_after();
-          }
+        auto scaled = [&](uint4 u) {
+          return make_uint4(pf_half2(bf16lo(u.x) * f, bf16lo(u.z) * f), pf_half2(bf16hi(u.x) * f, bf16hi(u.z) * f),
+                            pf_half2(bf16lo(u.y) * f, bf16lo(u.w) * f), pf_half2(bf16hi(u.y) * f, bf16hi(u.w) * f));
+        };
+        if (keep) {
+          if (C::QSMEM) {
+#pragma unroll 4
+            for (int i = 0; i < D / 8; ++i) {
+              const uint4 u = scaled(pf_lds128(place(i)));
+              pf_sts128(place(i), u.x, u.y, u.z, u.w);
+            }
+          } else {
+            tmem_st_wait();
 #pragma unroll 1
-          for (int i = 0; i < D / 8; i += 4) {
-            uint4 v[4];
+            for (int i = 0; i < D / 2; i += 16) {
+              uint32_t w[16];
+              tmem_ld16(qc + i, w);
+              pf_ld_wait_for(w);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) v[k] = r < a.rows ? src[i + k] : make_uint4(0u, 0u, 0u, 0u);
-            uint32_t w[16];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const uint4 u = v[k];
-              w[4 * k] = pf_half2(bf16lo(u.x) * f, bf16lo(u.z) * f);
-              w[4 * k + 1] = pf_half2(bf16hi(u.x) * f, bf16hi(u.z) * f);
-              w[4 * k + 2] = pf_half2(bf16lo(u.y) * f, bf16lo(u.w) * f);
-              w[4 * k + 3] = pf_half2(bf16hi(u.y) * f, bf16hi(u.w) * f);
+              for (int k = 0; k < 16; k += 4) {
+                const uint4 u = scaled(make_uint4(w[k], w[k + 1], w[k + 2], w[k + 3]));
+                w[k] = u.x;
+                w[k + 1] = u.y;
+                w[k + 2] = u.z;
+                w[k + 3] = u.w;
+              }
+              tmem_st16(qc + i, w);
             }
-            if (C::QSMEM) {
-              const uint32_t at = smem_u32(smem) + C::Q + t * (128 * D * 2) + (i / 8) * 16384 + row * 128;
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                pf_sts128(at + ((((i & 7) + k) ^ (row & 7)) << 4), w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
-            } else {
-              tmem_st16(tl + C::QC + (R == 2 ? t * C::QCOLS : 0) + 4 * i, w);
-            }
+            tmem_st_wait();
           }
-          tmem_st_wait();
           fence_proxy_async_smem();
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&cs.q_full[t]);
         }
       }
-      float m_ref = -INFINITY, l = 0.f;
-      int G = 0;  // O counts 2^G
-      const bool live = r - lane < a.rows;  // a warp past the last row takes part in the waits alone
-      // columns 8 c + 4 r + i of a half are tokens of its record r: those that are not there are hidden; the others' maximum
-      auto hide = [](uint32_t (&x)[32], uint32_t gone) {
-        float m = -INFINITY;
-#pragma unroll
-        for (int k = 0; k < 32; ++k) {
-          if ((gone >> ((k >> 2) & 1)) & 1u) x[k] = 0xFF800000u;
-          m = fmaxf(m, __uint_as_float(x[k]));
-        }
-        return m;
-      };
+      // m: the reference of l = sum of P, P = 2^(x - m); ref: that of O = sum of P' V', P' = 2^(x + g - ref).  Both are set to the
+      // largest that the row sees when a term passes 2^15 of them; what the sums hold is then scaled down.  So neither an improbable token
+      // nor the size of V in another record takes bits from the rest.
+      float m = -INFINITY, ref = -INFINITY, l = 0.f;
       const int jobs = R == 2 ? n : (n - t + 1) / 2;
       for (int j = 0; j < jobs; ++j, ++done) {
         const uint32_t tile = tc + (R == 2 ? j : 2 * j + t), st = tile % NS;
-        ok = mbar_wait(&cs.v_full[st], (tile / NS) & 1, abort, a.status) && mbar_wait(&cs.s_full[t], done & 1, abort, a.status);
+        // (V's barrier is what orders the reads of the tile's powers)
+        ok = mbar_wait(&cs.s_full[t], done & 1, abort, a.status);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
-        // 32 columns are held at a time; the others are read for their maximum now and once more for their turn
-        uint32_t v[32];
-        float mx = -INFINITY, m1;
-        const float mult = rm * cs.info[tile & 7].k_unit;
-        const int g = cs.info[tile & 7].g;
-        const uint32_t missing = cs.info[tile & 7].missing;
+        uint32_t v[2][32];
+        float mh[2];
         if (live) {
-          tmem_ld32_max(sc + 32, v, m1);
-          pf_ld_wait_for(v, m1);
-          if (missing) m1 = hide(v, missing >> 2);
-          tmem_ld32_max(sc, v, mx);
-          pf_ld_wait_for(v, mx);
-          if (missing) mx = hide(v, missing);
-          mx = fmaxf(mx, m1) * mult;
+          tmem_ld32_max(sc, v[0], mh[0]);
+          tmem_ld32_max(sc + 32, v[1], mh[1]);
+          pf_ld_wait_for(v[0], mh[0]);
+          pf_ld_wait_for(v[1], mh[1]);
+          tc_fence_before();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&cs.s_free[t]);
+        ok = mbar_wait(&cs.v_full[st], (tile / NS) & 1, abort, a.status);
+        const PfInfo info = cs.info[tile & 15];
+        if (info.missing && live) {  // columns 32 h + 8 c + 4 r + i are tokens of record 2 h + r
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            mh[h] = -INFINITY;
+#pragma unroll
+            for (int k = 0; k < 32; ++k) {
+              if ((info.missing >> (2 * h + ((k >> 2) & 1))) & 1u) v[h][k] = 0xFF800000u;
+              mh[h] = fmaxf(mh[h], __uint_as_float(v[h][k]));
+            }
+          }
         }
         if (j > 0) {  // the product before this one has read its P and added to O
-          ok = __all_sync(0xffffffffu, mbar_wait(&cs.pv_done[t], (done - 1) & 1, abort, a.status));
-          if (!ok) break;
-          tc_fence_after();
+          ok = ok && mbar_wait(&cs.pv_done[t], (done - 1) & 1, abort, a.status);
         }
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
         if (live) {
-          if (m_ref == -INFINITY) G = g;
-          const bool resc = mx > m_ref + PF_RESCALE || mx - m_ref + static_cast<float>(g - G) > PF_TOP;
-          if (__any_sync(0xffffffffu, resc)) {
+          const float mult = fminf(fmaxf(rm * pf_pow2(-info.kf), 0x1p-126f), 0x1p127f);  // (no 0 times -inf, no infinity times 0)
+          const float g = static_cast<float>(-info.vf);
+          const float xm = fmaxf(mh[0], mh[1]) * mult, ym = xm + g;
+          const bool move = xm > m + PF_TOP || ym > ref + PF_TOP;
+          bool tiny = (ref - m) - g > 60.f;  // V of this tile is so small beside what O holds that P' says nothing of P
+          if (__any_sync(0xffffffffu, move || tiny)) {
             float f = 1.f;
-            if (resc) {
-              const float to = fmaxf(m_ref, mx), al = fast_exp2(m_ref - to);
-              // O's unit follows: this tile's, or what the sums before need
-              const int Gn = m_ref == -INFINITY ? g : max(g, __float2int_ru(fmaxf(static_cast<float>(G) + (m_ref - to), -1000.f)));
-              f = al * pf_pow2(min(max(G - Gn, -126), 127));
-              l *= al;
-              m_ref = to;
-              G = Gn;
+            if (move) {
+              const float mn = fmaxf(m, xm), rn = fmaxf(ym, ref);
+              l *= m == -INFINITY ? 0.f : fast_exp2(m - mn);
+              f = ref == -INFINITY ? 0.f : fast_exp2(ref - rn);
+              m = mn;
+              ref = rn;
             }
+            tiny = __any_sync(0xffffffffu, (ref - m) - g > 60.f);
             if (j > 0) {
 #pragma unroll 1
               for (int q = 0; q < D / 16; ++q) {
                 uint32_t o[16];
                 tmem_ld16(oc + 16 * q, o);
-                tmem_ld_wait();
+                pf_ld_wait_for(o);
 #pragma unroll
                 for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
                 tmem_st16(oc + 16 * q, o);
               }
             }
           }
-          // P' = 2^(x - m_ref + g - G); a row whose reference is still -inf has only hidden columns (or NaN)
-          const int up = G - g;
-          const float nref = m_ref == -INFINITY ? 0.f : -m_ref;
-          const bool tiny = __any_sync(0xffffffffu, up > 60);  // V of this tile beside what O holds: the sum of P goes by itself
-          const float2 m2 = make_float2(mult, mult), nr2 = make_float2(nref - static_cast<float>(up), nref - static_cast<float>(up));
-          float2 rs[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll 1
-          for (int h = 0; h < 2; ++h) {
-            if (h == 1) {
-              tmem_ld32_max(sc + 32, v, m1);
-              pf_ld_wait_for(v, m1);
-              if (missing) hide(v, missing >> 2);
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(&cs.s_free[t]);
-            }
-            if (tiny) {
-              float sum = 0.f;
+          // (a row whose references are still -inf has only hidden columns, or NaN)
+          const bool none = ref == -INFINITY;
+          const float nr = none ? 0.f : g - ref, back = none ? 0.f : (ref - m) - g;  // P' = 2^(x + nr), P = P' 2^back
+          const float2 m2 = make_float2(mult, mult), n2 = make_float2(nr, nr);
+          float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-              for (int k = 0; k < 32; ++k) sum += fast_exp2(fmaf(__uint_as_float(v[k]), mult, nref));
-              l += sum;
-            }
+          for (int h = 0; h < 2; ++h) {
             uint32_t pk[16];
 #pragma unroll
             for (int k = 0; k < 16; ++k) {
-              const float2 e2 = ffma2(make_float2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])), m2, nr2);
+              const float2 e2 = ffma2(make_float2(__uint_as_float(v[h][2 * k]), __uint_as_float(v[h][2 * k + 1])), m2, n2);
               const float2 p2 = make_float2(fast_exp2(e2.x), fast_exp2(e2.y));
-              rs[k & 1] = fadd2(rs[k & 1], p2);
+              sum[k & 1] = fadd2(sum[k & 1], p2);
               pk[k] = pack_f16x2(p2.x, p2.y);
             }
             tmem_st16(pc + 16 * h, pk);
           }
-          const float2 sum = fadd2(rs[0], rs[1]);
-          if (!tiny) l = fmaf(sum.x + sum.y, pf_pow2(max(up, -126)), l);
           tmem_st_wait();
-        } else if (lane == 0) {
-          mbar_arrive(&cs.s_free[t]);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&cs.p_full[t]);
+          if (tiny) {
+            float s = 0.f;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+              for (int k = 0; k < 32; ++k) s += fast_exp2(fmaf(__uint_as_float(v[h][k]), mult, none ? 0.f : -m));
+            l += s;
+          } else {
+            const float2 s2 = fadd2(sum[0], sum[1]);
+            l = fmaf(s2.x + s2.y, fast_exp2(back), l);
+          }
+        } else {
+          if (lane == 0) mbar_arrive(&cs.p_full[t]);
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&cs.p_full[t]);
       }
-      if (!ok) break;
-      // ---- the piece's end: O (times 2^G), the reference and the sum ----
-      if (jobs > 0) {
+      // ---- the piece's end: O against m, 32 channels of the stream's rows at a time through shared memory, then the references and
+      // sums.  (The four warps leave together if one's wait gave up.) ----
+      if (ok && jobs > 0) {
         ok = __all_sync(0xffffffffu, mbar_wait(&cs.pv_done[t], (done - 1) & 1, abort, a.status));
-        if (!ok) break;
         tc_fence_after();
       }
-      const int64_t at = (static_cast<int64_t>(blockIdx.x) + item) * PF_ROWS + t * 128 + row;
-      if (r < a.rows) *reinterpret_cast<float2 *>(a.part_ml + 2 * at) = make_float2(m_ref, l);
-      if (jobs > 0 && live) {
-        const float back = pf_pow2(min(max(G, -126), 127));
-        float *to = a.part_o + at * D;
+      if (bar_red_or(1 + t, 128, !ok)) {
+        ok = false;
+        break;
+      }
+      const int64_t slot = static_cast<int64_t>(blockIdx.x) + item;
+      if (r < a.rows) *reinterpret_cast<float2 *>(a.part_ml + 2 * (slot * PF_ROWS + t * 128 + row)) = make_float2(m, l);
+      if (jobs > 0) {
+        const float back = ref == -INFINITY ? 1.f : fast_exp2(ref - m);
 #pragma unroll 1
-        for (int q = 0; q < D / 16; ++q) {
-          uint32_t o[16];
-          tmem_ld16(oc + 16 * q, o);
-          tmem_ld_wait();
-          if (r < a.rows) {
+        for (int q = 0; q < D / 32; ++q) {
+          if (live) {
+            uint32_t o[32];
+            tmem_ld32(oc + 32 * q, o);
+            pf_ld_wait_for(o);
 #pragma unroll
-            for (int k = 0; k < 16; k += 4)
-              *reinterpret_cast<float4 *>(to + 16 * q + k) =
-                  make_float4(__uint_as_float(o[k]) * back, __uint_as_float(o[k + 1]) * back, __uint_as_float(o[k + 2]) * back,
-                              __uint_as_float(o[k + 3]) * back);
+            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * back);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) pf_sts128(qb + row * 128 + ((k ^ (row & 7)) << 4), o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
           }
+          fence_proxy_async_smem();
+          bar_sync(1 + t, 128);
+          if ((threadIdx.x & 127) == 0) {
+            pf_bulk_store(a.part_o + ((slot * (D / 32) + q) * PF_ROWS + t * 128) * 32, qb, C::OUT);
+            bulk_commit();
+            bulk_wait_read_all();
+          }
+          bar_sync(1 + t, 128);
         }
         tc_fence_before();
       }
       tc += n;
     }
+    if ((threadIdx.x & 127) == 0) bulk_wait_all();
   } else if (warp < PF_PROD) {
     // ------------------------------------ widening: codes to f16 tiles ------------------------------------
-    // A tile's power of two for K and the one for V follow from the words of all its tokens.  The words of the group's next tiles are
-    // looked at, and the next table is made, around the widening of the one in front, so that one barrier a tile is enough.
-    const int w4 = warp & 3, tid = w4 * 32 + lane, group = (warp - PF_SOFT) >> 2;
-    const int side = tid >> 6, rec = (tid >> 4) & 3, tk = tid & 15;  // this thread's token and side in words and tables
-    const uint32_t base = smem_u32(smem);
-    float s[NG], m[NG];  // its words of the tile behind
-    bool ok = true;
-    auto words = [&](uint32_t tile) {
-      const uint32_t rs = tile % RS;
-      // (a warp whose wait gives up goes on to the next barrier, where all four leave together)
-      ok = __all_sync(0xffffffffu, mbar_wait(&cs.raw_full[rs], (tile / RS) & 1, abort, a.status)) && ok;
-      const bool gone = cs.bad[rs][rec] != 0;
-      const uint8_t *at = smem + C::RING + rs * C::RAW + rec * C::PITCH + (side ? Rec::VW : Rec::KW) + tk * NG * 4;
-      int need = -200;  // f <= -need: code * 2^-24 s 2^(f + 24) is within f16, and so is the value
-#pragma unroll
-      for (int g = 0; g < NG; ++g) {
-        const uint32_t word = *reinterpret_cast<const uint32_t *>(at + 4 * g);
-        s[g] = gone ? 0.f : bf16lo(word);
-        m[g] = gone ? 0.f : bf16hi(word);
-        if (fabsf(s[g]) < INFINITY && fabsf(m[g]) < INFINITY)
-          need = max(need, max(pf_exponent(s[g]) + 9, max(pf_exponent(m[g]), pf_exponent(fmaf(15.f, s[g], m[g]))) - 14));
-      }
-      need = __reduce_max_sync(0xffffffffu, need);
-      if (lane == 0) cs.need[tile & 3][w4] = need;
-    };
-    int fk = 0, fv = 0;
-    auto table = [&](uint32_t tile) {
-      const int *need = cs.need[tile & 3];
-      fk = min(max(-max(need[0], need[1]), -126), 100);
-      fv = min(max(-max(need[2], need[3]), -126), 100);
-      const int f = side ? fv : fk;
-      const float fs = pf_pow2(f + 24), fm = pf_pow2(f);
-      const int pos = 32 * (rec >> 1) + 8 * ((tk & 7) >> 1) + 4 * (rec & 1) + 2 * (tk >> 3) + (tk & 1);
-      uint8_t *tk_ = smem + C::TABK + (tile & 3) * 1024, *tv = smem + C::TABV + (tile & 3) * 512;
-#pragma unroll
-      for (int g = 0; g < NG; ++g) {
-        const uint32_t ss = pf_half2(s[g] * fs, s[g] * fs), mm = pf_half2(m[g] * fm, m[g] * fm);
-        if (side) {
-          *reinterpret_cast<uint16_t *>(tv + (g * 64 + pos) * 2) = static_cast<uint16_t>(ss);
-          *reinterpret_cast<uint16_t *>(tv + 256 + (g * 64 + pos) * 2) = static_cast<uint16_t>(mm);
-        } else {
-          *reinterpret_cast<uint2 *>(tk_ + pos * 16 + g * 8) = make_uint2(ss, mm);
-        }
-      }
-    };
-    auto all_ok = [&]() { return ok = !bar_red_or(1 + group, 128, !ok); };
+    // K and V have stages of their own, so that K's is free with the scores, and V's is not held while they are turned into P.
+    const int w4 = warp & 3;
     const uint32_t total = static_cast<uint32_t>(share.end - share.at);  // tiles of all the CTA's pieces
-    const uint32_t tile0 = group;  // the group takes every second tile
-    if (tile0 < total) {
-      words(tile0);
-      if (all_ok()) {
-        table(tile0);
-        if (tile0 + 2 < total) words(tile0 + 2);
-      }
-    }
-    for (uint32_t tile = tile0; tile < total; tile += 2) {
+    for (uint32_t tile = (warp - PF_SOFT) >> 2; tile < total; tile += PF_TEAMS) {
+      const uint32_t rs = tile % RS, st = tile % NS;
+      bool ok = mbar_wait(&cs.info_full[rs], (tile / RS) & 1, abort, a.status) && mbar_wait(&cs.raw_full[rs], (tile / RS) & 1, abort, a.status);
+      if (tile >= NS) ok = ok && mbar_wait(&cs.v_free[st], (tile / NS - 1) & 1, abort, a.status);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      const uint8_t *raw = smem + C::RING + rs * C::RAW;
+      const PfInfo info = cs.info[tile & 15];
+      const int pk = w4 & 1;  // the pair of records whose K this warp takes
+      // ---- K: a lane takes the codes of 8-channel piece c of every 32 channels of a token ----
       {
-        const uint32_t rs = tile % RS, st = tile % NS;
-        if (tile >= NS) ok = __all_sync(0xffffffffu, mbar_wait(&cs.k_free[st], (tile / NS - 1) & 1, abort, a.status)) && ok;
-        const int k_is = fk, v_is = fv;
-        if (!all_ok()) break;  // this tile's table and the next one's powers are there
-        const uint8_t *raw = smem + C::RING + rs * C::RAW;
-        const uint8_t *tabk = smem + C::TABK + (tile & 3) * 1024, *tabv = smem + C::TABV + (tile & 3) * 512;
-        if (tid == 0) {
-          PfInfo &i = cs.info[tile & 7];
-          i.k_unit = pf_pow2(-k_is);
-          i.g = -v_is;
-          i.missing = cs.bad[rs][0] | (cs.bad[rs][1] << 1) | (cs.bad[rs][2] << 2) | (cs.bad[rs][3] << 3);
+        const int c = lane & 3, r = (lane >> 2) & 1;
+        const int f = info.kf;
+        const bool there = !((info.missing >> (2 * pk + r)) & 1u);
+        const float fs = there ? pf_pow2(f + 24) : 0.f, fm = there ? pf_pow2(f) : 0.f;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int t = ((w4 >> 1) + 2 * k) * 4 + (lane >> 3);
+          const int pos = 32 * pk + 8 * ((t & 7) >> 1) + 4 * r + 2 * (t >> 3) + (t & 1);
+          const uint8_t *from = raw + (2 * pk + r) * C::PITCH, *src = from + Rec::K + t * (D / 2) + c * (D / 8);
+          uint32_t code[2 * NG], word[NG];
+          if constexpr (D == 128) {
+            const uint4 u = *reinterpret_cast<const uint4 *>(src);
+            const uint2 x = *reinterpret_cast<const uint2 *>(from + Rec::KW + t * 8);
+            code[0] = u.x; code[1] = u.y; code[2] = u.z; code[3] = u.w;
+            word[0] = x.x; word[1] = x.y;
+          } else {
+            const uint2 u = *reinterpret_cast<const uint2 *>(src);
+            code[0] = u.x; code[1] = u.y;
+            word[0] = *reinterpret_cast<const uint32_t *>(from + Rec::KW + t * 4);
+          }
+          const uint32_t to = base + C::K + st * C::TILE + pos * 128;
+#pragma unroll
+          for (int w = 0; w < 2 * NG; ++w) {
+            const float sf = there ? bf16lo(word[w / 2]) * fs : 0.f, mf = there ? bf16hi(word[w / 2]) * fm : 0.f;
+            const uint32_t lo = pf_half2(sf, sf), hi = pf_sixteenth2(lo), m = pf_half2(mf, mf), u = code[w], u8 = u >> 8;
+            pf_sts128(to + (w >> 1) * 8192 + (((4 * (w & 1) + c) ^ (pos & 7)) << 4), pf_hfma2(u & 0x000F000Fu, lo, m),
+                      pf_hfma2(u & 0x00F000F0u, hi, m), pf_hfma2(u8 & 0x000F000Fu, lo, m), pf_hfma2(u8 & 0x00F000F0u, hi, m));
+          }
         }
-        if (tile + 2 < total) table(tile + 2);
-        // ---- K: a lane takes the codes of 8-channel piece c of every 32 channels of a token ----
-        {
-          const int c = lane & 3, r = (lane >> 2) & 1;
+      }
+      // ---- V, transposed: lane 4 g + c holds channels g and g + 8 of every 16 for tokens 2c, 2c + 1, 2c + 8, 2c + 9 of two records ----
+      {
+        const int g = lane >> 2, c = lane & 3;
+        constexpr int NU = 2 * NG;  // words of a warp: d = 128: a half of the channels and a pair of records; d = 64: a quarter
+        const int part = D == 128 ? w4 >> 1 : 0, u0 = D == 128 ? 0 : 2 * (w4 >> 1), pr = (w4 & 1) ^ (g & 1);
+        uint32_t ss[4], sh[4], mm[4], code[2][NU];  // of tokens (2c, 2c + 1) and (2c + 8, 2c + 9) of either record
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const uint8_t *from = raw + (2 * pr + r) * C::PITCH, *src = from + Rec::V + part * 512 + 16 * lane + 4 * u0;
+          const int f = info.vf;
+          const bool there = !((info.missing >> (2 * pr + r)) & 1u);
+          const float fs = pf_pow2(f + 24), fm = pf_pow2(f);
+          if constexpr (NU == 4) {
+            const uint4 u = *reinterpret_cast<const uint4 *>(src);
+            code[r][0] = u.x; code[r][1] = u.y; code[r][2] = u.z; code[r][3] = u.w;
+          } else {
+            const uint2 u = *reinterpret_cast<const uint2 *>(src);
+            code[r][0] = u.x; code[r][1] = u.y;
+          }
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            const int task = w4 + 4 * k, pr = task & 1, t = (task >> 1) * 4 + (lane >> 3);
-            const int pos = 32 * pr + 8 * ((t & 7) >> 1) + 4 * r + 2 * (t >> 3) + (t & 1);
-            const uint8_t *src = raw + (2 * pr + r) * C::PITCH + Rec::K + t * (D / 2) + c * (D / 8);
-            uint32_t code[2 * NG];
-            uint2 sm[NG];
-            if constexpr (D == 128) {
-              const uint4 u = *reinterpret_cast<const uint4 *>(src), x = *reinterpret_cast<const uint4 *>(tabk + pos * 16);
-              code[0] = u.x; code[1] = u.y; code[2] = u.z; code[3] = u.w;
-              sm[0] = make_uint2(x.x, x.y);
-              sm[1] = make_uint2(x.z, x.w);
+            uint32_t x, y;
+            if constexpr (NG == 2) {
+              const uint4 u = *reinterpret_cast<const uint4 *>(from + Rec::VW + (2 * c + 8 * k) * 8);
+              x = part ? u.y : u.x;
+              y = part ? u.w : u.z;
             } else {
-              const uint2 u = *reinterpret_cast<const uint2 *>(src);
-              code[0] = u.x; code[1] = u.y;
-              sm[0] = *reinterpret_cast<const uint2 *>(tabk + pos * 16);
+              const uint2 u = *reinterpret_cast<const uint2 *>(from + Rec::VW + (2 * c + 8 * k) * 4);
+              x = u.x;
+              y = u.y;
             }
-            const uint32_t to = base + C::K + st * C::TILE + pos * 128;
-#pragma unroll
-            for (int w = 0; w < 2 * NG; ++w) {
-              const uint32_t lo = sm[w / 2].x, hi = pf_sixteenth2(lo), mm = sm[w / 2].y, u = code[w], u8 = u >> 8;
-              pf_sts128(to + (w >> 1) * 8192 + (((4 * (w & 1) + c) ^ (pos & 7)) << 4), pf_hfma2(u & 0x000F000Fu, lo, mm),
-                        pf_hfma2(u & 0x00F000F0u, hi, mm), pf_hfma2(u8 & 0x000F000Fu, lo, mm), pf_hfma2(u8 & 0x00F000F0u, hi, mm));
-            }
+            if (!there) x = y = 0u;
+            ss[2 * r + k] = pf_half2(bf16lo(x) * fs, bf16lo(y) * fs);
+            mm[2 * r + k] = pf_half2(bf16hi(x) * fm, bf16hi(y) * fm);
+            sh[2 * r + k] = pf_sixteenth2(ss[2 * r + k]);
           }
         }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&cs.k_full[st]);
-        // (a warp whose wait gives up leaves its V as it is and goes on to the next barrier)
-        if (tile >= NS) ok = __all_sync(0xffffffffu, mbar_wait(&cs.v_free[st], (tile / NS - 1) & 1, abort, a.status)) && ok;
-        // ---- V, transposed: lane 4 g + c holds channels g and g + 8 of every 16 for tokens 2c, 2c + 1, 2c + 8, 2c + 9 of two records ----
-        {
-          const int g = lane >> 2, c = lane & 3;
-          constexpr int NU = 2 * NG;  // words of a warp: d = 128: a half of the channels and a pair of records; d = 64: a quarter
-          const int part = D == 128 ? w4 >> 1 : 0, u0 = D == 128 ? 0 : 2 * (w4 >> 1), pr = (w4 & 1) ^ (g & 1);
-          const uint4 s4 = *reinterpret_cast<const uint4 *>(tabv + (part * 64 + 32 * pr + 8 * c) * 2);
-          const uint4 m4 = *reinterpret_cast<const uint4 *>(tabv + 256 + (part * 64 + 32 * pr + 8 * c) * 2);
-          const uint32_t ss[4] = {s4.x, s4.y, s4.z, s4.w}, mm[4] = {m4.x, m4.y, m4.z, m4.w};
-          uint32_t sh[4], code[2][NU];
+        const uint32_t to = base + C::V + st * C::TILE + (((4 * pr + c) ^ g) << 4);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) sh[k] = pf_sixteenth2(ss[k]);
-#pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            const uint8_t *src = raw + (2 * pr + r) * C::PITCH + Rec::V + part * 512 + 16 * lane + 4 * u0;
-            if constexpr (NU == 4) {
-              const uint4 u = *reinterpret_cast<const uint4 *>(src);
-              code[r][0] = u.x; code[r][1] = u.y; code[r][2] = u.z; code[r][3] = u.w;
-            } else {
-              const uint2 u = *reinterpret_cast<const uint2 *>(src);
-              code[r][0] = u.x; code[r][1] = u.y;
-            }
-          }
-          const uint32_t to = base + C::V + st * C::TILE + (((4 * pr + c) ^ g) << 4);
-#pragma unroll
-          for (int u = 0; u < NU; ++u) {
-            const uint32_t at = to + (64 * part + 16 * (u0 + u) + g) * 128;
-            const uint32_t a0 = code[0][u], a8 = a0 >> 8, b0 = code[1][u], b8 = b0 >> 8;
-            pf_sts128(at, pf_hfma2(a0 & 0x000F000Fu, ss[0], mm[0]), pf_hfma2(a8 & 0x000F000Fu, ss[1], mm[1]),
-                      pf_hfma2(b0 & 0x000F000Fu, ss[2], mm[2]), pf_hfma2(b8 & 0x000F000Fu, ss[3], mm[3]));
-            pf_sts128(at + 8 * 128, pf_hfma2(a0 & 0x00F000F0u, sh[0], mm[0]), pf_hfma2(a8 & 0x00F000F0u, sh[1], mm[1]),
-                      pf_hfma2(b0 & 0x00F000F0u, sh[2], mm[2]), pf_hfma2(b8 & 0x00F000F0u, sh[3], mm[3]));
-          }
+        for (int u = 0; u < NU; ++u) {
+          const uint32_t at = to + (64 * part + 16 * (u0 + u) + g) * 128;
+          const uint32_t a0 = code[0][u], a8 = a0 >> 8, b0 = code[1][u], b8 = b0 >> 8;
+          pf_sts128(at, pf_hfma2(a0 & 0x000F000Fu, ss[0], mm[0]), pf_hfma2(a8 & 0x000F000Fu, ss[1], mm[1]),
+                    pf_hfma2(b0 & 0x000F000Fu, ss[2], mm[2]), pf_hfma2(b8 & 0x000F000Fu, ss[3], mm[3]));
+          pf_sts128(at + 8 * 128, pf_hfma2(a0 & 0x00F000F0u, sh[0], mm[0]), pf_hfma2(a8 & 0x00F000F0u, sh[1], mm[1]),
+                    pf_hfma2(b0 & 0x00F000F0u, sh[2], mm[2]), pf_hfma2(b8 & 0x00F000F0u, sh[3], mm[3]));
         }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&cs.v_full[st]);
-          mbar_arrive(&cs.raw_free[rs]);
-        }
-        if (tile + 4 < total) words(tile + 4);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&cs.v_full[st]);
+        mbar_arrive(&cs.raw_free[rs]);
       }
     }
   } else if (warp < PF_LOAD) {
@@ -534,8 +570,8 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefix_attn_kernel(const Prefix
     // (a thread for each stream: waits, fences and issue of a job take it about as long as the tensor unit takes the products)
     const int t = warp - PF_PROD;
     if (lane == 0) {
-      const uint64_t dk = smem_desc_sw128(smem_u32(smem + C::K), 16, 1024), dv = smem_desc_sw128(smem_u32(smem + C::V), 16, 1024);
-      const uint64_t dq = smem_desc_sw128(smem_u32(smem + C::Q) + (C::QSMEM ? t * 128 * D * 2 : 0), 16, 1024);
+      const uint64_t dk = smem_desc_sw128(base + C::K, 16, 1024), dv = smem_desc_sw128(base + C::V, 16, 1024);
+      const uint64_t dq = smem_desc_sw128(base + C::Q + (C::QSMEM ? t * C::QB : 0), 16, 1024);
       const uint32_t sc = tmem + C::S + t * 64, oc = tmem + C::O + t * D, pc = tmem + C::P + t * 32;
       const uint32_t qc = tmem + C::QC + (R == 2 ? t * C::QCOLS : 0);
       uint32_t done = 0, piece = 0;  // jobs so far, pieces
@@ -546,7 +582,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefix_attn_kernel(const Prefix
         for (int j = 0; ok && j <= jobs; ++j) {
           if (j < jobs) {  // scores of job j, once the softmax has read those before
             const uint32_t tile = tc + (R == 2 ? j : 2 * j + t), st = tile % NS;
-            ok = mbar_wait(&cs.k_full[st], (tile / NS) & 1, abort, a.status) &&
+            ok = mbar_wait(&cs.v_full[st], (tile / NS) & 1, abort, a.status) &&
                  (done == 0 || mbar_wait(&cs.s_free[t], (done - 1) & 1, abort, a.status));
             if (!ok) break;
             tc_fence_after();
@@ -559,13 +595,12 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefix_attn_kernel(const Prefix
                 mma_bf16_ts(sc, qc + s * 8, b + (s >> 2) * (8192 >> 4) + (s & 3) * 2, IDESC_S, s > 0 ? 1u : 0u);
             }
             mma_commit(&cs.s_full[t]);
-            mma_commit(&cs.k_free[st]);
             if (R == 1 && t == 1 && j == jobs - 1) mma_commit(&cs.q_free);
             ++done;
           }
           if (j > 0) {  // P V of job j - 1
             const uint32_t tile = tc + (R == 2 ? j - 1 : 2 * (j - 1) + t), st = tile % NS, nth = done - (j < jobs ? 2 : 1);
-            ok = mbar_wait(&cs.v_full[st], (tile / NS) & 1, abort, a.status) && mbar_wait(&cs.p_full[t], nth & 1, abort, a.status);
+            ok = mbar_wait(&cs.p_full[t], nth & 1, abort, a.status);
             if (!ok) break;
             tc_fence_after();
             const uint64_t b = dv + st * (C::TILE >> 4);
@@ -584,7 +619,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefix_attn_kernel(const Prefix
       }
     }
     __syncwarp();
-  } else {
+  } else if (warp == PF_LOAD) {
     // ------------------------------------ loads ------------------------------------
     bool ok = true;
     while (ok && share.next(a, item, tile0, n)) {
@@ -627,6 +662,34 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefix_attn_kernel(const Prefix
       while (global_timer_ns() - t0 < 1000000ull) {
       }
     }
+  } else {
+    // ------------------------------------ powers of two ------------------------------------
+    // A tile's K and its V get one each from its 64 tokens' words: the largest scale to [2^-9, 2^-8), which is what a code of
+    // 2^-24 code leaves in f16, or where the minima are larger the largest of them to [2^13, 2^14).
+    const uint32_t total = static_cast<uint32_t>(share.end - share.at);
+    for (uint32_t tile = 0; tile < total; ++tile) {
+      const uint32_t rs = tile % RS;
+      if (!__all_sync(0xffffffffu, mbar_wait(&cs.raw_full[rs], (tile / RS) & 1, abort, a.status))) break;
+      const uint32_t bad = *reinterpret_cast<const uint32_t *>(cs.bad[rs]);  // a byte a record
+      int f[2];  // of K, V
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        int need = -200;
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {  // lane 16 y + t looks at token t of records 2 p + y
+          const int rec = 2 * p + (lane >> 4);
+          const uint8_t *at = smem + C::RING + rs * C::RAW + rec * C::PITCH + (s ? Rec::VW : Rec::KW) + (lane & 15) * NG * 4;
+#pragma unroll
+          for (int g = 0; g < NG; ++g) need = max(need, (bad >> (8 * rec)) & 1u ? -200 : pf_need(*reinterpret_cast<const uint32_t *>(at + 4 * g)));
+        }
+        f[s] = pf_power(__reduce_max_sync(0xffffffffu, need));
+      }
+      if (lane == 0) {
+        cs.info[tile & 15] = {f[0], f[1], (bad & 1u) | ((bad >> 7) & 2u) | ((bad >> 14) & 4u) | ((bad >> 21) & 8u), 0u};
+        mbar_arrive(&cs.info_full[rs]);
+      }
+      __syncwarp();
+    }
   }
   tc_fence_before();
   __syncthreads();
@@ -636,7 +699,8 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefix_attn_kernel(const Prefix
 
 // --------------------------------------------------------------------------------------------
 // Every row's shares - of the prefix from each CTA that held some of it, of the sequence's own tokens from those of the
-// cache attention - weighted by 2^(m - M) and divided by the weighted sum.  A warp per row, eight shares loaded at a time.
+// cache attention - weighted by 2^(m - M) and divided by the weighted sum.  W warps per row, each loads eight shares at a time: loads of a
+// microsecond each bound it, so a row of many shares wants many of them in flight.
 // --------------------------------------------------------------------------------------------
 struct PfCombineArgs {
   SplitArgs own;
@@ -646,56 +710,66 @@ struct PfCombineArgs {
   int tiles, ctas, groups, R, rt, width, rec_shift, prefix;
 };
 
-constexpr int PC_THREADS = 128, PC_FEW = 8;
-template <int D>
+constexpr int PC_THREADS = 256, PC_FEW = 8;
+template <int D, int W>
 __global__ void __launch_bounds__(PC_THREADS) prefix_combine_kernel(const PfCombineArgs a) {
-  constexpr int NL = D / 4;
+  constexpr int NL = D / 4, ROWS = PC_THREADS / 32 / W;
+  __shared__ float4 part[W > 1 ? PC_THREADS : 1];
+  __shared__ float2 part_ml[PC_THREADS / 32];
   start_after_earlier();
-  const int lane = threadIdx.x & 31;
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * (PC_THREADS / 32) + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31, sub = (threadIdx.x >> 5) % W;
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * ROWS + (threadIdx.x >> 5) / W;
   const int rows = a.own.rows;                      // of a sequence and KV head
   const int64_t per = static_cast<int64_t>(a.own.B) * rows;
   const int kvh = static_cast<int>(i / per);
-  if (kvh >= a.own.Hkv) return;
-  const int r = static_cast<int>(i - kvh * per), b = r / rows, rr = r % rows;
+  const bool mine = kvh < a.own.Hkv;
+  if (!mine && W == 1) return;
+  const int r = mine ? static_cast<int>(i - kvh * per) : 0, b = r / rows, rr = r % rows;
   const int64_t cap = static_cast<int64_t>(a.width) << (a.rec_shift + 4);
   const int len = max(a.lens[b] > cap ? static_cast<int>(cap) : a.lens[b], 0);
-  __nv_bfloat16 *out = a.own.row(b, kvh, rr) + 4 * lane;
-  if (len == 0) {
-    if (lane < NL) put_row(out, make_float4(0.f, 0.f, 0.f, 0.f), 0.f);
-    return;
-  }
   const int tile = 8 * a.rt, oitem = (b * a.own.Hkv + kvh) * a.own.ntile + rr / tile;
-  const int2 ends = a.own.ends[oitem];
-  const int n_own = ends.y - ends.x + 1;
-  const int64_t own0 = (static_cast<int64_t>(ends.x) + oitem) * tile + rr % tile;
-  int n = n_own;
-  int64_t pre0 = 0;
-  if (len - a.own.Nq >= a.prefix) {
-    const int prow = 128 * a.R, item = kvh * a.groups + r / prow;
+  int n_own = 0, n = 0, prow = 0;
+  int64_t own0 = 0, slot0 = 0;
+  if (mine && len > 0) {
+    const int2 ends = a.own.ends[oitem];
+    n = n_own = ends.y - ends.x + 1;
+    own0 = (static_cast<int64_t>(ends.x) + oitem) * tile + rr % tile;
+  }
+  if (mine && len > 0 && len - a.own.Nq >= a.prefix) {
+    const int item = kvh * a.groups + r / (128 * a.R);
     // CTA c holds tiles total c / ctas .. total (c + 1) / ctas - 1
     const int64_t t0 = static_cast<int64_t>(item) * a.tiles, t1 = t0 + a.tiles - 1;
     const int c0 = static_cast<int>(((t0 + 1) * a.ctas - 1) / a.total), c1 = static_cast<int>(((t1 + 1) * a.ctas - 1) / a.total);
-    pre0 = (static_cast<int64_t>(c0) + item) * PF_ROWS + r % prow;
+    slot0 = static_cast<int64_t>(c0) + item;
+    prow = r % (128 * a.R);
     n += (c1 - c0 + 1) * (a.R == 2 ? 1 : 2);
   }
-  const int64_t pstep = a.R == 2 ? PF_ROWS : 128;
+  // share k of the prefix: a slot's row or, with one row tile, the rows of its two streams
+  auto at = [&](int k, int &in) {
+    in = a.R == 2 ? prow : (k & 1) * 128 + prow;
+    return slot0 + (a.R == 2 ? k : k >> 1);
+  };
   float M = -INFINITY, L = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int w = 0; w < n; w += PC_FEW) {
+  for (int w = sub * PC_FEW; w < n; w += W * PC_FEW) {
     float2 ml = make_float2(-INFINITY, 0.f);
     if (lane < PC_FEW && w + lane < n) {
       const int k = w + lane;
+      int in;
+      const int64_t slot = at(k - n_own, in);
       ml = k < n_own ? *reinterpret_cast<const float2 *>(a.own.part_ml + 2 * (own0 + static_cast<int64_t>(k) * tile))
-                     : *reinterpret_cast<const float2 *>(a.part_ml + 2 * (pre0 + (k - n_own) * pstep));
+                     : *reinterpret_cast<const float2 *>(a.part_ml + 2 * (slot * PF_ROWS + in));
     }
     float4 v[PC_FEW];
 #pragma unroll
     for (int u = 0; u < PC_FEW; ++u) {
       const int k = w + u;
+      int in;
+      const int64_t slot = at(k - n_own, in);
       if (k < n && lane < NL)
         v[u] = k < n_own ? *reinterpret_cast<const float4 *>(a.own.part_o + (own0 + static_cast<int64_t>(k) * tile) * D + 4 * lane)
-                         : *reinterpret_cast<const float4 *>(a.part_o + (pre0 + (k - n_own) * pstep) * D + 4 * lane);
+                         : *reinterpret_cast<const float4 *>(a.part_o + ((slot * (D / 32) + lane / 8) * PF_ROWS + in) * 32 +
+                                                             4 * ((lane & 7) ^ (in & 7)));
     }
     float m = ml.x;
 #pragma unroll
@@ -716,7 +790,25 @@ __global__ void __launch_bounds__(PC_THREADS) prefix_combine_kernel(const PfComb
     }
     o = s;
   }
-  if (lane < NL) put_row(out, o, L == 0.f ? 0.f : 1.f / L);
+  if constexpr (W > 1) {  // the first warp of a row puts its warps' sums together
+    part[threadIdx.x] = o;
+    if (lane == 0) part_ml[threadIdx.x >> 5] = make_float2(M, L);
+    __syncthreads();
+    if (sub > 0 || !mine) return;
+    float m = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < W; ++k) m = fmaxf(m, part_ml[(threadIdx.x >> 5) + k].x);
+    L = 0.f;
+    o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < W; ++k) {
+      const float2 ml = part_ml[(threadIdx.x >> 5) + k];
+      const float f = share_weight(ml.x, ml.y, m);
+      if (f != 0.f) L = fmaf(f, ml.y, L);
+      add_share(o, f, part[threadIdx.x + 32 * k]);
+    }
+  }
+  if (lane < NL) put_row(a.own.row(b, kvh, rr) + 4 * lane, o, L == 0.f ? 0.f : 1.f / L);
 }
 
 // Row tiles of a CTA, groups of rows and CTAs of a call.
@@ -734,6 +826,18 @@ PfPlan plan(int64_t rows, int64_t Hkv, int64_t tiles) {
   return p;
 }
 
+// What one of the paths takes beyond what both do, in us, from times measured over 2 to 64 sequences with 1K to 64K shared tokens, 8
+// to 64 query heads over 1 to 8 KV heads and 1 to 4 queries (both sides of the rule's edge: 4 sequences over 64K tokens, 32 over 8
+// heads, d = 128: 57 alone, 68 shared; 8 over 64K: 103 and 70; 8 over 16K: 34 and 32; 16 over 4K: 23 and 27).
+double alone_us(int64_t B, int64_t rows, int64_t Hkv, int64_t d, int64_t recs) {  // the records of every sequence, from L2 for the most part
+  const double mb = 18e-6 * static_cast<double>(B) * Hkv * d * recs;
+  return mb * (rows <= 8 ? 0.165 : 0.24 * ((rows + 15) / 16));
+}
+double shared_us(const PfPlan &p, int64_t rows, int64_t Hkv, int64_t d, int64_t tiles) {  // two launches more, tiles, rows put together
+  const double tile = d == 128 ? (p.R == 2 ? 1.15 : 0.85) : (p.R == 2 ? 0.9 : 0.6);
+  return 14. + tile * static_cast<double>(p.items) * tiles / CA_SMS + 0.0022 * static_cast<double>(rows) * Hkv;
+}
+
 template <int D, int R>
 cudaError_t launch_t(const PrefixArgs &a, int ctas, cudaStream_t st) {
   static std::atomic<unsigned long long> smem_set{0};
@@ -749,6 +853,12 @@ size_t prefix_ws_bytes(int64_t rows, int64_t Hkv, int64_t d) {
   const PfPlan p = plan(rows, Hkv, INT_MAX);
   const size_t slots = static_cast<size_t>(p.items + CA_SMS);
   return ((slots * PF_ROWS * d * 4 + 255) & ~size_t(255)) + ((slots * PF_ROWS * 8 + 255) & ~size_t(255));
+}
+
+// Whether B sequences of `rows` query rows per KV head gain from a prefix of `recs` records being attended once for all of them.
+bool prefix_shared(int64_t B, int64_t rows, int64_t Hkv, int64_t d, int64_t recs) {
+  const int64_t tiles = (recs + 3) / 4;
+  return alone_us(B, rows, Hkv, d, recs) > shared_us(plan(B * rows, Hkv, tiles), B * rows, Hkv, d, tiles);
 }
 
 cudaError_t launch_prefix_attn(const PrefixAttn &l, const SplitArgs &own, cudaStream_t st) {
@@ -792,9 +902,18 @@ cudaError_t launch_prefix_combine(const PrefixAttn &l, const SplitArgs &own, cud
   a.width = l.width;
   a.rec_shift = l.rec_shift;
   a.prefix = l.prefix;
-  const dim3 grid(static_cast<unsigned>((rows * own.Hkv + PC_THREADS / 32 - 1) / (PC_THREADS / 32)));
-  return l.d == 128 ? launch_dependent(prefix_combine_kernel<128>, grid, PC_THREADS, 0, st, a)
-                    : launch_dependent(prefix_combine_kernel<64>, grid, PC_THREADS, 0, st, a);
+  // Warps of a row: by the shares that it has of the prefix, as long as all rows' warps are resident at once.  Measured at 256 rows
+  // of 300 shares: 48 us with a warp each, 15 with eight; 4096 rows of 9: 10 us with one, 20 with four.
+  const int64_t shares = ((p.ctas + p.items - 1) / p.items + 1) * (p.R == 2 ? 1 : 2), all = rows * own.Hkv;
+  const int W = shares <= 12 || all > 2048 ? 1 : shares <= 32 || all > 1024 ? 4 : 8, per = PC_THREADS / 32 / W;
+  const dim3 grid(static_cast<unsigned>((rows * own.Hkv + per - 1) / per));
+  auto run = [&](auto d) {
+    constexpr int D = decltype(d)::value;
+    return W == 1 ? launch_dependent(prefix_combine_kernel<D, 1>, grid, PC_THREADS, 0, st, a)
+         : W == 4 ? launch_dependent(prefix_combine_kernel<D, 4>, grid, PC_THREADS, 0, st, a)
+                  : launch_dependent(prefix_combine_kernel<D, 8>, grid, PC_THREADS, 0, st, a);
+  };
+  return l.d == 128 ? run(std::integral_constant<int, 128>()) : run(std::integral_constant<int, 64>());
 }
 
 }  // namespace sparge

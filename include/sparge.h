@@ -449,11 +449,18 @@ int sparge_cache4_pages_attn(const sparge_tensor *q, const sparge_cache4 *cache,
  * prefix_pages[0 .. n_prefix-1], every token of them.  They are read and multiplied once for all sequences.  Each row of table
  * holds these pages in its first n_prefix columns (n_prefix <= width), then the sequence's own; kv_lens counts both.  A sequence whose
  * queries do not all stand behind the prefix is attended over its own row alone, so any length is taken.
+ * path SPARGE_PREFIX_AUTO: where that takes less time by the call's sizes (few sequences, or a short prefix), every sequence is
+ * attended over its own row as in sparge_cache4_attn; SPARGE_PREFIX_SHARED: never.  The two round differently.
+ * Shared keys and values enter the products as f16, 64 tokens of a head with one power of two each: an element x of a token is off
+ * by at most |x| 2^-11 + s 2^-15 + m 2^-37, s and m the largest scale (step between codes) and |minimum| among the 64, as long as
+ * they are below 2^116.
  */
+#define SPARGE_PREFIX_AUTO 0
+#define SPARGE_PREFIX_SHARED 1
 size_t sparge_cache4_prefix_attn_workspace_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_t Nq, int64_t d);
 int sparge_cache4_prefix_attn(const sparge_tensor *q, const sparge_cache4 *cache, const int32_t *prefix_pages, int64_t n_prefix,
                               const int32_t *table, int64_t width, int64_t table_stride, const int32_t *kv_lens, float scale,
-                              sparge_tensor *o, void *ws, size_t ws_bytes, sparge_stream_t stream);
+                              int path, sparge_tensor *o, void *ws, size_t ws_bytes, sparge_stream_t stream);
 
 /*
  * Hilbert-curve token order (SpargeAttention summary page: a space-filling Hilbert-curve

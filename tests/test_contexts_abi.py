@@ -87,12 +87,13 @@ def test_pages_attn_refuses(lib, change, code):
     (dict(n=-1), BAD), (dict(n=9), BAD), (dict(prefix=None), BAD), (dict(width=-1), BAD), (dict(stride=7), BAD),
     (dict(width=1 << 30, stride=1 << 30), BAD), (dict(scale=-1.0), BAD), (dict(scale=math.inf), BAD), (dict(table=None), BAD),
     (dict(lens=None), BAD), (dict(ws=None), SMALL), (dict(wsb=100), SMALL), (dict(ws=PTR + 16), BAD), (dict(q=None), BAD),
+    (dict(path=-1), BAD), (dict(path=2), BAD),
 ])
 def test_prefix_attn_refuses(lib, change, code):
-    a = dict(q=t(), o=t(), c=pool(), prefix=PTR, n=3, table=PTR, width=8, stride=8, lens=PTR, scale=0.0, ws=PTR, wsb=BIG)
+    a = dict(q=t(), o=t(), c=pool(), prefix=PTR, n=3, table=PTR, width=8, stride=8, lens=PTR, scale=0.0, ws=PTR, wsb=BIG, path=0)
     a.update(change)
     refused(lib, lib.sparge_cache4_prefix_attn(ref(a["q"]), ref(a["c"]), a["prefix"], a["n"], a["table"], a["width"], a["stride"],
-                                               a["lens"], a["scale"], ref(a["o"]), a["ws"], a["wsb"], None), code)
+                                               a["lens"], a["scale"], a["path"], ref(a["o"]), a["ws"], a["wsb"], None), code)
 
 
 def test_calls_of_nothing(lib):
@@ -103,7 +104,7 @@ def test_calls_of_nothing(lib):
     assert lib.sparge_cache4_bounds_load(ref(c), None, 0, None, 0, None, None, None) == 0
     assert lib.sparge_cache4_select(ref(e), ref(c), None, 0, None, 0, 0, PTR, 2, 1, 1, None, None, None, 0, None) == 0
     assert lib.sparge_cache4_pages_attn(ref(e), ref(c), None, 4, None, 0.0, ref(e), PTR, BIG, None) == 0
-    assert lib.sparge_cache4_prefix_attn(ref(e), ref(c), None, 0, None, 0, 0, None, 0.0, ref(e), PTR, BIG, None) == 0
+    assert lib.sparge_cache4_prefix_attn(ref(e), ref(c), None, 0, None, 0, 0, None, 0.0, 0, ref(e), PTR, BIG, None) == 0
 
 
 def test_sizes(lib):

@@ -412,7 +412,7 @@ def test_prefix_attn(Hq, Hkv, Nq, d, page, prefix, own):
     pool, pages, table, lens = shared(g, prefix, own, Hkv, d, page)
     q = rand(g, len(own), Hq, Nq, d)
     q[0, 0, 0] = 0.0
-    out = fbs.cache4_prefix_attn(q, pool, pages, table, i32(*lens))
+    out = fbs.cache4_prefix_attn(q, pool, pages, table, i32(*lens), path=fbs.SPARGE_PREFIX_SHARED)
     check_cache_attn(q, pool, table, lens, out, d)
 
 
@@ -424,10 +424,10 @@ def test_prefix_attn_sequences_that_do_not_hold_it():
     lens = [lens[0], 323, 324, 321, 0, 150]
     table[4] = -1
     q = rand(g, 6, 4, 4, d)
-    out = fbs.cache4_prefix_attn(q, pool, pages, table, i32(*lens))
+    out = fbs.cache4_prefix_attn(q, pool, pages, table, i32(*lens), path=fbs.SPARGE_PREFIX_SHARED)
     check_cache_attn(q, pool, table, lens, out, d)
     assert (out[4] == 0).all()
-    none = fbs.cache4_prefix_attn(q, pool, pages[:0], table, i32(*lens))
+    none = fbs.cache4_prefix_attn(q, pool, pages[:0], table, i32(*lens), path=fbs.SPARGE_PREFIX_SHARED)
     check_cache_attn(q, pool, table, lens, none, d)
     assert fbs.device_status() == 0
 
@@ -440,13 +440,13 @@ def test_prefix_attn_strides_scale_and_bad_pages():
     out = torch.empty(2, 3, 8, d, dtype=torch.bfloat16, device="cuda").transpose(1, 2)
     wide = torch.full((2, table.shape[1] + 5), 77777, dtype=torch.int32, device="cuda")
     wide[:, :table.shape[1]] = table
-    assert fbs.cache4_prefix_attn(q, pool, pages, wide[:, :table.shape[1]], i32(*lens), scale=0.3, out=out) is out
+    assert fbs.cache4_prefix_attn(q, pool, pages, wide[:, :table.shape[1]], i32(*lens), scale=0.3, out=out, path=1) is out
     check_cache_attn(q, pool, table, lens, out, d, scale=0.3)
     bad, bad_table = pages.clone(), table.clone()
     bad[1], bad[7], bad[39] = -1, pool.shape[0], 2 ** 31 - 1
     for j in (1, 7, 39):
         bad_table[:, j] = -1
-    got = fbs.cache4_prefix_attn(q, pool, bad, bad_table, i32(*lens))
+    got = fbs.cache4_prefix_attn(q, pool, bad, bad_table, i32(*lens), path=fbs.SPARGE_PREFIX_SHARED)
     assert fbs.device_status() == fbs.SPARGE_ERR_INVALID_ARG
     # as if the tokens of those pages were not there
     keep = [j for j in range(table.shape[1]) if j not in (1, 7, 39)]
@@ -476,7 +476,7 @@ def test_a_step_of_all_of_them():
         fbs.cache4_store(b, v, slots, pool)
         fbs.cache4_bounds_update(pool, table, kv, 1, bounds)
         some, n = fbs.cache4_select(a, pool, bounds, table, kv, 12, first=2, last=2)
-        return a, some, n, fbs.cache4_pages_attn(a, pool, some, n), fbs.cache4_prefix_attn(a, pool, pages, table, kv)
+        return a, some, n, fbs.cache4_pages_attn(a, pool, some, n), fbs.cache4_prefix_attn(a, pool, pages, table, kv, path=1)
 
     def check(a, some, n, near, whole):
         want, mag = C.norm_rope_axes(q.double(), None, freq, axes.tolist(), pos, 1e-6, False)
