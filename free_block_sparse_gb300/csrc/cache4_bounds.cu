@@ -38,6 +38,12 @@ __device__ __forceinline__ float code_unit(float a) {
 // 1 / s for a power of two s in 2^-126 .. 2^126
 __device__ __forceinline__ float over_unit(float s) { return __uint_as_float((254u << 23) - __float_as_uint(s)); }
 
+__device__ __forceinline__ float fmin3(float a, float b, float c) {  // as fmax3: a NaN among them counts for nothing
+  float r;
+  asm("min.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
 struct BoundsArgs {
   const uint8_t *pool;
   uint8_t *bounds;
@@ -84,39 +90,53 @@ __global__ void __launch_bounds__(128) bounds_update_kernel(const BoundsArgs a) 
     lo[i] = INFINITY;
   }
   bool bad = false;
-#pragma unroll 2
-  for (int t0 = 0; t0 < n; t0 += 8) {
-    const int t = t0 + tt;
+  // two tokens at a time, one of every record's halves: a value then costs half a three-way maximum and minimum
+#pragma unroll 1
+  for (int t0 = 0; t0 < n; t0 += C4_TOKENS) {
     const uint8_t *rec = src + (t0 >> 4) * R::BYTES;
-    uint32_t k[NW], word[R::NG];
-    if (t < n) {
-      if constexpr (D == 128) {
-        const uint4 u = *reinterpret_cast<const uint4 *>(rec + R::K + (t & 15) * (D / 2) + c * (D / 8));
-        const uint2 w = *reinterpret_cast<const uint2 *>(rec + R::KW + (t & 15) * 8);
-        k[0] = u.x; k[1] = u.y; k[2] = u.z; k[3] = u.w;
-        word[0] = w.x; word[1] = w.y;
-      } else {
-        const uint2 u = *reinterpret_cast<const uint2 *>(rec + R::K + (t & 15) * (D / 2) + c * (D / 8));
-        k[0] = u.x; k[1] = u.y;
-        word[0] = *reinterpret_cast<const uint32_t *>(rec + R::KW + (t & 15) * 4);
+    uint32_t k[2][NW], word[2][R::NG];
+#pragma unroll
+    for (int y = 0; y < 2; ++y) {
+      const int t = 8 * y + tt;
+#pragma unroll
+      for (int w = 0; w < NW; ++w) k[y][w] = 0u;
+#pragma unroll
+      for (int g = 0; g < R::NG; ++g) word[y][g] = 0x7FC07FC0u;  // a token that is not there: NaN, which no maximum takes
+      if (t0 + t < n) {
+        if constexpr (D == 128) {
+          const uint4 u = *reinterpret_cast<const uint4 *>(rec + R::K + t * (D / 2) + c * (D / 8));
+          const uint2 w = *reinterpret_cast<const uint2 *>(rec + R::KW + t * 8);
+          k[y][0] = u.x; k[y][1] = u.y; k[y][2] = u.z; k[y][3] = u.w;
+          word[y][0] = w.x; word[y][1] = w.y;
+        } else {
+          const uint2 u = *reinterpret_cast<const uint2 *>(rec + R::K + t * (D / 2) + c * (D / 8));
+          k[y][0] = u.x; k[y][1] = u.y;
+          word[y][0] = *reinterpret_cast<const uint32_t *>(rec + R::KW + t * 4);
+        }
+#pragma unroll
+        for (int g = 0; g < R::NG; ++g)
+          bad = bad || !(fabsf(bf16lo(word[y][g])) < INFINITY) || !(fabsf(bf16hi(word[y][g])) < INFINITY);
       }
+    }
 #pragma unroll
-      for (int w = 0; w < NW; ++w) {
-        const float s = bf16lo(word[w / 2]), m = bf16hi(word[w / 2]);
-        bad = bad || !(fabsf(s) < INFINITY) || !(fabsf(m) < INFINITY);
-        const uint32_t even = k[w] & 0x0F0F0F0Fu, odd = (k[w] >> 4) & 0x0F0F0F0Fu;
+    for (int w = 0; w < NW; ++w) {
 #pragma unroll
-        for (int j = 0; j < 8; j += 2) {
+      for (int j = 0; j < 8; j += 2) {
+        float2 x[2];
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          const uint32_t even = k[y][w] & 0x0F0F0F0Fu, odd = (k[y][w] >> 4) & 0x0F0F0F0Fu;
+          const float s = bf16lo(word[y][w / 2]), m = bf16hi(word[y][w / 2]);
           // a code's byte becomes the low byte of 2^23 (code + 2^23, exactly)
           const float2 f = fadd2(make_float2(__uint_as_float(__byte_perm(even, 0x4B000000u, 0x7650 + j / 2)),
                                              __uint_as_float(__byte_perm(odd, 0x4B000000u, 0x7650 + j / 2))),
                                  make_float2(-8388608.f, -8388608.f));
-          const float2 x = ffma2(f, make_float2(s, s), make_float2(m, m));
-          hi[8 * w + j] = fmaxf(hi[8 * w + j], x.x);
-          lo[8 * w + j] = fminf(lo[8 * w + j], x.x);
-          hi[8 * w + j + 1] = fmaxf(hi[8 * w + j + 1], x.y);
-          lo[8 * w + j + 1] = fminf(lo[8 * w + j + 1], x.y);
+          x[y] = ffma2(f, make_float2(s, s), make_float2(m, m));
         }
+        hi[8 * w + j] = fmax3(hi[8 * w + j], x[0].x, x[1].x);
+        lo[8 * w + j] = fmin3(lo[8 * w + j], x[0].x, x[1].x);
+        hi[8 * w + j + 1] = fmax3(hi[8 * w + j + 1], x[0].y, x[1].y);
+        lo[8 * w + j + 1] = fmin3(lo[8 * w + j + 1], x[0].y, x[1].y);
       }
     }
   }
