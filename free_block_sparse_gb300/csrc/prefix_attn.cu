@@ -1,4 +1,35 @@
 // Attention of a whole batch over a prefix that its sequences share, from the paged 4-bit cache, on tcgen05 tensor cores.
+//
+//   O = softmax(scale Q K^^T) V^ over the shared tokens for all B G Nq query rows of a KV head at once, K^ and V^ = code * scale +
+//   minimum; left as shares (reference m, sum l, sum P V) that prefix_combine_kernel puts together with those of the
+//   sequences' own tokens, which the cache attention makes.
+//
+// A sequence by itself reads every shared record again: 64 sequences over 32K tokens of 8 heads are 1.2 GB from L2, 196 us.  Here a
+// record is read once, and its codes, widened once, serve 256 rows.
+//
+// Widening.  A code n is the subnormal f16 n 2^-24 once its four bits are masked out in place, so one fma.rn.f16x2 with (s 2^(f + 24),
+// m 2^f) makes two elements of s n + m times 2^f: no conversion, one rounding, to f16.  f, one number for a tile's K and one for its V,
+// takes the tile's largest scale to [2^-9, 2^-8), the most that s 2^(f + 24) allows (or the largest minimum below 2^14).  An element is
+// off by at most 2^-11 of itself, and by 2^-15 of the largest scale where its own is far smaller.  Words give the
+// channels of eight in the order 0 4 1 5 2 6 3 7, so Q is stored in that order; tokens of a tile stand in the order that the
+// V records give (position 32 p + 8 c + 4 r + 2 h + i: token 2 c + 8 h + i of record 2 p + r), for K and V alike.
+//
+// Products.  S = Q K'^T (M = 128 rows, N = 64 tokens) and O += P' V' (N = d), kind::f16 with fp32 sums in TMEM.  P' = 2^(x + g - ref),
+// g = -f of V: V's powers enter through P, and ref follows the largest x + g of the row when a P' passes 2^15, so O needs no rescaling
+// when V's sizes change from tile to tile.  l is summed in fp32 against a reference m of its own.  Q is f16 times a power of two per row.
+//
+// A CTA holds two streams, each with its softmax warps, its thread that issues products, and its S, P and O: two tiles of 128 rows
+// over the same tokens (more than 128 rows) or one tile of rows whose streams take the token tiles in turns.  The line of all
+// (KV head, row group) items' tiles is cut into equal shares, so any batch fills all SMs.
+//
+// What bounds it (64 sequences over 32K tokens of 8 heads, 4 rows each, d = 128; 256 rows: 43 us; 8.7e10 flops would take 18.5 us): a tile
+// takes its stream about 2100 cycles: the score product with N = 64 (600, the tensor unit hardly faster than with N = 128),
+// 64 exponentials a row (800 with both streams on the special function unit), P to TMEM, P V (270) and the waits between them.
+// The other stream fills those gaps only in part.  DRAM is idle at 9 %.  12 over 128K (48 rows of 128 in use): 100 us, 1600 cycles
+// a tile, bytes would take 25.7; widening a tile (1300 cycles of four warps) is as long as a stream's turn there.  Tried and slower: P in two
+// places so that it need not wait for P V (+4 %), K and V freed apart (two commits more: +5 %), powers of two per record (maxima no
+// longer come with the load: +15 %), two teams that widen in turns (+-2 %), one product of 128 tokens for both streams of one
+// row tile (they then wait for one another: +30 %).
 #include <climits>
 #include <cmath>
 #include <type_traits>
@@ -14,13 +45,9 @@
 namespace sparge {
 namespace {
 
-// Warps: softmax (4 per stream, a row a thread), widening (groups of four that take turns over the tiles), products (one per
-// stream), loads, powers of two: the registers are dealt out by groups of four.
-constexpr int PF_SOFT = 8, PF_WIDE = 4, PF_TEAMS = 1, PF_PROD = PF_SOFT + PF_TEAMS * PF_WIDE, PF_LOAD = PF_PROD + 2;
-constexpr int PF_THREADS = (PF_PROD + 4) * 32;
-constexpr int PF_REGS = 65536 / PF_THREADS / 8 * 8;  // a thread's at launch
-constexpr int PF_SOFT_REGS = 152, PF_WIDE_REGS = 120, PF_REST_REGS = 88;
-static_assert(PF_SOFT * PF_SOFT_REGS + PF_TEAMS * PF_WIDE * PF_WIDE_REGS + 4 * PF_REST_REGS <= PF_REGS * PF_THREADS / 32, "registers");
+// Warps: softmax (4 per stream, a row a thread), widening, products (one per stream), loads, powers of two.
+constexpr int PF_SOFT = 8, PF_WIDE = 4, PF_PROD = PF_SOFT + PF_WIDE, PF_LOAD = PF_PROD + 2;
+constexpr int PF_THREADS = (PF_LOAD + 2) * 32;
 constexpr int PF_ROWS = 256;     // rows of a slot: two streams of 128
 constexpr float PF_TOP = 15.f;   // the references move when a P or a P' passes 2^15, the last power of two within f16
 
@@ -61,7 +88,7 @@ struct alignas(16) PfInfo {
 };
 struct PfCtrl {
   PfInfo info[16];  // (tile % 16: a tile that far behind has been turned into P)
-  uint64_t raw_full[8], raw_free[8], info_full[8], k_full[4], k_free[4], v_full[4], v_free[4];
+  uint64_t raw_full[8], raw_free[8], info_full[8], kv_full[4], kv_free[4];
   uint64_t q_full[2], q_free, s_full[2], s_free[2], p_full[2], pv_done[2], drained[2];
   uint8_t bad[8][4];
   uint32_t tmem;
@@ -77,14 +104,6 @@ __device__ __forceinline__ void pf_bulk_load(void *dst, const void *src, uint32_
 }
 __device__ __forceinline__ void pf_bulk_store(void *dst, uint32_t src, uint32_t bytes) {
   asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes) : "memory");
-}
-template <int N>
-__device__ __forceinline__ void pf_more_regs() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void pf_fewer_regs() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 __device__ __forceinline__ float pf_pow2(int e) { return __int_as_float((e + 127) << 23); }  // e in -126..127
 __device__ __forceinline__ int pf_exponent(float x) { return static_cast<int>((__float_as_uint(x) >> 23) & 0xFFu) - 127; }
@@ -189,10 +208,8 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefix_attn_kernel(const Prefix
       mbar_init(&cs.info_full[s], 1);
     }
     for (int s = 0; s < NS; ++s) {
-      mbar_init(&cs.k_full[s], PF_WIDE);
-      mbar_init(&cs.k_free[s], R);
-      mbar_init(&cs.v_full[s], PF_WIDE);
-      mbar_init(&cs.v_free[s], R);
+      mbar_init(&cs.kv_full[s], PF_WIDE);
+      mbar_init(&cs.kv_free[s], R);
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(&cs.q_full[t], 4);
@@ -343,7 +360,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefix_attn_kernel(const Prefix
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&cs.s_free[t]);
-        ok = mbar_wait(&cs.v_full[st], (tile / NS) & 1, abort, a.status);
+        ok = mbar_wait(&cs.kv_full[st], (tile / NS) & 1, abort, a.status);
         const PfInfo info = cs.info[tile & 15];
         if (info.missing && live) {  // columns 32 h + 8 c + 4 r + i are tokens of record 2 h + r
 #pragma unroll
@@ -470,10 +487,10 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefix_attn_kernel(const Prefix
     // K and V have stages of their own, so that K's is free with the scores, and V's is not held while they are turned into P.
     const int w4 = warp & 3;
     const uint32_t total = static_cast<uint32_t>(share.end - share.at);  // tiles of all the CTA's pieces
-    for (uint32_t tile = (warp - PF_SOFT) >> 2; tile < total; tile += PF_TEAMS) {
+    for (uint32_t tile = 0; tile < total; ++tile) {
       const uint32_t rs = tile % RS, st = tile % NS;
       bool ok = mbar_wait(&cs.info_full[rs], (tile / RS) & 1, abort, a.status) && mbar_wait(&cs.raw_full[rs], (tile / RS) & 1, abort, a.status);
-      if (tile >= NS) ok = ok && mbar_wait(&cs.v_free[st], (tile / NS - 1) & 1, abort, a.status);
+      if (tile >= NS) ok = ok && mbar_wait(&cs.kv_free[st], (tile / NS - 1) & 1, abort, a.status);
       if (!__all_sync(0xffffffffu, ok)) break;
       const uint8_t *raw = smem + C::RING + rs * C::RAW;
       const PfInfo info = cs.info[tile & 15];
@@ -561,7 +578,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefix_attn_kernel(const Prefix
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(&cs.v_full[st]);
+        mbar_arrive(&cs.kv_full[st]);
         mbar_arrive(&cs.raw_free[rs]);
       }
     }
@@ -582,7 +599,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefix_attn_kernel(const Prefix
         for (int j = 0; ok && j <= jobs; ++j) {
           if (j < jobs) {  // scores of job j, once the softmax has read those before
             const uint32_t tile = tc + (R == 2 ? j : 2 * j + t), st = tile % NS;
-            ok = mbar_wait(&cs.v_full[st], (tile / NS) & 1, abort, a.status) &&
+            ok = mbar_wait(&cs.kv_full[st], (tile / NS) & 1, abort, a.status) &&
                  (done == 0 || mbar_wait(&cs.s_free[t], (done - 1) & 1, abort, a.status));
             if (!ok) break;
             tc_fence_after();
@@ -607,7 +624,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefix_attn_kernel(const Prefix
 #pragma unroll
             for (int s = 0; s < 4; ++s) mma_bf16_ts(oc, pc + s * 8, b + s * 2, IDESC_PV, s > 0 || j > 1 ? 1u : 0u);
             mma_commit(&cs.pv_done[t]);
-            mma_commit(&cs.v_free[st]);
+            mma_commit(&cs.kv_free[st]);
           }
         }
         if (R == 1 && t == 1 && jobs == 0) mma_commit(&cs.q_free);
