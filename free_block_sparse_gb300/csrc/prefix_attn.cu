@@ -105,6 +105,26 @@ __device__ __forceinline__ void pf_bulk_load(void *dst, const void *src, uint32_
 __device__ __forceinline__ void pf_bulk_store(void *dst, uint32_t src, uint32_t bytes) {
   asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes) : "memory");
 }
+// mbar_wait in few instructions: the loop's code of all roles has to stay in the instruction cache.
+__device__ __forceinline__ bool pf_wait(uint64_t *bar, uint32_t parity, volatile int *abort) {
+  if (mbar_try_wait(bar, parity)) return true;
+  uint32_t t0, t;
+  asm volatile("mov.u32 %0, %globaltimer_lo;" : "=r"(t0));
+#pragma unroll 1
+  while (!mbar_try_wait(bar, parity)) {
+    asm volatile("mov.u32 %0, %globaltimer_lo;" : "=r"(t));
+    if (t - t0 > 2000000000u) *abort = 1;
+    if (*abort) return false;
+  }
+  return true;
+}
+// One lane of the warp, always the same one.  The products' warps run as a whole and branch on values that are the same in all lanes, so
+// that descriptors are made in uniform registers.
+__device__ __forceinline__ bool pf_one_lane() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0u;
+}
 __device__ __forceinline__ float pf_pow2(int e) { return __int_as_float((e + 127) << 23); }  // e in -126..127
 __device__ __forceinline__ int pf_exponent(float x) { return static_cast<int>((__float_as_uint(x) >> 23) & 0xFFu) - 127; }
 __device__ __forceinline__ uint32_t pf_half2(float lo, float hi) {  // an infinity or a NaN stays one
@@ -253,7 +273,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefix_attn_kernel(const Prefix
       float rm;  // 2^(e - 14) scale: what a product of the scaled row counts
       {
         if (R == 1 && t == 0 && piece > 0) {  // the other stream's products with the rows before these have been made (this one's have)
-          ok = __all_sync(0xffffffffu, mbar_wait(&cs.q_free, (piece - 1) & 1, abort, a.status));
+          ok = __all_sync(0xffffffffu, pf_wait(&cs.q_free, (piece - 1) & 1, abort));
           if (bar_red_or(1 + t, 128, !ok)) {  // (all four warps leave, or none)
             ok = false;
             break;
@@ -345,7 +365,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefix_attn_kernel(const Prefix
       for (int j = 0; j < jobs; ++j, ++done) {
         const uint32_t tile = tc + (R == 2 ? j : 2 * j + t), st = tile % NS;
         // (V's barrier is what orders the reads of the tile's powers)
-        ok = mbar_wait(&cs.s_full[t], done & 1, abort, a.status);
+        ok = pf_wait(&cs.s_full[t], done & 1, abort);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
@@ -360,7 +380,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefix_attn_kernel(const Prefix
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&cs.s_free[t]);
-        ok = mbar_wait(&cs.kv_full[st], (tile / NS) & 1, abort, a.status);
+        ok = pf_wait(&cs.kv_full[st], (tile / NS) & 1, abort);
         const PfInfo info = cs.info[tile & 15];
         if (info.missing && live) {  // columns 32 h + 8 c + 4 r + i are tokens of record 2 h + r
 #pragma unroll
@@ -374,7 +394,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefix_attn_kernel(const Prefix
           }
         }
         if (j > 0) {  // the product before this one has read its P and added to O
-          ok = ok && mbar_wait(&cs.pv_done[t], (done - 1) & 1, abort, a.status);
+          ok = ok && pf_wait(&cs.pv_done[t], (done - 1) & 1, abort);
         }
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
@@ -384,8 +404,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefix_attn_kernel(const Prefix
           const float g = static_cast<float>(-info.vf);
           const float xm = fmaxf(mh[0], mh[1]) * mult, ym = xm + g;
           const bool move = xm > m + PF_TOP || ym > ref + PF_TOP;
-          bool tiny = (ref - m) - g > 60.f;  // V of this tile is so small beside what O holds that P' says nothing of P
-          if (__any_sync(0xffffffffu, move || tiny)) {
+          if (__any_sync(0xffffffffu, move)) {
             float f = 1.f;
             if (move) {
               const float mn = fmaxf(m, xm), rn = fmaxf(ym, ref);
@@ -394,7 +413,6 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefix_attn_kernel(const Prefix
               m = mn;
               ref = rn;
             }
-            tiny = __any_sync(0xffffffffu, (ref - m) - g > 60.f);
             if (j > 0) {
 #pragma unroll 1
               for (int q = 0; q < D / 16; ++q) {
@@ -409,7 +427,8 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefix_attn_kernel(const Prefix
           }
           // (a row whose references are still -inf has only hidden columns, or NaN)
           const bool none = ref == -INFINITY;
-          const float nr = none ? 0.f : g - ref, back = none ? 0.f : (ref - m) - g;  // P' = 2^(x + nr), P = P' 2^back
+          // P' = 2^(x + nr), P = P' 2^back; where V of this tile is so small beside what O holds that its P' is 0, back stops where l's terms do not
+          const float back = none ? 0.f : fminf((ref - m) - g, 60.f), nr = none ? 0.f : -m - back;
           const float2 m2 = make_float2(mult, mult), n2 = make_float2(nr, nr);
           float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
@@ -428,17 +447,8 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefix_attn_kernel(const Prefix
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&cs.p_full[t]);
-          if (tiny) {
-            float s = 0.f;
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-              for (int k = 0; k < 32; ++k) s += fast_exp2(fmaf(__uint_as_float(v[h][k]), mult, none ? 0.f : -m));
-            l += s;
-          } else {
-            const float2 s2 = fadd2(sum[0], sum[1]);
-            l = fmaf(s2.x + s2.y, fast_exp2(back), l);
-          }
+          const float2 s2 = fadd2(sum[0], sum[1]);
+          l = fmaf(s2.x + s2.y, fast_exp2(back), l);
         } else {
           if (lane == 0) mbar_arrive(&cs.p_full[t]);
         }
@@ -446,7 +456,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefix_attn_kernel(const Prefix
       // ---- the piece's end: O against m, 32 channels of the stream's rows at a time through shared memory, then the references and
       // sums.  (The four warps leave together if one's wait gave up.) ----
       if (ok && jobs > 0) {
-        ok = __all_sync(0xffffffffu, mbar_wait(&cs.pv_done[t], (done - 1) & 1, abort, a.status));
+        ok = __all_sync(0xffffffffu, pf_wait(&cs.pv_done[t], (done - 1) & 1, abort));
         tc_fence_after();
       }
       if (bar_red_or(1 + t, 128, !ok)) {
@@ -489,8 +499,8 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefix_attn_kernel(const Prefix
     const uint32_t total = static_cast<uint32_t>(share.end - share.at);  // tiles of all the CTA's pieces
     for (uint32_t tile = 0; tile < total; ++tile) {
       const uint32_t rs = tile % RS, st = tile % NS;
-      bool ok = mbar_wait(&cs.info_full[rs], (tile / RS) & 1, abort, a.status) && mbar_wait(&cs.raw_full[rs], (tile / RS) & 1, abort, a.status);
-      if (tile >= NS) ok = ok && mbar_wait(&cs.kv_free[st], (tile / NS - 1) & 1, abort, a.status);
+      bool ok = pf_wait(&cs.info_full[rs], (tile / RS) & 1, abort) && pf_wait(&cs.raw_full[rs], (tile / RS) & 1, abort);
+      if (tile >= NS) ok = ok && pf_wait(&cs.kv_free[st], (tile / NS - 1) & 1, abort);
       if (!__all_sync(0xffffffffu, ok)) break;
       const uint8_t *raw = smem + C::RING + rs * C::RAW;
       const PfInfo info = cs.info[tile & 15];
@@ -584,25 +594,26 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefix_attn_kernel(const Prefix
     }
   } else if (warp < PF_LOAD) {
     // ------------------------------------ products of one stream ------------------------------------
-    // (a thread for each stream: waits, fences and issue of a job take it about as long as the tensor unit takes the products)
-    const int t = warp - PF_PROD;
-    if (lane == 0) {
-      const uint64_t dk = smem_desc_sw128(base + C::K, 16, 1024), dv = smem_desc_sw128(base + C::V, 16, 1024);
-      const uint64_t dq = smem_desc_sw128(base + C::Q + (C::QSMEM ? t * C::QB : 0), 16, 1024);
-      const uint32_t sc = tmem + C::S + t * 64, oc = tmem + C::O + t * D, pc = tmem + C::P + t * 32;
-      const uint32_t qc = tmem + C::QC + (R == 2 ? t * C::QCOLS : 0);
-      uint32_t done = 0, piece = 0;  // jobs so far, pieces
-      bool ok = true;
-      for (; ok && share.next(a, item, tile0, n); ++piece) {
-        const int jobs = R == 2 ? n : (n - t + 1) / 2;
-        ok = mbar_wait(&cs.q_full[R == 2 ? t : 0], piece & 1, abort, a.status);
-        for (int j = 0; ok && j <= jobs; ++j) {
-          if (j < jobs) {  // scores of job j, once the softmax has read those before
-            const uint32_t tile = tc + (R == 2 ? j : 2 * j + t), st = tile % NS;
-            ok = mbar_wait(&cs.kv_full[st], (tile / NS) & 1, abort, a.status) &&
-                 (done == 0 || mbar_wait(&cs.s_free[t], (done - 1) & 1, abort, a.status));
-            if (!ok) break;
-            tc_fence_after();
+    // (a warp for each stream: waits, fences and issue of a job take it about as long as the tensor unit takes the products)
+    const int t = __shfl_sync(0xffffffffu, warp - PF_PROD, 0);
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+    const uint64_t dk = smem_desc_sw128(base + C::K, 16, 1024), dv = smem_desc_sw128(base + C::V, 16, 1024);
+    const uint64_t dq = smem_desc_sw128(base + C::Q + (C::QSMEM ? t * C::QB : 0), 16, 1024);
+    const uint32_t sc = tm + C::S + t * 64, oc = tm + C::O + t * D, pc = tm + C::P + t * 32;
+    const uint32_t qc = tm + C::QC + (R == 2 ? t * C::QCOLS : 0);
+    uint32_t done = 0, piece = 0;  // jobs so far, pieces
+    bool ok = true;
+    for (; ok && share.next(a, item, tile0, n); ++piece) {
+      const int jobs = R == 2 ? n : (n - t + 1) / 2;
+      ok = __all_sync(0xffffffffu, pf_wait(&cs.q_full[R == 2 ? t : 0], piece & 1, abort));
+      for (int j = 0; ok && j <= jobs; ++j) {
+        if (j < jobs) {  // scores of job j, once the softmax has read those before
+          const uint32_t tile = tc + (R == 2 ? j : 2 * j + t), st = tile % NS;
+          ok = pf_wait(&cs.kv_full[st], (tile / NS) & 1, abort) && (done == 0 || pf_wait(&cs.s_free[t], (done - 1) & 1, abort));
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          tc_fence_after();
+          if (pf_one_lane()) {
             const uint64_t b = dk + st * (C::TILE >> 4);
 #pragma unroll
             for (int s = 0; s < D / 16; ++s) {
@@ -613,27 +624,33 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefix_attn_kernel(const Prefix
             }
             mma_commit(&cs.s_full[t]);
             if (R == 1 && t == 1 && j == jobs - 1) mma_commit(&cs.q_free);
-            ++done;
           }
-          if (j > 0) {  // P V of job j - 1
-            const uint32_t tile = tc + (R == 2 ? j - 1 : 2 * (j - 1) + t), st = tile % NS, nth = done - (j < jobs ? 2 : 1);
-            ok = mbar_wait(&cs.p_full[t], nth & 1, abort, a.status);
-            if (!ok) break;
-            tc_fence_after();
+          __syncwarp();
+          ++done;
+        }
+        if (j > 0) {  // P V of job j - 1
+          const uint32_t tile = tc + (R == 2 ? j - 1 : 2 * (j - 1) + t), st = tile % NS, nth = done - (j < jobs ? 2 : 1);
+          ok = __all_sync(0xffffffffu, pf_wait(&cs.p_full[t], nth & 1, abort));
+          if (!ok) break;
+          tc_fence_after();
+          if (pf_one_lane()) {
             const uint64_t b = dv + st * (C::TILE >> 4);
 #pragma unroll
             for (int s = 0; s < 4; ++s) mma_bf16_ts(oc, pc + s * 8, b + s * 2, IDESC_PV, s > 0 || j > 1 ? 1u : 0u);
             mma_commit(&cs.pv_done[t]);
             mma_commit(&cs.kv_free[st]);
           }
+          __syncwarp();
         }
-        if (R == 1 && t == 1 && jobs == 0) mma_commit(&cs.q_free);
-        tc += n;
       }
-      if (!ok) {  // products in flight end before the CTA gives its TMEM back
-        mma_commit(&cs.drained[t]);
-        mbar_wait(&cs.drained[t], 0, &cs.no_abort, a.status);
-      }
+      if (R == 1 && t == 1 && jobs == 0 && pf_one_lane()) mma_commit(&cs.q_free);
+      __syncwarp();
+      tc += n;
+    }
+    if (!ok) {  // products in flight end before the CTA gives its TMEM back
+      if (pf_one_lane()) mma_commit(&cs.drained[t]);
+      __syncwarp();
+      pf_wait(&cs.drained[t], 0, &cs.no_abort);
     }
     __syncwarp();
   } else if (warp == PF_LOAD) {
@@ -657,7 +674,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefix_attn_kernel(const Prefix
           }
         }
         const uint32_t tile = tc + j, rs = tile % RS;
-        if (tile >= RS) ok = mbar_wait(&cs.raw_free[rs], (tile / RS - 1) & 1, abort, a.status);
+        if (tile >= RS) ok = pf_wait(&cs.raw_free[rs], (tile / RS - 1) & 1, abort);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         if (lane / 4 == j - j0) {
@@ -686,7 +703,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefix_attn_kernel(const Prefix
     const uint32_t total = static_cast<uint32_t>(share.end - share.at);
     for (uint32_t tile = 0; tile < total; ++tile) {
       const uint32_t rs = tile % RS;
-      if (!__all_sync(0xffffffffu, mbar_wait(&cs.raw_full[rs], (tile / RS) & 1, abort, a.status))) break;
+      if (!__all_sync(0xffffffffu, pf_wait(&cs.raw_full[rs], (tile / RS) & 1, abort))) break;
       const uint32_t bad = *reinterpret_cast<const uint32_t *>(cs.bad[rs]);  // a byte a record
       int f[2];  // of K, V
 #pragma unroll
@@ -711,6 +728,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefix_attn_kernel(const Prefix
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if (threadIdx.x == 0 && (cs.abort | cs.no_abort)) record_status(a.status, -5 /* SPARGE_ERR_DEVICE_TIMEOUT */);
   if (warp == PF_PROD) tmem_dealloc(tmem, 512);
 }
 
