@@ -22,14 +22,16 @@
 // over the same tokens (more than 128 rows) or one tile of rows whose streams take the token tiles in turns.  The line of all
 // (KV head, row group) items' tiles is cut into equal shares, so any batch fills all SMs.
 //
-// What bounds it (64 sequences over 32K tokens of 8 heads, 4 rows each, d = 128; 256 rows: 43 us; 8.7e10 flops would take 18.5 us): a tile
-// takes its stream about 2100 cycles: the score product with N = 64 (600, the tensor unit hardly faster than with N = 128),
-// 64 exponentials a row (800 with both streams on the special function unit), P to TMEM, P V (270) and the waits between them.
-// The other stream fills those gaps only in part.  DRAM is idle at 9 %.  12 over 128K (48 rows of 128 in use): 100 us, 1600 cycles
-// a tile, bytes would take 25.7; widening a tile (1300 cycles of four warps) is as long as a stream's turn there.  Tried and slower: P in two
-// places so that it need not wait for P V (+4 %), K and V freed apart (two commits more: +5 %), powers of two per record (maxima no
-// longer come with the load: +15 %), two teams that widen in turns (+-2 %), one product of 128 tokens for both streams of one
-// row tile (they then wait for one another: +30 %).
+// What bounds it (64 sequences over 32K tokens of 8 heads, 4 rows each, d = 128, so 256 rows: 38.7 us; 8.7e10 flops would take 18.5 us):
+// a tile takes 1900 cycles, of which the tensor unit works 39 %, the schedulers issue 48 % and the special function unit (64
+// exponentials a row) 50 %; a stream's chain - scores, their way to registers, exponentials, P's way to TMEM, P V, a wait of some 100
+// cycles at each - is not covered by the other stream alone.  DRAM is idle at 9 %.  12 over 128K (48 rows of 128 in use): 95 us, 1500
+// cycles a tile, bytes would take 25.7.  The code of the roles' loops is larger than what the SM's instruction cache holds:
+// shorter code pays by itself (waits of ten instructions instead of forty and no second path for tiny V: hits 80 -> 96 %,
+// 43 -> 41 and 104 -> 94 us), and so do products that a whole warp issues, with descriptors in uniform registers (41 -> 38.7).  Tried and
+// not faster: P in two places so that it need not wait for P V (39.1 and 95), two teams that widen in turns (39.7 and 93), K
+// and V freed apart (+5 %), powers of two per record (maxima no longer come with the load: +15 %), one product of 128 tokens for both
+// streams of one row tile (they then wait for one another: +30 %).
 #include <climits>
 #include <cmath>
 #include <type_traits>
@@ -213,7 +215,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefix_attn_kernel(const Prefix
   constexpr uint32_t IDESC_PV = idesc_f32acc(128, D, FMT_F16, false);
   extern __shared__ __align__(1024) uint8_t smem[];
   if (smem_u32(smem) & 1023u) {  // the swizzle of the MMA descriptors assumes 1024-byte aligned tiles
-    start_after_earlier();
+    start_then_let_follower();
     if (threadIdx.x == 0) record_status(a.status, -4 /* SPARGE_ERR_CUDA */);
     return;
   }
@@ -251,7 +253,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefix_attn_kernel(const Prefix
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  start_after_earlier();
+  start_then_let_follower();
   const uint32_t tmem = cs.tmem;
   PfShare share(a);
   int item, tile0, n;  // the piece: tiles tile0 .. tile0 + n - 1 of the item
@@ -869,8 +871,8 @@ double alone_us(int64_t B, int64_t rows, int64_t Hkv, int64_t d, int64_t recs) {
   return mb * (rows <= 8 ? 0.165 : 0.24 * ((rows + 15) / 16));
 }
 double shared_us(const PfPlan &p, int64_t rows, int64_t Hkv, int64_t d, int64_t tiles) {  // two launches more, tiles, rows put together
-  const double tile = d == 128 ? (p.R == 2 ? 1.15 : 0.85) : (p.R == 2 ? 0.9 : 0.6);
-  return 14. + tile * static_cast<double>(p.items) * tiles / CA_SMS + 0.0022 * static_cast<double>(rows) * Hkv;
+  const double tile = d == 128 ? (p.R == 2 ? 1.0 : 0.8) : (p.R == 2 ? 0.85 : 0.55);
+  return 13. + tile * static_cast<double>(p.items) * tiles / CA_SMS + 0.0022 * static_cast<double>(rows) * Hkv;
 }
 
 template <int D, int R>
