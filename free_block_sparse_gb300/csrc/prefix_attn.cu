@@ -749,7 +749,7 @@ struct PfCombineArgs {
 
 constexpr int PC_THREADS = 256, PC_FEW = 8;
 template <int D, int W>
-__global__ void __launch_bounds__(PC_THREADS) prefix_combine_kernel(const PfCombineArgs a) {
+__global__ void __launch_bounds__(PC_THREADS, 4) prefix_combine_kernel(const PfCombineArgs a) {
   constexpr int NL = D / 4, ROWS = PC_THREADS / 32 / W;
   __shared__ float4 part[W > 1 ? PC_THREADS : 1];
   __shared__ float2 part_ml[PC_THREADS / 32];
@@ -942,12 +942,12 @@ cudaError_t launch_prefix_combine(const PrefixAttn &l, const SplitArgs &own, cud
   // Warps of a row: by the shares that it has of the prefix, as long as all rows' warps are resident at once.  Measured at 256 rows
   // of 300 shares: 48 us with a warp each, 15 with eight; 4096 rows of 9: 10 us with one, 20 with four.
   const int64_t shares = ((p.ctas + p.items - 1) / p.items + 1) * (p.R == 2 ? 1 : 2), all = rows * own.Hkv;
-  const int W = shares <= 12 || all > 2048 ? 1 : shares <= 32 || all > 1024 ? 4 : 8, per = PC_THREADS / 32 / W;
+  const int W = shares <= 12 || all > 2048 ? 1 : shares <= 32 || all > 1024 ? 2 : 8, per = PC_THREADS / 32 / W;
   const dim3 grid(static_cast<unsigned>((rows * own.Hkv + per - 1) / per));
   auto run = [&](auto d) {
     constexpr int D = decltype(d)::value;
     return W == 1 ? launch_dependent(prefix_combine_kernel<D, 1>, grid, PC_THREADS, 0, st, a)
-         : W == 4 ? launch_dependent(prefix_combine_kernel<D, 4>, grid, PC_THREADS, 0, st, a)
+         : W == 2 ? launch_dependent(prefix_combine_kernel<D, 2>, grid, PC_THREADS, 0, st, a)
                   : launch_dependent(prefix_combine_kernel<D, 8>, grid, PC_THREADS, 0, st, a);
   };
   return l.d == 128 ? run(std::integral_constant<int, 128>()) : run(std::integral_constant<int, 64>());
