@@ -218,14 +218,14 @@ __global__ void __launch_bounds__(256) bounds_load_kernel(const BoundsArgs a) {
 
 // --------------------------------------------------------------------------------------------
 // Selection, in two kernels.  The first scores pages: all sequences' and heads' pages stand in one line of stretches that is
-// cut into equal shares, one per CTA, so ragged lengths fill the part evenly; a warp takes 16 (d = 64: 32) pages at a time against the
+// cut into equal shares, one per CTA, so ragged lengths fill the part evenly; a warp takes 16 pages at a time against the
 // rows of up to SEL_ROWS query heads, on mma.sync with the codes as f16 (whole numbers up to 127; sums below 2^21 are exact in fp32 in any
 // order).  It is bound by the latency of its chain - page number, bounds, product - so both are loaded a step ahead, 4 KB a warp, and
-// 16 warps share an SM.
+// 16 warps share an SM: 384 lists of up to 8K pages, d = 64, 28 us for 54 MB of bounds (1.9 TB/s, 47 % of the issue slots).
 // The second has a CTA for each list: it takes the list's scores into shared memory, finds the smallest to keep, and writes the
 // pages in order.  That score comes from one histogram of 256 equal steps between the smallest
 // and the largest score, then the scores of the step that holds it are ranked among themselves; more than 256 of them, or infinities
-// at the ends, go digit by digit from the highest bit that differs.
+// at the ends, go digit by digit from the highest bit that differs.  15 us for those lists: barriers and latencies of its six passes.
 // --------------------------------------------------------------------------------------------
 struct SelectArgs {
   const __nv_bfloat16 *q;
@@ -257,8 +257,7 @@ struct SelectArgs {
 };
 
 constexpr int SEL_THREADS = 128, SEL_WARPS = SEL_THREADS / 32, SEL_CTAS = 4;
-__host__ __device__ constexpr int sel_tiles(int) { return 1; }                             // tiles of 16 pages of a warp and step
-__host__ __device__ constexpr int sel_stretch(int D) { return SEL_WARPS * 16 * sel_tiles(D); }  // pages of a CTA and step
+constexpr int SEL_STRETCH = SEL_WARPS * 16;   // pages of a CTA and step
 constexpr int SEL_HEADS = 64, SEL_ROWS = 64;  // query heads of a KV head at most; rows of a round
 constexpr int SEL_PAGES = 32768;              // scores that shared memory holds
 constexpr int LIST_THREADS = 256, LIST_WARPS = LIST_THREADS / 32;
@@ -318,7 +317,6 @@ __device__ __forceinline__ float code_row(const uint32_t (&u)[D / 64], uint8_t *
 template <int D>
 __global__ void __launch_bounds__(SEL_THREADS, SEL_CTAS) select_score_kernel(const SelectArgs a) {
   constexpr int S = D / 8, NP = D / 32;  // steps of a product, 16 codes each, hi's then lo's; 16-byte pieces of a page and lane
-  constexpr int MT = sel_tiles(D), STRETCH = sel_stretch(D);
   __shared__ __align__(16) uint8_t codes[SEL_ROWS * 4 * D];
   __shared__ float2 unit[SEL_ROWS / 2];  // t of the rows
   __shared__ int limit[SEL_ROWS];        // pages to choose from of each query of the round
@@ -327,7 +325,7 @@ __global__ void __launch_bounds__(SEL_THREADS, SEL_CTAS) select_score_kernel(con
   const int i0 = blockIdx.y * a.at_once, ni = min(a.at_once, a.Nq - i0);
   // ---- this CTA's share of the line: every warp for itself; the last query of the round sees the most pages ----
   auto stretches = [&](int b) {
-    return static_cast<int64_t>((a.choices(length_of(a.lens, b, a.width, a.page_shift), i0 + ni - 1) + STRETCH - 1) / STRETCH) * a.Hkv;
+    return static_cast<int64_t>((a.choices(length_of(a.lens, b, a.width, a.page_shift), i0 + ni - 1) + SEL_STRETCH - 1) / SEL_STRETCH) * a.Hkv;
   };
   const int per = (a.B + 31) / 32, bt = min(a.B, lane * per), bu = min(a.B, bt + per);
   int64_t own = 0;
@@ -350,7 +348,7 @@ __global__ void __launch_bounds__(SEL_THREADS, SEL_CTAS) select_score_kernel(con
   b = __shfl_sync(0xffffffffu, b, __ffs(here) - 1);
   off = __shfl_sync(0xffffffffu, off, __ffs(here) - 1);
   while (left > 0) {
-    const int len = length_of(a.lens, b, a.width, a.page_shift), most = a.choices(len, i0 + ni - 1), nst = (most + STRETCH - 1) / STRETCH;
+    const int len = length_of(a.lens, b, a.width, a.page_shift), most = a.choices(len, i0 + ni - 1), nst = (most + SEL_STRETCH - 1) / SEL_STRETCH;
     if (off >= static_cast<int64_t>(nst) * a.Hkv) {
       off -= static_cast<int64_t>(nst) * a.Hkv;
       ++b;
@@ -363,14 +361,12 @@ __global__ void __launch_bounds__(SEL_THREADS, SEL_CTAS) select_score_kernel(con
     const int32_t *table = a.table + static_cast<int64_t>(b) * a.table_stride + a.first;
     const uint8_t *base = a.bounds + h * 2 * D + 16 * c, *scales = a.bounds + a.Hkv * 2 * D + 4 * h;
     // ---- the pages' numbers of the first step, and the queries' codes meanwhile ----
-    const int p_end = min(most, s1 * STRETCH);
-    int p0 = s0 * STRETCH + warp * (16 * MT);
-    int id[MT][2];  // of the step after this one: pages g and g + 8 of each tile
+    const int p_end = min(most, s1 * SEL_STRETCH);
+    int p0 = s0 * SEL_STRETCH + warp * 16;
+    int id[2];  // of the step after this one: pages g and g + 8 of each tile
     auto look_up = [&](int p) {
 #pragma unroll
-      for (int u = 0; u < MT; ++u)
-#pragma unroll
-        for (int y = 0; y < 2; ++y) id[u][y] = p + 16 * u + g + 8 * y < p_end ? table[p + 16 * u + g + 8 * y] : -1;
+      for (int y = 0; y < 2; ++y) id[y] = p + g + 8 * y < p_end ? table[p + g + 8 * y] : -1;
     };
     look_up(p0);
     const int rows = a.tiles ? ni * a.tiles * 8 : ni << a.rows_log, nt = (rows + 7) / 8;
@@ -400,60 +396,57 @@ __global__ void __launch_bounds__(SEL_THREADS, SEL_CTAS) select_score_kernel(con
     float *keys = a.keys + ((static_cast<int64_t>(b) * a.Nq + i0) * a.Hkv + h) * a.pitch + g;
     const int64_t query = static_cast<int64_t>(a.Hkv) * a.pitch;
     __syncthreads();
-    // ---- 16 MT pages a step: lane 4 g + c reads of pages g and g + 8 of a tile the 16 codes from 64 j + 16 c on, and holds the sums of
+    // ---- 16 pages a step: lane 4 g + c reads of pages g and g + 8 of a tile the 16 codes from 64 j + 16 c on, and holds the sums of
     // rows 2c and 2c + 1 with them ----
-    uint4 code[MT][2][NP];
-    float next[MT][2];  // the pages' scales; NaN: there is no such page
+    uint4 code[2][NP];
+    float next[2];  // the pages' scales; NaN: there is no such page
     auto fetch = [&](int p) {
 #pragma unroll
-      for (int u = 0; u < MT; ++u)
+      for (int y = 0; y < 2; ++y) {
+        const bool there = static_cast<uint32_t>(id[y]) < static_cast<uint32_t>(a.n_pages);
+        const int64_t at = static_cast<int64_t>(id[y]) * a.row;
+        if (!there && p + g + 8 * y < p_end) record_status(a.status, -1 /* SPARGE_ERR_INVALID_ARG */);
+        next[y] = __uint_as_float(0x7FFFFFFFu);
 #pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          const bool there = static_cast<uint32_t>(id[u][y]) < static_cast<uint32_t>(a.n_pages);
-          const int64_t at = static_cast<int64_t>(there ? id[u][y] : 0) * a.row;  // (page 0's codes are as good as any)
-          if (!there && p + 16 * u + g + 8 * y < p_end) record_status(a.status, -1 /* SPARGE_ERR_INVALID_ARG */);
+        for (int k = 0; k < NP; ++k) code[y][k] = make_uint4(0u, 0u, 0u, 0u);
+        if (there) {
 #pragma unroll
-          for (int k = 0; k < NP; ++k) code[u][y][k] = *reinterpret_cast<const uint4 *>(base + at + 64 * k);
-          const float sc = *reinterpret_cast<const float *>(scales + at);
-          next[u][y] = there ? sc : __uint_as_float(0x7FFFFFFFu);
+          for (int k = 0; k < NP; ++k) code[y][k] = *reinterpret_cast<const uint4 *>(base + at + 64 * k);
+          next[y] = *reinterpret_cast<const float *>(scales + at);
         }
+      }
     };
     fetch(p0);
-    look_up(p0 + STRETCH);
-    for (; p0 < p_end; p0 += STRETCH) {
-      uint32_t w[MT][S][4];  // the pages' codes as A operands
-      float s[MT][2];
+    look_up(p0 + SEL_STRETCH);
+    for (; p0 < p_end; p0 += SEL_STRETCH) {
+      uint32_t w[S][4];  // the pages' codes as A operands
+      float s[2];
 #pragma unroll
-      for (int u = 0; u < MT; ++u)
+      for (int y = 0; y < 2; ++y) {
+        s[y] = next[y];
 #pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          s[u][y] = next[u][y];
-#pragma unroll
-          for (int k = 0; k < NP; ++k) {
-            const uint4 v = code[u][y][k];
-            widen4(v.x, w[u][4 * k][y], w[u][4 * k][2 + y]);
-            widen4(v.y, w[u][4 * k + 1][y], w[u][4 * k + 1][2 + y]);
-            widen4(v.z, w[u][4 * k + 2][y], w[u][4 * k + 2][2 + y]);
-            widen4(v.w, w[u][4 * k + 3][y], w[u][4 * k + 3][2 + y]);
-          }
+        for (int k = 0; k < NP; ++k) {
+          const uint4 v = code[y][k];
+          widen4(v.x, w[4 * k][y], w[4 * k][2 + y]);
+          widen4(v.y, w[4 * k + 1][y], w[4 * k + 1][2 + y]);
+          widen4(v.z, w[4 * k + 2][y], w[4 * k + 2][2 + y]);
+          widen4(v.w, w[4 * k + 3][y], w[4 * k + 3][2 + y]);
         }
-      fetch(p0 + STRETCH);
-      look_up(p0 + 2 * STRETCH);
-      float best[MT][2];  // of a query of several tiles of rows
-#pragma unroll
-      for (int u = 0; u < MT; ++u) best[u][0] = best[u][1] = -INFINITY;
+      }
+      fetch(p0 + SEL_STRETCH);
+      look_up(p0 + 2 * SEL_STRETCH);
+      float best[2];  // of a query of several tiles of rows
+      best[0] = best[1] = -INFINITY;
       int i = 0, nth = 0;  // of a query of whole tiles: the query, its tile
       const uint8_t *tile = codes + lane * 8;
 #pragma unroll 1
       for (int t = 0; t < nt; ++t, tile += S * 256) {
-        float acc[MT][4];
-#pragma unroll
-        for (int u = 0; u < MT; ++u) acc[u][0] = acc[u][1] = acc[u][2] = acc[u][3] = 0.f;
+        float acc[4];
+        acc[0] = acc[1] = acc[2] = acc[3] = 0.f;
 #pragma unroll
         for (int k = 0; k < S; ++k) {
           const uint2 q = *reinterpret_cast<const uint2 *>(tile + k * 256);
-#pragma unroll
-          for (int u = 0; u < MT; ++u) mma_codes(acc[u], w[u][k][0], w[u][k][1], w[u][k][2], w[u][k][3], q);
+          mma_codes(acc, w[k][0], w[k][1], w[k][2], w[k][3], q);
         }
         const float2 un = unit[t * 4 + c];
         // which lanes write: each its first row's value, the largest of a query's rows; with one row a query its second's too
@@ -463,30 +456,27 @@ __global__ void __launch_bounds__(SEL_THREADS, SEL_CTAS) select_score_kernel(con
         const int lim0 = (put && at < ni ? limit[at] : 0) - p0 - g, lim1 = (!several && at + 1 < ni ? limit[at + 1] : 0) - p0 - g;
         float *to = keys + at * query + p0;
 #pragma unroll
-        for (int u = 0; u < MT; ++u)
-#pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            float v = acc[u][2 * y] * un.x;
-            const float v1 = acc[u][2 * y + 1] * un.y;
-            if (several) {
-              v = fmaxf(v, v1);
-              if (a.rows_log > 1 || a.tiles) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
-              if (a.tiles) {
-                v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
-                best[u][y] = v = fmaxf(best[u][y], v);
-              }
+        for (int y = 0; y < 2; ++y) {
+          float v = acc[2 * y] * un.x;
+          const float v1 = acc[2 * y + 1] * un.y;
+          if (several) {
+            v = fmaxf(v, v1);
+            if (a.rows_log > 1 || a.tiles) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
+            if (a.tiles) {
+              v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
+              best[y] = v = fmaxf(best[y], v);
             }
-            const float sc = s[u][y];
-            auto score = [&](float x) { return sc < INFINITY ? x * sc : sc == INFINITY ? INFINITY : -INFINITY; };
-            const int p = 16 * u + 8 * y;
-            if (p < lim0) to[p] = score(v);
-            if (p < lim1) to[query + p] = score(v1);
           }
+          const float sc = s[y];
+          auto score = [&](float x) { return sc < INFINITY ? x * sc : sc == INFINITY ? INFINITY : -INFINITY; };
+          const int p = 8 * y;
+          if (p < lim0) to[p] = score(v);
+          if (p < lim1) to[query + p] = score(v1);
+        }
         if (a.tiles && ++nth == a.tiles) {
           nth = 0;
           ++i;
-#pragma unroll
-          for (int u = 0; u < MT; ++u) best[u][0] = best[u][1] = -INFINITY;
+          best[0] = best[1] = -INFINITY;
         }
       }
     }
@@ -893,7 +883,7 @@ int sparge_cache4_select(const sparge_tensor *q, const sparge_cache4 *cache, con
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e = cudaSuccess;
   if (width > keep && keep > first + last) {  // else there is nothing to choose
-    const int64_t most = qv.B * c.H * ((width + sel_stretch(c.d) - 1) / sel_stretch(c.d)), ctas = most < 152 * SEL_CTAS ? most : 152 * SEL_CTAS;
+    const int64_t most = qv.B * c.H * ((width + SEL_STRETCH - 1) / SEL_STRETCH), ctas = most < 152 * SEL_CTAS ? most : 152 * SEL_CTAS;
     const dim3 grid(static_cast<unsigned>(ctas), static_cast<unsigned>(rounds));
     e = c.d == 128 ? launch_dependent(select_score_kernel<128>, grid, SEL_THREADS, 0, s, a)
                    : launch_dependent(select_score_kernel<64>, grid, SEL_THREADS, 0, s, a);

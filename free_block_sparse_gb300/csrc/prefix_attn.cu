@@ -863,16 +863,17 @@ PfPlan plan(int64_t rows, int64_t Hkv, int64_t tiles) {
   return p;
 }
 
-// What one of the paths takes beyond what both do, in us, from times measured over 2 to 64 sequences with 1K to 64K shared tokens, 8
-// to 64 query heads over 1 to 8 KV heads and 1 to 4 queries (both sides of the rule's edge: 4 sequences over 64K tokens, 32 over 8
-// heads, d = 128: 57 alone, 68 shared; 8 over 64K: 103 and 70; 8 over 16K: 34 and 32; 16 over 4K: 23 and 27).
+// What one of the paths takes beyond what both do, in us, fitted to 115 pairs of times: 2 to 64 sequences with 1K to 64K shared tokens, 8
+// to 64 query heads over 1 to 8 KV heads, 1 to 4 queries (d = 128, 32 over 8 heads, alone and shared: 4 sequences over 64K tokens
+// 57 and 62, 8 over 64K 103 and 63, 8 over 16K 34 and 31, 16 over 4K 23.0 and 23.3, 2 over 4K 12 and 21).  The rule takes the slower
+// path in two of the pairs, by 8 and 16 %.
 double alone_us(int64_t B, int64_t rows, int64_t Hkv, int64_t d, int64_t recs) {  // the records of every sequence, from L2 for the most part
   const double mb = 18e-6 * static_cast<double>(B) * Hkv * d * recs;
   return mb * (rows <= 8 ? 0.165 : 0.24 * ((rows + 15) / 16));
 }
 double shared_us(const PfPlan &p, int64_t rows, int64_t Hkv, int64_t d, int64_t tiles) {  // two launches more, tiles, rows put together
   const double tile = d == 128 ? (p.R == 2 ? 1.0 : 0.8) : (p.R == 2 ? 0.85 : 0.55);
-  return 13. + tile * static_cast<double>(p.items) * tiles / CA_SMS + 0.0022 * static_cast<double>(rows) * Hkv;
+  return 9. + tile * static_cast<double>(p.items) * tiles / CA_SMS + 0.0022 * static_cast<double>(rows) * Hkv;
 }
 
 template <int D, int R>
@@ -940,7 +941,7 @@ cudaError_t launch_prefix_combine(const PrefixAttn &l, const SplitArgs &own, cud
   a.rec_shift = l.rec_shift;
   a.prefix = l.prefix;
   // Warps of a row: by the shares that it has of the prefix, as long as all rows' warps are resident at once.  Measured at 256 rows
-  // of 300 shares: 48 us with a warp each, 15 with eight; 4096 rows of 9: 10 us with one, 20 with four.
+  // of 300 shares: 48 us with a warp each, 15 with eight; 2048 rows of 20: 75.0 us the whole call with one, 73.6 with two, 75.3 with four.
   const int64_t shares = ((p.ctas + p.items - 1) / p.items + 1) * (p.R == 2 ? 1 : 2), all = rows * own.Hkv;
   const int W = shares <= 12 || all > 2048 ? 1 : shares <= 32 || all > 1024 ? 2 : 8, per = PC_THREADS / 32 / W;
   const dim3 grid(static_cast<unsigned>((rows * own.Hkv + per - 1) / per));

@@ -391,3 +391,28 @@ def test_calls_refuse_what_they_cannot_take():
         with pytest.raises((ValueError, TypeError, fbs.SpargeError)):
             bad()
     assert fbs.device_status() == 0
+
+
+def test_empty_pools_and_batches():
+    """A pool without pages has no token: tables that count some are reported, and nothing is read through them."""
+    d, page = 128, 16
+    pool, bounds = fbs.cache4_pool(0, page, 2, d), fbs.cache4_bounds(0, 2, d)
+    q = torch.ones(3, 4, 1, d, dtype=torch.bfloat16, device="cuda")
+    table = torch.zeros(3, 40, dtype=torch.int32, device="cuda")
+    kv = i32(640, 0, 100)
+    fbs.cache4_bounds_update(pool, table, kv, 640, bounds)
+    assert fbs.device_status() == fbs.SPARGE_ERR_INVALID_ARG
+    pages, lens = fbs.cache4_select(q, pool, bounds, table, kv, 4)
+    assert fbs.device_status() == fbs.SPARGE_ERR_INVALID_ARG
+    assert lens.flatten().tolist() == [64, 0, 52] and (pages[1] == -1).all()
+    out = fbs.cache4_pages_attn(q, pool, pages, lens)
+    assert fbs.device_status() == fbs.SPARGE_ERR_INVALID_ARG and (out == 0).all()
+    for path in (0, SHARED):
+        out = fbs.cache4_prefix_attn(q, pool, table[0, :20].contiguous(), table, kv, path=path)
+        assert fbs.device_status() == fbs.SPARGE_ERR_INVALID_ARG and (out == 0).all()
+    g = gen(68)
+    pool, pages, table, kv, bounds = _setting(g)
+    none = pool.new_empty(0, 8, 1, 128).view(torch.bfloat16).new_empty(0, 8, 1, 128)
+    assert fbs.cache4_prefix_attn(none, pool, pages, table[:0], kv[:0], path=SHARED).shape == (0, 8, 1, 128)
+    got = fbs.cache4_select(none, pool, bounds, table[:0], kv[:0], 4)
+    assert got[0].shape == (0, 1, 2, 4) and fbs.cache4_pages_attn(none, pool, *got).shape == (0, 8, 1, 128)
