@@ -7,6 +7,8 @@
 //
 // Bound by memory: q and k are read once and written once; fp32 arithmetic, one rounding to bf16.
 // Measured at 32K tokens of 32 + 8 heads, d = 128: 104 us for 671 MB, 96% of the measured copy rate.
+// With several position axes (AXES: a pair turns by the position on its own axis, all of a token's positions in registers) 108 us,
+// 93 %; 17776 tokens of 30 + 30 heads, d = 64, three axes: 47 us for 273 MB, 87 %.
 // D / 16 threads share a row, 16 channels each as two 16-byte pieces chosen so that both channels of
 // every pair are in one thread.  A thread keeps its place in the row for all heads of a token, so
 // the angles of its 8 pairs are computed once per token and serve every head of its share, and with

@@ -22,7 +22,7 @@
 // over the same tokens (more than 128 rows) or one tile of rows whose streams take the token tiles in turns.  The line of all
 // (KV head, row group) items' tiles is cut into equal shares, so any batch fills all SMs.
 //
-// What bounds it (64 sequences over 32K tokens of 8 heads, 4 rows each, d = 128, so 256 rows: 38.7 us; 8.7e10 flops would take 18.5 us):
+// What bounds it (64 sequences over 32K tokens of 8 heads, 4 rows each, d = 128, so 256 rows: 38.7 us; 3.5e10 flops would take 18.5 us):
 // a tile takes 1900 cycles, of which the tensor unit works 39 %, the schedulers issue 48 % and the special function unit (64
 // exponentials a row) 50 %; a stream's chain - scores, their way to registers, exponentials, P's way to TMEM, P V, a wait of some 100
 // cycles at each - is not covered by the other stream alone.  DRAM is idle at 9 %.  12 over 128K (48 rows of 128 in use): 95 us, 1500
