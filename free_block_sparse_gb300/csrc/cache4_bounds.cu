@@ -64,6 +64,9 @@ __device__ __forceinline__ int length_of(const int32_t *lens, int b, int width, 
 // the channels 32 w + 8 c + j of every eighth token (the order of the codes in memory: 16-byte loads without gaps) and keeps their
 // maxima and minima in registers; at the page's end the eight lanes of a channel exchange halves (28 + 28 values
 // instead of 96 + 96) until each holds four channels in a row.
+// Four dependent latencies (length, page, records, write) bound it and, with many pages, its instructions (44 % of the issue slots): an update
+// for 256 sequences of one new token and the reading back of their pages take 9.6 us, for 4 of 8192 14.9 (23 MB).  Two warps
+// for a page's 128 channels, twice the warps resident: 10.4 and 17.6.
 template <int D>
 __global__ void __launch_bounds__(128) bounds_update_kernel(const BoundsArgs a) {
   using R = Rec4<D>;
@@ -221,11 +224,11 @@ __global__ void __launch_bounds__(256) bounds_load_kernel(const BoundsArgs a) {
 // cut into equal shares, one per CTA, so ragged lengths fill the part evenly; a warp takes 16 pages at a time against the
 // rows of up to SEL_ROWS query heads, on mma.sync with the codes as f16 (whole numbers up to 127; sums below 2^21 are exact in fp32 in any
 // order).  It is bound by the latency of its chain - page number, bounds, product - so both are loaded a step ahead, 4 KB a warp, and
-// 16 warps share an SM: 384 lists of up to 8K pages, d = 64, 28 us for 54 MB of bounds (1.9 TB/s, 47 % of the issue slots).
+// 16 warps share an SM: 384 lists of up to 8K pages, d = 64, 24 us for 54 MB of bounds (2.2 TB/s).
 // The second has a CTA for each list: it takes the list's scores into shared memory, finds the smallest to keep, and writes the
 // pages in order.  That score comes from one histogram of 256 equal steps between the smallest
 // and the largest score, then the scores of the step that holds it are ranked among themselves; more than 256 of them, or infinities
-// at the ends, go digit by digit from the highest bit that differs.  15 us for those lists: barriers and latencies of its six passes.
+// at the ends, go digit by digit from the highest bit that differs.  14 us for those lists: barriers and latencies of its six passes.
 // --------------------------------------------------------------------------------------------
 struct SelectArgs {
   const __nv_bfloat16 *q;
@@ -256,11 +259,12 @@ struct SelectArgs {
   }
 };
 
-constexpr int SEL_THREADS = 128, SEL_WARPS = SEL_THREADS / 32, SEL_CTAS = 4;
+constexpr int SEL_THREADS = 128, SEL_WARPS = SEL_THREADS / 32;
+// of an SM; d = 128: four (128 registers, spills) took 23.0 us a call for 8 lists of 512 pages and 88.5 for 512, three 21.8 and 85.7
+__host__ __device__ constexpr int sel_ctas(int D) { return D == 128 ? 3 : 4; }
 constexpr int SEL_STRETCH = SEL_WARPS * 16;   // pages of a CTA and step
 constexpr int SEL_HEADS = 64, SEL_ROWS = 64;  // query heads of a KV head at most; rows of a round
 constexpr int SEL_PAGES = 32768;              // scores that shared memory holds
-constexpr int LIST_THREADS = 256, LIST_WARPS = LIST_THREADS / 32;
 
 // Codes as f16, two channels a register.
 __device__ __forceinline__ uint32_t half2_of(int lo, int hi) {
@@ -315,7 +319,7 @@ __device__ __forceinline__ float code_row(const uint32_t (&u)[D / 64], uint8_t *
 }
 
 template <int D>
-__global__ void __launch_bounds__(SEL_THREADS, SEL_CTAS) select_score_kernel(const SelectArgs a) {
+__global__ void __launch_bounds__(SEL_THREADS, sel_ctas(D)) select_score_kernel(const SelectArgs a) {
   constexpr int S = D / 8, NP = D / 32;  // steps of a product, 16 codes each, hi's then lo's; 16-byte pieces of a page and lane
   __shared__ __align__(16) uint8_t codes[SEL_ROWS * 4 * D];
   __shared__ float2 unit[SEL_ROWS / 2];  // t of the rows
@@ -398,7 +402,7 @@ __global__ void __launch_bounds__(SEL_THREADS, SEL_CTAS) select_score_kernel(con
     __syncthreads();
     // ---- 16 pages a step: lane 4 g + c reads of pages g and g + 8 of a tile the 16 codes from 64 j + 16 c on, and holds the sums of
     // rows 2c and 2c + 1 with them ----
-    uint4 code[2][NP];
+    uint4 code[2][NP] = {};  // (of a page that is not there: those of one before)
     float next[2];  // the pages' scales; NaN: there is no such page
     auto fetch = [&](int p) {
 #pragma unroll
@@ -407,8 +411,6 @@ __global__ void __launch_bounds__(SEL_THREADS, SEL_CTAS) select_score_kernel(con
         const int64_t at = static_cast<int64_t>(id[y]) * a.row;
         if (!there && p + g + 8 * y < p_end) record_status(a.status, -1 /* SPARGE_ERR_INVALID_ARG */);
         next[y] = __uint_as_float(0x7FFFFFFFu);
-#pragma unroll
-        for (int k = 0; k < NP; ++k) code[y][k] = make_uint4(0u, 0u, 0u, 0u);
         if (there) {
 #pragma unroll
           for (int k = 0; k < NP; ++k) code[y][k] = *reinterpret_cast<const uint4 *>(base + at + 64 * k);
@@ -483,10 +485,11 @@ __global__ void __launch_bounds__(SEL_THREADS, SEL_CTAS) select_score_kernel(con
   }
 }
 
+template <int T>  // threads of a list's CTA
 struct ListShared {
   uint32_t hist[256];
-  float cand[LIST_THREADS], red[2][LIST_WARPS];
-  uint32_t count[LIST_WARPS][2], found[3], n_cand;
+  float cand[T], red[2][T / 32];
+  uint32_t count[T / 32][2], found[3], n_cand;
   float bound;
 };
 
@@ -498,7 +501,8 @@ __device__ __forceinline__ float warp_min(float x) {
 __device__ __forceinline__ float warp_max(float x) { return -warp_min(-x); }
 
 // minimum and maximum over the CTA
-__device__ __forceinline__ void min_max(ListShared &sh, float &low, float &high) {
+template <int T>
+__device__ __forceinline__ void min_max(ListShared<T> &sh, float &low, float &high) {
   low = warp_min(low);
   high = warp_max(high);
   __syncthreads();
@@ -508,13 +512,14 @@ __device__ __forceinline__ void min_max(ListShared &sh, float &low, float &high)
   }
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < LIST_WARPS; ++w) {
+  for (int w = 0; w < T / 32; ++w) {
     low = fminf(low, sh.red[0][w]);
     high = fmaxf(high, sh.red[1][w]);
   }
 }
 // The histogram's place (found[0]) that holds the want-th largest, its rank there (found[1]) and the place's count (found[2]).
-__device__ __forceinline__ void find_place(ListShared &sh, uint32_t want) {
+template <int T>
+__device__ __forceinline__ void find_place(ListShared<T> &sh, uint32_t want) {
   __syncthreads();
   if (threadIdx.x < 32) {  // lane l: places 8 (31 - l) + 7 .. 8 (31 - l), from the largest down
     const int lane = threadIdx.x;
@@ -547,12 +552,12 @@ __device__ __forceinline__ void find_place(ListShared &sh, uint32_t want) {
 
 // f(score) for every score, four at a time of a thread.  The array is filled up to whole fours with -inf: below or equal to every score,
 // and behind all of them.
-template <typename F>
+template <int T, typename F>
 __device__ __forceinline__ void each_score(const float *scores, int m, F f) {
   const float4 *at = reinterpret_cast<const float4 *>(scores);
   const int n = (m + 3) / 4;
 #pragma unroll 4
-  for (int k = threadIdx.x; k < n; k += LIST_THREADS) {
+  for (int k = threadIdx.x; k < n; k += T) {
     const float4 v = at[k];
     f(v.x);
     f(v.y);
@@ -563,8 +568,9 @@ __device__ __forceinline__ void each_score(const float *scores, int m, F f) {
 
 // The want-th largest of m scores, and how many of its equals are among the want largest.  Called by the whole CTA; low and high:
 // the smallest and the largest score that the thread has seen.
-__device__ __forceinline__ void want_th(ListShared &sh, const float *scores, int m, int want, float low, float high, float &bound, int &left) {
-  sh.hist[threadIdx.x] = 0u;
+template <int T>
+__device__ __forceinline__ void want_th(ListShared<T> &sh, const float *scores, int m, int want, float low, float high, float &bound, int &left) {
+  if (threadIdx.x < 256) sh.hist[threadIdx.x] = 0u;
   if (threadIdx.x == 0) sh.n_cand = 0u;
   min_max(sh, low, high);
   const float range = high - low;
@@ -572,12 +578,12 @@ __device__ __forceinline__ void want_th(ListShared &sh, const float *scores, int
   if (range > 1e-30f && range < 1e30f) {
     const float step = 255.f / range, zero = low;
     auto place = [&](float x) { return min(static_cast<uint32_t>((x - zero) * step), 255u); };  // (-inf: 0)
-    each_score(scores, m, [&](float x) { atomicAdd(&sh.hist[place(x)], 1u); });
+    each_score<T>(scores, m, [&](float x) { atomicAdd(&sh.hist[place(x)], 1u); });
     find_place(sh, static_cast<uint32_t>(want));
     const uint32_t at = sh.found[0], n = sh.found[2];
     left = static_cast<int>(sh.found[1]);
-    if (n <= LIST_THREADS) {
-      each_score(scores, m, [&](float x) {
+    if (n <= T) {
+      each_score<T>(scores, m, [&](float x) {
         if (place(x) == at) sh.cand[atomicAdd(&sh.n_cand, 1u)] = x;
       });
       __syncthreads();
@@ -600,7 +606,7 @@ __device__ __forceinline__ void want_th(ListShared &sh, const float *scores, int
     }
     low = INFINITY;
     high = -INFINITY;
-    each_score(scores, m, [&](float x) {
+    each_score<T>(scores, m, [&](float x) {
       if (place(x) == at) {
         low = fminf(low, x);
         high = fmaxf(high, x);
@@ -619,9 +625,9 @@ __device__ __forceinline__ void want_th(ListShared &sh, const float *scores, int
   while (top > 0) {
     const int shift = max(top - 8, 0);
     __syncthreads();
-    sh.hist[threadIdx.x] = 0u;
+    if (threadIdx.x < 256) sh.hist[threadIdx.x] = 0u;
     __syncthreads();
-    each_score(scores, m, [&](float x) {
+    each_score<T>(scores, m, [&](float x) {
       const uint32_t k = key_of(x);
       if (k >= first && k <= last && (top == 32 || (k >> top) == (key >> top)))
         atomicAdd(&sh.hist[(k >> shift) & ((1u << (top - shift)) - 1u)], 1u);
@@ -634,9 +640,10 @@ __device__ __forceinline__ void want_th(ListShared &sh, const float *scores, int
   bound = __uint_as_float((key & 0x80000000u) ? key & 0x7FFFFFFFu : ~key);
 }
 
-__global__ void __launch_bounds__(LIST_THREADS) select_list_kernel(const SelectArgs a) {
+template <int T>
+__global__ void __launch_bounds__(T) select_list_kernel(const SelectArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ ListShared sh;
+  __shared__ ListShared<T> sh;
   start_after_earlier();
   float4 *scores = reinterpret_cast<float4 *>(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, P = 1 << a.page_shift;
@@ -651,7 +658,7 @@ __global__ void __launch_bounds__(LIST_THREADS) select_list_kernel(const SelectA
   float low = INFINITY, high = -INFINITY;
   const float4 *from = reinterpret_cast<const float4 *>(a.keys + list * a.pitch);
 #pragma unroll 4
-  for (int k = threadIdx.x; k < m4; k += LIST_THREADS) {
+  for (int k = threadIdx.x; k < m4; k += T) {
     float4 v = from[k];
     if (4 * k + 3 >= m) {
       if (4 * k + 1 >= m) v.y = -INFINITY;
@@ -663,7 +670,7 @@ __global__ void __launch_bounds__(LIST_THREADS) select_list_kernel(const SelectA
     scores[k] = v;
   }
   // every page, or those that are kept whatever their scores; then the places without one
-  for (int k = threadIdx.x; k < a.keep; k += LIST_THREADS) {
+  for (int k = threadIdx.x; k < a.keep; k += T) {
     const bool middle = np > a.keep && k >= a.first && k < a.keep - a.last;
     if (!middle) out[k] = k >= n ? -1 : table[np > a.keep && k >= a.first ? np - (a.keep - k) : k];
   }
@@ -674,7 +681,7 @@ __global__ void __launch_bounds__(LIST_THREADS) select_list_kernel(const SelectA
   want_th(sh, reinterpret_cast<const float *>(scores), m, a.keep - a.first - a.last, low, high, bound, left);
   // scores above the bound, and the first `left` that equal it: every warp a stretch, a lane four in a row; counts of those above in
   // the low and of equal ones in the high half
-  const int per = (m4 + LIST_THREADS - 1) / LIST_THREADS * 32, f0 = min(warp * per, m4), f1 = min(f0 + per, m4);
+  const int per = (m4 + T - 1) / T * 32, f0 = min(warp * per, m4), f1 = min(f0 + per, m4);
   auto counts = [&](const float4 &v) {
     return (v.x > bound) + (v.y > bound) + (v.z > bound) + (v.w > bound) +
            (((v.x == bound) + (v.y == bound) + (v.z == bound) + (v.w == bound)) << 16);
@@ -722,7 +729,14 @@ __global__ void __launch_bounds__(LIST_THREADS) select_list_kernel(const SelectA
   }
   // places in the sequence's row become pages, all at once
   __syncthreads();
-  for (int k = a.first + threadIdx.x; k < a.keep - a.last; k += LIST_THREADS) out[k] = table[out[k]];
+  for (int k = a.first + threadIdx.x; k < a.keep - a.last; k += T) out[k] = table[out[k]];
+}
+
+template <int T>
+cudaError_t launch_list(const SelectArgs &a, int64_t lists, cudaStream_t s) {
+  static std::atomic<unsigned long long> smem_set{0};
+  if (cudaError_t e = set_smem_limit_once(select_list_kernel<T>, SEL_PAGES * 4, smem_set); e != cudaSuccess) return e;
+  return launch_dependent(select_list_kernel<T>, dim3(static_cast<unsigned>(lists)), T, static_cast<size_t>((a.width + 3) / 4 * 16), s, a);
 }
 
 // A bounds array for the pool: its bytes fit and it is aligned.
@@ -883,17 +897,13 @@ int sparge_cache4_select(const sparge_tensor *q, const sparge_cache4 *cache, con
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e = cudaSuccess;
   if (width > keep && keep > first + last) {  // else there is nothing to choose
-    const int64_t most = qv.B * c.H * ((width + SEL_STRETCH - 1) / SEL_STRETCH), ctas = most < 152 * SEL_CTAS ? most : 152 * SEL_CTAS;
+    const int64_t most = qv.B * c.H * ((width + SEL_STRETCH - 1) / SEL_STRETCH), full = 152 * sel_ctas(c.d), ctas = most < full ? most : full;
     const dim3 grid(static_cast<unsigned>(ctas), static_cast<unsigned>(rounds));
     e = c.d == 128 ? launch_dependent(select_score_kernel<128>, grid, SEL_THREADS, 0, s, a)
                    : launch_dependent(select_score_kernel<64>, grid, SEL_THREADS, 0, s, a);
   }
-  if (e == cudaSuccess) {
-    static std::atomic<unsigned long long> smem_set{0};
-    e = set_smem_limit_once(select_list_kernel, SEL_PAGES * 4, smem_set);
-  }
-  if (e == cudaSuccess)
-    e = launch_dependent(select_list_kernel, dim3(static_cast<unsigned>(lists)), LIST_THREADS, static_cast<size_t>((width + 3) / 4 * 16), s, a);
+  // threads of a list: 512 lists over up to 512 pages 84.9 us a call with 256, 86.3 with 512; 384 lists over up to 8192 66 and 58
+  if (e == cudaSuccess) e = width > 2048 ? launch_list<512>(a, lists, s) : launch_list<256>(a, lists, s);
   return e == cudaSuccess ? SPARGE_OK : cuda_fail(e, "page selection launch");
 }
 
