@@ -4,7 +4,7 @@
 //   minimum; left as shares (reference m, sum l, sum P V) that prefix_combine_kernel puts together with those of the
 //   sequences' own tokens, which the cache attention makes.
 //
-// A sequence by itself reads every shared record again: 64 sequences over 32K tokens of 8 heads are 1.2 GB from L2, 196 us.  Here a
+// A sequence by itself reads every shared record again: 64 sequences over 32K tokens of 8 heads are 2.4 GB from L2, 370 us.  Here a
 // record is read once, and its codes, widened once, serve 256 rows.
 //
 // Widening.  A code n is the subnormal f16 n 2^-24 once its four bits are masked out in place, so one fma.rn.f16x2 with (s 2^(f + 24),
