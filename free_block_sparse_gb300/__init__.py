@@ -491,6 +491,8 @@ def rope_axes(sections, woven: bool = False, device="cuda"):
     """The axis of each rotated pair, int32, for qk_norm_rope_axes: sections[x] pairs of axis x, one axis after the other, or
     (woven) the axes taking turns pair by pair while they have pairs left."""
     torch = _torch()
+    if any(n < 0 for n in sections):
+        raise ValueError("sections must not be negative: %r" % (tuple(sections),))
     if woven:
         left, axes = list(sections), []
         while any(left):
@@ -571,7 +573,8 @@ def cache4_bounds(n_pages: int, H: int, d: int, device="cuda"):
 
 def cache4_bounds_update(pool, table, kv_lens, N: int, bounds):
     """Renews the bounds of the pages on which the last N of each sequence's kv_lens[b] tokens lie (after a
-    cache4_store of N new ones); table ((B, width) int32) and kv_lens as cache4_attn takes them."""
+    cache4_store of N new ones); table ((B, width) int32) and kv_lens as cache4_attn takes them.  Sequences that share a page have to
+    hold the same number of its tokens."""
     (_binding_module or _load_binding()).cache4_bounds_update(pool, table, kv_lens, N, bounds)
 
 

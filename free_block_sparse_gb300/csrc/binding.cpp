@@ -529,7 +529,8 @@ PyObject *cache4_prefix_attn(const Args &a) {
   const int64_t stride = h.table(table, dq.B);
   const int32_t *lens = static_cast<int32_t *>(h.array(a.tensor(4, "kv_lens"), at::kInt, "kv_lens", {dq.B}));
   const float scale = a.real(5);
-  const int path = static_cast<int>(a.integer(6));
+  const int64_t given = a.integer(6);
+  const int path = given == static_cast<int>(given) ? static_cast<int>(given) : -1;
   at::Tensor out = given_rows(a, 7, h, "out"), ws = given_workspace(a, 8, h);
   done(unlocked([&] {
     if (!out.defined()) out = h.make_like(q);

@@ -120,6 +120,22 @@ def test_sizes(lib):
         assert f(65536, 32, 8, 1, 128) == 0 and f(65535, 32, 32, 1 << 30, 128) == 0
 
 
+def test_rope_axes():
+    pytest.importorskip("torch")
+    assert fbs.rope_axes((2, 0, 3), device="cpu").tolist() == [0, 0, 2, 2, 2]
+    assert fbs.rope_axes((2, 0, 3), woven=True, device="cpu").tolist() == [0, 2, 0, 2, 2]
+    assert fbs.rope_axes((), woven=True, device="cpu").numel() == 0
+    for woven in (False, True):
+        with pytest.raises(ValueError):
+            fbs.rope_axes((3, -1), woven=woven, device="cpu")
+
+
+def test_grid_positions_on_the_host():
+    pytest.importorskip("torch")
+    pos = fbs.rope_grid_positions(2, 1, 2, 2, device="cpu")
+    assert pos.tolist() == [[[0, 1, 2, 2, 2, 2]], [[0, 1, 2, 2, 3, 3]], [[0, 1, 2, 3, 2, 3]]]
+
+
 def test_binding_refuses_host_tensors(lib):
     torch = pytest.importorskip("torch")
     t4 = torch.zeros(1, 1, 1, 64, dtype=torch.bfloat16)
