@@ -18,13 +18,12 @@
 // g = -f of V: V's powers enter through P, and ref follows the largest x + g of the row when a P' passes 2^15, so O needs no rescaling
 // when V's sizes change from tile to tile.  l is summed in fp32 against a reference m of its own.  Q is f16 times a power of two per row.
 //
-// A CTA holds two streams, each with its softmax warps, its thread that issues products, and its S, P and O: two tiles of 128 rows
+// A CTA holds two streams, each with its softmax warps, its warp that issues products, and its S, P and O: two tiles of 128 rows
 // over the same tokens (more than 128 rows) or one tile of rows whose streams take the token tiles in turns.  The line of all
 // (KV head, row group) items' tiles is cut into equal shares, so any batch fills all SMs.
 //
 // What bounds it (64 sequences over 32K tokens of 8 heads, 4 rows each, d = 128, so 256 rows: 38.7 us; 3.5e10 flops would take 18.5 us):
-// a tile takes 1900 cycles, of which the tensor unit works 39 %, the schedulers issue 48 % and the special function unit (64
-// exponentials a row) 50 %; a stream's chain - scores, their way to registers, exponentials, P's way to TMEM, P V, a wait of some 100
+// a tile takes 1900 cycles, of which the tensor unit works 39 %, the schedulers issue 48 % and the special function unit 20 %; a stream's chain - scores, their way to registers, exponentials, P's way to TMEM, P V, a wait of some 100
 // cycles at each - is not covered by the other stream alone.  DRAM is idle at 9 %.  12 over 128K (48 rows of 128 in use): 95 us, 1500
 // cycles a tile, bytes would take 25.7.  The code of the roles' loops is larger than what the SM's instruction cache holds:
 // shorter code pays by itself (waits of ten instructions instead of forty and no second path for tiny V: hits 80 -> 96 %,
@@ -35,8 +34,6 @@
 #include <climits>
 #include <cmath>
 #include <type_traits>
-
-#include <cuda_fp16.h>
 
 #include "cache4.cuh"
 #include "common.cuh"
@@ -361,7 +358,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefix_attn_kernel(const Prefix
       }
       // m: the reference of l = sum of P, P = 2^(x - m); ref: that of O = sum of P' V', P' = 2^(x + g - ref).  Both are set to the
       // largest that the row sees when a term passes 2^15 of them; what the sums hold is then scaled down.  So neither an improbable token
-      // nor the size of V in another record takes bits from the rest.
+      // nor the size of V in another tile takes bits from the rest.
       float m = -INFINITY, ref = -INFINITY, l = 0.f;
       const int jobs = R == 2 ? n : (n - t + 1) / 2;
       for (int j = 0; j < jobs; ++j, ++done) {
