@@ -28,8 +28,8 @@
 // cycles a tile, bytes would take 25.7.  The code of the roles' loops is larger than what the SM's instruction cache holds:
 // shorter code pays by itself (waits of ten instructions instead of forty and no second path for tiny V: hits 80 -> 96 %,
 // 43 -> 41 and 104 -> 94 us), and so do products that a whole warp issues, with descriptors in uniform registers (41 -> 38.7).  Tried and
-// not faster: P in two places so that it need not wait for P V (39.1 and 95), two teams that widen in turns (39.7 and 93), K
-// and V freed apart (+5 %), powers of two per record (maxima no longer come with the load: +15 %), one product of 128 tokens for both
+// not faster: P in two places so that it need not wait for P V (39.1 and 95), scores in two places with P over them
+// (39.0 and 95), two threads a row (46 and 95), two teams that widen in turns (39.7 and 93), K and V freed apart (+5 %), powers of two per record (maxima no longer come with the load: +15 %), one product of 128 tokens for both
 // streams of one row tile (they then wait for one another: +30 %).
 #include <climits>
 #include <cmath>
