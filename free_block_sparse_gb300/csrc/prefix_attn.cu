@@ -23,14 +23,16 @@
 // (KV head, row group) items' tiles is cut into equal shares, so any batch fills all SMs.
 //
 // What bounds it (64 sequences over 32K tokens of 8 heads, 4 rows each, d = 128, so 256 rows: 38.7 us; 3.5e10 flops would take 18.5 us):
-// a tile takes 1900 cycles, of which the tensor unit works 39 %, the schedulers issue 48 % and the special function unit 20 %; a stream's chain - scores, their way to registers, exponentials, P's way to TMEM, P V, a wait of some 100
-// cycles at each - is not covered by the other stream alone.  DRAM is idle at 9 %.  12 over 128K (48 rows of 128 in use): 95 us, 1500
+// a tile takes 1900 cycles, of which the tensor unit works 39 %, the schedulers issue 48 % and the special function unit 20 %.  The
+// score products with N = 64 and Q from shared memory take 600 of them a stream where their arithmetic would take 340, P V 270, and a
+// stream's chain - scores, their way to registers, exponentials, P's way to TMEM, P V, a wait of some 100 cycles at each - is
+// not covered by the other stream alone.  DRAM is idle at 9 %.  12 over 128K (48 rows of 128 in use): 95 us, 1500
 // cycles a tile, bytes would take 25.7.  The code of the roles' loops is larger than what the SM's instruction cache holds:
 // shorter code pays by itself (waits of ten instructions instead of forty and no second path for tiny V: hits 80 -> 96 %,
 // 43 -> 41 and 104 -> 94 us), and so do products that a whole warp issues, with descriptors in uniform registers (41 -> 38.7).  Tried and
 // not faster: P in two places so that it need not wait for P V (39.1 and 95), scores in two places with P over them
-// (39.0 and 95), two threads a row (46 and 95), two teams that widen in turns (39.7 and 93), K and V freed apart (+5 %), powers of two per record (maxima no longer come with the load: +15 %), one product of 128 tokens for both
-// streams of one row tile (they then wait for one another: +30 %).
+// (39.0 and 95), two threads a row (46 and 95), two teams that widen in turns (39.7 and 93), K and V freed apart (+5 %), powers of two
+// per record (maxima no longer come with the load: +15 %), one product of 128 tokens for both streams of one row tile (they then wait for one another: +30 %).
 #include <climits>
 #include <cmath>
 #include <type_traits>
