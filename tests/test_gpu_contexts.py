@@ -2,7 +2,8 @@
 page bounds and the selection by them, attention over selected pages, attention behind a shared prefix.
 
 Tolerances.  Rotation and attention over pages as in test_gpu_serving.py (the same arithmetic).  Bounds, selections and lengths are
-exact."""
+exact.  Attention behind a prefix rounds the shared keys and values to f16 beside that (test_gpu_contexts_edges.py counts it); the
+cases here keep to the cache attention's tolerance all the same, their elements' roundings pointing both ways."""
 import math
 
 import pytest

@@ -416,3 +416,25 @@ def test_empty_pools_and_batches():
     assert fbs.cache4_prefix_attn(none, pool, pages, table[:0], kv[:0], path=SHARED).shape == (0, 8, 1, 128)
     got = fbs.cache4_select(none, pool, bounds, table[:0], kv[:0], 4)
     assert got[0].shape == (0, 1, 2, 4) and fbs.cache4_pages_attn(none, pool, *got).shape == (0, 8, 1, 128)
+
+
+@pytest.mark.parametrize("Hq,Hkv,Nq,d,own", [(8, 2, 33, 128, [40, 33, 700]), (64, 1, 1, 64, [5, 1, 17]), (64, 1, 3, 128, [5, 100])])
+def test_prefix_many_rows_of_a_sequence(Hq, Hkv, Nq, d, own):
+    """Chunks of queries and wide groups: rows of one sequence in several row tiles and warps."""
+    g = gen(69)
+    pool, pages, table, lens = shared(g, 704, own, Hkv, d, 16)
+    q = rand(g, len(own), Hq, Nq, d)
+    out = fbs.cache4_prefix_attn(q, pool, pages, table, i32(*lens), path=SHARED)
+    check_prefix(q, pool, table, lens, out, d)
+
+
+def test_prefix_lengths_outside_the_table():
+    """Negative lengths are nothing, lengths past the table all of it."""
+    g = gen(70)
+    d, page, prefix = 128, 16, 320
+    pool, pages, table, lens = shared(g, prefix, [48, 48, 48], 2, d, page)
+    q = rand(g, 3, 4, 2, d)
+    want = fbs.cache4_prefix_attn(q, pool, pages, table, i32(368, 0, 368), path=SHARED)
+    got = fbs.cache4_prefix_attn(q, pool, pages, table, i32(2 ** 31 - 1, -(2 ** 31), 369), path=SHARED)
+    assert torch.equal(want, got) and (got[1] == 0).all()
+    check_prefix(q[:1], pool, table[:1], [368], got[:1], d)
