@@ -706,16 +706,32 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefix_attn_kernel(const Prefix
       const uint32_t rs = tile % RS;
       if (!__all_sync(0xffffffffu, pf_wait(&cs.raw_full[rs], (tile / RS) & 1, abort))) break;
       const uint32_t bad = *reinterpret_cast<const uint32_t *>(cs.bad[rs]);  // a byte a record
+      // lane 8 rec + k looks at the k-th eighth of a record's words: their exponents' maxima, two at a time
+      const int rec = lane >> 3;
+      const uint8_t *at = smem + C::RING + rs * C::RAW + rec * C::PITCH + (lane & 7) * (8 * NG);
+      uint32_t u[2][2 * NG], top[2];
+      if constexpr (NG == 2) {
+        const uint4 x = *reinterpret_cast<const uint4 *>(at + Rec::KW), y = *reinterpret_cast<const uint4 *>(at + Rec::VW);
+        u[0][0] = x.x; u[0][1] = x.y; u[0][2] = x.z; u[0][3] = x.w;
+        u[1][0] = y.x; u[1][1] = y.y; u[1][2] = y.z; u[1][3] = y.w;
+      } else {
+        const uint2 x = *reinterpret_cast<const uint2 *>(at + Rec::KW), y = *reinterpret_cast<const uint2 *>(at + Rec::VW);
+        u[0][0] = x.x; u[0][1] = x.y;
+        u[1][0] = y.x; u[1][1] = y.y;
+      }
+      const bool there = ((bad >> (8 * rec)) & 1u) == 0u;
       int f[2];  // of K, V
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
-        int need = -200;
+        top[s] = 0u;
 #pragma unroll
-        for (int p = 0; p < 2; ++p) {  // lane 16 y + t looks at token t of records 2 p + y
-          const int rec = 2 * p + (lane >> 4);
-          const uint8_t *at = smem + C::RING + rs * C::RAW + rec * C::PITCH + (s ? Rec::VW : Rec::KW) + (lane & 15) * NG * 4;
+        for (int k = 0; k < 2 * NG; ++k) top[s] = __vmaxu2(top[s], u[s][k] & 0x7F807F80u);
+        const int lo = top[s] & 0xFFFFu, hi = top[s] >> 16;
+        int need = there ? max((lo >> 7) + 9, (hi >> 7) - 13) - 127 : -200;
+        if (__any_sync(0xffffffffu, there && max(lo, hi) == 0x7F80)) {  // words that are not finite are passed over one by one
+          need = -200;
 #pragma unroll
-          for (int g = 0; g < NG; ++g) need = max(need, (bad >> (8 * rec)) & 1u ? -200 : pf_need(*reinterpret_cast<const uint32_t *>(at + 4 * g)));
+          for (int k = 0; k < 2 * NG; ++k) need = max(need, there ? pf_need(u[s][k]) : -200);
         }
         f[s] = pf_power(__reduce_max_sync(0xffffffffu, need));
       }
