@@ -26,12 +26,14 @@
 // a tile takes 1900 cycles, of which the tensor unit works 39 %, the schedulers issue 48 % and the special function unit 20 %.  The
 // score products with N = 64 and Q from shared memory take 600 of them a stream where their arithmetic would take 340, P V 270, and a
 // stream's chain - scores, their way to registers, exponentials, P's way to TMEM, P V, a wait of some 100 cycles at each - is
-// not covered by the other stream alone.  DRAM is idle at 9 %.  12 over 128K (48 rows of 128 in use): 95 us, 1500
-// cycles a tile, bytes would take 25.7.  The code of the roles' loops is larger than what the SM's instruction cache holds:
+// not covered by the other stream alone.  DRAM is idle at 9 %.  12 over 128K (48 rows of 128 in use): 85 us, 1300
+// cycles a tile, as long as its widening takes four warps with their waits; bytes would take 25.7.  Every role is a warp or four that
+// take the tiles one by one, so none may take longer than the rest: the powers of two cost their warp 1100 cycles a tile word by word and
+// 600 from packed maxima (95 -> 85 us).  The code of the roles' loops is larger than what the SM's instruction cache holds:
 // shorter code pays by itself (waits of ten instructions instead of forty and no second path for tiny V: hits 80 -> 96 %,
 // 43 -> 41 and 104 -> 94 us), and so do products that a whole warp issues, with descriptors in uniform registers (41 -> 38.7).  Tried and
-// not faster: P in two places so that it need not wait for P V (39.1 and 95), scores in two places with P over them
-// (39.0 and 95), two threads a row (46 and 95), two teams that widen in turns (39.7 and 93), K and V freed apart (+5 %), powers of two
+// not faster: P in two places so that it need not wait for P V (39.1), scores in two places with P over them (39.0),
+// two threads a row (46), eight warps that widen, in turns (39.5 and 83) or together (41 and 84), K and V freed apart (+5 %), powers of two
 // per record (maxima no longer come with the load: +15 %), one product of 128 tokens for both streams of one row tile (they then wait for one another: +30 %).
 #include <climits>
 #include <cmath>
@@ -880,8 +882,8 @@ PfPlan plan(int64_t rows, int64_t Hkv, int64_t tiles) {
 
 // What one of the paths takes beyond what both do, in us, fitted to 115 pairs of times: 2 to 64 sequences with 1K to 64K shared tokens, 8
 // to 64 query heads over 1 to 8 KV heads, 1 to 4 queries (d = 128, 32 over 8 heads, alone and shared: 4 sequences over 64K tokens
-// 57 and 62, 8 over 64K 103 and 63, 8 over 16K 34 and 31, 16 over 4K 23.0 and 23.3, 2 over 4K 12 and 21).  The rule takes the slower
-// path in two of the pairs, by 8 and 16 %.
+// 57 and 59, 8 over 64K 103 and 60, 8 over 16K 34 and 30, 16 over 4K 23.1 and 23.0, 2 over 4K 12 and 20).  The rule takes the slower
+// path in two of the pairs, by 8 and 15 %.
 double alone_us(int64_t B, int64_t rows, int64_t Hkv, int64_t d, int64_t recs) {  // the records of every sequence, from L2 for the most part
   const double mb = 18e-6 * static_cast<double>(B) * Hkv * d * recs;
   return mb * (rows <= 8 ? 0.165 : 0.24 * ((rows + 15) / 16));
