@@ -52,7 +52,9 @@ namespace {
 constexpr int PF_SOFT = 8, PF_WIDE = 4, PF_PROD = PF_SOFT + PF_WIDE, PF_LOAD = PF_PROD + 2;
 constexpr int PF_THREADS = (PF_LOAD + 2) * 32;
 constexpr int PF_ROWS = 256;     // rows of a slot: two streams of 128
-constexpr float PF_TOP = 15.f;   // the references move when a P or a P' passes 2^15, the last power of two within f16
+// The references move when a P or a P' passes 2^15, the last power of two within f16, and the row's largest P' then stands at 2^8: with
+// 2^7 to grow before the next move, and 22 powers of two below it that f16 holds whole.
+constexpr float PF_TOP = 15.f, PF_ROOM = 8.f;
 
 struct PrefixArgs {
   const __nv_bfloat16 *q;
@@ -360,9 +362,8 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefix_attn_kernel(const Prefix
           if (lane == 0) mbar_arrive(&cs.q_full[t]);
         }
       }
-      // m: the reference of l = sum of P, P = 2^(x - m); ref: that of O = sum of P' V', P' = 2^(x + g - ref).  Both are set to the
-      // largest that the row sees when a term passes 2^15 of them; what the sums hold is then scaled down.  So neither an improbable token
-      // nor the size of V in another tile takes bits from the rest.
+      // m: the reference of l = sum of P, P = 2^(x - m); ref: that of O = sum of P' V', P' = 2^(x + g - ref).  When a term passes 2^15 of
+      // them, m is set to the largest x that the row sees and ref to 2^PF_ROOM below its largest x + g; what the sums hold is then scaled down.
       float m = -INFINITY, ref = -INFINITY, l = 0.f;
       const int jobs = R == 2 ? n : (n - t + 1) / 2;
       for (int j = 0; j < jobs; ++j, ++done) {
@@ -410,7 +411,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefix_attn_kernel(const Prefix
           if (__any_sync(0xffffffffu, move)) {
             float f = 1.f;
             if (move) {
-              const float mn = fmaxf(m, xm), rn = fmaxf(ym, ref);
+              const float mn = fmaxf(m, xm), rn = fmaxf(ym - PF_ROOM, ref);
               l *= m == -INFINITY ? 0.f : fast_exp2(m - mn);
               f = ref == -INFINITY ? 0.f : fast_exp2(ref - rn);
               m = mn;

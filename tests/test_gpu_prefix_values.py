@@ -1,0 +1,87 @@
+"""Attention behind a shared prefix where the tokens' weights and sizes differ by many powers of two, against fp64.
+
+Keys are vectors of one number (a scale of 0, a minimum that bf16 holds), which f16 holds too, so a score is off by fp32 sums alone:
+2^-16 of sum |q||k| scale at most, the same for all equal keys.  Values are normal numbers of both signs, so the roundings of P and of V to
+f16 (half a step: 2^-11 of each) point both ways, and what they add up to has the root mean square of the outputs times at most
+2^-11 each, to which the bf16 output adds at most 2^-9: less than 2^-8 in all, which the channels of all rows together are held to, and
+2^-7 those of one row (32 of them at least).  A P that is subnormal in f16 is off by 2^-25: for weights down to 2^-22 of the row's largest
+that is 2^-11 of themselves again, as the largest is held at 2^8 and above."""
+import pytest
+import torch
+
+import free_block_sparse_gb300 as fbs
+import serving_ref as R
+from test_gpu_contexts import i32, shared
+from test_gpu_serving import gen
+
+pytestmark = pytest.mark.gpu
+SHARED = fbs.SPARGE_PREFIX_SHARED
+# rows of a KV head in one row tile, or in two: 4 x 304 tiles of 64 tokens are 8 for each CTA, 512 tokens of a head
+SETTINGS = [(2, 2, 64, 4), (2, 2, 128, 4), (70, 2, 64, 4), (70, 2, 128, 4)]  # sequences, heads of a group, d, KV heads
+PREFIX, SHARE = 19456, 512
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    fbs.lib()
+    yield
+    torch.cuda.synchronize()
+    assert fbs.device_status() == 0
+
+
+def stored(g, B, d, H, score, v, page=64):
+    """A prefix of PREFIX tokens whose keys are score[t] in every channel (or score (H, PREFIX, d)) and its values v (H, PREFIX, d); each
+    sequence has one token of its own that hardly counts."""
+    pool, pages, table, lens = shared(g, PREFIX, [1] * B, H, d, page)
+    t = torch.arange(PREFIX, device="cuda")
+    k = (score[None] if score.dim() == 3 else score[None, None, :, None].expand(1, H, PREFIX, d)).bfloat16().contiguous()
+    fbs.cache4_store(k, v[None].bfloat16().contiguous(), (table[0].long()[t // page] * page + t % page)[None].contiguous(), pool)
+    low = torch.full((1, H, 1, d), -60.0, dtype=torch.bfloat16, device="cuda")
+    for b in range(B):
+        fbs.cache4_store(low, torch.zeros_like(low), (table[b].long()[-1:] * page)[None].contiguous(), pool)
+    return pool, pages, table, lens
+
+
+def queries(g, B, H, G, d):
+    """Rows whose sum is about d, so that a key of one number n scores about n log 2 at the scale of scale_of(d)."""
+    return (1 + 0.25 * torch.randn(B, H * G, 1, d, generator=g, device="cuda")).bfloat16()
+
+
+def scale_of(d):
+    return 0.6931471805599453 / d
+
+
+def check(q, pool, table, lens, out, d, channels, scale=None):
+    """Channels (a slice) of the rows against fp64."""
+    page = 16 * pool.shape[2]
+    kn, ks, km, vn, vs, vm = R.read_pool(pool, d)
+    K, V = R.dequantise(kn, ks, km), R.dequantise(vn, vs, vm)
+    off, ref = [], []
+    for b in sorted({0, 1, len(lens) // 2, len(lens) - 1}):
+        n = lens[b]
+        t = torch.arange(n, device="cuda")
+        k, v = (x[table[b].long()[t // page], :, t % page].transpose(0, 1) for x in (K, V))
+        o, _, _ = R.attention(q[b].double(), k, v, torch.tensor([n - 1], device="cuda"), 0, 0, scale or scale_of(d))
+        off.append((out[b].double() - o)[..., channels].square().sum(-1))
+        ref.append(o[..., channels].square().sum(-1))
+    off, ref = torch.cat(off), torch.cat(ref)
+    assert (ref > 0).all()
+    assert off.sum() <= 2.0 ** -16 * ref.sum(), float((off.sum() / ref.sum()).sqrt())
+    assert (off <= 2.0 ** -14 * ref).all(), float((off / ref).amax().sqrt())
+
+
+@pytest.mark.parametrize("B,G,d,H", SETTINGS)
+@pytest.mark.parametrize("at", [0, 200, 511])
+@pytest.mark.parametrize("below", [6, 12, 18, 22])
+def test_tokens_far_below_the_largest(B, G, d, H, at, below):
+    """One token of every share takes 2^6 to 2^22 times the others' weight, but its values are zero in every second channel: there
+    the others' sum is all there is."""
+    g = gen(81)
+    t = torch.arange(PREFIX, device="cuda")
+    score = torch.where(t % SHARE == at, 0.0, -float(below))
+    v = torch.randn(H, PREFIX, d, generator=g, device="cuda")
+    v[:, t % SHARE == at] = (torch.arange(d, device="cuda") % 2 == 0).float()
+    pool, pages, table, lens = stored(g, B, d, H, score, v)
+    q = queries(g, B, H, G, d)
+    out = fbs.cache4_prefix_attn(q, pool, pages, table, i32(*lens), scale=scale_of(d), path=SHARED)
+    check(q, pool, table, lens, out, d, slice(1, None, 2))
