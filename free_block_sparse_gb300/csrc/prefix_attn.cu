@@ -9,14 +9,18 @@
 //
 // Widening.  A code n is the subnormal f16 n 2^-24 once its four bits are masked out in place, so one fma.rn.f16x2 with (s 2^(f + 24),
 // m 2^f) makes two elements of s n + m times 2^f: no conversion, one rounding, to f16.  f, one number for a tile's K and one for its V,
-// takes the tile's largest scale to [2^-9, 2^-8), the most that s 2^(f + 24) allows (or the largest minimum below 2^14).  An element is
-// off by at most 2^-11 of itself, and by 2^-15 of the largest scale where its own is far smaller.  Words give the
+// takes the tile's largest scale to [2^-9, 2^-8), the most that s 2^(f + 24) allows (or the largest minimum: K's below 2^14, V's to
+// 2^-3).  An element is off by at most 2^-11 of itself and 2^-15 of the largest scale.  So that no token takes bits from smaller ones, a
+// tile whose tokens' sizes are more than 2^PF_EVEN apart is an uneven one: the warp that finds the powers scales the smaller tokens' words to
+// the size of the largest, and the softmax takes each token's own powers from shared memory.  (It passes twice over the scores, in
+// a loop that stays small beside the even tiles' code: unrolled, or with the scores in local memory, it cost those 5 to 20 %.  64 over
+// 32K with every tile uneven: 79 us in place of 39, one of 16 tiles 46.)  Words give the
 // channels of eight in the order 0 4 1 5 2 6 3 7, so Q is stored in that order; tokens of a tile stand in the order that the
 // V records give (position 32 p + 8 c + 4 r + 2 h + i: token 2 c + 8 h + i of record 2 p + r), for K and V alike.
 //
 // Products.  S = Q K'^T (M = 128 rows, N = 64 tokens) and O += P' V' (N = d), kind::f16 with fp32 sums in TMEM.  P' = 2^(x + g - ref),
-// g = -f of V: V's powers enter through P, and ref follows the largest x + g of the row when a P' passes 2^15, so O needs no rescaling
-// when V's sizes change from tile to tile.  l is summed in fp32 against a reference m of its own.  Q is f16 times a power of two per row.
+// g = -f of V, the token's own in an uneven tile: V's powers enter through P, and ref follows the row's largest x + g (of one token) when a P'
+// passes 2^15, so O needs no rescaling when V's sizes change from tile to tile.  l is summed in fp32 against a reference m of its own.  Q is f16 times a power of two per row.
 //
 // A CTA holds two streams, each with its softmax warps, its warp that issues products, and its S, P and O: two tiles of 128 rows
 // over the same tokens (more than 128 rows) or one tile of rows whose streams take the token tiles in turns.  The line of all
@@ -55,6 +59,8 @@ constexpr int PF_ROWS = 256;     // rows of a slot: two streams of 128
 // The references move when a P or a P' passes 2^15, the last power of two within f16, and the row's largest P' then stands at 2^8: with
 // 2^7 to grow before the next move, and 22 powers of two below it that f16 holds whole.
 constexpr float PF_TOP = 15.f, PF_ROOM = 8.f;
+// Tokens of a tile whose sizes' exponents are no further apart share its powers of two; in an uneven tile each has its own.
+constexpr int PF_EVEN = 4;
 
 struct PrefixArgs {
   const __nv_bfloat16 *q;
@@ -80,26 +86,28 @@ struct PfCfg {
   static constexpr uint32_t TILE = 64 * D * 2;       // of K or V, f16
   static constexpr uint32_t OUT = 128 * 32 * 4;      // 32 channels of a stream's O on their way out; over its Q where that lies here
   static constexpr uint32_t K = 0, V = K + NS * TILE, Q = V + NS * TILE, QB = QSMEM ? 128 * D * 2 : OUT, RING = Q + 2 * QB;
-  static constexpr uint32_t CTRL = RING + RS * RAW, SMEM = CTRL + 1024;
+  static constexpr uint32_t CTRL = RING + RS * RAW, SMEM = CTRL + 9216;
   // TMEM columns
   static constexpr uint32_t O = 0, S = 2 * D, P = S + 128, QC = P + 64, QCOLS = D / 2;
   static_assert(QC + (QSMEM ? 0 : R) * QCOLS <= 512, "TMEM");
   static_assert(SMEM <= 227 * 1024, "shared memory");
 };
-// What goes with a tile: K = K' 2^-kf, V = V' 2^-vf; bit r of missing: its record r is not there.
+// What goes with a tile: K = K' 2^-kf, V = V' 2^-vf; bit r of missing: its record r is not there.  In an uneven tile (one that misses
+// records is) a token's are K' 2^-kf k_by and V' 2^v_by.
 struct alignas(16) PfInfo {
   int kf, vf;
-  uint32_t missing, pad;
+  uint32_t missing, uneven;
 };
 struct PfCtrl {
   PfInfo info[16];  // (tile % 16: a tile that far behind has been turned into P)
+  alignas(16) float k_by[16][64], v_by[16][64];  // of uneven tiles, in the order of the scores' columns
   uint64_t raw_full[8], raw_free[8], info_full[8], kv_full[4], kv_free[4];
   uint64_t q_full[2], q_free, s_full[2], s_free[2], p_full[2], pv_done[2], drained[2];
   uint8_t bad[8][4];
   uint32_t tmem;
   int abort, no_abort;
 };
-static_assert(sizeof(PfCtrl) <= 1024, "control block");
+static_assert(sizeof(PfCtrl) <= 9216, "control block");
 
 __device__ __forceinline__ void pf_bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
@@ -182,13 +190,25 @@ __device__ __forceinline__ void pf_ld_wait_for(uint32_t (&r)[32], float &m) {
                :
                : "memory");
 }
-// What a tile's power of two f has to keep to, from a word of its: f <= -need, so that a code's 2^-24 code * s 2^(f + 24) is within
-// f16 and the value below 2^15.  (A scale or minimum that is not finite makes its own values NaN and counts for nothing here.)
+// What a power of two f has to keep to, from the exponents of scales and minima: f <= -need, so that a code's 2^-24 code * s 2^(f + 24)
+// is within f16 and K's minimum below 2^14.  V's minimum goes to 2^-3, where its scale's codes are, so that x - f says within a
+// few powers of two what a token of score x can add to O.
+template <bool V>
 __device__ __forceinline__ int pf_need(uint32_t word) {
-  const int s = (word >> 7) & 0xFF, m = (word >> 23) & 0xFF;
-  return max(s, m) == 255 ? -200 : max(s + 9, m - 13) - 127;
+  return max(static_cast<int>((word >> 7) & 0xFFu) + 9, static_cast<int>((word >> 23) & 0xFFu) + (V ? 4 : -13)) - 127;
+}
+// Nothing: a scale or minimum that is not finite makes its own values NaN, whatever the power.
+constexpr int PF_NO_NEED = -200;
+template <bool V>
+__device__ __forceinline__ int pf_finite_need(uint32_t word) {
+  return ((word & 0x7F80u) == 0x7F80u || (word & 0x7F800000u) == 0x7F800000u) ? PF_NO_NEED : pf_need<V>(word);
 }
 __device__ __forceinline__ int pf_power(int need) { return min(max(-need, -126), 100); }
+// A scale and a minimum times 2^by, exactly.
+__device__ __forceinline__ uint32_t pf_word_by(uint32_t word, int by) {
+  const float f = pf_pow2(by);
+  return pack_bf16x2(bf16lo(word) * f, bf16hi(word) * f);
+}
 
 // A CTA's share of the line of all items' tiles, and its pieces: item, first tile, tiles.
 struct PfShare {
@@ -368,14 +388,49 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefix_attn_kernel(const Prefix
       const int jobs = R == 2 ? n : (n - t + 1) / 2;
       for (int j = 0; j < jobs; ++j, ++done) {
         const uint32_t tile = tc + (R == 2 ? j : 2 * j + t), st = tile % NS;
-        // (V's barrier is what orders the reads of the tile's powers)
-        ok = pf_wait(&cs.s_full[t], done & 1, abort);
+        // (what the widened tile's barrier orders, its powers among it, is there before its scores are)
+        ok = pf_wait(&cs.s_full[t], done & 1, abort) && pf_wait(&cs.kv_full[st], (tile / NS) & 1, abort);
+        const PfInfo info = cs.info[tile & 15];
+        float mult = fminf(fmaxf(rm * pf_pow2(-info.kf), 0x1p-126f), 0x1p127f);  // (no 0 times -inf, no infinity times 0)
+        float g = static_cast<float>(-info.vf), apart = 0.f;
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
         uint32_t v[2][32];
         float mh[2];
         if (live) {
+          if (info.uneven) [[unlikely]] {  // l and m from the scores, then x + g of each token in their place
+            float xm = -INFINITY;
+#pragma unroll 1
+            for (int i = 0; i < 128; i += 16) {  // every 16 columns for the maximum, then again for the sum
+              uint32_t x[16];
+              tmem_ld16(sc + (i & 63), x);
+              pf_ld_wait_for(x);
+              if (i == 64) {
+                const float mn = fmaxf(m, xm);
+                l *= m == -INFINITY ? 0.f : fast_exp2(m - mn);
+                m = mn;
+              }
+              const float *by = (i < 64 ? cs.k_by : cs.v_by)[tile & 15] + (i & 63);
+#pragma unroll
+              for (int k = 0; k < 16; ++k) {
+                float y = __uint_as_float(x[k]);
+                if (i < 64) {  // column 32 h + 8 c + 4 r + i is a token of record 2 h + r
+                  y = ((info.missing >> (2 * (i >> 5) + ((k >> 2) & 1))) & 1u) ? -INFINITY : y * by[k] * mult;
+                  xm = fmaxf(xm, y);
+                } else {
+                  l += fast_exp2(m == -INFINITY ? y : y - m);
+                  y += by[k];
+                }
+                x[k] = __float_as_uint(y);
+              }
+              tmem_st16(sc + (i & 63), x);
+              tmem_st_wait();
+            }
+            mult = 1.f;
+            g = 0.f;
+            apart = -INFINITY;
+          }
           tmem_ld32_max(sc, v[0], mh[0]);
           tmem_ld32_max(sc + 32, v[1], mh[1]);
           pf_ld_wait_for(v[0], mh[0]);
@@ -384,19 +439,6 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefix_attn_kernel(const Prefix
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&cs.s_free[t]);
-        ok = pf_wait(&cs.kv_full[st], (tile / NS) & 1, abort);
-        const PfInfo info = cs.info[tile & 15];
-        if (info.missing && live) {  // columns 32 h + 8 c + 4 r + i are tokens of record 2 h + r
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            mh[h] = -INFINITY;
-#pragma unroll
-            for (int k = 0; k < 32; ++k) {
-              if ((info.missing >> (2 * h + ((k >> 2) & 1))) & 1u) v[h][k] = 0xFF800000u;
-              mh[h] = fmaxf(mh[h], __uint_as_float(v[h][k]));
-            }
-          }
-        }
         if (j > 0) {  // the product before this one has read its P and added to O
           ok = ok && pf_wait(&cs.pv_done[t], (done - 1) & 1, abort);
         }
@@ -404,9 +446,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefix_attn_kernel(const Prefix
         if (!ok) break;
         tc_fence_after();
         if (live) {
-          const float mult = fminf(fmaxf(rm * pf_pow2(-info.kf), 0x1p-126f), 0x1p127f);  // (no 0 times -inf, no infinity times 0)
-          const float g = static_cast<float>(-info.vf);
-          const float xm = fmaxf(mh[0], mh[1]) * mult, ym = xm + g;
+          const float top = fmaxf(mh[0], mh[1]) * mult, ym = top + g, xm = top + apart;
           const bool move = xm > m + PF_TOP || ym > ref + PF_TOP;
           if (__any_sync(0xffffffffu, move)) {
             float f = 1.f;
@@ -432,7 +472,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefix_attn_kernel(const Prefix
           // (a row whose references are still -inf has only hidden columns, or NaN)
           const bool none = ref == -INFINITY;
           // P' = 2^(x + nr), P = P' 2^back; where V of this tile is so small beside what O holds that its P' is 0, back stops where l's terms do not
-          const float back = none ? 0.f : fminf((ref - m) - g, 60.f), nr = none ? 0.f : -m - back;
+          const float back = none ? 0.f : fminf((ref - m) - g, 60.f - apart), nr = none ? 0.f : -m - back;
           const float2 m2 = make_float2(mult, mult), n2 = make_float2(nr, nr);
           float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
@@ -452,7 +492,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefix_attn_kernel(const Prefix
           __syncwarp();
           if (lane == 0) mbar_arrive(&cs.p_full[t]);
           const float2 s2 = fadd2(sum[0], sum[1]);
-          l = fmaf(s2.x + s2.y, fast_exp2(back), l);
+          l = fmaf(s2.x + s2.y, fast_exp2(back + apart), l);
         } else {
           if (lane == 0) mbar_arrive(&cs.p_full[t]);
         }
@@ -709,10 +749,10 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefix_attn_kernel(const Prefix
       const uint32_t rs = tile % RS;
       if (!__all_sync(0xffffffffu, pf_wait(&cs.raw_full[rs], (tile / RS) & 1, abort))) break;
       const uint32_t bad = *reinterpret_cast<const uint32_t *>(cs.bad[rs]);  // a byte a record
-      // lane 8 rec + k looks at the k-th eighth of a record's words: their exponents' maxima, two at a time
+      // lane 8 rec + k looks at the words of tokens 2k and 2k + 1 of a record
       const int rec = lane >> 3;
       const uint8_t *at = smem + C::RING + rs * C::RAW + rec * C::PITCH + (lane & 7) * (8 * NG);
-      uint32_t u[2][2 * NG], top[2];
+      uint32_t u[2][2 * NG];
       if constexpr (NG == 2) {
         const uint4 x = *reinterpret_cast<const uint4 *>(at + Rec::KW), y = *reinterpret_cast<const uint4 *>(at + Rec::VW);
         u[0][0] = x.x; u[0][1] = x.y; u[0][2] = x.z; u[0][3] = x.w;
@@ -723,23 +763,56 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefix_attn_kernel(const Prefix
         u[1][0] = y.x; u[1][1] = y.y;
       }
       const bool there = ((bad >> (8 * rec)) & 1u) == 0u;
-      int f[2];  // of K, V
+      int own[2][2], top[2], low[2];  // of K, V: the two tokens' needs, the tile's largest and (but for tokens of zeros) smallest
+      uint32_t some[2][2];            // a token's scales and minima
+      auto reduce = [&] {
 #pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        top[s] = 0u;
-#pragma unroll
-        for (int k = 0; k < 2 * NG; ++k) top[s] = __vmaxu2(top[s], u[s][k] & 0x7F807F80u);
-        const int lo = top[s] & 0xFFFFu, hi = top[s] >> 16;
-        int need = there ? max((lo >> 7) + 9, (hi >> 7) - 13) - 127 : -200;
-        if (__any_sync(0xffffffffu, there && max(lo, hi) == 0x7F80)) {  // words that are not finite are passed over one by one
-          need = -200;
-#pragma unroll
-          for (int k = 0; k < 2 * NG; ++k) need = max(need, there ? pf_need(u[s][k]) : -200);
+        for (int s = 0; s < 2; ++s) {
+          top[s] = __reduce_max_sync(0xffffffffu, there ? max(own[s][0], own[s][1]) : PF_NO_NEED);
+          low[s] = __reduce_min_sync(0xffffffffu, min(there && some[s][0] != 0u ? own[s][0] : 255, there && some[s][1] != 0u ? own[s][1] : 255));
         }
-        f[s] = pf_power(__reduce_max_sync(0xffffffffu, need));
+      };
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+          some[s][k] = NG == 2 ? __vmaxu2(u[s][NG * k] & 0x7F807F80u, u[s][NG * k + NG - 1] & 0x7F807F80u) : u[s][k] & 0x7F807F80u;
+        own[0][k] = pf_need<false>(some[0][k]);
+        own[1][k] = pf_need<true>(some[1][k]);
+      }
+      reduce();
+      if (max(top[0], top[1]) >= 100) [[unlikely]] {  // words that are not finite may be among them, and are passed over
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          own[0][k] = max(pf_finite_need<false>(u[0][NG * k]), pf_finite_need<false>(u[0][NG * k + NG - 1]));
+          own[1][k] = max(pf_finite_need<true>(u[1][NG * k]), pf_finite_need<true>(u[1][NG * k + NG - 1]));
+#pragma unroll
+          for (int s = 0; s < 2; ++s)
+            if (own[s][k] == PF_NO_NEED) some[s][k] = 0u;
+        }
+        reduce();
+      }
+      const int f[2] = {pf_power(top[0]), pf_power(top[1])};
+      const bool uneven = bad != 0u || low[0] < top[0] - PF_EVEN || low[1] < top[1] - PF_EVEN;
+      if (uneven) [[unlikely]] {  // the smaller tokens' words take their own powers here, so that widening knows one for all
+        const int col = 32 * (rec >> 1) + 8 * (lane & 3) + 4 * (rec & 1) + 2 * ((lane >> 2) & 1);
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          uint32_t *to = reinterpret_cast<uint32_t *>(smem + C::RING + rs * C::RAW + rec * C::PITCH + (s ? Rec::VW : Rec::KW)) + (lane & 7) * (2 * NG);
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const int by = there && some[s][k] != 0u ? min(max(min(-own[s][k], 100) - f[s], 0), 100) : 0;
+            (s ? cs.v_by : cs.k_by)[tile & 15][col + k] = s ? static_cast<float>(-f[1] - by) : pf_pow2(-by);
+#pragma unroll
+            for (int w = 0; w < NG; ++w)
+              if (by > 0) to[NG * k + w] = pf_word_by(to[NG * k + w], by);
+          }
+        }
+        fence_proxy_async_smem();  // before the ring's next copy
+        __syncwarp();
       }
       if (lane == 0) {
-        cs.info[tile & 15] = {f[0], f[1], (bad & 1u) | ((bad >> 7) & 2u) | ((bad >> 14) & 4u) | ((bad >> 21) & 8u), 0u};
+        cs.info[tile & 15] = {f[0], f[1], (bad & 1u) | ((bad >> 7) & 2u) | ((bad >> 14) & 4u) | ((bad >> 21) & 8u), uneven ? 1u : 0u};
         mbar_arrive(&cs.info_full[rs]);
       }
       __syncwarp();

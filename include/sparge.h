@@ -452,9 +452,12 @@ int sparge_cache4_pages_attn(const sparge_tensor *q, const sparge_cache4 *cache,
  * queries do not all stand behind the prefix is attended over its own row alone, so any length is taken.
  * path SPARGE_PREFIX_AUTO: where that takes less time by the call's sizes (few sequences, or a short prefix), every sequence is
  * attended over its own row as in sparge_cache4_attn; SPARGE_PREFIX_SHARED: never.  The two round differently.
- * Shared keys and values enter the products as f16, 64 tokens of a head with one power of two each: an element x of a token is off
- * by at most |x| 2^-11 + s 2^-15 + m 2^-37, s and m the largest scale (step between codes) and |minimum| among the 64, as long as
- * they are below 2^116.
+ * Shared keys and values enter the products as f16, 64 tokens of a head with one power of two each, or where their sizes (the larger
+ * of a token's scales, its steps between codes, and of its |minima| / 32) are more than 2^4 apart each token with its own: an element x of a
+ * token is off by at most |x| 2^-11 + s 2^-15 + m 2^-20, s and m the largest scale and |minimum| of the tokens that share a power, as long as
+ * they are below 2^116.  A token's weight is f16 too: off by 2^-11 of itself where weight times size (of its values) is at least 2^-17 of the row's
+ * largest, else by at most what 2^-28 of that largest makes of it.  (A token's channels share its power: where one group of 64 is far larger than the
+ * other, that counts for both; sparge_cache4_attn keeps them apart.)
  */
 #define SPARGE_PREFIX_AUTO 0
 #define SPARGE_PREFIX_SHARED 1

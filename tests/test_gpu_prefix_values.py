@@ -1,11 +1,12 @@
 """Attention behind a shared prefix where the tokens' weights and sizes differ by many powers of two, against fp64.
 
 Keys are vectors of one number (a scale of 0, a minimum that bf16 holds), which f16 holds too, so a score is off by fp32 sums alone:
-2^-16 of sum |q||k| scale at most, the same for all equal keys.  Values are normal numbers of both signs, so the roundings of P and of V to
-f16 (half a step: 2^-11 of each) point both ways, and what they add up to has the root mean square of the outputs times at most
-2^-11 each, to which the bf16 output adds at most 2^-9: less than 2^-8 in all, which the channels of all rows together are held to, and
-2^-7 those of one row (32 of them at least).  A P that is subnormal in f16 is off by 2^-25: for weights down to 2^-22 of the row's largest
-that is 2^-11 of themselves again, as the largest is held at 2^8 and above."""
+2^-16 of sum |q||k| scale at most, the same for all equal keys; random keys are off by half an f16 step each, which moves a score by a root
+mean square of 2^-11 / sqrt 3 of |q||k| scale, less than 2^-11 here.  Values are normal numbers of both signs, so the roundings of P and of V
+to f16 (half a step: 2^-11 of each) point both ways, and what they add up to has the root mean square of the outputs times at most
+2^-11 each, to which the bf16 output adds at most 2^-8 / sqrt 3: less than 2^-8 in all, which the channels of all rows together are held
+to, and 2^-7 those of one row (32 of them at least).  A P that is subnormal in f16 is off by 2^-25: for weights down to 2^-22 of the row's
+largest that is 2^-11 of themselves again, as the largest is held at 2^8 and above."""
 import pytest
 import torch
 
@@ -85,3 +86,69 @@ def test_tokens_far_below_the_largest(B, G, d, H, at, below):
     q = queries(g, B, H, G, d)
     out = fbs.cache4_prefix_attn(q, pool, pages, table, i32(*lens), scale=scale_of(d), path=SHARED)
     check(q, pool, table, lens, out, d, slice(1, None, 2))
+
+
+@pytest.mark.parametrize("B,G,d,H", SETTINGS)
+@pytest.mark.parametrize("at", [0, 200, 511])
+@pytest.mark.parametrize("power", [8, 12, 16, 20, 24, 28])
+def test_large_values_of_improbable_tokens(B, G, d, H, at, power):
+    """A token of every share with a weight of 2^-30 of the others' has values 2^8 to 2^28 in every second channel, and zeros in the
+    rest, where the others' sum stays as exact as without it."""
+    g = gen(82)
+    t = torch.arange(PREFIX, device="cuda")
+    score = torch.where(t % SHARE == at, -30.0, 0.0)
+    v = torch.randn(H, PREFIX, d, generator=g, device="cuda")
+    v[:, t % SHARE == at] = (torch.arange(d, device="cuda") % 2 == 0).float() * 2.0 ** power
+    pool, pages, table, lens = stored(g, B, d, H, score, v)
+    q = queries(g, B, H, G, d)
+    out = fbs.cache4_prefix_attn(q, pool, pages, table, i32(*lens), scale=scale_of(d), path=SHARED)
+    check(q, pool, table, lens, out, d, slice(1, None, 2))
+
+
+@pytest.mark.parametrize("B,G,d,H", SETTINGS)
+@pytest.mark.parametrize("at", [0, 200, 511])
+@pytest.mark.parametrize("power", [0, 8, 16, 30])
+def test_small_values_of_a_probable_token(B, G, d, H, at, power):
+    """A token of every share takes 2^12 times each other one's weight with values 2^-30 of theirs and more."""
+    g = gen(83)
+    t = torch.arange(PREFIX, device="cuda")
+    score = torch.where(t % SHARE == at, 0.0, -12.0)
+    v = torch.randn(H, PREFIX, d, generator=g, device="cuda")
+    v[:, t % SHARE == at] *= 2.0 ** -power
+    pool, pages, table, lens = stored(g, B, d, H, score, v)
+    q = queries(g, B, H, G, d)
+    out = fbs.cache4_prefix_attn(q, pool, pages, table, i32(*lens), scale=scale_of(d), path=SHARED)
+    check(q, pool, table, lens, out, d, slice(None))
+
+
+@pytest.mark.parametrize("B,G,d,H", SETTINGS)
+@pytest.mark.parametrize("at", [0, 200, 511])
+def test_zero_values(B, G, d, H, at):
+    """Tokens whose values are all zero, and tiles of nothing else, beside tokens of any size."""
+    g = gen(84)
+    t = torch.arange(PREFIX, device="cuda")
+    score = torch.where(t % SHARE == at, 0.0, -10.0)
+    v = torch.randn(H, PREFIX, d, generator=g, device="cuda")
+    v[:, (t % SHARE == at) | (t // 64 % 3 == 1) | (t % 5 == 0)] = 0.0
+    v[:, t % 7 == 1] *= 2.0 ** 20
+    pool, pages, table, lens = stored(g, B, d, H, score, v)
+    q = queries(g, B, H, G, d)
+    out = fbs.cache4_prefix_attn(q, pool, pages, table, i32(*lens), scale=scale_of(d), path=SHARED)
+    check(q, pool, table, lens, out, d, slice(None))
+
+
+@pytest.mark.parametrize("B,G,d,H", SETTINGS)
+@pytest.mark.parametrize("at", [0, 200, 511])
+@pytest.mark.parametrize("power", [8, 16, 24, 60])
+def test_large_keys_of_improbable_tokens(B, G, d, H, at, power):
+    """A token of every share whose keys are 2^8 to 2^60 times the others' and point away from the queries: the others' scores stay
+    as exact as without it."""
+    g = gen(85)
+    t = torch.arange(PREFIX, device="cuda")
+    k = 2.0 * torch.randn(H, PREFIX, d, generator=g, device="cuda")
+    k[:, t % SHARE == at] = -(2.0 ** power) * (0.5 + torch.rand(d, generator=g, device="cuda"))
+    v = torch.randn(H, PREFIX, d, generator=g, device="cuda")
+    pool, pages, table, lens = stored(g, B, d, H, k, v)
+    q = queries(g, B, H, G, d)
+    out = fbs.cache4_prefix_attn(q, pool, pages, table, i32(*lens), scale=8 * scale_of(d), path=SHARED)
+    check(q, pool, table, lens, out, d, slice(None), scale=8 * scale_of(d))
