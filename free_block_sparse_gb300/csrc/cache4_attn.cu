@@ -245,12 +245,8 @@ __global__ void __launch_bounds__(CA_WARPS * 32, ca_ctas(D, RT)) cache4_attn_ker
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
   uint8_t *ring = smem + warp * S::WRING;
 
-  if constexpr (Args::PARTIAL) {  // the kernel in front attends the prefix: waited for at the end
-    start_beside_earlier();
-  } else {
-    let_dependents_start();
-    wait_for_earlier();
-  }
+  let_dependents_start();
+  wait_for_earlier();
 
   // ---- this CTA's share [start, end) of the line of tiles, and the sequence it starts in; every warp for
   // itself, so that no barrier holds up the first loads ----
@@ -274,10 +270,7 @@ __global__ void __launch_bounds__(CA_WARPS * 32, ca_ctas(D, RT)) cache4_attn_ker
   const int64_t total = __shfl_sync(0xffffffffu, inc, a.B > 1 ? 31 : 0);
   // shares only for as many CTAs as there are places: between an item's first and last CTA each holds some of it
   const int64_t shares = total < gridDim.x ? total : gridDim.x;
-  if (blockIdx.x >= shares) {
-    if constexpr (Args::PARTIAL) wait_for_earlier();
-    return;
-  }
+  if (blockIdx.x >= shares) return;
   const int64_t start = divide(total * blockIdx.x, shares), end = divide(total * (blockIdx.x + 1), shares);
   int b = bt;
   int64_t off = start - (inc - own), left = end - start;
@@ -739,7 +732,6 @@ __global__ void __launch_bounds__(CA_WARPS * 32, ca_ctas(D, RT)) cache4_attn_ker
     while (global_timer_ns() - t0 < 1000000ull) {
     }
   }
-  if constexpr (Args::PARTIAL) wait_for_earlier();
 }
 
 // Query rows of a KV head and items that a call takes (its places are 32-bit numbers).

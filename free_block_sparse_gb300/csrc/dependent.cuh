@@ -23,18 +23,6 @@ __device__ __forceinline__ void start_after_earlier() {
   wait_for_earlier();
 }
 
-// The same for a kernel whose follower does not need it: what came before both is complete when the follower starts, which then runs
-// beside this kernel and waits for it, before it ends, in every CTA.
-__device__ __forceinline__ void start_then_let_follower() {
-  wait_for_earlier();
-  __threadfence();
-  let_dependents_start();
-}
-__device__ __forceinline__ void start_beside_earlier() {  // such a follower's start
-  let_dependents_start();
-  __threadfence();
-}
-
 // 16 bytes that are read once: past the L1 cache
 __device__ __forceinline__ uint4 ld_once_v4(const void *p) {
   uint4 v;

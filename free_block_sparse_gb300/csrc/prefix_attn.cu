@@ -238,7 +238,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefix_attn_kernel(const Prefix
   constexpr uint32_t IDESC_PV = idesc_f32acc(128, D, FMT_F16, false);
   extern __shared__ __align__(1024) uint8_t smem[];
   if (smem_u32(smem) & 1023u) {  // the swizzle of the MMA descriptors assumes 1024-byte aligned tiles
-    start_then_let_follower();
+    start_after_earlier();
     if (threadIdx.x == 0) record_status(a.status, -4 /* SPARGE_ERR_CUDA */);
     return;
   }
@@ -276,7 +276,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefix_attn_kernel(const Prefix
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  start_then_let_follower();
+  start_after_earlier();
   const uint32_t tmem = cs.tmem;
   PfShare share(a);
   int item, tile0, n;  // the piece: tiles tile0 .. tile0 + n - 1 of the item
