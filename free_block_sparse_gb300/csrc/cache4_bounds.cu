@@ -6,9 +6,10 @@
 // 2^-126).  A page that holds an infinity or a NaN has s = infinity.
 // Score of a page for a query row: r_c = round-to-even(q_c / t), t a power of two in the same way, and
 //   t s sum_c max(r_c hi_c, r_c lo_c) = t s (sum r+ hi + sum r- lo),   r+ = max(r, 0), r- = min(r, 0),
-// which no token of the page exceeds in t r . k.  The sums are whole numbers below 2^21 and the factors powers of two, so a
-// score is exact and the selection does not depend on the order of any sum.  A KV head's score is the largest of its
-// heads'.  d + d bytes of codes per page and head in place of 9 d / 16 for every token.
+// which no token of the page exceeds in t r . k.  A KV head's score is the largest of its heads'.  The sums are whole numbers below 2^21
+// and the factors powers of two, so the selection does not depend on the order of any sum.  Scores are held in units of 2^15 times the
+// largest t of the group's heads, which changes no list: so none leaves fp32's range (2^127 at most), and each is exact where its head's t / that
+// largest * s is 2^-134 or more.  d + d bytes of codes per page and head in place of 9 d / 16 for every token.
 //
 // Layout of a page's bounds: codes [H][hi, lo][d], scales [H] (fp32), padded to 32 bytes.
 #include <climits>
@@ -37,6 +38,9 @@ __device__ __forceinline__ float code_unit(float a) {
 }
 // 1 / s for a power of two s in 2^-126 .. 2^126
 __device__ __forceinline__ float over_unit(float s) { return __uint_as_float((254u << 23) - __float_as_uint(s)); }
+
+// 2^-15 / t for t = 2^-126 .. 2^121 (0 for 0: rows that have no say)
+__device__ __forceinline__ float score_unit(float t) { return t > 0.f ? over_unit(t) * 0x1p-15f : 0.f; }
 
 __device__ __forceinline__ float fmin3(float a, float b, float c) {  // as fmax3: a NaN among them counts for nothing
   float r;
@@ -322,7 +326,8 @@ template <int D>
 __global__ void __launch_bounds__(SEL_THREADS, sel_ctas(D)) select_score_kernel(const SelectArgs a) {
   constexpr int S = D / 8, NP = D / 32;  // steps of a product, 16 codes each, hi's then lo's; 16-byte pieces of a page and lane
   __shared__ __align__(16) uint8_t codes[SEL_ROWS * 4 * D];
-  __shared__ float2 unit[SEL_ROWS / 2];  // t of the rows
+  __shared__ float2 unit[SEL_ROWS / 2];  // t of the rows, in the unit of their query where it has no more than four
+  __shared__ float top[SEL_ROWS / 4];    // the largest t of four rows
   __shared__ int limit[SEL_ROWS];        // pages to choose from of each query of the round
   start_after_earlier();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
@@ -390,11 +395,16 @@ __global__ void __launch_bounds__(SEL_THREADS, sel_ctas(D)) select_score_kernel(
           u[k][0] = *reinterpret_cast<const uint32_t *>(q + 2 * lane);
         }
       }
+      float t[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float t = code_row<D>(u[k], codes, r0 + k, lane);
-        if (lane == 0) reinterpret_cast<float *>(unit)[r0 + k] = t;
+      for (int k = 0; k < 4; ++k) t[k] = code_row<D>(u[k], codes, r0 + k, lane);
+      const float t01 = fmaxf(t[0], t[1]), t23 = fmaxf(t[2], t[3]), all = fmaxf(t01, t23);
+      if (lane < 4) {
+        const float own = lane == 0 ? t[0] : lane == 1 ? t[1] : lane == 2 ? t[2] : t[3];
+        const float most = a.rows_log == 0 ? own : a.rows_log == 1 ? (lane < 2 ? t01 : t23) : all;
+        reinterpret_cast<float *>(unit)[r0 + lane] = a.tiles ? own : own * score_unit(most);
       }
+      if (lane == 0) top[r0 / 4] = all;
     }
     for (int i = threadIdx.x; i < ni; i += SEL_THREADS) limit[i] = a.choices(len, i0 + i);
     float *keys = a.keys + ((static_cast<int64_t>(b) * a.Nq + i0) * a.Hkv + h) * a.pitch + g;
@@ -440,6 +450,7 @@ __global__ void __launch_bounds__(SEL_THREADS, sel_ctas(D)) select_score_kernel(
       float best[2];  // of a query of several tiles of rows
       best[0] = best[1] = -INFINITY;
       int i = 0, nth = 0;  // of a query of whole tiles: the query, its tile
+      float of_query = 1.f;
       const uint8_t *tile = codes + lane * 8;
 #pragma unroll 1
       for (int t = 0; t < nt; ++t, tile += S * 256) {
@@ -450,7 +461,12 @@ __global__ void __launch_bounds__(SEL_THREADS, sel_ctas(D)) select_score_kernel(
           const uint2 q = *reinterpret_cast<const uint2 *>(tile + k * 256);
           mma_codes(acc, w[k][0], w[k][1], w[k][2], w[k][3], q);
         }
-        const float2 un = unit[t * 4 + c];
+        if (a.tiles && nth == 0) {
+          float most = 0.f;
+          for (int x = 0; x < 2 * a.tiles; ++x) most = fmaxf(most, top[2 * t + x]);
+          of_query = score_unit(most);
+        }
+        const float2 un = make_float2(unit[t * 4 + c].x * of_query, unit[t * 4 + c].y * of_query);
         // which lanes write: each its first row's value, the largest of a query's rows; with one row a query its second's too
         const bool several = a.rows_log > 0 || a.tiles > 0;
         const bool put = !several || (a.tiles ? c == 0 && nth == a.tiles - 1 : a.rows_log == 1 || (c & 1) == 0);

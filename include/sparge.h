@@ -420,7 +420,8 @@ int sparge_cache4_bounds_load(const sparge_cache4 *cache, const void *bounds, si
  * The pages that matter to each query, by the bounds.  q (B,Hq,Nq,d), table and kv_lens as in sparge_cache4_attn: query r of
  * sequence b sees seen = kv_lens[b] - Nq + r + 1 tokens on its first ceil(seen / page_size) pages.  A page's score for a query row is
  * t s sum_c max(r_c hi_c, r_c lo_c) with r = round-to-even(q / t) in int8, t the least power of two for it as s above: no
- * token of the page has a larger product with t r.  A key/value head's score is the largest of its query heads'; a page of infinite s
+ * token of the page has a larger product with t r.  Scores rank exactly, whatever their size (down to t s of 2^-134 of the largest t of the
+ * group's heads).  A key/value head's score is the largest of its query heads'; a page of infinite s
  * scores infinity, a query row with an infinity or a NaN scores every finite page 0.  Kept are the `first` first and the `last` last pages of those
  * that the query sees (last >= 1), then the largest scores, the earlier page where scores are equal, up to `keep`
  * pages in all.

@@ -1,0 +1,65 @@
+"""Page bounds, selection and attention behind a prefix at their ends, against the fp64 definitions in contexts_ref.py."""
+import math
+
+import pytest
+import torch
+
+import contexts_ref as C
+import free_block_sparse_gb300 as fbs
+import serving_ref as R
+from test_gpu_contexts import check_select, i32, loaded
+from test_gpu_serving import filled, gen, rand
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    fbs.lib()
+    yield
+    torch.cuda.synchronize()
+    assert fbs.device_status() == 0
+
+
+# ------------------------------------------------------------------------------------------------ selection
+def of_size(g, n, H, d, page, size):
+    """A sequence of n tokens whose keys have about this size, and bounds."""
+    pool, table = filled(g, [n], H, d, page)
+    t = torch.arange(n, device="cuda")
+    k = (torch.randn(1, H, n, d, generator=g, device="cuda").double() * size).bfloat16()
+    fbs.cache4_store(k, k, (table[0].long()[t // page] * page + t % page)[None].contiguous(), pool)
+    bounds = fbs.cache4_bounds(pool.shape[0], H, d)
+    fbs.cache4_bounds_update(pool, table, i32(n), n, bounds)
+    return pool, table, bounds
+
+
+@pytest.mark.parametrize("G,Nq,d", [(1, 1, 64), (2, 3, 128), (3, 1, 64), (4, 2, 128), (7, 1, 128), (20, 2, 64)])
+@pytest.mark.parametrize("keys,queries", [(100, 30), (110, 110), (-100, -50), (-110, -110), (-60, 60), (115, -20)])
+def test_select_scores_of_any_size(G, Nq, d, keys, queries):
+    """Products of keys and queries far outside fp32's range rank as they do in 64 bits: heads of a group have sizes 2^5 apart."""
+    g = gen(91)
+    n, page, H = 1600, 16, 2
+    pool, table, bounds = of_size(g, n, H, d, page, 2.0 ** keys)
+    q = rand(g, 1, H * G, Nq, d).double() * 2.0 ** queries
+    q = (q * 2.0 ** (-5.0 * (torch.arange(H * G, device="cuda") % G % 3))[None, :, None, None]).bfloat16()
+    got = fbs.cache4_select(q, pool, bounds, table, i32(n), 12)
+    check_select(q, pool, table, [n], bounds, 12, 1, 1, got)
+
+
+def test_select_large_negative_scores_and_pages_that_are_not_there():
+    """Pages with scores of -2^140 are pages: they come in front of places without one."""
+    g = gen(92)
+    d, page, n = 64, 16, 16 * 60
+    pool, table = filled(g, [n], 1, d, page)
+    t = torch.arange(n, device="cuda")
+    k = (2.0 ** 100 * (1 + torch.rand(1, 1, n, d, generator=g, device="cuda"))).bfloat16()
+    fbs.cache4_store(k, k, (table[0].long()[t // page] * page + t % page)[None].contiguous(), pool)
+    bounds = fbs.cache4_bounds(pool.shape[0], 1, d)
+    fbs.cache4_bounds_update(pool, table, i32(n), n, bounds)
+    q = torch.full((1, 2, 1, d), -(2.0 ** 40), dtype=torch.bfloat16, device="cuda")
+    bad = table.clone()
+    bad[0, 5:25] = -1
+    pages, lens = fbs.cache4_select(q, pool, bounds, bad, i32(n), 40)
+    assert fbs.device_status() == fbs.SPARGE_ERR_INVALID_ARG
+    there = [j for j in range(60) if not 5 <= j < 25]
+    assert pages[0, 0, 0].tolist() == [int(table[0, j]) for j in there] and int(lens[0, 0]) == 40 * page
