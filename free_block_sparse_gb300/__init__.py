@@ -573,8 +573,8 @@ def cache4_bounds(n_pages: int, H: int, d: int, device="cuda"):
 
 def cache4_bounds_update(pool, table, kv_lens, N: int, bounds):
     """Renews the bounds of the pages on which the last N of each sequence's kv_lens[b] tokens lie (after a
-    cache4_store of N new ones); table ((B, width) int32) and kv_lens as cache4_attn takes them.  Sequences that share a page have to
-    hold the same number of its tokens."""
+    cache4_store of N new ones); table ((B, width) int32) and kv_lens as cache4_attn takes them.  Of sequences that share
+    a page (in the same column of table) the one with the most tokens on it counts."""
     (_binding_module or _load_binding()).cache4_bounds_update(pool, table, kv_lens, N, bounds)
 
 

@@ -53,7 +53,7 @@ struct BoundsArgs {
   uint8_t *bounds;
   const int32_t *table, *lens, *pages;
   int64_t table_stride, n_pages, row, N, count;
-  int width, page_shift, H, most;  // most: pages of a sequence that its last N tokens can lie on
+  int B, width, page_shift, H, most;  // most: pages of a sequence that its last N tokens can lie on
   __nv_bfloat16 *hi, *lo;
   int *status;
 };
@@ -82,13 +82,23 @@ __global__ void __launch_bounds__(128) bounds_update_kernel(const BoundsArgs a) 
   const int len = length_of(a.lens, b, a.width, a.page_shift);
   const int first = static_cast<int>((len - a.N > 0 ? len - a.N : 0) >> a.page_shift), col = first + nth;
   const int64_t from = static_cast<int64_t>(col) << a.page_shift;
-  if (h >= a.H || from >= len) return;
+  if (from >= len) return;
   const int page = a.table[static_cast<int64_t>(b) * a.table_stride + col];
+  const int P = 1 << a.page_shift, n = static_cast<int>(len - from < P ? len - from : P);
+  // sequences that hold the page in common (a fork) may count different numbers of its tokens: the most of them, by that one's warps
+  if (n < P) {
+    bool more = false;
+    for (int o = threadIdx.x; o < a.B; o += 128) {
+      const int theirs = length_of(a.lens, o, a.width, a.page_shift), p = a.table[static_cast<int64_t>(o) * a.table_stride + col];
+      more = more || (p == page && theirs > len);
+    }
+    if (__syncthreads_or(more)) return;
+  }
+  if (h >= a.H) return;
   if (page < 0 || page >= a.n_pages) {
     if (lane == 0) record_status(a.status, -1 /* SPARGE_ERR_INVALID_ARG */);
     return;
   }
-  const int P = 1 << a.page_shift, n = static_cast<int>(len - from < P ? len - from : P);
   const uint8_t *src = a.pool + (static_cast<int64_t>(page) * a.H + h) * (static_cast<int64_t>(P / C4_TOKENS) * R::BYTES);
   float hi[NV], lo[NV];
 #pragma unroll
@@ -795,6 +805,7 @@ int sparge_cache4_bounds_update(const sparge_cache4 *cache, const int32_t *table
   if (N < 0) return fail(SPARGE_ERR_INVALID_ARG, "N=%lld is negative", (long long)N);
   if (B == 0 || N == 0 || width == 0) return SPARGE_OK;
   BoundsArgs a = {};
+  a.B = static_cast<int>(B);
   a.pool = c.data;
   a.bounds = static_cast<uint8_t *>(bounds);
   a.table = table;

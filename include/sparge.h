@@ -404,8 +404,8 @@ int sparge_cache4_attn(const sparge_tensor *q, const sparge_cache4 *cache, const
  * 32 bytes; sparge_cache4_bounds_bytes for n_pages of them (0 for an unsupported shape), 16-byte aligned.
  * sparge_cache4_bounds_update renews the bounds of the pages on which the last N of the kv_lens[b] tokens of each sequence
  * lie (lengths and table as sparge_cache4_attn takes them), all other pages' stay as they are: call it after a store, with
- * the N new tokens.  A page in two rows of the table has to hold the same number of tokens for both (whole pages of a shared prefix
- * do): with two numbers its bounds may be a mixture of both.
+ * the N new tokens.  A page that several rows of the table hold in the same column (a shared prefix, a fork) counts the most tokens that one of
+ * them says; in different columns they have to say the same number.
  * sparge_cache4_bounds_load reads the bounds of pages[0 .. n-1] back as values: hi and lo (n,H,d) bf16 (exact), zero
  * rows for negative pages.  A page past the pool is left out (there: a zero row) and records SPARGE_ERR_INVALID_ARG in the
  * device status word.

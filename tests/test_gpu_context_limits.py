@@ -63,3 +63,39 @@ def test_select_large_negative_scores_and_pages_that_are_not_there():
     assert fbs.device_status() == fbs.SPARGE_ERR_INVALID_ARG
     there = [j for j in range(60) if not 5 <= j < 25]
     assert pages[0, 0, 0].tolist() == [int(table[0, j]) for j in there] and int(lens[0, 0]) == 40 * page
+
+
+# ------------------------------------------------------------------------------------------------ bounds
+@pytest.mark.parametrize("d,page,H", [(128, 64, 8), (64, 16, 3), (64, 256, 1)])
+@pytest.mark.parametrize("B", [2, 7, 300])
+def test_bounds_of_a_page_that_sequences_hold_to_different_lengths(B, d, page, H):
+    """Forks of one sequence whose last page they share, each up to a token of its own: the page's bounds cover the most of them,
+    whatever the order, and one call's are another's."""
+    g = gen(93)
+    n = 3 * page
+    pool, one = filled(g, [n], H, d, page)
+    table = one.expand(B, -1).contiguous()
+    K = R.dequantise(*R.read_pool(pool, d)[:3])
+    for most in (1, 5, page - 1, page):
+        lens = 2 * page + 1 + torch.randint(0, most, (B,), generator=g, device="cuda").to(torch.int32)
+        lens[int(torch.randint(0, B, (1,), generator=g, device="cuda"))] = 2 * page + most
+        for _ in range(20):
+            bounds = fbs.cache4_bounds(pool.shape[0], H, d)
+            fbs.cache4_bounds_update(pool, table, lens, 1, bounds)
+            hi, lo = loaded(pool, bounds)
+            p = int(one[0, 2])
+            for h in range(H):
+                want = C.page_bounds(K[p, h, :most])
+                assert torch.equal(hi[p, h], want[0].cpu()) and torch.equal(lo[p, h], want[1].cpu())
+
+
+def test_bounds_of_a_page_that_a_longer_sequence_has_whole():
+    """A sequence that ends on a page which another one has filled leaves the bounds of the whole page as they are."""
+    g = gen(94)
+    d, page, H = 64, 32, 2
+    pool, one = filled(g, [4 * page], H, d, page)
+    table, bounds = one.expand(3, -1).contiguous(), fbs.cache4_bounds(pool.shape[0], H, d)
+    fbs.cache4_bounds_update(pool, table[:1], i32(4 * page), 4 * page, bounds)
+    whole = bounds.clone()
+    fbs.cache4_bounds_update(pool, table, i32(page + 3, 4 * page, 7), 1, bounds)
+    assert torch.equal(bounds, whole)
