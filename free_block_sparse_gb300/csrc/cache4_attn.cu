@@ -754,8 +754,10 @@ cudaError_t launch_cache_attn(const Args &a, int64_t tiles, cudaStream_t st) {
   if (cudaError_t e = launch_dependent(cache4_attn_kernel<D, RT, Args>, dim3(static_cast<unsigned>(ctas)), CA_WARPS * 32, S::TOTAL, st, a);
       e != cudaSuccess)
     return e;
-  if constexpr (Args::PARTIAL) return cudaSuccess;
-  return launch_split_combine<D, RT>(a, ctas, st);
+  if constexpr (Args::PARTIAL)
+    return cudaSuccess;
+  else
+    return launch_split_combine<D, RT>(a, ctas, st);
 }
 
 // recs: an upper bound of the records that a sequence's queries see, for the number of CTAs (the lengths are on the device)

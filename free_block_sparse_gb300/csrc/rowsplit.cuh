@@ -227,6 +227,7 @@ __global__ void __launch_bounds__(CC_THREADS) split_combine_kernel(const Args a,
 // shares: the attention kernel's CTAs, at most
 template <int D, int RT, typename Args>
 cudaError_t launch_split_combine(const Args &a, int64_t shares, cudaStream_t st) {
+  static_assert(!Args::PARTIAL, "an item inside one CTA has to be written there");
   // rows of a combining CTA: one per warp where items outnumber half the shares (an item then has few), else one
   const int64_t items = static_cast<int64_t>(a.B) * a.Hkv * a.ntile;
   const int nrow = 2 * items > shares ? CC_THREADS / 32 : 1, rows = a.rows < 8 * RT ? a.rows : 8 * RT;
