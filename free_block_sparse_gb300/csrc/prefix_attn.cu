@@ -1031,10 +1031,11 @@ cudaError_t launch_prefix_combine(const PrefixAttn &l, const SplitArgs &own, cud
   a.width = l.width;
   a.rec_shift = l.rec_shift;
   a.prefix = l.prefix;
-  // Warps of a row: by the shares that it has of the prefix, as long as all rows' warps are resident at once.  Measured at 256 rows
-  // of 300 shares: 48 us with a warp each, 15 with eight; 2048 rows of 20: 75.0 us the whole call with one, 73.6 with two, 75.3 with four.
+  // Warps of a row: by its shares of the prefix and the rows in all.  Measured with one, two and eight (d = 128): 256 rows of 153 shares 33,
+  // 25 and 16 us, 608 of 52 23, 17 and 11; 1024 of 39 20, 16 and 15 (two waves of blocks with eight, and ahead all the same); 1200 of 20 17, 13.5 and
+  // 14.4; 2400 of 17 17.5, 14.6 and 23, with 2432 of two warps resident at once; 2800 of 15 16.1, 16.3 and 25; 3000 of 12 13.7, 14.5 and 24.
   const int64_t shares = ((p.ctas + p.items - 1) / p.items + 1) * (p.R == 2 ? 1 : 2), all = rows * own.Hkv;
-  const int W = shares <= 12 || all > 2048 ? 1 : shares <= 32 || all > 1024 ? 2 : 8, per = PC_THREADS / 32 / W;
+  const int W = shares <= 12 || all > 16 * CA_SMS ? 1 : shares <= 32 || all > 1024 ? 2 : 8, per = PC_THREADS / 32 / W;
   const dim3 grid(static_cast<unsigned>((rows * own.Hkv + per - 1) / per));
   auto run = [&](auto d) {
     constexpr int D = decltype(d)::value;
