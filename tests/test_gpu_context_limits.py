@@ -99,3 +99,76 @@ def test_bounds_of_a_page_that_a_longer_sequence_has_whole():
     whole = bounds.clone()
     fbs.cache4_bounds_update(pool, table, i32(page + 3, 4 * page, 7), 1, bounds)
     assert torch.equal(bounds, whole)
+
+
+@pytest.mark.parametrize("H,d,page,lens", [(8, 128, 64, [64, 65, 0, 15, 200]), (3, 128, 16, [100, 3]), (2, 64, 256, [300, 700])])
+def test_bounds_hold_every_key(H, d, page, lens):
+    """As loaded, no key of a page lies outside, and each bound is less than a unit from one."""
+    g = gen(95)
+    pool, table = filled(g, lens, H, d, page)
+    bounds = fbs.cache4_bounds(pool.shape[0], H, d)
+    fbs.cache4_bounds_update(pool, table, i32(*lens), max(lens), bounds)
+    hi, lo = loaded(pool, bounds)
+    K = R.dequantise(*R.read_pool(pool, d)[:3]).cpu()
+    for b, n in enumerate(lens):
+        for j in range(-(-n // page)):
+            p = int(table[b, j])
+            k = K[p, :, :min(page, n - j * page)]
+            assert (k <= hi[p][:, None]).all() and (k >= lo[p][:, None]).all()
+            for h in range(H):
+                s = C.unit(float(k[h].abs().max()))
+                assert (hi[p, h] - k[h].amax(0) < s).all() and (k[h].amin(0) - lo[p, h] < s).all()
+
+
+@pytest.mark.parametrize("G,d,page,outliers", [(1, 128, 64, False), (4, 128, 64, False), (4, 64, 16, False), (1, 128, 64, True), (4, 64, 16, True)])
+def test_selection_beside_unrounded_bounds(G, d, page, outliers):
+    """How far the rounding of bounds and queries can move a selection.  A score is at least the row's bound of t r over the page's own
+    largest and smallest keys and at most s t sum |r| above it, and a query is off by t / 2 a channel: so no page that is left out has a bound
+    (of unrounded keys and queries) above a kept one's by more than s t sum |r| of the kept page and t / 2 sum max|k| of both.  Outliers: one
+    key of one in eight pages, in a channel where the queries are zero, doubles that page's unit several times."""
+    g = gen(96)
+    n_pages, H, keep = 300, 2, 40
+    n = n_pages * page
+    pool, table = filled(g, [n], H, d, page)
+    t = torch.arange(n, device="cuda")
+    k = torch.randn(1, H, n, d, generator=g, device="cuda")
+    k += 0.5 * torch.randn(1, H, n_pages, 1, d, generator=g, device="cuda").expand(-1, -1, -1, page, -1).reshape(1, H, n, d)
+    if outliers:
+        k[:, :, ::8 * page, 5] = 40.0
+    q = rand(g, 1, H * G, 1, d)
+    if outliers:
+        q[..., 5] = 0.0
+    fbs.cache4_store(k.bfloat16(), k.bfloat16(), (table[0].long()[t // page] * page + t % page)[None].contiguous(), pool)
+    bounds = fbs.cache4_bounds(pool.shape[0], H, d)
+    fbs.cache4_bounds_update(pool, table, i32(n), n, bounds)
+    pages, _ = fbs.cache4_select(q, pool, bounds, table, i32(n), keep)
+    K = R.dequantise(*R.read_pool(pool, d)[:3])[table[0].long()].cpu()                # pages, H, tokens, d
+    qd = q.double().cpu()[0, :, 0]
+    where = {int(p): j for j, p in enumerate(table[0].tolist())}
+    for h in range(H):
+        hi, lo = K[:, h].amax(1), K[:, h].amin(1)
+        s = torch.tensor([C.unit(float(x)) for x in K[:, h].abs().amax((1, 2))], dtype=torch.float64)
+        rows = qd[h * G:(h + 1) * G]
+        u = torch.maximum(rows[:, None] * hi, rows[:, None] * lo).sum(-1).amax(0)     # the unrounded bound of each page
+        ts = [C.unit(float(r.abs().max())) for r in rows]
+        off = max(ts) / 2 * torch.maximum(hi.abs(), lo.abs()).sum(-1)
+        up = max(float((torch.round(r / x) * x).abs().sum()) for r, x in zip(rows, ts))
+        kept = [where[p] for p in pages[0, 0, h].tolist()]
+        kept = [j for j in kept if 0 < j < n_pages - 1]
+        left = [j for j in range(1, n_pages - 1) if j not in kept]
+        assert len(kept) == keep - 2
+        assert float((u - off)[left].max()) <= float((u + off + s * up)[kept].min())
+
+
+# ------------------------------------------------------------------------------------------------ shared prefix
+def test_auto_shares_where_that_is_faster():
+    """The call that names no path, at a size where sharing takes less time: bit for bit the shared path, which rounds otherwise than
+    each sequence by itself."""
+    from test_gpu_contexts import shared
+    g = gen(97)
+    d, page, B = 128, 64, 32
+    pool, pages, table, lens = shared(g, 16384, [20 + b for b in range(B)], 2, d, page)
+    q = rand(g, B, 8, 1, d)
+    auto = fbs.cache4_prefix_attn(q, pool, pages, table, i32(*lens))
+    assert torch.equal(auto, fbs.cache4_prefix_attn(q, pool, pages, table, i32(*lens), path=fbs.SPARGE_PREFIX_SHARED))
+    assert not torch.equal(auto, fbs.cache4_attn(q, pool, table, i32(*lens)))

@@ -152,3 +152,24 @@ def test_large_keys_of_improbable_tokens(B, G, d, H, at, power):
     q = queries(g, B, H, G, d)
     out = fbs.cache4_prefix_attn(q, pool, pages, table, i32(*lens), scale=8 * scale_of(d), path=SHARED)
     check(q, pool, table, lens, out, d, slice(None), scale=8 * scale_of(d))
+
+
+@pytest.mark.parametrize("B,G,d,H", SETTINGS)
+@pytest.mark.parametrize("kind", ["climbs", "falls", "peak", "turns"])
+def test_scores_that_climb_and_peak(B, G, d, H, kind):
+    """The references move at nearly every tile, or once, for one token late in the prefix that takes everything; a row that sees all of
+    it the other way round; and what the check would say of an output that is nothing, or the values' mean."""
+    g = gen(86)
+    t = torch.arange(PREFIX, device="cuda")
+    score = {"climbs": t * (200.0 / PREFIX), "falls": 200.0 - t * (200.0 / PREFIX), "peak": torch.where(t == 17777, 60.0, 0.0),
+             "turns": t // 64 % 7 * 13.0}[kind]
+    v = torch.randn(H, PREFIX, d, generator=g, device="cuda")
+    pool, pages, table, lens = stored(g, B, d, H, score - 20.0, v)
+    q = queries(g, B, H, G, d)
+    q[1] *= -0.25                                  # (the own token's score is then +15)
+    out = fbs.cache4_prefix_attn(q, pool, pages, table, i32(*lens), scale=scale_of(d), path=SHARED)
+    check(q, pool, table, lens, out, d, slice(None))
+    mean = v.mean(1).bfloat16()[None, :, None].expand(B, -1, G, -1).reshape(out.shape)
+    for wrong in (torch.zeros_like(out), mean):
+        with pytest.raises(AssertionError):
+            check(q, pool, table, lens, wrong, d, slice(None))
