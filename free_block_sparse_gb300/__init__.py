@@ -587,7 +587,8 @@ def cache4_bounds_load(pool, bounds, pages):
 def cache4_select(q, pool, bounds, table, kv_lens, keep: int, first: int = 1, last: int = 1, pages=None, lens=None,
                   ws=None):
     """For each query of q (B,Hq,Nq,d) and KV head the pages that its keys' bounds say matter most: the `first` first and the `last`
-    last pages that the query sees, then the largest bounds on a product with a query of the head's group, up to keep pages.
+    last pages that the query sees, then the largest bounds on a product with a query of the head's group, up to keep pages.  (Bounds are
+    rounded to one power of two a page and head: a page with one key far above its others ranks too high, by at most that power times sum |q|.)
     Returns (pages (B,Nq,Hkv,keep) int32, in order, -1 behind them; lens (B,Nq) int32, the tokens on them)."""
     return (_binding_module or _load_binding()).cache4_select(q, pool, bounds, table, kv_lens, keep, first, last, pages, lens,
                                                             ws)

@@ -112,7 +112,8 @@ struct CacheListArgs : CacheAttnArgs {
 
 // What stands behind a prefix that is attended elsewhere: a sequence's records from first_rec on (all of them if its queries do
 // not all stand behind the prefix), as shares for another kernel to combine.  64 sequences of 64 to 2048 own tokens, 32 over 8 heads,
-// d = 128: about 22 us for 78 MB: an item of one head and sequence is a few steps, so starts and ends bound it.
+// d = 128: 22 to 26 us for 78 MB: an item of one head and sequence is a few steps, so starts and ends bound it.  (It starts behind the
+// prefix kernel.  Beside that one's last CTAs, reading before its wait what calls in front had written, it gained 2 us; that order is not promised.)
 struct CacheTailArgs : CacheAttnArgs {
   int first_rec;
   static constexpr bool PARTIAL = true;

@@ -68,9 +68,10 @@ __device__ __forceinline__ int length_of(const int32_t *lens, int b, int width, 
 // the channels 32 w + 8 c + j of every eighth token (the order of the codes in memory: 16-byte loads without gaps) and keeps their
 // maxima and minima in registers; at the page's end the eight lanes of a channel exchange halves (28 + 28 values
 // instead of 96 + 96) until each holds four channels in a row.
-// Four dependent latencies (length, page, records, write) bound it and, with many pages, its instructions (44 % of the issue slots): an update
-// for 256 sequences of one new token and the reading back of their pages take 9.6 us, for 4 of 8192 14.9 (23 MB).  Two warps
-// for a page's 128 channels, twice the warps resident: 10.4 and 17.6.
+// Dependent latencies bound it: length, page, then one record after another (a record's loads wait until the one before is reduced: four in a
+// page of 64 tokens, sixteen in one of 256), write.  An update for 256 sequences of one new token and the reading back of their pages
+// take 9.5 us, for 4 of 8192 16.2 (23 MB), of which the reading back is 2 and 3.5.  Two warps for a page's 128 channels, twice the warps
+// resident, took 0.8 and 2.7 us more; the search for a longer sequence on the page two rows at a time, in 96 registers for 127, 10.4 and 15.7.
 template <int D>
 __global__ void __launch_bounds__(128) bounds_update_kernel(const BoundsArgs a) {
   using R = Rec4<D>;
@@ -929,7 +930,9 @@ int sparge_cache4_select(const sparge_tensor *q, const sparge_cache4 *cache, con
     e = c.d == 128 ? launch_dependent(select_score_kernel<128>, grid, SEL_THREADS, 0, s, a)
                    : launch_dependent(select_score_kernel<64>, grid, SEL_THREADS, 0, s, a);
   }
-  // threads of a list: 512 lists over up to 512 pages 84.9 us a call with 256, 86.3 with 512; 384 lists over up to 8192 66 and 58
+  // threads of a list, the list kernel alone with 256 and 512 in us: 8 lists of 1024 pages 4.4 and 4.7, 2048 5.2 and 5.0, 4096 6.4 and
+  // 6.0, 8192 9.5 and 8.4; 512 lists of 512 11.4 and 13.9, 2048 18.6 and 19.8, 2560 21.4 and 23.2, 4096 32 and 31.4, 8192 36 and 40, but 384 of 32
+  // to 8192, whose longest ends last, 66 and 58 with scores and attention: the edge lies between those of few and of many lists
   if (e == cudaSuccess) e = width > 2048 ? launch_list<512>(a, lists, s) : launch_list<256>(a, lists, s);
   return e == cudaSuccess ? SPARGE_OK : cuda_fail(e, "page selection launch");
 }

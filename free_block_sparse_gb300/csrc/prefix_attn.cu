@@ -26,17 +26,18 @@
 // over the same tokens (more than 128 rows) or one tile of rows whose streams take the token tiles in turns.  The line of all
 // (KV head, row group) items' tiles is cut into equal shares, so any batch fills all SMs.
 //
-// What bounds it (64 sequences over 32K tokens of 8 heads, 4 rows each, d = 128, so 256 rows: 38.7 us; 3.5e10 flops would take 18.5 us):
-// a tile takes 1900 cycles, of which the tensor unit works 39 %, the schedulers issue 48 % and the special function unit 20 %.  The
-// score products with N = 64 and Q from shared memory take 600 of them a stream where their arithmetic would take 340, P V 270, and a
-// stream's chain - scores, their way to registers, exponentials, P's way to TMEM, P V, a wait of some 100 cycles at each - is
-// not covered by the other stream alone.  DRAM is idle at 9 %.  12 over 128K (48 rows of 128 in use): 85 us, 1300
-// cycles a tile, as long as its widening takes four warps with their waits; bytes would take 25.7.  Every role is a warp or four that
-// take the tiles one by one, so none may take longer than the rest: the powers of two cost their warp 1100 cycles a tile word by word and
-// 600 from packed maxima (95 -> 85 us).  The code of the roles' loops is larger than what the SM's instruction cache holds:
-// shorter code pays by itself (waits of ten instructions instead of forty and no second path for tiny V: hits 80 -> 96 %,
-// 43 -> 41 and 104 -> 94 us), and so do products that a whole warp issues, with descriptors in uniform registers (41 -> 38.7).  Tried and
-// not faster: P in two places so that it need not wait for P V (39.1), scores in two places with P over them (39.0),
+// What bounds it.  64 sequences over 32K tokens of 8 heads, 4 rows each, d = 128, so 256 rows: 38.8 us (3.5e10 flops would take 18.5), of which
+// 26.9 tiles of a CTA take 0.99 us each and 12 us are fixed: launch, Q, the first tiles' way through the roles, the shares' way out (65.5 us
+// over 64K).  Over the kernel the tensor unit works 40 %, the schedulers issue 47 %, the special function unit 20 %, DRAM 12 %: no unit, but
+// each stream's chain of scores, their way to registers, exponentials, P's way to TMEM and P V, with a wait at each step, that the other
+// stream's alone does not cover.  12 over 128K (48 rows of 128 in use): 88.9 us, 0.75 a tile and 8 fixed; bytes would take 25.7.  Two
+// streams take turns there, so a job of one takes 1.5 us, longer than with all rows in use; why is not known (more widening warps
+// took it to 83 us in an earlier state, and fewer exponentials to nothing).  Every role is a warp or four that take the tiles one by one,
+// so none may take longer than the rest: powers of two word by word, 1100 cycles a tile, took the kernel from 85 to 95 us.
+// The code of the roles' loops is larger than what the SM's instruction cache holds: shorter code pays by itself (waits of ten
+// instructions instead of forty and no second path for tiny V: hits 80 -> 96 %, 43 -> 41 and 104 -> 94 us; tiles that miss records by way of the
+// uneven ones': 40.3 -> 38.1 and 90.7 -> 87.2), and so do products that a whole warp issues, with descriptors in uniform registers
+// (41 -> 38.7).  Tried and not faster: P in two places so that it need not wait for P V (39.1), scores in two places with P over them (39.0),
 // two threads a row (46), eight warps that widen, in turns (39.5 and 83) or together (41 and 84), K and V freed apart (+5 %), powers of two
 // per record (maxima no longer come with the load: +15 %), one product of 128 tokens for both streams of one row tile (they then wait for one another: +30 %).
 #include <climits>

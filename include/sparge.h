@@ -425,6 +425,10 @@ int sparge_cache4_bounds_load(const sparge_cache4 *cache, const void *bounds, si
  * scores infinity, a query row with an infinity or a NaN scores every finite page 0.  Kept are the `first` first and the `last` last pages of those
  * that the query sees (last >= 1), then the largest scores, the earlier page where scores are equal, up to `keep`
  * pages in all.
+ * A page's codes share one s, so each of its bounds is up to s above the keys': a score is at most t s sum |r| above the unrounded bound of t r,
+ * and a page whose largest key is far above its others ranks by that key: it counts for more than its keys warrant, even where
+ * the query is zero in that channel.  (Keys of even size: 4 to 7 % of a list differ from what unrounded bounds choose; with one key 10 times the
+ * others' in one page of eight half the list and more.)
  * pages (B,Nq,H,keep) int32 receives the kept pages' numbers in the pool, in the order of the sequence, -1 behind them; lens (B,Nq)
  * int32 the number of tokens on them (lens must not be kv_lens).  At most 64 query heads per key/value head and 32768 table
  * columns.  ws: 256-byte aligned, sparge_cache4_select_workspace_bytes(...) bytes (a score for every query, head and table
