@@ -802,7 +802,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefix_attn_kernel(const Prefix
           uint32_t *to = reinterpret_cast<uint32_t *>(smem + C::RING + rs * C::RAW + rec * C::PITCH + (s ? Rec::VW : Rec::KW)) + (lane & 7) * (2 * NG);
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            const int by = there && some[s][k] != 0u ? min(max(min(-own[s][k], 100) - f[s], 0), 100) : 0;
+            const int by = there && some[s][k] != 0u ? min(max(min(-own[s][k], 100) - f[s], 0), 126) : 0;
             (s ? cs.v_by : cs.k_by)[tile & 15][col + k] = s ? static_cast<float>(-f[1] - by) : pf_pow2(-by);
 #pragma unroll
             for (int w = 0; w < NG; ++w)

@@ -139,9 +139,9 @@ def test_zero_values(B, G, d, H, at):
 
 @pytest.mark.parametrize("B,G,d,H", SETTINGS)
 @pytest.mark.parametrize("at", [0, 200, 511])
-@pytest.mark.parametrize("power", [8, 16, 24, 60])
+@pytest.mark.parametrize("power", [8, 16, 24, 60, 112])
 def test_large_keys_of_improbable_tokens(B, G, d, H, at, power):
-    """A token of every share whose keys are 2^8 to 2^60 times the others' and point away from the queries: the others' scores stay
+    """A token of every share whose keys are 2^8 to 2^112 times the others' and point away from the queries: the others' scores stay
     as exact as without it."""
     g = gen(85)
     t = torch.arange(PREFIX, device="cuda")
@@ -173,3 +173,35 @@ def test_scores_that_climb_and_peak(B, G, d, H, kind):
     for wrong in (torch.zeros_like(out), mean):
         with pytest.raises(AssertionError):
             check(q, pool, table, lens, wrong, d, slice(None))
+
+
+@pytest.mark.parametrize("B", [2, 70])
+@pytest.mark.parametrize("d", [64, 128])
+def test_uneven_tiles_with_pages_and_numbers_that_are_not_there(B, d):
+    """Tokens of any size beside pages outside the pool, and beside a value that is a NaN: the rest as without them."""
+    g = gen(87)
+    H, G, page = 2, 2, 16
+    pool, pages, table, lens = shared(g, 1280, [1] * B, H, d, page)
+    t = torch.arange(1280, device="cuda")
+    size = 2.0 ** (7 * (t % 6) - 20)
+    k = torch.where(t % 5 == 1, -3000.0, 1.0)[:, None] * (1 + torch.rand(H, 1280, d, generator=g, device="cuda"))
+    v = torch.randn(H, 1280, d, generator=g, device="cuda") * size[:, None]
+    at = (table[0].long()[t // page] * page + t % page)[None].contiguous()
+    fbs.cache4_store(k[None].bfloat16().contiguous(), v[None].bfloat16().contiguous(), at, pool)
+    q = queries(g, B, H, G, d)
+    gone = [0, 3, 4, 5, 6, 7, 41, 79]                                       # a tile's first page, whole tiles, the last page
+    kept = [j for j in range(table.shape[1]) if j not in gone]
+    bad, bad_table = pages.clone(), table.clone()
+    bad[gone] = torch.tensor([-1, pool.shape[0], -5, 2 ** 31 - 1, -1, -1, -1, -2 ** 31], dtype=torch.int32, device="cuda")
+    bad_table[:, gone] = -1
+    out = fbs.cache4_prefix_attn(q, pool, bad, bad_table, i32(*lens), scale=scale_of(d), path=SHARED)
+    assert fbs.device_status() == fbs.SPARGE_ERR_INVALID_ARG
+    check(q, pool, table[:, kept].contiguous(), [n - page * len(gone) for n in lens], out, d, slice(None))
+    word = 17 * d + (3 * (d // 64) + d // 64 - 1) * 4                       # token 3's word of V's last 64 channels
+    pool[int(pages[20]), 0, 0, word:word + 2] = 255
+    got = fbs.cache4_prefix_attn(q, pool, bad, bad_table, i32(*lens), scale=scale_of(d), path=SHARED)
+    assert fbs.device_status() == fbs.SPARGE_ERR_INVALID_ARG
+    assert torch.isnan(got[:, :G, :, d - 64:]).all() and torch.equal(got[:, G:], out[:, G:])
+    if d == 128:                                                           # (the token's other channels, under another power)
+        off = (got[:, :G, :, :64].double() - out[:, :G, :, :64].double()).square().sum()
+        assert off <= 2.0 ** -14 * out[:, :G, :, :64].double().square().sum()
