@@ -16,6 +16,8 @@
 
 #include <cstdint>
 
+#include "common.cuh"
+
 namespace sparge {
 
 constexpr int C4_TOKENS = 16;  // tokens of a record
@@ -36,5 +38,23 @@ struct Cache4 {
   int page_size, page_shift;  // page_size = 1 << page_shift tokens
   int H, d;
 };
+
+// An untiled copy to shared memory: both addresses and the size multiples of 16 bytes.
+__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+// two floats to f16x2 without saturation: an infinity or a NaN stays one
+__device__ __forceinline__ uint32_t half2_of(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// 2^e for a whole e in -126..127
+__device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }
+// exponent of |x| (0 and subnormals: -127)
+__device__ __forceinline__ int exponent_of(float x) { return static_cast<int>((__float_as_uint(x) >> 23) & 0xFFu) - 127; }
 
 }  // namespace sparge

@@ -171,12 +171,6 @@ __device__ __forceinline__ int64_t divide(int64_t x, int64_t y) {
   return ((x | y) >> 32) == 0 ? static_cast<uint32_t>(x) / static_cast<uint32_t>(y) : x / y;
 }
 
-__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                   smem_u32(dst)),
-               "l"(src), "r"(bytes), "r"(smem_u32(bar))
-               : "memory");
-}
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
   asm(
@@ -205,17 +199,6 @@ __device__ __forceinline__ void words(const uint8_t *p, uint32_t (&u)[NG], uint3
     v[0] = *reinterpret_cast<const uint32_t *>(p + 32 + g * 4);
   }
 }
-// two floats to f16x2 without saturation: an infinity or a NaN stays one
-__device__ __forceinline__ uint32_t half2_of(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-// 2^e for a whole e in -126..127
-__device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }
-// exponent of |x| (0 and subnormals: -127)
-__device__ __forceinline__ int exponent_of(float x) { return static_cast<int>((__float_as_uint(x) >> 23) & 0xFFu) - 127; }
-
 // 2^e / f for a power of two f
 __device__ __forceinline__ float over2(float f, int e) {
   return __uint_as_float((static_cast<uint32_t>(254 + e) << 23) - __float_as_uint(f));

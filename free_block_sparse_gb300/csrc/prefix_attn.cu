@@ -110,12 +110,6 @@ struct PfCtrl {
 };
 static_assert(sizeof(PfCtrl) <= 9216, "control block");
 
-__device__ __forceinline__ void pf_bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                   smem_u32(dst)),
-               "l"(src), "r"(bytes), "r"(smem_u32(bar))
-               : "memory");
-}
 __device__ __forceinline__ void pf_bulk_store(void *dst, uint32_t src, uint32_t bytes) {
   asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes) : "memory");
 }
@@ -138,13 +132,6 @@ __device__ __forceinline__ bool pf_one_lane() {
   uint32_t r;
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
   return r != 0u;
-}
-__device__ __forceinline__ float pf_pow2(int e) { return __int_as_float((e + 127) << 23); }  // e in -126..127
-__device__ __forceinline__ int pf_exponent(float x) { return static_cast<int>((__float_as_uint(x) >> 23) & 0xFFu) - 127; }
-__device__ __forceinline__ uint32_t pf_half2(float lo, float hi) {  // an infinity or a NaN stays one
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
 }
 __device__ __forceinline__ uint32_t pf_hfma2(uint32_t a, uint32_t b, uint32_t c) {
   uint32_t r;
@@ -207,7 +194,7 @@ __device__ __forceinline__ int pf_finite_need(uint32_t word) {
 __device__ __forceinline__ int pf_power(int need) { return min(max(-need, -126), 100); }
 // A scale and a minimum times 2^by, exactly.
 __device__ __forceinline__ uint32_t pf_word_by(uint32_t word, int by) {
-  const float f = pf_pow2(by);
+  const float f = pow2i(by);
   return pack_bf16x2(bf16lo(word) * f, bf16hi(word) * f);
 }
 
@@ -344,12 +331,12 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefix_attn_kernel(const Prefix
             }
           }
         }
-        const int e = min(max(pf_exponent(mx), -100), 116);
-        const float f = pf_pow2(14 - e);
-        rm = a.scale_log2 * pf_pow2(e - 14);
+        const int e = min(max(exponent_of(mx), -100), 116);
+        const float f = pow2i(14 - e);
+        rm = a.scale_log2 * pow2i(e - 14);
         auto scaled = [&](uint4 u) {
-          return make_uint4(pf_half2(bf16lo(u.x) * f, bf16lo(u.z) * f), pf_half2(bf16hi(u.x) * f, bf16hi(u.z) * f),
-                            pf_half2(bf16lo(u.y) * f, bf16lo(u.w) * f), pf_half2(bf16hi(u.y) * f, bf16hi(u.w) * f));
+          return make_uint4(half2_of(bf16lo(u.x) * f, bf16lo(u.z) * f), half2_of(bf16hi(u.x) * f, bf16hi(u.z) * f),
+                            half2_of(bf16lo(u.y) * f, bf16lo(u.w) * f), half2_of(bf16hi(u.y) * f, bf16hi(u.w) * f));
         };
         if (keep) {
           if (C::QSMEM) {
@@ -392,7 +379,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefix_attn_kernel(const Prefix
         // (what the widened tile's barrier orders, its powers among it, is there before its scores are)
         ok = pf_wait(&cs.s_full[t], done & 1, abort) && pf_wait(&cs.kv_full[st], (tile / NS) & 1, abort);
         const PfInfo info = cs.info[tile & 15];
-        float mult = fminf(fmaxf(rm * pf_pow2(-info.kf), 0x1p-126f), 0x1p127f);  // (no 0 times -inf, no infinity times 0)
+        float mult = fminf(fmaxf(rm * pow2i(-info.kf), 0x1p-126f), 0x1p127f);  // (no 0 times -inf, no infinity times 0)
         float g = static_cast<float>(-info.vf), apart = 0.f;
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
@@ -555,7 +542,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefix_attn_kernel(const Prefix
         const int c = lane & 3, r = (lane >> 2) & 1;
         const int f = info.kf;
         const bool there = !((info.missing >> (2 * pk + r)) & 1u);
-        const float fs = there ? pf_pow2(f + 24) : 0.f, fm = there ? pf_pow2(f) : 0.f;
+        const float fs = there ? pow2i(f + 24) : 0.f, fm = there ? pow2i(f) : 0.f;
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           const int t = ((w4 >> 1) + 2 * k) * 4 + (lane >> 3);
@@ -576,7 +563,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefix_attn_kernel(const Prefix
 #pragma unroll
           for (int w = 0; w < 2 * NG; ++w) {
             const float sf = there ? bf16lo(word[w / 2]) * fs : 0.f, mf = there ? bf16hi(word[w / 2]) * fm : 0.f;
-            const uint32_t lo = pf_half2(sf, sf), hi = pf_sixteenth2(lo), m = pf_half2(mf, mf), u = code[w], u8 = u >> 8;
+            const uint32_t lo = half2_of(sf, sf), hi = pf_sixteenth2(lo), m = half2_of(mf, mf), u = code[w], u8 = u >> 8;
             pf_sts128(to + (w >> 1) * 8192 + (((4 * (w & 1) + c) ^ (pos & 7)) << 4), pf_hfma2(u & 0x000F000Fu, lo, m),
                       pf_hfma2(u & 0x00F000F0u, hi, m), pf_hfma2(u8 & 0x000F000Fu, lo, m), pf_hfma2(u8 & 0x00F000F0u, hi, m));
           }
@@ -593,7 +580,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefix_attn_kernel(const Prefix
           const uint8_t *from = raw + (2 * pr + r) * C::PITCH, *src = from + Rec::V + part * 512 + 16 * lane + 4 * u0;
           const int f = info.vf;
           const bool there = !((info.missing >> (2 * pr + r)) & 1u);
-          const float fs = pf_pow2(f + 24), fm = pf_pow2(f);
+          const float fs = pow2i(f + 24), fm = pow2i(f);
           if constexpr (NU == 4) {
             const uint4 u = *reinterpret_cast<const uint4 *>(src);
             code[r][0] = u.x; code[r][1] = u.y; code[r][2] = u.z; code[r][3] = u.w;
@@ -614,8 +601,8 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefix_attn_kernel(const Prefix
               y = u.y;
             }
             if (!there) x = y = 0u;
-            ss[2 * r + k] = pf_half2(bf16lo(x) * fs, bf16lo(y) * fs);
-            mm[2 * r + k] = pf_half2(bf16hi(x) * fm, bf16hi(y) * fm);
+            ss[2 * r + k] = half2_of(bf16lo(x) * fs, bf16lo(y) * fs);
+            mm[2 * r + k] = half2_of(bf16hi(x) * fm, bf16hi(y) * fm);
             sh[2 * r + k] = pf_sixteenth2(ss[2 * r + k]);
           }
         }
@@ -727,7 +714,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefix_attn_kernel(const Prefix
           cs.bad[rs][lane & 3] = src == nullptr;
           if (src != nullptr) {
             mbar_arrive_expect_tx(bar, Rec::BYTES);
-            pf_bulk_load(smem + C::RING + rs * C::RAW + (lane & 3) * C::PITCH, src, Rec::BYTES, bar);
+            bulk_load(smem + C::RING + rs * C::RAW + (lane & 3) * C::PITCH, src, Rec::BYTES, bar);
           } else {
             mbar_arrive(bar);
           }
@@ -803,7 +790,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefix_attn_kernel(const Prefix
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             const int by = there && some[s][k] != 0u ? min(max(min(-own[s][k], 100) - f[s], 0), 126) : 0;
-            (s ? cs.v_by : cs.k_by)[tile & 15][col + k] = s ? static_cast<float>(-f[1] - by) : pf_pow2(-by);
+            (s ? cs.v_by : cs.k_by)[tile & 15][col + k] = s ? static_cast<float>(-f[1] - by) : pow2i(-by);
 #pragma unroll
             for (int w = 0; w < NG; ++w)
               if (by > 0) to[NG * k + w] = pf_word_by(to[NG * k + w], by);
