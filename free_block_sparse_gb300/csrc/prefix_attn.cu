@@ -13,8 +13,8 @@
 // 2^-3).  An element is off by at most 2^-11 of itself and 2^-15 of the largest scale.  So that no token takes bits from smaller ones, a
 // tile whose tokens' sizes are more than 2^PF_EVEN apart is an uneven one: the warp that finds the powers scales the smaller tokens' words to
 // the size of the largest, and the softmax takes each token's own powers from shared memory.  (It passes twice over the scores, in
-// a loop that stays small beside the even tiles' code: unrolled, or with the scores in local memory, it cost those 5 to 20 %.  64 over
-// 32K with every tile uneven: 79 us in place of 39, one of 16 tiles 46.)  Words give the
+// a function of its own: within the even tiles' code it cost those 5 % as a loop, up to 20 % unrolled or with the scores in local memory.  64 over
+// 32K with every tile uneven: 78 us in place of 38, one of 16 tiles 43.)  Words give the
 // channels of eight in the order 0 4 1 5 2 6 3 7, so Q is stored in that order; tokens of a tile stand in the order that the
 // V records give (position 32 p + 8 c + 4 r + 2 h + i: token 2 c + 8 h + i of record 2 p + r), for K and V alike.
 //
@@ -26,17 +26,17 @@
 // over the same tokens (more than 128 rows) or one tile of rows whose streams take the token tiles in turns.  The line of all
 // (KV head, row group) items' tiles is cut into equal shares, so any batch fills all SMs.
 //
-// What bounds it.  64 sequences over 32K tokens of 8 heads, 4 rows each, d = 128, so 256 rows: 38.8 us (3.5e10 flops would take 18.5), of which
-// 26.9 tiles of a CTA take 0.99 us each and 12 us are fixed: launch, Q, the first tiles' way through the roles, the shares' way out (65.5 us
+// What bounds it.  64 sequences over 32K tokens of 8 heads, 4 rows each, d = 128, so 256 rows: 37.7 us (3.5e10 flops would take 18.5), of which
+// 26.9 tiles of a CTA take 0.95 us each and 12 us are fixed: launch, Q, the first tiles' way through the roles, the shares' way out (63.2 us
 // over 64K).  Over the kernel the tensor unit works 40 %, the schedulers issue 47 %, the special function unit 20 %, DRAM 12 %: no unit, but
 // each stream's chain of scores, their way to registers, exponentials, P's way to TMEM and P V, with a wait at each step, that the other
-// stream's alone does not cover.  12 over 128K (48 rows of 128 in use): 88.9 us, 0.75 a tile and 8 fixed; bytes would take 25.7.  Two
-// streams take turns there, so a job of one takes 1.5 us, longer than with all rows in use; why is not known (more widening warps
+// stream's alone does not cover.  12 over 128K (48 rows of 128 in use): 84.6 us, 0.70 a tile and 9 fixed; bytes would take 25.7.  Two
+// streams take turns there, so a job of one takes 1.4 us, longer than with all rows in use; why is not known (more widening warps
 // took it to 83 us in an earlier state, and fewer exponentials to nothing).  Every role is a warp or four that take the tiles one by one,
 // so none may take longer than the rest: powers of two word by word, 1100 cycles a tile, took the kernel from 85 to 95 us.
 // The code of the roles' loops is larger than what the SM's instruction cache holds: shorter code pays by itself (waits of ten
 // instructions instead of forty and no second path for tiny V: hits 80 -> 96 %, 43 -> 41 and 104 -> 94 us; tiles that miss records by way of the
-// uneven ones': 40.3 -> 38.1 and 90.7 -> 87.2), and so do products that a whole warp issues, with descriptors in uniform registers
+// uneven ones', and those in a function of their own: 40.3 -> 37.7 and 90.7 -> 84.6), and so do products that a whole warp issues, with descriptors in uniform registers
 // (41 -> 38.7).  Tried and not faster: P in two places so that it need not wait for P V (39.1), scores in two places with P over them (39.0),
 // two threads a row (46), eight warps that widen, in turns (39.5 and 83) or together (41 and 84), K and V freed apart (+5 %), powers of two
 // per record (maxima no longer come with the load: +15 %), one product of 128 tokens for both streams of one row tile (they then wait for one another: +30 %).
@@ -196,6 +196,38 @@ __device__ __forceinline__ int pf_power(int need) { return min(max(-need, -126),
 __device__ __forceinline__ uint32_t pf_word_by(uint32_t word, int by) {
   const float f = pow2i(by);
   return pack_bf16x2(bf16lo(word) * f, bf16hi(word) * f);
+}
+
+// An uneven tile's scores, 64 columns of TMEM: l and m take them in, then x + g of each token stands in their place.
+__device__ __noinline__ float2 pf_uneven(uint32_t sc, const float *k_by, const float *v_by, uint32_t missing, float mult, float m, float l) {
+  float xm = -INFINITY;
+#pragma unroll 1
+  for (int i = 0; i < 128; i += 16) {  // every 16 columns for the maximum, then again for the sum
+    uint32_t x[16];
+    tmem_ld16(sc + (i & 63), x);
+    pf_ld_wait_for(x);
+    if (i == 64) {
+      const float mn = fmaxf(m, xm);
+      l *= m == -INFINITY ? 0.f : fast_exp2(m - mn);
+      m = mn;
+    }
+    const float *by = (i < 64 ? k_by : v_by) + (i & 63);
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      float y = __uint_as_float(x[k]);
+      if (i < 64) {  // column 32 h + 8 c + 4 r + i is a token of record 2 h + r
+        y = ((missing >> (2 * (i >> 5) + ((k >> 2) & 1))) & 1u) ? -INFINITY : y * by[k] * mult;
+        xm = fmaxf(xm, y);
+      } else {
+        l += fast_exp2(m == -INFINITY ? y : y - m);
+        y += by[k];
+      }
+      x[k] = __float_as_uint(y);
+    }
+    tmem_st16(sc + (i & 63), x);
+    tmem_st_wait();
+  }
+  return make_float2(m, l);
 }
 
 // A CTA's share of the line of all items' tiles, and its pieces: item, first tile, tiles.
@@ -387,34 +419,10 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefix_attn_kernel(const Prefix
         uint32_t v[2][32];
         float mh[2];
         if (live) {
-          if (info.uneven) [[unlikely]] {  // l and m from the scores, then x + g of each token in their place
-            float xm = -INFINITY;
-#pragma unroll 1
-            for (int i = 0; i < 128; i += 16) {  // every 16 columns for the maximum, then again for the sum
-              uint32_t x[16];
-              tmem_ld16(sc + (i & 63), x);
-              pf_ld_wait_for(x);
-              if (i == 64) {
-                const float mn = fmaxf(m, xm);
-                l *= m == -INFINITY ? 0.f : fast_exp2(m - mn);
-                m = mn;
-              }
-              const float *by = (i < 64 ? cs.k_by : cs.v_by)[tile & 15] + (i & 63);
-#pragma unroll
-              for (int k = 0; k < 16; ++k) {
-                float y = __uint_as_float(x[k]);
-                if (i < 64) {  // column 32 h + 8 c + 4 r + i is a token of record 2 h + r
-                  y = ((info.missing >> (2 * (i >> 5) + ((k >> 2) & 1))) & 1u) ? -INFINITY : y * by[k] * mult;
-                  xm = fmaxf(xm, y);
-                } else {
-                  l += fast_exp2(m == -INFINITY ? y : y - m);
-                  y += by[k];
-                }
-                x[k] = __float_as_uint(y);
-              }
-              tmem_st16(sc + (i & 63), x);
-              tmem_st_wait();
-            }
+          if (info.uneven) [[unlikely]] {
+            const float2 ml = pf_uneven(sc, cs.k_by[tile & 15], cs.v_by[tile & 15], info.missing, mult, m, l);
+            m = ml.x;
+            l = ml.y;
             mult = 1.f;
             g = 0.f;
             apart = -INFINITY;
