@@ -28,7 +28,7 @@
 //
 // What bounds it.  64 sequences over 32K tokens of 8 heads, 4 rows each, d = 128, so 256 rows: 37.7 us (3.5e10 flops would take 18.5), of which
 // 26.9 tiles of a CTA take 0.95 us each and 12 us are fixed: launch, Q, the first tiles' way through the roles, the shares' way out (63.2 us
-// over 64K).  Over the kernel the tensor unit works 40 %, the schedulers issue 47 %, the special function unit 20 %, DRAM 12 %: no unit, but
+// over 64K).  Over the kernel the tensor unit works 40 %, the schedulers issue 48 %, the special function unit 21 %, DRAM 12 %: no unit, but
 // each stream's chain of scores, their way to registers, exponentials, P's way to TMEM and P V, with a wait at each step, that the other
 // stream's alone does not cover.  12 over 128K (48 rows of 128 in use): 84.6 us, 0.70 a tile and 9 fixed; bytes would take 25.7.  Two
 // streams take turns there, so a job of one takes 1.4 us, longer than with all rows in use; why is not known (more widening warps
