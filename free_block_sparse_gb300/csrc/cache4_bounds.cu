@@ -8,7 +8,7 @@
 //   t s sum_c max(r_c hi_c, r_c lo_c) = t s (sum r+ hi + sum r- lo),   r+ = max(r, 0), r- = min(r, 0),
 // which no token of the page exceeds in t r . k.  A KV head's score is the largest of its heads'.  The sums are whole numbers below 2^21
 // and the factors powers of two, so the selection does not depend on the order of any sum.  Scores are held in units of 2^15 times the
-// largest t of the group's heads, which changes no list: so none leaves fp32's range (2^127 at most), and each is exact where its head's t / that
+// largest t of the group's heads, which changes no list: so none leaves fp32's range (they stay below 2^128), and each is exact where its head's t / that
 // largest * s is 2^-134 or more.  d + d bytes of codes per page and head in place of 9 d / 16 for every token.
 //
 // Layout of a page's bounds: codes [H][hi, lo][d], scales [H] (fp32), padded to 32 bytes.

@@ -172,3 +172,40 @@ def test_auto_shares_where_that_is_faster():
     auto = fbs.cache4_prefix_attn(q, pool, pages, table, i32(*lens))
     assert torch.equal(auto, fbs.cache4_prefix_attn(q, pool, pages, table, i32(*lens), path=fbs.SPARGE_PREFIX_SHARED))
     assert not torch.equal(auto, fbs.cache4_attn(q, pool, table, i32(*lens)))
+
+
+@pytest.mark.parametrize("B,Hq,Hkv,Nq,d,prefix,page", [
+    (2000, 8, 4, 1, 64, 64, 16),        # 64 items of one tile: several to a CTA, two tiles of rows each
+    (300, 64, 64, 1, 128, 80, 16),      # 128 items of two tiles, the second of one record
+    (2, 400, 200, 1, 128, 48, 16),      # 200 items of a part of a tile, one tile of rows: the second stream has none
+    (3, 120, 60, 2, 64, 208, 16),       # 60 items of four tiles, cut in odd places
+])
+def test_prefix_of_many_items(B, Hq, Hkv, Nq, d, prefix, page):
+    """More items than CTAs, or nearly: pieces of one tile, several for a CTA; a few sequences of all are looked at."""
+    from test_gpu_contexts import shared
+    from test_gpu_contexts_edges import check_prefix
+    g = gen(98)
+    pool, pages, table, lens = shared(g, prefix, [Nq + b % 7 for b in range(B)], Hkv, d, page)
+    q = rand(g, B, Hq, Nq, d)
+    out = fbs.cache4_prefix_attn(q, pool, pages, table, i32(*lens), path=fbs.SPARGE_PREFIX_SHARED)
+    some = torch.tensor(sorted({0, 1, B // 3, B // 2, B - 1}), device="cuda")
+    check_prefix(q[some], pool, table[some], [lens[b] for b in some.tolist()], out[some], d)
+    assert torch.equal(out, fbs.cache4_prefix_attn(q, pool, pages, table, i32(*lens), path=fbs.SPARGE_PREFIX_SHARED))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_outputs_over_the_queries(d):
+    """The output in the queries' place gives what one of its own gives: a row's queries are read before it is written."""
+    from test_gpu_contexts import shared
+    g = gen(99)
+    B, page = 40, 16
+    pool, pages, table, lens = shared(g, 640, [3 + 5 * b for b in range(B)], 2, d, page)
+    kv, bounds = i32(*lens), fbs.cache4_bounds(pool.shape[0], 2, d)
+    fbs.cache4_bounds_update(pool, table, kv, max(lens), bounds)
+    q = rand(g, B, 8, 3, d)
+    some = fbs.cache4_select(q, pool, bounds, table, kv, 20)
+    for call in (lambda x, out: fbs.cache4_attn(x, pool, table, kv, out=out),
+                 lambda x, out: fbs.cache4_pages_attn(x, pool, *some, out=out),
+                 lambda x, out: fbs.cache4_prefix_attn(x, pool, pages, table, kv, out=out, path=fbs.SPARGE_PREFIX_SHARED)):
+        x = q.clone()
+        assert torch.equal(call(x, x), call(q, None))
