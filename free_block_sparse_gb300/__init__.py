@@ -137,6 +137,7 @@ EXPORTS = {
                                                 ctypes.c_void_p, ctypes.c_float, ctypes.c_void_p, ctypes.c_void_p,
                                                 ctypes.c_size_t, ctypes.c_void_p]),
     "sparge_cache4_prefix_attn_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int64] * 5),
+    "sparge_cache4_prefix_attn_workspace_bytes_of": (ctypes.c_size_t, [ctypes.c_int64] * 6 + [ctypes.c_int]),
     "sparge_cache4_prefix_attn": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64,
                                                  ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64, ctypes.c_void_p,
                                                  ctypes.c_float, ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p,

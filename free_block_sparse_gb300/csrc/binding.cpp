@@ -534,7 +534,8 @@ PyObject *cache4_prefix_attn(const Args &a) {
   at::Tensor out = given_rows(a, 7, h, "out"), ws = given_workspace(a, 8, h);
   done(unlocked([&] {
     if (!out.defined()) out = h.make_like(q);
-    if (!ws.defined()) ws = make_workspace(h, sparge_cache4_prefix_attn_workspace_bytes(dq.B, dq.H, c.H, dq.N, dq.d));
+    if (!ws.defined())
+      ws = make_workspace(h, sparge_cache4_prefix_attn_workspace_bytes_of(dq.B, dq.H, c.H, dq.N, dq.d, n * c.page_size, path));
     sparge_tensor o = Here::describe(out);
     return sparge_cache4_prefix_attn(&dq, &c, ids, n, static_cast<const int32_t *>(table.data_ptr()), table.size(1), stride, lens, scale,
                                      path, &o, ws.data_ptr(), ws.nbytes(), h.s());

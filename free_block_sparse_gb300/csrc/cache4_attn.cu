@@ -800,6 +800,11 @@ int set_split(CacheAttnArgs &a, int64_t B, int64_t Nq, int64_t d, void *ws, size
   return SPARGE_OK;
 }
 
+// Whether a call attends its prefix of `recs` records once for all sequences (rows: query rows of a KV head and sequence).
+bool shares_prefix(int path, int64_t B, int64_t rows, int64_t Hkv, int64_t d, int64_t recs) {
+  return recs > 0 && B * rows > 0 && (path == SPARGE_PREFIX_SHARED || prefix_shared(B, rows, Hkv, d, recs));
+}
+
 }  // namespace
 }  // namespace sparge
 
@@ -881,6 +886,14 @@ size_t sparge_cache4_prefix_attn_workspace_bytes(int64_t B, int64_t Hq, int64_t 
   return own == 0 || B * (Hq / Hkv) * Nq > INT_MAX / 2 ? 0 : own + prefix_ws_bytes(B * (Hq / Hkv) * Nq, Hkv, d);
 }
 
+size_t sparge_cache4_prefix_attn_workspace_bytes_of(int64_t B, int64_t Hq, int64_t Hkv, int64_t Nq, int64_t d, int64_t prefix_tokens,
+                                                    int path) {
+  const size_t most = sparge_cache4_prefix_attn_workspace_bytes(B, Hq, Hkv, Nq, d);
+  if (most == 0 || prefix_tokens < 0 || prefix_tokens > INT_MAX || (path != SPARGE_PREFIX_AUTO && path != SPARGE_PREFIX_SHARED)) return 0;
+  const bool shared = shares_prefix(path, B, Hq / Hkv * Nq, Hkv, d, prefix_tokens / 16);
+  return shared ? most : sparge_cache4_attn_workspace_bytes(B, Hq, Hkv, Nq, d);
+}
+
 int sparge_cache4_prefix_attn(const sparge_tensor *q, const sparge_cache4 *cache, const int32_t *prefix_pages, int64_t n_prefix,
                               const int32_t *table, int64_t width, int64_t table_stride, const int32_t *kv_lens, float scale,
                               int path, sparge_tensor *o, void *ws, size_t ws_bytes, sparge_stream_t stream) {
@@ -897,7 +910,9 @@ int sparge_cache4_prefix_attn(const sparge_tensor *q, const sparge_cache4 *cache
   if (n_prefix && !prefix_pages) return fail(SPARGE_ERR_INVALID_ARG, "prefix_pages is NULL");
   if (qv.B * a.G * qv.N > INT_MAX / 2) return fail(SPARGE_ERR_UNSUPPORTED, "too many query rows");
   if ((rc = set_split(a, qv.B, qv.N, qv.d, ws, ws_bytes))) return rc;
-  const size_t own = ws_layout(qv.B, c.H, a.rows, qv.d).total, need = own + prefix_ws_bytes(qv.B * a.rows, c.H, qv.d);
+  const int d = static_cast<int>(qv.d), per = c.page_size / 16;
+  const bool shared = shares_prefix(path, qv.B, a.rows, c.H, d, n_prefix * per);
+  const size_t own = ws_layout(qv.B, c.H, a.rows, d).total, need = own + (shared ? prefix_ws_bytes(qv.B * a.rows, c.H, d) : 0);
   if (ws_bytes < need) return fail(SPARGE_ERR_WORKSPACE_TOO_SMALL, "workspace %zu bytes, need %zu", ws_bytes, need);
   if (qv.B == 0 || qv.N == 0) return SPARGE_OK;
   if (!kv_lens || (width && !table)) return fail(SPARGE_ERR_INVALID_ARG, "table or kv_lens is NULL");
@@ -906,10 +921,9 @@ int sparge_cache4_prefix_attn(const sparge_tensor *q, const sparge_cache4 *cache
   a.table_stride = table_stride;
   a.width = static_cast<int>(width);
   a.status = status_ptr();
-  const int d = static_cast<int>(qv.d), per = c.page_size / 16;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e;
-  if (n_prefix == 0 || (path == SPARGE_PREFIX_AUTO && !prefix_shared(qv.B, a.rows, c.H, d, n_prefix * per))) {
+  if (!shared) {
     e = run_cache_attn(static_cast<const CacheAttnArgs &>(a), d, width * per, s);
     return e == cudaSuccess ? SPARGE_OK : cuda_fail(e, "cache attention launch");
   }

@@ -467,6 +467,10 @@ int sparge_cache4_pages_attn(const sparge_tensor *q, const sparge_cache4 *cache,
 #define SPARGE_PREFIX_AUTO 0
 #define SPARGE_PREFIX_SHARED 1
 size_t sparge_cache4_prefix_attn_workspace_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_t Nq, int64_t d);
+/* what a call with that path and a prefix of that many tokens needs (the former is enough for any): sparge_cache4_attn's where it attends every
+   sequence over its own row */
+size_t sparge_cache4_prefix_attn_workspace_bytes_of(int64_t B, int64_t Hq, int64_t Hkv, int64_t Nq, int64_t d, int64_t prefix_tokens,
+                                                    int path);
 int sparge_cache4_prefix_attn(const sparge_tensor *q, const sparge_cache4 *cache, const int32_t *prefix_pages, int64_t n_prefix,
                               const int32_t *table, int64_t width, int64_t table_stride, const int32_t *kv_lens, float scale,
                               int path, sparge_tensor *o, void *ws, size_t ws_bytes, sparge_stream_t stream);
